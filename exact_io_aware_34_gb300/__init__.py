@@ -13,6 +13,8 @@ from .fa import (  # noqa: F401
     FaError,
     fa_fwd,
     fa_fwd_fault_test,
+    fa_fwd_varlen,
+    fa_fwd_varlen_workspace_bytes,
     fa_get_device_status,
     fa_last_cuda_error,
     fa_naive_fwd,

@@ -19,6 +19,7 @@
 #include "fa_bwd_kernel.cuh"
 #include "fa_decode_kernel.cuh"
 #include "fa_fwd_kernel.cuh"
+#include "fa_varlen_kernel.cuh"
 #include "naive_kernels.cuh"
 
 // Device scratch for fa_naive_fwd_noalloc: the score/probability matrices of
@@ -681,7 +682,7 @@ fa_status_t fa_get_device_status(cudaStream_t stream, unsigned int* info) {
   e = cudaMemcpyToSymbol(fa::g_status_word, zeros, sizeof(unsigned int));
   if (e == cudaSuccess) e = cudaMemcpyToSymbol(fa::g_status_info, zeros, sizeof(zeros));
   if (e != cudaSuccess) return cuda_fail(e);
-  return FA_ERR_TIMEOUT;
+  return word == fa::kStatusBadOffsets ? FA_ERR_INVALID_ARG : FA_ERR_TIMEOUT;
 }
 
 size_t fa_naive_workspace_bytes(int B, int H, int N) {
@@ -1101,3 +1102,5 @@ const char* fa_status_string(fa_status_t status) {
 int fa_last_cuda_error(void) { return t_last_cuda_error; }
 
 }  // extern "C"
+
+#include "fa_varlen_api.cuh"

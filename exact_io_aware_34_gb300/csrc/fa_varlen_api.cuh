@@ -1,0 +1,236 @@
+// Entry points for packed sequences of different lengths (declared in
+// include/fa.h): argument checks, descriptors, workspace layout, launches.
+// Part of fa_api.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+// A tensor [T, heads, d] with element strides for T and heads (d contiguous).
+struct Rows {
+  const void* p;
+  int T, heads, d;
+  long long st, sh;
+  int elem;                       // bytes per element
+
+  // Bytes from the first element to behind the last, and of one token's heads.
+  long long row_span() const { return ((heads - 1) * sh + d) * elem; }
+  long long span() const { return (T - 1) * st * elem + row_span(); }
+};
+
+// Fills strides in (NULL: contiguous [T, heads, d]) and checks what a TMA
+// descriptor and 16-byte accesses need: positive strides, whole 16-byte units,
+// below 2^40 bytes. The stride of a dimension of one entry is never used.
+bool make_rows(Rows* r, const void* p, int T, int heads, int d, const fa_strides_t* s, int elem = 2) {
+  *r = Rows{p, T, heads, d, s ? s->token : static_cast<long long>(heads) * d, s ? s->head : d, elem};
+  if (T == 1) r->st = static_cast<long long>(heads) * d;
+  if (heads == 1) r->sh = d;
+  if (T == 1 && heads > 1) r->st = heads * r->sh;
+  for (long long v : {r->st, r->sh})
+    if (v <= 0 || v * elem % 16 != 0 || v >= (1LL << 39)) return false;
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0;
+}
+
+// No two elements of a written tensor share an address.
+bool rows_distinct(const Rows& r) {
+  const bool heads_in = r.sh >= r.d && r.st >= (r.heads - 1) * r.sh + r.d;
+  const bool tokens_in = r.st >= r.d && r.sh >= (r.T - 1) * r.st + r.d;
+  return heads_in || tokens_in;
+}
+
+// Whether two tensors may share an element. Tensors that are column ranges of
+// one wider buffer (equal token strides, each token's heads inside one stride)
+// are told apart by their place within the stride; others by their extents.
+bool rows_overlap(const Rows& a, const Rows& b) {
+  const auto x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  if (!(x < y + b.span() && y < x + a.span())) return false;
+  const long long sa = a.st * a.elem, sb = b.st * b.elem;
+  if (sa == sb && a.row_span() <= sa && b.row_span() <= sa) {
+    const long long off = ((static_cast<long long>(x - y) % sa) + sa) % sa;   // a's place after b's, modulo the stride
+    return !(off >= b.row_span() && sa - off >= a.row_span());
+  }
+  return true;
+}
+
+bool rows_overlap(const Rows& a, const void* b, size_t nb) {
+  return overlaps(a.p, static_cast<size_t>(a.span()), b, nb);
+}
+
+// bf16 map [d][n1][n2] with element strides s1, s2; box 64 x b1 x b2, 128-byte swizzle.
+bool make_map_strided(CUtensorMap* m, const void* base, int d, int n1, long long s1, int n2, long long s2, int b1,
+                      int b2) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// |scale| * log2(e) for kernels that mask with -inf: never zero, so that a
+// masked score stays -inf (a finite score times 2^-126 counts as 0).
+float masked_scale_log2(float scale) {
+  return std::max(static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634074), 1.17549435e-38f);
+}
+
+// Sizes every entry point for packed sequences accepts.
+fa_status_t varlen_sizes(int B, int H, int H_kv, int T_q, int T_kv, int d, float scale, int causal) {
+  if (B < 1 || H < 1 || H_kv < 1 || T_q < 1 || T_kv < 1 || d < 1) return FA_ERR_INVALID_ARG;
+  if (B > (1 << 24) || H > 65535 || H % H_kv != 0) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(H) * T_q >= (1LL << 31) || static_cast<long long>(H_kv) * T_kv >= (1LL << 31))
+    return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (H / H_kv > 128) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+// Units (per K/V head) of the forward list: every sequence rounds up once.
+long long varlen_fwd_cap(int B, int H, int H_kv, int T_q) {
+  const int tp = 128 / (H / H_kv);
+  return T_q / (2 * tp) + static_cast<long long>(B);
+}
+
+size_t varlen_fwd_ws(int B, int H, int H_kv, int T_q) {
+  return sizeof(fa::VarPlan) + static_cast<size_t>(varlen_fwd_cap(B, H, H_kv, T_q)) * sizeof(fa::VarUnit);
+}
+
+template <int HD>
+fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const Rows& o, float* LSE, const int* cu_q,
+                              const int* cu_kv, int B, float scale, int causal, void* ws, int drop_load,
+                              unsigned long long timeout_ns, cudaStream_t stream) {
+  using C = fa::FwdCfg<HD>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= 64) return FA_ERR_UNSUPPORTED;
+  static std::once_flag once[64];
+  static cudaError_t attr_err[64];
+  static bool regs_ok[64];
+  std::call_once(once[dev], [&] {
+    attr_err[dev] = cudaFuncSetAttribute(fa::fa_varlen_fwd_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         C::kSmemBytes);
+    // The warpgroups' register split must fit the registers the block is
+    // launched with (see the forward launch).
+    cudaFuncAttributes fattr;
+    if (attr_err[dev] == cudaSuccess) attr_err[dev] = cudaFuncGetAttributes(&fattr, fa::fa_varlen_fwd_kernel<HD>);
+    regs_ok[dev] = attr_err[dev] == cudaSuccess && 8 * C::kRegsSoftmax + 4 * C::kRegsControl <= 12 * fattr.numRegs;
+  });
+  if (attr_err[dev] != cudaSuccess) return cuda_fail(attr_err[dev]);
+  if (!regs_ok[dev]) return FA_ERR_UNSUPPORTED;
+
+  const int H_kv = k.heads, G = q.heads / k.heads, tp = 128 / G;
+  CUtensorMap mq, mk, mv;
+  if (!make_map_strided(&mq, q.p, HD, q.heads, q.sh, q.T, q.st, G, tp) ||
+      !make_map_strided(&mk, k.p, HD, k.T, k.st, k.heads, k.sh, 128, 1) ||
+      !make_map_strided(&mv, v.p, HD, v.T, v.st, v.heads, v.sh, 128, 1))
+    return cuda_fail(cudaErrorInvalidValue);
+
+  const long long cap = varlen_fwd_cap(B, q.heads, H_kv, q.T);
+  auto* plan = static_cast<fa::VarPlan*>(ws);
+  auto* list = reinterpret_cast<fa::VarUnit*>(plan + 1);
+  fa::varlen_plan_kernel<<<1, fa::kPlanThreads, 0, stream>>>(cu_q, cu_kv, plan, list, B, q.T, k.T, tp, causal,
+                                                            static_cast<int>(cap));
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+
+  fa::VarParams p;
+  p.O = static_cast<__nv_bfloat16*>(const_cast<void*>(o.p));
+  p.LSE = LSE;
+  p.plan = plan;
+  p.list = list;
+  p.o_st = o.st;
+  p.o_sh = o.sh;
+  p.T_q = q.T;
+  p.H_kv = H_kv;
+  p.G = G;
+  p.tp = tp;
+  p.causal = causal;
+  p.scale_log2 = masked_scale_log2(scale);
+  p.idesc_qk = C::kIdescQK | (scale < 0.f ? fa::ptx::kIdescNegateA : 0u);
+  p.timeout_ns = timeout_ns;
+  p.drop_load = drop_load;
+  // A programmatic dependent launch: the grid sets up while the list is made
+  // and waits for it on the device.
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(cap * H_kv, sm_count(dev))));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, fa::fa_varlen_fwd_kernel<HD>, mq, mk, mv, p);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return FA_OK;
+}
+
+fa_status_t varlen_fwd_impl(const void* Q, const void* K, const void* V, void* O, float* LSE, const int* cu_q,
+                            const int* cu_kv, int B, int H, int H_kv, int T_q, int T_kv, int d,
+                            const fa_strides_t* q_str, const fa_strides_t* k_str, const fa_strides_t* v_str,
+                            const fa_strides_t* o_str, float scale, int causal, void* workspace,
+                            size_t workspace_bytes, int drop_load, unsigned long long timeout_ns,
+                            cudaStream_t stream) {
+  if (!Q || !K || !V || !O || !LSE || !cu_q || !cu_kv) return FA_ERR_INVALID_ARG;
+  const fa_status_t st = varlen_sizes(B, H, H_kv, T_q, T_kv, d, scale, causal);
+  if (st != FA_OK) return st;
+  Rows q, k, v, o;
+  if (!make_rows(&q, Q, T_q, H, d, q_str) || !make_rows(&k, K, T_kv, H_kv, d, k_str) ||
+      !make_rows(&v, V, T_kv, H_kv, d, v_str) || !make_rows(&o, O, T_q, H, d, o_str) || !rows_distinct(o))
+    return FA_ERR_INVALID_ARG;
+  for (const void* ptr : {static_cast<const void*>(LSE), static_cast<const void*>(cu_q), static_cast<const void*>(cu_kv)})
+    if (reinterpret_cast<uintptr_t>(ptr) % 4 != 0) return FA_ERR_INVALID_ARG;
+  if (varlen_fwd_cap(B, H, H_kv, T_q) * H_kv >= (1LL << 31) - 65536) return FA_ERR_UNSUPPORTED;
+  const size_t need = varlen_fwd_ws(B, H, H_kv, T_q), n_lse = static_cast<size_t>(H) * T_q * 4;
+  const size_t n_cu = (static_cast<size_t>(B) + 1) * 4;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 128 != 0 || workspace_bytes < need)
+    return FA_ERR_INVALID_ARG;
+  // O, LSE and the workspace are disjoint from every input and each other.
+  for (const Rows* in : {&q, &k, &v})
+    if (rows_overlap(o, *in) || rows_overlap(*in, LSE, n_lse) || rows_overlap(*in, workspace, need))
+      return FA_ERR_INVALID_ARG;
+  if (rows_overlap(o, LSE, n_lse) || rows_overlap(o, workspace, need) || overlaps(LSE, n_lse, workspace, need))
+    return FA_ERR_INVALID_ARG;
+  for (const int* cu : {cu_q, cu_kv})
+    if (rows_overlap(o, cu, n_cu) || overlaps(LSE, n_lse, cu, n_cu) || overlaps(workspace, need, cu, n_cu))
+      return FA_ERR_INVALID_ARG;
+  if (d == 64)
+    return varlen_fwd_launch<64>(q, k, v, o, LSE, cu_q, cu_kv, B, scale, causal, workspace, drop_load, timeout_ns,
+                                 stream);
+  return varlen_fwd_launch<128>(q, k, v, o, LSE, cu_q, cu_kv, B, scale, causal, workspace, drop_load, timeout_ns,
+                                stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q) {
+  if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || H / H_kv > 128 || T_q < 1) return 0;
+  return varlen_fwd_ws(B, H, H_kv, T_q);
+}
+
+fa_status_t fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, float* LSE, const int* cu_q,
+                          const int* cu_kv, int B, int H, int H_kv, int T_q, int T_kv, int d,
+                          const fa_strides_t* q_strides, const fa_strides_t* k_strides, const fa_strides_t* v_strides,
+                          const fa_strides_t* o_strides, float scale, int causal, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
+  return varlen_fwd_impl(Q, K, V, O, LSE, cu_q, cu_kv, B, H, H_kv, T_q, T_kv, d, q_strides, k_strides, v_strides,
+                         o_strides, scale, causal, workspace, workspace_bytes, -1, kDefaultTimeoutNs, stream);
+}
+
+fa_status_t fa_fwd_varlen_fault_test(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                                     const int* cu_q, const int* cu_kv, int B, int H, int H_kv, int T_q, int T_kv,
+                                     int d, float scale, int causal, void* workspace, size_t workspace_bytes,
+                                     int drop_load, unsigned long long timeout_ns, cudaStream_t stream) {
+  if (timeout_ns == 0) return FA_ERR_INVALID_ARG;
+  return varlen_fwd_impl(Q, K, V, O, LSE, cu_q, cu_kv, B, H, H_kv, T_q, T_kv, d, nullptr, nullptr, nullptr, nullptr,
+                         scale, causal, workspace, workspace_bytes, drop_load < 0 ? -1 : drop_load, timeout_ns,
+                         stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,661 @@
+// Exact attention over packed sequences of different lengths, causal or not,
+// with shared K/V heads: the prompt (prefill) shape. sm_103a, tcgen05 + TMEM
+// + TMA.
+//
+// B sequences lie one behind the other in Q [T_q, H, d] and K, V
+// [T_kv, H_kv, d]; cu_q and cu_kv (device, B + 1 offsets each) say where each
+// begins. With n_q and n_kv its lengths, row i of a sequence sees key j of
+// the same sequence when j < n_kv and, if causal, j <= i + n_kv - n_q: the
+// last row sees every key, as when the first n_kv - n_q keys came from
+// earlier calls. The update per key block is the forward kernel's (online
+// softmax with a lazily moved maximum); O / l and LSE are unchanged by it. A
+// row that sees no key gets O = 0 and LSE = -inf.
+//
+// Packing. The G = H / H_kv query heads of a K/V head see the same keys, so a
+// tile's 128 rows are tp = 128 / G consecutive tokens x G heads (row
+// x * G + g; one TMA box {64, G, tp} of Q's [T_q][H][d] view loads them).
+// Against 128 tokens of one head, a unit of two tiles then spans 2 tp tokens
+// instead of 256: the keys past the diagonal that its blocks compute and mask
+// shrink with it, and a short sequence still fills its tiles. K and V are
+// read once per group. When G does not divide 128 the last rows of a tile
+// stay empty (126 of 128 used for G = 7).
+//
+// Work. A unit is two tiles of one (sequence, K/V head). varlen_plan_kernel
+// reads the offsets, lists the units of all sequences with the most key
+// blocks first, and zeroes a counter; the persistent grid takes units from
+// the list by that counter, so the long units start first and the short ones
+// fill the end. Lengths never reach the host: a captured call may be replayed
+// with other offsets of the same totals.
+//
+// Masking. Keys past a row's limit get the score -inf before the maximum and
+// the exponential. (scale = 0 is run as 2^-126: then -inf stays -inf and a
+// finite score counts as 0.) Rows of the V tile past the sequence's end
+// belong to the next sequence, or to nobody, and could hold infinities or
+// NaN, which a probability of zero does not cancel: they are zeroed in shared
+// memory before P V.
+//
+// Warp roles: the forward kernel's (warps 0-7 softmax and epilogue of tiles 0
+// and 1, warp 8 TMA producer, warp 9 MMA issuer), and warp 10 fetches units
+// one ahead and hands them to the others through a two-slot ring.
+#pragma once
+
+#include "fa_fwd_kernel.cuh"
+
+namespace fa {
+
+enum : unsigned int { kRoleVarProducer = 13, kRoleVarMma = 14, kRoleVarSoftmax = 15, kRoleVarFetch = 16 };
+
+// Words of g_status_word: 1 a wait ran out of time, 2 offsets or lengths in
+// device memory that do not describe the caller's buffers.
+constexpr unsigned int kStatusBadOffsets = 2;
+
+struct VarUnit {
+  int q_row0;     // first token of the unit in Q / O
+  int n_tok;      // tokens of the sequence from there on (may exceed the unit's 2 tp)
+  int kv_row0;    // first token of the sequence in K / V
+  int n_kv;       // its keys
+  int lim0;       // keys the first token sees, before clamping to [0, n_kv] (n_kv when not causal)
+  int nb0, nb1;   // key blocks of tiles 0 and 1 (1 <= nb0 <= nb1; a tile that sees nothing masks one block)
+  int pad;
+};
+
+struct VarPlan {          // head of the workspace; the list follows
+  int num_units;          // entries of the list (each stands for H_kv units)
+  int next;               // units handed out beyond the grid's first
+  int pad[6];
+};
+
+struct VarParams {
+  __nv_bfloat16* O;
+  float* LSE;             // [H][T_q]
+  VarPlan* plan;
+  const VarUnit* list;
+  long long o_st, o_sh;   // element strides of O (token, head)
+  int T_q;
+  int H_kv;
+  int G;                  // query heads per K/V head
+  int tp;                 // tokens per tile: 128 / G
+  int causal;
+  float scale_log2;       // |scale| * log2(e), at least 2^-126
+  uint32_t idesc_qk;
+  unsigned long long timeout_ns;
+  int drop_load;
+};
+
+// ---------------------------------------------------------------- unit list
+// One CTA. Sequences are taken kSeqs at a time: a scan gives each sequence
+// its place among the chunk's units, then every thread takes units and finds
+// their sequence by bisection, so that one long sequence is spread over the
+// threads. Two rounds over the units: count per cost class, then place.
+// Classes are eighths of a power of two of the number of key blocks.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanClasses = 256;
+
+__device__ __forceinline__ int cost_class(int blocks) {
+  const int e = 31 - __clz(blocks);
+  const int m = e >= 3 ? (blocks >> (e - 3)) & 7 : (blocks << (3 - e)) & 7;
+  return min(kPlanClasses - 1, 8 * e + m);
+}
+
+struct SeqSpan {
+  int q0, nq, kv0, nkv;
+};
+
+// Offsets of sequence i; an entry that does not lie in its buffer counts as an
+// empty span and is reported through the device status word.
+__device__ __forceinline__ SeqSpan seq_span(const int* cu_q, const int* cu_kv, int i, int T_q, int T_kv) {
+  SeqSpan s;
+  s.q0 = cu_q[i];
+  s.kv0 = cu_kv[i];
+  const int q1 = cu_q[i + 1], kv1 = cu_kv[i + 1];
+  const bool q_ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= T_q, kv_ok = s.kv0 >= 0 && kv1 >= s.kv0 && kv1 <= T_kv;
+  s.nq = q_ok ? q1 - s.q0 : 0;
+  s.nkv = kv_ok ? kv1 - s.kv0 : 0;
+  if (!q_ok) s.q0 = 0;
+  if (!kv_ok) s.kv0 = 0;
+  if (!(q_ok && kv_ok) && atomicCAS(&g_status_word, 0u, kStatusBadOffsets) == 0u) {
+    g_status_info[0] = kRoleVarFetch;
+    g_status_info[1] = static_cast<unsigned int>(i);
+    g_status_info[2] = g_status_info[3] = 0u;
+  }
+  return s;
+}
+
+// Inclusive scan of one int per thread over the CTA; returns the total too.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int s = lane < kPlanThreads / 32 ? warp_sums[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane < kPlanThreads / 32) warp_sums[lane] = s;
+  }
+  __syncthreads();
+  if (warp > 0) v += warp_sums[warp - 1];
+  total = warp_sums[kPlanThreads / 32 - 1];
+  __syncthreads();
+  return v;
+}
+
+__device__ __forceinline__ VarUnit make_unit(const SeqSpan& s, int u, int tp, int causal) {
+  VarUnit r;
+  const int x0 = u * 2 * tp;
+  r.q_row0 = s.q0 + x0;
+  r.n_tok = s.nq - x0;
+  r.kv_row0 = s.kv0;
+  r.n_kv = s.nkv;
+  r.lim0 = causal ? x0 + 1 + s.nkv - s.nq : s.nkv;
+  const int step = causal ? 1 : 0;
+  const int last0 = min(s.nkv, r.lim0 + step * (min(tp, r.n_tok) - 1));
+  const int last1 = min(s.nkv, r.lim0 + step * (min(2 * tp, r.n_tok) - 1));
+  r.nb0 = max(1, (max(last0, 0) + 127) >> 7);
+  r.nb1 = max(1, (max(last1, 0) + 127) >> 7);
+  r.pad = 0;
+  return r;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+    varlen_plan_kernel(const int* __restrict__ cu_q, const int* __restrict__ cu_kv, VarPlan* __restrict__ plan,
+                       VarUnit* __restrict__ list, int B, int T_q, int T_kv, int tp, int causal, int cap) {
+  __shared__ int cum[kPlanThreads + 1];
+  __shared__ SeqSpan span[kPlanThreads];
+  __shared__ int hist[kPlanClasses];
+  __shared__ int warp_sums[kPlanThreads / 32];
+  // The grid that reads the list may be scheduled now; it waits for this one's end.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x;
+  if (tid < kPlanClasses) hist[tid] = 0;
+  const int unit_tok = 2 * tp;
+  int total = 0;
+  for (int round = 0; round < 2; ++round) {
+    for (int c0 = 0; c0 < B; c0 += kPlanThreads) {
+      int nu = 0, chunk;
+      if (round == 0 || B > kPlanThreads) {   // one chunk's spans stay for the second round
+        __syncthreads();
+        if (c0 + tid < B) {
+          span[tid] = seq_span(cu_q, cu_kv, c0 + tid, T_q, T_kv);
+          nu = span[tid].nq / unit_tok + (span[tid].nq % unit_tok != 0);
+        }
+        const int incl = block_scan(nu, warp_sums, chunk);
+        cum[tid + 1] = incl;
+        if (tid == 0) cum[0] = 0;
+        __syncthreads();
+      }
+      chunk = cum[kPlanThreads];
+      for (int e = tid; e < chunk; e += kPlanThreads) {
+        int lo = 0, hi = kPlanThreads - 1;    // the last sequence whose first unit is <= e
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (cum[mid] <= e) lo = mid; else hi = mid - 1;
+        }
+        const VarUnit u = make_unit(span[lo], e - cum[lo], tp, causal);
+        if (round == 0) {
+          atomicAdd(&hist[cost_class(u.nb1)], 1);
+        } else {
+          const int at = atomicAdd(&hist[cost_class(u.nb1)], 1);
+          if (at < cap) list[at] = u;   // (overlapping spans of broken offsets could exceed the list)
+        }
+      }
+      if (round == 0) total += chunk;
+    }
+    __syncthreads();
+    if (round == 0) {
+      // Places: the most expensive class first.
+      int sum;
+      const int mine = tid < kPlanClasses ? hist[kPlanClasses - 1 - tid] : 0;
+      const int incl = block_scan(mine, warp_sums, sum);
+      if (tid < kPlanClasses) hist[kPlanClasses - 1 - tid] = incl - mine;
+      __syncthreads();
+    }
+  }
+  if (tid == 0) {
+    plan->num_units = min(total, cap);
+    plan->next = 0;
+  }
+}
+
+// ---------------------------------------------------------------- forward
+// What the fetch warp hands to the other roles.
+struct VarJob {
+  VarUnit u;
+  int kvh;        // K/V head; -1: no more units
+};
+
+template <int HD>
+__global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
+    fa_varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const VarParams p) {
+  using C = FwdCfg<HD>;
+  constexpr int kPolls = HD == 128 ? 8 : 1;   // as in the forward kernel
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_q_full;
+  __shared__ __align__(8) uint64_t bar_q_empty;
+  __shared__ __align__(8) uint64_t bar_kv_full[C::kStages];
+  __shared__ __align__(8) uint64_t bar_kv_empty[C::kStages];
+  __shared__ __align__(8) uint64_t bar_s_full[2];
+  __shared__ __align__(8) uint64_t bar_p_full[2];
+  __shared__ __align__(8) uint64_t bar_p_half[2];
+  __shared__ __align__(8) uint64_t bar_o_full[2];
+  __shared__ __align__(8) uint64_t bar_job_full[2];
+  __shared__ __align__(8) uint64_t bar_job_empty[2];
+  __shared__ __align__(8) uint64_t bar_drain;
+  __shared__ __align__(16) VarJob jobs[2];
+  __shared__ uint32_t tmem_base_slot;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int box_rows = p.G * p.tp;            // rows of a tile that hold queries
+
+  const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sQ = smem_base;
+  const uint32_t sKV = smem_base + C::kSmemQ;
+  uint8_t* generic = smem_raw + (smem_base - ptx::smem_u32(smem_raw));
+
+  // Rows of the Q tiles that no query fills stay zero for the kernel's life.
+  for (int c = 0; c < C::kQTiles * C::kChunks; ++c)
+    for (int i = threadIdx.x; i < (C::kBM - box_rows) * 8; i += C::kThreads)
+      reinterpret_cast<uint4*>(generic + c * C::kChunkBytes + box_rows * 128)[i] = make_uint4(0u, 0u, 0u, 0u);
+  ptx::fence_proxy_async_smem();
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(ptx::smem_u32(&bar_q_full), 1);
+    ptx::mbar_init(ptx::smem_u32(&bar_q_empty), 1);
+    for (int s = 0; s < C::kStages; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&bar_kv_full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bar_kv_empty[s]), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(ptx::smem_u32(&bar_s_full[t]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bar_p_full[t]), C::kBM);
+      ptx::mbar_init(ptx::smem_u32(&bar_p_half[t]), C::kBM);
+      ptx::mbar_init(ptx::smem_u32(&bar_o_full[t]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bar_job_full[t]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bar_job_empty[t]), 10);   // producer, issuer, eight softmax warps
+    }
+    ptx::mbar_init(ptx::smem_u32(&bar_drain), 1);
+    abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(ptx::smem_u32(&tmem_base_slot), C::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    ptx::prefetch_tmap(&tmQ);
+    ptx::prefetch_tmap(&tmK);
+    ptx::prefetch_tmap(&tmV);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = tmem_base_slot;
+  volatile int* abort_ptr = &abort_flag;
+
+  if (warp >= 8) ptx::setmaxnreg_dec<C::kRegsControl>();
+  if (warp == 10) {
+    // ------------------------------------------------------------ unit fetch
+    if (lane == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");   // the list is complete and visible
+      const int total = p.plan->num_units * p.H_kv;
+      int idx = blockIdx.x;
+      for (int n = 0;; ++n) {
+        VarJob job;
+        job.kvh = -1;
+        if (idx < total) {
+          const int e = idx / p.H_kv;
+          job.kvh = idx - e * p.H_kv;
+          job.u = p.list[e];
+        }
+        if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
+                           kRoleVarFetch))
+          break;
+        jobs[n & 1] = job;
+        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
+        if (job.kvh < 0) break;
+        idx = static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t pol_q = ptx::policy_evict_first();
+      const uint64_t pol_kv = ptx::policy_evict_last();
+      const uint32_t q_full = ptx::smem_u32(&bar_q_full);
+      int it = 0;           // K/V loads so far (the ring position runs on across units)
+      int q_issued = 0;
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        ok = wait_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
+                                   kRoleVarProducer);
+        if (!ok) break;
+        const VarJob job = jobs[n & 1];
+        ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
+        if (job.kvh < 0) break;
+        if (n > 0 && !wait_or_abort<kPolls>(ptx::smem_u32(&bar_q_empty), (n - 1) & 1, abort_ptr, p.timeout_ns,
+                                            kRoleVarProducer)) {
+          ok = false;
+          break;
+        }
+        ptx::mbar_arrive_expect_tx(q_full, C::kQTiles * C::kChunks * 128 * box_rows);
+        for (int t = 0; t < C::kQTiles; ++t)
+          for (int c = 0; c < C::kChunks; ++c)
+            ptx::tma_load_3d(sQ + t * C::kTileBytes + c * C::kChunkBytes, &tmQ, q_full, c * 64, job.kvh * p.G,
+                             job.u.q_row0 + t * p.tp, pol_q);
+        q_issued = n + 1;
+        for (int j = 0; j < job.u.nb1 && ok; ++j) {
+          for (int kv = 0; kv < 2; ++kv) {
+            const int slot = it % C::kStages;
+            if (!wait_or_abort<kPolls>(ptx::smem_u32(&bar_kv_empty[slot]), ((it / C::kStages) & 1) ^ 1u, abort_ptr,
+                                       p.timeout_ns, kRoleVarProducer)) {
+              ok = false;
+              break;
+            }
+            const int me = it++;
+            if (me == p.drop_load) continue;   // test hook: this tile never arrives
+            const uint32_t full = ptx::smem_u32(&bar_kv_full[slot]);
+            ptx::mbar_arrive_expect_tx(full, C::kTileBytes);
+            const void* map = kv ? static_cast<const void*>(&tmV) : static_cast<const void*>(&tmK);
+            for (int c = 0; c < C::kChunks; ++c)
+              ptx::tma_load_3d(sKV + slot * C::kTileBytes + c * C::kChunkBytes, map, full, c * 64,
+                               job.u.kv_row0 + j * C::kBN, job.kvh, pol_kv);
+          }
+        }
+      }
+      if (!ok || *abort_ptr) {
+        // Let every copy this thread started land before the CTA exits.
+        if (q_issued > 0) drain_wait(q_full, (q_issued - 1) & 1, p.timeout_ns);
+        for (int i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
+          if (i != p.drop_load)
+            drain_wait(ptx::smem_u32(&bar_kv_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    auto issue_pv_half = [&](int t, int it, bool accumulate, int half) {
+      const uint64_t b_desc = ptx::desc_mnmajor_sw128(sKV + (it % C::kStages) * C::kTileBytes, C::kChunkBytes);
+      const uint32_t d_tmem = tmem_base + C::kColO + HD * t, a_tmem = tmem_base + C::kColS + 128 * t;
+      if (half == 0)
+        ptx::mma_ts_k64half_warp<0>(d_tmem, a_tmem, ptx::desc_lo(b_desc), ptx::desc_hi(b_desc), C::kIdescPV,
+                                    accumulate ? 1u : 0u);
+      else
+        ptx::mma_ts_k64half_warp<1>(d_tmem, a_tmem, ptx::desc_lo(b_desc), ptx::desc_hi(b_desc), C::kIdescPV, 1u);
+    };
+    auto issue_qk = [&](int t, int it) {
+      const uint64_t a_desc = ptx::desc_kmajor_sw128(sQ + t * C::kTileBytes);
+      const uint64_t b_desc = ptx::desc_kmajor_sw128(sKV + (it % C::kStages) * C::kTileBytes);
+      const uint32_t d_tmem = tmem_base + C::kColS + 128 * t;
+      if constexpr (HD == 128)
+        ptx::mma_ss_k128_warp(d_tmem, ptx::desc_lo(a_desc), ptx::desc_lo(b_desc), ptx::desc_hi(a_desc), p.idesc_qk, 0u);
+      else
+        ptx::mma_ss_k64_warp(d_tmem, ptx::desc_lo(a_desc), ptx::desc_lo(b_desc), ptx::desc_hi(a_desc), p.idesc_qk, 0u);
+    };
+    bool ok = true;
+    int it0 = 0;              // K/V loads of the units before this one
+    int g[2] = {0, 0};        // key blocks of each tile so far (phases of s_full, p_half, p_full)
+    for (int n = 0; ok; ++n) {
+      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
+                                      kRoleVarMma);
+      if (!ok) break;
+      const int kvh = jobs[n & 1].kvh;
+      const int nb0 = jobs[n & 1].u.nb0, nb1 = jobs[n & 1].u.nb1;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
+      if (kvh < 0) break;
+      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_q_full), n & 1, abort_ptr, p.timeout_ns, kRoleVarMma);
+      if (ok)
+        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[it0 % C::kStages]), (it0 / C::kStages) & 1,
+                                        abort_ptr, p.timeout_ns, kRoleVarMma);
+      // Step j: per tile P V of block j - 1, then Q K^T of block j. Every
+      // later K_{j+1} and V_j is waited for by the softmax warps before their
+      // first hand-off for block j.
+      for (int j = 0; j <= nb1 && ok; ++j) {
+        const int itK = it0 + 2 * j, itV = itK - 1;   // K_j and V_{j-1}
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int nb = t ? nb1 : nb0;
+          if (j > 0 && j <= nb) {
+            const uint32_t par = static_cast<uint32_t>(g[t] - 1) & 1u;
+            ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_half[t]), par, abort_ptr, p.timeout_ns, kRoleVarMma);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            issue_pv_half(t, itV, j > 1, 0);
+            ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_full[t]), par, abort_ptr, p.timeout_ns, kRoleVarMma);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            issue_pv_half(t, itV, true, 1);
+            if (j == nb) ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[t]));
+          }
+          if (t == 1 && j > 0) ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[itV % C::kStages]));
+          if (j < nb) {
+            issue_qk(t, itK);
+            ptx::mma_commit_warp(ptx::smem_u32(&bar_s_full[t]));
+            ++g[t];
+          }
+        }
+        if (ok && j < nb1) {
+          ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[itK % C::kStages]));
+          if (j == nb1 - 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty));
+        }
+      }
+      it0 += 2 * nb1;
+    }
+    if (!ok) {
+      // Wait for every MMA already issued before TMEM is freed.
+      ptx::mma_commit_warp(ptx::smem_u32(&bar_drain));
+      drain_wait(ptx::smem_u32(&bar_drain), 0, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax + epilogue
+    ptx::setmaxnreg_inc<C::kRegsSoftmax>();
+    const int t = warp >> 2;                 // query tile
+    const int quarter = warp & 3;            // TMEM lane quarter
+    const int row = quarter * 32 + lane;     // row within the tile: token row / G, head row % G
+    const int x = min(row / p.G, p.tp - 1);
+    const int hq = row - (row / p.G) * p.G;
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem_base + lane_addr + C::kColS + 128 * t;
+    const uint32_t tO = tmem_base + lane_addr + C::kColO + HD * t;
+    const float sl2 = p.scale_log2;
+    bool ok = true;
+    int it0 = 0, g = 0;
+    for (int n = 0; ok; ++n) {
+      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
+                                      kRoleVarSoftmax);
+      if (!ok) break;
+      const VarJob job = jobs[n & 1];
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
+      if (job.kvh < 0) break;
+      const int nb = t ? job.u.nb1 : job.u.nb0;
+      const int xt = t * p.tp + x;             // token of this row within the unit
+      // Keys this row sees. Rows past the sequence's end (never stored) take
+      // the last token's, so that they do not mask blocks the others need not.
+      const int limit =
+          p.causal ? max(0, min(job.u.n_kv, job.u.lim0 + min(xt, job.u.n_tok - 1))) : job.u.n_kv;
+      float m_use = -INFINITY;   // raw-score maximum the exponentials are taken against
+      float l = 0.f;             // running sum of exp, relative to m_use (for LSE)
+      float lo = 0.f;            // the same with each block's largest term as P V sees it (for O)
+      for (int j = 0; j < nb; ++j, ++g) {
+        const int itV = it0 + 2 * j + 1;
+        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[itV % C::kStages]), (itV / C::kStages) & 1,
+                                        abort_ptr, p.timeout_ns, kRoleVarSoftmax);
+        if (ok && j + 1 < job.u.nb1)
+          ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[(itV + 1) % C::kStages]),
+                                          ((itV + 1) / C::kStages) & 1, abort_ptr, p.timeout_ns, kRoleVarSoftmax);
+        if (!ok) break;
+        const int have = job.u.n_kv - j * C::kBN;    // keys of the sequence in this block
+        if (have < C::kBN && t == (j < job.u.nb0 ? 0 : 1)) {
+          // Whole 128-byte rows, so the swizzle does not matter. Tile 0's P V
+          // is issued first, so its warps clear V for both tiles.
+          uint8_t* v_tile = generic + C::kSmemQ + (itV % C::kStages) * C::kTileBytes;
+          const int first = max(have, 0);
+          for (int c = 0; c < C::kChunks; ++c)
+            for (int i = row; i < (C::kBN - first) * 8; i += C::kBM)
+              reinterpret_cast<uint4*>(v_tile + c * C::kChunkBytes + first * 128)[i] = make_uint4(0u, 0u, 0u, 0u);
+          ptx::fence_proxy_async_smem();
+        }
+        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_s_full[t]), g & 1, abort_ptr, p.timeout_ns,
+                                        kRoleVarSoftmax);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        uint32_t s[4][32];
+        float mr[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld32_max(tS + 32 * c, s[c], mr[c]);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          ptx::reg_fence32(s[c]);
+          ptx::reg_fence1(mr[c]);
+        }
+        const int valid = limit - j * C::kBN;        // keys of this block that this row sees
+        float mt;
+        if (__all_sync(0xffffffffu, valid >= C::kBN)) {
+          mt = ptx::max3(mr[0], mr[1], fmaxf(mr[2], mr[3]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= valid) s[c][i] = __float_as_uint(-INFINITY);
+          float mc[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int c = k >> 1, b = (k & 1) * 16;
+            mc[k] = fmaxf(__uint_as_float(s[c][b]), __uint_as_float(s[c][b + 1]));
+#pragma unroll
+            for (int i = 2; i < 16; i += 2)
+              mc[k] = ptx::max3(mc[k], __uint_as_float(s[c][b + i]), __uint_as_float(s[c][b + i + 1]));
+          }
+          mt = ptx::max3(ptx::max3(mc[0], mc[1], mc[2]), ptx::max3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
+        }
+        // A row sees keys from the first block on or none at all, so after
+        // block 0 the maximum is -inf only for a row that sees nothing.
+        float alpha = 1.f;
+        bool rescale_o = false;
+        if (j == 0) {
+          m_use = mt;
+        } else {
+          const bool need = (mt - m_use) * sl2 > kRescaleLog2;
+          rescale_o = __any_sync(0xffffffffu, need);
+          if (need) {
+            alpha = ptx::ex2_approx((m_use - mt) * sl2);
+            m_use = mt;
+          }
+        }
+        const uint64_t sl2x2 = ptx::f2_pack(sl2, sl2);
+        const float neg_m = m_use == -INFINITY ? 0.f : -m_use * sl2;
+        const uint64_t negmx2 = ptx::f2_pack(neg_m, neg_m);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t pk[2][32];
+        auto exponents = [&](int c) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float x0, x1;
+            ptx::f2_unpack(
+                ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])), sl2x2, negmx2), x0,
+                x1);
+            const float p0 = ptx::ex2_approx(x0);
+            const float p1 = ptx::ex2_approx(x1);
+            acc[(i >> 1) & 3] = ptx::f2_add(acc[(i >> 1) & 3], ptx::f2_pack(p0, p1));
+            pk[c >> 1][(c & 1) * 16 + (i >> 1)] = ptx::pack_bf16x2(p0, p1);
+          }
+        };
+        exponents(0);
+        exponents(1);
+        if (rescale_o) {
+#pragma unroll
+          for (int c = 0; c < HD / 32; ++c) {
+            uint32_t o[32];
+            ptx::tmem_ld32(tO + 32 * c, o);
+            ptx::tmem_ld_wait();
+            ptx::reg_fence32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            ptx::tmem_st32(tO + 32 * c, o);
+          }
+        }
+        ptx::tmem_st32(tS, pk[0]);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_u32(&bar_p_half[t]));
+        exponents(2);
+        exponents(3);
+        float sum;
+        {
+          float a0, a1, b0, b1;
+          ptx::f2_unpack(ptx::f2_add(acc[0], acc[1]), a0, a1);
+          ptx::f2_unpack(ptx::f2_add(acc[2], acc[3]), b0, b1);
+          sum = (a0 + a1) + (b0 + b1);
+        }
+        // P V sees every probability rounded to bf16; the block's largest
+        // enters O's normaliser rounded too, so that a row dominated by one
+        // key weights it exactly 1 (as in the forward kernel).
+        const float pmax = ptx::ex2_approx(fmaf(mt, sl2, neg_m));
+        l = l * alpha + sum;
+        lo = lo * alpha + (sum + (ptx::round_bf16(pmax) - pmax));
+        ptx::tmem_st32(tS + 32, pk[1]);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_u32(&bar_p_full[t]));
+      }
+      if (ok)
+        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_o_full[t]), n & 1, abort_ptr, p.timeout_ns,
+                                        kRoleVarSoftmax);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      it0 += 2 * job.u.nb1;
+      const bool live = row < box_rows && xt < job.u.n_tok;
+      const bool none = limit == 0;
+      const long long token = static_cast<long long>(job.u.q_row0) + xt;
+      const int head = job.kvh * p.G + hq;
+      const float inv_l = 1.f / lo;
+      __nv_bfloat16* orow = p.O + token * p.o_st + head * p.o_sh;
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t o[32];
+        ptx::tmem_ld32(tO + 32 * c, o);
+        ptx::tmem_ld_wait();
+        ptx::reg_fence32(o);
+        uint32_t packed[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          packed[i] =
+              none ? 0u : ptx::pack_bf16x2(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
+        if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            dst[v] = make_uint4(packed[4 * v], packed[4 * v + 1], packed[4 * v + 2], packed[4 * v + 3]);
+        }
+      }
+      if (live)
+        p.LSE[static_cast<long long>(head) * p.T_q + token] =
+            none ? -INFINITY : (m_use * sl2 + __log2f(l)) * 0.69314718055994530942f;
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+}
+
+}  // namespace fa

@@ -8,6 +8,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -28,9 +29,15 @@ EXPORTED = ("fa_fwd", "fa_get_device_status", "fa_status_string", "fa_last_cuda_
             "fa_naive_fwd", "fa_naive_workspace_bytes", "fa_naive_fwd_noalloc", "fa_bwd", "fa_bwd_workspace_bytes",
             "fa_bwd_fault_test", "fa_fwd_kv", "fa_fwd_kv_num_splits", "fa_fwd_kv_workspace_bytes",
             "fa_fwd_kv_fault_test", "fa_merge_partials", "fa_fwd_host", "fa_fwd_host_workspace_bytes",
-            "fa_fwd_kv_f32", "fa_fwd_kv_f32_workspace_bytes", "fa_fwd_launch_shape")
+            "fa_fwd_kv_f32", "fa_fwd_kv_f32_workspace_bytes", "fa_fwd_launch_shape",
+            "fa_fwd_varlen", "fa_fwd_varlen_workspace_bytes", "fa_fwd_varlen_fault_test")
 
 _lib = None
+
+
+class Strides(ctypes.Structure):
+    """fa_strides_t: element strides of a packed tensor [T, heads, d]."""
+    _fields_ = [("token", ctypes.c_longlong), ("head", ctypes.c_longlong)]
 
 
 class FaError(RuntimeError):
@@ -95,6 +102,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_fwd_launch_shape.restype = i
     lib.fa_merge_partials.argtypes = [vp, vp, vp, vp, i, ctypes.c_longlong, i, vp]
     lib.fa_merge_partials.restype = i
+    sz, st = ctypes.c_size_t, ctypes.POINTER(Strides)
+    lib.fa_fwd_varlen_workspace_bytes.argtypes = [i, i, i, i]
+    lib.fa_fwd_varlen_workspace_bytes.restype = sz
+    lib.fa_fwd_varlen.argtypes = [vp] * 7 + [i] * 6 + [st] * 4 + [f, i, vp, sz, vp]
+    lib.fa_fwd_varlen.restype = i
+    lib.fa_fwd_varlen_fault_test.argtypes = [vp] * 7 + [i] * 6 + [f, i, vp, sz, i, u64, vp]
+    lib.fa_fwd_varlen_fault_test.restype = i
     _lib = lib
     return lib
 
@@ -111,6 +125,19 @@ def _stream_handle(stream, device) -> int:
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on_stream(stream, device):
+    """Context in which ``device`` is current and allocations belong to
+    ``stream`` (None: torch's current stream of that device)."""
+    if stream is None:
+        return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) \
+            else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+    return torch.cuda.stream(stream)
 
 
 def _check_qkv(q, k, v):
@@ -429,6 +456,101 @@ def fa_bwd(q, k, v, o, do, lse, dq=None, dk=None, dv=None, scale: float | None =
     if st != FA_OK:
         raise FaError(st, "fa_bwd")
     return tuple(outs)
+
+
+def _check_packed(name, t, device, T=None, heads=None, d=None):
+    """A bf16 CUDA tensor [T, heads, d] with contiguous d; its Strides."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor [T, heads, d]")
+    shape = t.shape
+    if (T is not None and shape[0] != T) or (heads is not None and shape[1] != heads) \
+            or (d is not None and shape[2] != d):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{T}, {heads}, {d}]")
+    strides = t.stride()
+    if strides[2] != 1 and shape[2] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return Strides(strides[0], strides[1])
+
+
+def _check_offsets(name, t, device, n=None):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() \
+            or t.device != device or t.shape[0] < 2 or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of B + 1 offsets on {device}")
+
+
+def _check_lse(name, lse, shape, device):
+    if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or tuple(lse.shape) != shape \
+            or not lse.is_contiguous() or lse.device != device:
+        raise ValueError(f"{name} must be a contiguous float32 tensor {list(shape)} on {device}")
+
+
+def _workspace(workspace, need, device):
+    """(tensor, pointer, bytes) of the caller's workspace, or of a new one."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def fa_fwd_varlen_workspace_bytes(B: int, H: int, H_kv: int, T_q: int) -> int:
+    return int(load_library().fa_fwd_varlen_workspace_bytes(int(B), int(H), int(H_kv), int(T_q)))
+
+
+def fa_fwd_varlen(q, k, v, cu_q, cu_kv, o=None, lse=None, scale: float | None = None, causal: bool = True,
+                  workspace=None, stream=None):
+    """Attention over packed sequences of different lengths with shared K/V heads.
+
+    q: bf16 [T_q, H, d]; k, v: bf16 [T_kv, H_kv, d], H a multiple of H_kv. Only
+    d has to be contiguous: slices of one projection's output need no copy.
+    cu_q, cu_kv: int32 CUDA [B + 1]; sequence b has the query rows
+    [cu_q[b], cu_q[b+1]) and the keys [cu_kv[b], cu_kv[b+1]). With ``causal`` row
+    i of a sequence sees its keys j <= i + n_kv - n_q, else all of them; a row
+    that sees none gets o = 0 and lse = -inf. Rows of no sequence are not written.
+    The offsets stay on the device; ones outside the buffers are reported by
+    :func:`fa_get_device_status`. Returns (o bf16 [T_q, H, d], lse float32 [H, T_q]).
+    """
+    device = getattr(q, "device", None)
+    q_st = _check_packed("q", q, device)
+    T_q, H, d = q.shape
+    k_st = _check_packed("k", k, device, d=d)
+    T_kv, H_kv = k.shape[0], k.shape[1]
+    v_st = _check_packed("v", v, device, T_kv, H_kv, d)
+    _check_offsets("cu_q", cu_q, device)
+    _check_offsets("cu_kv", cu_kv, device, cu_q.shape[0])
+    B = cu_q.shape[0] - 1
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    lib = load_library()
+    with _on_stream(stream, device):
+        if o is None:
+            o = torch.empty((T_q, H, d), dtype=torch.bfloat16, device=device)
+        o_st = _check_packed("o", o, device, T_q, H, d)
+        if lse is None:
+            lse = torch.empty((H, T_q), dtype=torch.float32, device=device)
+        _check_lse("lse", lse, (H, T_q), device)
+        workspace, ws_ptr, ws_bytes = _workspace(workspace, lib.fa_fwd_varlen_workspace_bytes(B, H, H_kv, T_q), device)
+        st = lib.fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                               cu_q.data_ptr(), cu_kv.data_ptr(), B, H, H_kv, T_q, T_kv, d, q_st, k_st, v_st, o_st,
+                               scale, bool(causal), ws_ptr, ws_bytes, torch.cuda.current_stream(device).cuda_stream)
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_varlen")
+    return o, lse
+
+
+def fa_fwd_varlen_fault_test(q, k, v, o, lse, cu_q, cu_kv, scale: float, causal: bool, workspace, drop_load: int,
+                             timeout_ns: int, stream=None) -> int:
+    """Test hook of the C ABI (see include/fa.h): returns the raw status code."""
+    T_q, H, d = q.shape
+    lib = load_library()
+    with torch.cuda.device(q.device):
+        return int(lib.fa_fwd_varlen_fault_test(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu_q.data_ptr(), cu_kv.data_ptr(),
+            cu_q.shape[0] - 1, H, k.shape[1], T_q, k.shape[0], d, float(scale), bool(causal), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), int(drop_load), int(timeout_ns),
+            _stream_handle(stream, q.device)))
 
 
 def fa_bwd_fault_test(q, k, v, o, do, lse, dq, dk, dv, scale: float, workspace, drop_load: int, timeout_ns: int,

@@ -134,12 +134,15 @@ fa_status_t fa_fwd_host(const void* Qh, const void* Kh, const void* Vh, void* Oh
  * fa_get_device_status -- synchronise `stream`, then read and clear the
  * library's device status word on the current device. Returns FA_OK, or
  * FA_ERR_TIMEOUT if any kernel of this library on this device gave up on a
- * wait since the last call, or FA_ERR_CUDA if the synchronisation failed.
- * `info`, if not NULL, receives 4 words describing the first timeout:
+ * wait since the last call, or FA_ERR_INVALID_ARG if one found sequence
+ * offsets in device memory that do not lie in the caller's
+ * buffers (whichever came first), or FA_ERR_CUDA if the synchronisation failed.
+ * `info`, if not NULL, receives 4 words describing the first of them:
  * {role (forward: 1 producer, 2 mma, 3 softmax/epilogue; backward dQ CTA:
  * 4, 5, 6; backward dK/dV CTA: 7, 8, 9; short-query kernel of fa_fwd_kv:
- * 10, 11, 12, in the same order), blockIdx.x, blockIdx.y,
- * blockIdx.z}; all zero when there was none. (`info` is this library's
+ * 10, 11, 12, in the same order; fa_fwd_varlen: 13, 14, 15, and 16 for the
+ * warp that hands out work), blockIdx.x, blockIdx.y, blockIdx.z}, or {16,
+ * index of the sequence, 0, 0} for bad offsets; all zero when there was none. (`info` is this library's
  * addition for diagnosing a timeout; with info = NULL the call only reports
  * the status.)
  */
@@ -375,6 +378,75 @@ fa_status_t fa_bwd_fault_test(const void* Q, const void* K, const void* V, const
                               int B, int H, int N, int d, float scale,
                               void* workspace, size_t workspace_bytes,
                               int drop_load, unsigned long long timeout_ns, cudaStream_t stream);
+
+/* Element strides of a packed tensor [T, heads, d] whose d elements are
+ * contiguous. NULL in a call stands for {heads * d, d}. */
+typedef struct {
+  long long token;
+  long long head;
+} fa_strides_t;
+
+/*
+ * fa_fwd_varlen_workspace_bytes -- device workspace fa_fwd_varlen needs (the
+ * list of its units of work). 0 for sizes it rejects.
+ */
+size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q);
+
+/*
+ * fa_fwd_varlen -- the forward pass over B packed sequences of different
+ * lengths with shared K/V heads, causal or not: a batch of prompts, or of
+ * prompt pieces whose earlier tokens are already in the cache.
+ *   Q, O   : device, bf16 [T_q, H, d]; K, V : device, bf16 [T_kv, H_kv, d].
+ *            H is a multiple of H_kv with H / H_kv <= 128; query head h
+ *            attends to K/V head h / (H / H_kv).
+ *   LSE    : device, float32 [H, T_q], written (natural log).
+ *   cu_q, cu_kv : device, int32 [B + 1], not decreasing. Sequence b has the
+ *            query rows [cu_q[b], cu_q[b+1]) and the keys
+ *            [cu_kv[b], cu_kv[b+1]); either may be empty. They are read on
+ *            the device, in stream order: the host needs no lengths, and a
+ *            captured call may be replayed with other offsets.
+ *   causal : 1: with n_q and n_kv the lengths of its sequence, row i sees the
+ *            keys j <= i + n_kv - n_q (the last row sees all); 0: all n_kv.
+ *   q_strides, k_strides, v_strides, o_strides : NULL for contiguous tensors,
+ *            else positive multiples of 8 elements, so that slices of one
+ *            projection's output [T, H + 2 H_kv, d] or a head-major
+ *            [heads, T, d] need no copy.
+ *   workspace : device, fa_fwd_varlen_workspace_bytes(...) bytes at least,
+ *            128-byte aligned; overwritten. Calls that may run at the same
+ *            time (other streams, graph replays) need workspaces of their own.
+ * A row that sees no key gets O = 0 and LSE = -inf. Rows of no sequence
+ * (behind cu_q[B]) are not written, and no value outside a sequence reaches
+ * it, NaN and infinities included; within a sequence, a non-finite V row can
+ * reach earlier rows of its 128-key block although they do not see it.
+ * Offsets that do not lie in the buffers (negative, decreasing, past T_q or
+ * T_kv) empty that side of their sequence and are reported by
+ * fa_get_device_status as FA_ERR_INVALID_ARG.
+ * Two launches on `stream` (the unit list, then the attention as its
+ * programmatic dependent). Each row's result depends on its sequence alone,
+ * not on the batch around it, and is the same from run to run.
+ * Limits: T_q, T_kv >= 1, H * T_q and H_kv * T_kv below 2^31, d in {64, 128},
+ * scale finite. Q, K, V, O 16-byte, LSE and offsets 4-byte aligned; O, LSE and
+ * the workspace overlap no input nor each other. FA_ERR_UNSUPPORTED for other
+ * d or H / H_kv > 128, FA_ERR_INVALID_ARG for the rest.
+ */
+fa_status_t fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                          const int* cu_q, const int* cu_kv,
+                          int B, int H, int H_kv, int T_q, int T_kv, int d,
+                          const fa_strides_t* q_strides, const fa_strides_t* k_strides,
+                          const fa_strides_t* v_strides, const fa_strides_t* o_strides,
+                          float scale, int causal, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fa_fwd_varlen_fault_test -- TEST HOOK, not for production use. fa_fwd_varlen
+ * on contiguous tensors with every device-side wait limited to `timeout_ns`,
+ * and, when drop_load >= 0, the drop_load-th K/V tile load of every CTA
+ * skipped.
+ */
+fa_status_t fa_fwd_varlen_fault_test(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                                     const int* cu_q, const int* cu_kv,
+                                     int B, int H, int H_kv, int T_q, int T_kv, int d, float scale, int causal,
+                                     void* workspace, size_t workspace_bytes,
+                                     int drop_load, unsigned long long timeout_ns, cudaStream_t stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */

@@ -14,6 +14,12 @@ from .backward import (  # noqa: F401
     attention_bwd_recompute,
     naive_bf16_attention_bwd,
 )
+from .packed import (  # noqa: F401
+    attention_packed,
+    attention_packed_bwd,
+    attention_prefix,
+    masked_head,
+)
 from .gqa import (  # noqa: F401
     attention_gqa,
     attention_gqa_rows,

@@ -1,0 +1,265 @@
+"""fa_fwd_varlen against the float64 oracle, through the C ABI (needs a GB300).
+
+Tolerances, from the arithmetic: P V sees each probability rounded to bf16
+(off by at most 2^-8 of itself) and so is the largest one in O's normaliser;
+O is rounded once more. So |O - ref| <= 2^-8 (A + 2 |ref|) with A = P |V|, and
+float32 sums and exponentials add a few 2^-22 of A. LSE is float32: a score's
+sum of d products is off by at most d 2^-24 scale |q|.|k|, the rest by 2^-22
+steps of values below 32.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from exact_io_aware_34_gb300 import fa
+from tests import parity
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from exact_io_aware_34_gb300 import build
+    build.build()
+    fa.load_library()
+
+
+def offsets(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32)
+
+
+def draw(seed, *shapes):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(s, generator=g).to(torch.bfloat16) for s in shapes]
+
+
+def ok():
+    torch.cuda.synchronize()
+    st, info = fa.fa_get_device_status()
+    assert st == fa.FA_OK, (fa.fa_status_string(st), info)
+
+
+def check_o(o, ref, A, scale_up=1.0):
+    err = np.abs(parity.to64(o) - ref)
+    tol = 2.0 ** -8 * (A + 2 * np.abs(ref)) + 1e-5 * A + 1e-30
+    assert np.isfinite(parity.to64(o)).all()
+    assert (err <= tol * scale_up).all(), float((err / tol).max())
+
+
+def lse_tol(q, k, scale):
+    """Largest |scale| sum |q||k| of any pair, times d 2^-24, plus the exponentials' share."""
+    n = float(q.float().abs().amax() * k.float().abs().amax()) * abs(scale) * q.shape[-1] if q.numel() and k.numel() else 0
+    return n * q.shape[-1] * 2.0 ** -24 / 4 + 32 * 2.0 ** -22
+
+
+def check_lse(lse, ref, tol):
+    got = lse.double().cpu().numpy()
+    none = np.isneginf(ref)
+    assert np.array_equal(np.isneginf(got), none)
+    assert np.isfinite(got[~none]).all()
+    if (~none).any():
+        off = float(np.abs(got[~none] - ref[~none]).max())
+        assert off <= tol, off
+
+
+def check(q, k, v, ql, kl, causal, scale=None, **kw):
+    d = q.shape[-1]
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    cq, ck = offsets(ql), offsets(kl)
+    o, lse = fa.fa_fwd_varlen(q.cuda(), k.cuda(), v.cuda(), cq.cuda(), ck.cuda(), scale=scale, causal=causal, **kw)
+    ok()
+    n = int(cq[-1])
+    O, L, A = oracle.attention_packed(*(parity.to64(x) for x in (q, k, v)), cq.tolist(), ck.tolist(), scale, causal)
+    check_o(o[:n], O[:n], A[:n])
+    check_lse(lse[:, :n], L[:, :n], lse_tol(q, k, scale))
+    return o, lse
+
+
+LENS = [
+    ([1], [1]), ([37], [37]), ([128], [128]), ([129], [129]), ([300, 1, 64, 0, 257], None),
+    ([5, 1, 100], [700, 129, 100]),         # later pieces of prompts
+    ([10, 200, 3], [4, 0, 128]),            # rows that see nothing, a sequence without keys
+    ([0, 0, 7, 0], [3, 0, 260, 0]),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,H_kv,d", [(4, 1, 128), (8, 2, 64), (2, 2, 128), (7, 1, 64), (3, 1, 128)])
+@pytest.mark.parametrize("case", range(len(LENS)))
+def test_lengths(case, H, H_kv, d, causal):
+    ql, kl = LENS[case]
+    kl = kl or ql
+    q, k, v = draw(case * 100 + H + d, (sum(ql), H, d), (max(1, sum(kl)), H_kv, d), (max(1, sum(kl)), H_kv, d))
+    check(q, k, v, ql, kl, causal)
+
+
+@pytest.mark.parametrize("G", [1, 2, 5, 12, 16, 32, 64, 100, 128])
+def test_heads_per_group(G):
+    q, k, v = draw(G, (150, 2 * G, 64), (400, 2, 64), (400, 2, 64))
+    check(q, k, v, [3, 140, 7], [200, 141, 59], True)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_sequences(causal):
+    """More sequences than the plan's chunk, most of one to three tokens."""
+    r = np.random.default_rng(5)
+    ql = r.integers(0, 4, 1300)
+    kl = ql + r.integers(0, 3, 1300)
+    ql[700], kl[700] = 500, 700
+    q, k, v = draw(9, (int(ql.sum()), 2, 64), (int(kl.sum()), 1, 64), (int(kl.sum()), 1, 64))
+    check(q, k, v, ql.tolist(), kl.tolist(), causal)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.11, 3.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales(scale, d):
+    q, k, v = draw(17, (200, 4, d), (350, 2, d), (350, 2, d))
+    check(q, k, v, [150, 50], [200, 150], True, scale=scale)
+
+
+def test_layouts():
+    """Slices of one buffer, head-major tensors and outputs inside wider buffers: the same bits."""
+    H, Hk, d, ql = 8, 2, 128, [100, 201, 3]
+    T = sum(ql)
+    qkv, = draw(3, (T, H + 2 * Hk, d))
+    qkv = qkv.cuda()
+    q, k, v = qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:]
+    cu = offsets(ql).cuda()
+    o0, l0 = fa.fa_fwd_varlen(q.contiguous(), k.contiguous(), v.contiguous(), cu, cu)
+    o1, l1 = fa.fa_fwd_varlen(q, k, v, cu, cu)
+    heads = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v)]
+    wide = torch.full((T, H + 3, d + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    o2, l2 = fa.fa_fwd_varlen(*heads, cu, cu, o=wide[:, 1:H + 1, :d])
+    o3 = torch.empty(H, T, d, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    fa.fa_fwd_varlen(*heads, cu, cu, o=o3)
+    ok()
+    for o, l in ((o1, l1), (o2, l2), (o3, l0)):
+        assert torch.equal(o, o0) and torch.equal(l, l0)
+    wide[:, 1:H + 1, :d] = 7.0
+    assert bool((wide == 7.0).all())
+
+
+def test_foreign_rows_do_not_matter_and_stay():
+    """NaN and infinities in other sequences' and nobody's rows; rows behind the last sequence are not written."""
+    H, Hk, d = 4, 2, 128
+    q, k, v = draw(21, (300, H, d), (500, Hk, d), (500, Hk, d))
+    cq, ck = [0, 90, 90 + 70], [0, 130, 130 + 200]
+    clean = [x.clone() for x in (q, k, v)]
+    for x, y in ((q, float("nan")), (k, float("nan")), (v, float("inf"))):
+        x[160 if x is q else 330:] = y
+    k[:130], v[:130] = float("nan"), float("-inf")
+    cqd, ckd = (torch.tensor(c, dtype=torch.int32, device="cuda") for c in (cq, ck))
+    o = torch.full((300, H, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((H, 300), 5.0, device="cuda")
+    fa.fa_fwd_varlen(q.cuda(), k.cuda(), v.cuda(), cqd, ckd, o=o, lse=lse)
+    ok()
+    assert bool((o[160:] == 5).all()) and bool((lse[:, 160:] == 5).all())
+    o_ref, l_ref = fa.fa_fwd_varlen(*(x.cuda() for x in clean), cqd, ckd)
+    ok()
+    assert torch.equal(o[90:160], o_ref[90:160]) and torch.equal(lse[:, 90:160], l_ref[:, 90:160])
+    # the first sequence's last block holds the second's keys
+    q2, k2, v2 = (x.clone() for x in clean)
+    k2[130:], v2[130:] = float("nan"), float("nan")
+    o2, l2 = fa.fa_fwd_varlen(q2.cuda(), k2.cuda(), v2.cuda(), cqd, ckd, causal=False)
+    o3, l3 = fa.fa_fwd_varlen(*(x.cuda() for x in clean), cqd, ckd, causal=False)
+    ok()
+    assert torch.equal(o2[:90], o3[:90]) and torch.equal(l2[:, :90], l3[:, :90])
+
+
+def test_sequence_result_does_not_depend_on_the_batch():
+    q, k, v = (x.cuda() for x in draw(31, (700, 8, 128), (700, 2, 128), (700, 2, 128)))
+    cu = offsets([200, 300, 200]).cuda()
+    o, lse = fa.fa_fwd_varlen(q, k, v, cu, cu)
+    one = offsets([300]).cuda()
+    o1, l1 = fa.fa_fwd_varlen(q[200:500], k[200:500], v[200:500], one, one)
+    o2, l2 = fa.fa_fwd_varlen(q, k, v, cu, cu)
+    ok()
+    assert torch.equal(o[200:500], o1) and torch.equal(lse[:, 200:500], l1)
+    assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
+def test_graph_replayed_with_other_offsets_and_streams():
+    q, k, v = (x.cuda() for x in draw(33, (600, 4, 64), (600, 2, 64), (600, 2, 64)))
+    cu = offsets([600]).cuda()
+    o = torch.empty(600, 4, 64, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(4, 600, device="cuda")
+    ws = torch.empty(fa.fa_fwd_varlen_workspace_bytes(3, 4, 2, 600), dtype=torch.uint8, device="cuda")
+    cu3 = offsets([100, 250, 250]).cuda()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    fa.fa_fwd_varlen(q, k, v, cu3, cu3, o=o, lse=lse, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fa.fa_fwd_varlen(q, k, v, cu3, cu3, o=o, lse=lse, workspace=ws)
+    cu3.copy_(offsets([1, 599, 0]))
+    g.replay()
+    ref = fa.fa_fwd_varlen(q, k, v, offsets([1, 599, 0]).cuda(), offsets([1, 599, 0]).cuda(), stream=s.cuda_stream)
+    ok()
+    assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+    assert cu.shape[0] == 2
+
+
+def test_long_prompt_sampled_rows():
+    """8192 tokens, 32 heads on 8 (the 8k workload's sizes): rows of every block against the oracle."""
+    T, H, Hk, d = 8192, 32, 8, 128
+    q, k, v = draw(41, (T, H, d), (T, Hk, d), (T, Hk, d))
+    cu = offsets([T]).cuda()
+    o, lse = fa.fa_fwd_varlen(q.cuda(), k.cuda(), v.cuda(), cu, cu)
+    ok()
+    scale = 1 / math.sqrt(d)
+    for i in list(range(0, T, 509)) + [T - 1]:
+        h = (i * 7) % H
+        see = np.ones((1, i + 1), dtype=bool)
+        O, L, A, _ = oracle.masked_head(parity.to64(q[i:i + 1, h]), parity.to64(k[:i + 1, h // 4]),
+                                        parity.to64(v[:i + 1, h // 4]), scale, see)
+        check_o(o[i:i + 1, h], O, A)
+        check_lse(lse[h, i:i + 1], L, lse_tol(q, k, scale))
+
+
+@pytest.mark.parametrize("drop", [0, 1, 3])
+def test_dropped_load_times_out_cleanly(drop):
+    q, k, v = (x.cuda() for x in draw(51, (300, 4, 128), (300, 2, 128), (300, 2, 128)))
+    cu = offsets([300]).cuda()
+    o, lse = torch.zeros_like(q), torch.zeros(4, 300, device="cuda")
+    ws = torch.empty(fa.fa_fwd_varlen_workspace_bytes(1, 4, 2, 300), dtype=torch.uint8, device="cuda")
+    assert fa.fa_fwd_varlen_fault_test(q, k, v, o, lse, cu, cu, 0.1, True, ws, drop, 20_000_000) == fa.FA_OK
+    st, info = fa.fa_get_device_status()
+    assert st == fa.FA_ERR_TIMEOUT and info[0] in (13, 14, 15, 16), (st, info)
+    assert fa.fa_get_device_status()[0] == fa.FA_OK
+    check(q.cpu(), k.cpu(), v.cpu(), [300], [300], True)
+
+
+@pytest.mark.parametrize("bad", [[0, 50, 40, 100], [-1, 20, 40, 100], [0, 20, 40, 101], [0, 20, 1 << 30, 100]])
+def test_bad_offsets_are_reported_and_stay_inside(bad):
+    """The kernel's own checks turn them into empty sequences; nothing outside the tensors is touched."""
+    q, k, v = (x.cuda() for x in draw(61, (100, 4, 64), (100, 2, 64), (100, 2, 64)))
+    good = offsets([20, 20, 60]).cuda()
+    bad = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    room = torch.full((140, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    for cq, ck in ((bad, good), (good, bad), (bad, bad)):
+        fa.fa_fwd_varlen(q, k, v, cq, ck, o=room[20:120])
+        st, info = fa.fa_get_device_status()
+        assert st == fa.FA_ERR_INVALID_ARG and info[0] == 16 and info[1] < 3, (st, info)
+    assert bool((room[:20] == 3).all()) and bool((room[120:] == 3).all())
+    assert fa.fa_get_device_status()[0] == fa.FA_OK
+
+
+def test_binding_refusals():
+    q, k, v = (x.cuda() for x in draw(71, (10, 4, 64), (10, 2, 64), (10, 2, 64)))
+    cu = offsets([10]).cuda()
+    for args in [(q.float(), k, v, cu, cu), (q, k[:5], v, cu, cu), (q, k, v, cu.long(), cu), (q, k, v, cu.cpu(), cu),
+                 (q, k, v, cu, offsets([5, 5]).cuda()), (q[..., ::2], k[..., ::2], v[..., ::2], cu, cu),
+                 (q[0], k, v, cu, cu)]:
+        with pytest.raises(ValueError):
+            fa.fa_fwd_varlen(*args)
+    for kw in [dict(o=q.float()), dict(lse=torch.empty(10, 4, device="cuda")), dict(workspace=torch.empty(4096))]:
+        with pytest.raises(ValueError):
+            fa.fa_fwd_varlen(q, k, v, cu, cu, **kw)
+    with pytest.raises(fa.FaError):
+        fa.fa_fwd_varlen(q, k, v, cu, cu, o=q)
+    with pytest.raises(fa.FaError):
+        fa.fa_fwd_varlen(q, k, v, cu, cu, workspace=torch.empty(32, dtype=torch.uint8, device="cuda"))

@@ -1,0 +1,69 @@
+"""Packed-sequence entry points: argument checks on the host (CPU only). The
+addresses are never dereferenced: every call is rejected before any CUDA call."""
+import ctypes
+
+import pytest
+import torch
+
+from exact_io_aware_34_gb300 import build as fa_build
+from exact_io_aware_34_gb300 import fa
+
+A, GAP = 0x7F0000000000, 1 << 30
+
+
+@pytest.fixture(scope="module")
+def lib():
+    fa_build.build()
+    return fa.load_library()
+
+
+def fwd(lib, q_st=None, k_st=None, v_st=None, o_st=None, **kw):
+    a = dict(Q=A, K=A + GAP, V=A + 2 * GAP, O=A + 3 * GAP, L=A + 4 * GAP, cq=A + 5 * GAP, ck=A + 6 * GAP, B=2, H=8,
+             H_kv=2, Tq=100, Tk=200, d=128, scale=0.1, causal=1, ws=A + 7 * GAP, n=1 << 20)
+    a.update(kw)
+    st = [ctypes.byref(fa.Strides(*s)) if s else None for s in (q_st, k_st, v_st, o_st)]
+    return lib.fa_fwd_varlen(a["Q"], a["K"], a["V"], a["O"], a["L"], a["cq"], a["ck"], a["B"], a["H"], a["H_kv"],
+                             a["Tq"], a["Tk"], a["d"], *st, a["scale"], a["causal"], a["ws"], a["n"], None)
+
+
+BAD, NO = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw,expect", [
+    *[({n: 0}, BAD) for n in ("Q", "K", "V", "O", "L", "cq", "ck", "ws", "B", "H", "H_kv", "Tq", "Tk", "d")],
+    (dict(H=7), BAD), (dict(H=1 << 16, H_kv=1 << 16), BAD), (dict(B=(1 << 24) + 1), BAD),
+    (dict(Tq=1 << 28), BAD), (dict(Tk=1 << 30), BAD), (dict(causal=2), BAD),
+    (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD),
+    (dict(d=96), NO), (dict(H=258, H_kv=2), NO),
+    (dict(Q=A + 8), BAD), (dict(O=A + 3 * GAP + 2), BAD), (dict(L=A + 4 * GAP + 2), BAD),
+    (dict(cq=A + 5 * GAP + 1), BAD), (dict(ws=A + 7 * GAP + 64), BAD), (dict(n=100), BAD),
+    (dict(O=A), BAD), (dict(O=A + GAP + 256), BAD), (dict(L=A + 2 * GAP), BAD), (dict(ws=A + 3 * GAP), BAD),
+    (dict(ws=A + 4 * GAP), BAD), (dict(cq=A + 3 * GAP), BAD), (dict(ck=A + 4 * GAP), BAD), (dict(ck=A + 7 * GAP), BAD),
+    (dict(q_st=(1024, 132)), BAD), (dict(q_st=(-1024, 128)), BAD), (dict(k_st=(0, 128)), BAD),
+    (dict(v_st=(1 << 39, 128)), BAD), (dict(o_st=(512, 128)), BAD),         # O's rows would share memory
+    (dict(o_st=(128, 128 * 99)), BAD),
+    # O as columns of the buffer that holds Q, overlapping Q's last head
+    (dict(q_st=(2048, 128), o_st=(2048, 128), O=A + 2 * 7 * 128), BAD),
+])
+def test_forward_refusals(lib, kw, expect):
+    assert fwd(lib, **kw) == expect
+
+
+def test_workspace_sizes(lib):
+    assert fa.fa_fwd_varlen_workspace_bytes(1, 8, 2, 1) > 0
+    for bad in [(0, 8, 2, 1), (1, 8, 3, 1), (1, 8, 0, 1), (1, 258, 2, 1), (1, 8, 2, 0)]:
+        assert fa.fa_fwd_varlen_workspace_bytes(*bad) == 0
+    assert fwd(lib, n=fa.fa_fwd_varlen_workspace_bytes(2, 8, 2, 100) - 1) == BAD
+
+
+def test_fault_hook_rejects_zero_timeout(lib):
+    assert lib.fa_fwd_varlen_fault_test(A, A + GAP, A + 2 * GAP, A + 3 * GAP, A + 4 * GAP, A + 5 * GAP, A + 6 * GAP, 1,
+                                        1, 1, 8, 8, 128, 0.1, 1, A + 7 * GAP, 1 << 20, 0, 0, None) == BAD
+
+
+def test_binding_refuses_cpu_tensors():
+    x, cu = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.tensor([0, 4], dtype=torch.int32)
+    with pytest.raises(ValueError):
+        fa.fa_fwd_varlen(x, x, x, cu, cu)
+    with pytest.raises(ValueError):
+        fa.fa_fwd_varlen(None, x, x, cu, cu)
