@@ -11,6 +11,8 @@ from .fa import (  # noqa: F401
     FA_ERR_UNSUPPORTED,
     FA_OK,
     FaError,
+    fa_bwd_varlen,
+    fa_bwd_varlen_workspace_bytes,
     fa_fwd,
     fa_fwd_fault_test,
     fa_fwd_varlen,

@@ -19,6 +19,7 @@
 #include "fa_bwd_kernel.cuh"
 #include "fa_decode_kernel.cuh"
 #include "fa_fwd_kernel.cuh"
+#include "fa_varlen_bwd_kernel.cuh"
 #include "fa_varlen_kernel.cuh"
 #include "naive_kernels.cuh"
 

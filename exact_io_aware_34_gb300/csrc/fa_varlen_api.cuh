@@ -131,8 +131,7 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   const long long cap = varlen_fwd_cap(B, q.heads, H_kv, q.T);
   auto* plan = static_cast<fa::VarPlan*>(ws);
   auto* list = reinterpret_cast<fa::VarUnit*>(plan + 1);
-  fa::varlen_plan_kernel<<<1, fa::kPlanThreads, 0, stream>>>(cu_q, cu_kv, plan, list, B, q.T, k.T, tp, causal,
-                                                            static_cast<int>(cap));
+  fa::varlen_plan_kernel<<<1, fa::kPlanThreads, 0, stream>>>(cu_q, cu_kv, plan, list, B, q.T, k.T, tp, causal);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
 
@@ -171,16 +170,16 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
 
 fa_status_t varlen_fwd_impl(const void* Q, const void* K, const void* V, void* O, float* LSE, const int* cu_q,
                             const int* cu_kv, int B, int H, int H_kv, int T_q, int T_kv, int d,
-                            const fa_strides_t* q_str, const fa_strides_t* k_str, const fa_strides_t* v_str,
-                            const fa_strides_t* o_str, float scale, int causal, void* workspace,
+                            const fa_strides_t* str, float scale, int causal, void* workspace,
                             size_t workspace_bytes, int drop_load, unsigned long long timeout_ns,
                             cudaStream_t stream) {
   if (!Q || !K || !V || !O || !LSE || !cu_q || !cu_kv) return FA_ERR_INVALID_ARG;
   const fa_status_t st = varlen_sizes(B, H, H_kv, T_q, T_kv, d, scale, causal);
   if (st != FA_OK) return st;
   Rows q, k, v, o;
-  if (!make_rows(&q, Q, T_q, H, d, q_str) || !make_rows(&k, K, T_kv, H_kv, d, k_str) ||
-      !make_rows(&v, V, T_kv, H_kv, d, v_str) || !make_rows(&o, O, T_q, H, d, o_str) || !rows_distinct(o))
+  if (!make_rows(&q, Q, T_q, H, d, str) || !make_rows(&k, K, T_kv, H_kv, d, str ? str + 1 : nullptr) ||
+      !make_rows(&v, V, T_kv, H_kv, d, str ? str + 2 : nullptr) ||
+      !make_rows(&o, O, T_q, H, d, str ? str + 3 : nullptr) || !rows_distinct(o))
     return FA_ERR_INVALID_ARG;
   for (const void* ptr : {static_cast<const void*>(LSE), static_cast<const void*>(cu_q), static_cast<const void*>(cu_kv)})
     if (reinterpret_cast<uintptr_t>(ptr) % 4 != 0) return FA_ERR_INVALID_ARG;
@@ -205,6 +204,159 @@ fa_status_t varlen_fwd_impl(const void* Q, const void* K, const void* V, void* O
                                 stream);
 }
 
+// ---------------------------------------------------------------- backward
+// Workspace: plan, unit list, query tiles, then -LSE log2(e) and -D per tile row.
+struct VarBwdLayout {
+  long long tiles, units;          // upper bounds (per K/V head)
+  size_t list, tile_list, nlse2, ndelta, bytes;
+};
+
+VarBwdLayout varlen_bwd_layout(int B, int H, int H_kv, int T_q, int T_kv) {
+  const int tp = 128 / (H / H_kv);
+  auto up = [](size_t n) { return (n + 127) / 128 * 128; };
+  VarBwdLayout w;
+  w.tiles = T_q / tp + static_cast<long long>(B);
+  w.units = w.tiles + T_kv / 128 + B;
+  const size_t rows = static_cast<size_t>(H_kv) * w.tiles * 128 * 4;
+  w.list = up(sizeof(fa::VarBwdPlan));
+  w.tile_list = w.list + up(static_cast<size_t>(w.units) * sizeof(fa::VarBwdUnit));
+  w.nlse2 = w.tile_list + up(static_cast<size_t>(w.tiles) * sizeof(int2));
+  w.ndelta = w.nlse2 + rows;
+  w.bytes = w.ndelta + rows;
+  return w;
+}
+
+template <int HD>
+fa_status_t varlen_bwd_launch(const Rows& q, const Rows& k, const Rows& v, const Rows& o, const Rows& go,
+                              const float* LSE, const Rows& dq, const Rows& dk, const Rows& dv, const int* cu_q,
+                              const int* cu_kv, int B, float scale, int causal, const VarBwdLayout& w, void* workspace,
+                              int drop_load, unsigned long long timeout_ns, cudaStream_t stream) {
+  using C = fa::BwdCfg<HD>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= 64) return FA_ERR_UNSUPPORTED;
+  static std::once_flag once[64];
+  static cudaError_t attr_err[64];
+  constexpr int kSmem = fa::DqCfg<HD>::kSmemBytes > C::kSmemBytes ? fa::DqCfg<HD>::kSmemBytes : C::kSmemBytes;
+  std::call_once(once[dev], [&] {
+    attr_err[dev] =
+        cudaFuncSetAttribute(fa::fa_varlen_bwd_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  });
+  if (attr_err[dev] != cudaSuccess) return cuda_fail(attr_err[dev]);
+
+  const int H_kv = k.heads, G = q.heads / k.heads, tp = 128 / G;
+  CUtensorMap mq, mk, mv, mdo;
+  if (!make_map_strided(&mq, q.p, HD, q.heads, q.sh, q.T, q.st, G, tp) ||
+      !make_map_strided(&mdo, go.p, HD, go.heads, go.sh, go.T, go.st, G, tp) ||
+      !make_map_strided(&mk, k.p, HD, k.T, k.st, k.heads, k.sh, 128, 1) ||
+      !make_map_strided(&mv, v.p, HD, v.T, v.st, v.heads, v.sh, 128, 1))
+    return cuda_fail(cudaErrorInvalidValue);
+
+  char* ws = static_cast<char*>(workspace);
+  auto* plan = reinterpret_cast<fa::VarBwdPlan*>(ws);
+  auto* list = reinterpret_cast<fa::VarBwdUnit*>(ws + w.list);
+  auto* tiles = reinterpret_cast<int2*>(ws + w.tile_list);
+  auto* nlse2 = reinterpret_cast<float*>(ws + w.nlse2);
+  auto* ndelta = reinterpret_cast<float*>(ws + w.ndelta);
+  fa::varlen_bwd_plan_kernel<<<1, fa::kPlanThreads, 0, stream>>>(cu_q, cu_kv, plan, list, tiles, B, q.T, k.T, tp,
+                                                                causal);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+
+  // Each of the other two is a programmatic dependent of the launch before it.
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * w.tiles), static_cast<unsigned>(H_kv));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, fa::varlen_bwd_rows_kernel<HD>, static_cast<const __nv_bfloat16*>(o.p),
+                         static_cast<const __nv_bfloat16*>(go.p), LSE, static_cast<const fa::VarBwdPlan*>(plan),
+                         static_cast<const int2*>(tiles), nlse2, ndelta, o.st, o.sh, go.st, go.sh, q.T,
+                         static_cast<int>(w.tiles), G);
+  if (e != cudaSuccess) return cuda_fail(e);
+
+  fa::VarBwdParams p;
+  p.dQ = static_cast<__nv_bfloat16*>(const_cast<void*>(dq.p));
+  p.dK = static_cast<__nv_bfloat16*>(const_cast<void*>(dk.p));
+  p.dV = static_cast<__nv_bfloat16*>(const_cast<void*>(dv.p));
+  p.dq_st = dq.st;
+  p.dq_sh = dq.sh;
+  p.dk_st = dk.st;
+  p.dk_sh = dk.sh;
+  p.dv_st = dv.st;
+  p.dv_sh = dv.sh;
+  p.plan = plan;
+  p.list = list;
+  p.nlse2 = nlse2;
+  p.ndelta = ndelta;
+  p.tile_cap = static_cast<int>(w.tiles);
+  p.H_kv = H_kv;
+  p.G = G;
+  p.tp = tp;
+  p.causal = causal;
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  p.scale = scale;
+  p.timeout_ns = timeout_ns;
+  p.drop_load = drop_load;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(w.units * H_kv, sm_count(dev))));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  e = cudaLaunchKernelEx(&cfg, fa::fa_varlen_bwd_kernel<HD>, mq, mk, mv, mdo, p);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return FA_OK;
+}
+
+fa_status_t varlen_bwd_impl(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                            const float* LSE, void* dQ, void* dK, void* dV, const int* cu_q, const int* cu_kv, int B,
+                            int H, int H_kv, int T_q, int T_kv, int d, const fa_strides_t* str, float scale,
+                            int causal, void* workspace, size_t workspace_bytes, int drop_load,
+                            unsigned long long timeout_ns, cudaStream_t stream) {
+  if (!Q || !K || !V || !O || !dO || !LSE || !dQ || !dK || !dV || !cu_q || !cu_kv) return FA_ERR_INVALID_ARG;
+  const fa_status_t st = varlen_sizes(B, H, H_kv, T_q, T_kv, d, scale, causal);
+  if (st != FA_OK) return st;
+  Rows in[5], out[3];   // Q K V O dO, dQ dK dV
+  const void* ptr[8] = {Q, K, V, O, dO, dQ, dK, dV};
+  const bool keys[8] = {false, true, true, false, false, false, true, true};
+  for (int a = 0; a < 8; ++a) {
+    Rows* r = a < 5 ? &in[a] : &out[a - 5];
+    if (!make_rows(r, ptr[a], keys[a] ? T_kv : T_q, keys[a] ? H_kv : H, d, str ? str + a : nullptr))
+      return FA_ERR_INVALID_ARG;
+    if (a >= 5 && !rows_distinct(*r)) return FA_ERR_INVALID_ARG;
+  }
+  for (const void* a : {static_cast<const void*>(LSE), static_cast<const void*>(cu_q), static_cast<const void*>(cu_kv)})
+    if (reinterpret_cast<uintptr_t>(a) % 4 != 0) return FA_ERR_INVALID_ARG;
+  const VarBwdLayout w = varlen_bwd_layout(B, H, H_kv, T_q, T_kv);
+  if (w.units * H_kv >= (1LL << 31) - 65536) return FA_ERR_UNSUPPORTED;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 128 != 0 || workspace_bytes < w.bytes)
+    return FA_ERR_INVALID_ARG;
+  // dQ, dK, dV and the workspace are disjoint from every input and each other.
+  const size_t n_lse = static_cast<size_t>(H) * T_q * 4, n_cu = (static_cast<size_t>(B) + 1) * 4;
+  for (int a = 0; a < 3; ++a) {
+    for (const Rows& r : in)
+      if (rows_overlap(out[a], r)) return FA_ERR_INVALID_ARG;
+    for (int b = a + 1; b < 3; ++b)
+      if (rows_overlap(out[a], out[b])) return FA_ERR_INVALID_ARG;
+    if (rows_overlap(out[a], LSE, n_lse) || rows_overlap(out[a], cu_q, n_cu) || rows_overlap(out[a], cu_kv, n_cu) ||
+        rows_overlap(out[a], workspace, w.bytes))
+      return FA_ERR_INVALID_ARG;
+  }
+  for (const Rows& r : in)
+    if (rows_overlap(r, workspace, w.bytes)) return FA_ERR_INVALID_ARG;
+  if (overlaps(workspace, w.bytes, LSE, n_lse) || overlaps(workspace, w.bytes, cu_q, n_cu) ||
+      overlaps(workspace, w.bytes, cu_kv, n_cu))
+    return FA_ERR_INVALID_ARG;
+  if (d == 64)
+    return varlen_bwd_launch<64>(in[0], in[1], in[2], in[3], in[4], LSE, out[0], out[1], out[2], cu_q, cu_kv, B, scale,
+                                 causal, w, workspace, drop_load, timeout_ns, stream);
+  return varlen_bwd_launch<128>(in[0], in[1], in[2], in[3], in[4], LSE, out[0], out[1], out[2], cu_q, cu_kv, B, scale,
+                                causal, w, workspace, drop_load, timeout_ns, stream);
+}
+
 }  // namespace
 
 extern "C" {
@@ -216,11 +368,10 @@ size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q) {
 
 fa_status_t fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, float* LSE, const int* cu_q,
                           const int* cu_kv, int B, int H, int H_kv, int T_q, int T_kv, int d,
-                          const fa_strides_t* q_strides, const fa_strides_t* k_strides, const fa_strides_t* v_strides,
-                          const fa_strides_t* o_strides, float scale, int causal, void* workspace,
+                          const fa_strides_t* strides, float scale, int causal, void* workspace,
                           size_t workspace_bytes, cudaStream_t stream) {
-  return varlen_fwd_impl(Q, K, V, O, LSE, cu_q, cu_kv, B, H, H_kv, T_q, T_kv, d, q_strides, k_strides, v_strides,
-                         o_strides, scale, causal, workspace, workspace_bytes, -1, kDefaultTimeoutNs, stream);
+  return varlen_fwd_impl(Q, K, V, O, LSE, cu_q, cu_kv, B, H, H_kv, T_q, T_kv, d, strides, scale, causal, workspace,
+                         workspace_bytes, -1, kDefaultTimeoutNs, stream);
 }
 
 fa_status_t fa_fwd_varlen_fault_test(const void* Q, const void* K, const void* V, void* O, float* LSE,
@@ -228,9 +379,31 @@ fa_status_t fa_fwd_varlen_fault_test(const void* Q, const void* K, const void* V
                                      int d, float scale, int causal, void* workspace, size_t workspace_bytes,
                                      int drop_load, unsigned long long timeout_ns, cudaStream_t stream) {
   if (timeout_ns == 0) return FA_ERR_INVALID_ARG;
-  return varlen_fwd_impl(Q, K, V, O, LSE, cu_q, cu_kv, B, H, H_kv, T_q, T_kv, d, nullptr, nullptr, nullptr, nullptr,
-                         scale, causal, workspace, workspace_bytes, drop_load < 0 ? -1 : drop_load, timeout_ns,
+  return varlen_fwd_impl(Q, K, V, O, LSE, cu_q, cu_kv, B, H, H_kv, T_q, T_kv, d, nullptr, scale, causal, workspace, workspace_bytes, drop_load < 0 ? -1 : drop_load, timeout_ns,
                          stream);
+}
+
+size_t fa_bwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q, int T_kv) {
+  if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || H / H_kv > 128 || T_q < 1 || T_kv < 1) return 0;
+  return varlen_bwd_layout(B, H, H_kv, T_q, T_kv).bytes;
+}
+
+fa_status_t fa_bwd_varlen(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                          const float* LSE, void* dQ, void* dK, void* dV, const int* cu_q, const int* cu_kv, int B,
+                          int H, int H_kv, int T_q, int T_kv, int d, const fa_strides_t* strides, float scale,
+                          int causal, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return varlen_bwd_impl(Q, K, V, O, dO, LSE, dQ, dK, dV, cu_q, cu_kv, B, H, H_kv, T_q, T_kv, d, strides, scale,
+                         causal, workspace, workspace_bytes, -1, kDefaultTimeoutNs, stream);
+}
+
+fa_status_t fa_bwd_varlen_fault_test(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                                     const float* LSE, void* dQ, void* dK, void* dV, const int* cu_q,
+                                     const int* cu_kv, int B, int H, int H_kv, int T_q, int T_kv, int d, float scale,
+                                     int causal, void* workspace, size_t workspace_bytes, int drop_load,
+                                     unsigned long long timeout_ns, cudaStream_t stream) {
+  if (timeout_ns == 0) return FA_ERR_INVALID_ARG;
+  return varlen_bwd_impl(Q, K, V, O, dO, LSE, dQ, dK, dV, cu_q, cu_kv, B, H, H_kv, T_q, T_kv, d, nullptr, scale,
+                         causal, workspace, workspace_bytes, drop_load < 0 ? -1 : drop_load, timeout_ns, stream);
 }
 
 }  // extern "C"

@@ -101,24 +101,31 @@ struct SeqSpan {
   int q0, nq, kv0, nkv;
 };
 
-// Offsets of sequence i; an entry that does not lie in its buffer counts as an
-// empty span and is reported through the device status word.
-__device__ __forceinline__ SeqSpan seq_span(const int* cu_q, const int* cu_kv, int i, int T_q, int T_kv) {
+__device__ __forceinline__ SeqSpan seq_span(const int* cu_q, const int* cu_kv, int i) {
   SeqSpan s;
   s.q0 = cu_q[i];
+  s.nq = cu_q[i + 1] - s.q0;
   s.kv0 = cu_kv[i];
-  const int q1 = cu_q[i + 1], kv1 = cu_kv[i + 1];
-  const bool q_ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= T_q, kv_ok = s.kv0 >= 0 && kv1 >= s.kv0 && kv1 <= T_kv;
-  s.nq = q_ok ? q1 - s.q0 : 0;
-  s.nkv = kv_ok ? kv1 - s.kv0 : 0;
-  if (!q_ok) s.q0 = 0;
-  if (!kv_ok) s.kv0 = 0;
-  if (!(q_ok && kv_ok) && atomicCAS(&g_status_word, 0u, kStatusBadOffsets) == 0u) {
-    g_status_info[0] = kRoleVarFetch;
-    g_status_info[1] = static_cast<unsigned int>(i);
-    g_status_info[2] = g_status_info[3] = 0u;
-  }
+  s.nkv = cu_kv[i + 1] - s.kv0;
   return s;
+}
+
+// Whether the offsets describe the caller's buffers: they start at 0 or later,
+// never decrease and end inside. If not, the call computes nothing and the
+// device status word says so. The same answer in every thread of the CTA.
+__device__ __forceinline__ bool offsets_ok(const int* cu_q, const int* cu_kv, int B, int T_q, int T_kv) {
+  bool bad = false;
+  for (int i = threadIdx.x; i < B; i += kPlanThreads) {
+    const int q0 = cu_q[i], q1 = cu_q[i + 1], k0 = cu_kv[i], k1 = cu_kv[i + 1];
+    const bool here = q0 < 0 || q1 < q0 || q1 > T_q || k0 < 0 || k1 < k0 || k1 > T_kv;
+    if (here && atomicCAS(&g_status_word, 0u, kStatusBadOffsets) == 0u) {
+      g_status_info[0] = kRoleVarFetch;
+      g_status_info[1] = static_cast<unsigned int>(i);
+      g_status_info[2] = g_status_info[3] = 0u;
+    }
+    bad |= here;
+  }
+  return !__syncthreads_or(bad);
 }
 
 // Inclusive scan of one int per thread over the CTA; returns the total too.
@@ -166,7 +173,7 @@ __device__ __forceinline__ VarUnit make_unit(const SeqSpan& s, int u, int tp, in
 
 __global__ void __launch_bounds__(kPlanThreads)
     varlen_plan_kernel(const int* __restrict__ cu_q, const int* __restrict__ cu_kv, VarPlan* __restrict__ plan,
-                       VarUnit* __restrict__ list, int B, int T_q, int T_kv, int tp, int causal, int cap) {
+                       VarUnit* __restrict__ list, int B, int T_q, int T_kv, int tp, int causal) {
   __shared__ int cum[kPlanThreads + 1];
   __shared__ SeqSpan span[kPlanThreads];
   __shared__ int hist[kPlanClasses];
@@ -174,6 +181,13 @@ __global__ void __launch_bounds__(kPlanThreads)
   // The grid that reads the list may be scheduled now; it waits for this one's end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
+  if (!offsets_ok(cu_q, cu_kv, B, T_q, T_kv)) {
+    if (tid == 0) {
+      plan->num_units = 0;
+      plan->next = 0;
+    }
+    return;
+  }
   if (tid < kPlanClasses) hist[tid] = 0;
   const int unit_tok = 2 * tp;
   int total = 0;
@@ -183,7 +197,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       if (round == 0 || B > kPlanThreads) {   // one chunk's spans stay for the second round
         __syncthreads();
         if (c0 + tid < B) {
-          span[tid] = seq_span(cu_q, cu_kv, c0 + tid, T_q, T_kv);
+          span[tid] = seq_span(cu_q, cu_kv, c0 + tid);
           nu = span[tid].nq / unit_tok + (span[tid].nq % unit_tok != 0);
         }
         const int incl = block_scan(nu, warp_sums, chunk);
@@ -202,8 +216,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         if (round == 0) {
           atomicAdd(&hist[cost_class(u.nb1)], 1);
         } else {
-          const int at = atomicAdd(&hist[cost_class(u.nb1)], 1);
-          if (at < cap) list[at] = u;   // (overlapping spans of broken offsets could exceed the list)
+          list[atomicAdd(&hist[cost_class(u.nb1)], 1)] = u;
         }
       }
       if (round == 0) total += chunk;
@@ -219,7 +232,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
   }
   if (tid == 0) {
-    plan->num_units = min(total, cap);
+    plan->num_units = total;
     plan->next = 0;
   }
 }

@@ -30,7 +30,8 @@ EXPORTED = ("fa_fwd", "fa_get_device_status", "fa_status_string", "fa_last_cuda_
             "fa_bwd_fault_test", "fa_fwd_kv", "fa_fwd_kv_num_splits", "fa_fwd_kv_workspace_bytes",
             "fa_fwd_kv_fault_test", "fa_merge_partials", "fa_fwd_host", "fa_fwd_host_workspace_bytes",
             "fa_fwd_kv_f32", "fa_fwd_kv_f32_workspace_bytes", "fa_fwd_launch_shape",
-            "fa_fwd_varlen", "fa_fwd_varlen_workspace_bytes", "fa_fwd_varlen_fault_test")
+            "fa_fwd_varlen", "fa_fwd_varlen_workspace_bytes", "fa_fwd_varlen_fault_test",
+            "fa_bwd_varlen", "fa_bwd_varlen_workspace_bytes", "fa_bwd_varlen_fault_test")
 
 _lib = None
 
@@ -105,10 +106,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     sz, st = ctypes.c_size_t, ctypes.POINTER(Strides)
     lib.fa_fwd_varlen_workspace_bytes.argtypes = [i, i, i, i]
     lib.fa_fwd_varlen_workspace_bytes.restype = sz
-    lib.fa_fwd_varlen.argtypes = [vp] * 7 + [i] * 6 + [st] * 4 + [f, i, vp, sz, vp]
+    lib.fa_fwd_varlen.argtypes = [vp] * 7 + [i] * 6 + [st, f, i, vp, sz, vp]
     lib.fa_fwd_varlen.restype = i
     lib.fa_fwd_varlen_fault_test.argtypes = [vp] * 7 + [i] * 6 + [f, i, vp, sz, i, u64, vp]
     lib.fa_fwd_varlen_fault_test.restype = i
+    lib.fa_bwd_varlen_workspace_bytes.argtypes = [i, i, i, i, i]
+    lib.fa_bwd_varlen_workspace_bytes.restype = sz
+    lib.fa_bwd_varlen.argtypes = [vp] * 11 + [i] * 6 + [st, f, i, vp, sz, vp]
+    lib.fa_bwd_varlen.restype = i
+    lib.fa_bwd_varlen_fault_test.argtypes = [vp] * 11 + [i] * 6 + [f, i, vp, sz, i, u64, vp]
+    lib.fa_bwd_varlen_fault_test.restype = i
     _lib = lib
     return lib
 
@@ -459,7 +466,7 @@ def fa_bwd(q, k, v, o, do, lse, dq=None, dk=None, dv=None, scale: float | None =
 
 
 def _check_packed(name, t, device, T=None, heads=None, d=None):
-    """A bf16 CUDA tensor [T, heads, d] with contiguous d; its Strides."""
+    """A bf16 CUDA tensor [T, heads, d] with contiguous d; its token and head strides."""
     if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_cuda:
         raise ValueError(f"{name} must be a bf16 CUDA tensor [T, heads, d]")
     shape = t.shape
@@ -471,7 +478,7 @@ def _check_packed(name, t, device, T=None, heads=None, d=None):
         raise ValueError(f"{name}: the last dimension must be contiguous")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    return Strides(strides[0], strides[1])
+    return strides[0], strides[1]
 
 
 def _check_offsets(name, t, device, n=None):
@@ -509,8 +516,8 @@ def fa_fwd_varlen(q, k, v, cu_q, cu_kv, o=None, lse=None, scale: float | None = 
     [cu_q[b], cu_q[b+1]) and the keys [cu_kv[b], cu_kv[b+1]). With ``causal`` row
     i of a sequence sees its keys j <= i + n_kv - n_q, else all of them; a row
     that sees none gets o = 0 and lse = -inf. Rows of no sequence are not written.
-    The offsets stay on the device; ones outside the buffers are reported by
-    :func:`fa_get_device_status`. Returns (o bf16 [T_q, H, d], lse float32 [H, T_q]).
+    The offsets stay on the device; with ones outside the buffers nothing is
+    written and :func:`fa_get_device_status` says so. Returns (o bf16 [T_q, H, d], lse float32 [H, T_q]).
     """
     device = getattr(q, "device", None)
     q_st = _check_packed("q", q, device)
@@ -533,8 +540,8 @@ def fa_fwd_varlen(q, k, v, cu_q, cu_kv, o=None, lse=None, scale: float | None = 
         _check_lse("lse", lse, (H, T_q), device)
         workspace, ws_ptr, ws_bytes = _workspace(workspace, lib.fa_fwd_varlen_workspace_bytes(B, H, H_kv, T_q), device)
         st = lib.fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                               cu_q.data_ptr(), cu_kv.data_ptr(), B, H, H_kv, T_q, T_kv, d, q_st, k_st, v_st, o_st,
-                               scale, bool(causal), ws_ptr, ws_bytes, torch.cuda.current_stream(device).cuda_stream)
+                               cu_q.data_ptr(), cu_kv.data_ptr(), B, H, H_kv, T_q, T_kv, d,
+                               (Strides * 4)(q_st, k_st, v_st, o_st), scale, bool(causal), ws_ptr, ws_bytes, torch.cuda.current_stream(device).cuda_stream)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_varlen")
     return o, lse
@@ -549,6 +556,64 @@ def fa_fwd_varlen_fault_test(q, k, v, o, lse, cu_q, cu_kv, scale: float, causal:
         return int(lib.fa_fwd_varlen_fault_test(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu_q.data_ptr(), cu_kv.data_ptr(),
             cu_q.shape[0] - 1, H, k.shape[1], T_q, k.shape[0], d, float(scale), bool(causal), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), int(drop_load), int(timeout_ns),
+            _stream_handle(stream, q.device)))
+
+
+def fa_bwd_varlen_workspace_bytes(B: int, H: int, H_kv: int, T_q: int, T_kv: int) -> int:
+    return int(load_library().fa_bwd_varlen_workspace_bytes(int(B), int(H), int(H_kv), int(T_q), int(T_kv)))
+
+
+def fa_bwd_varlen(q, k, v, o, do, lse, cu_q, cu_kv, dq=None, dk=None, dv=None, scale: float | None = None,
+                  causal: bool = True, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of <do, o> for :func:`fa_fwd_varlen`'s ``o``, from
+    its outputs ``o`` and ``lse``. do, dq: bf16 [T_q, H, d]; dk, dv: bf16
+    [T_kv, H_kv, d], summed over the query heads of a K/V head. Other arguments
+    as for the forward. Rows and keys of no sequence are not written."""
+    device = getattr(q, "device", None)
+    q_st = _check_packed("q", q, device)
+    T_q, H, d = q.shape
+    k_st = _check_packed("k", k, device, d=d)
+    T_kv, H_kv = k.shape[0], k.shape[1]
+    strides = [q_st, k_st, _check_packed("v", v, device, T_kv, H_kv, d), _check_packed("o", o, device, T_q, H, d),
+               _check_packed("do", do, device, T_q, H, d)]
+    _check_lse("lse", lse, (H, T_q), device)
+    _check_offsets("cu_q", cu_q, device)
+    _check_offsets("cu_kv", cu_kv, device, cu_q.shape[0])
+    B = cu_q.shape[0] - 1
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    lib = load_library()
+    with _on_stream(stream, device):
+        if dq is None:
+            dq = torch.empty((T_q, H, d), dtype=torch.bfloat16, device=device)
+        if dk is None:
+            dk = torch.empty((T_kv, H_kv, d), dtype=torch.bfloat16, device=device)
+        if dv is None:
+            dv = torch.empty((T_kv, H_kv, d), dtype=torch.bfloat16, device=device)
+        strides += [_check_packed("dq", dq, device, T_q, H, d), _check_packed("dk", dk, device, T_kv, H_kv, d),
+                    _check_packed("dv", dv, device, T_kv, H_kv, d)]
+        workspace, ws_ptr, ws_bytes = _workspace(
+            workspace, lib.fa_bwd_varlen_workspace_bytes(B, H, H_kv, T_q, T_kv), device)
+        st = lib.fa_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
+                               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_q.data_ptr(), cu_kv.data_ptr(), B, H,
+                               H_kv, T_q, T_kv, d, (Strides * 8)(*strides), scale, bool(causal), ws_ptr, ws_bytes,
+                               torch.cuda.current_stream(device).cuda_stream)
+    if st != FA_OK:
+        raise FaError(st, "fa_bwd_varlen")
+    return dq, dk, dv
+
+
+def fa_bwd_varlen_fault_test(q, k, v, o, do, lse, cu_q, cu_kv, dq, dk, dv, scale: float, causal: bool, workspace,
+                             drop_load: int, timeout_ns: int, stream=None) -> int:
+    """Test hook of the C ABI (see include/fa.h): returns the raw status code."""
+    T_q, H, d = q.shape
+    lib = load_library()
+    with torch.cuda.device(q.device):
+        return int(lib.fa_bwd_varlen_fault_test(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+            dk.data_ptr(), dv.data_ptr(), cu_q.data_ptr(), cu_kv.data_ptr(), cu_q.shape[0] - 1, H, k.shape[1], T_q,
+            k.shape[0], d, float(scale), bool(causal), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), int(drop_load), int(timeout_ns),
             _stream_handle(stream, q.device)))
 

@@ -141,7 +141,8 @@ fa_status_t fa_fwd_host(const void* Qh, const void* Kh, const void* Vh, void* Oh
  * {role (forward: 1 producer, 2 mma, 3 softmax/epilogue; backward dQ CTA:
  * 4, 5, 6; backward dK/dV CTA: 7, 8, 9; short-query kernel of fa_fwd_kv:
  * 10, 11, 12, in the same order; fa_fwd_varlen: 13, 14, 15, and 16 for the
- * warp that hands out work), blockIdx.x, blockIdx.y, blockIdx.z}, or {16,
+ * warp that hands out work; fa_bwd_varlen: query role 17, 18, 19, key-block
+ * role 20, 21, 22), blockIdx.x, blockIdx.y, blockIdx.z}, or {16,
  * index of the sequence, 0, 0} for bad offsets; all zero when there was none. (`info` is this library's
  * addition for diagnosing a timeout; with info = NULL the call only reports
  * the status.)
@@ -407,8 +408,8 @@ size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q);
  *            captured call may be replayed with other offsets.
  *   causal : 1: with n_q and n_kv the lengths of its sequence, row i sees the
  *            keys j <= i + n_kv - n_q (the last row sees all); 0: all n_kv.
- *   q_strides, k_strides, v_strides, o_strides : NULL for contiguous tensors,
- *            else positive multiples of 8 elements, so that slices of one
+ *   strides : NULL for contiguous tensors, else four entries (host), for Q, K,
+ *            V and O: positive multiples of 8 elements, so that slices of one
  *            projection's output [T, H + 2 H_kv, d] or a head-major
  *            [heads, T, d] need no copy.
  *   workspace : device, fa_fwd_varlen_workspace_bytes(...) bytes at least,
@@ -418,9 +419,9 @@ size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q);
  * (behind cu_q[B]) are not written, and no value outside a sequence reaches
  * it, NaN and infinities included; within a sequence, a non-finite V row can
  * reach earlier rows of its 128-key block although they do not see it.
- * Offsets that do not lie in the buffers (negative, decreasing, past T_q or
- * T_kv) empty that side of their sequence and are reported by
- * fa_get_device_status as FA_ERR_INVALID_ARG.
+ * With offsets that do not describe the buffers (negative, decreasing, past
+ * T_q or T_kv) nothing is written, and fa_get_device_status reports
+ * FA_ERR_INVALID_ARG.
  * Two launches on `stream` (the unit list, then the attention as its
  * programmatic dependent). Each row's result depends on its sequence alone,
  * not on the batch around it, and is the same from run to run.
@@ -432,9 +433,8 @@ size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q);
 fa_status_t fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, float* LSE,
                           const int* cu_q, const int* cu_kv,
                           int B, int H, int H_kv, int T_q, int T_kv, int d,
-                          const fa_strides_t* q_strides, const fa_strides_t* k_strides,
-                          const fa_strides_t* v_strides, const fa_strides_t* o_strides,
-                          float scale, int causal, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+                          const fa_strides_t* strides, float scale, int causal,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * fa_fwd_varlen_fault_test -- TEST HOOK, not for production use. fa_fwd_varlen
@@ -446,6 +446,54 @@ fa_status_t fa_fwd_varlen_fault_test(const void* Q, const void* K, const void* V
                                      const int* cu_q, const int* cu_kv,
                                      int B, int H, int H_kv, int T_q, int T_kv, int d, float scale, int causal,
                                      void* workspace, size_t workspace_bytes,
+                                     int drop_load, unsigned long long timeout_ns, cudaStream_t stream);
+
+/*
+ * fa_bwd_varlen_workspace_bytes -- device workspace fa_bwd_varlen needs: the
+ * list of its units of work and two float32 values per row of its query tiles.
+ * 0 for sizes it rejects.
+ */
+size_t fa_bwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q, int T_kv);
+
+/*
+ * fa_bwd_varlen -- gradients of <dO, O> for fa_fwd_varlen's O, by
+ * recomputation as in fa_bwd: with P = exp(scale Q K^T - LSE) on the visible
+ * pairs and D = rowsum(dO * O),
+ *     dV = sum_heads P^T dO,  dS = P * (dO V^T - D),
+ *     dQ = scale dS K,        dK = scale sum_heads dS^T Q,
+ * the sums running over the H / H_kv query heads of a K/V head.
+ *   Q, K, V, cu_q, cu_kv, B .. d, scale, causal : those of the forward call;
+ *   O, LSE  : its outputs, read only.
+ *   dO, dQ  : device, bf16 [T_q, H, d], read / written.
+ *   dK, dV  : device, bf16 [T_kv, H_kv, d], written.
+ *   strides : NULL, or eight entries (host) for Q, K, V, O, dO, dQ, dK, dV.
+ *   workspace : as for fa_fwd_varlen, fa_bwd_varlen_workspace_bytes(...) bytes.
+ * Rows that see no key and keys of a sequence without query rows get zero
+ * gradients. Rows and keys of no sequence are not written, and what they hold
+ * reaches no gradient, NaN and infinities included; values of a sequence's
+ * own rows and keys are taken to be finite. Accumulation is float32, in an
+ * order that depends on the sequence alone (no atomics), rounded once.
+ * Three launches on `stream`. Bad offsets, limits and errors as for
+ * fa_fwd_varlen; dQ, dK, dV and the workspace overlap no input nor each other
+ * (column ranges of one buffer are fine).
+ */
+fa_status_t fa_bwd_varlen(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                          const float* LSE, void* dQ, void* dK, void* dV, const int* cu_q, const int* cu_kv,
+                          int B, int H, int H_kv, int T_q, int T_kv, int d,
+                          const fa_strides_t* strides, float scale, int causal,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fa_bwd_varlen_fault_test -- TEST HOOK, not for production use. fa_bwd_varlen
+ * on contiguous tensors with every device-side wait limited to `timeout_ns`,
+ * and, when drop_load >= 0, a load skipped in every unit: in the query role the
+ * drop_load-th of K_0, V_0, K_1, ..., in the key-block role the Q and dO tiles
+ * of step drop_load.
+ */
+fa_status_t fa_bwd_varlen_fault_test(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                                     const float* LSE, void* dQ, void* dK, void* dV, const int* cu_q,
+                                     const int* cu_kv, int B, int H, int H_kv, int T_q, int T_kv, int d, float scale,
+                                     int causal, void* workspace, size_t workspace_bytes,
                                      int drop_load, unsigned long long timeout_ns, cudaStream_t stream);
 
 #ifdef __cplusplus

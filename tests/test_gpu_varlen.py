@@ -234,17 +234,17 @@ def test_dropped_load_times_out_cleanly(drop):
 
 
 @pytest.mark.parametrize("bad", [[0, 50, 40, 100], [-1, 20, 40, 100], [0, 20, 40, 101], [0, 20, 1 << 30, 100]])
-def test_bad_offsets_are_reported_and_stay_inside(bad):
-    """The kernel's own checks turn them into empty sequences; nothing outside the tensors is touched."""
+def test_bad_offsets_are_reported_and_write_nothing(bad):
+    """The plan's own check of the offsets finds them, lists no work and says so in the status word."""
     q, k, v = (x.cuda() for x in draw(61, (100, 4, 64), (100, 2, 64), (100, 2, 64)))
     good = offsets([20, 20, 60]).cuda()
     bad = torch.tensor(bad, dtype=torch.int32, device="cuda")
-    room = torch.full((140, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    o = torch.full((100, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
     for cq, ck in ((bad, good), (good, bad), (bad, bad)):
-        fa.fa_fwd_varlen(q, k, v, cq, ck, o=room[20:120])
+        fa.fa_fwd_varlen(q, k, v, cq, ck, o=o)
         st, info = fa.fa_get_device_status()
         assert st == fa.FA_ERR_INVALID_ARG and info[0] == 16 and info[1] < 3, (st, info)
-    assert bool((room[:20] == 3).all()) and bool((room[120:] == 3).all())
+    assert bool((o == 3).all())
     assert fa.fa_get_device_status()[0] == fa.FA_OK
 
 

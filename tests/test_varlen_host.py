@@ -1,7 +1,5 @@
 """Packed-sequence entry points: argument checks on the host (CPU only). The
 addresses are never dereferenced: every call is rejected before any CUDA call."""
-import ctypes
-
 import pytest
 import torch
 
@@ -21,9 +19,12 @@ def fwd(lib, q_st=None, k_st=None, v_st=None, o_st=None, **kw):
     a = dict(Q=A, K=A + GAP, V=A + 2 * GAP, O=A + 3 * GAP, L=A + 4 * GAP, cq=A + 5 * GAP, ck=A + 6 * GAP, B=2, H=8,
              H_kv=2, Tq=100, Tk=200, d=128, scale=0.1, causal=1, ws=A + 7 * GAP, n=1 << 20)
     a.update(kw)
-    st = [ctypes.byref(fa.Strides(*s)) if s else None for s in (q_st, k_st, v_st, o_st)]
+    st = None
+    if q_st or k_st or v_st or o_st:
+        dense = [(a["H"] * a["d"], a["d"]), (a["H_kv"] * a["d"], a["d"])]
+        st = (fa.Strides * 4)(q_st or dense[0], k_st or dense[1], v_st or dense[1], o_st or dense[0])
     return lib.fa_fwd_varlen(a["Q"], a["K"], a["V"], a["O"], a["L"], a["cq"], a["ck"], a["B"], a["H"], a["H_kv"],
-                             a["Tq"], a["Tk"], a["d"], *st, a["scale"], a["causal"], a["ws"], a["n"], None)
+                             a["Tq"], a["Tk"], a["d"], st, a["scale"], a["causal"], a["ws"], a["n"], None)
 
 
 BAD, NO = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED
@@ -49,16 +50,49 @@ def test_forward_refusals(lib, kw, expect):
     assert fwd(lib, **kw) == expect
 
 
+def bwd(lib, st=None, **kw):
+    names = ("Q", "K", "V", "O", "dO", "L", "dQ", "dK", "dV", "cq", "ck")
+    a = {n: A + i * GAP for i, n in enumerate(names)}
+    a.update(B=2, H=8, H_kv=2, Tq=100, Tk=200, d=128, scale=0.1, causal=1, ws=A + 20 * GAP, n=1 << 24)
+    a.update(kw)
+    if st is not None:
+        dense = [(a["H"] * a["d"], a["d"]), (a["H_kv"] * a["d"], a["d"])]
+        st = (fa.Strides * 8)(*[st.get(n, dense[n in ("K", "V", "dK", "dV")])
+                                for n in ("Q", "K", "V", "O", "dO", "dQ", "dK", "dV")])
+    return lib.fa_bwd_varlen(*[a[n] for n in names], a["B"], a["H"], a["H_kv"], a["Tq"], a["Tk"], a["d"], st,
+                             a["scale"], a["causal"], a["ws"], a["n"], None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    *[({n: 0}, BAD) for n in ("Q", "K", "V", "O", "dO", "L", "dQ", "dK", "dV", "cq", "ck", "ws", "B", "H", "Tq", "Tk")],
+    (dict(H=7), BAD), (dict(d=80), NO), (dict(H=258, H_kv=2), NO), (dict(causal=-1), BAD),
+    (dict(scale=float("nan")), BAD), (dict(n=1000), BAD), (dict(ws=A + 20 * GAP + 16), BAD),
+    (dict(dQ=A), BAD), (dict(dK=A + GAP), BAD), (dict(dV=A + 3 * GAP), BAD), (dict(dK=A + 8 * GAP), BAD),
+    (dict(dV=A + 5 * GAP), BAD), (dict(dQ=A + 9 * GAP), BAD), (dict(ws=A + 4 * GAP), BAD), (dict(ws=A + 10 * GAP), BAD),
+    (dict(st={"dQ": (512, 128)}), BAD), (dict(st={"dO": (1024, 4)}), BAD),
+    # dK and dV as columns of one buffer [200, 4, 128], one head apart: they share a column
+    (dict(st={"dK": (512, 128), "dV": (512, 128)}, dK=A + 30 * GAP, dV=A + 30 * GAP + 256), BAD),
+])
+def test_backward_refusals(lib, kw, expect):
+    assert bwd(lib, **kw) == expect
+
+
 def test_workspace_sizes(lib):
     assert fa.fa_fwd_varlen_workspace_bytes(1, 8, 2, 1) > 0
     for bad in [(0, 8, 2, 1), (1, 8, 3, 1), (1, 8, 0, 1), (1, 258, 2, 1), (1, 8, 2, 0)]:
         assert fa.fa_fwd_varlen_workspace_bytes(*bad) == 0
+    assert fa.fa_bwd_varlen_workspace_bytes(1, 8, 2, 1, 1) > 0
+    for bad in [(0, 8, 2, 1, 1), (1, 8, 3, 1, 1), (1, 258, 2, 1, 1), (1, 8, 2, 0, 1), (1, 8, 2, 1, 0)]:
+        assert fa.fa_bwd_varlen_workspace_bytes(*bad) == 0
+    assert bwd(lib, n=fa.fa_bwd_varlen_workspace_bytes(2, 8, 2, 100, 200) - 1) == BAD
     assert fwd(lib, n=fa.fa_fwd_varlen_workspace_bytes(2, 8, 2, 100) - 1) == BAD
 
 
 def test_fault_hook_rejects_zero_timeout(lib):
     assert lib.fa_fwd_varlen_fault_test(A, A + GAP, A + 2 * GAP, A + 3 * GAP, A + 4 * GAP, A + 5 * GAP, A + 6 * GAP, 1,
                                         1, 1, 8, 8, 128, 0.1, 1, A + 7 * GAP, 1 << 20, 0, 0, None) == BAD
+    assert lib.fa_bwd_varlen_fault_test(*[A + i * GAP for i in range(11)], 1, 1, 1, 8, 8, 128, 0.1, 1, A + 20 * GAP,
+                                        1 << 24, 0, 0, None) == BAD
 
 
 def test_binding_refuses_cpu_tensors():
