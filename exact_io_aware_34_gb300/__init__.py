@@ -15,6 +15,8 @@ from .fa import (  # noqa: F401
     fa_bwd_varlen_workspace_bytes,
     fa_fwd,
     fa_fwd_fault_test,
+    fa_fwd_prefix,
+    fa_fwd_prefix_workspace_bytes,
     fa_fwd_varlen,
     fa_fwd_varlen_workspace_bytes,
     fa_get_device_status,

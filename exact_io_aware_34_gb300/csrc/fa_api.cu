@@ -19,6 +19,7 @@
 #include "fa_bwd_kernel.cuh"
 #include "fa_decode_kernel.cuh"
 #include "fa_fwd_kernel.cuh"
+#include "fa_prefix_kernel.cuh"
 #include "fa_varlen_bwd_kernel.cuh"
 #include "fa_varlen_kernel.cuh"
 #include "naive_kernels.cuh"
@@ -1105,3 +1106,4 @@ int fa_last_cuda_error(void) { return t_last_cuda_error; }
 }  // extern "C"
 
 #include "fa_varlen_api.cuh"
+#include "fa_prefix_api.cuh"

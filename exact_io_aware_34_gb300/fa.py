@@ -31,7 +31,8 @@ EXPORTED = ("fa_fwd", "fa_get_device_status", "fa_status_string", "fa_last_cuda_
             "fa_fwd_kv_fault_test", "fa_merge_partials", "fa_fwd_host", "fa_fwd_host_workspace_bytes",
             "fa_fwd_kv_f32", "fa_fwd_kv_f32_workspace_bytes", "fa_fwd_launch_shape",
             "fa_fwd_varlen", "fa_fwd_varlen_workspace_bytes", "fa_fwd_varlen_fault_test",
-            "fa_bwd_varlen", "fa_bwd_varlen_workspace_bytes", "fa_bwd_varlen_fault_test")
+            "fa_bwd_varlen", "fa_bwd_varlen_workspace_bytes", "fa_bwd_varlen_fault_test",
+            "fa_fwd_prefix", "fa_fwd_prefix_workspace_bytes", "fa_fwd_prefix_fault_test")
 
 _lib = None
 
@@ -39,6 +40,11 @@ _lib = None
 class Strides(ctypes.Structure):
     """fa_strides_t: element strides of a packed tensor [T, heads, d]."""
     _fields_ = [("token", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
+class BatchStrides(ctypes.Structure):
+    """fa_batch_strides_t: element strides of a tensor [B, heads, N, d]."""
+    _fields_ = [("batch", ctypes.c_longlong), ("head", ctypes.c_longlong), ("row", ctypes.c_longlong)]
 
 
 class FaError(RuntimeError):
@@ -116,6 +122,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_bwd_varlen.restype = i
     lib.fa_bwd_varlen_fault_test.argtypes = [vp] * 11 + [i] * 6 + [f, i, vp, sz, i, u64, vp]
     lib.fa_bwd_varlen_fault_test.restype = i
+    bst = ctypes.POINTER(BatchStrides)
+    lib.fa_fwd_prefix_workspace_bytes.argtypes = [i] * 7
+    lib.fa_fwd_prefix_workspace_bytes.restype = sz
+    lib.fa_fwd_prefix.argtypes = [vp] * 8 + [i] * 7 + [bst, f, i, vp, sz, vp]
+    lib.fa_fwd_prefix.restype = i
+    lib.fa_fwd_prefix_fault_test.argtypes = [vp] * 8 + [i] * 7 + [f, i, vp, sz, i, u64, vp]
+    lib.fa_fwd_prefix_fault_test.restype = i
     _lib = lib
     return lib
 
@@ -616,6 +629,93 @@ def fa_bwd_varlen_fault_test(q, k, v, o, do, lse, cu_q, cu_kv, dq, dk, dv, scale
             k.shape[0], d, float(scale), bool(causal), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), int(drop_load), int(timeout_ns),
             _stream_handle(stream, q.device)))
+
+
+def fa_fwd_prefix_workspace_bytes(B: int, H: int, H_kv: int, N_q: int, N_prefix: int, N_own: int, d: int) -> int:
+    return int(load_library().fa_fwd_prefix_workspace_bytes(int(B), int(H), int(H_kv), int(N_q), int(N_prefix),
+                                                             int(N_own), int(d)))
+
+
+def _check_batch(name, t, device, shape=None):
+    """A bf16 CUDA tensor [B, heads, N, d] (or [heads, N, d]) with contiguous d; its strides."""
+    dims = 4 if shape is None else len(shape)
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != dims or not t.is_cuda:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor of {dims} dimensions")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    strides = t.stride()
+    if strides[-1] != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return (0, *strides[:-1]) if dims == 3 else strides[:-1]
+
+
+def fa_fwd_prefix(q, k_prefix, v_prefix, k, v, seq_lens, o=None, lse=None, scale: float | None = None,
+                  causal: bool = False, workspace=None, stream=None):
+    """Attention of a few new tokens per sequence over a prefix that the batch
+    shares and each sequence's own cache.
+
+    q: bf16 [B, H, N_q, d], N_q <= 128; k_prefix, v_prefix: bf16
+    [H_kv, N_prefix, d], or None when nothing is shared; k, v: bf16
+    [B, H_kv, N_own, d], of which the first seq_lens[b] rows count (int32 CUDA
+    [B], read on the device). Only d has to be contiguous. With ``causal`` the
+    N_q new tokens are the last of the own cache and row i sees its keys
+    j < seq_lens[b] - (N_q - 1 - i). A row that sees no key gets o = 0 and
+    lse = -inf. Returns (o bf16 [B, H, N_q, d], lse float32 [B, H, N_q]).
+    """
+    device = getattr(q, "device", None)
+    q_st = _check_batch("q", q, device)
+    B, H, N_q, d = q.shape
+    k_st = _check_batch("k", k, device)
+    H_kv, N_own = k.shape[1], k.shape[2]
+    if k.shape[0] != B or k.shape[3] != d:
+        raise ValueError(f"shapes do not match: q {tuple(q.shape)} k {tuple(k.shape)}")
+    v_st = _check_batch("v", v, device, tuple(k.shape))
+    N_prefix, kp_st, vp_st, kp_ptr, vp_ptr = 0, (0, 0, 0), (0, 0, 0), None, None
+    if (k_prefix is None) != (v_prefix is None):
+        raise ValueError("k_prefix and v_prefix come together")
+    if k_prefix is not None:
+        N_prefix = k_prefix.shape[1] if k_prefix.dim() == 3 else -1
+        kp_st = _check_batch("k_prefix", k_prefix, device, (H_kv, N_prefix, d))
+        vp_st = _check_batch("v_prefix", v_prefix, device, (H_kv, N_prefix, d))
+        if N_prefix:
+            kp_ptr, vp_ptr = k_prefix.data_ptr(), v_prefix.data_ptr()
+    if not isinstance(seq_lens, torch.Tensor) or seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (B,) \
+            or not seq_lens.is_contiguous() or seq_lens.device != device:
+        raise ValueError(f"seq_lens must be a contiguous int32 [B] tensor on {device}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    lib = load_library()
+    with _on_stream(stream, device):
+        if o is None:
+            o = torch.empty((B, H, N_q, d), dtype=torch.bfloat16, device=device)
+        o_st = _check_batch("o", o, device, (B, H, N_q, d))
+        if lse is None:
+            lse = torch.empty((B, H, N_q), dtype=torch.float32, device=device)
+        _check_lse("lse", lse, (B, H, N_q), device)
+        workspace, ws_ptr, ws_bytes = _workspace(
+            workspace, lib.fa_fwd_prefix_workspace_bytes(B, H, H_kv, N_q, N_prefix, N_own, d), device)
+        strides = (BatchStrides * 6)(q_st, kp_st, vp_st, k_st, v_st, o_st)
+        st = lib.fa_fwd_prefix(q.data_ptr(), kp_ptr, vp_ptr, k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(),
+                               o.data_ptr(), lse.data_ptr(), B, H, H_kv, N_q, N_prefix, N_own, d, strides, scale,
+                               bool(causal), ws_ptr, ws_bytes, torch.cuda.current_stream(device).cuda_stream)
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_prefix")
+    return o, lse
+
+
+def fa_fwd_prefix_fault_test(q, k_prefix, v_prefix, k, v, seq_lens, o, lse, scale: float, causal: bool, workspace,
+                             drop_load: int, timeout_ns: int, stream=None) -> int:
+    """Test hook of the C ABI (see include/fa.h): returns the raw status code."""
+    B, H, N_q, d = q.shape
+    lib = load_library()
+    with torch.cuda.device(q.device):
+        return int(lib.fa_fwd_prefix_fault_test(
+            q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(),
+            o.data_ptr(), lse.data_ptr(), B, H, k.shape[1], N_q, k_prefix.shape[1], k.shape[2], d, float(scale),
+            bool(causal), workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(drop_load),
+            int(timeout_ns), _stream_handle(stream, q.device)))
 
 
 def fa_bwd_fault_test(q, k, v, o, do, lse, dq, dk, dv, scale: float, workspace, drop_load: int, timeout_ns: int,

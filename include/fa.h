@@ -135,15 +135,16 @@ fa_status_t fa_fwd_host(const void* Qh, const void* Kh, const void* Vh, void* Oh
  * library's device status word on the current device. Returns FA_OK, or
  * FA_ERR_TIMEOUT if any kernel of this library on this device gave up on a
  * wait since the last call, or FA_ERR_INVALID_ARG if one found sequence
- * offsets in device memory that do not lie in the caller's
+ * offsets or lengths in device memory that do not lie in the caller's
  * buffers (whichever came first), or FA_ERR_CUDA if the synchronisation failed.
  * `info`, if not NULL, receives 4 words describing the first of them:
  * {role (forward: 1 producer, 2 mma, 3 softmax/epilogue; backward dQ CTA:
  * 4, 5, 6; backward dK/dV CTA: 7, 8, 9; short-query kernel of fa_fwd_kv:
  * 10, 11, 12, in the same order; fa_fwd_varlen: 13, 14, 15, and 16 for the
  * warp that hands out work; fa_bwd_varlen: query role 17, 18, 19, key-block
- * role 20, 21, 22), blockIdx.x, blockIdx.y, blockIdx.z}, or {16,
- * index of the sequence, 0, 0} for bad offsets; all zero when there was none. (`info` is this library's
+ * role 20, 21, 22; fa_fwd_prefix: 23, 24, 25, and 26 for the warp that hands
+ * out work), blockIdx.x, blockIdx.y, blockIdx.z}, or {16 (offsets) or 26
+ * (lengths), index of the sequence, 0, 0} for bad ones; all zero when there was none. (`info` is this library's
  * addition for diagnosing a timeout; with info = NULL the call only reports
  * the status.)
  */
@@ -494,6 +495,75 @@ fa_status_t fa_bwd_varlen_fault_test(const void* Q, const void* K, const void* V
                                      const float* LSE, void* dQ, void* dK, void* dV, const int* cu_q,
                                      const int* cu_kv, int B, int H, int H_kv, int T_q, int T_kv, int d, float scale,
                                      int causal, void* workspace, size_t workspace_bytes,
+                                     int drop_load, unsigned long long timeout_ns, cudaStream_t stream);
+
+/* Element strides of a tensor [B, heads, N, d] whose d elements are
+ * contiguous. NULL in a call stands for a contiguous tensor. */
+typedef struct {
+  long long batch;
+  long long head;
+  long long row;
+} fa_batch_strides_t;
+
+/*
+ * fa_fwd_prefix_workspace_bytes -- device workspace fa_fwd_prefix needs:
+ * float32 partial results of the pieces the keys are cut into. 0 for sizes it
+ * rejects. Depends on the current device's SM count (148 when there is none).
+ */
+size_t fa_fwd_prefix_workspace_bytes(int B, int H, int H_kv, int N_q, int N_prefix, int N_own, int d);
+
+/*
+ * fa_fwd_prefix -- attention of a few new tokens per sequence (1 when
+ * generating, more when checking drafted tokens) over keys that the whole
+ * batch shares and a cache of each sequence's own, of its own length. The
+ * shared keys are read once for the batch, not once per sequence.
+ *   Q, O   : device, bf16 [B, H, N_q, d], 1 <= N_q <= 128; H is a multiple of
+ *            H_kv with H / H_kv <= 128, heads grouped as in fa_fwd_kv.
+ *   K_prefix, V_prefix : device, bf16 [H_kv, N_prefix, d]. N_prefix may be 0 (a
+ *            batch that shares nothing); they are not read then.
+ *   K, V   : device, bf16 [B, H_kv, N_own, d], N_own >= 1 rows of room each, of
+ *            which sequence b's first seq_lens[b] hold keys.
+ *   seq_lens : device, int32 [B], 0 .. N_own, read on the device in stream
+ *            order (a captured call may be replayed with other lengths).
+ *   LSE    : device, float32 [B, H, N_q], written (natural log).
+ *   causal : 1: the N_q new tokens are the last N_q of the own cache and see
+ *            each other in order: row i sees the own keys
+ *            j < seq_lens[b] - (N_q - 1 - i); 0: all seq_lens[b]. Every row
+ *            sees the whole prefix.
+ *   strides : NULL for contiguous tensors, else six entries (host), for Q,
+ *            K_prefix, V_prefix (batch unused), K, V and O: positive multiples
+ *            of 8 elements; a cache stored as [B, N_own, H_kv, d] needs no copy.
+ *   workspace : device, fa_fwd_prefix_workspace_bytes(...) bytes at least,
+ *            128-byte aligned; overwritten. Calls that may run at the same
+ *            time (other streams, graph replays) need workspaces of their own.
+ * A row that sees no key gets O = 0 and LSE = -inf. Cache rows past a
+ * sequence's length are never part of a result, whatever they hold. Lengths
+ * outside 0 .. N_own are clamped, and reported by fa_get_device_status as
+ * FA_ERR_INVALID_ARG. Two launches on `stream`, the merge of the pieces as a
+ * programmatic dependent. The pieces, so the order of a row's sums, depend on
+ * all lengths of the batch and the SM count; the same call gives the same bits.
+ * Limits: B, H <= 65535; B * H * N_q, B * H_kv * N_own and H_kv * N_prefix below
+ * 2^31; d in {64, 128}; scale finite. Pointers 16-byte, LSE and seq_lens 4-byte
+ * aligned; O, LSE and the workspace overlap no input nor each other (judged by
+ * first and last byte). FA_ERR_UNSUPPORTED for other d, N_q > 128 or
+ * H / H_kv > 128, FA_ERR_INVALID_ARG for the rest.
+ */
+fa_status_t fa_fwd_prefix(const void* Q, const void* K_prefix, const void* V_prefix, const void* K, const void* V,
+                          const int* seq_lens, void* O, float* LSE,
+                          int B, int H, int H_kv, int N_q, int N_prefix, int N_own, int d,
+                          const fa_batch_strides_t* strides, float scale, int causal,
+                          void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fa_fwd_prefix_fault_test -- TEST HOOK, not for production use. fa_fwd_prefix
+ * on contiguous tensors with every device-side wait limited to `timeout_ns`,
+ * and, when drop_load >= 0, the drop_load-th K/V tile load of every CTA
+ * skipped.
+ */
+fa_status_t fa_fwd_prefix_fault_test(const void* Q, const void* K_prefix, const void* V_prefix, const void* K,
+                                     const void* V, const int* seq_lens, void* O, float* LSE,
+                                     int B, int H, int H_kv, int N_q, int N_prefix, int N_own, int d,
+                                     float scale, int causal, void* workspace, size_t workspace_bytes,
                                      int drop_load, unsigned long long timeout_ns, cudaStream_t stream);
 
 #ifdef __cplusplus
