@@ -47,6 +47,10 @@ class BatchStrides(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_longlong), ("head", ctypes.c_longlong), ("row", ctypes.c_longlong)]
 
 
+# Strides as the C ABI's arrays of fa_strides_t / fa_batch_strides_t, flat.
+_LL8, _LL16, _LL18 = (ctypes.c_longlong * n for n in (8, 16, 18))
+
+
 class FaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -109,23 +113,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_fwd_launch_shape.restype = i
     lib.fa_merge_partials.argtypes = [vp, vp, vp, vp, i, ctypes.c_longlong, i, vp]
     lib.fa_merge_partials.restype = i
-    sz, st = ctypes.c_size_t, ctypes.POINTER(Strides)
+    sz = ctypes.c_size_t
     lib.fa_fwd_varlen_workspace_bytes.argtypes = [i, i, i, i]
     lib.fa_fwd_varlen_workspace_bytes.restype = sz
-    lib.fa_fwd_varlen.argtypes = [vp] * 7 + [i] * 6 + [st, f, i, vp, sz, vp]
+    lib.fa_fwd_varlen.argtypes = [vp] * 7 + [i] * 6 + [vp, f, i, vp, sz, vp]
     lib.fa_fwd_varlen.restype = i
     lib.fa_fwd_varlen_fault_test.argtypes = [vp] * 7 + [i] * 6 + [f, i, vp, sz, i, u64, vp]
     lib.fa_fwd_varlen_fault_test.restype = i
     lib.fa_bwd_varlen_workspace_bytes.argtypes = [i, i, i, i, i]
     lib.fa_bwd_varlen_workspace_bytes.restype = sz
-    lib.fa_bwd_varlen.argtypes = [vp] * 11 + [i] * 6 + [st, f, i, vp, sz, vp]
+    lib.fa_bwd_varlen.argtypes = [vp] * 11 + [i] * 6 + [vp, f, i, vp, sz, vp]
     lib.fa_bwd_varlen.restype = i
     lib.fa_bwd_varlen_fault_test.argtypes = [vp] * 11 + [i] * 6 + [f, i, vp, sz, i, u64, vp]
     lib.fa_bwd_varlen_fault_test.restype = i
-    bst = ctypes.POINTER(BatchStrides)
     lib.fa_fwd_prefix_workspace_bytes.argtypes = [i] * 7
     lib.fa_fwd_prefix_workspace_bytes.restype = sz
-    lib.fa_fwd_prefix.argtypes = [vp] * 8 + [i] * 7 + [bst, f, i, vp, sz, vp]
+    lib.fa_fwd_prefix.argtypes = [vp] * 8 + [i] * 7 + [vp, f, i, vp, sz, vp]
     lib.fa_fwd_prefix.restype = i
     lib.fa_fwd_prefix_fault_test.argtypes = [vp] * 8 + [i] * 7 + [f, i, vp, sz, i, u64, vp]
     lib.fa_fwd_prefix_fault_test.restype = i
@@ -151,13 +154,23 @@ def _on_stream(stream, device):
     """Context in which ``device`` is current and allocations belong to
     ``stream`` (None: torch's current stream of that device)."""
     if stream is None:
-        return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        return torch.cuda.device(device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) \
             else torch.cuda.default_stream(device)
     if stream.device != device:
         raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
     return torch.cuda.stream(stream)
+
+
+def _launch(fn, stream, device):
+    """fn() with ``device`` current and ``stream`` torch's current stream: what
+    fn allocates and enqueues belongs to it. (The usual case enters no context;
+    small calls are bound by the host.)"""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return fn()
+    with _on_stream(stream, device):
+        return fn()
 
 
 def _check_qkv(q, k, v):
@@ -478,41 +491,66 @@ def fa_bwd(q, k, v, o, do, lse, dq=None, dk=None, dv=None, scale: float | None =
     return tuple(outs)
 
 
-def _check_packed(name, t, device, T=None, heads=None, d=None):
-    """A bf16 CUDA tensor [T, heads, d] with contiguous d; its token and head strides."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_cuda:
-        raise ValueError(f"{name} must be a bf16 CUDA tensor [T, heads, d]")
-    shape = t.shape
-    if (T is not None and shape[0] != T) or (heads is not None and shape[1] != heads) \
-            or (d is not None and shape[2] != d):
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{T}, {heads}, {d}]")
-    strides = t.stride()
-    if strides[2] != 1 and shape[2] != 1:
+def _strided(name, t, device, shape):
+    """Strides of a bf16 tensor of this shape on this device whose last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on {device}")
+    s = t.stride()
+    if s[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return strides[0], strides[1]
+    return s[:-1]
 
 
-def _check_offsets(name, t, device, n=None):
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() \
-            or t.device != device or t.shape[0] < 2 or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of B + 1 offsets on {device}")
+def _leading(name, t, dims):
+    """Shape of a CUDA tensor that others are checked against."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != dims:
+        raise ValueError(f"{name} must be a CUDA tensor of {dims} dimensions")
+    return t.shape
 
 
-def _check_lse(name, lse, shape, device):
-    if not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or tuple(lse.shape) != shape \
-            or not lse.is_contiguous() or lse.device != device:
-        raise ValueError(f"{name} must be a contiguous float32 tensor {list(shape)} on {device}")
+def _int32(name, t, device, n):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.shape != (n,) or t.device != device \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{n}] on {device}")
+
+
+def _out_lse(lse, shape, device):
+    if lse is None:
+        return torch.empty(shape, dtype=torch.float32, device=device)
+    if not isinstance(lse, torch.Tensor) or lse.dtype is not torch.float32 or lse.shape != shape \
+            or lse.device != device or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 tensor {list(shape)} on {device}")
+    return lse
+
+
+def _out_bf16(name, t, device, shape):
+    """(tensor, strides) of an output, allocated when not given."""
+    if t is None:
+        t = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    return t, _strided(name, t, device, shape)
 
 
 def _workspace(workspace, need, device):
-    """(tensor, pointer, bytes) of the caller's workspace, or of a new one."""
+    """(tensor, bytes) of the caller's workspace, or of a new one."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _raw_stream(device) -> int:
+    """Handle of torch's current stream of a device."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _packed_sizes(q, k, cu_q):
+    """(device, T_q, H, T_kv, H_kv, d, B) of packed tensors, from q, k and cu_q."""
+    T_q, H, d = _leading("q", q, 3)
+    T_kv, H_kv, _ = _leading("k", k, 3)
+    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise ValueError("cu_q must hold B + 1 offsets")
+    return q.device, T_q, H, T_kv, H_kv, d, cu_q.shape[0] - 1
 
 
 def fa_fwd_varlen_workspace_bytes(B: int, H: int, H_kv: int, T_q: int) -> int:
@@ -532,32 +570,27 @@ def fa_fwd_varlen(q, k, v, cu_q, cu_kv, o=None, lse=None, scale: float | None = 
     The offsets stay on the device; with ones outside the buffers nothing is
     written and :func:`fa_get_device_status` says so. Returns (o bf16 [T_q, H, d], lse float32 [H, T_q]).
     """
-    device = getattr(q, "device", None)
-    q_st = _check_packed("q", q, device)
-    T_q, H, d = q.shape
-    k_st = _check_packed("k", k, device, d=d)
-    T_kv, H_kv = k.shape[0], k.shape[1]
-    v_st = _check_packed("v", v, device, T_kv, H_kv, d)
-    _check_offsets("cu_q", cu_q, device)
-    _check_offsets("cu_kv", cu_kv, device, cu_q.shape[0])
-    B = cu_q.shape[0] - 1
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    device, T_q, H, T_kv, H_kv, d, B = _packed_sizes(q, k, cu_q)
+    q_st = _strided("q", q, device, (T_q, H, d))
+    k_st = _strided("k", k, device, (T_kv, H_kv, d))
+    v_st = _strided("v", v, device, (T_kv, H_kv, d))
+    _int32("cu_q", cu_q, device, B + 1)
+    _int32("cu_kv", cu_kv, device, B + 1)
     lib = load_library()
-    with _on_stream(stream, device):
-        if o is None:
-            o = torch.empty((T_q, H, d), dtype=torch.bfloat16, device=device)
-        o_st = _check_packed("o", o, device, T_q, H, d)
-        if lse is None:
-            lse = torch.empty((H, T_q), dtype=torch.float32, device=device)
-        _check_lse("lse", lse, (H, T_q), device)
-        workspace, ws_ptr, ws_bytes = _workspace(workspace, lib.fa_fwd_varlen_workspace_bytes(B, H, H_kv, T_q), device)
-        st = lib.fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+
+    def run():
+        out, o_st = _out_bf16("o", o, device, (T_q, H, d))
+        out_lse = _out_lse(lse, (H, T_q), device)
+        ws, ws_bytes = _workspace(workspace, lib.fa_fwd_varlen_workspace_bytes(B, H, H_kv, T_q), device)
+        st = lib.fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), out_lse.data_ptr(),
                                cu_q.data_ptr(), cu_kv.data_ptr(), B, H, H_kv, T_q, T_kv, d,
-                               (Strides * 4)(q_st, k_st, v_st, o_st), scale, bool(causal), ws_ptr, ws_bytes, torch.cuda.current_stream(device).cuda_stream)
-    if st != FA_OK:
-        raise FaError(st, "fa_fwd_varlen")
-    return o, lse
+                               _LL8(*q_st, *k_st, *v_st, *o_st), d ** -0.5 if scale is None else scale, bool(causal),
+                               ws.data_ptr(), ws_bytes, _raw_stream(device))
+        if st != FA_OK:
+            raise FaError(st, "fa_fwd_varlen")
+        return out, out_lse
+
+    return _launch(run, stream, device)
 
 
 def fa_fwd_varlen_fault_test(q, k, v, o, lse, cu_q, cu_kv, scale: float, causal: bool, workspace, drop_load: int,
@@ -583,38 +616,32 @@ def fa_bwd_varlen(q, k, v, o, do, lse, cu_q, cu_kv, dq=None, dk=None, dv=None, s
     its outputs ``o`` and ``lse``. do, dq: bf16 [T_q, H, d]; dk, dv: bf16
     [T_kv, H_kv, d], summed over the query heads of a K/V head. Other arguments
     as for the forward. Rows and keys of no sequence are not written."""
-    device = getattr(q, "device", None)
-    q_st = _check_packed("q", q, device)
-    T_q, H, d = q.shape
-    k_st = _check_packed("k", k, device, d=d)
-    T_kv, H_kv = k.shape[0], k.shape[1]
-    strides = [q_st, k_st, _check_packed("v", v, device, T_kv, H_kv, d), _check_packed("o", o, device, T_q, H, d),
-               _check_packed("do", do, device, T_q, H, d)]
-    _check_lse("lse", lse, (H, T_q), device)
-    _check_offsets("cu_q", cu_q, device)
-    _check_offsets("cu_kv", cu_kv, device, cu_q.shape[0])
-    B = cu_q.shape[0] - 1
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    device, T_q, H, T_kv, H_kv, d, B = _packed_sizes(q, k, cu_q)
+    rows, keys = (T_q, H, d), (T_kv, H_kv, d)
+    inputs = (*_strided("q", q, device, rows), *_strided("k", k, device, keys), *_strided("v", v, device, keys),
+              *_strided("o", o, device, rows), *_strided("do", do, device, rows))
+    if not isinstance(lse, torch.Tensor):
+        raise ValueError("lse must be a tensor")
+    _out_lse(lse, (H, T_q), device)
+    _int32("cu_q", cu_q, device, B + 1)
+    _int32("cu_kv", cu_kv, device, B + 1)
     lib = load_library()
-    with _on_stream(stream, device):
-        if dq is None:
-            dq = torch.empty((T_q, H, d), dtype=torch.bfloat16, device=device)
-        if dk is None:
-            dk = torch.empty((T_kv, H_kv, d), dtype=torch.bfloat16, device=device)
-        if dv is None:
-            dv = torch.empty((T_kv, H_kv, d), dtype=torch.bfloat16, device=device)
-        strides += [_check_packed("dq", dq, device, T_q, H, d), _check_packed("dk", dk, device, T_kv, H_kv, d),
-                    _check_packed("dv", dv, device, T_kv, H_kv, d)]
-        workspace, ws_ptr, ws_bytes = _workspace(
-            workspace, lib.fa_bwd_varlen_workspace_bytes(B, H, H_kv, T_q, T_kv), device)
+
+    def run():
+        gq, gq_st = _out_bf16("dq", dq, device, rows)
+        gk, gk_st = _out_bf16("dk", dk, device, keys)
+        gv, gv_st = _out_bf16("dv", dv, device, keys)
+        ws, ws_bytes = _workspace(workspace, lib.fa_bwd_varlen_workspace_bytes(B, H, H_kv, T_q, T_kv), device)
         st = lib.fa_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
-                               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_q.data_ptr(), cu_kv.data_ptr(), B, H,
-                               H_kv, T_q, T_kv, d, (Strides * 8)(*strides), scale, bool(causal), ws_ptr, ws_bytes,
-                               torch.cuda.current_stream(device).cuda_stream)
-    if st != FA_OK:
-        raise FaError(st, "fa_bwd_varlen")
-    return dq, dk, dv
+                               gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), cu_q.data_ptr(), cu_kv.data_ptr(), B, H,
+                               H_kv, T_q, T_kv, d, _LL16(*inputs, *gq_st, *gk_st, *gv_st),
+                               d ** -0.5 if scale is None else scale, bool(causal), ws.data_ptr(), ws_bytes,
+                               _raw_stream(device))
+        if st != FA_OK:
+            raise FaError(st, "fa_bwd_varlen")
+        return gq, gk, gv
+
+    return _launch(run, stream, device)
 
 
 def fa_bwd_varlen_fault_test(q, k, v, o, do, lse, cu_q, cu_kv, dq, dk, dv, scale: float, causal: bool, workspace,
@@ -636,21 +663,6 @@ def fa_fwd_prefix_workspace_bytes(B: int, H: int, H_kv: int, N_q: int, N_prefix:
                                                              int(N_own), int(d)))
 
 
-def _check_batch(name, t, device, shape=None):
-    """A bf16 CUDA tensor [B, heads, N, d] (or [heads, N, d]) with contiguous d; its strides."""
-    dims = 4 if shape is None else len(shape)
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != dims or not t.is_cuda:
-        raise ValueError(f"{name} must be a bf16 CUDA tensor of {dims} dimensions")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    strides = t.stride()
-    if strides[-1] != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return (0, *strides[:-1]) if dims == 3 else strides[:-1]
-
-
 def fa_fwd_prefix(q, k_prefix, v_prefix, k, v, seq_lens, o=None, lse=None, scale: float | None = None,
                   causal: bool = False, workspace=None, stream=None):
     """Attention of a few new tokens per sequence over a prefix that the batch
@@ -664,45 +676,37 @@ def fa_fwd_prefix(q, k_prefix, v_prefix, k, v, seq_lens, o=None, lse=None, scale
     j < seq_lens[b] - (N_q - 1 - i). A row that sees no key gets o = 0 and
     lse = -inf. Returns (o bf16 [B, H, N_q, d], lse float32 [B, H, N_q]).
     """
-    device = getattr(q, "device", None)
-    q_st = _check_batch("q", q, device)
-    B, H, N_q, d = q.shape
-    k_st = _check_batch("k", k, device)
-    H_kv, N_own = k.shape[1], k.shape[2]
-    if k.shape[0] != B or k.shape[3] != d:
-        raise ValueError(f"shapes do not match: q {tuple(q.shape)} k {tuple(k.shape)}")
-    v_st = _check_batch("v", v, device, tuple(k.shape))
-    N_prefix, kp_st, vp_st, kp_ptr, vp_ptr = 0, (0, 0, 0), (0, 0, 0), None, None
+    B, H, N_q, d = rows = tuple(_leading("q", q, 4))
+    _, H_kv, N_own, _ = _leading("k", k, 4)
+    device, cache = q.device, (B, H_kv, N_own, d)
+    q_st = _strided("q", q, device, rows)
+    k_st = _strided("k", k, device, cache)
+    v_st = _strided("v", v, device, cache)
     if (k_prefix is None) != (v_prefix is None):
         raise ValueError("k_prefix and v_prefix come together")
+    N_prefix, p_st, p_ptr = 0, (0,) * 6, (None, None)
     if k_prefix is not None:
-        N_prefix = k_prefix.shape[1] if k_prefix.dim() == 3 else -1
-        kp_st = _check_batch("k_prefix", k_prefix, device, (H_kv, N_prefix, d))
-        vp_st = _check_batch("v_prefix", v_prefix, device, (H_kv, N_prefix, d))
-        if N_prefix:
-            kp_ptr, vp_ptr = k_prefix.data_ptr(), v_prefix.data_ptr()
-    if not isinstance(seq_lens, torch.Tensor) or seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (B,) \
-            or not seq_lens.is_contiguous() or seq_lens.device != device:
-        raise ValueError(f"seq_lens must be a contiguous int32 [B] tensor on {device}")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+        N_prefix = _leading("k_prefix", k_prefix, 3)[1]
+        shared = (H_kv, N_prefix, d)
+        p_st = (0, *_strided("k_prefix", k_prefix, device, shared), 0, *_strided("v_prefix", v_prefix, device, shared))
+        p_ptr = k_prefix.data_ptr(), v_prefix.data_ptr()
+    _int32("seq_lens", seq_lens, device, B)
     lib = load_library()
-    with _on_stream(stream, device):
-        if o is None:
-            o = torch.empty((B, H, N_q, d), dtype=torch.bfloat16, device=device)
-        o_st = _check_batch("o", o, device, (B, H, N_q, d))
-        if lse is None:
-            lse = torch.empty((B, H, N_q), dtype=torch.float32, device=device)
-        _check_lse("lse", lse, (B, H, N_q), device)
-        workspace, ws_ptr, ws_bytes = _workspace(
-            workspace, lib.fa_fwd_prefix_workspace_bytes(B, H, H_kv, N_q, N_prefix, N_own, d), device)
-        strides = (BatchStrides * 6)(q_st, kp_st, vp_st, k_st, v_st, o_st)
-        st = lib.fa_fwd_prefix(q.data_ptr(), kp_ptr, vp_ptr, k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(),
-                               o.data_ptr(), lse.data_ptr(), B, H, H_kv, N_q, N_prefix, N_own, d, strides, scale,
-                               bool(causal), ws_ptr, ws_bytes, torch.cuda.current_stream(device).cuda_stream)
-    if st != FA_OK:
-        raise FaError(st, "fa_fwd_prefix")
-    return o, lse
+
+    def run():
+        out, o_st = _out_bf16("o", o, device, rows)
+        out_lse = _out_lse(lse, (B, H, N_q), device)
+        ws, ws_bytes = _workspace(workspace, lib.fa_fwd_prefix_workspace_bytes(B, H, H_kv, N_q, N_prefix, N_own, d),
+                                  device)
+        st = lib.fa_fwd_prefix(q.data_ptr(), *p_ptr, k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+                               out_lse.data_ptr(), B, H, H_kv, N_q, N_prefix, N_own, d,
+                               _LL18(*q_st, *p_st, *k_st, *v_st, *o_st), d ** -0.5 if scale is None else scale,
+                               bool(causal), ws.data_ptr(), ws_bytes, _raw_stream(device))
+        if st != FA_OK:
+            raise FaError(st, "fa_fwd_prefix")
+        return out, out_lse
+
+    return _launch(run, stream, device)
 
 
 def fa_fwd_prefix_fault_test(q, k_prefix, v_prefix, k, v, seq_lens, o, lse, scale: float, causal: bool, workspace,
