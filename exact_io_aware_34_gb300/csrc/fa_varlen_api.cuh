@@ -122,10 +122,14 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   if (!regs_ok[dev]) return FA_ERR_UNSUPPORTED;
 
   const int H_kv = k.heads, G = q.heads / k.heads, tp = 128 / G;
-  CUtensorMap mq, mk, mv;
+  // O's box: a warp's 32 rows, G heads of 32 / G tokens or 32 heads of one.
+  const bool o_tma = (G & (G - 1)) == 0;
+  CUtensorMap mq, mk, mv, mo;
   if (!make_map_strided(&mq, q.p, HD, q.heads, q.sh, q.T, q.st, G, tp) ||
       !make_map_strided(&mk, k.p, HD, k.T, k.st, k.heads, k.sh, 128, 1) ||
-      !make_map_strided(&mv, v.p, HD, v.T, v.st, v.heads, v.sh, 128, 1))
+      !make_map_strided(&mv, v.p, HD, v.T, v.st, v.heads, v.sh, 128, 1) ||
+      !make_map_strided(&mo, o.p, HD, o.heads, o.sh, o.T, o.st, o_tma ? std::min(G, 32) : 1,
+                        o_tma ? std::max(1, 32 / G) : 1))
     return cuda_fail(cudaErrorInvalidValue);
 
   const long long cap = varlen_fwd_cap(B, q.heads, H_kv, q.T);
@@ -147,6 +151,7 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   p.G = G;
   p.tp = tp;
   p.causal = causal;
+  p.o_tma = o_tma ? 1 : 0;
   p.scale_log2 = masked_scale_log2(scale);
   p.idesc_qk = C::kIdescQK | (scale < 0.f ? fa::ptx::kIdescNegateA : 0u);
   p.timeout_ns = timeout_ns;
@@ -163,7 +168,7 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fa::fa_varlen_fwd_kernel<HD>, mq, mk, mv, p);
+  e = cudaLaunchKernelEx(&cfg, fa::fa_varlen_fwd_kernel<HD>, mq, mk, mv, mo, p);
   if (e != cudaSuccess) return cuda_fail(e);
   return FA_OK;
 }

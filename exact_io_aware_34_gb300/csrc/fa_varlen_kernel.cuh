@@ -76,6 +76,7 @@ struct VarParams {
   int G;                  // query heads per K/V head
   int tp;                 // tokens per tile: 128 / G
   int causal;
+  int o_tma;              // 1: G is a power of two, so a warp's 32 rows are a box of O
   float scale_log2;       // |scale| * log2(e), at least 2^-126
   uint32_t idesc_qk;
   unsigned long long timeout_ns;
@@ -247,7 +248,8 @@ struct VarJob {
 template <int HD>
 __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     fa_varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                         const __grid_constant__ CUtensorMap tmV, const VarParams p) {
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                         const VarParams p) {
   using C = FwdCfg<HD>;
   constexpr int kPolls = HD == 128 ? 8 : 1;   // as in the forward kernel
   extern __shared__ uint8_t smem_raw[];
@@ -273,6 +275,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
   const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = smem_base;
   const uint32_t sKV = smem_base + C::kSmemQ;
+  const uint32_t sStage = sKV + C::kSmemKV;
   uint8_t* generic = smem_raw + (smem_base - ptx::smem_u32(smem_raw));
 
   // Rows of the Q tiles that no query fills stay zero for the kernel's life.
@@ -541,21 +544,26 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
         if (__all_sync(0xffffffffu, valid >= C::kBN)) {
           mt = ptx::max3(mr[0], mr[1], fmaxf(mr[2], mr[3]));
         } else {
+          // Per 32 keys: all seen by the whole warp (as loaded), or masked
+          // element by element.
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            if (!__all_sync(0xffffffffu, valid >= 32 * c + 32)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= valid) s[c][i] = __float_as_uint(-INFINITY);
-          float mc[8];
+              for (int i = 0; i < 32; ++i)
+                if (32 * c + i >= valid) s[c][i] = __float_as_uint(-INFINITY);
+              float m4[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int c = k >> 1, b = (k & 1) * 16;
-            mc[k] = fmaxf(__uint_as_float(s[c][b]), __uint_as_float(s[c][b + 1]));
+              for (int k = 0; k < 4; ++k) {
+                m4[k] = fmaxf(__uint_as_float(s[c][8 * k]), __uint_as_float(s[c][8 * k + 1]));
 #pragma unroll
-            for (int i = 2; i < 16; i += 2)
-              mc[k] = ptx::max3(mc[k], __uint_as_float(s[c][b + i]), __uint_as_float(s[c][b + i + 1]));
+                for (int i = 2; i < 8; i += 2)
+                  m4[k] = ptx::max3(m4[k], __uint_as_float(s[c][8 * k + i]), __uint_as_float(s[c][8 * k + i + 1]));
+              }
+              mr[c] = ptx::max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
+            }
           }
-          mt = ptx::max3(ptx::max3(mc[0], mc[1], mc[2]), ptx::max3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
+          mt = ptx::max3(mr[0], mr[1], fmaxf(mr[2], mr[3]));
         }
         // A row sees keys from the first block on or none at all, so after
         // block 0 the maximum is -inf only for a row that sees nothing.
@@ -638,23 +646,56 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
       const long long token = static_cast<long long>(job.u.q_row0) + xt;
       const int head = job.kvh * p.G + hq;
       const float inv_l = 1.f / lo;
+      // O leaves through shared memory in 64-column pieces that one lane
+      // stores with a tiled TMA store, when the warp's rows are a box of O that
+      // lies inside the sequence; else every thread writes its row.
+      const uint32_t stage = sStage + static_cast<uint32_t>(warp) * (32u * 128u);
+      const int x_first = quarter * 32 / p.G, x_last = (quarter * 32 + 31) / p.G;
+      const bool boxed = p.o_tma && t * p.tp + x_last < job.u.n_tok;
       __nv_bfloat16* orow = p.O + token * p.o_st + head * p.o_sh;
 #pragma unroll
-      for (int c = 0; c < HD / 32; ++c) {
-        uint32_t o[32];
-        ptx::tmem_ld32(tO + 32 * c, o);
-        ptx::tmem_ld_wait();
-        ptx::reg_fence32(o);
-        uint32_t packed[16];
+      for (int k = 0; k < HD / 64; ++k) {
+        if (boxed) {
+          // The staging rows are free once this warp's previous store has read them.
+          if (lane == 0) ptx::bulk_wait_group_read0();
+          __syncwarp();
+        }
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          packed[i] =
-              none ? 0u : ptx::pack_bf16x2(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
-        if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t o[32];
+          ptx::tmem_ld32(tO + 64 * k + 32 * h, o);
+          ptx::tmem_ld_wait();
+          ptx::reg_fence32(o);
+          uint32_t packed[16];
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            dst[v] = make_uint4(packed[4 * v], packed[4 * v + 1], packed[4 * v + 2], packed[4 * v + 3]);
+          for (int i = 0; i < 16; ++i)
+            packed[i] =
+                none ? 0u : ptx::pack_bf16x2(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
+          if (boxed) {
+            const uint32_t row_addr = stage + static_cast<uint32_t>(lane) * 128u;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const uint32_t unit = 4u * h + v;      // 16-byte unit within the 128-byte row
+              const uint32_t addr = row_addr + ((unit ^ static_cast<uint32_t>(lane & 7)) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(packed[4 * v]),
+                           "r"(packed[4 * v + 1]), "r"(packed[4 * v + 2]), "r"(packed[4 * v + 3])
+                           : "memory");
+            }
+          } else if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(orow + 64 * k + 32 * h);
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              dst[v] = make_uint4(packed[4 * v], packed[4 * v + 1], packed[4 * v + 2], packed[4 * v + 3]);
+          }
+        }
+        if (boxed) {
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::tma_store_3d(&tmO, stage, 64 * k, job.kvh * p.G + (quarter * 32 - x_first * p.G),
+                              job.u.q_row0 + t * p.tp + x_first);
+            ptx::bulk_commit_group();
+          }
         }
       }
       if (live)
@@ -663,6 +704,9 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     }
   }
 
+  // The O stores must have read the staging rows before the CTA's shared
+  // memory is released.
+  if (warp < 8 && lane == 0) ptx::bulk_wait_group_read0();
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == 9) {
