@@ -55,17 +55,18 @@ bool rows_overlap(const Rows& a, const void* b, size_t nb) {
   return overlaps(a.p, static_cast<size_t>(a.span()), b, nb);
 }
 
-// bf16 map [d][n1][n2] with element strides s1, s2; box 64 x b1 x b2, 128-byte swizzle.
+// bf16 map [d][n1][n2] with element strides s1, s2; box b0 x b1 x b2 with b0 =
+// 64 (128-byte swizzle) or 32 (64-byte swizzle).
 bool make_map_strided(CUtensorMap* m, const void* base, int d, int n1, long long s1, int n2, long long s2, int b1,
-                      int b2) {
+                      int b2, int b0 = 64) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(b0), static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2)};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, b0 == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -93,7 +94,13 @@ long long varlen_fwd_cap(int B, int H, int H_kv, int T_q) {
   return T_q / (2 * tp) + static_cast<long long>(B);
 }
 
+// Whether the grid holds every unit at once: then there is no list.
+bool varlen_fwd_direct(int B, int H, int H_kv, int T_q) {
+  return varlen_fwd_cap(B, H, H_kv, T_q) * H_kv <= device_sm_count();
+}
+
 size_t varlen_fwd_ws(int B, int H, int H_kv, int T_q) {
+  if (varlen_fwd_direct(B, H, H_kv, T_q)) return 0;
   return sizeof(fa::VarPlan) + static_cast<size_t>(varlen_fwd_cap(B, H, H_kv, T_q)) * sizeof(fa::VarUnit);
 }
 
@@ -129,19 +136,26 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
       !make_map_strided(&mk, k.p, HD, k.T, k.st, k.heads, k.sh, 128, 1) ||
       !make_map_strided(&mv, v.p, HD, v.T, v.st, v.heads, v.sh, 128, 1) ||
       !make_map_strided(&mo, o.p, HD, o.heads, o.sh, o.T, o.st, o_tma ? std::min(G, 32) : 1,
-                        o_tma ? std::max(1, 32 / G) : 1))
+                        o_tma ? std::max(1, 32 / G) : 1, 32))
     return cuda_fail(cudaErrorInvalidValue);
 
   const long long cap = varlen_fwd_cap(B, q.heads, H_kv, q.T);
-  auto* plan = static_cast<fa::VarPlan*>(ws);
+  const bool direct = varlen_fwd_direct(B, q.heads, H_kv, q.T);
+  auto* plan = direct ? nullptr : static_cast<fa::VarPlan*>(ws);
   auto* list = reinterpret_cast<fa::VarUnit*>(plan + 1);
-  fa::varlen_plan_kernel<<<1, fa::kPlanThreads, 0, stream>>>(cu_q, cu_kv, plan, list, B, q.T, k.T, tp, causal);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e);
+  if (!direct) {
+    fa::varlen_plan_kernel<<<1, fa::kPlanThreads, 0, stream>>>(cu_q, cu_kv, plan, list, B, q.T, k.T, tp, causal);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
 
   fa::VarParams p;
   p.O = static_cast<__nv_bfloat16*>(const_cast<void*>(o.p));
   p.LSE = LSE;
+  p.cu_q = cu_q;
+  p.cu_kv = cu_kv;
+  p.B = B;
+  p.T_kv = k.T;
   p.plan = plan;
   p.list = list;
   p.o_st = o.st;
@@ -150,14 +164,15 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   p.H_kv = H_kv;
   p.G = G;
   p.tp = tp;
+  p.inv_g = (65536 + G - 1) / G;
   p.causal = causal;
   p.o_tma = o_tma ? 1 : 0;
   p.scale_log2 = masked_scale_log2(scale);
   p.idesc_qk = C::kIdescQK | (scale < 0.f ? fa::ptx::kIdescNegateA : 0u);
   p.timeout_ns = timeout_ns;
   p.drop_load = drop_load;
-  // A programmatic dependent launch: the grid sets up while the list is made
-  // and waits for it on the device.
+  // Behind a plan, a programmatic dependent launch: the grid sets up while the
+  // list is made and waits for it on the device.
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(cap * H_kv, sm_count(dev))));
   cfg.blockDim = dim3(C::kThreads);
@@ -167,7 +182,7 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = direct ? 0 : 1;
   e = cudaLaunchKernelEx(&cfg, fa::fa_varlen_fwd_kernel<HD>, mq, mk, mv, mo, p);
   if (e != cudaSuccess) return cuda_fail(e);
   return FA_OK;
@@ -191,7 +206,7 @@ fa_status_t varlen_fwd_impl(const void* Q, const void* K, const void* V, void* O
   if (varlen_fwd_cap(B, H, H_kv, T_q) * H_kv >= (1LL << 31) - 65536) return FA_ERR_UNSUPPORTED;
   const size_t need = varlen_fwd_ws(B, H, H_kv, T_q), n_lse = static_cast<size_t>(H) * T_q * 4;
   const size_t n_cu = (static_cast<size_t>(B) + 1) * 4;
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 128 != 0 || workspace_bytes < need)
+  if (need > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 128 != 0 || workspace_bytes < need))
     return FA_ERR_INVALID_ARG;
   // O, LSE and the workspace are disjoint from every input and each other.
   for (const Rows* in : {&q, &k, &v})

@@ -68,13 +68,16 @@ struct VarPlan {          // head of the workspace; the list follows
 struct VarParams {
   __nv_bfloat16* O;
   float* LSE;             // [H][T_q]
-  VarPlan* plan;
+  const int *cu_q, *cu_kv;
+  int B, T_kv;
+  VarPlan* plan;          // null: CTA i takes the i-th unit in the sequences' order, without a list
   const VarUnit* list;
   long long o_st, o_sh;   // element strides of O (token, head)
   int T_q;
   int H_kv;
   int G;                  // query heads per K/V head
   int tp;                 // tokens per tile: 128 / G
+  int inv_g;              // ceil(65536 / G): r / G = r * inv_g >> 16 for r < 128
   int causal;
   int o_tma;              // 1: G is a power of two, so a warp's 32 rows are a box of O
   float scale_log2;       // |scale| * log2(e), at least 2^-126
@@ -111,21 +114,25 @@ __device__ __forceinline__ SeqSpan seq_span(const int* cu_q, const int* cu_kv, i
   return s;
 }
 
-// Whether the offsets describe the caller's buffers: they start at 0 or later,
-// never decrease and end inside. If not, the call computes nothing and the
-// device status word says so. The same answer in every thread of the CTA.
+// Whether sequence i's offsets do not describe the caller's buffers (they
+// start at 0 or later, never decrease and end inside); the device status word
+// then says so.
+__device__ __forceinline__ bool span_bad(const int* cu_q, const int* cu_kv, int i, int T_q, int T_kv) {
+  const int q0 = cu_q[i], q1 = cu_q[i + 1], k0 = cu_kv[i], k1 = cu_kv[i + 1];
+  const bool bad = q0 < 0 || q1 < q0 || q1 > T_q || k0 < 0 || k1 < k0 || k1 > T_kv;
+  if (bad && atomicCAS(&g_status_word, 0u, kStatusBadOffsets) == 0u) {
+    g_status_info[0] = kRoleVarFetch;
+    g_status_info[1] = static_cast<unsigned int>(i);
+    g_status_info[2] = g_status_info[3] = 0u;
+  }
+  return bad;
+}
+
+// Whether all offsets are good; if not, the call computes nothing. The same
+// answer in every thread of the CTA.
 __device__ __forceinline__ bool offsets_ok(const int* cu_q, const int* cu_kv, int B, int T_q, int T_kv) {
   bool bad = false;
-  for (int i = threadIdx.x; i < B; i += kPlanThreads) {
-    const int q0 = cu_q[i], q1 = cu_q[i + 1], k0 = cu_kv[i], k1 = cu_kv[i + 1];
-    const bool here = q0 < 0 || q1 < q0 || q1 > T_q || k0 < 0 || k1 < k0 || k1 > T_kv;
-    if (here && atomicCAS(&g_status_word, 0u, kStatusBadOffsets) == 0u) {
-      g_status_info[0] = kRoleVarFetch;
-      g_status_info[1] = static_cast<unsigned int>(i);
-      g_status_info[2] = g_status_info[3] = 0u;
-    }
-    bad |= here;
-  }
+  for (int i = threadIdx.x; i < B; i += kPlanThreads) bad |= span_bad(cu_q, cu_kv, i, T_q, T_kv);
   return !__syncthreads_or(bad);
 }
 
@@ -245,6 +252,42 @@ struct VarJob {
   int kvh;        // K/V head; -1: no more units
 };
 
+// The unit of this CTA without a list (one warp): unit blockIdx.x / H_kv of
+// the sequences in order, K/V head blockIdx.x % H_kv. For grids that hold every
+// unit at once, where no order and no counter is needed: it saves the plan's
+// launch, 4 of 10 us for one short prompt.
+__device__ __forceinline__ void direct_unit(const VarParams& p, VarJob* job) {
+  const int lane = threadIdx.x & 31;
+  const int e = static_cast<int>(blockIdx.x) / p.H_kv;
+  int base = 0, found = -1, first = 0;
+  bool bad = false;
+  for (int c0 = 0; c0 < p.B; c0 += 32) {
+    const int i = c0 + lane;
+    int nu = 0;
+    if (i < p.B) {
+      bad |= span_bad(p.cu_q, p.cu_kv, i, p.T_q, p.T_kv);
+      const int nq = p.cu_q[i + 1] - p.cu_q[i];
+      nu = nq > 0 ? (nq - 1) / (2 * p.tp) + 1 : 0;
+    }
+    int incl = nu;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    const unsigned mine = __ballot_sync(0xffffffffu, e >= base + incl - nu && e < base + incl);
+    if (mine && found < 0) {
+      const int src = __ffs(mine) - 1;
+      found = c0 + src;
+      first = base + __shfl_sync(0xffffffffu, incl - nu, src);
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (__any_sync(0xffffffffu, bad) || found < 0) return;
+  job->u = make_unit(seq_span(p.cu_q, p.cu_kv, found), e - first, p.tp, p.causal);
+  job->kvh = static_cast<int>(blockIdx.x) - e * p.H_kv;
+}
+
 template <int HD>
 __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     fa_varlen_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -253,8 +296,8 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
   using C = FwdCfg<HD>;
   constexpr int kPolls = HD == 128 ? 8 : 1;   // as in the forward kernel
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_q_full;
-  __shared__ __align__(8) uint64_t bar_q_empty;
+  __shared__ __align__(8) uint64_t bar_q_full[2];
+  __shared__ __align__(8) uint64_t bar_q_empty[2];
   __shared__ __align__(8) uint64_t bar_kv_full[C::kStages];
   __shared__ __align__(8) uint64_t bar_kv_empty[C::kStages];
   __shared__ __align__(8) uint64_t bar_s_full[2];
@@ -263,6 +306,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
   __shared__ __align__(8) uint64_t bar_o_full[2];
   __shared__ __align__(8) uint64_t bar_job_full[2];
   __shared__ __align__(8) uint64_t bar_job_empty[2];
+  __shared__ __align__(8) uint64_t bar_claim;
   __shared__ __align__(8) uint64_t bar_drain;
   __shared__ __align__(16) VarJob jobs[2];
   __shared__ uint32_t tmem_base_slot;
@@ -285,13 +329,13 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
   ptx::fence_proxy_async_smem();
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(ptx::smem_u32(&bar_q_full), 1);
-    ptx::mbar_init(ptx::smem_u32(&bar_q_empty), 1);
     for (int s = 0; s < C::kStages; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bar_kv_full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&bar_kv_empty[s]), 1);
     }
     for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(ptx::smem_u32(&bar_q_full[t]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bar_q_empty[t]), 1);
       ptx::mbar_init(ptx::smem_u32(&bar_s_full[t]), 1);
       ptx::mbar_init(ptx::smem_u32(&bar_p_full[t]), C::kBM);
       ptx::mbar_init(ptx::smem_u32(&bar_p_half[t]), C::kBM);
@@ -299,6 +343,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&bar_job_full[t]), 1);
       ptx::mbar_init(ptx::smem_u32(&bar_job_empty[t]), 10);   // producer, issuer, eight softmax warps
     }
+    ptx::mbar_init(ptx::smem_u32(&bar_claim), 1);
     ptx::mbar_init(ptx::smem_u32(&bar_drain), 1);
     abort_flag = 0;
     ptx::fence_mbar_init();
@@ -321,7 +366,17 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
   if (warp >= 8) ptx::setmaxnreg_dec<C::kRegsControl>();
   if (warp == 10) {
     // ------------------------------------------------------------ unit fetch
-    if (lane == 0) {
+    if (!p.plan) {
+      VarJob job;
+      job.kvh = -1;
+      direct_unit(p, &job);
+      if (lane == 0) {
+        jobs[0] = job;
+        jobs[1].kvh = -1;
+        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[0]));
+        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[1]));
+      }
+    } else if (lane == 0) {
       asm volatile("griddepcontrol.wait;" ::: "memory");   // the list is complete and visible
       const int total = p.plan->num_units * p.H_kv;
       int idx = blockIdx.x;
@@ -339,6 +394,9 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
         jobs[n & 1] = job;
         ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
         if (job.kvh < 0) break;
+        // The next unit is taken when the loads of this one near their end, not
+        // at its start: a CTA in a long unit leaves the list to the others.
+        if (!wait_or_abort(ptx::smem_u32(&bar_claim), n & 1, abort_ptr, p.timeout_ns, kRoleVarFetch)) break;
         idx = static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1);
       }
     }
@@ -348,50 +406,58 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     if (lane == 0) {
       const uint64_t pol_q = ptx::policy_evict_first();
       const uint64_t pol_kv = ptx::policy_evict_last();
-      const uint32_t q_full = ptx::smem_u32(&bar_q_full);
       int it = 0;           // K/V loads so far (the ring position runs on across units)
-      int q_issued = 0;
+      int q_issued[2] = {0, 0};
       bool ok = true;
+      VarJob job;
+      // The next K (even it) or V tile of block j into its ring slot.
+      auto load_kv = [&](int j) {
+        const int slot = it % C::kStages;
+        if (!wait_or_abort<kPolls>(ptx::smem_u32(&bar_kv_empty[slot]), ((it / C::kStages) & 1) ^ 1u, abort_ptr,
+                                   p.timeout_ns, kRoleVarProducer))
+          return false;
+        const int me = it++;
+        if (me == p.drop_load) return true;   // test hook: this tile never arrives
+        const uint32_t full = ptx::smem_u32(&bar_kv_full[slot]);
+        ptx::mbar_arrive_expect_tx(full, C::kTileBytes);
+        const void* map = (me & 1) ? static_cast<const void*>(&tmV) : static_cast<const void*>(&tmK);
+        for (int c = 0; c < C::kChunks; ++c)
+          ptx::tma_load_3d(sKV + slot * C::kTileBytes + c * C::kChunkBytes, map, full, c * 64,
+                           job.u.kv_row0 + j * C::kBN, job.kvh, pol_kv);
+        return true;
+      };
       for (int n = 0; ok; ++n) {
         ok = wait_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
                                    kRoleVarProducer);
         if (!ok) break;
-        const VarJob job = jobs[n & 1];
+        job = jobs[n & 1];
         ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
         if (job.kvh < 0) break;
-        if (n > 0 && !wait_or_abort<kPolls>(ptx::smem_u32(&bar_q_empty), (n - 1) & 1, abort_ptr, p.timeout_ns,
-                                            kRoleVarProducer)) {
-          ok = false;
-          break;
-        }
-        ptx::mbar_arrive_expect_tx(q_full, C::kQTiles * C::kChunks * 128 * box_rows);
-        for (int t = 0; t < C::kQTiles; ++t)
+        // Each Q tile is free once its last Q K^T of the unit before has completed.
+        for (int t = 0; t < C::kQTiles && ok; ++t) {
+          if (n > 0 && !wait_or_abort<kPolls>(ptx::smem_u32(&bar_q_empty[t]), (n - 1) & 1, abort_ptr, p.timeout_ns,
+                                              kRoleVarProducer)) {
+            ok = false;
+            break;
+          }
+          const uint32_t q_full = ptx::smem_u32(&bar_q_full[t]);
+          ptx::mbar_arrive_expect_tx(q_full, C::kChunks * 128 * box_rows);
           for (int c = 0; c < C::kChunks; ++c)
             ptx::tma_load_3d(sQ + t * C::kTileBytes + c * C::kChunkBytes, &tmQ, q_full, c * 64, job.kvh * p.G,
                              job.u.q_row0 + t * p.tp, pol_q);
-        q_issued = n + 1;
-        for (int j = 0; j < job.u.nb1 && ok; ++j) {
-          for (int kv = 0; kv < 2; ++kv) {
-            const int slot = it % C::kStages;
-            if (!wait_or_abort<kPolls>(ptx::smem_u32(&bar_kv_empty[slot]), ((it / C::kStages) & 1) ^ 1u, abort_ptr,
-                                       p.timeout_ns, kRoleVarProducer)) {
-              ok = false;
-              break;
-            }
-            const int me = it++;
-            if (me == p.drop_load) continue;   // test hook: this tile never arrives
-            const uint32_t full = ptx::smem_u32(&bar_kv_full[slot]);
-            ptx::mbar_arrive_expect_tx(full, C::kTileBytes);
-            const void* map = kv ? static_cast<const void*>(&tmV) : static_cast<const void*>(&tmK);
-            for (int c = 0; c < C::kChunks; ++c)
-              ptx::tma_load_3d(sKV + slot * C::kTileBytes + c * C::kChunkBytes, map, full, c * 64,
-                               job.u.kv_row0 + j * C::kBN, job.kvh, pol_kv);
-          }
+          q_issued[t] = n + 1;
+          if (t == 0) ok = load_kv(0) && load_kv(0);
+        }
+        if (job.u.nb1 <= 2) ptx::mbar_arrive(ptx::smem_u32(&bar_claim));
+        for (int j = 1; j < job.u.nb1 && ok; ++j) {
+          if (job.u.nb1 > 2 && j == job.u.nb1 - 2) ptx::mbar_arrive(ptx::smem_u32(&bar_claim));
+          ok = load_kv(j) && load_kv(j);
         }
       }
       if (!ok || *abort_ptr) {
         // Let every copy this thread started land before the CTA exits.
-        if (q_issued > 0) drain_wait(q_full, (q_issued - 1) & 1, p.timeout_ns);
+        for (int t = 0; t < 2; ++t)
+          if (q_issued[t] > 0) drain_wait(ptx::smem_u32(&bar_q_full[t]), (q_issued[t] - 1) & 1, p.timeout_ns);
         for (int i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
           if (i != p.drop_load)
             drain_wait(ptx::smem_u32(&bar_kv_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
@@ -421,7 +487,39 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     bool ok = true;
     int it0 = 0;              // K/V loads of the units before this one
     int g[2] = {0, 0};        // key blocks of each tile so far (phases of s_full, p_half, p_full)
+    int was0 = 0, was1 = 0;   // key blocks of the unit before
+    // P V of tile t from the V tile of load it, once its probabilities are handed over.
+    auto finish_pv = [&](int t, int it, bool accumulate) {
+      const uint32_t par = static_cast<uint32_t>(g[t] - 1) & 1u;
+      if (!wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_half[t]), par, abort_ptr, p.timeout_ns, kRoleVarMma))
+        return false;
+      ptx::tc_fence_after();
+      issue_pv_half(t, it, accumulate, 0);
+      if (!wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_full[t]), par, abort_ptr, p.timeout_ns, kRoleVarMma))
+        return false;
+      ptx::tc_fence_after();
+      issue_pv_half(t, it, true, 1);
+      return true;
+    };
+    auto start_qk = [&](int t, int it) {
+      issue_qk(t, it);
+      ptx::mma_commit_warp(ptx::smem_u32(&bar_s_full[t]));
+      ++g[t];
+    };
     for (int n = 0; ok; ++n) {
+      // The last P V of the unit before, whose epilogue then runs beside this
+      // unit's first Q K^T.
+      if (n > 0 && was0 == was1) {
+        ok = finish_pv(0, it0 - 1, was1 > 1);
+        if (!ok) break;
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[0]));
+      }
+      if (n > 0) {
+        ok = finish_pv(1, it0 - 1, was1 > 1);
+        if (!ok) break;
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[1]));
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[(it0 - 1) % C::kStages]));
+      }
       ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
                                       kRoleVarMma);
       if (!ok) break;
@@ -430,44 +528,43 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
       if (kvh < 0) break;
-      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_q_full), n & 1, abort_ptr, p.timeout_ns, kRoleVarMma);
+      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_q_full[0]), n & 1, abort_ptr, p.timeout_ns, kRoleVarMma);
       if (ok)
         ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[it0 % C::kStages]), (it0 / C::kStages) & 1,
                                         abort_ptr, p.timeout_ns, kRoleVarMma);
-      // Step j: per tile P V of block j - 1, then Q K^T of block j. Every
-      // later K_{j+1} and V_j is waited for by the softmax warps before their
-      // first hand-off for block j.
-      for (int j = 0; j <= nb1 && ok; ++j) {
-        const int itK = it0 + 2 * j, itV = itK - 1;   // K_j and V_{j-1}
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int nb = t ? nb1 : nb0;
-          if (j > 0 && j <= nb) {
-            const uint32_t par = static_cast<uint32_t>(g[t] - 1) & 1u;
-            ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_half[t]), par, abort_ptr, p.timeout_ns, kRoleVarMma);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            issue_pv_half(t, itV, j > 1, 0);
-            ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_full[t]), par, abort_ptr, p.timeout_ns, kRoleVarMma);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            issue_pv_half(t, itV, true, 1);
-            if (j == nb) ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[t]));
-          }
-          if (t == 1 && j > 0) ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[itV % C::kStages]));
-          if (j < nb) {
-            issue_qk(t, itK);
-            ptx::mma_commit_warp(ptx::smem_u32(&bar_s_full[t]));
-            ++g[t];
-          }
+      if (!ok) break;
+      ptx::tc_fence_after();
+      start_qk(0, it0);
+      if (nb0 == 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[0]));
+      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_q_full[1]), n & 1, abort_ptr, p.timeout_ns, kRoleVarMma);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      start_qk(1, it0);
+      ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[it0 % C::kStages]));
+      if (nb1 == 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[1]));
+      // Later blocks: K_j and V_{j-1} were waited for by the softmax warps
+      // before their first hand-off for block j - 1. Tile 1 visits every block,
+      // tile 0 all (nb0 = nb1) or all but the last.
+      for (int j = 1; j < nb1 && ok; ++j) {
+        const int itK = it0 + 2 * j;
+        ok = finish_pv(0, itK - 1, j > 1);
+        if (!ok) break;
+        if (j < nb0) {
+          start_qk(0, itK);
+          if (j == nb0 - 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[0]));
+        } else {
+          ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[0]));
         }
-        if (ok && j < nb1) {
-          ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[itK % C::kStages]));
-          if (j == nb1 - 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty));
-        }
+        ok = finish_pv(1, itK - 1, j > 1);
+        if (!ok) break;
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[(itK - 1) % C::kStages]));
+        start_qk(1, itK);
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[itK % C::kStages]));
+        if (j == nb1 - 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[1]));
       }
       it0 += 2 * nb1;
+      was0 = nb0;
+      was1 = nb1;
     }
     if (!ok) {
       // Wait for every MMA already issued before TMEM is freed.
@@ -481,8 +578,6 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     const int t = warp >> 2;                 // query tile
     const int quarter = warp & 3;            // TMEM lane quarter
     const int row = quarter * 32 + lane;     // row within the tile: token row / G, head row % G
-    const int x = min(row / p.G, p.tp - 1);
-    const int hq = row - (row / p.G) * p.G;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem_base + lane_addr + C::kColS + 128 * t;
     const uint32_t tO = tmem_base + lane_addr + C::kColO + HD * t;
@@ -493,29 +588,34 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
       ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
                                       kRoleVarSoftmax);
       if (!ok) break;
-      const VarJob job = jobs[n & 1];
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
+      // The slot is given back in the epilogue, which reads the rest of it
+      // (few values may live through the block loop without spilling).
+      const VarJob& job = jobs[n & 1];
       if (job.kvh < 0) break;
-      const int nb = t ? job.u.nb1 : job.u.nb0;
-      const int xt = t * p.tp + x;             // token of this row within the unit
+      const int nb1 = job.u.nb1, nb = t ? nb1 : job.u.nb0, n_kv = job.u.n_kv;
+      const int clear_from = t ? job.u.nb0 : 0;   // first block whose V this tile clears (see below)
       // Keys this row sees. Rows past the sequence's end (never stored) take
       // the last token's, so that they do not mask blocks the others need not.
       const int limit =
-          p.causal ? max(0, min(job.u.n_kv, job.u.lim0 + min(xt, job.u.n_tok - 1))) : job.u.n_kv;
+          p.causal ? max(0, min(n_kv, job.u.lim0 + min(t * p.tp + min((row * p.inv_g) >> 16, p.tp - 1),
+                                                       job.u.n_tok - 1)))
+                   : n_kv;
       float m_use = -INFINITY;   // raw-score maximum the exponentials are taken against
       float l = 0.f;             // running sum of exp, relative to m_use (for LSE)
       float lo = 0.f;            // the same with each block's largest term as P V sees it (for O)
       for (int j = 0; j < nb; ++j, ++g) {
+        // V_j and K_{j+1} must have landed before this block's hand-off (the
+        // issuer does not wait for them); waiting here costs nothing, S_t(j)
+        // comes later.
         const int itV = it0 + 2 * j + 1;
-        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[itV % C::kStages]), (itV / C::kStages) & 1,
-                                        abort_ptr, p.timeout_ns, kRoleVarSoftmax);
-        if (ok && j + 1 < job.u.nb1)
+        const int have = n_kv - j * C::kBN;    // keys of the sequence in this block
+          ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[itV % C::kStages]), (itV / C::kStages) & 1,
+                                          abort_ptr, p.timeout_ns, kRoleVarSoftmax);
+        if (ok && j + 1 < nb1)
           ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[(itV + 1) % C::kStages]),
                                           ((itV + 1) / C::kStages) & 1, abort_ptr, p.timeout_ns, kRoleVarSoftmax);
         if (!ok) break;
-        const int have = job.u.n_kv - j * C::kBN;    // keys of the sequence in this block
-        if (have < C::kBN && t == (j < job.u.nb0 ? 0 : 1)) {
+        if (have < C::kBN && j >= clear_from) {
           // Whole 128-byte rows, so the swizzle does not matter. Tile 0's P V
           // is issued first, so its warps clear V for both tiles.
           uint8_t* v_tile = generic + C::kSmemQ + (itV % C::kStages) * C::kTileBytes;
@@ -529,6 +629,28 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
                                         kRoleVarSoftmax);
         if (!ok) break;
         ptx::tc_fence_after();
+        const int valid = limit - j * C::kBN;        // keys of this block that this row sees
+        // Scores past a row's limit become -inf in TMEM, 32 columns at a time,
+        // before the common path reads them. A loop of few instructions: this
+        // runs about once per unit, and the unrolled masking of a block in
+        // registers spent most of its time fetching instructions.
+        if (!__all_sync(0xffffffffu, valid >= C::kBN)) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const int v = valid - 32 * c;
+            if (__all_sync(0xffffffffu, v >= 32)) continue;
+            uint32_t r[32];
+            ptx::tmem_ld32(tS + 32 * c, r);
+            ptx::tmem_ld_wait();
+            ptx::reg_fence32(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i >= v) r[i] = __float_as_uint(-INFINITY);
+            ptx::tmem_st32(tS + 32 * c, r);
+          }
+          ptx::tmem_st_wait();
+        }
+        // The loads also reduce each 32-column piece to its maximum.
         uint32_t s[4][32];
         float mr[4];
 #pragma unroll
@@ -539,32 +661,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
           ptx::reg_fence32(s[c]);
           ptx::reg_fence1(mr[c]);
         }
-        const int valid = limit - j * C::kBN;        // keys of this block that this row sees
-        float mt;
-        if (__all_sync(0xffffffffu, valid >= C::kBN)) {
-          mt = ptx::max3(mr[0], mr[1], fmaxf(mr[2], mr[3]));
-        } else {
-          // Per 32 keys: all seen by the whole warp (as loaded), or masked
-          // element by element.
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (!__all_sync(0xffffffffu, valid >= 32 * c + 32)) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (32 * c + i >= valid) s[c][i] = __float_as_uint(-INFINITY);
-              float m4[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                m4[k] = fmaxf(__uint_as_float(s[c][8 * k]), __uint_as_float(s[c][8 * k + 1]));
-#pragma unroll
-                for (int i = 2; i < 8; i += 2)
-                  m4[k] = ptx::max3(m4[k], __uint_as_float(s[c][8 * k + i]), __uint_as_float(s[c][8 * k + i + 1]));
-              }
-              mr[c] = ptx::max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-            }
-          }
-          mt = ptx::max3(mr[0], mr[1], fmaxf(mr[2], mr[3]));
-        }
+        const float mt = ptx::max3(mr[0], mr[1], fmaxf(mr[2], mr[3]));
         // A row sees keys from the first block on or none at all, so after
         // block 0 the maximum is -inf only for a row that sees nothing.
         float alpha = 1.f;
@@ -635,72 +732,79 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
         ptx::tc_fence_before();
         ptx::mbar_arrive(ptx::smem_u32(&bar_p_full[t]));
       }
+      // A block that only tile 1 visits: its V load is waited for all the same,
+      // so that no later wait on its slot meets the phase before.
+      for (int j = nb; j < nb1 && ok; ++j) {
+        const int itV = it0 + 2 * j + 1;
+        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[itV % C::kStages]), (itV / C::kStages) & 1,
+                                        abort_ptr, p.timeout_ns, kRoleVarSoftmax);
+      }
+      const int xr = (row * p.inv_g) >> 16;             // token of this row within the tile
+      const int head = job.kvh * p.G + row - xr * p.G;
+      const long long token = static_cast<long long>(job.u.q_row0) + t * p.tp + xr;
+      const bool live = row < box_rows && t * p.tp + xr < job.u.n_tok;
+      const bool none = limit == 0;
+      if (live && ok)
+        p.LSE[static_cast<long long>(head) * p.T_q + token] =
+            none ? -INFINITY : (m_use * sl2 + __log2f(l)) * 0.69314718055994530942f;
+      const float inv_l = 1.f / lo;
+      // The warp's rows as a box of O: first token, last token, first head.
+      const int x_first = t * p.tp + ((quarter * 32 * p.inv_g) >> 16);
+      const int x_last = t * p.tp + (((quarter * 32 + 31) * p.inv_g) >> 16);
+      const int h_first = quarter * 32 - (x_first - t * p.tp) * p.G;
+      const bool boxed = p.o_tma && x_last < job.u.n_tok;
+      const int box_head = job.kvh * p.G + h_first, box_token = job.u.q_row0 + x_first;
+      const uint32_t stage = sStage + static_cast<uint32_t>(warp) * 4096u;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
       if (ok)
         ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_o_full[t]), n & 1, abort_ptr, p.timeout_ns,
                                         kRoleVarSoftmax);
       if (!ok) break;
       ptx::tc_fence_after();
-      it0 += 2 * job.u.nb1;
-      const bool live = row < box_rows && xt < job.u.n_tok;
-      const bool none = limit == 0;
-      const long long token = static_cast<long long>(job.u.q_row0) + xt;
-      const int head = job.kvh * p.G + hq;
-      const float inv_l = 1.f / lo;
-      // O leaves through shared memory in 64-column pieces that one lane
-      // stores with a tiled TMA store, when the warp's rows are a box of O that
-      // lies inside the sequence; else every thread writes its row.
-      const uint32_t stage = sStage + static_cast<uint32_t>(warp) * (32u * 128u);
-      const int x_first = quarter * 32 / p.G, x_last = (quarter * 32 + 31) / p.G;
-      const bool boxed = p.o_tma && t * p.tp + x_last < job.u.n_tok;
-      __nv_bfloat16* orow = p.O + token * p.o_st + head * p.o_sh;
+      it0 += 2 * nb1;
+      // O leaves in 32-column pieces through shared memory, where one lane
+      // stores them with a tiled TMA store, when the warp's rows are a box of O
+      // that lies inside the sequence; else every thread writes its row. Two
+      // staging buffers of 32 rows x 64 bytes (64-byte swizzle) per warp.
+#pragma unroll 1
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t o[32];
+        ptx::tmem_ld32(tO + 32 * c, o);
+        ptx::tmem_ld_wait();
+        ptx::reg_fence32(o);
+        uint32_t packed[16];
 #pragma unroll
-      for (int k = 0; k < HD / 64; ++k) {
+        for (int i = 0; i < 16; ++i)
+          packed[i] = ptx::pack_bf16x2(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
+        if (none) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) packed[i] = 0u;
+        }
         if (boxed) {
-          // The staging rows are free once this warp's previous store has read them.
-          if (lane == 0) ptx::bulk_wait_group_read0();
+          if (lane == 0) ptx::bulk_wait_group_read1();   // the buffer's previous store has read it
           __syncwarp();
-        }
+          const uint32_t buf = stage + static_cast<uint32_t>(c & 1) * 2048u;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t o[32];
-          ptx::tmem_ld32(tO + 64 * k + 32 * h, o);
-          ptx::tmem_ld_wait();
-          ptx::reg_fence32(o);
-          uint32_t packed[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            packed[i] =
-                none ? 0u : ptx::pack_bf16x2(__uint_as_float(o[2 * i]) * inv_l, __uint_as_float(o[2 * i + 1]) * inv_l);
-          if (boxed) {
-            const uint32_t row_addr = stage + static_cast<uint32_t>(lane) * 128u;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const uint32_t unit = 4u * h + v;      // 16-byte unit within the 128-byte row
-              const uint32_t addr = row_addr + ((unit ^ static_cast<uint32_t>(lane & 7)) << 4);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(packed[4 * v]),
-                           "r"(packed[4 * v + 1]), "r"(packed[4 * v + 2]), "r"(packed[4 * v + 3])
-                           : "memory");
-            }
-          } else if (live) {
-            uint4* dst = reinterpret_cast<uint4*>(orow + 64 * k + 32 * h);
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              dst[v] = make_uint4(packed[4 * v], packed[4 * v + 1], packed[4 * v + 2], packed[4 * v + 3]);
+          for (int v = 0; v < 4; ++v) {
+            const uint32_t addr = buf + static_cast<uint32_t>(lane) * 64u + ((v ^ ((lane >> 1) & 3u)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(packed[4 * v]),
+                         "r"(packed[4 * v + 1]), "r"(packed[4 * v + 2]), "r"(packed[4 * v + 3])
+                         : "memory");
           }
-        }
-        if (boxed) {
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            ptx::tma_store_3d(&tmO, stage, 64 * k, job.kvh * p.G + (quarter * 32 - x_first * p.G),
-                              job.u.q_row0 + t * p.tp + x_first);
+            ptx::tma_store_3d(&tmO, buf, 32 * c, box_head, box_token);
             ptx::bulk_commit_group();
           }
+        } else if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(p.O + token * p.o_st + head * p.o_sh + 32 * c);
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            dst[v] = make_uint4(packed[4 * v], packed[4 * v + 1], packed[4 * v + 2], packed[4 * v + 3]);
         }
       }
-      if (live)
-        p.LSE[static_cast<long long>(head) * p.T_q + token] =
-            none ? -INFINITY : (m_use * sl2 + __log2f(l)) * 0.69314718055994530942f;
     }
   }
 

@@ -531,12 +531,15 @@ def _out_bf16(name, t, device, shape):
 
 
 def _workspace(workspace, need, device):
-    """(tensor, bytes) of the caller's workspace, or of a new one."""
+    """(tensor, pointer, bytes) of the caller's workspace, or of a new one if any is needed."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device), need
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
     if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _raw_stream(device) -> int:
@@ -581,11 +584,11 @@ def fa_fwd_varlen(q, k, v, cu_q, cu_kv, o=None, lse=None, scale: float | None = 
     def run():
         out, o_st = _out_bf16("o", o, device, (T_q, H, d))
         out_lse = _out_lse(lse, (H, T_q), device)
-        ws, ws_bytes = _workspace(workspace, lib.fa_fwd_varlen_workspace_bytes(B, H, H_kv, T_q), device)
+        ws, ws_ptr, ws_bytes = _workspace(workspace, lib.fa_fwd_varlen_workspace_bytes(B, H, H_kv, T_q), device)
         st = lib.fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), out_lse.data_ptr(),
                                cu_q.data_ptr(), cu_kv.data_ptr(), B, H, H_kv, T_q, T_kv, d,
                                _LL8(*q_st, *k_st, *v_st, *o_st), d ** -0.5 if scale is None else scale, bool(causal),
-                               ws.data_ptr(), ws_bytes, _raw_stream(device))
+                               ws_ptr, ws_bytes, _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_fwd_varlen")
         return out, out_lse
@@ -631,11 +634,11 @@ def fa_bwd_varlen(q, k, v, o, do, lse, cu_q, cu_kv, dq=None, dk=None, dv=None, s
         gq, gq_st = _out_bf16("dq", dq, device, rows)
         gk, gk_st = _out_bf16("dk", dk, device, keys)
         gv, gv_st = _out_bf16("dv", dv, device, keys)
-        ws, ws_bytes = _workspace(workspace, lib.fa_bwd_varlen_workspace_bytes(B, H, H_kv, T_q, T_kv), device)
+        ws, ws_ptr, ws_bytes = _workspace(workspace, lib.fa_bwd_varlen_workspace_bytes(B, H, H_kv, T_q, T_kv), device)
         st = lib.fa_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
                                gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), cu_q.data_ptr(), cu_kv.data_ptr(), B, H,
                                H_kv, T_q, T_kv, d, _LL16(*inputs, *gq_st, *gk_st, *gv_st),
-                               d ** -0.5 if scale is None else scale, bool(causal), ws.data_ptr(), ws_bytes,
+                               d ** -0.5 if scale is None else scale, bool(causal), ws_ptr, ws_bytes,
                                _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_bwd_varlen")
@@ -696,12 +699,12 @@ def fa_fwd_prefix(q, k_prefix, v_prefix, k, v, seq_lens, o=None, lse=None, scale
     def run():
         out, o_st = _out_bf16("o", o, device, rows)
         out_lse = _out_lse(lse, (B, H, N_q), device)
-        ws, ws_bytes = _workspace(workspace, lib.fa_fwd_prefix_workspace_bytes(B, H, H_kv, N_q, N_prefix, N_own, d),
+        ws, ws_ptr, ws_bytes = _workspace(workspace, lib.fa_fwd_prefix_workspace_bytes(B, H, H_kv, N_q, N_prefix, N_own, d),
                                   device)
         st = lib.fa_fwd_prefix(q.data_ptr(), *p_ptr, k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
                                out_lse.data_ptr(), B, H, H_kv, N_q, N_prefix, N_own, d,
                                _LL18(*q_st, *p_st, *k_st, *v_st, *o_st), d ** -0.5 if scale is None else scale,
-                               bool(causal), ws.data_ptr(), ws_bytes, _raw_stream(device))
+                               bool(causal), ws_ptr, ws_bytes, _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_fwd_prefix")
         return out, out_lse

@@ -390,7 +390,9 @@ typedef struct {
 
 /*
  * fa_fwd_varlen_workspace_bytes -- device workspace fa_fwd_varlen needs (the
- * list of its units of work). 0 for sizes it rejects.
+ * list of its units of work). 0 when the units fit the device at once (no list
+ * is needed then, and workspace may be NULL) and for sizes it rejects. Depends
+ * on the current device's SM count (148 when there is none).
  */
 size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q);
 
@@ -423,8 +425,8 @@ size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q);
  * With offsets that do not describe the buffers (negative, decreasing, past
  * T_q or T_kv) nothing is written, and fa_get_device_status reports
  * FA_ERR_INVALID_ARG.
- * Two launches on `stream` (the unit list, then the attention as its
- * programmatic dependent). Each row's result depends on its sequence alone,
+ * One launch on `stream`, or two (the unit list, then the attention as its
+ * programmatic dependent) when the units do not fit the device at once. Each row's result depends on its sequence alone,
  * not on the batch around it, and is the same from run to run.
  * Limits: T_q, T_kv >= 1, H * T_q and H_kv * T_kv below 2^31, d in {64, 128},
  * scale finite. Q, K, V, O 16-byte, LSE and offsets 4-byte aligned; O, LSE and

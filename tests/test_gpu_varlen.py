@@ -88,10 +88,13 @@ LENS = [
 
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("H,H_kv,d", [(4, 1, 128), (8, 2, 64), (2, 2, 128), (7, 1, 64), (3, 1, 128)])
+@pytest.mark.parametrize("empty", [0, 200])
 @pytest.mark.parametrize("case", range(len(LENS)))
-def test_lengths(case, H, H_kv, d, causal):
+def test_lengths(case, empty, H, H_kv, d, causal):
+    """Without a list of units, and (200 empty sequences behind) with one."""
     ql, kl = LENS[case]
-    kl = kl or ql
+    kl = (kl or ql) + [0] * empty
+    ql = ql + [0] * empty
     q, k, v = draw(case * 100 + H + d, (sum(ql), H, d), (max(1, sum(kl)), H_kv, d), (max(1, sum(kl)), H_kv, d))
     check(q, k, v, ql, kl, causal)
 
@@ -233,17 +236,18 @@ def test_dropped_load_times_out_cleanly(drop):
     check(q.cpu(), k.cpu(), v.cpu(), [300], [300], True)
 
 
+@pytest.mark.parametrize("empty", [0, 300])
 @pytest.mark.parametrize("bad", [[0, 50, 40, 100], [-1, 20, 40, 100], [0, 20, 40, 101], [0, 20, 1 << 30, 100]])
-def test_bad_offsets_are_reported_and_write_nothing(bad):
+def test_bad_offsets_are_reported_and_write_nothing(bad, empty):
     """The plan's own check of the offsets finds them, lists no work and says so in the status word."""
     q, k, v = (x.cuda() for x in draw(61, (100, 4, 64), (100, 2, 64), (100, 2, 64)))
-    good = offsets([20, 20, 60]).cuda()
-    bad = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    good = offsets([20, 20, 60] + [0] * empty).cuda()
+    bad = torch.tensor(bad + bad[-1:] * empty, dtype=torch.int32, device="cuda")
     o = torch.full((100, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
     for cq, ck in ((bad, good), (good, bad), (bad, bad)):
         fa.fa_fwd_varlen(q, k, v, cq, ck, o=o)
         st, info = fa.fa_get_device_status()
-        assert st == fa.FA_ERR_INVALID_ARG and info[0] == 16 and info[1] < 3, (st, info)
+        assert st == fa.FA_ERR_INVALID_ARG and info[0] == 16 and info[1] < 3 + empty, (st, info)
     assert bool((o == 3).all())
     assert fa.fa_get_device_status()[0] == fa.FA_OK
 
@@ -262,4 +266,5 @@ def test_binding_refusals():
     with pytest.raises(fa.FaError):
         fa.fa_fwd_varlen(q, k, v, cu, cu, o=q)
     with pytest.raises(fa.FaError):
-        fa.fa_fwd_varlen(q, k, v, cu, cu, workspace=torch.empty(32, dtype=torch.uint8, device="cuda"))
+        x = torch.zeros(20000, 4, 64, dtype=torch.bfloat16, device="cuda")
+        fa.fa_fwd_varlen(x, k, v, offsets([20000]).cuda(), cu, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))

@@ -17,7 +17,7 @@ def lib():
 
 def fwd(lib, q_st=None, k_st=None, v_st=None, o_st=None, **kw):
     a = dict(Q=A, K=A + GAP, V=A + 2 * GAP, O=A + 3 * GAP, L=A + 4 * GAP, cq=A + 5 * GAP, ck=A + 6 * GAP, B=2, H=8,
-             H_kv=2, Tq=100, Tk=200, d=128, scale=0.1, causal=1, ws=A + 7 * GAP, n=1 << 20)
+             H_kv=2, Tq=100000, Tk=200, d=128, scale=0.1, causal=1, ws=A + 7 * GAP, n=1 << 20)
     a.update(kw)
     st = None
     if q_st or k_st or v_st or o_st:
@@ -78,14 +78,15 @@ def test_backward_refusals(lib, kw, expect):
 
 
 def test_workspace_sizes(lib):
-    assert fa.fa_fwd_varlen_workspace_bytes(1, 8, 2, 1) > 0
-    for bad in [(0, 8, 2, 1), (1, 8, 3, 1), (1, 8, 0, 1), (1, 258, 2, 1), (1, 8, 2, 0)]:
+    assert fa.fa_fwd_varlen_workspace_bytes(1, 8, 2, 1) == 0           # every unit at once: no list
+    assert fa.fa_fwd_varlen_workspace_bytes(1, 8, 2, 100000) > 0
+    for bad in [(0, 8, 2, 99999), (1, 8, 3, 99999), (1, 8, 0, 99999), (1, 258, 2, 99999), (1, 8, 2, 0)]:
         assert fa.fa_fwd_varlen_workspace_bytes(*bad) == 0
     assert fa.fa_bwd_varlen_workspace_bytes(1, 8, 2, 1, 1) > 0
     for bad in [(0, 8, 2, 1, 1), (1, 8, 3, 1, 1), (1, 258, 2, 1, 1), (1, 8, 2, 0, 1), (1, 8, 2, 1, 0)]:
         assert fa.fa_bwd_varlen_workspace_bytes(*bad) == 0
     assert bwd(lib, n=fa.fa_bwd_varlen_workspace_bytes(2, 8, 2, 100, 200) - 1) == BAD
-    assert fwd(lib, n=fa.fa_fwd_varlen_workspace_bytes(2, 8, 2, 100) - 1) == BAD
+    assert fwd(lib, n=fa.fa_fwd_varlen_workspace_bytes(2, 8, 2, 100000) - 1) == BAD
 
 
 def test_fault_hook_rejects_zero_timeout(lib):
