@@ -318,13 +318,15 @@ fa_status_t varlen_bwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   p.H_kv = H_kv;
   p.G = G;
   p.tp = tp;
+  p.inv_g = (65536 + G - 1) / G;
   p.causal = causal;
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  p.scale_log2 = masked_scale_log2(scale);
   p.scale = scale;
+  p.idesc_s = C::kIdescS | (scale < 0.f ? fa::ptx::kIdescNegateA : 0u);
   p.timeout_ns = timeout_ns;
   p.drop_load = drop_load;
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(w.units * H_kv, sm_count(dev))));
-  cfg.blockDim = dim3(C::kThreads);
+  cfg.blockDim = dim3(fa::kVarBwdThreads);
   cfg.dynamicSmemBytes = kSmem;
   e = cudaLaunchKernelEx(&cfg, fa::fa_varlen_bwd_kernel<HD>, mq, mk, mv, mdo, p);
   if (e != cudaSuccess) return cuda_fail(e);

@@ -13,14 +13,21 @@
 //   * Only pairs of blocks with a visible (row, key) are visited: the query
 //     role stops at the last key its tile sees, the key-block role starts at
 //     the first tile that sees its keys.
-//   * The units of both roles are listed by varlen_bwd_plan_kernel, the
-//     most expensive first, and a persistent grid takes them by a counter.
+//   * The units of both roles are listed by varlen_bwd_plan_kernel: those of
+//     the key-block role, then those of the query role, the most expensive
+//     first in each. A persistent grid takes them by a counter. Within a role
+//     the pipeline runs on from unit to unit (rings and barrier phases are
+//     never reset): the next unit's fixed tiles are loaded as soon as the last
+//     products that read the old ones have completed, and its first products
+//     run beside the epilogue. A CTA changes roles once.
 //   * Rows of a tile that lie behind a sequence's end belong to the next
-//     sequence or to nobody and may hold anything. In the query role they only
-//     reach accumulator rows that are not stored; where they are summed over
-//     (Q and dO in the key-block role, K in the query role) they are cleared
-//     in shared memory once the products that form S and dP have read them,
-//     and their P and dS are zeroed by selection.
+//     sequence or to nobody and may hold anything. Scores of invisible pairs
+//     become -inf in tensor memory before the exponential (the tensor core
+//     forms -S for a negative scale, as in the forward, and scale = 0 runs as
+//     2^-126), and dP of rows behind the end becomes 0. Where such rows are
+//     summed over (Q and dO in the key-block role, K in the query role) they
+//     are cleared in shared memory once the products that form S and dP have
+//     read them; elsewhere they only reach accumulator rows that are not stored.
 // Three launches: the plan; -LSE log2(e) and -D of every tile row
 // (varlen_bwd_rows_kernel); the products.
 #pragma once
@@ -61,8 +68,11 @@ struct VarBwdParams {
   const float* ndelta;    // the same shape: -D, or 0
   int tile_cap;
   int H_kv, G, tp;
+  int inv_g;              // ceil(65536 / G): r / G = r * inv_g >> 16 for r < 128
   int causal;
-  float scale_log2, scale;
+  float scale_log2;       // |scale| * log2(e), at least 2^-126
+  float scale;
+  uint32_t idesc_s;       // instruction descriptor of S and S^T (A negated when scale < 0)
   unsigned long long timeout_ns;
   int drop_load;
 };
@@ -98,15 +108,16 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int cum[kPlanThreads + 1];        // units of the chunk before each sequence
   __shared__ int cum_t[kPlanThreads + 1];      // its query tiles
   __shared__ SeqSpan span[kPlanThreads];
-  __shared__ int hist[kPlanClasses];
+  __shared__ int hist[2 * kPlanClasses];       // key-block role, query role
   __shared__ int warp_sums[kPlanThreads / 32];
+  static_assert(2 * kPlanClasses == kPlanThreads, "one class per thread");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   if (!offsets_ok(cu_q, cu_kv, B, T_q, T_kv)) {
     if (tid == 0) plan->num_units = plan->num_tiles = plan->next = 0;
     return;
   }
-  if (tid < kPlanClasses) hist[tid] = 0;
+  hist[tid] = 0;
   int total = 0, total_tiles = 0;
   for (int round = 0; round < 2; ++round) {
     int tile_base = 0;
@@ -136,7 +147,8 @@ __global__ void __launch_bounds__(kPlanThreads)
         const SeqSpan s = span[lo];
         const int nt = s.nq / tp + (s.nq % tp != 0), nk = (s.nkv + 127) / 128;
         const VarBwdUnit u = make_bwd_unit(s, tile_base + cum_t[lo], e - cum[lo], nk, nt, tp, causal);
-        const int cls = cost_class(max(1, (u.dkdv ? 4 : 3) * u.n));
+        // (the place of a class in `hist`: expensive ones first)
+        const int cls = (u.dkdv ? 0 : kPlanClasses) + kPlanClasses - 1 - cost_class(max(1, u.n));
         const int at = atomicAdd(&hist[cls], 1);
         if (round == 1) list[at] = u;
         if (round == 0 && !u.dkdv) tiles[u.tile0 + u.blk] = make_int2(s.q0 + u.blk * tp, min(tp, s.nq - u.blk * tp));
@@ -148,9 +160,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     __syncthreads();
     if (round == 0) {
       int sum;
-      const int mine = tid < kPlanClasses ? hist[kPlanClasses - 1 - tid] : 0;
+      const int mine = hist[tid];
       const int incl = block_scan(mine, warp_sums, sum);
-      if (tid < kPlanClasses) hist[kPlanClasses - 1 - tid] = incl - mine;
+      hist[tid] = incl - mine;
       __syncthreads();
     }
   }
@@ -228,6 +240,40 @@ struct VarBwdJob {
   int kvh;       // -1: no more units
 };
 
+// Shared by both roles' loops: two job slots, handed over by the fetch warp.
+struct VarBwdJobs {
+  VarBwdJob job[2];
+  uint64_t full[2], empty[2];   // empty: producer, issuer, eight elementwise warps
+  uint64_t claim;               // the producer nears the end of a unit's loads
+};
+
+// A barrier of the ten warps that work on units (the fetch warp is not one).
+__device__ __forceinline__ void role_sync() { asm volatile("bar.sync 1, 320;" ::: "memory"); }
+
+// role_sync that tells every thread whether `ok` holds in all of them.
+__device__ __forceinline__ bool role_sync_and(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 320, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// issue_tile_qk with the caller's instruction descriptor.
+template <int HD>
+__device__ __forceinline__ void issue_tile_qk_desc(uint32_t d_tmem, uint32_t a_tile, uint32_t b_tile, uint32_t idesc) {
+  const uint64_t a_desc = ptx::desc_kmajor_sw128(a_tile), b_desc = ptx::desc_kmajor_sw128(b_tile);
+  if constexpr (HD == 128)
+    mma_ss_k128_warp64(d_tmem, ptx::desc_lo(a_desc), ptx::desc_lo(b_desc), ptx::desc_hi(a_desc), idesc, 0u);
+  else
+    mma_ss_k64_warp64(d_tmem, ptx::desc_lo(a_desc), ptx::desc_lo(b_desc), ptx::desc_hi(a_desc), idesc, 0u);
+}
+
 // Zeroes rows [from, to) of the 128-row tile at `tile` (generic address),
 // whole 128-byte rows, with 256 threads.
 template <int HD>
@@ -238,35 +284,49 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int to, int 
       reinterpret_cast<uint4*>(tile + c * C::kChunkBytes + from * 128)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Takes the next unit off the list (one thread).
-__device__ __forceinline__ void fetch_job(const VarBwdParams& p, int idx, VarBwdJob* job) {
-  job->kvh = -1;
-  if (idx < p.plan->num_units * p.H_kv) {
-    const int e = idx / p.H_kv;
-    job->u = p.list[e];
-    job->kvh = idx - e * p.H_kv;
+// Columns of this thread's row outside [from, to) of the 64 at `taddr` become
+// `fill`. A short loop, for the few blocks that need it.
+__device__ __forceinline__ void mask_columns(uint32_t taddr, int from, int to, uint32_t fill) {
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    const int lo = from - 32 * c, hi = to - 32 * c;
+    if (__all_sync(0xffffffffu, lo <= 0 && hi >= 32)) continue;
+    uint32_t r[32];
+    ptx::tmem_ld32(taddr + 32 * c, r);
+    ptx::tmem_ld_wait();
+    ptx::reg_fence32(r);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < lo || i >= hi) r[i] = fill;
+    ptx::tmem_st32(taddr + 32 * c, r);
   }
+  ptx::tmem_st_wait();
 }
 
-// A unit of the query role. Barriers live for the unit: initialised here, and
-// every arrival on them has been waited for or made by a thread of this CTA
-// before the closing __syncthreads.
+// This thread's row of HD / 2 accumulator columns, times `mul`, to bf16.
 template <int HD>
-__device__ __forceinline__ bool varlen_dq_unit(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                               const CUtensorMap& tmdO, const VarBwdParams& p, const VarBwdUnit u,
-                                               const int kvh, const uint32_t tmem_base, volatile int* abort_ptr,
-                                               VarBwdJob* next_job) {
+__device__ __forceinline__ void store_half_row(uint32_t taddr, float mul, __nv_bfloat16* dst, bool store) {
+#pragma unroll 1
+  for (int c = 0; c < HD / 64; ++c) store_row32(taddr + 32 * c, mul, dst + 32 * c, store);
+}
+
+// The query role: units from job n0 on, to the end of the list.
+template <int HD>
+__device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                               const CUtensorMap& tmdO, const VarBwdParams& p, VarBwdJobs& jobs, int n0,
+                                               const uint32_t tmem_base, volatile int* abort_ptr) {
   using C = BwdCfg<HD>;
   using D = DqCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_in_full;
+  __shared__ __align__(8) uint64_t bar_q_full, bar_q_empty;      // Q of the unit
+  __shared__ __align__(8) uint64_t bar_do_full, bar_do_empty;    // dO of the unit
   __shared__ __align__(8) uint64_t bar_k_full[D::kKSlots];
   __shared__ __align__(8) uint64_t bar_k_empty[D::kKSlots];
   __shared__ __align__(8) uint64_t bar_v_full[D::kVSlots];
   __shared__ __align__(8) uint64_t bar_v_empty[D::kVSlots];
-  __shared__ __align__(8) uint64_t bar_st_full;
-  __shared__ __align__(8) uint64_t bar_dpt_full;
-  __shared__ __align__(8) uint64_t bar_s_free;
+  __shared__ __align__(8) uint64_t bar_st_full;    // S_j complete
+  __shared__ __align__(8) uint64_t bar_dpt_full;   // dP_j complete
+  __shared__ __align__(8) uint64_t bar_s_free;     // S_j loaded (and K_{j+1} landed)
   __shared__ __align__(8) uint64_t bar_dp_free;
   __shared__ __align__(8) uint64_t bar_p_full[2];
   __shared__ __align__(8) uint64_t bar_acc_full;
@@ -274,7 +334,6 @@ __device__ __forceinline__ bool varlen_dq_unit(const CUtensorMap& tmQ, const CUt
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int n = u.n;
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t smem_base = (raw + 1023u) & ~1023u;
   const uint32_t sQ = smem_base;
@@ -283,7 +342,9 @@ __device__ __forceinline__ bool varlen_dq_unit(const CUtensorMap& tmQ, const CUt
   const uint32_t sV = sK + D::kKSlots * C::kTileBytes;
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(ptx::smem_u32(&bar_in_full), 1);
+    for (uint64_t* b : {&bar_q_full, &bar_q_empty, &bar_do_full, &bar_do_empty, &bar_st_full, &bar_dpt_full,
+                        &bar_acc_full, &bar_drain})
+      ptx::mbar_init(ptx::smem_u32(b), 1);
     for (int s = 0; s < D::kKSlots; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bar_k_full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&bar_k_empty[s]), 1);
@@ -292,194 +353,243 @@ __device__ __forceinline__ bool varlen_dq_unit(const CUtensorMap& tmQ, const CUt
       ptx::mbar_init(ptx::smem_u32(&bar_v_full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&bar_v_empty[s]), 1);
     }
-    ptx::mbar_init(ptx::smem_u32(&bar_st_full), 1);
-    ptx::mbar_init(ptx::smem_u32(&bar_dpt_full), 1);
-    ptx::mbar_init(ptx::smem_u32(&bar_s_free), 256);
-    ptx::mbar_init(ptx::smem_u32(&bar_dp_free), 256);
-    ptx::mbar_init(ptx::smem_u32(&bar_p_full[0]), 256);
-    ptx::mbar_init(ptx::smem_u32(&bar_p_full[1]), 256);
-    ptx::mbar_init(ptx::smem_u32(&bar_acc_full), 1);
-    ptx::mbar_init(ptx::smem_u32(&bar_drain), 1);
+    for (uint64_t* b : {&bar_s_free, &bar_dp_free, &bar_p_full[0], &bar_p_full[1]})
+      ptx::mbar_init(ptx::smem_u32(b), 256);
     ptx::fence_mbar_init();
   }
-  __syncthreads();
+  role_sync();
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       const uint64_t pol_once = ptx::policy_evict_first();
       const uint64_t pol_shared = ptx::policy_evict_last();
-      const uint32_t in_full = ptx::smem_u32(&bar_in_full);
-      const int token = u.q0 + u.blk * p.tp;
-      ptx::mbar_arrive_expect_tx(in_full, 2 * C::kChunks * 128 * p.G * p.tp);
-      for (int c = 0; c < C::kChunks; ++c) {
-        ptx::tma_load_3d(sQ + c * C::kChunkBytes, &tmQ, in_full, c * 64, kvh * p.G, token, pol_once);
-        ptx::tma_load_3d(sdO + c * C::kChunkBytes, &tmdO, in_full, c * 64, kvh * p.G, token, pol_once);
-      }
-      int issued = 0;    // loads started, in the order K_0, V_0, K_1, V_1, ...
+      int it = 0;        // loads of K (even) and V (odd) so far, in the order K_0, V_0, K_1, ...
+      int units = 0;
+      int issued[2] = {0, 0};    // loads of Q and dO
       bool ok = true;
-      for (int it = 0; it < 2 * n && ok; ++it) {
-        const int j = it >> 1;
+      VarBwdJob job;
+      auto load = [&](int j) {
+        const int g = it >> 1;
         const bool is_v = it & 1;
         const int slots = is_v ? D::kVSlots : D::kKSlots;
-        const int slot = j % slots;
+        const int slot = g % slots;
         uint64_t* empty = is_v ? bar_v_empty : bar_k_empty;
         uint64_t* full = is_v ? bar_v_full : bar_k_full;
-        if (!wait_or_abort(ptx::smem_u32(&empty[slot]), ((j / slots) & 1) ^ 1u, abort_ptr, p.timeout_ns,
-                           kRoleVarDqProducer)) {
-          ok = false;
-          break;
-        }
-        issued = it + 1;
-        if (it == p.drop_load) continue;   // test hook: this tile never arrives
+        if (!wait_or_abort(ptx::smem_u32(&empty[slot]), ((g / slots) & 1) ^ 1u, abort_ptr, p.timeout_ns,
+                           kRoleVarDqProducer))
+          return false;
+        const int me = it++;
+        if (me == p.drop_load) return true;   // test hook: this tile never arrives
         const uint32_t fb = ptx::smem_u32(&full[slot]);
         ptx::mbar_arrive_expect_tx(fb, C::kTileBytes);
         const uint32_t dst = (is_v ? sV : sK) + slot * C::kTileBytes;
         for (int c = 0; c < C::kChunks; ++c)
-          ptx::tma_load_3d(dst + c * C::kChunkBytes, is_v ? &tmV : &tmK, fb, c * 64, u.kv0 + j * C::kBlk, kvh,
+          ptx::tma_load_3d(dst + c * C::kChunkBytes, is_v ? &tmV : &tmK, fb, c * 64, job.u.kv0 + j * C::kBlk, job.kvh,
                            pol_shared);
+        return true;
+      };
+      for (int n = n0; ok; ++n) {
+        ok = wait_or_abort(ptx::smem_u32(&jobs.full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
+                           kRoleVarDqProducer);
+        if (!ok) break;
+        job = jobs.job[n & 1];
+        if (job.kvh < 0) break;
+        ptx::mbar_arrive(ptx::smem_u32(&jobs.empty[n & 1]));
+        const int token = job.u.q0 + job.u.blk * p.tp;
+        const uint32_t bytes = C::kChunks * 128 * p.G * p.tp;
+        for (int x = 0; x < 2 && ok; ++x) {     // Q, then dO
+          uint64_t& empty = x ? bar_do_empty : bar_q_empty;
+          const uint32_t full = ptx::smem_u32(x ? &bar_do_full : &bar_q_full);
+          if (units > 0)
+            ok = wait_or_abort(ptx::smem_u32(&empty), (units - 1) & 1, abort_ptr, p.timeout_ns, kRoleVarDqProducer);
+          if (!ok) break;
+          ptx::mbar_arrive_expect_tx(full, bytes);
+          for (int c = 0; c < C::kChunks; ++c)
+            ptx::tma_load_3d((x ? sdO : sQ) + c * C::kChunkBytes, x ? &tmdO : &tmQ, full, c * 64, job.kvh * p.G, token,
+                             pol_once);
+          issued[x] = units + 1;
+          if (x == 0) ok = load(0);
+        }
+        if (!ok) break;
+        ++units;
+        const int claim_at = max(0, job.u.n - 2);
+        if (claim_at == 0) ptx::mbar_arrive(ptx::smem_u32(&jobs.claim));
+        ok = load(0);
+        for (int j = 1; j < job.u.n && ok; ++j) {
+          if (j == claim_at) ptx::mbar_arrive(ptx::smem_u32(&jobs.claim));
+          ok = load(j) && load(j);
+        }
       }
-      if (ok) fetch_job(p, static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1), next_job);
-      // The issuer's last arrivals on the empty barriers.
-      for (int j = max(0, n - D::kKSlots); j < n && ok; ++j)
-        ok = wait_or_abort(ptx::smem_u32(&bar_k_empty[j % D::kKSlots]), (j / D::kKSlots) & 1, abort_ptr, p.timeout_ns,
-                           kRoleVarDqProducer);
-      for (int j = max(0, n - D::kVSlots); j < n && ok; ++j)
-        ok = wait_or_abort(ptx::smem_u32(&bar_v_empty[j % D::kVSlots]), (j / D::kVSlots) & 1, abort_ptr, p.timeout_ns,
-                           kRoleVarDqProducer);
       if (!ok || *abort_ptr) {
-        drain_wait(in_full, 0, p.timeout_ns);
-        for (int it = 0; it < issued; ++it) {
-          const int j = it >> 1;
-          const bool is_v = it & 1;
+        // Let every copy this thread started land before the CTA exits.
+        if (issued[0] > 0) drain_wait(ptx::smem_u32(&bar_q_full), (issued[0] - 1) & 1, p.timeout_ns);
+        if (issued[1] > 0) drain_wait(ptx::smem_u32(&bar_do_full), (issued[1] - 1) & 1, p.timeout_ns);
+        for (int i = 0; i < it; ++i) {
+          const int g = i >> 1;
+          const bool is_v = i & 1;
           const int slots = is_v ? D::kVSlots : D::kKSlots;
-          const int last_j = ((issued - 1 - (is_v ? 1 : 0)) >> 1);
-          if (j + slots <= last_j || it == p.drop_load) continue;
-          drain_wait(ptx::smem_u32(&(is_v ? bar_v_full : bar_k_full)[j % slots]), (j / slots) & 1, p.timeout_ns);
+          const int last = (it - 1 - (is_v ? 1 : 0)) >> 1;
+          if (g + slots <= last || i == p.drop_load) continue;
+          drain_wait(ptx::smem_u32(&(is_v ? bar_v_full : bar_k_full)[g % slots]), (g / slots) & 1, p.timeout_ns);
         }
       }
     }
     __syncwarp();
   } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer (as in bwd_dq_cta)
-    auto k_tile = [&](int j) { return sK + (j % D::kKSlots) * C::kTileBytes; };
-    auto v_tile = [&](int j) { return sV + (j % D::kVSlots) * C::kTileBytes; };
-    auto issue_s = [&](int j) {
+    // ------------------------------------------------------------ MMA issuer
+    auto k_tile = [&](int g) { return sK + (g % D::kKSlots) * C::kTileBytes; };
+    auto v_tile = [&](int g) { return sV + (g % D::kVSlots) * C::kTileBytes; };
+    // S_g = Q K^T and dP_g = dO V^T, each committed to its own barrier. A unit's
+    // K_0 and V_0 are waited for here; every later K by the elementwise warps
+    // before their s_free, V before their dp_free.
+    auto issue_s = [&](int g, bool last) {
       ptx::tc_fence_after();
-      issue_tile_qk<HD>(tmem_base + D::kColS, sQ, k_tile(j));
+      issue_tile_qk_desc<HD>(tmem_base + D::kColS, sQ, k_tile(g), p.idesc_s);
       ptx::mma_commit_warp(ptx::smem_u32(&bar_st_full));
+      if (last) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty));
     };
-    auto issue_dp = [&](int j) {
+    auto issue_dp = [&](int g, bool last) {
       ptx::tc_fence_after();
-      issue_tile_qk<HD>(tmem_base + D::kColP, sdO, v_tile(j));
-      ptx::mma_commit_warp(ptx::smem_u32(&bar_v_empty[j % D::kVSlots]));
+      issue_tile_qk<HD>(tmem_base + D::kColP, sdO, v_tile(g));
+      ptx::mma_commit_warp(ptx::smem_u32(&bar_v_empty[g % D::kVSlots]));
       ptx::mma_commit_warp(ptx::smem_u32(&bar_dpt_full));
+      if (last) ptx::mma_commit_warp(ptx::smem_u32(&bar_do_empty));
     };
-    bool ok = wait_warp_or_abort(ptx::smem_u32(&bar_in_full), 0, abort_ptr, p.timeout_ns, kRoleVarDqMma);
-    if (ok) ok = wait_warp_or_abort(ptx::smem_u32(&bar_k_full[0]), 0, abort_ptr, p.timeout_ns, kRoleVarDqMma);
-    if (ok) ok = wait_warp_or_abort(ptx::smem_u32(&bar_v_full[0]), 0, abort_ptr, p.timeout_ns, kRoleVarDqMma);
-    if (ok) {
-      issue_s(0);
-      issue_dp(0);
-    }
-    for (int j = 0; j < n && ok; ++j) {
-      if (j + 1 < n) {
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_s_free), j & 1, abort_ptr, p.timeout_ns, kRoleVarDqMma);
-        if (!ok) break;
-        issue_s(j + 1);
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_dp_free), j & 1, abort_ptr, p.timeout_ns, kRoleVarDqMma);
-        if (!ok) break;
-        issue_dp(j + 1);
-      }
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_p_full[j & 1]), (j >> 1) & 1, abort_ptr, p.timeout_ns, kRoleVarDqMma);
+    auto wait = [&](uint64_t* b, int phase) {
+      return wait_warp_or_abort(ptx::smem_u32(b), phase & 1, abort_ptr, p.timeout_ns, kRoleVarDqMma);
+    };
+    bool ok = true;
+    int g = 0, units = 0;        // blocks and units so far
+    for (int n = n0; ok; ++n) {
+      ok = wait(&jobs.full[n & 1], n >> 1);
       if (!ok) break;
-      ptx::tc_fence_after();
-      issue_tile_acc<HD, 32>(tmem_base + D::kColDQ, tmem_base + D::kColDS + 64u * (j & 1), k_tile(j), j > 0);
-      ptx::mma_commit_warp(ptx::smem_u32(&bar_k_empty[j % D::kKSlots]));
+      const int kvh = jobs.job[n & 1].kvh, blocks = jobs.job[n & 1].u.n;
+      if (kvh < 0) break;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&jobs.empty[n & 1]));
+      ok = wait(&bar_q_full, units) && wait(&bar_k_full[g % D::kKSlots], g / D::kKSlots);
+      if (ok && g > 0) ok = wait(&bar_s_free, g - 1);
+      if (!ok) break;
+      issue_s(g, blocks == 1);
+      ok = wait(&bar_do_full, units) && wait(&bar_v_full[g % D::kVSlots], g / D::kVSlots);
+      if (ok && g > 0) ok = wait(&bar_dp_free, g - 1);
+      if (!ok) break;
+      issue_dp(g, blocks == 1);
+      ++units;
+      for (int j = 0; j < blocks; ++j, ++g) {
+        if (j + 1 < blocks) {
+          // S_{j+1} as soon as S_j has been read; dP_{j+1} once dP_j has.
+          ok = wait(&bar_s_free, g);
+          if (!ok) break;
+          issue_s(g + 1, j + 2 == blocks);
+          ok = wait(&bar_dp_free, g);
+          if (!ok) break;
+          issue_dp(g + 1, j + 2 == blocks);
+        }
+        ok = wait(&bar_p_full[g & 1], g >> 1);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        issue_tile_acc<HD, 32>(tmem_base + D::kColDQ, tmem_base + D::kColDS + 64u * (g & 1), k_tile(g), j > 0);
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_k_empty[g % D::kKSlots]));
+      }
+      if (ok) ptx::mma_commit_warp(ptx::smem_u32(&bar_acc_full));
     }
-    if (ok) {
-      ptx::mma_commit_warp(ptx::smem_u32(&bar_acc_full));
-    } else {
+    if (!ok) {
       ptx::mma_commit_warp(ptx::smem_u32(&bar_drain));
       drain_wait(ptx::smem_u32(&bar_drain), 0, p.timeout_ns);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ dS + epilogue
     const int quarter = warp & 3;
     const int half = warp >> 2;
     const int row = quarter * 32 + lane;
     const int tid = half * 128 + row;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    const int x = min(row / p.G, p.tp - 1), hq = row - (row / p.G) * p.G;
-    const int tok0 = u.blk * p.tp;
-    const int live_tok = min(p.tp, u.nq - tok0);
-    // Keys this row sees; rows that do not exist take the last token's.
-    const int limit =
-        p.causal ? max(0, min(u.nkv, tok0 + min(x, live_tok - 1) + 1 + u.nkv - u.nq)) : u.nkv;
-    const long long vrow = (static_cast<long long>(kvh) * p.tile_cap + u.tile0 + u.blk) * 128 + row;
-    const float nl = p.nlse2[vrow];
-    const float nd = p.ndelta[vrow];
     const uint64_t sl2x2 = ptx::f2_pack(p.scale_log2, p.scale_log2);
-    const uint64_t nlx2 = ptx::f2_pack(nl, nl);
-    const uint64_t ndx2 = ptx::f2_pack(nd, nd);
     const uint32_t tS = tmem_base + lane_addr + D::kColS + 64u * half;
     const uint32_t tP = tmem_base + lane_addr + D::kColP + 64u * half;
+    const int xr = (row * p.inv_g) >> 16;    // token of this row within a tile
+    auto wait = [&](uint64_t* b, int phase) {
+      return wait_warp_or_abort(ptx::smem_u32(b), phase & 1, abort_ptr, p.timeout_ns, kRoleVarDqSoftmax);
+    };
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_st_full), j & 1, abort_ptr, p.timeout_ns, kRoleVarDqSoftmax);
+    int g = 0, units = 0;
+    for (int n = n0; ok; ++n) {
+      ok = wait(&jobs.full[n & 1], n >> 1);
       if (!ok) break;
-      ptx::tc_fence_after();
-      uint32_t s[2][32], dp[2][32];
-      ptx::tmem_ld32(tS, s[0]);
-      ptx::tmem_ld32(tS + 32, s[1]);
-      ptx::tmem_ld_wait();
-      ptx::reg_fence32(s[0]);
-      ptx::reg_fence32(s[1]);
-      if (j + 1 < n) {
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_k_full[(j + 1) % D::kKSlots]), ((j + 1) / D::kKSlots) & 1,
-                                abort_ptr, p.timeout_ns, kRoleVarDqSoftmax);
+      const VarBwdJob& job = jobs.job[n & 1];
+      if (job.kvh < 0) break;
+      const int blocks = job.u.n, nkv = job.u.nkv;
+      // Keys this row sees; rows that do not exist take the last token's.
+      int limit = nkv;
+      {
+        const int tok0 = job.u.blk * p.tp;
+        const int last = min(p.tp, job.u.nq - tok0) - 1;
+        if (p.causal) limit = max(0, min(nkv, tok0 + min(xr, last) + 1 + nkv - job.u.nq));
+      }
+      const long long vrow = (static_cast<long long>(job.kvh) * p.tile_cap + job.u.tile0 + job.u.blk) * 128 + row;
+      const float nl = p.nlse2[vrow];
+      const float nd = p.ndelta[vrow];
+      const uint64_t nlx2 = ptx::f2_pack(nl, nl);
+      const uint64_t ndx2 = ptx::f2_pack(nd, nd);
+      for (int j = 0; j < blocks; ++j, ++g) {
+        ok = wait(&bar_st_full, g);
         if (!ok) break;
-      }
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(ptx::smem_u32(&bar_s_free));
-
-      const int have = u.nkv - j * C::kBlk;    // keys of the sequence in this block
-      if (have < C::kBlk) {
-        clear_rows<HD>(smem_raw + (sK - raw) + (j % D::kKSlots) * C::kTileBytes, max(have, 0), C::kBlk, tid);
-        ptx::fence_proxy_async_smem();
-      }
-      const int valid = limit - j * C::kBlk - 64 * half;   // keys of this warp's 64 that this row sees
-      const bool masked = !__all_sync(0xffffffffu, valid >= 64);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          float x0, x1;
-          ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])),
-                                     sl2x2, nlx2),
-                         x0, x1);
-          s[c][2 * k] = __float_as_uint(ptx::ex2_approx(x0));
-          s[c][2 * k + 1] = __float_as_uint(ptx::ex2_approx(x1));
+        ptx::tc_fence_after();
+        const int valid = limit - j * C::kBlk - 64 * half;   // keys of this warp's 64 that this row sees
+        if (!__all_sync(0xffffffffu, valid >= 64)) mask_columns(tS, 0, valid, __float_as_uint(-INFINITY));
+        uint32_t s[2][32], dp[2][32];
+        ptx::tmem_ld32(tS, s[0]);
+        ptx::tmem_ld32(tS + 32, s[1]);
+        ptx::tmem_ld_wait();
+        ptx::reg_fence32(s[0]);
+        ptx::reg_fence32(s[1]);
+        if (j + 1 < blocks) {
+          // K_{j+1} in place before the hand-off that lets S_{j+1} be issued.
+          ok = wait(&bar_k_full[(g + 1) % D::kKSlots], (g + 1) / D::kKSlots);
+          if (!ok) break;
         }
-      }
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_dpt_full), j & 1, abort_ptr, p.timeout_ns, kRoleVarDqSoftmax);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      ptx::tmem_ld32(tP, dp[0]);
-      ptx::tmem_ld32(tP + 32, dp[1]);
-      ptx::tmem_ld_wait();
-      ptx::reg_fence32(dp[0]);
-      ptx::reg_fence32(dp[1]);
-      if (j + 1 < n) {
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_v_full[(j + 1) % D::kVSlots]), ((j + 1) / D::kVSlots) & 1,
-                                abort_ptr, p.timeout_ns, kRoleVarDqSoftmax);
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_u32(&bar_s_free));
+
+        const int have = nkv - j * C::kBlk;    // keys of the sequence in this block
+        if (have < C::kBlk) {
+          clear_rows<HD>(smem_raw + (sK - raw) + (g % D::kKSlots) * C::kTileBytes, max(have, 0), C::kBlk, tid);
+          ptx::fence_proxy_async_smem();
+        }
+        // P (float32, kept in s) while dP_j is still on the tensor core.
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float x0, x1;
+            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])),
+                                       sl2x2, nlx2),
+                           x0, x1);
+            s[c][2 * k] = __float_as_uint(ptx::ex2_approx(x0));
+            s[c][2 * k + 1] = __float_as_uint(ptx::ex2_approx(x1));
+          }
+        }
+        ok = wait(&bar_dpt_full, g);
         if (!ok) break;
-      }
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(ptx::smem_u32(&bar_dp_free));
-      uint32_t pds[32];
-      auto ds_pass = [&](auto mask) {
+        ptx::tc_fence_after();
+        // dP of keys behind the end may be anything.
+        if (have < C::kBlk) mask_columns(tP, 0, have - 64 * half, 0u);
+        ptx::tmem_ld32(tP, dp[0]);
+        ptx::tmem_ld32(tP + 32, dp[1]);
+        ptx::tmem_ld_wait();
+        ptx::reg_fence32(dp[0]);
+        ptx::reg_fence32(dp[1]);
+        if (j + 1 < blocks) {
+          // V_{j+1} in place before the hand-off that lets dP_{j+1} be issued.
+          ok = wait(&bar_v_full[(g + 1) % D::kVSlots], (g + 1) / D::kVSlots);
+          if (!ok) break;
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_u32(&bar_dp_free));
+        uint32_t pds[32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -489,71 +599,51 @@ __device__ __forceinline__ bool varlen_dq_unit(const CUtensorMap& tmQ, const CUt
             float d0, d1;
             ptx::f2_unpack(
                 ptx::f2_mul(ptx::f2_pack(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), t), d0, d1);
-            if (decltype(mask)::value) {
-              if (32 * c + 2 * k >= valid) d0 = 0.f;
-              if (32 * c + 2 * k + 1 >= valid) d1 = 0.f;
-            }
             pds[16 * c + k] = ptx::pack_bf16x2(d0, d1);
           }
         }
-      };
-      if (masked) ds_pass(std::true_type{});
-      else ds_pass(std::false_type{});
-      ptx::tmem_st32(tmem_base + lane_addr + D::kColDS + 64u * (j & 1) + 32u * half, pds);
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(ptx::smem_u32(&bar_p_full[j & 1]));
-    }
-    if (ok) ok = wait_warp_or_abort(ptx::smem_u32(&bar_acc_full), 0, abort_ptr, p.timeout_ns, kRoleVarDqSoftmax);
-    if (ok) {
+        ptx::tmem_st32(tmem_base + lane_addr + D::kColDS + 64u * (g & 1) + 32u * half, pds);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_u32(&bar_p_full[g & 1]));
+      }
+      if (!ok) break;
+      const int tok0 = job.u.blk * p.tp;
+      const bool live = row < p.G * p.tp && xr < job.u.nq - tok0;
+      __nv_bfloat16* dst = p.dQ + (static_cast<long long>(job.u.q0) + tok0 + xr) * p.dq_st +
+                           (job.kvh * p.G + row - xr * p.G) * p.dq_sh + half * (HD / 2);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&jobs.empty[n & 1]));
+      ok = wait(&bar_acc_full, units++);
+      if (!ok) break;
       ptx::tc_fence_after();
-      const bool live = row < p.G * p.tp && x < live_tok;
-      __nv_bfloat16* dst = p.dQ + (static_cast<long long>(u.q0) + tok0 + x) * p.dq_st + (kvh * p.G + hq) * p.dq_sh +
-                           half * (HD / 2);
-#pragma unroll
-      for (int c = 0; c < HD / 64; ++c)
-        store_row32(tmem_base + lane_addr + D::kColDQ + half * (HD / 2) + 32 * c, p.scale, dst + 32 * c, live);
+      store_half_row<HD>(tmem_base + lane_addr + D::kColDQ + half * (HD / 2), p.scale, dst, live);
     }
   }
-
   ptx::tc_fence_before();
-  __syncthreads();
+  role_sync();
   ptx::tc_fence_after();
-  if (*abort_ptr) return false;
-  if (threadIdx.x == 0) {
-    ptx::mbar_inval(ptx::smem_u32(&bar_in_full));
-    for (int s = 0; s < D::kKSlots; ++s) {
-      ptx::mbar_inval(ptx::smem_u32(&bar_k_full[s]));
-      ptx::mbar_inval(ptx::smem_u32(&bar_k_empty[s]));
-    }
-    for (int s = 0; s < D::kVSlots; ++s) {
-      ptx::mbar_inval(ptx::smem_u32(&bar_v_full[s]));
-      ptx::mbar_inval(ptx::smem_u32(&bar_v_empty[s]));
-    }
-    for (uint64_t* b : {&bar_st_full, &bar_dpt_full, &bar_s_free, &bar_dp_free, &bar_p_full[0], &bar_p_full[1],
-                        &bar_acc_full, &bar_drain})
-      ptx::mbar_inval(ptx::smem_u32(b));
-  }
-  return true;
 }
 
-// A unit of the key-block role.
+// The key-block role: units from job 0 on, up to the first job of the other
+// role, or none (not released). Returns the number of jobs taken, or -1 when a
+// role gave up, the same in every thread.
 template <int HD>
-__device__ __forceinline__ bool varlen_dkdv_unit(const CUtensorMap& tmQ, const CUtensorMap& tmK,
-                                                 const CUtensorMap& tmV, const CUtensorMap& tmdO,
-                                                 const VarBwdParams& p, const VarBwdUnit u, const int kvh,
-                                                 const uint32_t tmem_base, volatile int* abort_ptr,
-                                                 VarBwdJob* next_job) {
+__device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                                const CUtensorMap& tmV, const CUtensorMap& tmdO,
+                                                const VarBwdParams& p, VarBwdJobs& jobs, const uint32_t tmem_base,
+                                                volatile int* abort_ptr) {
   using C = BwdCfg<HD>;
   constexpr uint32_t kColDV = 0;
   constexpr uint32_t kColDK = HD;
   constexpr uint32_t kColR = 2 * HD;    // R0 = kColR, R1 = kColR + 128
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_kv_full;
-  __shared__ __align__(8) uint64_t bar_q_full[C::kStages];
-  __shared__ __align__(8) uint64_t bar_q_empty[C::kStages];
-  __shared__ __align__(8) uint64_t bar_do_full[C::kStages];
-  __shared__ __align__(8) uint64_t bar_do_empty[C::kStages];
+  __shared__ __align__(8) uint64_t bar_k_full, bar_k_empty;     // K of the unit
+  __shared__ __align__(8) uint64_t bar_v_full, bar_v_empty;     // V of the unit
+  __shared__ __align__(8) uint64_t bar_q_full[C::kStages];      // Q_i and -LSE*log2e landed
+  __shared__ __align__(8) uint64_t bar_q_empty[C::kStages];     // dK(i) done with Q_i
+  __shared__ __align__(8) uint64_t bar_do_full[C::kStages];     // dO_i and -D landed
+  __shared__ __align__(8) uint64_t bar_do_empty[C::kStages];    // dV(i) done with dO_i
   __shared__ __align__(8) uint64_t bar_st_full;
   __shared__ __align__(8) uint64_t bar_dpt_full;
   __shared__ __align__(8) uint64_t bar_dp_free;
@@ -561,13 +651,11 @@ __device__ __forceinline__ bool varlen_dkdv_unit(const CUtensorMap& tmQ, const C
   __shared__ __align__(8) uint64_t bar_pt_stored;
   __shared__ __align__(8) uint64_t bar_acc_full;
   __shared__ __align__(8) uint64_t bar_drain;
+  __shared__ int taken;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int n = u.n;
   const int box_rows = p.G * p.tp;
-  const int key0 = u.blk * C::kBlk;                                     // first key, within the sequence
-  const int tile_first = (u.nq + p.tp - 1) / p.tp - n;                  // first query tile to visit
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t smem_base = (raw + 1023u) & ~1023u;
   const uint32_t sK = smem_base;
@@ -577,89 +665,106 @@ __device__ __forceinline__ bool varlen_dkdv_unit(const CUtensorMap& tmQ, const C
   const float* vec = reinterpret_cast<const float*>(smem_raw + (sVec - raw));
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(ptx::smem_u32(&bar_kv_full), 1);
-    for (int s = 0; s < C::kStages; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&bar_q_full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bar_q_empty[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bar_do_full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bar_do_empty[s]), 1);
-    }
-    ptx::mbar_init(ptx::smem_u32(&bar_st_full), 1);
-    ptx::mbar_init(ptx::smem_u32(&bar_dpt_full), 1);
-    ptx::mbar_init(ptx::smem_u32(&bar_dp_free), 256);
-    ptx::mbar_init(ptx::smem_u32(&bar_p_full), 256);
-    ptx::mbar_init(ptx::smem_u32(&bar_pt_stored), 256);
-    ptx::mbar_init(ptx::smem_u32(&bar_acc_full), 1);
-    ptx::mbar_init(ptx::smem_u32(&bar_drain), 1);
+    for (uint64_t* b : {&bar_k_full, &bar_k_empty, &bar_v_full, &bar_v_empty, &bar_st_full, &bar_dpt_full,
+                        &bar_acc_full, &bar_drain})
+      ptx::mbar_init(ptx::smem_u32(b), 1);
+    for (int s = 0; s < C::kStages; ++s)
+      for (uint64_t* b : {&bar_q_full[s], &bar_q_empty[s], &bar_do_full[s], &bar_do_empty[s]})
+        ptx::mbar_init(ptx::smem_u32(b), 1);
+    for (uint64_t* b : {&bar_dp_free, &bar_p_full, &bar_pt_stored}) ptx::mbar_init(ptx::smem_u32(b), 256);
     ptx::fence_mbar_init();
   }
-  // Rows that no load of this unit writes are zero (the memory may hold
-  // another role's tiles).
+  // Rows of the ring that no load writes are zero.
   if (box_rows < C::kBlk && warp < 8) {
     for (int s = 0; s < 2 * C::kStages; ++s)
       clear_rows<HD>(smem_raw + (sRing - raw) + s * C::kTileBytes, box_rows, C::kBlk, threadIdx.x);
     ptx::fence_proxy_async_smem();
   }
-  __syncthreads();
+  role_sync();
 
+  bool ok = true;
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       const uint64_t pol_shared = ptx::policy_evict_last();
-      const uint32_t kv_full = ptx::smem_u32(&bar_kv_full);
-      ptx::mbar_arrive_expect_tx(kv_full, C::kPairBytes);
-      for (int c = 0; c < C::kChunks; ++c) {
-        ptx::tma_load_3d(sK + c * C::kChunkBytes, &tmK, kv_full, c * 64, u.kv0 + key0, kvh, pol_shared);
-        ptx::tma_load_3d(sV + c * C::kChunkBytes, &tmV, kv_full, c * 64, u.kv0 + key0, kvh, pol_shared);
-      }
-      int issued_q = 0, issued_do = 0;
-      bool ok = true;
       const uint32_t bytes = C::kChunks * 128 * box_rows + C::kBlk * 4;
-      for (int i = 0; i < n && ok; ++i) {
-        const int slot = i % C::kStages;
-        const uint32_t par = ((i / C::kStages) & 1) ^ 1u;
-        const uint32_t dst = sRing + slot * C::kPairBytes;
-        const int token = u.q0 + (tile_first + i) * p.tp;
-        const long long voff = (static_cast<long long>(kvh) * p.tile_cap + u.tile0 + tile_first + i) * C::kBlk;
-        if (!wait_or_abort(ptx::smem_u32(&bar_q_empty[slot]), par, abort_ptr, p.timeout_ns, kRoleVarDkvProducer)) {
-          ok = false;
-          break;
-        }
-        issued_q = i + 1;
-        if (i != p.drop_load) {    // test hook: this step's tiles never arrive
-          const uint32_t full = ptx::smem_u32(&bar_q_full[slot]);
-          ptx::mbar_arrive_expect_tx(full, bytes);
-          for (int c = 0; c < C::kChunks; ++c)
-            ptx::tma_load_3d(dst + c * C::kChunkBytes, &tmQ, full, c * 64, kvh * p.G, token, pol_shared);
-          ptx::bulk_load_1d(sVec + slot * C::kVecBytes, p.nlse2 + voff, C::kBlk * 4, full, pol_shared);
-        }
-        if (!wait_or_abort(ptx::smem_u32(&bar_do_empty[slot]), par, abort_ptr, p.timeout_ns, kRoleVarDkvProducer)) {
-          ok = false;
-          break;
-        }
-        issued_do = i + 1;
-        if (i != p.drop_load) {
-          const uint32_t full = ptx::smem_u32(&bar_do_full[slot]);
-          ptx::mbar_arrive_expect_tx(full, bytes);
-          for (int c = 0; c < C::kChunks; ++c)
-            ptx::tma_load_3d(dst + C::kTileBytes + c * C::kChunkBytes, &tmdO, full, c * 64, kvh * p.G, token,
-                             pol_shared);
-          ptx::bulk_load_1d(sVec + slot * C::kVecBytes + C::kBlk * 4, p.ndelta + voff, C::kBlk * 4, full,
-                            pol_shared);
-        }
-      }
-      if (ok) fetch_job(p, static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1), next_job);
-      // K and V (nobody else waits for V), and the issuer's last arrivals on the empty barriers.
-      if (ok) ok = wait_or_abort(kv_full, 0, abort_ptr, p.timeout_ns, kRoleVarDkvProducer);
-      for (int i = max(0, n - C::kStages); i < n && ok; ++i) {
-        ok = wait_or_abort(ptx::smem_u32(&bar_q_empty[i % C::kStages]), (i / C::kStages) & 1, abort_ptr, p.timeout_ns,
+      int g = 0, units = 0, n = 0;          // query tiles, units, jobs so far
+      int issued_k = 0, issued_q = 0, issued_do = 0;
+      for (; ok; ++n) {
+        ok = wait_or_abort(ptx::smem_u32(&jobs.full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
                            kRoleVarDkvProducer);
-        if (ok)
-          ok = wait_or_abort(ptx::smem_u32(&bar_do_empty[i % C::kStages]), (i / C::kStages) & 1, abort_ptr,
-                             p.timeout_ns, kRoleVarDkvProducer);
+        if (!ok) break;
+        const VarBwdJob job = jobs.job[n & 1];
+        if (job.kvh < 0 || !job.u.dkdv) break;
+        ptx::mbar_arrive(ptx::smem_u32(&jobs.empty[n & 1]));
+        const int tile_first = (job.u.nq + p.tp - 1) / p.tp - job.u.n;   // first query tile to visit
+        const int claim_at = max(0, job.u.n - 2);
+        if (job.u.n == 0) ptx::mbar_arrive(ptx::smem_u32(&jobs.claim));
+        for (int i = 0; i < job.u.n && ok; ++i, ++g) {
+          if (i == claim_at) ptx::mbar_arrive(ptx::smem_u32(&jobs.claim));
+          const int slot = g % C::kStages;
+          const uint32_t par = ((g / C::kStages) & 1) ^ 1u;
+          const uint32_t dst = sRing + slot * C::kPairBytes;
+          const int token = job.u.q0 + (tile_first + i) * p.tp;
+          const long long voff =
+              (static_cast<long long>(job.kvh) * p.tile_cap + job.u.tile0 + tile_first + i) * C::kBlk;
+          if (i == 0) {
+            if (units > 0)
+              ok = wait_or_abort(ptx::smem_u32(&bar_k_empty), (units - 1) & 1, abort_ptr, p.timeout_ns,
+                                 kRoleVarDkvProducer);
+            if (!ok) break;
+            const uint32_t full = ptx::smem_u32(&bar_k_full);
+            ptx::mbar_arrive_expect_tx(full, C::kTileBytes);
+            for (int c = 0; c < C::kChunks; ++c)
+              ptx::tma_load_3d(sK + c * C::kChunkBytes, &tmK, full, c * 64, job.u.kv0 + job.u.blk * C::kBlk, job.kvh,
+                               pol_shared);
+            issued_k = units + 1;
+          }
+          if (!wait_or_abort(ptx::smem_u32(&bar_q_empty[slot]), par, abort_ptr, p.timeout_ns, kRoleVarDkvProducer)) {
+            ok = false;
+            break;
+          }
+          issued_q = g + 1;
+          if (g != p.drop_load) {    // test hook: this step's tiles never arrive
+            const uint32_t full = ptx::smem_u32(&bar_q_full[slot]);
+            ptx::mbar_arrive_expect_tx(full, bytes);
+            for (int c = 0; c < C::kChunks; ++c)
+              ptx::tma_load_3d(dst + c * C::kChunkBytes, &tmQ, full, c * 64, job.kvh * p.G, token, pol_shared);
+            ptx::bulk_load_1d(sVec + slot * C::kVecBytes, p.nlse2 + voff, C::kBlk * 4, full, pol_shared);
+          }
+          if (i == 0) {
+            if (units > 0)
+              ok = wait_or_abort(ptx::smem_u32(&bar_v_empty), (units - 1) & 1, abort_ptr, p.timeout_ns,
+                                 kRoleVarDkvProducer);
+            if (!ok) break;
+            const uint32_t full = ptx::smem_u32(&bar_v_full);
+            ptx::mbar_arrive_expect_tx(full, C::kTileBytes);
+            for (int c = 0; c < C::kChunks; ++c)
+              ptx::tma_load_3d(sV + c * C::kChunkBytes, &tmV, full, c * 64, job.u.kv0 + job.u.blk * C::kBlk, job.kvh,
+                               pol_shared);
+            ++units;
+          }
+          if (!wait_or_abort(ptx::smem_u32(&bar_do_empty[slot]), par, abort_ptr, p.timeout_ns, kRoleVarDkvProducer)) {
+            ok = false;
+            break;
+          }
+          issued_do = g + 1;
+          if (g != p.drop_load) {
+            const uint32_t full = ptx::smem_u32(&bar_do_full[slot]);
+            ptx::mbar_arrive_expect_tx(full, bytes);
+            for (int c = 0; c < C::kChunks; ++c)
+              ptx::tma_load_3d(dst + C::kTileBytes + c * C::kChunkBytes, &tmdO, full, c * 64, job.kvh * p.G, token,
+                               pol_shared);
+            ptx::bulk_load_1d(sVec + slot * C::kVecBytes + C::kBlk * 4, p.ndelta + voff, C::kBlk * 4, full,
+                              pol_shared);
+          }
+        }
       }
+      taken = n;
       if (!ok || *abort_ptr) {
-        drain_wait(kv_full, 0, p.timeout_ns);
+        // Let every copy this thread started land before the CTA exits.
+        if (issued_k > 0) drain_wait(ptx::smem_u32(&bar_k_full), (issued_k - 1) & 1, p.timeout_ns);
+        if (units > 0) drain_wait(ptx::smem_u32(&bar_v_full), (units - 1) & 1, p.timeout_ns);
         for (int i = issued_q > C::kStages ? issued_q - C::kStages : 0; i < issued_q; ++i)
           if (i != p.drop_load)
             drain_wait(ptx::smem_u32(&bar_q_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
@@ -671,84 +776,95 @@ __device__ __forceinline__ bool varlen_dkdv_unit(const CUtensorMap& tmQ, const C
     __syncwarp();
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer (as in bwd_dkdv_cta)
-    auto region = [&](int i) { return tmem_base + kColR + 128u * static_cast<uint32_t>(i & 1); };
-    auto q_tile = [&](int i) { return sRing + (i % C::kStages) * C::kPairBytes; };
-    bool ok = n > 0;
-    if (ok) ok = wait_warp_or_abort(ptx::smem_u32(&bar_kv_full), 0, abort_ptr, p.timeout_ns, kRoleVarDkvMma);
-    if (ok) ok = wait_warp_or_abort(ptx::smem_u32(&bar_q_full[0]), 0, abort_ptr, p.timeout_ns, kRoleVarDkvMma);
-    if (ok) {
+    auto region = [&](int g) { return tmem_base + kColR + 128u * static_cast<uint32_t>(g & 1); };
+    auto q_tile = [&](int g) { return sRing + (g % C::kStages) * C::kPairBytes; };
+    auto wait = [&](uint64_t* b, int phase) {
+      return wait_warp_or_abort(ptx::smem_u32(b), phase & 1, abort_ptr, p.timeout_ns, kRoleVarDkvMma);
+    };
+    // S_g^T = K Q^T; `last`: the unit's last use of K.
+    auto issue_s = [&](int g, bool last) {
       ptx::tc_fence_after();
-      issue_tile_qk<HD>(region(0), sK, q_tile(0));                   // S_0^T = K Q_0^T
+      issue_tile_qk_desc<HD>(region(g), sK, q_tile(g), p.idesc_s);
       ptx::mma_commit_warp(ptx::smem_u32(&bar_st_full));
-    }
-    if (ok) ok = wait_warp_or_abort(ptx::smem_u32(&bar_do_full[0]), 0, abort_ptr, p.timeout_ns, kRoleVarDkvMma);
-    if (ok) {
+      if (last) ptx::mma_commit_warp(ptx::smem_u32(&bar_k_empty));
+    };
+    // dP_g^T = V dO^T, then, once P^T is in place, dV += P^T dO.
+    auto issue_dp_dv = [&](int g, bool first, bool last) {
       ptx::tc_fence_after();
-      issue_tile_qk<HD>(region(1), sV, q_tile(0) + C::kTileBytes);   // dP_0^T = V dO_0^T
+      issue_tile_qk<HD>(region(g + 1), sV, q_tile(g) + C::kTileBytes);
       ptx::mma_commit_warp(ptx::smem_u32(&bar_dpt_full));
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_pt_stored), 0, abort_ptr, p.timeout_ns, kRoleVarDkvMma);
-      if (ok) {
-        ptx::tc_fence_after();
-        issue_tile_acc<HD, 64>(tmem_base + kColDV, region(0), q_tile(0) + C::kTileBytes, false);   // dV += P^T dO_0
-        ptx::mma_commit_warp(ptx::smem_u32(&bar_do_empty[0]));
-      }
-    }
-    for (int i = 0; i < n && ok; ++i) {
-      bool s_issued = false;
-      const int s1 = (i + 1) % C::kStages;
-      const uint32_t in_par = ((i + 1) / C::kStages) & 1;
-      const uint32_t q_full1 = ptx::smem_u32(&bar_q_full[s1]);
-      if (i + 1 < n) {
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_dp_free), i & 1, abort_ptr, p.timeout_ns, kRoleVarDkvMma);
-        if (!ok) break;
-        const uint64_t t0 = ptx::globaltimer_ns();
-        while (true) {
-          if (__all_sync(0xffffffffu, ptx::mbar_test_wait(q_full1, in_par))) {
-            ptx::tc_fence_after();
-            issue_tile_qk<HD>(region(i + 1), sK, q_tile(i + 1));      // S_{i+1}^T
-            ptx::mma_commit_warp(ptx::smem_u32(&bar_st_full));
-            s_issued = true;
-            break;
-          }
-          if (__all_sync(0xffffffffu, ptx::mbar_test_wait(ptx::smem_u32(&bar_p_full), i & 1))) break;
-          // Out of time or aborting: the bounded wait below reports it.
-          if (__any_sync(0xffffffffu, *abort_ptr != 0) || ptx::globaltimer_ns() - t0 > p.timeout_ns) break;
-          __nanosleep(32);
-        }
-      }
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_p_full), i & 1, abort_ptr, p.timeout_ns, kRoleVarDkvMma);
-      if (!ok) break;
+      if (last) ptx::mma_commit_warp(ptx::smem_u32(&bar_v_empty));
+      if (!wait(&bar_pt_stored, g)) return false;
       ptx::tc_fence_after();
-      issue_tile_acc<HD, 64>(tmem_base + kColDK, region(i) + 32, q_tile(i), i > 0);             // dK += dS^T Q_i
-      ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[i % C::kStages]));
-      if (i + 1 < n) {
-        if (!s_issued) {
-          ok = wait_warp_or_abort(q_full1, in_par, abort_ptr, p.timeout_ns, kRoleVarDkvMma);
+      issue_tile_acc<HD, 64>(tmem_base + kColDV, region(g), q_tile(g) + C::kTileBytes, !first);
+      ptx::mma_commit_warp(ptx::smem_u32(&bar_do_empty[g % C::kStages]));
+      return true;
+    };
+    int g = 0, units = 0;
+    for (int n = 0; ok; ++n) {
+      ok = wait(&jobs.full[n & 1], n >> 1);
+      if (!ok) break;
+      const int kvh = jobs.job[n & 1].kvh, steps = jobs.job[n & 1].u.n, mine = jobs.job[n & 1].u.dkdv;
+      if (kvh < 0 || !mine) break;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&jobs.empty[n & 1]));
+      if (steps == 0) continue;     // no query rows: the elementwise warps store zeros
+      ok = wait(&bar_k_full, units) && wait(&bar_q_full[g % C::kStages], g / C::kStages);
+      if (!ok) break;
+      issue_s(g, steps == 1);
+      ok = wait(&bar_v_full, units) && wait(&bar_do_full[g % C::kStages], g / C::kStages);
+      if (!ok) break;
+      ++units;
+      ok = issue_dp_dv(g, true, steps == 1);
+      for (int i = 0; i < steps && ok; ++i, ++g) {
+        // S_{i+1}^T goes in as soon as its region is free (dp_free(i)) and
+        // Q_{i+1} has landed, if that happens before p_full(i); otherwise
+        // after dK(i). A late Q must not hold back dK(i), whose commit frees
+        // the ring slot the next copy needs.
+        bool s_issued = false;
+        const bool more = i + 1 < steps, last = i + 2 == steps;
+        const int s1 = (g + 1) % C::kStages;
+        const int in_phase = (g + 1) / C::kStages;
+        if (more) {
+          ok = wait(&bar_dp_free, g);
           if (!ok) break;
-          ptx::tc_fence_after();
-          issue_tile_qk<HD>(region(i + 1), sK, q_tile(i + 1));        // S_{i+1}^T
-          ptx::mma_commit_warp(ptx::smem_u32(&bar_st_full));
+          const uint64_t t0 = ptx::globaltimer_ns();
+          while (true) {
+            if (__all_sync(0xffffffffu, ptx::mbar_test_wait(ptx::smem_u32(&bar_q_full[s1]), in_phase & 1))) {
+              issue_s(g + 1, last);
+              s_issued = true;
+              break;
+            }
+            if (__all_sync(0xffffffffu, ptx::mbar_test_wait(ptx::smem_u32(&bar_p_full), g & 1))) break;
+            // Out of time or aborting: the bounded wait below reports it.
+            if (__any_sync(0xffffffffu, *abort_ptr != 0) || ptx::globaltimer_ns() - t0 > p.timeout_ns) break;
+            __nanosleep(32);
+          }
         }
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_do_full[s1]), in_par, abort_ptr, p.timeout_ns, kRoleVarDkvMma);
+        ok = wait(&bar_p_full, g);
         if (!ok) break;
         ptx::tc_fence_after();
-        issue_tile_qk<HD>(region(i), sV, q_tile(i + 1) + C::kTileBytes);   // dP_{i+1}^T
-        ptx::mma_commit_warp(ptx::smem_u32(&bar_dpt_full));
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_pt_stored), (i + 1) & 1, abort_ptr, p.timeout_ns, kRoleVarDkvMma);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        issue_tile_acc<HD, 64>(tmem_base + kColDV, region(i + 1), q_tile(i + 1) + C::kTileBytes, true);   // dV
-        ptx::mma_commit_warp(ptx::smem_u32(&bar_do_empty[(i + 1) % C::kStages]));
+        issue_tile_acc<HD, 64>(tmem_base + kColDK, region(g) + 32, q_tile(g), i > 0);             // dK += dS^T Q_i
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[g % C::kStages]));
+        if (more) {
+          if (!s_issued) {
+            ok = wait(&bar_q_full[s1], in_phase);
+            if (!ok) break;
+            issue_s(g + 1, last);
+          }
+          ok = wait(&bar_do_full[s1], in_phase);
+          if (!ok) break;
+          ok = issue_dp_dv(g + 1, false, last);
+        }
       }
+      if (ok) ptx::mma_commit_warp(ptx::smem_u32(&bar_acc_full));
     }
-    if (ok) {
-      ptx::mma_commit_warp(ptx::smem_u32(&bar_acc_full));
-    } else if (n > 0) {
+    if (!ok) {
       ptx::mma_commit_warp(ptx::smem_u32(&bar_drain));
       drain_wait(ptx::smem_u32(&bar_drain), 0, p.timeout_ns);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ P, dS + epilogue
     const int quarter = warp & 3;
     const int half = warp >> 2;
@@ -756,32 +872,43 @@ __device__ __forceinline__ bool varlen_dkdv_unit(const CUtensorMap& tmQ, const C
     const int tid = half * 128 + row;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint64_t sl2x2 = ptx::f2_pack(p.scale_log2, p.scale_log2);
-    const int see0 = key0 + row - (u.nkv - u.nq);    // first token of the sequence that sees this key (causal)
-    bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const int tok0 = (tile_first + i) * p.tp;
-      const int live_tok = min(p.tp, u.nq - tok0);
-      const bool ragged = live_tok < p.tp;
-      // Columns x * G + g of this warp's 64 that count for this key: [from, to).
-      const int from = (p.causal ? max(0, min(see0 - tok0, p.tp)) * p.G : 0) - 64 * half;
-      const int to = (ragged ? live_tok * p.G : C::kBlk) - 64 * half;
-      const bool masked = !__all_sync(0xffffffffu, from <= 0 && to >= 64);
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_st_full), i & 1, abort_ptr, p.timeout_ns, kRoleVarDkvSoftmax);
+    auto wait = [&](uint64_t* b, int phase) {
+      return wait_warp_or_abort(ptx::smem_u32(b), phase & 1, abort_ptr, p.timeout_ns, kRoleVarDkvSoftmax);
+    };
+    int g = 0, units = 0;
+    for (int n = 0; ok; ++n) {
+      ok = wait(&jobs.full[n & 1], n >> 1);
       if (!ok) break;
-      ptx::tc_fence_after();
-      const uint32_t tS = tmem_base + lane_addr + kColR + 128u * (i & 1) + 64u * half;
-      const uint32_t tP = tmem_base + lane_addr + kColR + 128u * ((i + 1) & 1) + 64u * half;
-      uint32_t s[2][32], dp[2][32];
-      ptx::tmem_ld32(tS, s[0]);
-      ptx::tmem_ld32(tS + 32, s[1]);
-      ptx::tmem_ld_wait();
-      ptx::reg_fence32(s[0]);
-      ptx::reg_fence32(s[1]);
-      const float4* vl = reinterpret_cast<const float4*>(vec + (i % C::kStages) * (C::kVecBytes / 4) + 64 * half);
-      const float4* vd = vl + 32;    // + 128 floats
-      {
-        uint32_t pp[32];
-        auto p_pass = [&](auto mask) {
+      const VarBwdJob& job = jobs.job[n & 1];
+      if (job.kvh < 0 || !job.u.dkdv) break;
+      const int steps = job.u.n, nq = job.u.nq;
+      int tok0 = ((nq + p.tp - 1) / p.tp - steps) * p.tp;          // first token of step i's tile
+      // First token of the sequence that sees this key (causal).
+      const int see0 = p.causal ? job.u.blk * C::kBlk + row - (job.u.nkv - nq) : 0;
+      for (int i = 0; i < steps; ++i, ++g, tok0 += p.tp) {
+        const bool ragged = nq - tok0 < p.tp;
+        // Columns x * G + h of this warp's 64 that count for this key: [from, to).
+        const int from = max(0, min(see0 - tok0, p.tp)) * p.G - 64 * half;
+        const int to = (ragged ? (nq - tok0) * p.G : C::kBlk) - 64 * half;
+        // P^T as soon as S^T(i) is complete (it overlaps the tensor core's dK/dV
+        // of the previous block and dP^T of this one), then dS^T once dP^T(i) is.
+        ok = wait(&bar_st_full, g);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t tS = tmem_base + lane_addr + kColR + 128u * (g & 1) + 64u * half;
+        const uint32_t tP = tmem_base + lane_addr + kColR + 128u * ((g + 1) & 1) + 64u * half;
+        if (!__all_sync(0xffffffffu, from <= 0 && to >= 64)) mask_columns(tS, from, to, __float_as_uint(-INFINITY));
+        uint32_t s[2][32], dp[2][32];
+        ptx::tmem_ld32(tS, s[0]);
+        ptx::tmem_ld32(tS + 32, s[1]);
+        ptx::tmem_ld_wait();
+        ptx::reg_fence32(s[0]);
+        ptx::reg_fence32(s[1]);
+        // -LSE*log2e and -D of this warp's 64 query columns (broadcast reads).
+        const float4* vl = reinterpret_cast<const float4*>(vec + (g % C::kStages) * (C::kVecBytes / 4) + 64 * half);
+        const float4* vd = vl + 32;    // + 128 floats
+        {
+          uint32_t pp[32];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -795,49 +922,42 @@ __device__ __forceinline__ bool varlen_dkdv_unit(const CUtensorMap& tmQ, const C
                 ptx::f2_unpack(
                     ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), sl2x2, nl2), x0,
                     x1);
-                float p0 = ptx::ex2_approx(x0);
-                float p1 = ptx::ex2_approx(x1);
-                if (decltype(mask)::value) {
-                  const int col = 32 * c + e;
-                  if (col < from || col >= to) p0 = 0.f;
-                  if (col + 1 < from || col + 1 >= to) p1 = 0.f;
-                }
+                const float p0 = ptx::ex2_approx(x0);
+                const float p1 = ptx::ex2_approx(x1);
                 s[c][e] = __float_as_uint(p0);
                 s[c][e + 1] = __float_as_uint(p1);
                 pp[16 * c + 2 * v + h2] = ptx::pack_bf16x2(p0, p1);
               }
             }
           }
-        };
-        if (masked) p_pass(std::true_type{});
-        else p_pass(std::false_type{});
-        ptx::tmem_st32(tS, pp);
-        if (ragged) {
-          // Clear the rows behind the sequence's end before dV and dK sum
-          // over them; S^T and dP^T have read the tiles by now.
-          ok = wait_warp_or_abort(ptx::smem_u32(&bar_dpt_full), i & 1, abort_ptr, p.timeout_ns, kRoleVarDkvSoftmax);
-          if (!ok) break;
-          uint8_t* slot = smem_raw + (sRing - raw) + (i % C::kStages) * C::kPairBytes;
-          clear_rows<HD>(slot, live_tok * p.G, box_rows, tid);
-          clear_rows<HD>(slot + C::kTileBytes, live_tok * p.G, box_rows, tid);
-          ptx::fence_proxy_async_smem();
+          ptx::tmem_st32(tS, pp);
+          if (ragged) {
+            // Clear the rows behind the sequence's end before dV and dK sum
+            // over them; S^T and dP^T have read the tiles by now.
+            ok = wait(&bar_dpt_full, g);
+            if (!ok) break;
+            uint8_t* slot = smem_raw + (sRing - raw) + (g % C::kStages) * C::kPairBytes;
+            clear_rows<HD>(slot, (nq - tok0) * p.G, box_rows, tid);
+            clear_rows<HD>(slot + C::kTileBytes, (nq - tok0) * p.G, box_rows, tid);
+            ptx::fence_proxy_async_smem();
+          }
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(ptx::smem_u32(&bar_pt_stored));
         }
-        ptx::tmem_st_wait();
+        ok = wait(&bar_dpt_full, g);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        // dP of rows behind the end may be anything.
+        if (ragged) mask_columns(tP, 0, to, 0u);
+        ptx::tmem_ld32(tP, dp[0]);
+        ptx::tmem_ld32(tP + 32, dp[1]);
+        ptx::tmem_ld_wait();
+        ptx::reg_fence32(dp[0]);
+        ptx::reg_fence32(dp[1]);
         ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_u32(&bar_pt_stored));
-      }
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_dpt_full), i & 1, abort_ptr, p.timeout_ns, kRoleVarDkvSoftmax);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      ptx::tmem_ld32(tP, dp[0]);
-      ptx::tmem_ld32(tP + 32, dp[1]);
-      ptx::tmem_ld_wait();
-      ptx::reg_fence32(dp[0]);
-      ptx::reg_fence32(dp[1]);
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(ptx::smem_u32(&bar_dp_free));
-      uint32_t pds[32];
-      auto ds_pass = [&](auto mask) {
+        ptx::mbar_arrive(ptx::smem_u32(&bar_dp_free));
+        uint32_t pds[32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -852,36 +972,29 @@ __device__ __forceinline__ bool varlen_dkdv_unit(const CUtensorMap& tmQ, const C
               float d0, d1;
               ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), t), d0,
                              d1);
-              if (decltype(mask)::value) {   // dP of a column behind the end may be anything
-                if (32 * c + e >= to) d0 = 0.f;
-                if (32 * c + e + 1 >= to) d1 = 0.f;
-              }
               pds[16 * c + 2 * v + h2] = ptx::pack_bf16x2(d0, d1);
             }
           }
         }
-      };
-      if (ragged) ds_pass(std::true_type{});
-      else ds_pass(std::false_type{});
-      ptx::tmem_st32(tS + 32, pds);
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(ptx::smem_u32(&bar_p_full));
-    }
-    if (ok && n > 0)
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_acc_full), 0, abort_ptr, p.timeout_ns, kRoleVarDkvSoftmax);
-    if (ok) {
-      ptx::tc_fence_after();
-      const bool live = key0 + row < u.nkv;
-      const long long key = static_cast<long long>(u.kv0) + key0 + row;
-      __nv_bfloat16* dv = p.dV + key * p.dv_st + kvh * p.dv_sh + half * (HD / 2);
-      __nv_bfloat16* dk = p.dK + key * p.dk_st + kvh * p.dk_sh + half * (HD / 2);
-      if (n > 0) {
-#pragma unroll
-        for (int c = 0; c < HD / 64; ++c) {
-          store_row32(tmem_base + lane_addr + kColDV + half * (HD / 2) + 32 * c, 1.f, dv + 32 * c, live);
-          store_row32(tmem_base + lane_addr + kColDK + half * (HD / 2) + 32 * c, p.scale, dk + 32 * c, live);
-        }
+        ptx::tmem_st32(tS + 32, pds);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_u32(&bar_p_full));
+      }
+      if (!ok) break;
+      const int key_row = job.u.blk * C::kBlk + row;
+      const bool live = key_row < job.u.nkv;
+      const long long key = static_cast<long long>(job.u.kv0) + key_row;
+      __nv_bfloat16* dv = p.dV + key * p.dv_st + job.kvh * p.dv_sh + half * (HD / 2);
+      __nv_bfloat16* dk = p.dK + key * p.dk_st + job.kvh * p.dk_sh + half * (HD / 2);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&jobs.empty[n & 1]));
+      if (steps > 0) {
+        ok = wait(&bar_acc_full, units++);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        store_half_row<HD>(tmem_base + lane_addr + kColDV + half * (HD / 2), 1.f, dv, live);
+        store_half_row<HD>(tmem_base + lane_addr + kColDK + half * (HD / 2), p.scale, dk, live);
       } else if (live) {   // a sequence without query rows
         for (int c = 0; c < HD / 16; ++c) {
           reinterpret_cast<uint4*>(dv)[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -890,38 +1003,40 @@ __device__ __forceinline__ bool varlen_dkdv_unit(const CUtensorMap& tmQ, const C
       }
     }
   }
-
   ptx::tc_fence_before();
-  __syncthreads();
+  const bool all_ok = role_sync_and(ok);
   ptx::tc_fence_after();
-  if (*abort_ptr) return false;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s)
-      for (uint64_t* b : {&bar_q_full[s], &bar_q_empty[s], &bar_do_full[s], &bar_do_empty[s]})
-        ptx::mbar_inval(ptx::smem_u32(b));
-    for (uint64_t* b : {&bar_kv_full, &bar_st_full, &bar_dpt_full, &bar_dp_free, &bar_p_full, &bar_pt_stored,
-                        &bar_acc_full, &bar_drain})
-      ptx::mbar_inval(ptx::smem_u32(b));
-  }
-  return true;
+  return all_ok ? taken : -1;
 }
 
+constexpr int kVarBwdThreads = 352;   // the ten warps of BwdCfg and the fetch warp
+
 template <int HD>
-__global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
+__global__ void __launch_bounds__(kVarBwdThreads, 1)
     fa_varlen_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                          const VarBwdParams p) {
   using C = BwdCfg<HD>;
-  __shared__ VarBwdJob jobs[2];
+  __shared__ __align__(16) VarBwdJobs jobs;
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_ptr = &abort_flag;
   if (warp == 9) {
     ptx::tmem_alloc(ptx::smem_u32(&tmem_base_slot), C::kTmemCols);
     ptx::tmem_relinquish();
   }
-  if (threadIdx.x == 256) {
+  if (threadIdx.x == 0) {
     abort_flag = 0;
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&jobs.full[s]), 1);
+      ptx::mbar_init(ptx::smem_u32(&jobs.empty[s]), 10);
+    }
+    ptx::mbar_init(ptx::smem_u32(&jobs.claim), 1);
+    ptx::fence_mbar_init();
+  }
+  if (threadIdx.x == 256) {
     ptx::prefetch_tmap(&tmQ);
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
@@ -929,21 +1044,39 @@ __global__ void __launch_bounds__(BwdCfg<HD>::kThreads, 1)
   }
   // Every thread reads what the launches before wrote (the list, the rows' values).
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (threadIdx.x == 256) fetch_job(p, static_cast<int>(blockIdx.x), &jobs[0]);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_base_slot;
-  bool ok = true;
-  for (int k = 0; ok; ++k) {
-    const VarBwdUnit u = jobs[k & 1].u;
-    const int kvh = jobs[k & 1].kvh;
-    if (kvh < 0) break;
-    // The producer thread leaves the unit after this one in the other slot.
-    if (u.dkdv)
-      ok = varlen_dkdv_unit<HD>(tmQ, tmK, tmV, tmdO, p, u, kvh, tmem_base, &abort_flag, &jobs[(k + 1) & 1]);
-    else
-      ok = varlen_dq_unit<HD>(tmQ, tmK, tmV, tmdO, p, u, kvh, tmem_base, &abort_flag, &jobs[(k + 1) & 1]);
+  if (warp == 10) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ unit fetch
+      // (A unit is taken when the loads of the one before near their end.)
+      const int total = p.plan->num_units * p.H_kv;
+      int idx = blockIdx.x;
+      for (int n = 0;; ++n) {
+        VarBwdJob job;
+        job.kvh = -1;
+        job.u.dkdv = 0;
+        if (idx < total) {
+          const int e = idx / p.H_kv;
+          job.u = p.list[e];
+          job.kvh = idx - e * p.H_kv;
+        }
+        if (!wait_or_abort(ptx::smem_u32(&jobs.empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
+                           kRoleVarDqProducer))
+          break;
+        jobs.job[n & 1] = job;
+        ptx::mbar_arrive(ptx::smem_u32(&jobs.full[n & 1]));
+        if (job.kvh < 0) break;
+        if (!wait_or_abort(ptx::smem_u32(&jobs.claim), n & 1, abort_ptr, p.timeout_ns, kRoleVarDqProducer)) break;
+        idx = static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int n = varlen_dkdv_loop<HD>(tmQ, tmK, tmV, tmdO, p, jobs, tmem_base, abort_ptr);
+    if (n >= 0) varlen_dq_loop<HD>(tmQ, tmK, tmV, tmdO, p, jobs, n, tmem_base, abort_ptr);
   }
   __syncthreads();
   if (warp == 9) {
