@@ -316,6 +316,12 @@ fa_status_t varlen_bwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   p.ndelta = ndelta;
   p.tile_cap = static_cast<int>(w.tiles);
   p.H_kv = H_kv;
+  // Heads whose units are taken together: as many as stream at most 96 MB of
+  // Q, dO, K and V, so that they stay in L2 (129 MB). At 8192 tokens of 32
+  // heads, not causal: 2694 us with all heads together, 2531 in groups; at
+  // 48 MB short batches lose 2 % by fewer units to balance.
+  p.group = std::max(1, static_cast<int>(
+                            std::min<double>(H_kv, 96e6 / (4.0 * HD * (k.T + static_cast<double>(G) * q.T)))));
   p.G = G;
   p.tp = tp;
   p.inv_g = (65536 + G - 1) / G;

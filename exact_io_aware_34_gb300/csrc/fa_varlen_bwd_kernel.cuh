@@ -24,10 +24,13 @@
 //     sequence or to nobody and may hold anything. Scores of invisible pairs
 //     become -inf in tensor memory before the exponential (the tensor core
 //     forms -S for a negative scale, as in the forward, and scale = 0 runs as
-//     2^-126), and dP of rows behind the end becomes 0. Where such rows are
-//     summed over (Q and dO in the key-block role, K in the query role) they
-//     are cleared in shared memory once the products that form S and dP have
-//     read them; elsewhere they only reach accumulator rows that are not stored.
+//     2^-126). Where such rows are summed over (Q and dO in the key-block role,
+//     K and V in the query role) they are cleared in shared memory: the tile's
+//     load completes on a barrier of its own, warp 11 clears the rows and then
+//     completes the tile's barrier in its place, so that nobody else knows.
+//     (Clearing in the elementwise warps, behind branches that one step in a
+//     sequence takes, slowed their every step: 6 % of the call at d = 128, 13 %
+//     at 64.) Elsewhere such rows only reach accumulator rows that are not stored.
 // Three launches: the plan; -LSE log2(e) and -D of every tile row
 // (varlen_bwd_rows_kernel); the products.
 #pragma once
@@ -54,9 +57,10 @@ struct VarBwdUnit {
 
 struct VarBwdPlan {
   int num_units;          // list entries (each stands for H_kv units)
+  int num_dkdv;           // of which the first are the key-block role's
   int num_tiles;
   int next;
-  int pad[5];
+  int pad[4];
 };
 
 struct VarBwdParams {
@@ -68,6 +72,7 @@ struct VarBwdParams {
   const float* ndelta;    // the same shape: -D, or 0
   int tile_cap;
   int H_kv, G, tp;
+  int group;              // K/V heads whose units are taken together
   int inv_g;              // ceil(65536 / G): r / G = r * inv_g >> 16 for r < 128
   int causal;
   float scale_log2;       // |scale| * log2(e), at least 2^-126
@@ -114,13 +119,13 @@ __global__ void __launch_bounds__(kPlanThreads)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   if (!offsets_ok(cu_q, cu_kv, B, T_q, T_kv)) {
-    if (tid == 0) plan->num_units = plan->num_tiles = plan->next = 0;
+    if (tid == 0) plan->num_units = plan->num_dkdv = plan->num_tiles = plan->next = 0;
     return;
   }
   hist[tid] = 0;
   int total = 0, total_tiles = 0;
   for (int round = 0; round < 2; ++round) {
-    int tile_base = 0;
+    int tile_base = 0;                         // query tiles of the chunks before
     for (int c0 = 0; c0 < B; c0 += kPlanThreads) {
       if (round == 0 || B > kPlanThreads) {
         __syncthreads();
@@ -168,6 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   if (tid == 0) {
     plan->num_units = total;
+    plan->num_dkdv = total - total_tiles;
     plan->num_tiles = total_tiles;
     plan->next = 0;
   }
@@ -235,16 +241,32 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- products
+// The idx-th unit of n list entries x H_kv heads, taken `group` heads at a
+// time (the heads of a group together, so that what they stream stays in L2),
+// within a group in the list's order.
+__device__ __forceinline__ void place_unit(int idx, int n, int H_kv, int group, int* entry, int* kvh) {
+  const int g = idx / (n * group), r = idx - g * n * group;
+  const int heads = min(group, H_kv - g * group);
+  *entry = r / heads;
+  *kvh = g * group + r - *entry * heads;
+}
+
 struct VarBwdJob {
   VarBwdUnit u;
   int kvh;       // -1: no more units
 };
 
-// Shared by both roles' loops: two job slots, handed over by the fetch warp.
-struct VarBwdJobs {
+// Shared by both roles' loops: two job slots, handed over by the fetch warp,
+// and the barriers that the warp which clears tails takes part in. At most four
+// tiles of a kind are in flight, which is what their rings hold.
+template <int HD>
+struct VarBwdShared {
   VarBwdJob job[2];
-  uint64_t full[2], empty[2];   // empty: producer, issuer, eight elementwise warps
+  uint64_t full[2], empty[2];   // empty: warps 0-9 and 11
   uint64_t claim;               // the producer nears the end of a unit's loads
+  uint64_t q_full[BwdCfg<HD>::kStages], do_full[BwdCfg<HD>::kStages];    // key-block role: Q_i, dO_i (and their vectors)
+  uint64_t k_full[DqCfg<HD>::kKSlots], v_full[DqCfg<HD>::kVSlots];       // query role: K_j, V_j
+  uint64_t tail[4][4];          // Q, dO, K, V tiles with rows to clear have landed
 };
 
 // A barrier of the ten warps that work on units (the fetch warp is not one).
@@ -275,18 +297,18 @@ __device__ __forceinline__ void issue_tile_qk_desc(uint32_t d_tmem, uint32_t a_t
 }
 
 // Zeroes rows [from, to) of the 128-row tile at `tile` (generic address),
-// whole 128-byte rows, with 256 threads.
+// whole 128-byte rows, with `threads` threads.
 template <int HD>
-__device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int to, int tid) {
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int to, int tid, int threads) {
   using C = BwdCfg<HD>;
   for (int c = 0; c < C::kChunks; ++c)
-    for (int i = tid; i < (to - from) * 8; i += 256)
+    for (int i = tid; i < (to - from) * 8; i += threads)
       reinterpret_cast<uint4*>(tile + c * C::kChunkBytes + from * 128)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// Columns of this thread's row outside [from, to) of the 64 at `taddr` become
-// `fill`. A short loop, for the few blocks that need it.
-__device__ __forceinline__ void mask_columns(uint32_t taddr, int from, int to, uint32_t fill) {
+// Scores of this thread's row outside columns [from, to) of the 64 at `taddr`
+// become -inf. A short loop, out of the way of the blocks that do not need it.
+__device__ __noinline__ void mask_columns(uint32_t taddr, int from, int to) {
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     const int lo = from - 32 * c, hi = to - 32 * c;
@@ -297,7 +319,7 @@ __device__ __forceinline__ void mask_columns(uint32_t taddr, int from, int to, u
     ptx::reg_fence32(r);
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-      if (i < lo || i >= hi) r[i] = fill;
+      if (i < lo || i >= hi) r[i] = __float_as_uint(-INFINITY);
     ptx::tmem_st32(taddr + 32 * c, r);
   }
   ptx::tmem_st_wait();
@@ -313,16 +335,14 @@ __device__ __forceinline__ void store_half_row(uint32_t taddr, float mul, __nv_b
 // The query role: units from job n0 on, to the end of the list.
 template <int HD>
 __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                                               const CUtensorMap& tmdO, const VarBwdParams& p, VarBwdJobs& jobs, int n0,
+                                               const CUtensorMap& tmdO, const VarBwdParams& p, VarBwdShared<HD>& jobs, int n0,
                                                const uint32_t tmem_base, volatile int* abort_ptr) {
   using C = BwdCfg<HD>;
   using D = DqCfg<HD>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_q_full, bar_q_empty;      // Q of the unit
   __shared__ __align__(8) uint64_t bar_do_full, bar_do_empty;    // dO of the unit
-  __shared__ __align__(8) uint64_t bar_k_full[D::kKSlots];
   __shared__ __align__(8) uint64_t bar_k_empty[D::kKSlots];
-  __shared__ __align__(8) uint64_t bar_v_full[D::kVSlots];
   __shared__ __align__(8) uint64_t bar_v_empty[D::kVSlots];
   __shared__ __align__(8) uint64_t bar_st_full;    // S_j complete
   __shared__ __align__(8) uint64_t bar_dpt_full;   // dP_j complete
@@ -334,8 +354,7 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t raw = ptx::smem_u32(smem_raw);
-  const uint32_t smem_base = (raw + 1023u) & ~1023u;
+  const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = smem_base;
   const uint32_t sdO = smem_base + C::kTileBytes;
   const uint32_t sK = smem_base + 2 * C::kTileBytes;
@@ -345,14 +364,8 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
     for (uint64_t* b : {&bar_q_full, &bar_q_empty, &bar_do_full, &bar_do_empty, &bar_st_full, &bar_dpt_full,
                         &bar_acc_full, &bar_drain})
       ptx::mbar_init(ptx::smem_u32(b), 1);
-    for (int s = 0; s < D::kKSlots; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&bar_k_full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bar_k_empty[s]), 1);
-    }
-    for (int s = 0; s < D::kVSlots; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&bar_v_full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bar_v_empty[s]), 1);
-    }
+    for (int s = 0; s < D::kKSlots; ++s) ptx::mbar_init(ptx::smem_u32(&bar_k_empty[s]), 1);
+    for (int s = 0; s < D::kVSlots; ++s) ptx::mbar_init(ptx::smem_u32(&bar_v_empty[s]), 1);
     for (uint64_t* b : {&bar_s_free, &bar_dp_free, &bar_p_full[0], &bar_p_full[1]})
       ptx::mbar_init(ptx::smem_u32(b), 256);
     ptx::fence_mbar_init();
@@ -367,21 +380,26 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
       int it = 0;        // loads of K (even) and V (odd) so far, in the order K_0, V_0, K_1, ...
       int units = 0;
       int issued[2] = {0, 0};    // loads of Q and dO
+      int tails[2] = {0, 0};     // K and V tiles with rows to clear
       bool ok = true;
-      VarBwdJob job;
+      VarBwdJob job = {};
       auto load = [&](int j) {
         const int g = it >> 1;
         const bool is_v = it & 1;
         const int slots = is_v ? D::kVSlots : D::kKSlots;
         const int slot = g % slots;
         uint64_t* empty = is_v ? bar_v_empty : bar_k_empty;
-        uint64_t* full = is_v ? bar_v_full : bar_k_full;
+        uint64_t* full = is_v ? jobs.v_full : jobs.k_full;
         if (!wait_or_abort(ptx::smem_u32(&empty[slot]), ((g / slots) & 1) ^ 1u, abort_ptr, p.timeout_ns,
                            kRoleVarDqProducer))
           return false;
         const int me = it++;
         if (me == p.drop_load) return true;   // test hook: this tile never arrives
-        const uint32_t fb = ptx::smem_u32(&full[slot]);
+        uint32_t fb = ptx::smem_u32(&full[slot]);
+        if ((j + 1) * C::kBlk > job.u.nkv) {     // rows behind the end: warp 11 completes `full`
+          fb = ptx::smem_u32(&jobs.tail[2 + is_v][tails[is_v] & 3]);
+          ++tails[is_v];
+        }
         ptx::mbar_arrive_expect_tx(fb, C::kTileBytes);
         const uint32_t dst = (is_v ? sV : sK) + slot * C::kTileBytes;
         for (int c = 0; c < C::kChunks; ++c)
@@ -425,13 +443,16 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
         // Let every copy this thread started land before the CTA exits.
         if (issued[0] > 0) drain_wait(ptx::smem_u32(&bar_q_full), (issued[0] - 1) & 1, p.timeout_ns);
         if (issued[1] > 0) drain_wait(ptx::smem_u32(&bar_do_full), (issued[1] - 1) & 1, p.timeout_ns);
+        for (int x = 0; x < 2; ++x)
+          for (int r = max(0, tails[x] - 4); r < tails[x]; ++r)
+            drain_wait(ptx::smem_u32(&jobs.tail[2 + x][r & 3]), (r >> 2) & 1, p.timeout_ns);
         for (int i = 0; i < it; ++i) {
           const int g = i >> 1;
           const bool is_v = i & 1;
           const int slots = is_v ? D::kVSlots : D::kKSlots;
           const int last = (it - 1 - (is_v ? 1 : 0)) >> 1;
           if (g + slots <= last || i == p.drop_load) continue;
-          drain_wait(ptx::smem_u32(&(is_v ? bar_v_full : bar_k_full)[g % slots]), (g / slots) & 1, p.timeout_ns);
+          drain_wait(ptx::smem_u32(&(is_v ? jobs.v_full : jobs.k_full)[g % slots]), (g / slots) & 1, p.timeout_ns);
         }
       }
     }
@@ -468,11 +489,11 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
       if (kvh < 0) break;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&jobs.empty[n & 1]));
-      ok = wait(&bar_q_full, units) && wait(&bar_k_full[g % D::kKSlots], g / D::kKSlots);
+      ok = wait(&bar_q_full, units) && wait(&jobs.k_full[g % D::kKSlots], g / D::kKSlots);
       if (ok && g > 0) ok = wait(&bar_s_free, g - 1);
       if (!ok) break;
       issue_s(g, blocks == 1);
-      ok = wait(&bar_do_full, units) && wait(&bar_v_full[g % D::kVSlots], g / D::kVSlots);
+      ok = wait(&bar_do_full, units) && wait(&jobs.v_full[g % D::kVSlots], g / D::kVSlots);
       if (ok && g > 0) ok = wait(&bar_dp_free, g - 1);
       if (!ok) break;
       issue_dp(g, blocks == 1);
@@ -505,7 +526,6 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
     const int quarter = warp & 3;
     const int half = warp >> 2;
     const int row = quarter * 32 + lane;
-    const int tid = half * 128 + row;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint64_t sl2x2 = ptx::f2_pack(p.scale_log2, p.scale_log2);
     const uint32_t tS = tmem_base + lane_addr + D::kColS + 64u * half;
@@ -521,13 +541,13 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
       if (!ok) break;
       const VarBwdJob& job = jobs.job[n & 1];
       if (job.kvh < 0) break;
-      const int blocks = job.u.n, nkv = job.u.nkv;
+      const int blocks = job.u.n;
       // Keys this row sees; rows that do not exist take the last token's.
-      int limit = nkv;
-      {
+      int limit = job.u.nkv;
+      if (p.causal) {
         const int tok0 = job.u.blk * p.tp;
         const int last = min(p.tp, job.u.nq - tok0) - 1;
-        if (p.causal) limit = max(0, min(nkv, tok0 + min(xr, last) + 1 + nkv - job.u.nq));
+        limit = max(0, min(limit, tok0 + min(xr, last) + 1 + limit - job.u.nq));
       }
       const long long vrow = (static_cast<long long>(job.kvh) * p.tile_cap + job.u.tile0 + job.u.blk) * 128 + row;
       const float nl = p.nlse2[vrow];
@@ -539,7 +559,7 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
         if (!ok) break;
         ptx::tc_fence_after();
         const int valid = limit - j * C::kBlk - 64 * half;   // keys of this warp's 64 that this row sees
-        if (!__all_sync(0xffffffffu, valid >= 64)) mask_columns(tS, 0, valid, __float_as_uint(-INFINITY));
+        if (!__all_sync(0xffffffffu, valid >= 64)) mask_columns(tS, 0, valid);
         uint32_t s[2][32], dp[2][32];
         ptx::tmem_ld32(tS, s[0]);
         ptx::tmem_ld32(tS + 32, s[1]);
@@ -548,17 +568,12 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
         ptx::reg_fence32(s[1]);
         if (j + 1 < blocks) {
           // K_{j+1} in place before the hand-off that lets S_{j+1} be issued.
-          ok = wait(&bar_k_full[(g + 1) % D::kKSlots], (g + 1) / D::kKSlots);
+          ok = wait(&jobs.k_full[(g + 1) % D::kKSlots], (g + 1) / D::kKSlots);
           if (!ok) break;
         }
         ptx::tc_fence_before();
         ptx::mbar_arrive(ptx::smem_u32(&bar_s_free));
 
-        const int have = nkv - j * C::kBlk;    // keys of the sequence in this block
-        if (have < C::kBlk) {
-          clear_rows<HD>(smem_raw + (sK - raw) + (g % D::kKSlots) * C::kTileBytes, max(have, 0), C::kBlk, tid);
-          ptx::fence_proxy_async_smem();
-        }
         // P (float32, kept in s) while dP_j is still on the tensor core.
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -575,8 +590,6 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
         ok = wait(&bar_dpt_full, g);
         if (!ok) break;
         ptx::tc_fence_after();
-        // dP of keys behind the end may be anything.
-        if (have < C::kBlk) mask_columns(tP, 0, have - 64 * half, 0u);
         ptx::tmem_ld32(tP, dp[0]);
         ptx::tmem_ld32(tP + 32, dp[1]);
         ptx::tmem_ld_wait();
@@ -584,7 +597,7 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
         ptx::reg_fence32(dp[1]);
         if (j + 1 < blocks) {
           // V_{j+1} in place before the hand-off that lets dP_{j+1} be issued.
-          ok = wait(&bar_v_full[(g + 1) % D::kVSlots], (g + 1) / D::kVSlots);
+          ok = wait(&jobs.v_full[(g + 1) % D::kVSlots], (g + 1) / D::kVSlots);
           if (!ok) break;
         }
         ptx::tc_fence_before();
@@ -631,7 +644,7 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
 template <int HD>
 __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                                 const CUtensorMap& tmV, const CUtensorMap& tmdO,
-                                                const VarBwdParams& p, VarBwdJobs& jobs, const uint32_t tmem_base,
+                                                const VarBwdParams& p, VarBwdShared<HD>& jobs, const uint32_t tmem_base,
                                                 volatile int* abort_ptr) {
   using C = BwdCfg<HD>;
   constexpr uint32_t kColDV = 0;
@@ -640,9 +653,7 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_k_full, bar_k_empty;     // K of the unit
   __shared__ __align__(8) uint64_t bar_v_full, bar_v_empty;     // V of the unit
-  __shared__ __align__(8) uint64_t bar_q_full[C::kStages];      // Q_i and -LSE*log2e landed
   __shared__ __align__(8) uint64_t bar_q_empty[C::kStages];     // dK(i) done with Q_i
-  __shared__ __align__(8) uint64_t bar_do_full[C::kStages];     // dO_i and -D landed
   __shared__ __align__(8) uint64_t bar_do_empty[C::kStages];    // dV(i) done with dO_i
   __shared__ __align__(8) uint64_t bar_st_full;
   __shared__ __align__(8) uint64_t bar_dpt_full;
@@ -669,15 +680,14 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
                         &bar_acc_full, &bar_drain})
       ptx::mbar_init(ptx::smem_u32(b), 1);
     for (int s = 0; s < C::kStages; ++s)
-      for (uint64_t* b : {&bar_q_full[s], &bar_q_empty[s], &bar_do_full[s], &bar_do_empty[s]})
-        ptx::mbar_init(ptx::smem_u32(b), 1);
+      for (uint64_t* b : {&bar_q_empty[s], &bar_do_empty[s]}) ptx::mbar_init(ptx::smem_u32(b), 1);
     for (uint64_t* b : {&bar_dp_free, &bar_p_full, &bar_pt_stored}) ptx::mbar_init(ptx::smem_u32(b), 256);
     ptx::fence_mbar_init();
   }
   // Rows of the ring that no load writes are zero.
   if (box_rows < C::kBlk && warp < 8) {
     for (int s = 0; s < 2 * C::kStages; ++s)
-      clear_rows<HD>(smem_raw + (sRing - raw) + s * C::kTileBytes, box_rows, C::kBlk, threadIdx.x);
+      clear_rows<HD>(smem_raw + (sRing - raw) + s * C::kTileBytes, box_rows, C::kBlk, threadIdx.x, 256);
     ptx::fence_proxy_async_smem();
   }
   role_sync();
@@ -690,6 +700,7 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
       const uint32_t bytes = C::kChunks * 128 * box_rows + C::kBlk * 4;
       int g = 0, units = 0, n = 0;          // query tiles, units, jobs so far
       int issued_k = 0, issued_q = 0, issued_do = 0;
+      int tails_q = 0, tails_do = 0;        // Q and dO tiles with rows to clear
       for (; ok; ++n) {
         ok = wait_or_abort(ptx::smem_u32(&jobs.full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
                            kRoleVarDkvProducer);
@@ -706,6 +717,8 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
           const uint32_t par = ((g / C::kStages) & 1) ^ 1u;
           const uint32_t dst = sRing + slot * C::kPairBytes;
           const int token = job.u.q0 + (tile_first + i) * p.tp;
+          // Rows behind the end: warp 11 completes the tiles' barriers.
+          const bool tail = (tile_first + i + 1) * p.tp > job.u.nq;
           const long long voff =
               (static_cast<long long>(job.kvh) * p.tile_cap + job.u.tile0 + tile_first + i) * C::kBlk;
           if (i == 0) {
@@ -726,7 +739,7 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
           }
           issued_q = g + 1;
           if (g != p.drop_load) {    // test hook: this step's tiles never arrive
-            const uint32_t full = ptx::smem_u32(&bar_q_full[slot]);
+            const uint32_t full = ptx::smem_u32(tail ? &jobs.tail[0][tails_q++ & 3] : &jobs.q_full[slot]);
             ptx::mbar_arrive_expect_tx(full, bytes);
             for (int c = 0; c < C::kChunks; ++c)
               ptx::tma_load_3d(dst + c * C::kChunkBytes, &tmQ, full, c * 64, job.kvh * p.G, token, pol_shared);
@@ -750,7 +763,7 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
           }
           issued_do = g + 1;
           if (g != p.drop_load) {
-            const uint32_t full = ptx::smem_u32(&bar_do_full[slot]);
+            const uint32_t full = ptx::smem_u32(tail ? &jobs.tail[1][tails_do++ & 3] : &jobs.do_full[slot]);
             ptx::mbar_arrive_expect_tx(full, bytes);
             for (int c = 0; c < C::kChunks; ++c)
               ptx::tma_load_3d(dst + C::kTileBytes + c * C::kChunkBytes, &tmdO, full, c * 64, job.kvh * p.G, token,
@@ -765,12 +778,16 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
         // Let every copy this thread started land before the CTA exits.
         if (issued_k > 0) drain_wait(ptx::smem_u32(&bar_k_full), (issued_k - 1) & 1, p.timeout_ns);
         if (units > 0) drain_wait(ptx::smem_u32(&bar_v_full), (units - 1) & 1, p.timeout_ns);
+        for (int r = max(0, tails_q - 4); r < tails_q; ++r)
+          drain_wait(ptx::smem_u32(&jobs.tail[0][r & 3]), (r >> 2) & 1, p.timeout_ns);
+        for (int r = max(0, tails_do - 4); r < tails_do; ++r)
+          drain_wait(ptx::smem_u32(&jobs.tail[1][r & 3]), (r >> 2) & 1, p.timeout_ns);
         for (int i = issued_q > C::kStages ? issued_q - C::kStages : 0; i < issued_q; ++i)
           if (i != p.drop_load)
-            drain_wait(ptx::smem_u32(&bar_q_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
+            drain_wait(ptx::smem_u32(&jobs.q_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
         for (int i = issued_do > C::kStages ? issued_do - C::kStages : 0; i < issued_do; ++i)
           if (i != p.drop_load)
-            drain_wait(ptx::smem_u32(&bar_do_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
+            drain_wait(ptx::smem_u32(&jobs.do_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
       }
     }
     __syncwarp();
@@ -809,10 +826,10 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&jobs.empty[n & 1]));
       if (steps == 0) continue;     // no query rows: the elementwise warps store zeros
-      ok = wait(&bar_k_full, units) && wait(&bar_q_full[g % C::kStages], g / C::kStages);
+      ok = wait(&bar_k_full, units) && wait(&jobs.q_full[g % C::kStages], g / C::kStages);
       if (!ok) break;
       issue_s(g, steps == 1);
-      ok = wait(&bar_v_full, units) && wait(&bar_do_full[g % C::kStages], g / C::kStages);
+      ok = wait(&bar_v_full, units) && wait(&jobs.do_full[g % C::kStages], g / C::kStages);
       if (!ok) break;
       ++units;
       ok = issue_dp_dv(g, true, steps == 1);
@@ -830,7 +847,7 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
           if (!ok) break;
           const uint64_t t0 = ptx::globaltimer_ns();
           while (true) {
-            if (__all_sync(0xffffffffu, ptx::mbar_test_wait(ptx::smem_u32(&bar_q_full[s1]), in_phase & 1))) {
+            if (__all_sync(0xffffffffu, ptx::mbar_test_wait(ptx::smem_u32(&jobs.q_full[s1]), in_phase & 1))) {
               issue_s(g + 1, last);
               s_issued = true;
               break;
@@ -848,11 +865,11 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
         ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[g % C::kStages]));
         if (more) {
           if (!s_issued) {
-            ok = wait(&bar_q_full[s1], in_phase);
+            ok = wait(&jobs.q_full[s1], in_phase);
             if (!ok) break;
             issue_s(g + 1, last);
           }
-          ok = wait(&bar_do_full[s1], in_phase);
+          ok = wait(&jobs.do_full[s1], in_phase);
           if (!ok) break;
           ok = issue_dp_dv(g + 1, false, last);
         }
@@ -869,7 +886,6 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
     const int quarter = warp & 3;
     const int half = warp >> 2;
     const int row = quarter * 32 + lane;
-    const int tid = half * 128 + row;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint64_t sl2x2 = ptx::f2_pack(p.scale_log2, p.scale_log2);
     auto wait = [&](uint64_t* b, int phase) {
@@ -886,10 +902,8 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
       // First token of the sequence that sees this key (causal).
       const int see0 = p.causal ? job.u.blk * C::kBlk + row - (job.u.nkv - nq) : 0;
       for (int i = 0; i < steps; ++i, ++g, tok0 += p.tp) {
-        const bool ragged = nq - tok0 < p.tp;
-        // Columns x * G + h of this warp's 64 that count for this key: [from, to).
+        // Columns x * G + h of this warp's 64 that see this key: from here on.
         const int from = max(0, min(see0 - tok0, p.tp)) * p.G - 64 * half;
-        const int to = (ragged ? (nq - tok0) * p.G : C::kBlk) - 64 * half;
         // P^T as soon as S^T(i) is complete (it overlaps the tensor core's dK/dV
         // of the previous block and dP^T of this one), then dS^T once dP^T(i) is.
         ok = wait(&bar_st_full, g);
@@ -897,7 +911,7 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
         ptx::tc_fence_after();
         const uint32_t tS = tmem_base + lane_addr + kColR + 128u * (g & 1) + 64u * half;
         const uint32_t tP = tmem_base + lane_addr + kColR + 128u * ((g + 1) & 1) + 64u * half;
-        if (!__all_sync(0xffffffffu, from <= 0 && to >= 64)) mask_columns(tS, from, to, __float_as_uint(-INFINITY));
+        if (!__all_sync(0xffffffffu, from <= 0)) mask_columns(tS, from, 64);
         uint32_t s[2][32], dp[2][32];
         ptx::tmem_ld32(tS, s[0]);
         ptx::tmem_ld32(tS + 32, s[1]);
@@ -931,16 +945,6 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
             }
           }
           ptx::tmem_st32(tS, pp);
-          if (ragged) {
-            // Clear the rows behind the sequence's end before dV and dK sum
-            // over them; S^T and dP^T have read the tiles by now.
-            ok = wait(&bar_dpt_full, g);
-            if (!ok) break;
-            uint8_t* slot = smem_raw + (sRing - raw) + (g % C::kStages) * C::kPairBytes;
-            clear_rows<HD>(slot, (nq - tok0) * p.G, box_rows, tid);
-            clear_rows<HD>(slot + C::kTileBytes, (nq - tok0) * p.G, box_rows, tid);
-            ptx::fence_proxy_async_smem();
-          }
           ptx::tmem_st_wait();
           ptx::tc_fence_before();
           ptx::mbar_arrive(ptx::smem_u32(&bar_pt_stored));
@@ -948,8 +952,6 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
         ok = wait(&bar_dpt_full, g);
         if (!ok) break;
         ptx::tc_fence_after();
-        // dP of rows behind the end may be anything.
-        if (ragged) mask_columns(tP, 0, to, 0u);
         ptx::tmem_ld32(tP, dp[0]);
         ptx::tmem_ld32(tP + 32, dp[1]);
         ptx::tmem_ld_wait();
@@ -1009,7 +1011,59 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
   return all_ok ? taken : -1;
 }
 
-constexpr int kVarBwdThreads = 352;   // the ten warps of BwdCfg and the fetch warp
+// The warp that clears rows behind a sequence's end: the last Q and dO tiles
+// of a key-block unit, the last K and V tiles of a query unit.
+template <int HD>
+__device__ __forceinline__ void varlen_bwd_tails(const VarBwdParams& p, VarBwdShared<HD>& jobs,
+                                                 volatile int* abort_ptr) {
+  using C = BwdCfg<HD>;
+  using D = DqCfg<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_u32(smem_raw);
+  uint8_t* base = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const int lane = threadIdx.x & 31;
+  int g[2] = {0, 0}, tails[2] = {0, 0};      // steps and tail pairs so far, per role
+  for (int n = 0;; ++n) {
+    if (!wait_warp_or_abort(ptx::smem_u32(&jobs.full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
+                            kRoleVarDkvProducer))
+      return;
+    const int kvh = jobs.job[n & 1].kvh, dkdv = jobs.job[n & 1].u.dkdv, steps = jobs.job[n & 1].u.n;
+    const int nq = jobs.job[n & 1].u.nq, nkv = jobs.job[n & 1].u.nkv;
+    __syncwarp();
+    if (kvh < 0) return;
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&jobs.empty[n & 1]));
+    const int r = dkdv ? 0 : 1;
+    g[r] += steps;
+    // Rows [from, to) of the unit's last streamed pair of tiles.
+    const int tiles = (nq + p.tp - 1) / p.tp;
+    const int from = dkdv ? (nq - (tiles - 1) * p.tp) * p.G : max(0, nkv - (steps - 1) * C::kBlk);
+    const int to = dkdv ? p.G * p.tp : C::kBlk;
+    if (steps == 0 || from >= to) continue;
+    const int last = g[r] - 1;
+#pragma unroll 1
+    for (int x = 0; x < 2; ++x) {
+      if (!wait_warp_or_abort(ptx::smem_u32(&jobs.tail[2 * r + x][tails[r] & 3]), (tails[r] >> 2) & 1, abort_ptr,
+                              p.timeout_ns, kRoleVarDkvProducer))
+        return;
+      uint8_t* tile;
+      uint64_t* full;
+      if (dkdv) {
+        tile = base + C::kPairBytes + (last % C::kStages) * C::kPairBytes + x * C::kTileBytes;
+        full = (x ? jobs.do_full : jobs.q_full) + last % C::kStages;
+      } else {
+        tile = base + (2 + (x ? D::kKSlots + last % D::kVSlots : last % D::kKSlots)) * C::kTileBytes;
+        full = x ? jobs.v_full + last % D::kVSlots : jobs.k_full + last % D::kKSlots;
+      }
+      clear_rows<HD>(tile, from, to, lane, 32);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(full));
+    }
+    ++tails[r];
+  }
+}
+
+constexpr int kVarBwdThreads = 384;   // the ten warps of BwdCfg, the fetch warp and the one that clears tails
 
 template <int HD>
 __global__ void __launch_bounds__(kVarBwdThreads, 1)
@@ -1017,7 +1071,7 @@ __global__ void __launch_bounds__(kVarBwdThreads, 1)
                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                          const VarBwdParams p) {
   using C = BwdCfg<HD>;
-  __shared__ __align__(16) VarBwdJobs jobs;
+  __shared__ __align__(16) VarBwdShared<HD> jobs;
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5;
@@ -1031,8 +1085,13 @@ __global__ void __launch_bounds__(kVarBwdThreads, 1)
     abort_flag = 0;
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(ptx::smem_u32(&jobs.full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&jobs.empty[s]), 10);
+      ptx::mbar_init(ptx::smem_u32(&jobs.empty[s]), 11);
     }
+    for (uint64_t& b : jobs.q_full) ptx::mbar_init(ptx::smem_u32(&b), 1);
+    for (uint64_t& b : jobs.do_full) ptx::mbar_init(ptx::smem_u32(&b), 1);
+    for (uint64_t& b : jobs.k_full) ptx::mbar_init(ptx::smem_u32(&b), 1);
+    for (uint64_t& b : jobs.v_full) ptx::mbar_init(ptx::smem_u32(&b), 1);
+    for (int x = 0; x < 16; ++x) ptx::mbar_init(ptx::smem_u32(&jobs.tail[x >> 2][x & 3]), 1);
     ptx::mbar_init(ptx::smem_u32(&jobs.claim), 1);
     ptx::fence_mbar_init();
   }
@@ -1059,9 +1118,15 @@ __global__ void __launch_bounds__(kVarBwdThreads, 1)
         job.kvh = -1;
         job.u.dkdv = 0;
         if (idx < total) {
-          const int e = idx / p.H_kv;
+          const int n_k = p.plan->num_dkdv, in_k = n_k * p.H_kv;
+          int e;
+          if (idx < in_k) {
+            place_unit(idx, n_k, p.H_kv, p.group, &e, &job.kvh);
+          } else {
+            place_unit(idx - in_k, p.plan->num_units - n_k, p.H_kv, p.group, &e, &job.kvh);
+            e += n_k;
+          }
           job.u = p.list[e];
-          job.kvh = idx - e * p.H_kv;
         }
         if (!wait_or_abort(ptx::smem_u32(&jobs.empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
                            kRoleVarDqProducer))
@@ -1069,11 +1134,14 @@ __global__ void __launch_bounds__(kVarBwdThreads, 1)
         jobs.job[n & 1] = job;
         ptx::mbar_arrive(ptx::smem_u32(&jobs.full[n & 1]));
         if (job.kvh < 0) break;
+        if (!ptx::mbar_test_wait(ptx::smem_u32(&jobs.claim), n & 1)) __nanosleep(1000);
         if (!wait_or_abort(ptx::smem_u32(&jobs.claim), n & 1, abort_ptr, p.timeout_ns, kRoleVarDqProducer)) break;
         idx = static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1);
       }
     }
     __syncwarp();
+  } else if (warp == 11) {
+    varlen_bwd_tails<HD>(p, jobs, abort_ptr);
   } else {
     const int n = varlen_dkdv_loop<HD>(tmQ, tmK, tmV, tmdO, p, jobs, tmem_base, abort_ptr);
     if (n >= 0) varlen_dq_loop<HD>(tmQ, tmK, tmV, tmdO, p, jobs, n, tmem_base, abort_ptr);
