@@ -536,22 +536,29 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
     };
     bool ok = true;
     int g = 0, units = 0;
-    for (int n = n0; ok; ++n) {
-      ok = wait(&jobs.full[n & 1], n >> 1);
-      if (!ok) break;
+    // What the block loop needs of a unit; the next unit's is read while the
+    // last product of this one runs.
+    int blocks = 0;
+    int limit = 0;       // keys this row sees; rows that do not exist take the last token's
+    float nl = 0.f, nd = 0.f;
+    auto read_job = [&](int n) {
+      if (!wait(&jobs.full[n & 1], n >> 1)) return false;
       const VarBwdJob& job = jobs.job[n & 1];
-      if (job.kvh < 0) break;
-      const int blocks = job.u.n;
-      // Keys this row sees; rows that do not exist take the last token's.
-      int limit = job.u.nkv;
+      if (job.kvh < 0) return false;
+      const long long vrow = (static_cast<long long>(job.kvh) * p.tile_cap + job.u.tile0 + job.u.blk) * 128 + row;
+      nl = p.nlse2[vrow];
+      nd = p.ndelta[vrow];
+      blocks = job.u.n;
+      limit = job.u.nkv;
       if (p.causal) {
         const int tok0 = job.u.blk * p.tp;
         const int last = min(p.tp, job.u.nq - tok0) - 1;
         limit = max(0, min(limit, tok0 + min(xr, last) + 1 + limit - job.u.nq));
       }
-      const long long vrow = (static_cast<long long>(job.kvh) * p.tile_cap + job.u.tile0 + job.u.blk) * 128 + row;
-      const float nl = p.nlse2[vrow];
-      const float nd = p.ndelta[vrow];
+      return true;
+    };
+    bool more = read_job(n0);
+    for (int n = n0; more; ++n) {
       const uint64_t nlx2 = ptx::f2_pack(nl, nl);
       const uint64_t ndx2 = ptx::f2_pack(nd, nd);
       for (int j = 0; j < blocks; ++j, ++g) {
@@ -621,12 +628,14 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
         ptx::mbar_arrive(ptx::smem_u32(&bar_p_full[g & 1]));
       }
       if (!ok) break;
+      const VarBwdJob& job = jobs.job[n & 1];
       const int tok0 = job.u.blk * p.tp;
       const bool live = row < p.G * p.tp && xr < job.u.nq - tok0;
       __nv_bfloat16* dst = p.dQ + (static_cast<long long>(job.u.q0) + tok0 + xr) * p.dq_st +
                            (job.kvh * p.G + row - xr * p.G) * p.dq_sh + half * (HD / 2);
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&jobs.empty[n & 1]));
+      more = read_job(n + 1);
       ok = wait(&bar_acc_full, units++);
       if (!ok) break;
       ptx::tc_fence_after();
@@ -892,15 +901,22 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
       return wait_warp_or_abort(ptx::smem_u32(b), phase & 1, abort_ptr, p.timeout_ns, kRoleVarDkvSoftmax);
     };
     int g = 0, units = 0;
-    for (int n = 0; ok; ++n) {
+    // What the step loop needs of a unit; the next unit's is read while the
+    // last product of this one runs.
+    int steps = 0;
+    int tok0 = 0;        // first token of the step's tile
+    int see0 = 0;        // first token of the sequence that sees this key (causal)
+    auto read_job = [&](int n) {
       ok = wait(&jobs.full[n & 1], n >> 1);
-      if (!ok) break;
       const VarBwdJob& job = jobs.job[n & 1];
-      if (job.kvh < 0 || !job.u.dkdv) break;
-      const int steps = job.u.n, nq = job.u.nq;
-      int tok0 = ((nq + p.tp - 1) / p.tp - steps) * p.tp;          // first token of step i's tile
-      // First token of the sequence that sees this key (causal).
-      const int see0 = p.causal ? job.u.blk * C::kBlk + row - (job.u.nkv - nq) : 0;
+      if (!ok || job.kvh < 0 || !job.u.dkdv) return false;
+      steps = job.u.n;
+      tok0 = ((job.u.nq + p.tp - 1) / p.tp - steps) * p.tp;
+      see0 = p.causal ? job.u.blk * C::kBlk + row - (job.u.nkv - job.u.nq) : 0;
+      return true;
+    };
+    bool more = read_job(0);
+    for (int n = 0; more; ++n) {
       for (int i = 0; i < steps; ++i, ++g, tok0 += p.tp) {
         // Columns x * G + h of this warp's 64 that see this key: from here on.
         const int from = max(0, min(see0 - tok0, p.tp)) * p.G - 64 * half;
@@ -984,14 +1000,18 @@ __device__ __forceinline__ int varlen_dkdv_loop(const CUtensorMap& tmQ, const CU
         ptx::mbar_arrive(ptx::smem_u32(&bar_p_full));
       }
       if (!ok) break;
+      const VarBwdJob& job = jobs.job[n & 1];
       const int key_row = job.u.blk * C::kBlk + row;
       const bool live = key_row < job.u.nkv;
       const long long key = static_cast<long long>(job.u.kv0) + key_row;
       __nv_bfloat16* dv = p.dV + key * p.dv_st + job.kvh * p.dv_sh + half * (HD / 2);
       __nv_bfloat16* dk = p.dK + key * p.dk_st + job.kvh * p.dk_sh + half * (HD / 2);
+      const bool any = steps > 0;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&jobs.empty[n & 1]));
-      if (steps > 0) {
+      more = read_job(n + 1);
+      if (!ok) break;
+      if (any) {
         ok = wait(&bar_acc_full, units++);
         if (!ok) break;
         ptx::tc_fence_after();
