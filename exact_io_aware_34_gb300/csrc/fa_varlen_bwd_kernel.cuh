@@ -1044,7 +1044,7 @@ __device__ __forceinline__ void varlen_bwd_tails(const VarBwdParams& p, VarBwdSh
   const int lane = threadIdx.x & 31;
   int g[2] = {0, 0}, tails[2] = {0, 0};      // steps and tail pairs so far, per role
   for (int n = 0;; ++n) {
-    if (!wait_warp_or_abort(ptx::smem_u32(&jobs.full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
+    if (!wait_idle_or_abort(ptx::smem_u32(&jobs.full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
                             kRoleVarDkvProducer))
       return;
     const int kvh = jobs.job[n & 1].kvh, dkdv = jobs.job[n & 1].u.dkdv, steps = jobs.job[n & 1].u.n;
@@ -1128,9 +1128,9 @@ __global__ void __launch_bounds__(kVarBwdThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_base_slot;
   if (warp == 10) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ unit fetch
-      // (A unit is taken when the loads of the one before near their end.)
+    // ------------------------------------------------------------ unit fetch (converged; lane 0 writes)
+    // (A unit is taken when the loads of the one before near their end.)
+    {
       const int total = p.plan->num_units * p.H_kv;
       int idx = blockIdx.x;
       for (int n = 0;; ++n) {
@@ -1148,15 +1148,18 @@ __global__ void __launch_bounds__(kVarBwdThreads, 1)
           }
           job.u = p.list[e];
         }
-        if (!wait_or_abort(ptx::smem_u32(&jobs.empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
-                           kRoleVarDqProducer))
+        if (!wait_idle_or_abort(ptx::smem_u32(&jobs.empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
+                                kRoleVarDqProducer))
           break;
-        jobs.job[n & 1] = job;
-        ptx::mbar_arrive(ptx::smem_u32(&jobs.full[n & 1]));
+        if (lane == 0) {
+          jobs.job[n & 1] = job;
+          ptx::mbar_arrive(ptx::smem_u32(&jobs.full[n & 1]));
+        }
+        __syncwarp();
         if (job.kvh < 0) break;
-        if (!ptx::mbar_test_wait(ptx::smem_u32(&jobs.claim), n & 1)) __nanosleep(1000);
-        if (!wait_or_abort(ptx::smem_u32(&jobs.claim), n & 1, abort_ptr, p.timeout_ns, kRoleVarDqProducer)) break;
-        idx = static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1);
+        if (!wait_idle_or_abort(ptx::smem_u32(&jobs.claim), n & 1, abort_ptr, p.timeout_ns, kRoleVarDqProducer)) break;
+        if (lane == 0) idx = static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1);
+        idx = __shfl_sync(0xffffffffu, idx, 0);
       }
     }
     __syncwarp();

@@ -49,6 +49,19 @@ enum : unsigned int { kRoleVarProducer = 13, kRoleVarMma = 14, kRoleVarSoftmax =
 // device memory that do not describe the caller's buffers.
 constexpr unsigned int kStatusBadOffsets = 2;
 
+// Warp-uniform bounded wait of a warp with time to spare: polls twice a
+// microsecond, so that it takes no issue slots from the warps beside it.
+__device__ __forceinline__ bool wait_idle_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                   unsigned long long timeout_ns, unsigned int role) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (!__all_sync(0xffffffffu, ptx::mbar_test_wait(bar, parity))) {
+    if (__any_sync(0xffffffffu, *abort_flag != 0 || ptx::globaltimer_ns() - t0 > timeout_ns))
+      return wait_warp_or_abort(bar, parity, abort_flag, 0, role);   // reports it
+    __nanosleep(500);
+  }
+  return true;
+}
+
 struct VarUnit {
   int q_row0;     // first token of the unit in Q / O
   int n_tok;      // tokens of the sequence from there on (may exceed the unit's 2 tp)
