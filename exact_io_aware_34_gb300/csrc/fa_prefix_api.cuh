@@ -59,6 +59,12 @@ bool make_map4(CUtensorMap* m, const Cube& c, int b_row, int b_head, int b_batch
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Places of the line at most.
+long long pre_places(const fa::PreShape& s) {
+  return static_cast<long long>(s.p_units) * (s.p_blocks + fa::kUnitCost) +
+         static_cast<long long>(s.B) * s.H_kv * s.ht * ((s.room + 127LL) / 128 + fa::kUnitCost);
+}
+
 fa::PreShape pre_shape(int B, int H, int H_kv, int N_q, int n_p, int room) {
   fa::PreShape s;
   s.B = B;
@@ -74,14 +80,12 @@ fa::PreShape pre_shape(int B, int H, int H_kv, int N_q, int n_p, int room) {
   s.bt = (B + s.bp - 1) / s.bp;
   s.p_blocks = (n_p + 127) / 128;
   s.p_units = n_p > 0 ? H_kv * s.bt * s.ht : 0;
-  const long long most = static_cast<long long>(s.p_units) * s.p_blocks +
-                         static_cast<long long>(B) * H_kv * s.ht * ((room + 127LL) / 128);
-  s.ctas = static_cast<int>(std::min(most, 2LL * device_sm_count()));
+  s.ctas = static_cast<int>(std::min(pre_places(s), 2LL * device_sm_count()));
   return s;
 }
 
 struct PreLayout {
-  size_t cum, Op, Lp, Oo, Lo, bytes;   // the line's length is at the front
+  size_t Op, Lp, Oo, Lo, bytes;   // the units' segments are at the front
 };
 
 PreLayout pre_layout(const fa::PreShape& s, int d) {
@@ -89,8 +93,7 @@ PreLayout pre_layout(const fa::PreShape& s, int d) {
   const size_t p_rows = s.p_units ? (static_cast<size_t>(s.p_units) + s.ctas) * 128 : 0;
   const size_t o_rows = (static_cast<size_t>(s.B) * s.H_kv * s.ht + s.ctas) * s.hp * s.N_q;
   PreLayout w;
-  w.cum = 128;
-  w.Op = w.cum + up(static_cast<size_t>(s.B) * 4);
+  w.Op = up((static_cast<size_t>(s.p_units) + static_cast<size_t>(s.B) * s.H_kv * s.ht) * sizeof(int2));
   w.Lp = w.Op + p_rows * d * 4;
   w.Oo = w.Lp + up(p_rows * 4);
   w.Lo = w.Oo + o_rows * d * 4;
@@ -124,7 +127,7 @@ fa_status_t prefix_launch(const Cube& q, const Cube& kp, const Cube& vp, const C
   static bool regs_ok[64];
   std::call_once(once[dev], [&] {
     attr_err[dev] =
-        cudaFuncSetAttribute(fa::fa_prefix_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        cudaFuncSetAttribute(fa::fa_prefix_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, fa::PreCfg<HD>::kSmemBytes);
     // The warpgroups' register split must fit the registers the block is
     // launched with (see the forward launch).
     cudaFuncAttributes fattr;
@@ -144,8 +147,7 @@ fa_status_t prefix_launch(const Cube& q, const Cube& kp, const Cube& vp, const C
   fa::PreParams p;
   p.s = s;
   p.lens = lens;
-  p.total = reinterpret_cast<long long*>(ws);
-  p.cum = reinterpret_cast<int*>(ws + w.cum);
+  p.seg = reinterpret_cast<int2*>(ws);
   p.Op = reinterpret_cast<float*>(ws + w.Op);
   p.Lp = reinterpret_cast<float*>(ws + w.Lp);
   p.Oo = reinterpret_cast<float*>(ws + w.Oo);
@@ -155,7 +157,7 @@ fa_status_t prefix_launch(const Cube& q, const Cube& kp, const Cube& vp, const C
   p.idesc_qk = C::kIdescQK | (scale < 0.f ? fa::ptx::kIdescNegateA : 0u);
   p.timeout_ns = timeout_ns;
   p.drop_load = drop_load;
-  fa::fa_prefix_kernel<HD><<<static_cast<unsigned>(s.ctas), C::kThreads, C::kSmemBytes, stream>>>(mqp, mqo, mkp, mvp,
+  fa::fa_prefix_kernel<HD><<<static_cast<unsigned>(s.ctas), C::kThreads, fa::PreCfg<HD>::kSmemBytes, stream>>>(mqp, mqo, mkp, mvp,
                                                                                                  mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
@@ -165,8 +167,8 @@ fa_status_t prefix_launch(const Cube& q, const Cube& kp, const Cube& vp, const C
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -201,9 +203,7 @@ fa_status_t prefix_impl(const void* Q, const void* K_prefix, const void* V_prefi
   for (const void* a : {static_cast<const void*>(LSE), static_cast<const void*>(lens)})
     if (reinterpret_cast<uintptr_t>(a) % 4 != 0) return FA_ERR_INVALID_ARG;
   const fa::PreShape s = pre_shape(B, H, H_kv, N_q, n_p, room);
-  if ((static_cast<long long>(B) * H * N_q + 7) / 8 > 0x7fffffffLL ||
-      static_cast<long long>(B) * H_kv * s.ht + s.ctas > 0x7fffffffLL)
-    return FA_ERR_UNSUPPORTED;
+  if (pre_places(s) >= (1LL << 31) - 65536) return FA_ERR_UNSUPPORTED;   // counted in 32 bits on the device
   const size_t need = pre_layout(s, d).bytes, n_lse = static_cast<size_t>(B) * H * N_q * 4;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 128 != 0 || workspace_bytes < need)
     return FA_ERR_INVALID_ARG;

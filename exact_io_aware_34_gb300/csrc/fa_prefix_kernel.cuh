@@ -14,20 +14,24 @@
 //
 // Work. A unit is one 128-row query tile and its whole key range: (K/V head,
 // tile of sequences) for the prefix, (sequence, K/V head) for the own keys.
-// All units' 128-key blocks stand in one line, and the CTAs (two per SM) take
-// equal, contiguous pieces of it. So every CTA has the same number of blocks
+// All units' 128-key blocks stand in one line, each unit's behind kUnitCost
+// empty places (what a unit costs beside its blocks), and the CTAs (two per SM)
+// take equal, contiguous pieces of it. So every CTA has about the same work
 // whatever the lengths are, which only the device knows. A piece may hold
 // several units' ends and wholes (segments); each segment leaves a float32
 // partial result (O normalised by its own l, and LSE) in the workspace, at
 // slot (unit + CTA): that number grows by one or two from one segment to the
-// next, so no two share a slot and the merge finds them without a table.
+// next, so no two share a slot, and a unit's segments have consecutive ones.
 // prefix_merge_kernel, a programmatic dependent, combines a row's segments.
 //
 // Per CTA (256 threads): warps 0-3 softmax and epilogue, warp 4 TMA producer,
 // warp 5 MMA issuer, warp 6 walks the segments one ahead and hands them to
-// the others, as in fa_varlen_fwd_kernel. The block update, the masking with
-// -inf and the clearing of V rows past a sequence's length are that kernel's;
-// register split, ring and TMEM are fa_decode_kernel's.
+// the others through a two-slot ring, warp 7 clears the V rows past a
+// sequence's length (any value may stand there, and a probability of zero does
+// not cancel an infinity): such a tile's load completes on a barrier of its
+// own, and warp 7 completes the tile's barrier in its place. The block update
+// and the masking with -inf are fa_varlen_fwd_kernel's; register split, ring
+// and TMEM are fa_decode_kernel's.
 #pragma once
 
 #include "fa_decode_kernel.cuh"
@@ -36,6 +40,10 @@
 namespace fa {
 
 enum : unsigned int { kRolePreProducer = 23, kRolePreMma = 24, kRolePreSoftmax = 25, kRolePreWalk = 26 };
+
+// Places of a unit in the line beside its blocks: a one-block unit takes about
+// three times as long as one block of a long one.
+constexpr int kUnitCost = 2;
 
 // Sizes that the attention and the merge kernel share.
 struct PreShape {
@@ -54,8 +62,7 @@ struct PreShape {
 struct PreParams {
   PreShape s;
   const int* lens;        // [B]
-  int* cum;               // [B]: own blocks (per unit) of the sequences before b
-  long long* total;       // all blocks
+  int2* seg;              // [p_units + own units]: first slot and number of a unit's segments (none for empty units)
   float* Op;              // prefix partials [p_units + ctas][128][d]
   float* Lp;              // [p_units + ctas][128]
   float* Oo;              // own partials [B * H_kv * ht + ctas][hp * N_q][d]
@@ -72,22 +79,33 @@ struct PreJob {
   int b0, kvh, h0;        // first sequence, K/V head, first query head within the group
   int j0, j1;             // key blocks
   int n_keys;             // keys of the unit
+  int rows;               // rows of the tile that hold queries
   int slot;               // of the partial result, within its array
 };
 
-// CTA c of n takes blocks [line_begin(c), line_begin(c + 1)) of a line of w.
-__device__ __forceinline__ long long line_begin(long long w, int n, int c) {
-  const long long q = w / n, r = w - q * n;
-  return c * q + (c < r ? c : r);
+// CTA c of n takes places [line_begin(c), line_begin(c + 1)) of a line of w.
+__device__ __forceinline__ int line_begin(int w, int n, int c) {
+  const int q = w / n, r = w - q * n;
+  return c * q + min(c, r);
 }
-// The CTA that takes block x.
-__device__ __forceinline__ int line_owner(long long w, int n, long long x) {
-  const long long q = w / n, r = w - q * n;
-  const long long split = r * (q + 1);
-  return static_cast<int>(x < split ? x / (q + 1) : r + (x - split) / q);
+// The CTA that takes place x.
+__device__ __forceinline__ int line_owner(int w, int n, int x) {
+  const int q = w / n, r = w - q * n;
+  const int split = r * (q + 1);
+  return x < split ? x / (q + 1) : r + (x - split) / q;
 }
 
 __device__ __forceinline__ int own_len(const PreParams& p, int b) { return max(0, min(p.s.room, p.lens[b])); }
+// Places of a unit with `len` keys.
+__device__ __forceinline__ int unit_places(int len) { return len > 0 ? kUnitCost + ((len + 127) >> 7) : 0; }
+
+template <int HD>
+struct PreCfg {
+  static constexpr int kStageBytes = 4 * 2048;      // epilogue: per softmax warp 32 rows x 16 float32 columns
+  static constexpr int kSmemBytes = DecCfg<HD>::kSmemBytes + kStageBytes;
+  // Two CTAs on an SM, with 1 KB each for the system and 1 KB for the barriers.
+  static_assert(2 * (kSmemBytes + 2048) <= 228 * 1024, "two CTAs per SM");
+};
 
 template <int HD>
 __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
@@ -106,10 +124,11 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
   __shared__ __align__(8) uint64_t bar_o_full;
   __shared__ __align__(8) uint64_t bar_job_full[2];
   __shared__ __align__(8) uint64_t bar_job_empty[2];
+  __shared__ __align__(8) uint64_t bar_tail[4];   // V tiles with rows to clear have landed
   __shared__ __align__(8) uint64_t bar_drain;
   __shared__ __align__(16) PreJob jobs[2];
-  __shared__ long long warp_sum[C::kThreads / 32];
-  __shared__ int start_b, start_cum;          // sequence of this CTA's first own block, own blocks before it
+  __shared__ int warp_sum[C::kThreads / 32];
+  __shared__ int start_b, start_cum;          // sequence of this CTA's first own place, own places (per unit) before it
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
 
@@ -120,6 +139,7 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
   const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = smem_base;
   const uint32_t sKV = smem_base + C::kTileBytes;
+  const uint32_t sStage = sKV + C::kStages * C::kTileBytes;
   uint8_t* kv_generic = smem_raw + (sKV - ptx::smem_u32(smem_raw));
 
   if (threadIdx.x == 0) {
@@ -134,8 +154,9 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
     ptx::mbar_init(ptx::smem_u32(&bar_o_full), 1);
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(ptx::smem_u32(&bar_job_full[t]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bar_job_empty[t]), 6);   // producer, issuer, four softmax warps
+      ptx::mbar_init(ptx::smem_u32(&bar_job_empty[t]), 7);   // warps 0-5 and 7
     }
+    for (int r = 0; r < 4; ++r) ptx::mbar_init(ptx::smem_u32(&bar_tail[r]), 1);
     ptx::mbar_init(ptx::smem_u32(&bar_drain), 1);
     abort_flag = 0;
     start_b = sh.B;
@@ -155,33 +176,32 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
     ptx::prefetch_tmap(&tmV);
   }
 
-  // The line's length: every CTA adds up the own blocks of all sequences.
-  long long sum = 0;
-  for (int b = threadIdx.x; b < sh.B; b += C::kThreads) sum += (own_len(p, b) + 127) >> 7;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  // The line's length: every CTA adds up the own places of all sequences.
+  int sum = 0;
+  for (int b = threadIdx.x; b < sh.B; b += C::kThreads) sum += unit_places(own_len(p, b));
+  sum = __reduce_add_sync(0xffffffffu, sum);
   if (lane == 0) warp_sum[warp] = sum;
   __syncthreads();
-  long long own_sum = 0;
+  int own_sum = 0;
 #pragma unroll
   for (int w = 0; w < C::kThreads / 32; ++w) own_sum += warp_sum[w];
   const int own_units_per_seq = sh.H_kv * sh.ht;
-  const long long p_total = static_cast<long long>(sh.p_units) * sh.p_blocks;
-  const long long total = p_total + own_sum * own_units_per_seq;
-  const long long x_begin = line_begin(total, sh.ctas, blockIdx.x);
-  const long long x_end = line_begin(total, sh.ctas, blockIdx.x + 1);
-  // Where this CTA's first own block lies (CTA 0 walks on and notes the sums
-  // for the merge, and looks for lengths that do not fit the cache).
-  const bool note = blockIdx.x == 0;
-  if (note && threadIdx.x == 0) *p.total = total;
-  if (note || x_end > p_total) {
-    const long long target = (x_begin > p_total ? x_begin - p_total : 0) / own_units_per_seq;   // in blocks per unit
-    long long base = 0;
+  const int p_places = sh.p_blocks + kUnitCost;
+  const int p_total = sh.p_units * p_places;
+  const int total = p_total + own_sum * own_units_per_seq;
+  const int x_begin = line_begin(total, sh.ctas, blockIdx.x);
+  const int x_end = line_begin(total, sh.ctas, blockIdx.x + 1);
+  // Where this CTA's first own place lies. (CTA 0 goes through all lengths and
+  // looks for ones that do not fit the cache.)
+  const bool check = blockIdx.x == 0;
+  if (check || x_end > p_total) {
+    const int target = max(0, x_begin - p_total) / own_units_per_seq;   // in places per unit
+    int base = 0;
     for (int c0 = 0; c0 < sh.B; c0 += C::kThreads) {
       const int b = c0 + threadIdx.x;
       const int raw_len = b < sh.B ? p.lens[b] : 0;
-      const int nb = (max(0, min(sh.room, raw_len)) + 127) >> 7;
-      int incl = nb;
+      const int nu = unit_places(min(sh.room, raw_len));
+      int incl = nu;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, incl, o);
@@ -190,29 +210,26 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
       __syncthreads();
       if (lane == 31) warp_sum[warp] = incl;
       __syncthreads();
-      long long before = base;
-      long long chunk = 0;
+      int before = base, chunk = 0;
+#pragma unroll
       for (int w = 0; w < C::kThreads / 32; ++w) {
         if (w < warp) before += warp_sum[w];
         chunk += warp_sum[w];
       }
-      const long long excl = before + incl - nb;
-      if (nb > 0 && excl <= target && target < excl + nb) {
+      const int excl = before + incl - nu;
+      if (nu > 0 && excl <= target && target < excl + nu) {
         start_b = b;
-        start_cum = static_cast<int>(excl);
+        start_cum = excl;
       }
-      if (note && b < sh.B) {
-        p.cum[b] = static_cast<int>(excl);
-        if (raw_len < 0 || raw_len > sh.room) {
-          if (atomicCAS(&g_status_word, 0u, kStatusBadOffsets) == 0u) {
-            g_status_info[0] = kRolePreWalk;
-            g_status_info[1] = static_cast<unsigned int>(b);
-            g_status_info[2] = g_status_info[3] = 0u;
-          }
+      if (check && (raw_len < 0 || raw_len > sh.room)) {
+        if (atomicCAS(&g_status_word, 0u, kStatusBadOffsets) == 0u) {
+          g_status_info[0] = kRolePreWalk;
+          g_status_info[1] = static_cast<unsigned int>(b);
+          g_status_info[2] = g_status_info[3] = 0u;
         }
       }
       base += chunk;
-      if (!note && base > target) break;
+      if (!check && base > target) break;
     }
   }
   ptx::tc_fence_before();
@@ -225,47 +242,59 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
   if (warp == 6) {
     // ------------------------------------------------------------ segments
     if (lane == 0) {
-      long long x = x_begin;
-      int b = start_b;
-      long long cum = start_cum;
+      int x = x_begin, b = start_b, cum = start_cum;
       for (int n = 0;; ++n) {
         PreJob job;
         job.own = -1;
-        if (x < x_end) {
+        while (x < x_end && job.own < 0) {
+          int unit, first, len;      // the unit's number among all, its first place, its keys
           if (x < p_total) {
-            const int u = static_cast<int>(x / sh.p_blocks);
-            job.own = 0;
-            job.j0 = static_cast<int>(x - static_cast<long long>(u) * sh.p_blocks);
-            job.j1 = static_cast<int>(min(static_cast<long long>(sh.p_blocks), job.j0 + (x_end - x)));
-            const int per_head = sh.bt * sh.ht;
-            job.kvh = u / per_head;
-            const int t = u - job.kvh * per_head;
-            job.b0 = t / sh.ht * sh.bp;
-            job.h0 = (t - t / sh.ht * sh.ht) * sh.hp;
-            job.n_keys = sh.n_p;
-            job.slot = u + static_cast<int>(blockIdx.x);
+            unit = x / p_places;
+            first = unit * p_places;
+            len = sh.n_p;
           } else {
-            const long long y = x - p_total;
-            int len = own_len(p, b);
-            int nb = (len + 127) >> 7;
-            while (y >= (cum + nb) * own_units_per_seq && b + 1 < sh.B) {   // on to the sequence that holds block y
-              cum += nb;
+            const int y = x - p_total;
+            len = own_len(p, b);
+            int nu = unit_places(len);
+            while (y >= (cum + nu) * own_units_per_seq && b + 1 < sh.B) {   // on to the sequence that holds place y
+              cum += nu;
               ++b;
               len = own_len(p, b);
-              nb = (len + 127) >> 7;
+              nu = unit_places(len);
             }
-            const long long in_seq = y - cum * own_units_per_seq;
-            const int u = static_cast<int>(in_seq / nb);
+            if (nu == 0) break;      // (lengths that change under the call)
+            const int u = min((y - cum * own_units_per_seq) / nu, own_units_per_seq - 1);
+            unit = sh.p_units + b * own_units_per_seq + u;
+            first = p_total + cum * own_units_per_seq + u * nu;
+          }
+          const int places = unit_places(len);
+          const int from = x - first, to = min(places, from + (x_end - x));
+          x += to - from;
+          job.j0 = max(0, from - kUnitCost);
+          job.j1 = max(0, to - kUnitCost);
+          if (job.j1 <= job.j0) continue;        // only the places beside its blocks
+          job.n_keys = len;
+          if (unit < sh.p_units) {
+            const int per_head = sh.bt * sh.ht;
+            job.own = 0;
+            job.kvh = unit / per_head;
+            const int t = unit - job.kvh * per_head, tb = t / sh.ht;
+            job.b0 = tb * sh.bp;
+            job.h0 = (t - tb * sh.ht) * sh.hp;
+            job.rows = min(sh.hp, sh.G - job.h0) * sh.N_q * min(sh.bp, sh.B - job.b0);
+            job.slot = unit + static_cast<int>(blockIdx.x);
+          } else {
+            const int u = unit - sh.p_units - b * own_units_per_seq;
             job.own = 1;
-            job.j0 = static_cast<int>(in_seq - static_cast<long long>(u) * nb);
-            job.j1 = static_cast<int>(min(static_cast<long long>(nb), job.j0 + (x_end - x)));
             job.b0 = b;
             job.kvh = u / sh.ht;
             job.h0 = (u - job.kvh * sh.ht) * sh.hp;
-            job.n_keys = len;
-            job.slot = b * own_units_per_seq + u + static_cast<int>(blockIdx.x);
+            job.rows = min(sh.hp, sh.G - job.h0) * sh.N_q;
+            job.slot = unit - sh.p_units + static_cast<int>(blockIdx.x);
           }
-          x += job.j1 - job.j0;
+          if (job.j0 == 0)
+            p.seg[unit] = make_int2(job.slot, line_owner(total, sh.ctas, first + places - 1) -
+                                                  static_cast<int>(blockIdx.x) + 1);
         }
         if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
                            kRolePreWalk))
@@ -276,13 +305,42 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
       }
     }
     __syncwarp();
+  } else if (warp == 7) {
+    // ------------------------------------------------------------ tails of V tiles
+    bool ok = true;
+    int it0 = 0, tails = 0;
+    for (int n = 0; ok; ++n) {
+      ok = wait_idle_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns, kRolePreWalk);
+      if (!ok) break;
+      const int own = jobs[n & 1].own, blocks = jobs[n & 1].j1 - jobs[n & 1].j0;
+      const int have = jobs[n & 1].n_keys - (jobs[n & 1].j1 - 1) * C::kBN;    // keys in the segment's last block
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
+      if (own < 0) break;
+      it0 += 2 * blocks;
+      if (!own || have >= C::kBN) continue;    // (behind the prefix, TMA fills with zeros)
+      ok = wait_warp_or_abort(ptx::smem_u32(&bar_tail[tails & 3]), (tails >> 2) & 1, abort_ptr, p.timeout_ns,
+                              kRolePreWalk);
+      if (!ok) break;
+      ++tails;
+      // Whole 128-byte rows, so the swizzle does not matter.
+      const int slot = (it0 - 1) % C::kStages;
+      for (int c = 0; c < C::kChunks; ++c)
+        for (int i = lane; i < (C::kBN - have) * 8; i += 32)
+          reinterpret_cast<uint4*>(kv_generic + slot * C::kTileBytes + c * C::kChunkBytes + have * 128)[i] =
+              make_uint4(0u, 0u, 0u, 0u);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_kv_full[slot]));
+    }
+    __syncwarp();
   } else if (warp == 4) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
       const uint64_t pol_first = ptx::policy_evict_first();
       const uint64_t pol_last = ptx::policy_evict_last();    // prefix tiles are read by every tile of sequences
       const uint32_t q_full = ptx::smem_u32(&bar_q_full);
-      int it = 0, q_issued = 0;
+      int it = 0, q_issued = 0, tails = 0;
       bool ok = true;
       for (int n = 0; ok; ++n) {
         ok = wait_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
@@ -316,7 +374,9 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
             }
             const int me = it++;
             if (me == p.drop_load) continue;   // test hook: this tile never arrives
-            const uint32_t full = ptx::smem_u32(&bar_kv_full[slot]);
+            // A V tile with rows past the length: warp 7 completes its barrier.
+            const bool tail = kv && job.own && (j + 1) * C::kBN > job.n_keys;
+            const uint32_t full = ptx::smem_u32(tail ? &bar_tail[tails++ & 3] : &bar_kv_full[slot]);
             ptx::mbar_arrive_expect_tx(full, C::kTileBytes);
             for (int c = 0; c < C::kChunks; ++c)
               ptx::tma_load_4d(sKV + slot * C::kTileBytes + c * C::kChunkBytes, maps[kv], full, c * 64, j * C::kBN,
@@ -326,6 +386,8 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
       }
       if (!ok || *abort_ptr) {
         if (q_issued > 0) drain_wait(q_full, (q_issued - 1) & 1, p.timeout_ns);
+        for (int r = max(0, tails - 4); r < tails; ++r)
+          drain_wait(ptx::smem_u32(&bar_tail[r & 3]), (r >> 2) & 1, p.timeout_ns);
         for (int i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
           if (i != p.drop_load)
             drain_wait(ptx::smem_u32(&bar_kv_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
@@ -397,10 +459,10 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
     const uint32_t tO = tmem_base + lane_addr + C::kColO;
     const float sl2 = p.scale_log2;
     // Row of a tile: (sequence * hp + head) * N_q + new token.
-    const int per_seq = sh.hp * sh.N_q;
-    const int bi = row / per_seq, hi = (row - bi * per_seq) / sh.N_q, qi = row - bi * per_seq - hi * sh.N_q;
+    const int qi = row % sh.N_q;
+    const uint32_t stage = sStage + static_cast<uint32_t>(warp) * 2048u;
     bool ok = true;
-    int it0 = 0, g = 0;
+    int g = 0;
     for (int n = 0; ok; ++n) {
       ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
                               kRolePreSoftmax);
@@ -410,32 +472,34 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
       if (job.own < 0) break;
       const int limit = job.own && p.causal ? max(0, job.n_keys - (sh.N_q - 1 - qi)) : job.n_keys;
-      const bool live = bi < (job.own ? 1 : min(sh.bp, sh.B - job.b0)) && hi < min(sh.hp, sh.G - job.h0);
-      const bool active = __any_sync(0xffffffffu, live);   // a warp without query rows only keeps the hand-offs going
+      const bool active = warp * 32 < job.rows;   // a warp without query rows only keeps the hand-offs going
       float m_use = -INFINITY, l = 0.f, lo = 0.f;
       for (int j = job.j0; j < job.j1; ++j, ++g) {
         ok = wait_warp_or_abort(ptx::smem_u32(&bar_s_full), g & 1, abort_ptr, p.timeout_ns, kRolePreSoftmax);
         if (!ok) break;
-        // V rows past the length (any value may stand there) are cleared
-        // before P V. Q K^T of this block was issued behind the previous P V,
-        // which had waited for its V, so this wait is for the next phase.
-        const int have = job.n_keys - j * C::kBN;
-        if (have < C::kBN) {
-          const int itV = it0 + 2 * (j - job.j0) + 1;
-          ok = wait_warp_or_abort(ptx::smem_u32(&bar_kv_full[itV % C::kStages]), (itV / C::kStages) & 1, abort_ptr,
-                                  p.timeout_ns, kRolePreSoftmax);
-          if (!ok) break;
-          uint8_t* v_tile = kv_generic + (itV % C::kStages) * C::kTileBytes;
-          for (int c = 0; c < C::kChunks; ++c)
-            for (int i = row; i < (C::kBN - have) * 8; i += C::kBM)
-              reinterpret_cast<uint4*>(v_tile + c * C::kChunkBytes + have * 128)[i] = make_uint4(0u, 0u, 0u, 0u);
-          ptx::fence_proxy_async_smem();
-        }
         if (!active) {
           ptx::mbar_arrive(ptx::smem_u32(&bar_p_full));
           continue;
         }
         ptx::tc_fence_after();
+        const int valid = limit - j * C::kBN;
+        // Scores past a row's limit become -inf in TMEM, in a short loop (see fa_varlen_fwd_kernel).
+        if (!__all_sync(0xffffffffu, valid >= C::kBN)) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const int v = valid - 32 * c;
+            if (__all_sync(0xffffffffu, v >= 32)) continue;
+            uint32_t r[32];
+            ptx::tmem_ld32(tS + 32 * c, r);
+            ptx::tmem_ld_wait();
+            ptx::reg_fence32(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i >= v) r[i] = __float_as_uint(-INFINITY);
+            ptx::tmem_st32(tS + 32 * c, r);
+          }
+          ptx::tmem_st_wait();
+        }
         uint32_t s[4][32];
         float mr[4];
 #pragma unroll
@@ -446,27 +510,7 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
           ptx::reg_fence32(s[c]);
           ptx::reg_fence1(mr[c]);
         }
-        const int valid = limit - j * C::kBN;
-        float mt;
-        if (__all_sync(0xffffffffu, valid >= C::kBN)) {
-          mt = ptx::max3(mr[0], mr[1], fmaxf(mr[2], mr[3]));
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= valid) s[c][i] = __float_as_uint(-INFINITY);
-          float mc[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int c = k >> 1, bb = (k & 1) * 16;
-            mc[k] = fmaxf(__uint_as_float(s[c][bb]), __uint_as_float(s[c][bb + 1]));
-#pragma unroll
-            for (int i = 2; i < 16; i += 2)
-              mc[k] = ptx::max3(mc[k], __uint_as_float(s[c][bb + i]), __uint_as_float(s[c][bb + i + 1]));
-          }
-          mt = ptx::max3(ptx::max3(mc[0], mc[1], mc[2]), ptx::max3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
-        }
+        const float mt = ptx::max3(mr[0], mr[1], fmaxf(mr[2], mr[3]));
         float alpha = 1.f;
         bool rescale_o = false;
         if (j == job.j0) {
@@ -530,28 +574,49 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
       if (ok) ok = wait_warp_or_abort(ptx::smem_u32(&bar_o_full), n & 1, abort_ptr, p.timeout_ns, kRolePreSoftmax);
       if (!ok) break;
       ptx::tc_fence_after();
-      it0 += 2 * (job.j1 - job.j0);
       if (active) {
         const bool none = l == 0.f;            // this row sees none of the segment's keys
         const float inv_l = none ? 0.f : 1.f / lo;
-        const int rows = job.own ? per_seq : C::kBM;
-        const size_t at = static_cast<size_t>(job.slot) * rows + row;
-        float* dst_o = (job.own ? p.Oo : p.Op) + at * HD;
-#pragma unroll
+        const int per_slot = job.own ? sh.hp * sh.N_q : C::kBM;
+        const size_t at = static_cast<size_t>(job.slot) * per_slot + warp * 32;   // the warp's first row
+        float* dst = (job.own ? p.Oo : p.Op) + at * HD + 4 * (lane & 3);
+        const int rows = min(32, job.rows - warp * 32);
+        if (lane < rows)
+          (job.own ? p.Lo : p.Lp)[at + lane] = none ? -INFINITY : (m_use * sl2 + __log2f(l)) * 0.69314718055994530942f;
+        // O leaves through shared memory in 16-column pieces (16-byte units
+        // swizzled by row), so that four lanes write 64 bytes of a row.
+#pragma unroll 1
         for (int c = 0; c < HD / 32; ++c) {
           uint32_t o[32];
           ptx::tmem_ld32(tO + 32 * c, o);
           ptx::tmem_ld_wait();
           ptx::reg_fence32(o);
-          if (!live) continue;
-          float4* dst = reinterpret_cast<float4*>(dst_o + 32 * c);
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
-                                 __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
+          for (int k = 0; k < 2; ++k) {
+            __syncwarp();       // the piece before has been read
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const uint32_t addr = stage + static_cast<uint32_t>(lane) * 64u + ((v ^ ((lane >> 1) & 3u)) << 4);
+              const uint32_t* src = o + 16 * k + 4 * v;
+              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(__uint_as_float(src[0]) * inv_l),
+                           "f"(__uint_as_float(src[1]) * inv_l), "f"(__uint_as_float(src[2]) * inv_l),
+                           "f"(__uint_as_float(src[3]) * inv_l)
+                           : "memory");
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int r0 = 0; r0 < rows; r0 += 8) {
+              const int r = r0 + (lane >> 2);
+              float4 w;
+              const uint32_t addr = stage + static_cast<uint32_t>(r) * 64u + (((lane ^ (r >> 1)) & 3u) << 4);
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(w.x), "=f"(w.y), "=f"(w.z), "=f"(w.w)
+                           : "r"(addr)
+                           : "memory");
+              if (r < rows) *reinterpret_cast<float4*>(dst + static_cast<size_t>(r) * HD + 32 * c + 16 * k) = w;
+            }
+          }
         }
-        if (live)
-          (job.own ? p.Lo : p.Lp)[at] = none ? -INFINITY : (m_use * sl2 + __log2f(l)) * 0.69314718055994530942f;
       }
     }
   }
@@ -569,47 +634,40 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
 // One warp per query row: its segments' partial results over the prefix and
 // over the own keys, combined by LSE = m + ln sum_s e^{LSE_s - m},
 // O = sum_s e^{LSE_s - LSE} O_s and rounded once to bf16. The lanes read the
-// segments' LSE in parallel and pass the weights by shuffles.
+// segments' LSE in parallel (32 at a time) and pass the weights by shuffles;
+// eight segments' rows are requested before the first is used.
 template <int HD>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(128)
     prefix_merge_kernel(const PreParams p, __nv_bfloat16* __restrict__ O, float* __restrict__ LSE, long long o_sb,
                         long long o_sh, long long o_sn) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kPer = HD / 32;     // output elements per lane: 4 or 2
   const PreShape& sh = p.s;
-  const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const unsigned row = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  if (row >= static_cast<long long>(sh.B) * sh.H * sh.N_q) return;
   const int i = static_cast<int>(row % sh.N_q);
-  const long long bh = row / sh.N_q;
-  const int h = static_cast<int>(bh % sh.H), b = static_cast<int>(bh / sh.H);
-  const int kvh = h / sh.G, hg = h - kvh * sh.G, t = hg / sh.hp, hi = hg - t * sh.hp;
+  const unsigned bh = row / sh.N_q;
+  const int b = static_cast<int>(bh / sh.H), h = static_cast<int>(bh - static_cast<unsigned>(b) * sh.H);
+  const int kvh = h / sh.G, hg = h - kvh * sh.G, t = hg / sh.hp, in_tile = (hg - t * sh.hp) * sh.N_q + i;
   const int per_seq = sh.hp * sh.N_q;
-  const long long total = *p.total, p_total = static_cast<long long>(sh.p_units) * sh.p_blocks;
-  // Prefix segments [0, n0), own segments [n0, n0 + n1): consecutive slots, one row of each.
-  int n0 = 0, n1 = 0;
-  size_t row0 = 0, row1 = 0;
-  if (sh.p_units > 0) {
-    const int u = (kvh * sh.bt + b / sh.bp) * sh.ht + t;
-    const long long x = static_cast<long long>(u) * sh.p_blocks;
-    const int c = line_owner(total, sh.ctas, x);
-    n0 = line_owner(total, sh.ctas, x + sh.p_blocks - 1) - c + 1;
-    row0 = static_cast<size_t>(u + c) * 128 + (b % sh.bp) * per_seq + hi * sh.N_q + i;
-  }
-  const int nb = (own_len(p, b) + 127) >> 7;
-  if (nb > 0) {
-    const int per = sh.H_kv * sh.ht, u = kvh * sh.ht + t;
-    const long long x = p_total + static_cast<long long>(p.cum[b]) * per + static_cast<long long>(u) * nb;
-    const int c = line_owner(total, sh.ctas, x);
-    n1 = line_owner(total, sh.ctas, x + nb - 1) - c + 1;
-    row1 = (static_cast<size_t>(b) * per + u + c) * per_seq + hi * sh.N_q + i;
-  }
-  const int n = n0 + n1;
+  const int tb = b / sh.bp;
+  const int u0 = (kvh * sh.bt + tb) * sh.ht + t, u1 = sh.p_units + (b * sh.H_kv + kvh) * sh.ht + t;
+  if (b >= sh.B) return;
+  const int len = own_len(p, b);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Prefix segments [0, n0), own segments [n0, n): consecutive slots, one row of each.
+  int2 s0 = make_int2(0, 0), s1 = make_int2(0, 0);
+  if (sh.p_units > 0) s0 = p.seg[u0];
+  if (len > 0) s1 = p.seg[u1];
+  const int n0 = s0.y, n = s0.y + s1.y;
+  const size_t row0 = static_cast<size_t>(s0.x) * 128 + (b - tb * sh.bp) * per_seq + in_tile;
+  const size_t row1 = static_cast<size_t>(s1.x) * per_seq + in_tile;
   auto lse_of = [&](int s) {
     return s < n0 ? p.Lp[row0 + static_cast<size_t>(s) * 128] : p.Lo[row1 + static_cast<size_t>(s - n0) * per_seq];
   };
-  float m = -INFINITY;
-  bool any = false;                      // a segment whose keys this row sees (a NaN counts, and comes through)
-  for (int s = lane; s < n; s += 32) {
+  const float first = lane < n ? lse_of(lane) : -INFINITY;
+  float m = first;
+  bool any = first != -INFINITY;         // a segment whose keys this row sees (a NaN counts, and comes through)
+  for (int s = 32 + lane; s < n; s += 32) {
     const float v = lse_of(s);
     any |= v != -INFINITY;
     m = fmaxf(m, v);
@@ -618,34 +676,50 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (m == -INFINITY) m = 0.f;
-  constexpr int kPer = HD / 32;     // output elements per lane: 4 or 2
   float acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
   float sum = 0.f;
   if (!none) {
-    for (int s0 = 0; s0 < n; s0 += 32) {
-      const float w_me = s0 + lane < n ? __expf(lse_of(s0 + lane) - m) : 0.f;
+    for (int g0 = 0; g0 < n; g0 += 32) {
+      const float mine = g0 == 0 ? first : g0 + lane < n ? lse_of(g0 + lane) : -INFINITY;
+      const float w_me = __expf(mine - m);
       sum += w_me;
-      const int cnt = min(32, n - s0);
-#pragma unroll 4
-      for (int k = 0; k < cnt; ++k) {
-        const float w = __shfl_sync(0xffffffffu, w_me, k);
-        const int s = s0 + k;
-        const float* src = (s < n0 ? p.Op + (row0 + static_cast<size_t>(s) * 128) * HD
-                                   : p.Oo + (row1 + static_cast<size_t>(s - n0) * per_seq) * HD) + lane * kPer;
+      for (int k0 = 0; k0 < min(32, n - g0); k0 += 8) {
+        float v[8][kPer];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+        for (int k = 0; k < 8; ++k) {
+          const int s = min(g0 + k0 + k, n - 1);       // (past the end: the last again, with weight 0)
+          const float* src = (s < n0 ? p.Op + (row0 + static_cast<size_t>(s) * 128) * HD
+                                     : p.Oo + (row1 + static_cast<size_t>(s - n0) * per_seq) * HD) + lane * kPer;
+          if constexpr (kPer == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(src);
+            v[k][0] = f.x, v[k][1] = f.y, v[k][2] = f.z, v[k][3] = f.w;
+          } else {
+            const float2 f = *reinterpret_cast<const float2*>(src);
+            v[k][0] = f.x, v[k][1] = f.y;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float w = __shfl_sync(0xffffffffu, w_me, k0 + k);
+          if (g0 + k0 + k < n) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+          }
+        }
       }
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float inv = none ? 0.f : 1.f / sum;
-  __nv_bfloat16* dst = O + b * o_sb + h * o_sh + i * o_sn + lane * kPer;
+  uint32_t packed[kPer / 2];
 #pragma unroll
-  for (int e = 0; e < kPer; e += 2)
-    *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+  for (int e = 0; e < kPer; e += 2) packed[e / 2] = ptx::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  __nv_bfloat16* dst = O + b * o_sb + h * o_sh + i * o_sn + lane * kPer;
+  if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
+  else *reinterpret_cast<uint32_t*>(dst) = packed[0];
   if (lane == 0) LSE[row] = none ? -INFINITY : m + __logf(sum);
 }
 

@@ -547,8 +547,9 @@ size_t fa_fwd_prefix_workspace_bytes(int B, int H, int H_kv, int N_q, int N_pref
  * Limits: B, H <= 65535; B * H * N_q, B * H_kv * N_own and H_kv * N_prefix below
  * 2^31; d in {64, 128}; scale finite. Pointers 16-byte, LSE and seq_lens 4-byte
  * aligned; O, LSE and the workspace overlap no input nor each other (judged by
- * first and last byte). FA_ERR_UNSUPPORTED for other d, N_q > 128 or
- * H / H_kv > 128, FA_ERR_INVALID_ARG for the rest.
+ * first and last byte). FA_ERR_UNSUPPORTED for other d, N_q > 128,
+ * H / H_kv > 128 or more than about 2^31 blocks of 128 keys in all,
+ * FA_ERR_INVALID_ARG for the rest.
  */
 fa_status_t fa_fwd_prefix(const void* Q, const void* K_prefix, const void* V_prefix, const void* K, const void* V,
                           const int* seq_lens, void* O, float* LSE,
