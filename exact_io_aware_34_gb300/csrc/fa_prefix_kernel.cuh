@@ -246,8 +246,9 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
       for (int n = 0;; ++n) {
         PreJob job;
         job.own = -1;
+        int unit = 0, end = 0;       // the unit's number among all, its last place
         while (x < x_end && job.own < 0) {
-          int unit, first, len;      // the unit's number among all, its first place, its keys
+          int first, len;            // its first place, its keys
           if (x < p_total) {
             unit = x / p_places;
             first = unit * p_places;
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
           const int places = unit_places(len);
           const int from = x - first, to = min(places, from + (x_end - x));
           x += to - from;
+          end = first + places - 1;
           job.j0 = max(0, from - kUnitCost);
           job.j1 = max(0, to - kUnitCost);
           if (job.j1 <= job.j0) continue;        // only the places beside its blocks
@@ -292,9 +294,6 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
             job.rows = min(sh.hp, sh.G - job.h0) * sh.N_q;
             job.slot = unit - sh.p_units + static_cast<int>(blockIdx.x);
           }
-          if (job.j0 == 0)
-            p.seg[unit] = make_int2(job.slot, line_owner(total, sh.ctas, first + places - 1) -
-                                                  static_cast<int>(blockIdx.x) + 1);
         }
         if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
                            kRolePreWalk))
@@ -302,6 +301,9 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
         jobs[n & 1] = job;
         ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
         if (job.own < 0) break;
+        // The CTA with a unit's first block notes its segments for the merge.
+        if (job.j0 == 0)
+          p.seg[unit] = make_int2(job.slot, line_owner(total, sh.ctas, end) - static_cast<int>(blockIdx.x) + 1);
       }
     }
     __syncwarp();
@@ -579,18 +581,29 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
         const float inv_l = none ? 0.f : 1.f / lo;
         const int per_slot = job.own ? sh.hp * sh.N_q : C::kBM;
         const size_t at = static_cast<size_t>(job.slot) * per_slot + warp * 32;   // the warp's first row
-        float* dst = (job.own ? p.Oo : p.Op) + at * HD + 4 * (lane & 3);
+        float* dst = (job.own ? p.Oo : p.Op) + at * HD;
         const int rows = min(32, job.rows - warp * 32);
         if (lane < rows)
           (job.own ? p.Lo : p.Lp)[at + lane] = none ? -INFINITY : (m_use * sl2 + __log2f(l)) * 0.69314718055994530942f;
-        // O leaves through shared memory in 16-column pieces (16-byte units
-        // swizzled by row), so that four lanes write 64 bytes of a row.
+        // A few rows are written as they are; more leave through shared memory
+        // in 16-column pieces (16-byte units swizzled by row), so that four
+        // lanes write 64 bytes of a row.
 #pragma unroll 1
         for (int c = 0; c < HD / 32; ++c) {
           uint32_t o[32];
           ptx::tmem_ld32(tO + 32 * c, o);
           ptx::tmem_ld_wait();
           ptx::reg_fence32(o);
+          if (rows <= 8) {
+            if (lane < rows) {
+              float4* row_dst = reinterpret_cast<float4*>(dst + static_cast<size_t>(lane) * HD + 32 * c);
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                row_dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
+                                         __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
+            }
+            continue;
+          }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             __syncwarp();       // the piece before has been read
@@ -604,16 +617,21 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
                            : "memory");
             }
             __syncwarp();
-#pragma unroll 1
-            for (int r0 = 0; r0 < rows; r0 += 8) {
-              const int r = r0 + (lane >> 2);
-              float4 w;
+            float4 w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int r = 8 * q + (lane >> 2);
               const uint32_t addr = stage + static_cast<uint32_t>(r) * 64u + (((lane ^ (r >> 1)) & 3u) << 4);
               asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                           : "=f"(w.x), "=f"(w.y), "=f"(w.z), "=f"(w.w)
+                           : "=f"(w[q].x), "=f"(w[q].y), "=f"(w[q].z), "=f"(w[q].w)
                            : "r"(addr)
                            : "memory");
-              if (r < rows) *reinterpret_cast<float4*>(dst + static_cast<size_t>(r) * HD + 32 * c + 16 * k) = w;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int r = 8 * q + (lane >> 2);
+              if (r < rows)
+                *reinterpret_cast<float4*>(dst + static_cast<size_t>(r) * HD + 32 * c + 16 * k + 4 * (lane & 3)) = w[q];
             }
           }
         }
