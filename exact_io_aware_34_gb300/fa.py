@@ -47,10 +47,6 @@ class BatchStrides(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_longlong), ("head", ctypes.c_longlong), ("row", ctypes.c_longlong)]
 
 
-# Strides as the C ABI's arrays of fa_strides_t / fa_batch_strides_t, flat.
-_LL8, _LL16, _LL18 = (ctypes.c_longlong * n for n in (8, 16, 18))
-
-
 class FaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -491,14 +487,32 @@ def fa_bwd(q, k, v, o, do, lse, dq=None, dk=None, dv=None, scale: float | None =
     return tuple(outs)
 
 
-def _strided(name, t, device, shape):
-    """Strides of a bf16 tensor of this shape on this device whose last dimension is contiguous."""
+def _bf16(name, t, device, shape):
+    """Checks a bf16 tensor of this shape on this device whose last dimension is
+    contiguous; whether it is contiguous as a whole."""
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on {device}")
-    s = t.stride()
-    if s[-1] != 1:
+    if t.is_contiguous():
+        return True
+    if t.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return s[:-1]
+    return False
+
+
+def _strides(dense, *tensors):
+    """The C ABI's array of strides, or None (all contiguous). None among the
+    tensors: a prefix that is not there; a prefix has no batch stride."""
+    if dense:
+        return None
+    flat = []
+    for t in tensors:
+        if t is None:
+            flat += (0, 0, 0)
+        else:
+            if t.dim() == 3 and tensors[0].dim() == 4:
+                flat.append(0)
+            flat += t.stride()[:-1]
+    return (ctypes.c_longlong * len(flat))(*flat)
 
 
 def _leading(name, t, dims):
@@ -523,11 +537,28 @@ def _out_lse(lse, shape, device):
     return lse
 
 
-def _out_bf16(name, t, device, shape):
-    """(tensor, strides) of an output, allocated when not given."""
+def _out_bf16(name, t, device, shape, like=None):
+    """(tensor, whether it is contiguous) of an output, allocated when not given
+    (like a contiguous tensor of its shape, which is quicker)."""
     if t is None:
-        t = torch.empty(shape, dtype=torch.bfloat16, device=device)
-    return t, _strided(name, t, device, shape)
+        if like is not None and like.is_contiguous():
+            return torch.empty_like(like), True
+        return torch.empty(shape, dtype=torch.bfloat16, device=device), True
+    return t, _bf16(name, t, device, shape)
+
+
+#: workspace sizes by (function, device, sizes); small calls are bound by the host
+_need_of: dict = {}
+
+
+def _need(name, device, *sizes):
+    key = (name, device.index, *sizes)
+    need = _need_of.get(key)
+    if need is None:
+        if len(_need_of) > 4096:
+            _need_of.clear()
+        need = _need_of[key] = getattr(load_library(), name)(*sizes)
+    return need
 
 
 def _workspace(workspace, need, device):
@@ -574,21 +605,20 @@ def fa_fwd_varlen(q, k, v, cu_q, cu_kv, o=None, lse=None, scale: float | None = 
     written and :func:`fa_get_device_status` says so. Returns (o bf16 [T_q, H, d], lse float32 [H, T_q]).
     """
     device, T_q, H, T_kv, H_kv, d, B = _packed_sizes(q, k, cu_q)
-    q_st = _strided("q", q, device, (T_q, H, d))
-    k_st = _strided("k", k, device, (T_kv, H_kv, d))
-    v_st = _strided("v", v, device, (T_kv, H_kv, d))
+    rows, keys = (T_q, H, d), (T_kv, H_kv, d)
+    dense = _bf16("q", q, device, rows) & _bf16("k", k, device, keys) & _bf16("v", v, device, keys)
     _int32("cu_q", cu_q, device, B + 1)
     _int32("cu_kv", cu_kv, device, B + 1)
-    lib = load_library()
 
     def run():
-        out, o_st = _out_bf16("o", o, device, (T_q, H, d))
+        out, out_dense = _out_bf16("o", o, device, rows, q)
         out_lse = _out_lse(lse, (H, T_q), device)
-        ws, ws_ptr, ws_bytes = _workspace(workspace, lib.fa_fwd_varlen_workspace_bytes(B, H, H_kv, T_q), device)
-        st = lib.fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), out_lse.data_ptr(),
-                               cu_q.data_ptr(), cu_kv.data_ptr(), B, H, H_kv, T_q, T_kv, d,
-                               _LL8(*q_st, *k_st, *v_st, *o_st), d ** -0.5 if scale is None else scale, bool(causal),
-                               ws_ptr, ws_bytes, _raw_stream(device))
+        need = _need("fa_fwd_varlen_workspace_bytes", device, B, H, H_kv, T_q)
+        ws, ws_ptr, ws_bytes = _workspace(workspace, need, device)
+        st = load_library().fa_fwd_varlen(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), out_lse.data_ptr(), cu_q.data_ptr(),
+            cu_kv.data_ptr(), B, H, H_kv, T_q, T_kv, d, _strides(dense and out_dense, q, k, v, out),
+            d ** -0.5 if scale is None else scale, bool(causal), ws_ptr, ws_bytes, _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_fwd_varlen")
         return out, out_lse
@@ -621,25 +651,25 @@ def fa_bwd_varlen(q, k, v, o, do, lse, cu_q, cu_kv, dq=None, dk=None, dv=None, s
     as for the forward. Rows and keys of no sequence are not written."""
     device, T_q, H, T_kv, H_kv, d, B = _packed_sizes(q, k, cu_q)
     rows, keys = (T_q, H, d), (T_kv, H_kv, d)
-    inputs = (*_strided("q", q, device, rows), *_strided("k", k, device, keys), *_strided("v", v, device, keys),
-              *_strided("o", o, device, rows), *_strided("do", do, device, rows))
+    dense = (_bf16("q", q, device, rows) & _bf16("k", k, device, keys) & _bf16("v", v, device, keys)
+             & _bf16("o", o, device, rows) & _bf16("do", do, device, rows))
     if not isinstance(lse, torch.Tensor):
         raise ValueError("lse must be a tensor")
     _out_lse(lse, (H, T_q), device)
     _int32("cu_q", cu_q, device, B + 1)
     _int32("cu_kv", cu_kv, device, B + 1)
-    lib = load_library()
 
     def run():
-        gq, gq_st = _out_bf16("dq", dq, device, rows)
-        gk, gk_st = _out_bf16("dk", dk, device, keys)
-        gv, gv_st = _out_bf16("dv", dv, device, keys)
-        ws, ws_ptr, ws_bytes = _workspace(workspace, lib.fa_bwd_varlen_workspace_bytes(B, H, H_kv, T_q, T_kv), device)
-        st = lib.fa_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(),
-                               gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), cu_q.data_ptr(), cu_kv.data_ptr(), B, H,
-                               H_kv, T_q, T_kv, d, _LL16(*inputs, *gq_st, *gk_st, *gv_st),
-                               d ** -0.5 if scale is None else scale, bool(causal), ws_ptr, ws_bytes,
-                               _raw_stream(device))
+        gq, q_dense = _out_bf16("dq", dq, device, rows, o)
+        gk, k_dense = _out_bf16("dk", dk, device, keys, k)
+        gv, v_dense = _out_bf16("dv", dv, device, keys, v)
+        need = _need("fa_bwd_varlen_workspace_bytes", device, B, H, H_kv, T_q, T_kv)
+        ws, ws_ptr, ws_bytes = _workspace(workspace, need, device)
+        st = load_library().fa_bwd_varlen(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(), gq.data_ptr(),
+            gk.data_ptr(), gv.data_ptr(), cu_q.data_ptr(), cu_kv.data_ptr(), B, H, H_kv, T_q, T_kv, d,
+            _strides(dense and q_dense and k_dense and v_dense, q, k, v, o, do, gq, gk, gv),
+            d ** -0.5 if scale is None else scale, bool(causal), ws_ptr, ws_bytes, _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_bwd_varlen")
         return gq, gk, gv
@@ -679,32 +709,30 @@ def fa_fwd_prefix(q, k_prefix, v_prefix, k, v, seq_lens, o=None, lse=None, scale
     j < seq_lens[b] - (N_q - 1 - i). A row that sees no key gets o = 0 and
     lse = -inf. Returns (o bf16 [B, H, N_q, d], lse float32 [B, H, N_q]).
     """
-    B, H, N_q, d = rows = tuple(_leading("q", q, 4))
+    rows = _leading("q", q, 4)
+    B, H, N_q, d = rows
     _, H_kv, N_own, _ = _leading("k", k, 4)
     device, cache = q.device, (B, H_kv, N_own, d)
-    q_st = _strided("q", q, device, rows)
-    k_st = _strided("k", k, device, cache)
-    v_st = _strided("v", v, device, cache)
+    dense = _bf16("q", q, device, rows) & _bf16("k", k, device, cache) & _bf16("v", v, device, cache)
     if (k_prefix is None) != (v_prefix is None):
         raise ValueError("k_prefix and v_prefix come together")
-    N_prefix, p_st, p_ptr = 0, (0,) * 6, (None, None)
+    N_prefix, p_ptr = 0, (None, None)
     if k_prefix is not None:
         N_prefix = _leading("k_prefix", k_prefix, 3)[1]
         shared = (H_kv, N_prefix, d)
-        p_st = (0, *_strided("k_prefix", k_prefix, device, shared), 0, *_strided("v_prefix", v_prefix, device, shared))
+        dense &= _bf16("k_prefix", k_prefix, device, shared) & _bf16("v_prefix", v_prefix, device, shared)
         p_ptr = k_prefix.data_ptr(), v_prefix.data_ptr()
     _int32("seq_lens", seq_lens, device, B)
-    lib = load_library()
 
     def run():
-        out, o_st = _out_bf16("o", o, device, rows)
+        out, out_dense = _out_bf16("o", o, device, rows, q)
         out_lse = _out_lse(lse, (B, H, N_q), device)
-        ws, ws_ptr, ws_bytes = _workspace(workspace, lib.fa_fwd_prefix_workspace_bytes(B, H, H_kv, N_q, N_prefix, N_own, d),
-                                  device)
-        st = lib.fa_fwd_prefix(q.data_ptr(), *p_ptr, k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
-                               out_lse.data_ptr(), B, H, H_kv, N_q, N_prefix, N_own, d,
-                               _LL18(*q_st, *p_st, *k_st, *v_st, *o_st), d ** -0.5 if scale is None else scale,
-                               bool(causal), ws_ptr, ws_bytes, _raw_stream(device))
+        need = _need("fa_fwd_prefix_workspace_bytes", device, B, H, H_kv, N_q, N_prefix, N_own, d)
+        ws, ws_ptr, ws_bytes = _workspace(workspace, need, device)
+        st = load_library().fa_fwd_prefix(
+            q.data_ptr(), *p_ptr, k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), out_lse.data_ptr(),
+            B, H, H_kv, N_q, N_prefix, N_own, d, _strides(dense and out_dense, q, k_prefix, v_prefix, k, v, out),
+            d ** -0.5 if scale is None else scale, bool(causal), ws_ptr, ws_bytes, _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_fwd_prefix")
         return out, out_lse
