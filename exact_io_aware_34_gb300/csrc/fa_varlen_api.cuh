@@ -99,8 +99,19 @@ bool varlen_fwd_direct(int B, int H, int H_kv, int T_q) {
   return varlen_fwd_cap(B, H, H_kv, T_q) * H_kv <= device_sm_count();
 }
 
-size_t varlen_fwd_ws(int B, int H, int H_kv, int T_q) {
-  if (varlen_fwd_direct(B, H, H_kv, T_q)) return 0;
+// CTAs among which the keys of all units are split, or 0 (see split_line): at
+// most one per kSplitMin places of the longest line these sizes allow.
+int varlen_fwd_pieces(int B, int H, int H_kv, int T_q, int T_kv) {
+  if (T_kv <= fa::kSplitKeys || !varlen_fwd_direct(B, H, H_kv, T_q)) return 0;
+  const long long units = varlen_fwd_cap(B, H, H_kv, T_q) * H_kv;
+  const double places = static_cast<double>(units) * (fa::kSplitCost + 256.0 + T_kv);
+  return static_cast<int>(std::max<double>(units, std::min<double>(device_sm_count(), places / fa::kSplitMin + 1)));
+}
+
+size_t varlen_fwd_ws(int B, int H, int H_kv, int T_q, int T_kv, int d) {
+  if (varlen_fwd_direct(B, H, H_kv, T_q))   // per piece two partial results of 256 rows and an entry, or nothing
+    return static_cast<size_t>(varlen_fwd_pieces(B, H, H_kv, T_q, T_kv)) *
+           (2 * 256 * (d + 1) * sizeof(float) + sizeof(fa::VarCut));
   return sizeof(fa::VarPlan) + static_cast<size_t>(varlen_fwd_cap(B, H, H_kv, T_q)) * sizeof(fa::VarUnit);
 }
 
@@ -141,6 +152,7 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
 
   const long long cap = varlen_fwd_cap(B, q.heads, H_kv, q.T);
   const bool direct = varlen_fwd_direct(B, q.heads, H_kv, q.T);
+  const int pieces = varlen_fwd_pieces(B, q.heads, H_kv, q.T, k.T);
   auto* plan = direct ? nullptr : static_cast<fa::VarPlan*>(ws);
   auto* list = reinterpret_cast<fa::VarUnit*>(plan + 1);
   if (!direct) {
@@ -158,6 +170,9 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   p.T_kv = k.T;
   p.plan = plan;
   p.list = list;
+  p.Op = pieces ? static_cast<float*>(ws) : nullptr;
+  p.Lp = pieces ? p.Op + static_cast<size_t>(pieces) * 2 * 256 * HD : nullptr;
+  p.cut = pieces ? reinterpret_cast<fa::VarCut*>(p.Lp + static_cast<size_t>(pieces) * 2 * 256) : nullptr;
   p.o_st = o.st;
   p.o_sh = o.sh;
   p.T_q = q.T;
@@ -174,7 +189,7 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   // Behind a plan, a programmatic dependent launch: the grid sets up while the
   // list is made and waits for it on the device.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(cap * H_kv, sm_count(dev))));
+  cfg.gridDim = dim3(static_cast<unsigned>(pieces ? pieces : std::min<long long>(cap * H_kv, sm_count(dev))));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
@@ -185,6 +200,14 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   cfg.numAttrs = direct ? 0 : 1;
   e = cudaLaunchKernelEx(&cfg, fa::fa_varlen_fwd_kernel<HD>, mq, mk, mv, mo, p);
   if (e != cudaSuccess) return cuda_fail(e);
+  if (pieces > 1) {   // the merge, as a programmatic dependent too
+    cfg.gridDim = dim3(static_cast<unsigned>(pieces - 1), HD / 8);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, fa::varlen_merge_kernel<HD>, p);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
   return FA_OK;
 }
 
@@ -204,7 +227,7 @@ fa_status_t varlen_fwd_impl(const void* Q, const void* K, const void* V, void* O
   for (const void* ptr : {static_cast<const void*>(LSE), static_cast<const void*>(cu_q), static_cast<const void*>(cu_kv)})
     if (reinterpret_cast<uintptr_t>(ptr) % 4 != 0) return FA_ERR_INVALID_ARG;
   if (varlen_fwd_cap(B, H, H_kv, T_q) * H_kv >= (1LL << 31) - 65536) return FA_ERR_UNSUPPORTED;
-  const size_t need = varlen_fwd_ws(B, H, H_kv, T_q), n_lse = static_cast<size_t>(H) * T_q * 4;
+  const size_t need = varlen_fwd_ws(B, H, H_kv, T_q, T_kv, d), n_lse = static_cast<size_t>(H) * T_q * 4;
   const size_t n_cu = (static_cast<size_t>(B) + 1) * 4;
   if (need > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 128 != 0 || workspace_bytes < need))
     return FA_ERR_INVALID_ARG;
@@ -389,9 +412,9 @@ fa_status_t varlen_bwd_impl(const void* Q, const void* K, const void* V, const v
 
 extern "C" {
 
-size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q) {
-  if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || H / H_kv > 128 || T_q < 1) return 0;
-  return varlen_fwd_ws(B, H, H_kv, T_q);
+size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q, int T_kv, int d) {
+  if (varlen_sizes(B, H, H_kv, T_q, T_kv, d, 1.f, 0) != FA_OK) return 0;
+  return varlen_fwd_ws(B, H, H_kv, T_q, T_kv, d);
 }
 
 fa_status_t fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, float* LSE, const int* cu_q,

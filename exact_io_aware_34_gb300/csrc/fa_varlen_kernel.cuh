@@ -78,6 +78,13 @@ struct VarPlan {          // head of the workspace; the list follows
   int pad[6];
 };
 
+// A unit whose keys are split among the pieces first to last of the line, where
+// first is the piece that holds its first block (kvh < 0: none begins there).
+struct VarCut {
+  VarUnit u;
+  int kvh, first, last, pad;
+};
+
 struct VarParams {
   __nv_bfloat16* O;
   float* LSE;             // [H][T_q]
@@ -85,6 +92,8 @@ struct VarParams {
   int B, T_kv;
   VarPlan* plan;          // null: CTA i takes the i-th unit in the sequences' order, without a list
   const VarUnit* list;
+  VarCut* cut;            // split keys: one entry per piece; or null
+  float *Op, *Lp;         // split keys: partial O [slot][tile][d / 4][128][4] and log2-sum-exp [slot][tile][128]
   long long o_st, o_sh;   // element strides of O (token, head)
   int T_q;
   int H_kv;
@@ -263,6 +272,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 struct VarJob {
   VarUnit u;
   int kvh;        // K/V head; -1: no more units
+  int slot;       // place of the partial results; -1: the unit has all its keys, O and LSE are final
 };
 
 // The unit of this CTA without a list (one warp): unit blockIdx.x / H_kv of
@@ -299,6 +309,153 @@ __device__ __forceinline__ void direct_unit(const VarParams& p, VarJob* job) {
   if (__any_sync(0xffffffffu, bad) || found < 0) return;
   job->u = make_unit(seq_span(p.cu_q, p.cu_kv, found), e - first, p.tp, p.causal);
   job->kvh = static_cast<int>(blockIdx.x) - e * p.H_kv;
+  job->slot = -1;
+}
+
+// Split keys: few units on long caches (a piece of a prompt whose beginning is
+// in the cache) would leave most of the device idle. All units lie in one line,
+// head after head, each kSplitCost places for its start and end and then one
+// place per key (up to its last row's diagonal); CTA c takes the places
+// [c P, (c + 1) P), P the line's length over the grid. A unit whose blocks
+// fall to several CTAs leaves partial results, which varlen_merge_kernel joins.
+// Where the longest unit is at most kSplitGain places longer than P, splitting
+// gains less than the merge costs, and CTA i takes unit i whole. Unsplit and
+// split (32 heads on 8, d = 128): 64 rows on 16384 keys 167 and 33 us, 512 on
+// 32768 356 and 211; where nothing is split after all, finding that out and
+// the merge's empty launch make 28 us 31.
+constexpr int kSplitCost = 256;   // two key blocks' time
+constexpr int kSplitMin = 512;    // least P: four key blocks
+constexpr int kSplitGain = 1024;  // eight key blocks
+// Calls that could gain by it: units fit the device at once, and a cache this long.
+constexpr int kSplitKeys = kSplitMin + kSplitGain;
+
+struct VarLine {
+  long long head;       // places of one K/V head's units
+  long long piece;      // P
+  long long total;      // of all heads
+  bool whole, bad;
+};
+
+// A sequence's units on the line: nu units, the u-th base + u * step places
+// long and beginning at u * base + step * u (u - 1) / 2.
+struct LineSeq {
+  int nu;
+  long long base, step;
+  __device__ long long begin(long long u) const { return u * base + step * (u * (u - 1) / 2); }
+};
+
+__device__ __forceinline__ LineSeq line_seq(const VarParams& p, const SeqSpan& s) {
+  LineSeq r;
+  r.nu = s.nq > 0 ? (s.nq - 1) / (2 * p.tp) + 1 : 0;
+  r.step = p.causal ? 2 * p.tp : 0;
+  r.base = kSplitCost + (p.causal ? max(s.nkv - s.nq, 0) + 2 * p.tp : s.nkv);
+  return r;
+}
+
+__device__ __forceinline__ VarLine split_line(const VarParams& p, int pieces) {   // one warp
+  const int lane = threadIdx.x & 31;
+  VarLine l;
+  long long sum = 0, most = 0;
+  bool bad = false;
+  for (int i = lane; i < p.B; i += 32) {
+    bad |= span_bad(p.cu_q, p.cu_kv, i, p.T_q, p.T_kv);
+    const LineSeq s = line_seq(p, seq_span(p.cu_q, p.cu_kv, i));
+    sum += s.begin(s.nu);
+    if (s.nu > 0) most = max(most, s.base + s.step * (s.nu - 1));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
+  l.head = sum;
+  l.total = sum * p.H_kv;
+  l.piece = max(static_cast<long long>(kSplitMin), (l.total + pieces - 1) / pieces);
+  l.whole = most <= l.piece + kSplitGain;
+  l.bad = __any_sync(0xffffffffu, bad);
+  return l;
+}
+
+// The unit at place x < total of the line (one warp; the same in every lane).
+struct LineUnit {
+  SeqSpan s;
+  int u, kvh;
+  long long x0, x1;     // its places
+};
+
+__device__ __forceinline__ LineUnit line_find(const VarParams& p, const VarLine& l, long long x) {
+  const int lane = threadIdx.x & 31;
+  LineUnit r;
+  r.kvh = static_cast<int>(x / l.head);
+  const long long at = x - r.kvh * l.head;
+  long long base = 0, first = 0;
+  int found = 0;
+  for (int c0 = 0; c0 < p.B; c0 += 32) {
+    const int i = c0 + lane;
+    long long len = 0;
+    if (i < p.B) {
+      const LineSeq s = line_seq(p, seq_span(p.cu_q, p.cu_kv, i));
+      len = s.begin(s.nu);
+    }
+    long long incl = len;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    const unsigned mine = __ballot_sync(0xffffffffu, at >= base + incl - len && at < base + incl);
+    if (mine) {
+      const int src = __ffs(mine) - 1;
+      found = c0 + src;
+      first = base + __shfl_sync(0xffffffffu, incl - len, src);
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  r.s = seq_span(p.cu_q, p.cu_kv, found);
+  const LineSeq s = line_seq(p, r.s);
+  int lo = 0, hi = s.nu - 1;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo + 1) / 2;
+    if (s.begin(mid) <= at - first) lo = mid; else hi = mid - 1;
+  }
+  r.u = lo;
+  r.x0 = r.kvh * l.head + first + s.begin(lo);
+  r.x1 = r.kvh * l.head + first + s.begin(lo + 1);
+  return r;
+}
+
+// The key blocks [b0, b1) of a unit with nb blocks that CTA c's piece holds,
+// and the slot of their partial results. A piece has at most two units in
+// part: one that begins before it and one that ends behind it.
+struct LinePart {
+  int b0, b1, slot;
+};
+
+__device__ __forceinline__ LinePart line_part(const VarLine& l, const LineUnit& v, int nb, long long c) {
+  auto block = [&](long long y) {
+    return static_cast<int>(min(static_cast<long long>(nb), max(0ll, (y - kSplitCost + 64) >> 7)));
+  };
+  LinePart r;
+  r.b0 = c * l.piece <= v.x0 ? 0 : block(c * l.piece - v.x0);
+  r.b1 = (c + 1) * l.piece >= v.x1 ? nb : block((c + 1) * l.piece - v.x0);
+  r.slot = static_cast<int>(2 * c) + (r.b0 == 0 ? 1 : 0);
+  return r;
+}
+
+// The unit that begins to be split in piece c, whose end lies inside the line:
+// the one across the end, if its first block is in this piece, or the one
+// whose start alone lies in the piece before.
+__device__ __forceinline__ void note_cut(const VarParams& p, const VarLine& line, int c, VarCut* cut) {
+  const LineUnit v = line_find(p, line, (c + 1) * line.piece);
+  cut->u = make_unit(v.s, v.u, p.tp, p.causal);
+  const LinePart here = line_part(line, v, cut->u.nb1, c);
+  if (here.b0 > 0 || here.b1 == 0 || here.b1 == cut->u.nb1) return;
+  cut->kvh = v.kvh;
+  cut->first = c;
+  int last = static_cast<int>((v.x1 - 1) / line.piece);
+  const LinePart end = line_part(line, v, cut->u.nb1, last);
+  cut->last = end.b0 == end.b1 ? last - 1 : last;
 }
 
 template <int HD>
@@ -379,7 +536,50 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
   if (warp >= 8) ptx::setmaxnreg_dec<C::kRegsControl>();
   if (warp == 10) {
     // ------------------------------------------------------------ unit fetch
-    if (!p.plan) {
+    if (p.cut) {
+      // Split keys: this CTA's piece of the line, unit by unit.
+      const VarLine line = split_line(p, static_cast<int>(gridDim.x));
+      long long x = line.bad || line.whole ? line.total : min(line.total, static_cast<long long>(blockIdx.x) * line.piece);
+      const long long end = min(line.total, x + line.piece);
+      VarJob job;
+      job.kvh = -1;
+      if (line.whole && !line.bad) direct_unit(p, &job);
+      for (int n = 0;;) {
+        if (x < end) {
+          const LineUnit v = line_find(p, line, x);
+          x = v.x1;
+          job.u = make_unit(v.s, v.u, p.tp, p.causal);
+          const LinePart part = line_part(line, v, job.u.nb1, blockIdx.x);
+          if (part.b0 >= part.b1) continue;
+          job.kvh = v.kvh;
+          job.slot = part.b0 == 0 && part.b1 == job.u.nb1 ? -1 : part.slot;
+          job.u.kv_row0 += part.b0 * 128;
+          job.u.n_kv -= part.b0 * 128;
+          job.u.lim0 -= part.b0 * 128;
+          job.u.nb0 = max(1, min(job.u.nb0, part.b1) - part.b0);
+          job.u.nb1 = part.b1 - part.b0;
+        }
+        bool got = true;
+        if (lane == 0) {
+          got = wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
+                              kRoleVarFetch);
+          if (got) {
+            jobs[n & 1] = job;
+            ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
+          }
+        }
+        if (n == 0) {
+          // (The first job waits for nothing, so every piece leaves its entry.)
+          VarCut cut;
+          cut.kvh = -1;
+          if (end < line.total) note_cut(p, line, blockIdx.x, &cut);
+          if (lane == 0) p.cut[blockIdx.x] = cut;
+        }
+        if (!__shfl_sync(0xffffffffu, got, 0) || job.kvh < 0) break;
+        job.kvh = -1;
+        ++n;
+      }
+    } else if (!p.plan) {
       VarJob job;
       job.kvh = -1;
       direct_unit(p, &job);
@@ -400,6 +600,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
           const int e = idx / p.H_kv;
           job.kvh = idx - e * p.H_kv;
           job.u = p.list[e];
+          job.slot = -1;
         }
         if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
                            kRoleVarFetch))
@@ -757,10 +958,14 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
       const long long token = static_cast<long long>(job.u.q_row0) + t * p.tp + xr;
       const bool live = row < box_rows && t * p.tp + xr < job.u.n_tok;
       const bool none = limit == 0;
-      if (live && ok)
-        p.LSE[static_cast<long long>(head) * p.T_q + token] =
-            none ? -INFINITY : (m_use * sl2 + __log2f(l)) * 0.69314718055994530942f;
-      const float inv_l = 1.f / lo;
+      const float lse2 = m_use * sl2 + __log2f(l);
+      const int slot = job.slot;
+      if (slot >= 0) {
+        if (ok) p.Lp[(slot * 2 + t) * 128 + row] = lo == 0.f ? -INFINITY : lse2;
+      } else if (live && ok) {
+        p.LSE[static_cast<long long>(head) * p.T_q + token] = none ? -INFINITY : lse2 * 0.69314718055994530942f;
+      }
+      const float inv_l = slot >= 0 && lo == 0.f ? 0.f : 1.f / lo;
       // The warp's rows as a box of O: first token, last token, first head.
       const int x_first = t * p.tp + ((quarter * 32 * p.inv_g) >> 16);
       const int x_last = t * p.tp + (((quarter * 32 + 31) * p.inv_g) >> 16);
@@ -786,6 +991,14 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
         ptx::tmem_ld32(tO + 32 * c, o);
         ptx::tmem_ld_wait();
         ptx::reg_fence32(o);
+        if (slot >= 0) {   // a row's next four columns lie 2 KB further, so that a warp writes 512 bytes in one go
+          float4* dst = reinterpret_cast<float4*>(p.Op) + (static_cast<size_t>(slot * 2 + t) * (HD / 4) + 8 * c) * 128 + row;
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            dst[v * 128] = make_float4(__uint_as_float(o[4 * v]) * inv_l, __uint_as_float(o[4 * v + 1]) * inv_l,
+                                       __uint_as_float(o[4 * v + 2]) * inv_l, __uint_as_float(o[4 * v + 3]) * inv_l);
+          continue;
+        }
         uint32_t packed[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i)
@@ -821,6 +1034,8 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     }
   }
 
+  // The merge of split keys may be scheduled now; it waits for this grid's end.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // The O stores must have read the staging rows before the CTA's shared
   // memory is released.
   if (warp < 8 && lane == 0) ptx::bulk_wait_group_read0();
@@ -830,6 +1045,77 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem_base, C::kTmemCols);
   }
+}
+
+// Joins the parts of the unit that begins to be split in piece blockIdx.x:
+// LSE = m + log2 sum_s 2^{LSE_s - m}, O = sum_s 2^{LSE_s - LSE} O_s, rounded
+// once to bf16. A warp per 32 rows and 16 columns (blockIdx.y: tile, quarter,
+// and 64 columns), so that nothing is exchanged; the values of four parts are
+// requested before the first is used. What bounds it is the latency of its two
+// passes over the parts; the launch gap before it is 2 us of its time.
+template <int HD>
+__global__ void __launch_bounds__(128) varlen_merge_kernel(const VarParams p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.y & 1, row = 32 * ((blockIdx.y >> 1) & 3) + lane;
+  const int c4 = 16 * (blockIdx.y >> 3) + 4 * warp;       // first column / 4
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const VarCut cut = p.cut[blockIdx.x];
+  if (cut.kvh < 0) return;
+  const VarUnit u = cut.u;
+  const int n = cut.last - cut.first + 1;
+  const int xr = (row * p.inv_g) >> 16, x = t * p.tp + xr;
+  if (row >= p.G * p.tp || x >= u.n_tok) return;
+  // Part s: slot 2 (first + s), the first part's one further.
+  auto lse_of = [&](int s) { return p.Lp[static_cast<size_t>((2 * (cut.first + s) + (s == 0)) * 2 + t) * 128 + row]; };
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int s = 0; s < n; ++s) m = fmaxf(m, lse_of(s));     // (a NaN comes through by its weight)
+  if (m == -INFINITY) m = 0.f;
+  float4 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int s0 = 0; s0 < n; s0 += 4) {
+    float w[4];
+    float4 f[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int s = min(s0 + k, n - 1);                    // (past the end: the last again, with weight 0)
+      w[k] = s0 + k < n ? lse_of(s) : -INFINITY;
+      const float4* src = reinterpret_cast<const float4*>(p.Op) +
+                          (static_cast<size_t>((2 * (cut.first + s) + (s == 0)) * 2 + t) * (HD / 4) + c4) * 128 + row;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[k][i] = src[i * 128];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (s0 + k < n) {
+        const float e = ptx::ex2_approx(w[k] - m);
+        sum += e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[i].x = fmaf(e, f[k][i].x, acc[i].x);
+          acc[i].y = fmaf(e, f[k][i].y, acc[i].y);
+          acc[i].z = fmaf(e, f[k][i].z, acc[i].z);
+          acc[i].w = fmaf(e, f[k][i].w, acc[i].w);
+        }
+      }
+    }
+  }
+  const bool none = (p.causal ? u.lim0 + x : u.n_kv) <= 0 || u.n_kv == 0;     // the row sees no key
+  const float inv = none ? 0.f : 1.f / sum;
+  const int head = cut.kvh * p.G + row - xr * p.G;
+  const long long token = static_cast<long long>(u.q_row0) + x;
+  uint4* dst = reinterpret_cast<uint4*>(p.O + token * p.o_st + head * p.o_sh + 4 * c4);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    dst[i] = make_uint4(ptx::pack_bf16x2(acc[2 * i].x * inv, acc[2 * i].y * inv),
+                        ptx::pack_bf16x2(acc[2 * i].z * inv, acc[2 * i].w * inv),
+                        ptx::pack_bf16x2(acc[2 * i + 1].x * inv, acc[2 * i + 1].y * inv),
+                        ptx::pack_bf16x2(acc[2 * i + 1].z * inv, acc[2 * i + 1].w * inv));
+  if (c4 == 0)
+    p.LSE[static_cast<long long>(head) * p.T_q + token] =
+        none ? -INFINITY : (m + __log2f(sum)) * 0.69314718055994530942f;
 }
 
 }  // namespace fa

@@ -110,7 +110,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_merge_partials.argtypes = [vp, vp, vp, vp, i, ctypes.c_longlong, i, vp]
     lib.fa_merge_partials.restype = i
     sz = ctypes.c_size_t
-    lib.fa_fwd_varlen_workspace_bytes.argtypes = [i, i, i, i]
+    lib.fa_fwd_varlen_workspace_bytes.argtypes = [i, i, i, i, i, i]
     lib.fa_fwd_varlen_workspace_bytes.restype = sz
     lib.fa_fwd_varlen.argtypes = [vp] * 7 + [i] * 6 + [vp, f, i, vp, sz, vp]
     lib.fa_fwd_varlen.restype = i
@@ -587,8 +587,8 @@ def _packed_sizes(q, k, cu_q):
     return q.device, T_q, H, T_kv, H_kv, d, cu_q.shape[0] - 1
 
 
-def fa_fwd_varlen_workspace_bytes(B: int, H: int, H_kv: int, T_q: int) -> int:
-    return int(load_library().fa_fwd_varlen_workspace_bytes(int(B), int(H), int(H_kv), int(T_q)))
+def fa_fwd_varlen_workspace_bytes(B: int, H: int, H_kv: int, T_q: int, T_kv: int, d: int) -> int:
+    return int(load_library().fa_fwd_varlen_workspace_bytes(int(B), int(H), int(H_kv), int(T_q), int(T_kv), int(d)))
 
 
 def fa_fwd_varlen(q, k, v, cu_q, cu_kv, o=None, lse=None, scale: float | None = None, causal: bool = True,
@@ -613,7 +613,7 @@ def fa_fwd_varlen(q, k, v, cu_q, cu_kv, o=None, lse=None, scale: float | None = 
     def run():
         out, out_dense = _out_bf16("o", o, device, rows, q)
         out_lse = _out_lse(lse, (H, T_q), device)
-        need = _need("fa_fwd_varlen_workspace_bytes", device, B, H, H_kv, T_q)
+        need = _need("fa_fwd_varlen_workspace_bytes", device, B, H, H_kv, T_q, T_kv, d)
         ws, ws_ptr, ws_bytes = _workspace(workspace, need, device)
         st = load_library().fa_fwd_varlen(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), out_lse.data_ptr(), cu_q.data_ptr(),

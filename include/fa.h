@@ -389,12 +389,14 @@ typedef struct {
 } fa_strides_t;
 
 /*
- * fa_fwd_varlen_workspace_bytes -- device workspace fa_fwd_varlen needs (the
- * list of its units of work). 0 when the units fit the device at once (no list
- * is needed then, and workspace may be NULL) and for sizes it rejects. Depends
- * on the current device's SM count (148 when there is none).
+ * fa_fwd_varlen_workspace_bytes -- device workspace fa_fwd_varlen needs: the
+ * list of its units of work (tiles of query rows), or, when the units fit the
+ * device at once and T_kv is above 1536, partial results over split keys (at
+ * most 2 KB per SM and head dimension: 40 MB). 0 for few units on few keys
+ * (workspace may be NULL then) and for sizes it rejects. Depends on the current
+ * device's SM count (148 when there is none).
  */
-size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q);
+size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q, int T_kv, int d);
 
 /*
  * fa_fwd_varlen -- the forward pass over B packed sequences of different
@@ -425,9 +427,12 @@ size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q);
  * With offsets that do not describe the buffers (negative, decreasing, past
  * T_q or T_kv) nothing is written, and fa_get_device_status reports
  * FA_ERR_INVALID_ARG.
- * One launch on `stream`, or two (the unit list, then the attention as its
- * programmatic dependent) when the units do not fit the device at once. Each row's result depends on its sequence alone,
- * not on the batch around it, and is the same from run to run.
+ * One launch on `stream`, or two, the second a programmatic dependent of the
+ * first: the unit list and the attention when the units do not fit the device
+ * at once; the attention and the joining of partial results when they do and
+ * T_kv is above 1536. Results are the same from run to run. Where keys are
+ * split, where they are split depends on the whole batch, and so does the last
+ * bit of a row; in all other calls it depends on the row's sequence alone.
  * Limits: T_q, T_kv >= 1, H * T_q and H_kv * T_kv below 2^31, d in {64, 128},
  * scale finite. Q, K, V, O 16-byte, LSE and offsets 4-byte aligned; O, LSE and
  * the workspace overlap no input nor each other. FA_ERR_UNSUPPORTED for other

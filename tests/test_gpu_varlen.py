@@ -5,7 +5,8 @@ Tolerances, from the arithmetic: P V sees each probability rounded to bf16
 O is rounded once more. So |O - ref| <= 2^-8 (A + 2 |ref|) with A = P |V|, and
 float32 sums and exponentials add a few 2^-22 of A. LSE is float32: a score's
 sum of d products is off by at most d 2^-24 scale |q|.|k|, the rest by 2^-22
-steps of values below 32.
+steps of values below 32. Where keys are split, every part has a normaliser of
+its own, whose rounding moves that part's share of O: 2^-8 (2 A + |ref|).
 """
 import math
 
@@ -42,9 +43,9 @@ def ok():
     assert st == fa.FA_OK, (fa.fa_status_string(st), info)
 
 
-def check_o(o, ref, A, scale_up=1.0):
+def check_o(o, ref, A, scale_up=1.0, split=False):
     err = np.abs(parity.to64(o) - ref)
-    tol = 2.0 ** -8 * (A + 2 * np.abs(ref)) + 1e-5 * A + 1e-30
+    tol = 2.0 ** -8 * (2 * A + np.abs(ref) if split else A + 2 * np.abs(ref)) + 1e-5 * A + 1e-30
     assert np.isfinite(parity.to64(o)).all()
     assert (err <= tol * scale_up).all(), float((err / tol).max())
 
@@ -65,7 +66,7 @@ def check_lse(lse, ref, tol):
         assert off <= tol, off
 
 
-def check(q, k, v, ql, kl, causal, scale=None, **kw):
+def check(q, k, v, ql, kl, causal, scale=None, split=False, **kw):
     d = q.shape[-1]
     scale = 1 / math.sqrt(d) if scale is None else scale
     cq, ck = offsets(ql), offsets(kl)
@@ -73,7 +74,7 @@ def check(q, k, v, ql, kl, causal, scale=None, **kw):
     ok()
     n = int(cq[-1])
     O, L, A = oracle.attention_packed(*(parity.to64(x) for x in (q, k, v)), cq.tolist(), ck.tolist(), scale, causal)
-    check_o(o[:n], O[:n], A[:n])
+    check_o(o[:n], O[:n], A[:n], split=split)
     check_lse(lse[:, :n], L[:, :n], lse_tol(q, k, scale))
     return o, lse
 
@@ -189,7 +190,7 @@ def test_graph_replayed_with_other_offsets_and_streams():
     cu = offsets([600]).cuda()
     o = torch.empty(600, 4, 64, dtype=torch.bfloat16, device="cuda")
     lse = torch.empty(4, 600, device="cuda")
-    ws = torch.empty(fa.fa_fwd_varlen_workspace_bytes(3, 4, 2, 600), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(fa.fa_fwd_varlen_workspace_bytes(3, 4, 2, 600, 600, 64), dtype=torch.uint8, device="cuda")
     cu3 = offsets([100, 250, 250]).cuda()
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -204,6 +205,102 @@ def test_graph_replayed_with_other_offsets_and_streams():
     ok()
     assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
     assert cu.shape[0] == 2
+
+
+LONG = [
+    ([1], [5000]), ([100, 17, 0, 64], [4000, 333, 0, 2500]), ([513], [1800]),
+    ([70, 1, 33], [20, 6000, 0]),           # rows that see nothing, a sequence without keys
+    ([1] * 20 + [40], [5] * 20 + [9000]),   # pieces of many units beside one unit of many pieces
+    ([200], [1537]), ([0, 0], [2000, 1]),   # no piece is cut; no rows at all
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,H_kv,d", [(4, 1, 128), (8, 2, 64), (7, 1, 64), (3, 3, 128), (96, 1, 64)])
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_split_keys(case, H, H_kv, d, causal):
+    """Few rows on long caches: units whose keys are split among CTAs."""
+    ql, kl = LONG[case]
+    q, k, v = draw(case * 10 + H + d, (max(1, sum(ql)), H, d), (sum(kl), H_kv, d), (sum(kl), H_kv, d))
+    o, lse = check(q, k, v, ql, kl, causal, split=True)
+    cu = [offsets(x).cuda() for x in (ql, kl)]
+    o2, lse2 = fa.fa_fwd_varlen(q.cuda(), k.cuda(), v.cuda(), *cu, causal=causal)
+    n = sum(ql)
+    assert torch.equal(o[:n], o2[:n]) and torch.equal(lse[:, :n], lse2[:, :n])
+
+
+def test_split_keys_layouts_and_foreign_rows():
+    """Slices and wider outputs, rows of no sequence, NaN and infinities in other sequences' rows."""
+    H, Hk, d, ql, kl = 6, 2, 128, [50, 21], [2900, 1700]
+    q, k, v = draw(77, (90, H, d), (5000, Hk, d), (5000, Hk, d))
+    k[4600:], v[4600:], q[71:] = float("nan"), float("inf"), float("nan")
+    k2, v2 = k.clone(), v.clone()
+    k2[:2900], v2[:2900] = float("nan"), float("-inf")
+    cq, ck = offsets(ql).cuda(), offsets(kl).cuda()
+    o, lse = check(q[:71], k[:4600], v[:4600], ql, kl, True, split=True)
+    kv = torch.cat([k2, v2], 1).cuda()
+    wide = torch.full((90, H + 3, d + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    l2 = torch.full((H, 90), 5.0, device="cuda")
+    fa.fa_fwd_varlen(q.cuda(), kv[:, :Hk], kv[:, Hk:], cq, ck, o=wide[:, 1:H + 1, :d], lse=l2)
+    ok()
+    o2 = wide[:71, 1:H + 1, :d].clone()
+    check_o(o2[50:], parity.to64(o[50:]), 2 * np.abs(parity.to64(v[2900:4600])).max() + 0 * parity.to64(o[50:]))
+    assert bool((l2[:, 71:] == 5).all())
+    assert float((l2[:, 50:71] - lse[:, 50:]).abs().max()) <= 2 * lse_tol(q[:71], k[:4600], d ** -0.5)
+    wide[:71, 1:H + 1, :d] = 7.0
+    assert bool((wide == 7.0).all())
+
+
+def test_split_keys_scales_and_one_key_that_counts():
+    """A key far above the others in one part: the other parts' weights vanish and the row is its V."""
+    q, k, v = draw(78, (3, 2, 64), (4000, 1, 64), (4000, 1, 64))
+    for scale in (0.0, -0.2, 2.0):
+        check(q, k, v, [3], [4000], False, scale=scale, split=True)
+    k[2222] = 40 * q[1, 1].sign()
+    o, lse = fa.fa_fwd_varlen(q.cuda(), k.cuda(), v.cuda(), offsets([3]).cuda(), offsets([4000]).cuda(), scale=1.0)
+    ok()
+    assert torch.equal(o[1, 1].cpu(), v[2222, 0])
+
+
+def test_split_keys_graph_replayed_with_other_lengths():
+    """One captured call: split, whole and empty, each as a call of its own computes it."""
+    q, k, v = (x.cuda() for x in draw(79, (64, 4, 64), (6000, 2, 64), (6000, 2, 64)))
+    cq, ck = offsets([30, 34]).cuda(), offsets([5000, 1000]).cuda()
+    o, lse = torch.empty_like(q), torch.empty(4, 64, device="cuda")
+    ws = torch.empty(fa.fa_fwd_varlen_workspace_bytes(2, 4, 2, 64, 6000, 64), dtype=torch.uint8, device="cuda")
+    fa.fa_fwd_varlen(q, k, v, cq, ck, o=o, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fa.fa_fwd_varlen(q, k, v, cq, ck, o=o, lse=lse, workspace=ws)
+    for ql, kl in (([1, 63], [40, 900]), ([64, 0], [5990, 0]), ([2, 62], [3000, 3000]), ([0, 0], [6000, 0])):
+        cq.copy_(offsets(ql))
+        ck.copy_(offsets(kl))
+        ws.fill_(255)
+        o.fill_(9)
+        g.replay()
+        n = sum(ql)
+        o2, l2 = fa.fa_fwd_varlen(q, k, v, cq, ck)
+        ok()
+        assert torch.equal(o[:n], o2[:n]) and torch.equal(lse[:, :n], l2[:, :n])
+        assert bool((o[n:] == 9).all())
+
+
+def test_two_calls_at_once():
+    """Two streams, each call with its own workspace: the results of either alone."""
+    sets = []
+    for seed, ql, kl in ((80, [40, 3], [5000, 900]), (81, [700, 900, 400], [1000, 900, 400])):
+        q, k, v = (x.cuda() for x in draw(seed, (sum(ql), 8, 128), (sum(kl), 8, 128), (sum(kl), 8, 128)))
+        sets.append((q, k, v, offsets(ql).cuda(), offsets(kl).cuda()))
+    alone = [fa.fa_fwd_varlen(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    both = []
+    for _ in range(10):
+        both += [fa.fa_fwd_varlen(*x, stream=s) for x, s in zip(sets, streams)]
+    ok()
+    for i, (o, lse) in enumerate(both):
+        assert torch.equal(o, alone[i % 2][0]) and torch.equal(lse, alone[i % 2][1])
 
 
 def test_long_prompt_sampled_rows():
@@ -228,12 +325,35 @@ def test_dropped_load_times_out_cleanly(drop):
     q, k, v = (x.cuda() for x in draw(51, (300, 4, 128), (300, 2, 128), (300, 2, 128)))
     cu = offsets([300]).cuda()
     o, lse = torch.zeros_like(q), torch.zeros(4, 300, device="cuda")
-    ws = torch.empty(fa.fa_fwd_varlen_workspace_bytes(1, 4, 2, 300), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(fa.fa_fwd_varlen_workspace_bytes(1, 4, 2, 300, 300, 128), dtype=torch.uint8, device="cuda")
     assert fa.fa_fwd_varlen_fault_test(q, k, v, o, lse, cu, cu, 0.1, True, ws, drop, 20_000_000) == fa.FA_OK
     st, info = fa.fa_get_device_status()
     assert st == fa.FA_ERR_TIMEOUT and info[0] in (13, 14, 15, 16), (st, info)
     assert fa.fa_get_device_status()[0] == fa.FA_OK
     check(q.cpu(), k.cpu(), v.cpu(), [300], [300], True)
+
+
+def test_dropped_load_with_split_keys_times_out_cleanly():
+    q, k, v = (x.cuda() for x in draw(52, (60, 4, 128), (4000, 2, 128), (4000, 2, 128)))
+    cq, ck = offsets([60]).cuda(), offsets([4000]).cuda()
+    o, lse = torch.zeros_like(q), torch.zeros(4, 60, device="cuda")
+    ws = torch.empty(fa.fa_fwd_varlen_workspace_bytes(1, 4, 2, 60, 4000, 128), dtype=torch.uint8, device="cuda")
+    assert fa.fa_fwd_varlen_fault_test(q, k, v, o, lse, cq, ck, 0.1, True, ws, 2, 20_000_000) == fa.FA_OK
+    st, info = fa.fa_get_device_status()
+    assert st == fa.FA_ERR_TIMEOUT and info[0] in (13, 14, 15, 16), (st, info)
+    assert fa.fa_get_device_status()[0] == fa.FA_OK
+    check(q.cpu(), k.cpu(), v.cpu(), [60], [4000], True, split=True)
+
+
+def test_bad_offsets_with_split_keys():
+    q, k, v = (x.cuda() for x in draw(62, (100, 4, 64), (3000, 2, 64), (3000, 2, 64)))
+    good = offsets([20, 20, 60]).cuda()
+    o = torch.full((100, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    for bad in ([0, 50, 40, 3000], [-1, 20, 40, 100], [0, 20, 40, 3001], [0, 20, 1 << 30, 100]):
+        fa.fa_fwd_varlen(q, k, v, good, torch.tensor(bad, dtype=torch.int32, device="cuda"), o=o)
+        st, info = fa.fa_get_device_status()
+        assert st == fa.FA_ERR_INVALID_ARG and info[0] == 16 and info[1] < 3, (st, info)
+    assert bool((o == 3).all())
 
 
 @pytest.mark.parametrize("empty", [0, 300])

@@ -78,15 +78,21 @@ def test_backward_refusals(lib, kw, expect):
 
 
 def test_workspace_sizes(lib):
-    assert fa.fa_fwd_varlen_workspace_bytes(1, 8, 2, 1) == 0           # every unit at once: no list
-    assert fa.fa_fwd_varlen_workspace_bytes(1, 8, 2, 100000) > 0
-    for bad in [(0, 8, 2, 99999), (1, 8, 3, 99999), (1, 8, 0, 99999), (1, 258, 2, 99999), (1, 8, 2, 0)]:
-        assert fa.fa_fwd_varlen_workspace_bytes(*bad) == 0
+    def need(B=1, H=8, H_kv=2, Tq=99999, Tk=1, d=64):
+        return fa.fa_fwd_varlen_workspace_bytes(B, H, H_kv, Tq, Tk, d)
+
+    assert need(Tq=1) == 0 and need(Tq=1, Tk=1536) == 0      # every unit at once, few keys: no list
+    assert 0 < need(Tq=1, Tk=1537) < need(Tq=1, Tk=100000) < need(Tq=1, Tk=100000, d=128) < 42e6
+    assert need() > 0 and need(Tk=100000) == need()
+    for bad in [dict(B=0), dict(H_kv=3), dict(H_kv=0), dict(H=258), dict(Tq=0), dict(Tk=0), dict(d=96)]:
+        assert need(**bad) == 0
     assert fa.fa_bwd_varlen_workspace_bytes(1, 8, 2, 1, 1) > 0
     for bad in [(0, 8, 2, 1, 1), (1, 8, 3, 1, 1), (1, 258, 2, 1, 1), (1, 8, 2, 0, 1), (1, 8, 2, 1, 0)]:
         assert fa.fa_bwd_varlen_workspace_bytes(*bad) == 0
     assert bwd(lib, n=fa.fa_bwd_varlen_workspace_bytes(2, 8, 2, 100, 200) - 1) == BAD
-    assert fwd(lib, n=fa.fa_fwd_varlen_workspace_bytes(2, 8, 2, 100000) - 1) == BAD
+    assert fwd(lib, n=fa.fa_fwd_varlen_workspace_bytes(2, 8, 2, 100000, 200, 128) - 1) == BAD
+    assert fwd(lib, Tq=100, Tk=2000, n=fa.fa_fwd_varlen_workspace_bytes(2, 8, 2, 100, 2000, 128) - 1) == BAD
+    assert fwd(lib, Tq=100, Tk=2000, ws=0) == BAD
 
 
 def test_fault_hook_rejects_zero_timeout(lib):
