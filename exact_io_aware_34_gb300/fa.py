@@ -499,20 +499,32 @@ def _bf16(name, t, device, shape):
     return False
 
 
+#: arrays of strides for the C ABI by the tensors' strides, and workspace sizes
+#: by (function, device, sizes); small calls are bound by the host
+_strides_of: dict = {}
+_need_of: dict = {}
+
+
 def _strides(dense, *tensors):
     """The C ABI's array of strides, or None (all contiguous). None among the
     tensors: a prefix that is not there; a prefix has no batch stride."""
     if dense:
         return None
-    flat = []
-    for t in tensors:
-        if t is None:
-            flat += (0, 0, 0)
-        else:
-            if t.dim() == 3 and tensors[0].dim() == 4:
-                flat.append(0)
-            flat += t.stride()[:-1]
-    return (ctypes.c_longlong * len(flat))(*flat)
+    key = tuple([None if t is None else t.stride() for t in tensors])
+    array = _strides_of.get(key)
+    if array is None:
+        flat = []
+        for st in key:
+            if st is None:
+                flat += (0, 0, 0)
+            else:
+                if len(st) == 3 and len(key[0]) == 4:
+                    flat.append(0)
+                flat += st[:-1]
+        if len(_strides_of) > 4096:
+            _strides_of.clear()
+        array = _strides_of[key] = (ctypes.c_longlong * len(flat))(*flat)
+    return array
 
 
 def _leading(name, t, dims):
@@ -545,10 +557,6 @@ def _out_bf16(name, t, device, shape, like=None):
             return torch.empty_like(like), True
         return torch.empty(shape, dtype=torch.bfloat16, device=device), True
     return t, _bf16(name, t, device, shape)
-
-
-#: workspace sizes by (function, device, sizes); small calls are bound by the host
-_need_of: dict = {}
 
 
 def _need(name, device, *sizes):
