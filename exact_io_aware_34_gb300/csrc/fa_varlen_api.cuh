@@ -248,10 +248,10 @@ fa_status_t varlen_fwd_impl(const void* Q, const void* K, const void* V, void* O
 }
 
 // ---------------------------------------------------------------- backward
-// Workspace: plan, unit list, query tiles, then -LSE log2(e) and -D per tile row.
+// Workspace: plan, unit list, then -LSE log2(e) and -D per tile row.
 struct VarBwdLayout {
   long long tiles, units;          // upper bounds (per K/V head)
-  size_t list, tile_list, nlse2, ndelta, bytes;
+  size_t list, nlse2, ndelta, bytes;
 };
 
 VarBwdLayout varlen_bwd_layout(int B, int H, int H_kv, int T_q, int T_kv) {
@@ -262,8 +262,7 @@ VarBwdLayout varlen_bwd_layout(int B, int H, int H_kv, int T_q, int T_kv) {
   w.units = w.tiles + T_kv / 128 + B;
   const size_t rows = static_cast<size_t>(H_kv) * w.tiles * 128 * 4;
   w.list = up(sizeof(fa::VarBwdPlan));
-  w.tile_list = w.list + up(static_cast<size_t>(w.units) * sizeof(fa::VarBwdUnit));
-  w.nlse2 = w.tile_list + up(static_cast<size_t>(w.tiles) * sizeof(int2));
+  w.nlse2 = w.list + up(static_cast<size_t>(w.units) * sizeof(fa::VarBwdUnit));
   w.ndelta = w.nlse2 + rows;
   w.bytes = w.ndelta + rows;
   return w;
@@ -299,28 +298,13 @@ fa_status_t varlen_bwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   char* ws = static_cast<char*>(workspace);
   auto* plan = reinterpret_cast<fa::VarBwdPlan*>(ws);
   auto* list = reinterpret_cast<fa::VarBwdUnit*>(ws + w.list);
-  auto* tiles = reinterpret_cast<int2*>(ws + w.tile_list);
   auto* nlse2 = reinterpret_cast<float*>(ws + w.nlse2);
   auto* ndelta = reinterpret_cast<float*>(ws + w.ndelta);
-  fa::varlen_bwd_plan_kernel<<<1, fa::kPlanThreads, 0, stream>>>(cu_q, cu_kv, plan, list, tiles, B, q.T, k.T, tp,
-                                                                causal);
+  fa::varlen_bwd_prepare_kernel<HD>
+      <<<dim3(static_cast<unsigned>(1 + w.tiles), static_cast<unsigned>(H_kv)), fa::kPlanThreads, 0, stream>>>(
+          static_cast<const __nv_bfloat16*>(o.p), static_cast<const __nv_bfloat16*>(go.p), LSE, cu_q, cu_kv, plan, list,
+          nlse2, ndelta, o.st, o.sh, go.st, go.sh, B, q.T, k.T, tp, causal, static_cast<int>(w.tiles), G);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e);
-
-  // Each of the other two is a programmatic dependent of the launch before it.
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * w.tiles), static_cast<unsigned>(H_kv));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fa::varlen_bwd_rows_kernel<HD>, static_cast<const __nv_bfloat16*>(o.p),
-                         static_cast<const __nv_bfloat16*>(go.p), LSE, static_cast<const fa::VarBwdPlan*>(plan),
-                         static_cast<const int2*>(tiles), nlse2, ndelta, o.st, o.sh, go.st, go.sh, q.T,
-                         static_cast<int>(w.tiles), G);
   if (e != cudaSuccess) return cuda_fail(e);
 
   fa::VarBwdParams p;
@@ -354,9 +338,17 @@ fa_status_t varlen_bwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   p.idesc_s = C::kIdescS | (scale < 0.f ? fa::ptx::kIdescNegateA : 0u);
   p.timeout_ns = timeout_ns;
   p.drop_load = drop_load;
+  // A programmatic dependent launch: it sets up beside the last of the launch before.
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(w.units * H_kv, sm_count(dev))));
   cfg.blockDim = dim3(fa::kVarBwdThreads);
   cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, fa::fa_varlen_bwd_kernel<HD>, mq, mk, mv, mdo, p);
   if (e != cudaSuccess) return cuda_fail(e);
   return FA_OK;

@@ -13,7 +13,7 @@
 //   * Only pairs of blocks with a visible (row, key) are visited: the query
 //     role stops at the last key its tile sees, the key-block role starts at
 //     the first tile that sees its keys.
-//   * The units of both roles are listed by varlen_bwd_plan_kernel: those of
+//   * The units of both roles are listed by varlen_bwd_plan: those of
 //     the key-block role, then those of the query role, the most expensive
 //     first in each. A persistent grid takes them by a counter. Within a role
 //     the pipeline runs on from unit to unit (rings and barrier phases are
@@ -31,8 +31,8 @@
 //     (Clearing in the elementwise warps, behind branches that one step in a
 //     sequence takes, slowed their every step: 6 % of the call at d = 128, 13 %
 //     at 64.) Elsewhere such rows only reach accumulator rows that are not stored.
-// Three launches: the plan; -LSE log2(e) and -D of every tile row
-// (varlen_bwd_rows_kernel); the products.
+// Two launches: varlen_bwd_prepare_kernel (the plan by one CTA; -LSE log2(e)
+// and -D of every tile row by the others), then the products.
 #pragma once
 
 #include <type_traits>
@@ -50,7 +50,7 @@ enum : unsigned int {
 struct VarBwdUnit {
   int q0, nq, kv0, nkv;   // the sequence
   int blk;                // key block (dkdv) or query tile
-  int tile0;              // number of the sequence's first query tile among all sequences'
+  int tile0;              // place of the sequence's first query tile (bwd_tile0)
   int dkdv;               // role
   int n;                  // key-block role: query tiles to visit (the last n); query role: key blocks (the first n)
 };
@@ -58,9 +58,8 @@ struct VarBwdUnit {
 struct VarBwdPlan {
   int num_units;          // list entries (each stands for H_kv units)
   int num_dkdv;           // of which the first are the key-block role's
-  int num_tiles;
   int next;
-  int pad[4];
+  int pad[5];
 };
 
 struct VarBwdParams {
@@ -83,6 +82,11 @@ struct VarBwdParams {
 };
 
 // ---------------------------------------------------------------- plan
+// Query tiles are kept at places that need no sum over the sequences before:
+// floor(q0 / tp) + i for the first tile of sequence i leaves room for the tiles
+// of all before it, and the last place is below T_q / tp + B.
+__device__ __forceinline__ int bwd_tile0(int q0, int i, int tp) { return q0 / tp + i; }
+
 __device__ __forceinline__ VarBwdUnit make_bwd_unit(const SeqSpan& s, int tile0, int local, int key_blocks, int tiles,
                                                     int tp, int causal) {
   VarBwdUnit u;
@@ -106,26 +110,22 @@ __device__ __forceinline__ VarBwdUnit make_bwd_unit(const SeqSpan& s, int tile0,
   return u;
 }
 
-__global__ void __launch_bounds__(kPlanThreads)
-    varlen_bwd_plan_kernel(const int* __restrict__ cu_q, const int* __restrict__ cu_kv, VarBwdPlan* __restrict__ plan,
-                           VarBwdUnit* __restrict__ list, int2* __restrict__ tiles, int B, int T_q, int T_kv, int tp,
-                           int causal) {
+__device__ __forceinline__ void varlen_bwd_plan(const int* __restrict__ cu_q, const int* __restrict__ cu_kv,
+                                                VarBwdPlan* __restrict__ plan, VarBwdUnit* __restrict__ list, int B,
+                                                int T_q, int T_kv, int tp, int causal) {
   __shared__ int cum[kPlanThreads + 1];        // units of the chunk before each sequence
-  __shared__ int cum_t[kPlanThreads + 1];      // its query tiles
   __shared__ SeqSpan span[kPlanThreads];
   __shared__ int hist[2 * kPlanClasses];       // key-block role, query role
   __shared__ int warp_sums[kPlanThreads / 32];
   static_assert(2 * kPlanClasses == kPlanThreads, "one class per thread");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   if (!offsets_ok(cu_q, cu_kv, B, T_q, T_kv)) {
-    if (tid == 0) plan->num_units = plan->num_dkdv = plan->num_tiles = plan->next = 0;
+    if (tid == 0) plan->num_units = plan->num_dkdv = plan->next = 0;
     return;
   }
   hist[tid] = 0;
-  int total = 0, total_tiles = 0;
+  int total = 0;
   for (int round = 0; round < 2; ++round) {
-    int tile_base = 0;                         // query tiles of the chunks before
     for (int c0 = 0; c0 < B; c0 += kPlanThreads) {
       if (round == 0 || B > kPlanThreads) {
         __syncthreads();
@@ -135,11 +135,9 @@ __global__ void __launch_bounds__(kPlanThreads)
           nt = span[tid].nq / tp + (span[tid].nq % tp != 0);
           nk = (span[tid].nkv + 127) / 128;
         }
-        const int incl_t = block_scan(nt, warp_sums, sum);
-        cum_t[tid + 1] = incl_t;
         const int incl = block_scan(nt + nk, warp_sums, sum);
         cum[tid + 1] = incl;
-        if (tid == 0) cum[0] = cum_t[0] = 0;
+        if (tid == 0) cum[0] = 0;
         __syncthreads();
       }
       const int chunk = cum[kPlanThreads];
@@ -151,54 +149,67 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
         const SeqSpan s = span[lo];
         const int nt = s.nq / tp + (s.nq % tp != 0), nk = (s.nkv + 127) / 128;
-        const VarBwdUnit u = make_bwd_unit(s, tile_base + cum_t[lo], e - cum[lo], nk, nt, tp, causal);
+        const VarBwdUnit u = make_bwd_unit(s, bwd_tile0(s.q0, c0 + lo, tp), e - cum[lo], nk, nt, tp, causal);
         // (the place of a class in `hist`: expensive ones first)
         const int cls = (u.dkdv ? 0 : kPlanClasses) + kPlanClasses - 1 - cost_class(max(1, u.n));
         const int at = atomicAdd(&hist[cls], 1);
         if (round == 1) list[at] = u;
-        if (round == 0 && !u.dkdv) tiles[u.tile0 + u.blk] = make_int2(s.q0 + u.blk * tp, min(tp, s.nq - u.blk * tp));
       }
       if (round == 0) total += chunk;
-      tile_base += cum_t[kPlanThreads];
     }
-    total_tiles = tile_base;
     __syncthreads();
     if (round == 0) {
       int sum;
       const int mine = hist[tid];
       const int incl = block_scan(mine, warp_sums, sum);
       hist[tid] = incl - mine;
+      if (tid == kPlanClasses) plan->num_dkdv = incl - mine;     // units before the query role's first class
       __syncthreads();
     }
   }
   if (tid == 0) {
     plan->num_units = total;
-    plan->num_dkdv = total - total_tiles;
-    plan->num_tiles = total_tiles;
     plan->next = 0;
   }
 }
 
-// ---------------------------------------------------------------- rows
-// -LSE log2(e) and -D of the 128 rows of every (K/V head, query tile), in the
-// tile's row order. One CTA per 64 rows; HD / 8 lanes read a row in 16-byte
-// pieces, all of a warp's rows requested before the first product.
+// ---------------------------------------------------------------- plan and rows
+// CTA (0, 0) plans. CTA (1 + place, K/V head) writes -LSE log2(e) and -D of the
+// 128 rows of a query tile, in the tile's row order; it finds its sequence by
+// bisection and checks that one's offsets itself, so that both parts run at
+// once (one after the other, as two launches: 326 us instead of 323 at two
+// documents of 4096 tokens, 16 heads on 4). HD / 8 lanes read a row in 16-byte pieces, all of a warp's rows requested before the
+// first product.
 template <int HD>
-__global__ void __launch_bounds__(256)
-    varlen_bwd_rows_kernel(const __nv_bfloat16* __restrict__ O, const __nv_bfloat16* __restrict__ dO,
-                           const float* __restrict__ LSE, const VarBwdPlan* plan, const int2* tiles, float* nlse2,
-                           float* ndelta, long long o_st, long long o_sh, long long do_st, long long do_sh, int T_q,
-                           int tile_cap, int G) {
-  constexpr int kRowsPerWarp = 8;
+__global__ void __launch_bounds__(kPlanThreads)
+    varlen_bwd_prepare_kernel(const __nv_bfloat16* __restrict__ O, const __nv_bfloat16* __restrict__ dO,
+                              const float* __restrict__ LSE, const int* __restrict__ cu_q,
+                              const int* __restrict__ cu_kv, VarBwdPlan* __restrict__ plan,
+                              VarBwdUnit* __restrict__ list, float* __restrict__ nlse2, float* __restrict__ ndelta,
+                              long long o_st, long long o_sh, long long do_st, long long do_sh, int B, int T_q,
+                              int T_kv, int tp, int causal, int tile_cap, int G) {
+  constexpr int kRowsPerWarp = 128 / (kPlanThreads / 32);
   constexpr int kLanesPerRow = HD / 8;
   constexpr int kRowsPerLoad = 32 / kLanesPerRow;
   constexpr int kLoads = kRowsPerWarp / kRowsPerLoad;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tile = blockIdx.x >> 1, kvh = blockIdx.y;
-  if (tile >= plan->num_tiles) return;
-  const int2 tl = tiles[tile];
-  const int row0 = (blockIdx.x & 1) * 64 + (threadIdx.x >> 5) * kRowsPerWarp;
+  if (blockIdx.x == 0) {
+    if (blockIdx.y == 0) varlen_bwd_plan(cu_q, cu_kv, plan, list, B, T_q, T_kv, tp, causal);
+    return;
+  }
+  const int tile = blockIdx.x - 1, kvh = blockIdx.y;
+  int seq = 0;
+  for (int hi = B - 1; seq < hi;) {
+    const int mid = seq + (hi - seq + 1) / 2;
+    if (bwd_tile0(cu_q[mid], mid, tp) <= tile) seq = mid; else hi = mid - 1;
+  }
+  const int q0 = cu_q[seq], q1 = cu_q[seq + 1];
+  const int local = tile - bwd_tile0(q0, seq, tp);
+  if (q0 < 0 || q1 > T_q || q1 <= q0) return;      // (bad offsets are the plan's to report)
+  if (local < 0 || local > (q1 - q0 - 1) / tp) return;   // no tile at this place
+  const int tok0 = q0 + local * tp;
+  const int tokens = min(tp, q1 - tok0);           // of this tile
+  const int row0 = (threadIdx.x >> 5) * kRowsPerWarp;
   const int lane = threadIdx.x & 31, sub = lane / kLanesPerRow, piece = lane % kLanesPerRow;
   uint4 o4[kLoads], g4[kLoads];
   float lse[kLoads];
@@ -207,11 +218,11 @@ __global__ void __launch_bounds__(256)
   for (int i = 0; i < kLoads; ++i) {
     const int row = row0 + i * kRowsPerLoad + sub;
     const int x = row / G, h = kvh * G + row - x * G;
-    live[i] = x < tl.y;
+    live[i] = x < tokens;
     o4[i] = g4[i] = make_uint4(0u, 0u, 0u, 0u);
     lse[i] = -INFINITY;
     if (live[i]) {
-      const long long t = tl.x + x;
+      const long long t = tok0 + x;
       o4[i] = __ldg(reinterpret_cast<const uint4*>(O + t * o_st + h * o_sh + piece * 8));
       g4[i] = __ldg(reinterpret_cast<const uint4*>(dO + t * do_st + h * do_sh + piece * 8));
       if (piece == 0) lse[i] = __ldg(LSE + static_cast<long long>(h) * T_q + t);

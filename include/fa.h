@@ -481,7 +481,7 @@ size_t fa_bwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q, int T_kv);
  * reaches no gradient, NaN and infinities included; values of a sequence's
  * own rows and keys are taken to be finite. Accumulation is float32, in an
  * order that depends on the sequence alone (no atomics), rounded once.
- * Three launches on `stream`. Bad offsets, limits and errors as for
+ * Two launches on `stream`. Bad offsets, limits and errors as for
  * fa_fwd_varlen; dQ, dK, dV and the workspace overlap no input nor each other
  * (column ranges of one buffer are fine).
  */
