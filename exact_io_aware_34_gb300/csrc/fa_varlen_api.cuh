@@ -88,6 +88,15 @@ fa_status_t varlen_sizes(int B, int H, int H_kv, int T_q, int T_kv, int d, float
   return FA_OK;
 }
 
+// K/V heads whose long units are taken together: as many as stream at most
+// 48 MB, of which each of the two halves of L2 (129 MB) keeps a copy. Forward and
+// backward of 8192 tokens, 32 K/V heads, not causal: 724 and 2460 us with all
+// heads together, 703 and 2320 in groups; 24 MB cost the backward of two
+// documents of 4096 tokens 11 % by fewer units to balance.
+int head_group(int H_kv, double bytes_per_head) {
+  return std::max(1, static_cast<int>(std::min<double>(H_kv, 48e6 / bytes_per_head)));
+}
+
 // Units (per K/V head) of the forward list: every sequence rounds up once.
 long long varlen_fwd_cap(int B, int H, int H_kv, int T_q) {
   const int tp = 128 / (H / H_kv);
@@ -176,6 +185,7 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   p.o_st = o.st;
   p.o_sh = o.sh;
   p.T_q = q.T;
+  p.group = head_group(H_kv, 4.0 * HD * k.T);
   p.H_kv = H_kv;
   p.G = G;
   p.tp = tp;
@@ -323,12 +333,7 @@ fa_status_t varlen_bwd_launch(const Rows& q, const Rows& k, const Rows& v, const
   p.ndelta = ndelta;
   p.tile_cap = static_cast<int>(w.tiles);
   p.H_kv = H_kv;
-  // Heads whose units are taken together: as many as stream at most 96 MB of
-  // Q, dO, K and V, so that they stay in L2 (129 MB). At 8192 tokens of 32
-  // heads, not causal: 2694 us with all heads together, 2531 in groups; at
-  // 48 MB short batches lose 2 % by fewer units to balance.
-  p.group = std::max(1, static_cast<int>(
-                            std::min<double>(H_kv, 96e6 / (4.0 * HD * (k.T + static_cast<double>(G) * q.T)))));
+  p.group = head_group(H_kv, 4.0 * HD * (k.T + static_cast<double>(G) * q.T));
   p.G = G;
   p.tp = tp;
   p.inv_g = (65536 + G - 1) / G;

@@ -58,8 +58,9 @@ struct VarBwdUnit {
 struct VarBwdPlan {
   int num_units;          // list entries (each stands for H_kv units)
   int num_dkdv;           // of which the first are the key-block role's
+  int num_long;           // the query role's first entries, of more than half its most key blocks
   int next;
-  int pad[5];
+  int pad[4];
 };
 
 struct VarBwdParams {
@@ -117,13 +118,15 @@ __device__ __forceinline__ void varlen_bwd_plan(const int* __restrict__ cu_q, co
   __shared__ SeqSpan span[kPlanThreads];
   __shared__ int hist[2 * kPlanClasses];       // key-block role, query role
   __shared__ int warp_sums[kPlanThreads / 32];
+  __shared__ int top;                          // first place of the query role's classes with an entry
   static_assert(2 * kPlanClasses == kPlanThreads, "one class per thread");
   const int tid = threadIdx.x;
   if (!offsets_ok(cu_q, cu_kv, B, T_q, T_kv)) {
-    if (tid == 0) plan->num_units = plan->num_dkdv = plan->next = 0;
+    if (tid == 0) plan->num_units = plan->num_dkdv = plan->num_long = plan->next = 0;
     return;
   }
   hist[tid] = 0;
+  if (tid == 0) top = 2 * kPlanClasses - 1;
   int total = 0;
   for (int round = 0; round < 2; ++round) {
     for (int c0 = 0; c0 < B; c0 += kPlanThreads) {
@@ -161,9 +164,15 @@ __device__ __forceinline__ void varlen_bwd_plan(const int* __restrict__ cu_q, co
     if (round == 0) {
       int sum;
       const int mine = hist[tid];
+      if (mine > 0 && tid >= kPlanClasses) atomicMin(&top, tid);
       const int incl = block_scan(mine, warp_sums, sum);
       hist[tid] = incl - mine;
-      if (tid == kPlanClasses) plan->num_dkdv = incl - mine;     // units before the query role's first class
+      __syncthreads();
+      if (tid == 0) {
+        // Units before the query role's first class; its entries before the class an octave below its top.
+        plan->num_dkdv = hist[kPlanClasses];
+        plan->num_long = (top + 8 < 2 * kPlanClasses ? hist[top + 8] : sum) - hist[kPlanClasses];
+      }
       __syncthreads();
     }
   }
@@ -252,16 +261,6 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // ---------------------------------------------------------------- products
-// The idx-th unit of n list entries x H_kv heads, taken `group` heads at a
-// time (the heads of a group together, so that what they stream stays in L2),
-// within a group in the list's order.
-__device__ __forceinline__ void place_unit(int idx, int n, int H_kv, int group, int* entry, int* kvh) {
-  const int g = idx / (n * group), r = idx - g * n * group;
-  const int heads = min(group, H_kv - g * group);
-  *entry = r / heads;
-  *kvh = g * group + r - *entry * heads;
-}
-
 struct VarBwdJob {
   VarBwdUnit u;
   int kvh;       // -1: no more units
@@ -319,7 +318,7 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int from, int to, int 
 
 // Scores of this thread's row outside columns [from, to) of the 64 at `taddr`
 // become -inf. A short loop, out of the way of the blocks that do not need it.
-__device__ __noinline__ void mask_columns(uint32_t taddr, int from, int to) {
+__device__ __forceinline__ void mask_columns(uint32_t taddr, int from, int to) {
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     const int lo = from - 32 * c, hi = to - 32 * c;
@@ -1094,7 +1093,10 @@ __device__ __forceinline__ void varlen_bwd_tails(const VarBwdParams& p, VarBwdSh
   }
 }
 
-constexpr int kVarBwdThreads = 384;   // the ten warps of BwdCfg, the fetch warp and the one that clears tails
+// The ten warps of BwdCfg, the fetch warp and the one that clears tails. (All keep
+// the 168 registers of the launch: 216 for the elementwise warps, which needs a
+// copy of the loops for them alone, was 2 to 5 % slower.)
+constexpr int kVarBwdThreads = 384;
 
 template <int HD>
 __global__ void __launch_bounds__(kVarBwdThreads, 1)
@@ -1138,7 +1140,14 @@ __global__ void __launch_bounds__(kVarBwdThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_base_slot;
-  if (warp == 10) {
+  // (As one lambda: as plain calls in a branch the compiled loops are 4 % slower.)
+  auto work = [&] {
+    const int n = varlen_dkdv_loop<HD>(tmQ, tmK, tmV, tmdO, p, jobs, tmem_base, abort_ptr);
+    if (n >= 0) varlen_dq_loop<HD>(tmQ, tmK, tmV, tmdO, p, jobs, n, tmem_base, abort_ptr);
+  };
+  if (warp < 10) {
+    work();
+  } else if (warp == 10) {
     // ------------------------------------------------------------ unit fetch (converged; lane 0 writes)
     // (A unit is taken when the loads of the one before near their end.)
     {
@@ -1152,9 +1161,9 @@ __global__ void __launch_bounds__(kVarBwdThreads, 1)
           const int n_k = p.plan->num_dkdv, in_k = n_k * p.H_kv;
           int e;
           if (idx < in_k) {
-            place_unit(idx, n_k, p.H_kv, p.group, &e, &job.kvh);
+            place_unit(idx, n_k, p.H_kv, p.group, &e, &job.kvh);       // (the other role evens out its end)
           } else {
-            place_unit(idx - in_k, p.plan->num_units - n_k, p.H_kv, p.group, &e, &job.kvh);
+            place_unit(idx - in_k, p.plan->num_long, p.H_kv, p.group, &e, &job.kvh);
             e += n_k;
           }
           job.u = p.list[e];
@@ -1174,11 +1183,8 @@ __global__ void __launch_bounds__(kVarBwdThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 11) {
-    varlen_bwd_tails<HD>(p, jobs, abort_ptr);
   } else {
-    const int n = varlen_dkdv_loop<HD>(tmQ, tmK, tmV, tmdO, p, jobs, tmem_base, abort_ptr);
-    if (n >= 0) varlen_dq_loop<HD>(tmQ, tmK, tmV, tmdO, p, jobs, n, tmem_base, abort_ptr);
+    varlen_bwd_tails<HD>(p, jobs, abort_ptr);
   }
   __syncthreads();
   if (warp == 9) {

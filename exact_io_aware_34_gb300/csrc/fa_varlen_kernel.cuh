@@ -74,8 +74,9 @@ struct VarUnit {
 
 struct VarPlan {          // head of the workspace; the list follows
   int num_units;          // entries of the list (each stands for H_kv units)
+  int num_long;           // its first entries, of more than half the most key blocks
   int next;               // units handed out beyond the grid's first
-  int pad[6];
+  int pad[5];
 };
 
 // A unit whose keys are split among the pieces first to last of the line, where
@@ -98,6 +99,7 @@ struct VarParams {
   int T_q;
   int H_kv;
   int G;                  // query heads per K/V head
+  int group;              // K/V heads whose units are taken together
   int tp;                 // tokens per tile: 128 / G
   int inv_g;              // ceil(65536 / G): r / G = r * inv_g >> 16 for r < 128
   int causal;
@@ -208,17 +210,20 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ SeqSpan span[kPlanThreads];
   __shared__ int hist[kPlanClasses];
   __shared__ int warp_sums[kPlanThreads / 32];
+  __shared__ int top;                          // the most expensive class
   // The grid that reads the list may be scheduled now; it waits for this one's end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
   if (!offsets_ok(cu_q, cu_kv, B, T_q, T_kv)) {
     if (tid == 0) {
       plan->num_units = 0;
+      plan->num_long = 0;
       plan->next = 0;
     }
     return;
   }
   if (tid < kPlanClasses) hist[tid] = 0;
+  if (tid == 0) top = 0;
   const int unit_tok = 2 * tp;
   int total = 0;
   for (int round = 0; round < 2; ++round) {
@@ -256,8 +261,11 @@ __global__ void __launch_bounds__(kPlanThreads)
       // Places: the most expensive class first.
       int sum;
       const int mine = tid < kPlanClasses ? hist[kPlanClasses - 1 - tid] : 0;
+      if (mine > 0) atomicMax(&top, kPlanClasses - 1 - tid);
       const int incl = block_scan(mine, warp_sums, sum);
       if (tid < kPlanClasses) hist[kPlanClasses - 1 - tid] = incl - mine;
+      // Eight classes are an octave: entries before those of class top - 8 are long.
+      if (tid == kPlanClasses - 1 - max(top - 8, 0)) plan->num_long = top >= 8 ? incl - mine : sum;
       __syncthreads();
     }
   }
@@ -268,6 +276,25 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // ---------------------------------------------------------------- forward
+// The idx-th unit of n list entries x H_kv heads. Of the n_long long entries
+// `group` heads are taken at a time, the heads of a group together, so that what
+// they stream stays in L2; then the short entries of all heads, which even out
+// the end. Within either in the list's order.
+__device__ __forceinline__ void place_unit(int idx, int n_long, int H_kv, int group, int* entry, int* kvh) {
+  const int in_long = n_long * H_kv;
+  if (idx < in_long) {
+    const int g = idx / (n_long * group), r = idx - g * n_long * group;
+    const int heads = min(group, H_kv - g * group);
+    *entry = r / heads;
+    *kvh = g * group + r - *entry * heads;
+  } else {
+    const int r = idx - in_long;
+    *entry = r / H_kv;
+    *kvh = r - *entry * H_kv;
+    *entry += n_long;
+  }
+}
+
 // What the fetch warp hands to the other roles.
 struct VarJob {
   VarUnit u;
@@ -597,8 +624,8 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
         VarJob job;
         job.kvh = -1;
         if (idx < total) {
-          const int e = idx / p.H_kv;
-          job.kvh = idx - e * p.H_kv;
+          int e;
+          place_unit(idx, p.plan->num_long, p.H_kv, p.group, &e, &job.kvh);
           job.u = p.list[e];
           job.slot = -1;
         }
