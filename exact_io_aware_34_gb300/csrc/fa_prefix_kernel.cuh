@@ -239,220 +239,8 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
   volatile int* abort_ptr = &abort_flag;
 
   if (warp >= 4) ptx::setmaxnreg_dec<C::kRegsControl>();
-  if (warp == 6) {
-    // ------------------------------------------------------------ segments
-    if (lane == 0) {
-      int x = x_begin, b = start_b, cum = start_cum;
-      for (int n = 0;; ++n) {
-        PreJob job;
-        job.own = -1;
-        int unit = 0, end = 0;       // the unit's number among all, its last place
-        while (x < x_end && job.own < 0) {
-          int first, len;            // its first place, its keys
-          if (x < p_total) {
-            unit = x / p_places;
-            first = unit * p_places;
-            len = sh.n_p;
-          } else {
-            const int y = x - p_total;
-            len = own_len(p, b);
-            int nu = unit_places(len);
-            while (y >= (cum + nu) * own_units_per_seq && b + 1 < sh.B) {   // on to the sequence that holds place y
-              cum += nu;
-              ++b;
-              len = own_len(p, b);
-              nu = unit_places(len);
-            }
-            if (nu == 0) break;      // (lengths that change under the call)
-            const int u = min((y - cum * own_units_per_seq) / nu, own_units_per_seq - 1);
-            unit = sh.p_units + b * own_units_per_seq + u;
-            first = p_total + cum * own_units_per_seq + u * nu;
-          }
-          const int places = unit_places(len);
-          const int from = x - first, to = min(places, from + (x_end - x));
-          x += to - from;
-          end = first + places - 1;
-          job.j0 = max(0, from - kUnitCost);
-          job.j1 = max(0, to - kUnitCost);
-          if (job.j1 <= job.j0) continue;        // only the places beside its blocks
-          job.n_keys = len;
-          if (unit < sh.p_units) {
-            const int per_head = sh.bt * sh.ht;
-            job.own = 0;
-            job.kvh = unit / per_head;
-            const int t = unit - job.kvh * per_head, tb = t / sh.ht;
-            job.b0 = tb * sh.bp;
-            job.h0 = (t - tb * sh.ht) * sh.hp;
-            job.rows = min(sh.hp, sh.G - job.h0) * sh.N_q * min(sh.bp, sh.B - job.b0);
-            job.slot = unit + static_cast<int>(blockIdx.x);
-          } else {
-            const int u = unit - sh.p_units - b * own_units_per_seq;
-            job.own = 1;
-            job.b0 = b;
-            job.kvh = u / sh.ht;
-            job.h0 = (u - job.kvh * sh.ht) * sh.hp;
-            job.rows = min(sh.hp, sh.G - job.h0) * sh.N_q;
-            job.slot = unit - sh.p_units + static_cast<int>(blockIdx.x);
-          }
-        }
-        if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
-                           kRolePreWalk))
-          break;
-        jobs[n & 1] = job;
-        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
-        if (job.own < 0) break;
-        // The CTA with a unit's first block notes its segments for the merge.
-        if (job.j0 == 0)
-          p.seg[unit] = make_int2(job.slot, line_owner(total, sh.ctas, end) - static_cast<int>(blockIdx.x) + 1);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 7) {
-    // ------------------------------------------------------------ tails of V tiles
-    bool ok = true;
-    int it0 = 0, tails = 0;
-    for (int n = 0; ok; ++n) {
-      ok = wait_idle_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns, kRolePreWalk);
-      if (!ok) break;
-      const int own = jobs[n & 1].own, blocks = jobs[n & 1].j1 - jobs[n & 1].j0;
-      const int have = jobs[n & 1].n_keys - (jobs[n & 1].j1 - 1) * C::kBN;    // keys in the segment's last block
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
-      if (own < 0) break;
-      it0 += 2 * blocks;
-      if (!own || have >= C::kBN) continue;    // (behind the prefix, TMA fills with zeros)
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_tail[tails & 3]), (tails >> 2) & 1, abort_ptr, p.timeout_ns,
-                              kRolePreWalk);
-      if (!ok) break;
-      ++tails;
-      // Whole 128-byte rows, so the swizzle does not matter.
-      const int slot = (it0 - 1) % C::kStages;
-      for (int c = 0; c < C::kChunks; ++c)
-        for (int i = lane; i < (C::kBN - have) * 8; i += 32)
-          reinterpret_cast<uint4*>(kv_generic + slot * C::kTileBytes + c * C::kChunkBytes + have * 128)[i] =
-              make_uint4(0u, 0u, 0u, 0u);
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_kv_full[slot]));
-    }
-    __syncwarp();
-  } else if (warp == 4) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const uint64_t pol_first = ptx::policy_evict_first();
-      const uint64_t pol_last = ptx::policy_evict_last();    // prefix tiles are read by every tile of sequences
-      const uint32_t q_full = ptx::smem_u32(&bar_q_full);
-      int it = 0, q_issued = 0, tails = 0;
-      bool ok = true;
-      for (int n = 0; ok; ++n) {
-        ok = wait_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
-                           kRolePreProducer);
-        if (!ok) break;
-        const PreJob job = jobs[n & 1];
-        ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
-        if (job.own < 0) break;
-        if (n > 0 && !wait_or_abort(ptx::smem_u32(&bar_q_empty), (n - 1) & 1, abort_ptr, p.timeout_ns,
-                                    kRolePreProducer)) {
-          ok = false;
-          break;
-        }
-        // Rows of the tile beyond the box keep what they held: a row of S and
-        // of O depends on its own row of Q alone, and they are not stored.
-        const int box_rows = sh.hp * sh.N_q * (job.own ? 1 : sh.bp);
-        ptx::mbar_arrive_expect_tx(q_full, C::kChunks * 128 * box_rows);
-        for (int c = 0; c < C::kChunks; ++c)
-          ptx::tma_load_4d(sQ + c * C::kChunkBytes, job.own ? &tmQo : &tmQp, q_full, c * 64, 0,
-                           job.kvh * sh.G + job.h0, job.b0, pol_last);
-        q_issued = n + 1;
-        const CUtensorMap* maps[2] = {job.own ? &tmK : &tmKp, job.own ? &tmV : &tmVp};
-        const uint64_t pol = job.own || sh.bt * sh.ht == 1 ? pol_first : pol_last;
-        for (int j = job.j0; j < job.j1 && ok; ++j) {
-          for (int kv = 0; kv < 2; ++kv) {
-            const int slot = it % C::kStages;
-            if (!wait_or_abort(ptx::smem_u32(&bar_kv_empty[slot]), ((it / C::kStages) & 1) ^ 1u, abort_ptr,
-                               p.timeout_ns, kRolePreProducer)) {
-              ok = false;
-              break;
-            }
-            const int me = it++;
-            if (me == p.drop_load) continue;   // test hook: this tile never arrives
-            // A V tile with rows past the length: warp 7 completes its barrier.
-            const bool tail = kv && job.own && (j + 1) * C::kBN > job.n_keys;
-            const uint32_t full = ptx::smem_u32(tail ? &bar_tail[tails++ & 3] : &bar_kv_full[slot]);
-            ptx::mbar_arrive_expect_tx(full, C::kTileBytes);
-            for (int c = 0; c < C::kChunks; ++c)
-              ptx::tma_load_4d(sKV + slot * C::kTileBytes + c * C::kChunkBytes, maps[kv], full, c * 64, j * C::kBN,
-                               job.kvh, job.own ? job.b0 : 0, pol);
-          }
-        }
-      }
-      if (!ok || *abort_ptr) {
-        if (q_issued > 0) drain_wait(q_full, (q_issued - 1) & 1, p.timeout_ns);
-        for (int r = max(0, tails - 4); r < tails; ++r)
-          drain_wait(ptx::smem_u32(&bar_tail[r & 3]), (r >> 2) & 1, p.timeout_ns);
-        for (int i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
-          if (i != p.drop_load)
-            drain_wait(ptx::smem_u32(&bar_kv_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 5) {
-    // ------------------------------------------------------------ MMA issuer
-    bool ok = true;
-    int it0 = 0, g = 0;       // K/V loads and key blocks of the segments before
-    auto kv_wait = [&](int it) {
-      return wait_warp_or_abort(ptx::smem_u32(&bar_kv_full[it % C::kStages]), (it / C::kStages) & 1, abort_ptr,
-                                p.timeout_ns, kRolePreMma);
-    };
-    for (int n = 0; ok; ++n) {
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns, kRolePreMma);
-      if (!ok) break;
-      const int own = jobs[n & 1].own, blocks = jobs[n & 1].j1 - jobs[n & 1].j0;
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
-      if (own < 0) break;
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_q_full), n & 1, abort_ptr, p.timeout_ns, kRolePreMma);
-      // Step jj: P V of block jj - 1 (P sits in the S columns), then Q K^T of block jj.
-      for (int jj = 0; jj <= blocks && ok; ++jj) {
-        const int itK = it0 + 2 * jj, itV = itK - 1;
-        if (jj > 0) {
-          ok = wait_warp_or_abort(ptx::smem_u32(&bar_p_full), (g - 1) & 1, abort_ptr, p.timeout_ns, kRolePreMma);
-          if (ok) ok = kv_wait(itV);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          const uint64_t b_desc =
-              ptx::desc_mnmajor_sw128(sKV + (itV % C::kStages) * C::kTileBytes, C::kChunkBytes);
-          ptx::mma_ts_k128_warp<32>(tmem_base + C::kColO, tmem_base + C::kColS, ptx::desc_lo(b_desc),
-                                    ptx::desc_hi(b_desc), C::kIdescPV, jj > 1 ? 1u : 0u);
-          if (jj == blocks) ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full));
-          ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[itV % C::kStages]));
-        }
-        if (jj < blocks) {
-          ok = kv_wait(itK);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          const uint64_t a_desc = ptx::desc_kmajor_sw128(sQ);
-          const uint64_t b_desc = ptx::desc_kmajor_sw128(sKV + (itK % C::kStages) * C::kTileBytes);
-          if constexpr (HD == 128)
-            ptx::mma_ss_k128_warp(tmem_base + C::kColS, ptx::desc_lo(a_desc), ptx::desc_lo(b_desc),
-                                  ptx::desc_hi(a_desc), p.idesc_qk, 0u);
-          else
-            ptx::mma_ss_k64_warp(tmem_base + C::kColS, ptx::desc_lo(a_desc), ptx::desc_lo(b_desc),
-                                 ptx::desc_hi(a_desc), p.idesc_qk, 0u);
-          ptx::mma_commit_warp(ptx::smem_u32(&bar_s_full));
-          ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[itK % C::kStages]));
-          if (jj == blocks - 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty));
-          ++g;
-        }
-      }
-      it0 += 2 * blocks;
-    }
-    if (!ok) {
-      ptx::mma_commit_warp(ptx::smem_u32(&bar_drain));
-      drain_wait(ptx::smem_u32(&bar_drain), 0, p.timeout_ns);
-    }
-    __syncwarp();
-  } else if (warp < 4) {
+  // (The softmax stands first, as in fa_varlen_fwd_kernel: 1 to 2 % here.)
+  if (warp < 4) {
     // ------------------------------------------------------------ softmax + epilogue
     ptx::setmaxnreg_inc<C::kRegsSoftmax>();
     const int row = warp * 32 + lane;
@@ -637,6 +425,219 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
         }
       }
     }
+  } else if (warp == 4) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t pol_first = ptx::policy_evict_first();
+      const uint64_t pol_last = ptx::policy_evict_last();    // prefix tiles are read by every tile of sequences
+      const uint32_t q_full = ptx::smem_u32(&bar_q_full);
+      int it = 0, q_issued = 0, tails = 0;
+      bool ok = true;
+      for (int n = 0; ok; ++n) {
+        ok = wait_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
+                           kRolePreProducer);
+        if (!ok) break;
+        const PreJob job = jobs[n & 1];
+        ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
+        if (job.own < 0) break;
+        if (n > 0 && !wait_or_abort(ptx::smem_u32(&bar_q_empty), (n - 1) & 1, abort_ptr, p.timeout_ns,
+                                    kRolePreProducer)) {
+          ok = false;
+          break;
+        }
+        // Rows of the tile beyond the box keep what they held: a row of S and
+        // of O depends on its own row of Q alone, and they are not stored.
+        const int box_rows = sh.hp * sh.N_q * (job.own ? 1 : sh.bp);
+        ptx::mbar_arrive_expect_tx(q_full, C::kChunks * 128 * box_rows);
+        for (int c = 0; c < C::kChunks; ++c)
+          ptx::tma_load_4d(sQ + c * C::kChunkBytes, job.own ? &tmQo : &tmQp, q_full, c * 64, 0,
+                           job.kvh * sh.G + job.h0, job.b0, pol_last);
+        q_issued = n + 1;
+        const CUtensorMap* maps[2] = {job.own ? &tmK : &tmKp, job.own ? &tmV : &tmVp};
+        const uint64_t pol = job.own || sh.bt * sh.ht == 1 ? pol_first : pol_last;
+        for (int j = job.j0; j < job.j1 && ok; ++j) {
+          for (int kv = 0; kv < 2; ++kv) {
+            const int slot = it % C::kStages;
+            if (!wait_or_abort(ptx::smem_u32(&bar_kv_empty[slot]), ((it / C::kStages) & 1) ^ 1u, abort_ptr,
+                               p.timeout_ns, kRolePreProducer)) {
+              ok = false;
+              break;
+            }
+            const int me = it++;
+            if (me == p.drop_load) continue;   // test hook: this tile never arrives
+            // A V tile with rows past the length: warp 7 completes its barrier.
+            const bool tail = kv && job.own && (j + 1) * C::kBN > job.n_keys;
+            const uint32_t full = ptx::smem_u32(tail ? &bar_tail[tails++ & 3] : &bar_kv_full[slot]);
+            ptx::mbar_arrive_expect_tx(full, C::kTileBytes);
+            for (int c = 0; c < C::kChunks; ++c)
+              ptx::tma_load_4d(sKV + slot * C::kTileBytes + c * C::kChunkBytes, maps[kv], full, c * 64, j * C::kBN,
+                               job.kvh, job.own ? job.b0 : 0, pol);
+          }
+        }
+      }
+      if (!ok || *abort_ptr) {
+        if (q_issued > 0) drain_wait(q_full, (q_issued - 1) & 1, p.timeout_ns);
+        for (int r = max(0, tails - 4); r < tails; ++r)
+          drain_wait(ptx::smem_u32(&bar_tail[r & 3]), (r >> 2) & 1, p.timeout_ns);
+        for (int i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
+          if (i != p.drop_load)
+            drain_wait(ptx::smem_u32(&bar_kv_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA issuer
+    bool ok = true;
+    int it0 = 0, g = 0;       // K/V loads and key blocks of the segments before
+    auto kv_wait = [&](int it) {
+      return wait_warp_or_abort(ptx::smem_u32(&bar_kv_full[it % C::kStages]), (it / C::kStages) & 1, abort_ptr,
+                                p.timeout_ns, kRolePreMma);
+    };
+    for (int n = 0; ok; ++n) {
+      ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns, kRolePreMma);
+      if (!ok) break;
+      const int own = jobs[n & 1].own, blocks = jobs[n & 1].j1 - jobs[n & 1].j0;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
+      if (own < 0) break;
+      ok = wait_warp_or_abort(ptx::smem_u32(&bar_q_full), n & 1, abort_ptr, p.timeout_ns, kRolePreMma);
+      // Step jj: P V of block jj - 1 (P sits in the S columns), then Q K^T of block jj.
+      for (int jj = 0; jj <= blocks && ok; ++jj) {
+        const int itK = it0 + 2 * jj, itV = itK - 1;
+        if (jj > 0) {
+          ok = wait_warp_or_abort(ptx::smem_u32(&bar_p_full), (g - 1) & 1, abort_ptr, p.timeout_ns, kRolePreMma);
+          if (ok) ok = kv_wait(itV);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint64_t b_desc =
+              ptx::desc_mnmajor_sw128(sKV + (itV % C::kStages) * C::kTileBytes, C::kChunkBytes);
+          ptx::mma_ts_k128_warp<32>(tmem_base + C::kColO, tmem_base + C::kColS, ptx::desc_lo(b_desc),
+                                    ptx::desc_hi(b_desc), C::kIdescPV, jj > 1 ? 1u : 0u);
+          if (jj == blocks) ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full));
+          ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[itV % C::kStages]));
+        }
+        if (jj < blocks) {
+          ok = kv_wait(itK);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint64_t a_desc = ptx::desc_kmajor_sw128(sQ);
+          const uint64_t b_desc = ptx::desc_kmajor_sw128(sKV + (itK % C::kStages) * C::kTileBytes);
+          if constexpr (HD == 128)
+            ptx::mma_ss_k128_warp(tmem_base + C::kColS, ptx::desc_lo(a_desc), ptx::desc_lo(b_desc),
+                                  ptx::desc_hi(a_desc), p.idesc_qk, 0u);
+          else
+            ptx::mma_ss_k64_warp(tmem_base + C::kColS, ptx::desc_lo(a_desc), ptx::desc_lo(b_desc),
+                                 ptx::desc_hi(a_desc), p.idesc_qk, 0u);
+          ptx::mma_commit_warp(ptx::smem_u32(&bar_s_full));
+          ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[itK % C::kStages]));
+          if (jj == blocks - 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty));
+          ++g;
+        }
+      }
+      it0 += 2 * blocks;
+    }
+    if (!ok) {
+      ptx::mma_commit_warp(ptx::smem_u32(&bar_drain));
+      drain_wait(ptx::smem_u32(&bar_drain), 0, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 7) {
+    // ------------------------------------------------------------ tails of V tiles
+    bool ok = true;
+    int it0 = 0, tails = 0;
+    for (int n = 0; ok; ++n) {
+      ok = wait_idle_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns, kRolePreWalk);
+      if (!ok) break;
+      const int own = jobs[n & 1].own, blocks = jobs[n & 1].j1 - jobs[n & 1].j0;
+      const int have = jobs[n & 1].n_keys - (jobs[n & 1].j1 - 1) * C::kBN;    // keys in the segment's last block
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
+      if (own < 0) break;
+      it0 += 2 * blocks;
+      if (!own || have >= C::kBN) continue;    // (behind the prefix, TMA fills with zeros)
+      ok = wait_warp_or_abort(ptx::smem_u32(&bar_tail[tails & 3]), (tails >> 2) & 1, abort_ptr, p.timeout_ns,
+                              kRolePreWalk);
+      if (!ok) break;
+      ++tails;
+      // Whole 128-byte rows, so the swizzle does not matter.
+      const int slot = (it0 - 1) % C::kStages;
+      for (int c = 0; c < C::kChunks; ++c)
+        for (int i = lane; i < (C::kBN - have) * 8; i += 32)
+          reinterpret_cast<uint4*>(kv_generic + slot * C::kTileBytes + c * C::kChunkBytes + have * 128)[i] =
+              make_uint4(0u, 0u, 0u, 0u);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_kv_full[slot]));
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // ------------------------------------------------------------ segments
+    if (lane == 0) {
+      int x = x_begin, b = start_b, cum = start_cum;
+      for (int n = 0;; ++n) {
+        PreJob job;
+        job.own = -1;
+        int unit = 0, end = 0;       // the unit's number among all, its last place
+        while (x < x_end && job.own < 0) {
+          int first, len;            // its first place, its keys
+          if (x < p_total) {
+            unit = x / p_places;
+            first = unit * p_places;
+            len = sh.n_p;
+          } else {
+            const int y = x - p_total;
+            len = own_len(p, b);
+            int nu = unit_places(len);
+            while (y >= (cum + nu) * own_units_per_seq && b + 1 < sh.B) {   // on to the sequence that holds place y
+              cum += nu;
+              ++b;
+              len = own_len(p, b);
+              nu = unit_places(len);
+            }
+            if (nu == 0) break;      // (lengths that change under the call)
+            const int u = min((y - cum * own_units_per_seq) / nu, own_units_per_seq - 1);
+            unit = sh.p_units + b * own_units_per_seq + u;
+            first = p_total + cum * own_units_per_seq + u * nu;
+          }
+          const int places = unit_places(len);
+          const int from = x - first, to = min(places, from + (x_end - x));
+          x += to - from;
+          end = first + places - 1;
+          job.j0 = max(0, from - kUnitCost);
+          job.j1 = max(0, to - kUnitCost);
+          if (job.j1 <= job.j0) continue;        // only the places beside its blocks
+          job.n_keys = len;
+          if (unit < sh.p_units) {
+            const int per_head = sh.bt * sh.ht;
+            job.own = 0;
+            job.kvh = unit / per_head;
+            const int t = unit - job.kvh * per_head, tb = t / sh.ht;
+            job.b0 = tb * sh.bp;
+            job.h0 = (t - tb * sh.ht) * sh.hp;
+            job.rows = min(sh.hp, sh.G - job.h0) * sh.N_q * min(sh.bp, sh.B - job.b0);
+            job.slot = unit + static_cast<int>(blockIdx.x);
+          } else {
+            const int u = unit - sh.p_units - b * own_units_per_seq;
+            job.own = 1;
+            job.b0 = b;
+            job.kvh = u / sh.ht;
+            job.h0 = (u - job.kvh * sh.ht) * sh.hp;
+            job.rows = min(sh.hp, sh.G - job.h0) * sh.N_q;
+            job.slot = unit - sh.p_units + static_cast<int>(blockIdx.x);
+          }
+        }
+        if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
+                           kRolePreWalk))
+          break;
+        jobs[n & 1] = job;
+        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
+        if (job.own < 0) break;
+        // The CTA with a unit's first block notes its segments for the merge.
+        if (job.j0 == 0)
+          p.seg[unit] = make_int2(job.slot, line_owner(total, sh.ctas, end) - static_cast<int>(blockIdx.x) + 1);
+      }
+    }
+    __syncwarp();
   }
 
   // The merge may be scheduled now; it waits for this grid's end.

@@ -561,259 +561,9 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
   volatile int* abort_ptr = &abort_flag;
 
   if (warp >= 8) ptx::setmaxnreg_dec<C::kRegsControl>();
-  if (warp == 10) {
-    // ------------------------------------------------------------ unit fetch
-    if (p.cut) {
-      // Split keys: this CTA's piece of the line, unit by unit.
-      const VarLine line = split_line(p, static_cast<int>(gridDim.x));
-      long long x = line.bad || line.whole ? line.total : min(line.total, static_cast<long long>(blockIdx.x) * line.piece);
-      const long long end = min(line.total, x + line.piece);
-      VarJob job;
-      job.kvh = -1;
-      if (line.whole && !line.bad) direct_unit(p, &job);
-      for (int n = 0;;) {
-        if (x < end) {
-          const LineUnit v = line_find(p, line, x);
-          x = v.x1;
-          job.u = make_unit(v.s, v.u, p.tp, p.causal);
-          const LinePart part = line_part(line, v, job.u.nb1, blockIdx.x);
-          if (part.b0 >= part.b1) continue;
-          job.kvh = v.kvh;
-          job.slot = part.b0 == 0 && part.b1 == job.u.nb1 ? -1 : part.slot;
-          job.u.kv_row0 += part.b0 * 128;
-          job.u.n_kv -= part.b0 * 128;
-          job.u.lim0 -= part.b0 * 128;
-          job.u.nb0 = max(1, min(job.u.nb0, part.b1) - part.b0);
-          job.u.nb1 = part.b1 - part.b0;
-        }
-        bool got = true;
-        if (lane == 0) {
-          got = wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
-                              kRoleVarFetch);
-          if (got) {
-            jobs[n & 1] = job;
-            ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
-          }
-        }
-        if (n == 0) {
-          // (The first job waits for nothing, so every piece leaves its entry.)
-          VarCut cut;
-          cut.kvh = -1;
-          if (end < line.total) note_cut(p, line, blockIdx.x, &cut);
-          if (lane == 0) p.cut[blockIdx.x] = cut;
-        }
-        if (!__shfl_sync(0xffffffffu, got, 0) || job.kvh < 0) break;
-        job.kvh = -1;
-        ++n;
-      }
-    } else if (!p.plan) {
-      VarJob job;
-      job.kvh = -1;
-      direct_unit(p, &job);
-      if (lane == 0) {
-        jobs[0] = job;
-        jobs[1].kvh = -1;
-        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[0]));
-        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[1]));
-      }
-    } else if (lane == 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");   // the list is complete and visible
-      const int total = p.plan->num_units * p.H_kv;
-      int idx = blockIdx.x;
-      for (int n = 0;; ++n) {
-        VarJob job;
-        job.kvh = -1;
-        if (idx < total) {
-          int e;
-          place_unit(idx, p.plan->num_long, p.H_kv, p.group, &e, &job.kvh);
-          job.u = p.list[e];
-          job.slot = -1;
-        }
-        if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
-                           kRoleVarFetch))
-          break;
-        jobs[n & 1] = job;
-        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
-        if (job.kvh < 0) break;
-        // The next unit is taken when the loads of this one near their end, not
-        // at its start: a CTA in a long unit leaves the list to the others.
-        if (!wait_or_abort(ptx::smem_u32(&bar_claim), n & 1, abort_ptr, p.timeout_ns, kRoleVarFetch)) break;
-        idx = static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 8) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const uint64_t pol_q = ptx::policy_evict_first();
-      const uint64_t pol_kv = ptx::policy_evict_last();
-      int it = 0;           // K/V loads so far (the ring position runs on across units)
-      int q_issued[2] = {0, 0};
-      bool ok = true;
-      VarJob job;
-      // The next K (even it) or V tile of block j into its ring slot.
-      auto load_kv = [&](int j) {
-        const int slot = it % C::kStages;
-        if (!wait_or_abort<kPolls>(ptx::smem_u32(&bar_kv_empty[slot]), ((it / C::kStages) & 1) ^ 1u, abort_ptr,
-                                   p.timeout_ns, kRoleVarProducer))
-          return false;
-        const int me = it++;
-        if (me == p.drop_load) return true;   // test hook: this tile never arrives
-        const uint32_t full = ptx::smem_u32(&bar_kv_full[slot]);
-        ptx::mbar_arrive_expect_tx(full, C::kTileBytes);
-        const void* map = (me & 1) ? static_cast<const void*>(&tmV) : static_cast<const void*>(&tmK);
-        for (int c = 0; c < C::kChunks; ++c)
-          ptx::tma_load_3d(sKV + slot * C::kTileBytes + c * C::kChunkBytes, map, full, c * 64,
-                           job.u.kv_row0 + j * C::kBN, job.kvh, pol_kv);
-        return true;
-      };
-      for (int n = 0; ok; ++n) {
-        ok = wait_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
-                                   kRoleVarProducer);
-        if (!ok) break;
-        job = jobs[n & 1];
-        ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
-        if (job.kvh < 0) break;
-        // Each Q tile is free once its last Q K^T of the unit before has completed.
-        for (int t = 0; t < C::kQTiles && ok; ++t) {
-          if (n > 0 && !wait_or_abort<kPolls>(ptx::smem_u32(&bar_q_empty[t]), (n - 1) & 1, abort_ptr, p.timeout_ns,
-                                              kRoleVarProducer)) {
-            ok = false;
-            break;
-          }
-          const uint32_t q_full = ptx::smem_u32(&bar_q_full[t]);
-          ptx::mbar_arrive_expect_tx(q_full, C::kChunks * 128 * box_rows);
-          for (int c = 0; c < C::kChunks; ++c)
-            ptx::tma_load_3d(sQ + t * C::kTileBytes + c * C::kChunkBytes, &tmQ, q_full, c * 64, job.kvh * p.G,
-                             job.u.q_row0 + t * p.tp, pol_q);
-          q_issued[t] = n + 1;
-          if (t == 0) ok = load_kv(0) && load_kv(0);
-        }
-        if (job.u.nb1 <= 2) ptx::mbar_arrive(ptx::smem_u32(&bar_claim));
-        for (int j = 1; j < job.u.nb1 && ok; ++j) {
-          if (job.u.nb1 > 2 && j == job.u.nb1 - 2) ptx::mbar_arrive(ptx::smem_u32(&bar_claim));
-          ok = load_kv(j) && load_kv(j);
-        }
-      }
-      if (!ok || *abort_ptr) {
-        // Let every copy this thread started land before the CTA exits.
-        for (int t = 0; t < 2; ++t)
-          if (q_issued[t] > 0) drain_wait(ptx::smem_u32(&bar_q_full[t]), (q_issued[t] - 1) & 1, p.timeout_ns);
-        for (int i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
-          if (i != p.drop_load)
-            drain_wait(ptx::smem_u32(&bar_kv_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer
-    auto issue_pv_half = [&](int t, int it, bool accumulate, int half) {
-      const uint64_t b_desc = ptx::desc_mnmajor_sw128(sKV + (it % C::kStages) * C::kTileBytes, C::kChunkBytes);
-      const uint32_t d_tmem = tmem_base + C::kColO + HD * t, a_tmem = tmem_base + C::kColS + 128 * t;
-      if (half == 0)
-        ptx::mma_ts_k64half_warp<0>(d_tmem, a_tmem, ptx::desc_lo(b_desc), ptx::desc_hi(b_desc), C::kIdescPV,
-                                    accumulate ? 1u : 0u);
-      else
-        ptx::mma_ts_k64half_warp<1>(d_tmem, a_tmem, ptx::desc_lo(b_desc), ptx::desc_hi(b_desc), C::kIdescPV, 1u);
-    };
-    auto issue_qk = [&](int t, int it) {
-      const uint64_t a_desc = ptx::desc_kmajor_sw128(sQ + t * C::kTileBytes);
-      const uint64_t b_desc = ptx::desc_kmajor_sw128(sKV + (it % C::kStages) * C::kTileBytes);
-      const uint32_t d_tmem = tmem_base + C::kColS + 128 * t;
-      if constexpr (HD == 128)
-        ptx::mma_ss_k128_warp(d_tmem, ptx::desc_lo(a_desc), ptx::desc_lo(b_desc), ptx::desc_hi(a_desc), p.idesc_qk, 0u);
-      else
-        ptx::mma_ss_k64_warp(d_tmem, ptx::desc_lo(a_desc), ptx::desc_lo(b_desc), ptx::desc_hi(a_desc), p.idesc_qk, 0u);
-    };
-    bool ok = true;
-    int it0 = 0;              // K/V loads of the units before this one
-    int g[2] = {0, 0};        // key blocks of each tile so far (phases of s_full, p_half, p_full)
-    int was0 = 0, was1 = 0;   // key blocks of the unit before
-    // P V of tile t from the V tile of load it, once its probabilities are handed over.
-    auto finish_pv = [&](int t, int it, bool accumulate) {
-      const uint32_t par = static_cast<uint32_t>(g[t] - 1) & 1u;
-      if (!wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_half[t]), par, abort_ptr, p.timeout_ns, kRoleVarMma))
-        return false;
-      ptx::tc_fence_after();
-      issue_pv_half(t, it, accumulate, 0);
-      if (!wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_full[t]), par, abort_ptr, p.timeout_ns, kRoleVarMma))
-        return false;
-      ptx::tc_fence_after();
-      issue_pv_half(t, it, true, 1);
-      return true;
-    };
-    auto start_qk = [&](int t, int it) {
-      issue_qk(t, it);
-      ptx::mma_commit_warp(ptx::smem_u32(&bar_s_full[t]));
-      ++g[t];
-    };
-    for (int n = 0; ok; ++n) {
-      // The last P V of the unit before, whose epilogue then runs beside this
-      // unit's first Q K^T.
-      if (n > 0 && was0 == was1) {
-        ok = finish_pv(0, it0 - 1, was1 > 1);
-        if (!ok) break;
-        ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[0]));
-      }
-      if (n > 0) {
-        ok = finish_pv(1, it0 - 1, was1 > 1);
-        if (!ok) break;
-        ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[1]));
-        ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[(it0 - 1) % C::kStages]));
-      }
-      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
-                                      kRoleVarMma);
-      if (!ok) break;
-      const int kvh = jobs[n & 1].kvh;
-      const int nb0 = jobs[n & 1].u.nb0, nb1 = jobs[n & 1].u.nb1;
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
-      if (kvh < 0) break;
-      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_q_full[0]), n & 1, abort_ptr, p.timeout_ns, kRoleVarMma);
-      if (ok)
-        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[it0 % C::kStages]), (it0 / C::kStages) & 1,
-                                        abort_ptr, p.timeout_ns, kRoleVarMma);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      start_qk(0, it0);
-      if (nb0 == 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[0]));
-      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_q_full[1]), n & 1, abort_ptr, p.timeout_ns, kRoleVarMma);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      start_qk(1, it0);
-      ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[it0 % C::kStages]));
-      if (nb1 == 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[1]));
-      // Later blocks: K_j and V_{j-1} were waited for by the softmax warps
-      // before their first hand-off for block j - 1. Tile 1 visits every block,
-      // tile 0 all (nb0 = nb1) or all but the last.
-      for (int j = 1; j < nb1 && ok; ++j) {
-        const int itK = it0 + 2 * j;
-        ok = finish_pv(0, itK - 1, j > 1);
-        if (!ok) break;
-        if (j < nb0) {
-          start_qk(0, itK);
-          if (j == nb0 - 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[0]));
-        } else {
-          ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[0]));
-        }
-        ok = finish_pv(1, itK - 1, j > 1);
-        if (!ok) break;
-        ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[(itK - 1) % C::kStages]));
-        start_qk(1, itK);
-        ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[itK % C::kStages]));
-        if (j == nb1 - 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[1]));
-      }
-      it0 += 2 * nb1;
-      was0 = nb0;
-      was1 = nb1;
-    }
-    if (!ok) {
-      // Wait for every MMA already issued before TMEM is freed.
-      ptx::mma_commit_warp(ptx::smem_u32(&bar_drain));
-      drain_wait(ptx::smem_u32(&bar_drain), 0, p.timeout_ns);
-    }
-    __syncwarp();
-  } else if (warp < 8) {
+  // (The softmax stands first: behind the other branches the compiled kernel was
+  // 3 to 5 % slower.)
+  if (warp < 8) {
     // ------------------------------------------------------------ softmax + epilogue
     ptx::setmaxnreg_inc<C::kRegsSoftmax>();
     const int t = warp >> 2;                 // query tile
@@ -1059,6 +809,258 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
         }
       }
     }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t pol_q = ptx::policy_evict_first();
+      const uint64_t pol_kv = ptx::policy_evict_last();
+      int it = 0;           // K/V loads so far (the ring position runs on across units)
+      int q_issued[2] = {0, 0};
+      bool ok = true;
+      VarJob job;
+      // The next K (even it) or V tile of block j into its ring slot.
+      auto load_kv = [&](int j) {
+        const int slot = it % C::kStages;
+        if (!wait_or_abort<kPolls>(ptx::smem_u32(&bar_kv_empty[slot]), ((it / C::kStages) & 1) ^ 1u, abort_ptr,
+                                   p.timeout_ns, kRoleVarProducer))
+          return false;
+        const int me = it++;
+        if (me == p.drop_load) return true;   // test hook: this tile never arrives
+        const uint32_t full = ptx::smem_u32(&bar_kv_full[slot]);
+        ptx::mbar_arrive_expect_tx(full, C::kTileBytes);
+        const void* map = (me & 1) ? static_cast<const void*>(&tmV) : static_cast<const void*>(&tmK);
+        for (int c = 0; c < C::kChunks; ++c)
+          ptx::tma_load_3d(sKV + slot * C::kTileBytes + c * C::kChunkBytes, map, full, c * 64,
+                           job.u.kv_row0 + j * C::kBN, job.kvh, pol_kv);
+        return true;
+      };
+      for (int n = 0; ok; ++n) {
+        ok = wait_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
+                                   kRoleVarProducer);
+        if (!ok) break;
+        job = jobs[n & 1];
+        ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
+        if (job.kvh < 0) break;
+        // Each Q tile is free once its last Q K^T of the unit before has completed.
+        for (int t = 0; t < C::kQTiles && ok; ++t) {
+          if (n > 0 && !wait_or_abort<kPolls>(ptx::smem_u32(&bar_q_empty[t]), (n - 1) & 1, abort_ptr, p.timeout_ns,
+                                              kRoleVarProducer)) {
+            ok = false;
+            break;
+          }
+          const uint32_t q_full = ptx::smem_u32(&bar_q_full[t]);
+          ptx::mbar_arrive_expect_tx(q_full, C::kChunks * 128 * box_rows);
+          for (int c = 0; c < C::kChunks; ++c)
+            ptx::tma_load_3d(sQ + t * C::kTileBytes + c * C::kChunkBytes, &tmQ, q_full, c * 64, job.kvh * p.G,
+                             job.u.q_row0 + t * p.tp, pol_q);
+          q_issued[t] = n + 1;
+          if (t == 0) ok = load_kv(0) && load_kv(0);
+        }
+        if (job.u.nb1 <= 2) ptx::mbar_arrive(ptx::smem_u32(&bar_claim));
+        for (int j = 1; j < job.u.nb1 && ok; ++j) {
+          if (job.u.nb1 > 2 && j == job.u.nb1 - 2) ptx::mbar_arrive(ptx::smem_u32(&bar_claim));
+          ok = load_kv(j) && load_kv(j);
+        }
+      }
+      if (!ok || *abort_ptr) {
+        // Let every copy this thread started land before the CTA exits.
+        for (int t = 0; t < 2; ++t)
+          if (q_issued[t] > 0) drain_wait(ptx::smem_u32(&bar_q_full[t]), (q_issued[t] - 1) & 1, p.timeout_ns);
+        for (int i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
+          if (i != p.drop_load)
+            drain_wait(ptx::smem_u32(&bar_kv_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    auto issue_pv_half = [&](int t, int it, bool accumulate, int half) {
+      const uint64_t b_desc = ptx::desc_mnmajor_sw128(sKV + (it % C::kStages) * C::kTileBytes, C::kChunkBytes);
+      const uint32_t d_tmem = tmem_base + C::kColO + HD * t, a_tmem = tmem_base + C::kColS + 128 * t;
+      if (half == 0)
+        ptx::mma_ts_k64half_warp<0>(d_tmem, a_tmem, ptx::desc_lo(b_desc), ptx::desc_hi(b_desc), C::kIdescPV,
+                                    accumulate ? 1u : 0u);
+      else
+        ptx::mma_ts_k64half_warp<1>(d_tmem, a_tmem, ptx::desc_lo(b_desc), ptx::desc_hi(b_desc), C::kIdescPV, 1u);
+    };
+    auto issue_qk = [&](int t, int it) {
+      const uint64_t a_desc = ptx::desc_kmajor_sw128(sQ + t * C::kTileBytes);
+      const uint64_t b_desc = ptx::desc_kmajor_sw128(sKV + (it % C::kStages) * C::kTileBytes);
+      const uint32_t d_tmem = tmem_base + C::kColS + 128 * t;
+      if constexpr (HD == 128)
+        ptx::mma_ss_k128_warp(d_tmem, ptx::desc_lo(a_desc), ptx::desc_lo(b_desc), ptx::desc_hi(a_desc), p.idesc_qk, 0u);
+      else
+        ptx::mma_ss_k64_warp(d_tmem, ptx::desc_lo(a_desc), ptx::desc_lo(b_desc), ptx::desc_hi(a_desc), p.idesc_qk, 0u);
+    };
+    bool ok = true;
+    int it0 = 0;              // K/V loads of the units before this one
+    int g[2] = {0, 0};        // key blocks of each tile so far (phases of s_full, p_half, p_full)
+    int was0 = 0, was1 = 0;   // key blocks of the unit before
+    // P V of tile t from the V tile of load it, once its probabilities are handed over.
+    auto finish_pv = [&](int t, int it, bool accumulate) {
+      const uint32_t par = static_cast<uint32_t>(g[t] - 1) & 1u;
+      if (!wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_half[t]), par, abort_ptr, p.timeout_ns, kRoleVarMma))
+        return false;
+      ptx::tc_fence_after();
+      issue_pv_half(t, it, accumulate, 0);
+      if (!wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_full[t]), par, abort_ptr, p.timeout_ns, kRoleVarMma))
+        return false;
+      ptx::tc_fence_after();
+      issue_pv_half(t, it, true, 1);
+      return true;
+    };
+    auto start_qk = [&](int t, int it) {
+      issue_qk(t, it);
+      ptx::mma_commit_warp(ptx::smem_u32(&bar_s_full[t]));
+      ++g[t];
+    };
+    for (int n = 0; ok; ++n) {
+      // The last P V of the unit before, whose epilogue then runs beside this
+      // unit's first Q K^T.
+      if (n > 0 && was0 == was1) {
+        ok = finish_pv(0, it0 - 1, was1 > 1);
+        if (!ok) break;
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[0]));
+      }
+      if (n > 0) {
+        ok = finish_pv(1, it0 - 1, was1 > 1);
+        if (!ok) break;
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[1]));
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[(it0 - 1) % C::kStages]));
+      }
+      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, p.timeout_ns,
+                                      kRoleVarMma);
+      if (!ok) break;
+      const int kvh = jobs[n & 1].kvh;
+      const int nb0 = jobs[n & 1].u.nb0, nb1 = jobs[n & 1].u.nb1;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
+      if (kvh < 0) break;
+      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_q_full[0]), n & 1, abort_ptr, p.timeout_ns, kRoleVarMma);
+      if (ok)
+        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[it0 % C::kStages]), (it0 / C::kStages) & 1,
+                                        abort_ptr, p.timeout_ns, kRoleVarMma);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      start_qk(0, it0);
+      if (nb0 == 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[0]));
+      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_q_full[1]), n & 1, abort_ptr, p.timeout_ns, kRoleVarMma);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      start_qk(1, it0);
+      ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[it0 % C::kStages]));
+      if (nb1 == 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[1]));
+      // Later blocks: K_j and V_{j-1} were waited for by the softmax warps
+      // before their first hand-off for block j - 1. Tile 1 visits every block,
+      // tile 0 all (nb0 = nb1) or all but the last.
+      for (int j = 1; j < nb1 && ok; ++j) {
+        const int itK = it0 + 2 * j;
+        ok = finish_pv(0, itK - 1, j > 1);
+        if (!ok) break;
+        if (j < nb0) {
+          start_qk(0, itK);
+          if (j == nb0 - 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[0]));
+        } else {
+          ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[0]));
+        }
+        ok = finish_pv(1, itK - 1, j > 1);
+        if (!ok) break;
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[(itK - 1) % C::kStages]));
+        start_qk(1, itK);
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_kv_empty[itK % C::kStages]));
+        if (j == nb1 - 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[1]));
+      }
+      it0 += 2 * nb1;
+      was0 = nb0;
+      was1 = nb1;
+    }
+    if (!ok) {
+      // Wait for every MMA already issued before TMEM is freed.
+      ptx::mma_commit_warp(ptx::smem_u32(&bar_drain));
+      drain_wait(ptx::smem_u32(&bar_drain), 0, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ unit fetch
+    if (p.cut) {
+      // Split keys: this CTA's piece of the line, unit by unit.
+      const VarLine line = split_line(p, static_cast<int>(gridDim.x));
+      long long x = line.bad || line.whole ? line.total : min(line.total, static_cast<long long>(blockIdx.x) * line.piece);
+      const long long end = min(line.total, x + line.piece);
+      VarJob job;
+      job.kvh = -1;
+      if (line.whole && !line.bad) direct_unit(p, &job);
+      for (int n = 0;;) {
+        if (x < end) {
+          const LineUnit v = line_find(p, line, x);
+          x = v.x1;
+          job.u = make_unit(v.s, v.u, p.tp, p.causal);
+          const LinePart part = line_part(line, v, job.u.nb1, blockIdx.x);
+          if (part.b0 >= part.b1) continue;
+          job.kvh = v.kvh;
+          job.slot = part.b0 == 0 && part.b1 == job.u.nb1 ? -1 : part.slot;
+          job.u.kv_row0 += part.b0 * 128;
+          job.u.n_kv -= part.b0 * 128;
+          job.u.lim0 -= part.b0 * 128;
+          job.u.nb0 = max(1, min(job.u.nb0, part.b1) - part.b0);
+          job.u.nb1 = part.b1 - part.b0;
+        }
+        bool got = true;
+        if (lane == 0) {
+          got = wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
+                              kRoleVarFetch);
+          if (got) {
+            jobs[n & 1] = job;
+            ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
+          }
+        }
+        if (n == 0) {
+          // (The first job waits for nothing, so every piece leaves its entry.)
+          VarCut cut;
+          cut.kvh = -1;
+          if (end < line.total) note_cut(p, line, blockIdx.x, &cut);
+          if (lane == 0) p.cut[blockIdx.x] = cut;
+        }
+        if (!__shfl_sync(0xffffffffu, got, 0) || job.kvh < 0) break;
+        job.kvh = -1;
+        ++n;
+      }
+    } else if (!p.plan) {
+      VarJob job;
+      job.kvh = -1;
+      direct_unit(p, &job);
+      if (lane == 0) {
+        jobs[0] = job;
+        jobs[1].kvh = -1;
+        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[0]));
+        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[1]));
+      }
+    } else if (lane == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");   // the list is complete and visible
+      const int total = p.plan->num_units * p.H_kv;
+      int idx = blockIdx.x;
+      for (int n = 0;; ++n) {
+        VarJob job;
+        job.kvh = -1;
+        if (idx < total) {
+          int e;
+          place_unit(idx, p.plan->num_long, p.H_kv, p.group, &e, &job.kvh);
+          job.u = p.list[e];
+          job.slot = -1;
+        }
+        if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
+                           kRoleVarFetch))
+          break;
+        jobs[n & 1] = job;
+        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
+        if (job.kvh < 0) break;
+        // The next unit is taken when the loads of this one near their end, not
+        // at its start: a CTA in a long unit leaves the list to the others.
+        if (!wait_or_abort(ptx::smem_u32(&bar_claim), n & 1, abort_ptr, p.timeout_ns, kRoleVarFetch)) break;
+        idx = static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1);
+      }
+    }
+    __syncwarp();
   }
 
   // The merge of split keys may be scheduled now; it waits for this grid's end.
