@@ -20,12 +20,21 @@
 // read once per group. When G does not divide 128 the last rows of a tile
 // stay empty (126 of 128 used for G = 7).
 //
-// Work. A unit is two tiles of one (sequence, K/V head). varlen_plan_kernel
-// reads the offsets, lists the units of all sequences with the most key
-// blocks first, and zeroes a counter; the persistent grid takes units from
-// the list by that counter, so the long units start first and the short ones
-// fill the end. Lengths never reach the host: a captured call may be replayed
-// with other offsets of the same totals.
+// Work. A unit is two tiles of one (sequence, K/V head). Lengths never reach
+// the host: a captured call may be replayed with other offsets of the same
+// totals. Which of three ways the units are given out depends on sizes alone:
+//   * More units than the device holds at once: varlen_plan_kernel lists them,
+//     the most key blocks first, and the persistent grid takes them by a
+//     counter, so that the short ones fill the end.
+//   * Fewer, on at most kSplitKeys keys: CTA i finds unit i by itself; no list.
+//   * Fewer, on more keys: the keys are split too (see kSplitCost).
+//
+// What bounds it: 4 d flops per score on the tensor core against one
+// exponential, as in the forward kernel. 8192 tokens, 32 heads on 8, d = 128:
+// 312-316 us, 0.90 of the measured bf16 rate in visible scores (tensor pipe busy
+// 78 % of the cycles, exponentials 40 %; 101 MB read: Q, K and V once). Twelve
+// prompts of 1 to 2047 tokens (7914 in all): 89 us, 0.57: their scores lie in
+// fewer blocks per unit, of which the one or two on the diagonal are half empty.
 //
 // Masking. Keys past a row's limit get the score -inf before the maximum and
 // the exponential. (scale = 0 is run as 2^-126: then -inf stays -inf and a
@@ -600,8 +609,8 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
         // comes later.
         const int itV = it0 + 2 * j + 1;
         const int have = n_kv - j * C::kBN;    // keys of the sequence in this block
-          ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[itV % C::kStages]), (itV / C::kStages) & 1,
-                                          abort_ptr, p.timeout_ns, kRoleVarSoftmax);
+        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[itV % C::kStages]), (itV / C::kStages) & 1,
+                                        abort_ptr, p.timeout_ns, kRoleVarSoftmax);
         if (ok && j + 1 < nb1)
           ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_kv_full[(itV + 1) % C::kStages]),
                                           ((itV + 1) / C::kStages) & 1, abort_ptr, p.timeout_ns, kRoleVarSoftmax);
