@@ -46,6 +46,20 @@
 
 namespace fa {
 
+namespace ptx {
+
+// tma_load_3d for a 4-D map.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1, int c2,
+                                            int c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
+      : "memory");
+}
+
+}  // namespace ptx
+
 enum : unsigned int { kRolePreProducer = 23, kRolePreMma = 24, kRolePreSoftmax = 25, kRolePreWalk = 26 };
 
 // Places of a unit in the line beside its blocks: a one-block unit takes about

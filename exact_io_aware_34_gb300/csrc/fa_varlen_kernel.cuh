@@ -52,6 +52,15 @@
 
 namespace fa {
 
+namespace ptx {
+
+// Until all but the latest bulk group have read their shared memory.
+__device__ __forceinline__ void bulk_wait_group_read1() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
+
+}  // namespace ptx
+
 enum : unsigned int { kRoleVarProducer = 13, kRoleVarMma = 14, kRoleVarSoftmax = 15, kRoleVarFetch = 16 };
 
 // Words of g_status_word: 1 a wait ran out of time, 2 offsets or lengths in
