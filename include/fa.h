@@ -423,7 +423,8 @@ size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q, int T_kv, 
  * A row that sees no key gets O = 0 and LSE = -inf. Rows of no sequence
  * (behind cu_q[B]) are not written, and no value outside a sequence reaches
  * it, NaN and infinities included; within a sequence, a non-finite V row can
- * reach earlier rows of its 128-key block although they do not see it.
+ * reach rows that do not see it, up to 254 rows before those that do (its
+ * probability of zero times infinity, in the tile and key block they share).
  * With offsets that do not describe the buffers (negative, decreasing, past
  * T_q or T_kv) nothing is written, and fa_get_device_status reports
  * FA_ERR_INVALID_ARG.
@@ -544,7 +545,9 @@ size_t fa_fwd_prefix_workspace_bytes(int B, int H, int H_kv, int N_q, int N_pref
  *            128-byte aligned; overwritten. Calls that may run at the same
  *            time (other streams, graph replays) need workspaces of their own.
  * A row that sees no key gets O = 0 and LSE = -inf. Cache rows past a
- * sequence's length are never part of a result, whatever they hold. Lengths
+ * sequence's length are never part of a result, whatever they hold (with
+ * causal, a non-finite V row within it can reach the sequence's rows that do
+ * not see it). Lengths
  * outside 0 .. N_own are clamped, and reported by fa_get_device_status as
  * FA_ERR_INVALID_ARG. Two launches on `stream`, the merge of the pieces as a
  * programmatic dependent. The pieces, so the order of a row's sums, depend on

@@ -108,3 +108,20 @@ def test_calls_on_two_streams_at_once():
     for a, b, c in both:
         assert all(torch.equal(x, y) for x, y in zip(a, alone[0]))
         assert all(torch.equal(x, y) for r in (b, c) for x, y in zip(r, alone[1]))
+
+
+def test_a_non_finite_value_row_reaches_no_further_than_documented():
+    """A V row of infinities: rows more than 254 before those that see it, and other sequences, keep their bits."""
+    H, d = 4, 128
+    for G in (1, 4):
+        q, k, v = (x.cuda() for x in draw(8 + G, (1400, H, d), (1400, H // G, d), (1400, H // G, d)))
+        cu = offsets([900, 500]).cuda()
+        o, lse = fa.fa_fwd_varlen(q, k, v, cu, cu)
+        for row in (300, 511, 640):
+            bad = v.clone()
+            bad[row] = float("inf")
+            o2, lse2 = fa.fa_fwd_varlen(q, k, bad, cu, cu)
+            ok()
+            assert torch.equal(lse, lse2)
+            assert torch.equal(o[:max(0, row - 254)], o2[:max(0, row - 254)]) and torch.equal(o[900:], o2[900:])
+            assert not bool(torch.isfinite(o2[row:900].float()).any())
