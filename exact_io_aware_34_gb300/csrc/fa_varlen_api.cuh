@@ -112,6 +112,14 @@ bool varlen_fwd_direct(int B, int H, int H_kv, int T_q) {
 // most one per kSplitMin places of the longest line these sizes allow.
 int varlen_fwd_pieces(int B, int H, int H_kv, int T_q, int T_kv) {
   if (T_kv <= fa::kSplitKeys || !varlen_fwd_direct(B, H, H_kv, T_q)) return 0;
+  if (B == 1) {
+    // One sequence that fills its buffers, not causal, would be found not to need
+    // it: spare the call the finding out and the merge's empty launch (3 of 31 us).
+    const int unit_tokens = 2 * (128 / (H / H_kv));
+    const double unit = fa::kSplitCost + static_cast<double>(T_kv);
+    const double line = unit * H_kv * ((T_q - 1) / unit_tokens + 1);
+    if (unit <= std::max<double>(fa::kSplitMin, line / device_sm_count()) + fa::kSplitGain) return 0;
+  }
   const long long units = varlen_fwd_cap(B, H, H_kv, T_q) * H_kv;
   const double places = static_cast<double>(units) * (fa::kSplitCost + 256.0 + T_kv);
   return static_cast<int>(std::max<double>(units, std::min<double>(device_sm_count(), places / fa::kSplitMin + 1)));

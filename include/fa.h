@@ -391,8 +391,9 @@ typedef struct {
 /*
  * fa_fwd_varlen_workspace_bytes -- device workspace fa_fwd_varlen needs: the
  * list of its units of work (tiles of query rows), or, when the units fit the
- * device at once and T_kv is above 1536, partial results over split keys (at
- * most 2 KB per SM and head dimension: 40 MB). 0 for few units on few keys
+ * device at once and splitting their keys may pay (T_kv above 1536, and not one
+ * sequence whose units fill the device anyway), partial results over split keys
+ * (at most 2 KB per SM and head dimension: 40 MB). 0 for few units otherwise
  * (workspace may be NULL then) and for sizes it rejects. Depends on the current
  * device's SM count (148 when there is none).
  */
@@ -431,7 +432,7 @@ size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q, int T_kv, 
  * One launch on `stream`, or two, the second a programmatic dependent of the
  * first: the unit list and the attention when the units do not fit the device
  * at once; the attention and the joining of partial results when they do and
- * T_kv is above 1536. Results are the same from run to run. Where keys are
+ * their keys may be split. Results are the same from run to run. Where keys are
  * split, where they are split depends on the whole batch, and so does the last
  * bit of a row; in all other calls it depends on the row's sequence alone.
  * Limits: T_q, T_kv >= 1, H * T_q and H_kv * T_kv below 2^31, d in {64, 128},

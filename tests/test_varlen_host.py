@@ -84,6 +84,7 @@ def test_workspace_sizes(lib):
     assert need(Tq=1) == 0 and need(Tq=1, Tk=1536) == 0      # every unit at once, few keys: no list
     assert 0 < need(Tq=1, Tk=1537) < need(Tq=1, Tk=100000) < need(Tq=1, Tk=100000, d=128) < 42e6
     assert need() > 0 and need(Tk=100000) == need()
+    assert need(H=32, H_kv=4, Tq=1024, Tk=2048) == 0 < need(B=2, H=32, H_kv=4, Tq=512, Tk=2048)   # one that fills the device
     for bad in [dict(B=0), dict(H_kv=3), dict(H_kv=0), dict(H=258), dict(Tq=0), dict(Tk=0), dict(d=96)]:
         assert need(**bad) == 0
     assert fa.fa_bwd_varlen_workspace_bytes(1, 8, 2, 1, 1) > 0
