@@ -360,7 +360,8 @@ __device__ __forceinline__ void direct_unit(const VarParams& p, VarJob* job) {
 // Split keys: few units on long caches (a piece of a prompt whose beginning is
 // in the cache) would leave most of the device idle. All units lie in one line,
 // head after head, each kSplitCost places for its start and end and then one
-// place per key (up to its last row's diagonal); CTA c takes the places
+// place per key (up to its last row's diagonal; with more rows than keys the
+// count is too high, see note_cut); CTA c takes the places
 // [c P, (c + 1) P), P the line's length over the grid. A unit whose blocks
 // fall to several CTAs leaves partial results, which varlen_merge_kernel joins.
 // Where the longest unit is at most kSplitGain places longer than P, splitting
@@ -498,9 +499,15 @@ __device__ __forceinline__ void note_cut(const VarParams& p, const VarLine& line
   if (here.b0 > 0 || here.b1 == 0 || here.b1 == cut->u.nb1) return;
   cut->kvh = v.kvh;
   cut->first = c;
+  // The last piece that holds a block of it. A unit's places may go on behind its
+  // blocks, for several pieces where a causal sequence has more rows than keys
+  // (line_seq does not count the rows before the first key).
   int last = static_cast<int>((v.x1 - 1) / line.piece);
-  const LinePart end = line_part(line, v, cut->u.nb1, last);
-  cut->last = end.b0 == end.b1 ? last - 1 : last;
+  for (; last > c; --last) {
+    const LinePart end = line_part(line, v, cut->u.nb1, last);
+    if (end.b0 < end.b1) break;
+  }
+  cut->last = last;
 }
 
 template <int HD>

@@ -388,3 +388,29 @@ def test_binding_refusals():
     with pytest.raises(fa.FaError):
         x = torch.zeros(20000, 4, 64, dtype=torch.bfloat16, device="cuda")
         fa.fa_fwd_varlen(x, k, v, offsets([20000]).cuda(), cu, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+MORE_ROWS = [   # query rows, keys, heads, K/V heads, d: sequences with clearly more rows than keys
+    ([2200], [1900], 1, 1, 64), ([3000], [2000], 1, 1, 64), ([3000], [2000], 8, 8, 128), ([4500], [2000], 2, 2, 128),
+    ([222, 1433], [1856, 270], 8, 2, 64), ([1300, 300, 700], [300, 2100, 0], 6, 2, 128), ([500, 1, 2600], [40, 5000, 1700], 4, 4, 64),
+]
+
+
+@pytest.mark.parametrize("case", range(len(MORE_ROWS)))
+def test_split_keys_with_more_rows_than_keys(case):
+    """Whatever the workspace held (all ones, NaN, another call's partial results), the first rows see nothing and the
+    others what the oracle says."""
+    ql, kl, H, H_kv, d = MORE_ROWS[case]
+    T, Tk = sum(ql), sum(kl)
+    q, k, v, q2, k2 = draw(200 + case, (T, H, d), (Tk, H_kv, d), (Tk, H_kv, d), (T, H, d), (Tk, H_kv, d))
+    need = fa.fa_fwd_varlen_workspace_bytes(len(ql), H, H_kv, T, Tk, d)
+    ws = torch.empty(max(128, need), dtype=torch.uint8, device="cuda")
+    ws.fill_(0x7F)
+    a = check(q, k, v, ql, kl, True, split=True, workspace=ws)
+    ws.fill_(0xFF)
+    b = check(q, k, v, ql, kl, True, split=True, workspace=ws)
+    cq, ck = offsets(ql[::-1]).cuda(), offsets(kl[::-1]).cuda()
+    fa.fa_fwd_varlen(3 * q2.cuda(), k2.cuda(), v.cuda(), cq, ck, scale=1.0, workspace=ws)
+    c = check(q, k, v, ql, kl, True, split=True, workspace=ws)
+    for x in (b, c):
+        assert torch.equal(a[0], x[0]) and torch.equal(a[1], x[1])
