@@ -682,7 +682,8 @@ __global__ void __launch_bounds__(128)
                         long long o_sh, long long o_sn) {
   constexpr int kPer = HD / 32;     // output elements per lane: 4 or 2
   const PreShape& sh = p.s;
-  const unsigned row = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  // (Rows fit 32 bits; their threads, 32 each, do not.)
+  const unsigned row = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const int i = static_cast<int>(row % sh.N_q);
   const unsigned bh = row / sh.N_q;

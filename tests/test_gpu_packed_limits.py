@@ -125,3 +125,22 @@ def test_a_non_finite_value_row_reaches_no_further_than_documented():
             assert torch.equal(lse, lse2)
             assert torch.equal(o[:max(0, row - 254)], o2[:max(0, row - 254)]) and torch.equal(o[900:], o2[900:])
             assert not bool(torch.isfinite(o2[row:900].float()).any())
+
+
+def test_prefix_rows_past_two_to_the_27():
+    """134e6 rows: the first and the last sequences have the bits of calls on them alone. (Q's rows overlap: O, its
+    partial results and LSE take 52 GB.)"""
+    B, H, N_q, d, n = 8200, 128, 128, 64, 6
+    assert B * H * N_q > 1 << 27
+    x, k, v = (t.cuda() for t in draw(12, ((B + H + N_q) * 64,), (B, 1, 5, d), (B, 1, 5, d)))
+    view = lambda b0, b: x[64 * b0:].as_strided((b, H, N_q, d), (64, 64, 64, 1))  # noqa: E731
+    lens = torch.arange(B, device="cuda", dtype=torch.int32) % 6
+    o = torch.full((B, H, N_q, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, H, N_q), 7.0, device="cuda")
+    fa.fa_fwd_prefix(view(0, B), None, None, k, v, lens, o=o, lse=lse)
+    ok()
+    for b0 in (0, B // 2, B - n):
+        s = slice(b0, b0 + n)
+        o2, lse2 = fa.fa_fwd_prefix(view(b0, n), None, None, k[s], v[s], lens[s].contiguous())
+        ok()
+        assert torch.equal(o[s], o2) and torch.equal(lse[s], lse2)
