@@ -695,10 +695,19 @@ __global__ void __launch_bounds__(128)
   if (b >= sh.B) return;
   const int len = own_len(p, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // A unit's first slot and number of segments. A CTA that gave up on a wait has
+  // not noted the units behind it: their entries hold anything, and what is not a
+  // range of the unit's own slots counts as no segments.
+  auto segments = [&](int unit, int first_unit) {
+    const int2 s = p.seg[unit];
+    const int u = unit - first_unit;
+    const bool good = s.y > 0 && s.y <= sh.ctas && s.x >= u && s.x <= u + sh.ctas - s.y;
+    return good ? s : make_int2(u, 0);
+  };
   // Prefix segments [0, n0), own segments [n0, n): consecutive slots, one row of each.
   int2 s0 = make_int2(0, 0), s1 = make_int2(0, 0);
-  if (sh.p_units > 0) s0 = p.seg[u0];
-  if (len > 0) s1 = p.seg[u1];
+  if (sh.p_units > 0) s0 = segments(u0, 0);
+  if (len > 0) s1 = segments(u1, sh.p_units);
   const int n0 = s0.y, n = s0.y + s1.y;
   const size_t row0 = static_cast<size_t>(s0.x) * 128 + (b - tb * sh.bp) * per_seq + in_tile;
   const size_t row1 = static_cast<size_t>(s1.x) * per_seq + in_tile;

@@ -269,3 +269,26 @@ def test_binding_refusals():
     big = torch.zeros(1, 1, 129, 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(fa.FaError, match="UNSUPPORTED"):
         fa.fa_fwd_prefix(big, None, None, big, big.clone(), lens[:1], workspace=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("fill", [0x7F, 0xFF, 0x01, None])
+@pytest.mark.parametrize("n_p", [0, 300])
+def test_dropped_load_in_any_workspace(n_p, fill):
+    """Units behind the one whose load is dropped are never noted: what the workspace held there is no address."""
+    B, H, H_kv = 300, 16, 8
+    x = make(23, B, H, H_kv, 1, n_p, 40, 128)
+    dev = [None if t is None else t.cuda() for t in x]
+    kp, vp = (torch.empty(H_kv, 0, 128, dtype=torch.bfloat16, device="cuda") if t is None else t for t in dev[1:3])
+    lens = lens_of([40] * B)
+    o, lse = torch.zeros_like(dev[0]), torch.zeros(B, H, 1, device="cuda")
+    ws = torch.empty(fa.fa_fwd_prefix_workspace_bytes(B, H, H_kv, 1, n_p, 40, 128), dtype=torch.uint8, device="cuda")
+    if fill is None:
+        ws.random_(generator=torch.Generator("cuda").manual_seed(3))
+    else:
+        ws.fill_(fill)
+    args = (dev[0], kp, vp, dev[3], dev[4], lens, o, lse, 0.1, False, ws)
+    assert fa.fa_fwd_prefix_fault_test(*args, 0, 20_000_000) == fa.FA_OK
+    st, info = fa.fa_get_device_status()
+    assert st == fa.FA_ERR_TIMEOUT and 23 <= info[0] <= 26, (st, info)
+    assert fa.fa_get_device_status()[0] == fa.FA_OK
+    check(x, [40] * B)
