@@ -1143,7 +1143,9 @@ __global__ void __launch_bounds__(128) varlen_merge_kernel(const VarParams p) {
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (s0 + k < n) {
+      // A part of which the row sees nothing adds nothing, not even 0 times a NaN:
+      // its O may come from a block that no row of this tile sees.
+      if (s0 + k < n && w[k] != -INFINITY) {
         const float e = ptx::ex2_approx(w[k] - m);
         sum += e;
 #pragma unroll

@@ -144,3 +144,20 @@ def test_prefix_rows_past_two_to_the_27():
         o2, lse2 = fa.fa_fwd_prefix(view(b0, n), None, None, k[s], v[s], lens[s].contiguous())
         ok()
         assert torch.equal(o[s], o2) and torch.equal(lse[s], lse2)
+
+
+def test_a_non_finite_value_row_reaches_no_further_where_keys_are_split():
+    """As above, with a part that holds a block of which the unit's first tile sees nothing."""
+    for n_q, n_kv in ((390, 2183), (390, 2439), (390, 4231), (600, 2905)):
+        q, k, v = (x.cuda() for x in draw(n_kv, (n_q, 4, 128), (n_kv, 4, 128), (n_kv, 4, 128)))
+        cq, ck = offsets([n_q]).cuda(), offsets([n_kv]).cuda()
+        assert fa.fa_fwd_varlen_workspace_bytes(1, 4, 4, n_q, n_kv, 128) > 0
+        o, lse = fa.fa_fwd_varlen(q, k, v, cq, ck)
+        for first in (255, 300, 382):     # the first row that sees the bad one
+            bad = v.clone()
+            bad[n_kv - n_q + first] = float("inf")
+            o2, lse2 = fa.fa_fwd_varlen(q, k, bad, cq, ck)
+            ok()
+            assert torch.equal(lse, lse2)
+            assert torch.equal(o[:max(0, first - 254)], o2[:max(0, first - 254)])
+            assert not bool(torch.isfinite(o2[first:].float()).any())
