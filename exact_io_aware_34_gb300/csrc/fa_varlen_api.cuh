@@ -110,24 +110,37 @@ bool varlen_fwd_direct(int B, int H, int H_kv, int T_q) {
 
 // CTAs among which the keys of all units are split, or 0 (see split_line): at
 // most one per kSplitMin places of the longest line these sizes allow.
-int varlen_fwd_pieces(int B, int H, int H_kv, int T_q, int T_kv) {
+int varlen_fwd_pieces(int B, int H, int H_kv, int T_q, int T_kv, int causal) {
   if (T_kv <= fa::kSplitKeys || !varlen_fwd_direct(B, H, H_kv, T_q)) return 0;
   if (B == 1) {
     // One sequence that fills its buffers, not causal, would be found not to need
     // it: spare the call the finding out and the merge's empty launch (3 of 31 us).
     const int unit_tokens = 2 * (128 / (H / H_kv));
-    const double unit = fa::kSplitCost + static_cast<double>(T_kv);
-    const double line = unit * H_kv * ((T_q - 1) / unit_tokens + 1);
-    if (unit <= std::max<double>(fa::kSplitMin, line / device_sm_count()) + fa::kSplitGain) return 0;
+    const double units = (T_q - 1) / unit_tokens + 1;
+    auto gains = [&](double first, double longest, int gain) {   // places of its units, growing evenly
+      const double line = H_kv * units * (first + longest) / 2;
+      return longest > std::max<double>(fa::kSplitMin, line / device_sm_count()) + gain;
+    };
+    bool split = gains(fa::kSplitCost + static_cast<double>(T_kv), fa::kSplitCost + static_cast<double>(T_kv), fa::kSplitGain);
+    // Causal, the longest unit is up to twice the average, but joining the parts of
+    // a prompt that nearly fills the device takes as long as twelve blocks. 8 heads
+    // on 2, 4096 tokens (2385 places above the average): 47.1 us whole, 45.5 split,
+    // with d = 64 41.8 and 34.1; 16 on 4, 2048 and 2300 tokens (1200 and 1250
+    // above): 27.4 and 30.4 whole, 36.1 and 40.8 split.
+    if (causal && T_q <= T_kv) {
+      const double first = fa::kSplitCost + static_cast<double>(T_kv - T_q) + unit_tokens;
+      split |= gains(first, first + (units - 1) * unit_tokens, fa::kSplitGain + fa::kSplitGain / 2);
+    }
+    if (!split) return 0;
   }
   const long long units = varlen_fwd_cap(B, H, H_kv, T_q) * H_kv;
   const double places = static_cast<double>(units) * (fa::kSplitCost + 256.0 + T_kv);
   return static_cast<int>(std::max<double>(units, std::min<double>(device_sm_count(), places / fa::kSplitMin + 1)));
 }
 
-size_t varlen_fwd_ws(int B, int H, int H_kv, int T_q, int T_kv, int d) {
+size_t varlen_fwd_ws(int B, int H, int H_kv, int T_q, int T_kv, int d, int causal) {
   if (varlen_fwd_direct(B, H, H_kv, T_q))   // per piece two partial results of 256 rows and an entry, or nothing
-    return static_cast<size_t>(varlen_fwd_pieces(B, H, H_kv, T_q, T_kv)) *
+    return static_cast<size_t>(varlen_fwd_pieces(B, H, H_kv, T_q, T_kv, causal)) *
            (2 * 256 * (d + 1) * sizeof(float) + sizeof(fa::VarCut));
   return sizeof(fa::VarPlan) + static_cast<size_t>(varlen_fwd_cap(B, H, H_kv, T_q)) * sizeof(fa::VarUnit);
 }
@@ -169,7 +182,7 @@ fa_status_t varlen_fwd_launch(const Rows& q, const Rows& k, const Rows& v, const
 
   const long long cap = varlen_fwd_cap(B, q.heads, H_kv, q.T);
   const bool direct = varlen_fwd_direct(B, q.heads, H_kv, q.T);
-  const int pieces = varlen_fwd_pieces(B, q.heads, H_kv, q.T, k.T);
+  const int pieces = varlen_fwd_pieces(B, q.heads, H_kv, q.T, k.T, causal);
   auto* plan = direct ? nullptr : static_cast<fa::VarPlan*>(ws);
   auto* list = reinterpret_cast<fa::VarUnit*>(plan + 1);
   if (!direct) {
@@ -245,7 +258,7 @@ fa_status_t varlen_fwd_impl(const void* Q, const void* K, const void* V, void* O
   for (const void* ptr : {static_cast<const void*>(LSE), static_cast<const void*>(cu_q), static_cast<const void*>(cu_kv)})
     if (reinterpret_cast<uintptr_t>(ptr) % 4 != 0) return FA_ERR_INVALID_ARG;
   if (varlen_fwd_cap(B, H, H_kv, T_q) * H_kv >= (1LL << 31) - 65536) return FA_ERR_UNSUPPORTED;
-  const size_t need = varlen_fwd_ws(B, H, H_kv, T_q, T_kv, d), n_lse = static_cast<size_t>(H) * T_q * 4;
+  const size_t need = varlen_fwd_ws(B, H, H_kv, T_q, T_kv, d, causal), n_lse = static_cast<size_t>(H) * T_q * 4;
   const size_t n_cu = (static_cast<size_t>(B) + 1) * 4;
   if (need > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 128 != 0 || workspace_bytes < need))
     return FA_ERR_INVALID_ARG;
@@ -419,7 +432,7 @@ extern "C" {
 
 size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q, int T_kv, int d) {
   if (varlen_sizes(B, H, H_kv, T_q, T_kv, d, 1.f, 0) != FA_OK) return 0;
-  return varlen_fwd_ws(B, H, H_kv, T_q, T_kv, d);
+  return std::max(varlen_fwd_ws(B, H, H_kv, T_q, T_kv, d, 0), varlen_fwd_ws(B, H, H_kv, T_q, T_kv, d, 1));
 }
 
 fa_status_t fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, float* LSE, const int* cu_q,

@@ -414,3 +414,22 @@ def test_split_keys_with_more_rows_than_keys(case):
     c = check(q, k, v, ql, kl, True, split=True, workspace=ws)
     for x in (b, c):
         assert torch.equal(a[0], x[0]) and torch.equal(a[1], x[1])
+
+
+@pytest.mark.parametrize("H,H_kv,d", [(8, 2, 128), (8, 8, 64)])
+def test_one_causal_prompt_with_few_heads(H, H_kv, d):
+    """4096 tokens, whose units nearly fill the device and whose keys are split: rows of every block against the oracle."""
+    T = 4096
+    q, k, v = draw(43 + d, (T, H, d), (T, H_kv, d), (T, H_kv, d))
+    cu = offsets([T]).cuda()
+    ws = torch.empty(fa.fa_fwd_varlen_workspace_bytes(1, H, H_kv, T, T, d), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
+    ws.fill_(0x7F)
+    o, lse = fa.fa_fwd_varlen(q.cuda(), k.cuda(), v.cuda(), cu, cu, workspace=ws)
+    ok()
+    for i in list(range(0, T, 127)) + [T - 1]:
+        h = (i * 7) % H
+        O, L, A, _ = oracle.masked_head(parity.to64(q[i:i + 1, h]), parity.to64(k[:i + 1, h * H_kv // H]),
+                                        parity.to64(v[:i + 1, h * H_kv // H]), d ** -0.5, np.ones((1, i + 1), dtype=bool))
+        check_o(o[i:i + 1, h], O, A, split=True)
+        check_lse(lse[h, i:i + 1], L, lse_tol(q, k, d ** -0.5))

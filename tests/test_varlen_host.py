@@ -109,3 +109,15 @@ def test_binding_refuses_cpu_tensors():
         fa.fa_fwd_varlen(x, x, x, cu, cu)
     with pytest.raises(ValueError):
         fa.fa_fwd_varlen(None, x, x, cu, cu)
+
+
+def test_a_causal_prompt_that_gains_by_split_keys_has_room_for_them(lib):
+    """Units that nearly fill the device: the workspace size covers the causal call, which is split."""
+    need = fa.fa_fwd_varlen_workspace_bytes
+    for H, H_kv, T, d in ((8, 2, 4096, 128), (8, 8, 4096, 128), (8, 2, 4096, 64)):
+        n = need(1, H, H_kv, T, T, d)
+        assert 0 < n < 42e6
+        assert fwd(lib, B=1, H=H, H_kv=H_kv, Tq=T, Tk=T, d=d, n=n - 1) == BAD
+        assert fwd(lib, B=1, H=H, H_kv=H_kv, Tq=T, Tk=T, d=d, ws=0, n=0) == BAD
+    for H, H_kv, T in ((16, 4, 2048), (16, 16, 2048), (16, 4, 2300), (32, 4, 1100)):
+        assert need(1, H, H_kv, T, T, 128) == 0
