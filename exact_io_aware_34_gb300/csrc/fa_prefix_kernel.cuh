@@ -576,8 +576,8 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
       if (own < 0) break;
       it0 += 2 * blocks;
       if (!own || have >= C::kBN) continue;    // (behind the prefix, TMA fills with zeros)
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_tail[tails & 3]), (tails >> 2) & 1, abort_ptr, p.timeout_ns,
-                              kRolePreWalk);
+      ok = wait_warp_or_abort(ptx::smem_u32(&bar_tail[tails & 3]), (tails >> 2) & 1, abort_ptr,
+                              kUnitWaits * p.timeout_ns, kRolePreWalk);
       if (!ok) break;
       ++tails;
       // Whole 128-byte rows, so the swizzle does not matter.
@@ -647,8 +647,8 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
             job.slot = unit - sh.p_units + static_cast<int>(blockIdx.x);
           }
         }
-        if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
-                           kRolePreWalk))
+        if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr,
+                           kUnitWaits * p.timeout_ns, kRolePreWalk))
           break;
         jobs[n & 1] = job;
         ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));

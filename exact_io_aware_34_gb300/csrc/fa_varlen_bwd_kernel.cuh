@@ -1079,7 +1079,7 @@ __device__ __forceinline__ void varlen_bwd_tails(const VarBwdParams& p, VarBwdSh
 #pragma unroll 1
     for (int x = 0; x < 2; ++x) {
       if (!wait_warp_or_abort(ptx::smem_u32(&jobs.tail[2 * r + x][tails[r] & 3]), (tails[r] >> 2) & 1, abort_ptr,
-                              p.timeout_ns, kRoleVarDkvProducer))
+                              kUnitWaits * p.timeout_ns, kRoleVarDkvProducer))
         return;
       uint8_t* tile;
       uint64_t* full;

@@ -67,13 +67,19 @@ enum : unsigned int { kRoleVarProducer = 13, kRoleVarMma = 14, kRoleVarSoftmax =
 // device memory that do not describe the caller's buffers.
 constexpr unsigned int kStatusBadOffsets = 2;
 
+// Most waits last a step of the pipeline; those of the warps that hand out work
+// or clear tails last a whole unit (16.7 million steps, 27 s, at most), and have
+// this many times the limit. What stalls a unit stalls a step, so a role with the
+// shorter limit ends the wait by the abort flag.
+constexpr unsigned long long kUnitWaits = 64;
+
 // Warp-uniform bounded wait of a warp with time to spare: polls twice a
 // microsecond, so that it takes no issue slots from the warps beside it.
 __device__ __forceinline__ bool wait_idle_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                                    unsigned long long timeout_ns, unsigned int role) {
   const uint64_t t0 = ptx::globaltimer_ns();
   while (!__all_sync(0xffffffffu, ptx::mbar_test_wait(bar, parity))) {
-    if (__any_sync(0xffffffffu, *abort_flag != 0 || ptx::globaltimer_ns() - t0 > timeout_ns))
+    if (__any_sync(0xffffffffu, *abort_flag != 0 || ptx::globaltimer_ns() - t0 > kUnitWaits * timeout_ns))
       return wait_warp_or_abort(bar, parity, abort_flag, 0, role);   // reports it
     __nanosleep(500);
   }
@@ -1032,8 +1038,8 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
         }
         bool got = true;
         if (lane == 0) {
-          got = wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
-                              kRoleVarFetch);
+          got = wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr,
+                              kUnitWaits * p.timeout_ns, kRoleVarFetch);
           if (got) {
             jobs[n & 1] = job;
             ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
@@ -1073,15 +1079,15 @@ __global__ void __launch_bounds__(FwdCfg<HD>::kThreads, 1)
           job.u = p.list[e];
           job.slot = -1;
         }
-        if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr, p.timeout_ns,
-                           kRoleVarFetch))
+        if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr,
+                           kUnitWaits * p.timeout_ns, kRoleVarFetch))
           break;
         jobs[n & 1] = job;
         ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
         if (job.kvh < 0) break;
         // The next unit is taken when the loads of this one near their end, not
         // at its start: a CTA in a long unit leaves the list to the others.
-        if (!wait_or_abort(ptx::smem_u32(&bar_claim), n & 1, abort_ptr, p.timeout_ns, kRoleVarFetch)) break;
+        if (!wait_or_abort(ptx::smem_u32(&bar_claim), n & 1, abort_ptr, kUnitWaits * p.timeout_ns, kRoleVarFetch)) break;
         idx = static_cast<int>(gridDim.x) + atomicAdd(&p.plan->next, 1);
       }
     }

@@ -448,7 +448,8 @@ fa_status_t fa_fwd_varlen(const void* Q, const void* K, const void* V, void* O, 
 
 /*
  * fa_fwd_varlen_fault_test -- TEST HOOK, not for production use. fa_fwd_varlen
- * on contiguous tensors with every device-side wait limited to `timeout_ns`,
+ * on contiguous tensors with every device-side wait limited to `timeout_ns`
+ * (64 times that for the waits that last a whole unit of work),
  * and, when drop_load >= 0, the drop_load-th K/V tile load of every CTA
  * skipped.
  */
@@ -495,7 +496,8 @@ fa_status_t fa_bwd_varlen(const void* Q, const void* K, const void* V, const voi
 
 /*
  * fa_bwd_varlen_fault_test -- TEST HOOK, not for production use. fa_bwd_varlen
- * on contiguous tensors with every device-side wait limited to `timeout_ns`,
+ * on contiguous tensors with every device-side wait limited to `timeout_ns`
+ * (64 times that for the waits that last a whole unit of work),
  * and, when drop_load >= 0, a load skipped in every unit: in the query role the
  * drop_load-th of K_0, V_0, K_1, ..., in the key-block role the Q and dO tiles
  * of step drop_load.
@@ -568,7 +570,8 @@ fa_status_t fa_fwd_prefix(const void* Q, const void* K_prefix, const void* V_pre
 
 /*
  * fa_fwd_prefix_fault_test -- TEST HOOK, not for production use. fa_fwd_prefix
- * on contiguous tensors with every device-side wait limited to `timeout_ns`,
+ * on contiguous tensors with every device-side wait limited to `timeout_ns`
+ * (64 times that for the waits that last a whole unit of work),
  * and, when drop_load >= 0, the drop_load-th K/V tile load of every CTA
  * skipped.
  */

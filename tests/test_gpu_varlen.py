@@ -433,3 +433,17 @@ def test_one_causal_prompt_with_few_heads(H, H_kv, d):
                                         parity.to64(v[:i + 1, h * H_kv // H]), d ** -0.5, np.ones((1, i + 1), dtype=bool))
         check_o(o[i:i + 1, h], O, A, split=True)
         check_lse(lse[h, i:i + 1], L, lse_tol(q, k, d ** -0.5))
+
+
+def test_a_unit_may_last_longer_than_the_limit_of_a_wait():
+    """One unit of 3125 key blocks, each wait limited to a millisecond: the warp that hands out work waits for the whole
+    unit, and that is no timeout."""
+    q, k, v = (x.cuda() for x in draw(53, (64, 4, 64), (400_000, 2, 64), (400_000, 2, 64)))
+    cq, ck = (offsets([n] + [0] * 199).cuda() for n in (64, 400_000))     # (too many sequences to split the keys)
+    o, lse = torch.zeros_like(q), torch.zeros(4, 64, device="cuda")
+    ws = torch.empty(fa.fa_fwd_varlen_workspace_bytes(200, 4, 2, 64, 400_000, 64), dtype=torch.uint8, device="cuda")
+    o2, lse2 = fa.fa_fwd_varlen(q, k, v, cq, ck, scale=0.1)
+    ok()
+    assert fa.fa_fwd_varlen_fault_test(q, k, v, o, lse, cq, ck, 0.1, True, ws, -1, 1_000_000) == fa.FA_OK
+    ok()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)

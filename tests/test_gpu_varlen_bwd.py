@@ -218,3 +218,19 @@ def test_binding_refusals():
                dict(workspace=torch.empty(128, dtype=torch.uint8, device="cuda"))]:
         with pytest.raises(fa.FaError):
             fa.fa_bwd_varlen(q, k, v, torch.zeros_like(q), do, lse, cu, cu, **kw)
+
+
+def test_a_unit_may_last_longer_than_the_limit_of_a_wait():
+    """One key block of 20001 steps, each wait limited to two milliseconds: the warps that hand out work and clear
+    tails wait for the whole unit, and that is no timeout."""
+    n, m = 32 * 20_000 + 5, 100
+    q, k, v, do = (x.cuda() for x in draw(54, (n, 4, 64), (m, 1, 64), (m, 1, 64), (n, 4, 64)))
+    cq, ck = offsets([n]).cuda(), offsets([m]).cuda()
+    o, lse = fa.fa_fwd_varlen(q, k, v, cq, ck, scale=0.1, causal=False)
+    ref = fa.fa_bwd_varlen(q, k, v, o, do, lse, cq, ck, scale=0.1, causal=False)
+    ok()
+    g = [torch.zeros_like(x) for x in (q, k, v)]
+    ws = torch.empty(fa.fa_bwd_varlen_workspace_bytes(1, 4, 1, n, m), dtype=torch.uint8, device="cuda")
+    assert fa.fa_bwd_varlen_fault_test(q, k, v, o, do, lse, cq, ck, *g, 0.1, False, ws, -1, 2_000_000) == fa.FA_OK
+    ok()
+    assert all(torch.equal(x, y) for x, y in zip(g, ref))
