@@ -606,6 +606,7 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
             first = unit * p_places;
             len = sh.n_p;
           } else {
+            if (b >= sh.B) break;
             const int y = x - p_total;
             len = own_len(p, b);
             int nu = unit_places(len);
@@ -615,13 +616,17 @@ __global__ void __launch_bounds__(DecCfg<HD>::kThreads, DecCfg<HD>::kCtasPerSm)
               len = own_len(p, b);
               nu = unit_places(len);
             }
-            if (nu == 0) break;      // (lengths that change under the call)
+            if (nu == 0) break;
             const int u = min((y - cum * own_units_per_seq) / nu, own_units_per_seq - 1);
             unit = sh.p_units + b * own_units_per_seq + u;
             first = p_total + cum * own_units_per_seq + u * nu;
           }
           const int places = unit_places(len);
-          const int from = x - first, to = min(places, from + (x_end - x));
+          const int from = x - first;
+          // A place behind the last unit, or none that holds it (above): lengths that
+          // change under the call. What it returns is then undefined, but it ends.
+          if (from >= places) break;
+          const int to = min(places, from + (x_end - x));
           x += to - from;
           end = first + places - 1;
           job.j0 = max(0, from - kUnitCost);

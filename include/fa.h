@@ -411,7 +411,8 @@ size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q, int T_kv, 
  *            query rows [cu_q[b], cu_q[b+1]) and the keys
  *            [cu_kv[b], cu_kv[b+1]); either may be empty. They are read on
  *            the device, in stream order: the host needs no lengths, and a
- *            captured call may be replayed with other offsets.
+ *            captured call may be replayed with other offsets. They must not
+ *            change while the call runs.
  *   causal : 1: with n_q and n_kv the lengths of its sequence, row i sees the
  *            keys j <= i + n_kv - n_q (the last row sees all); 0: all n_kv.
  *   strides : NULL for contiguous tensors, else four entries (host), for Q, K,
@@ -535,7 +536,8 @@ size_t fa_fwd_prefix_workspace_bytes(int B, int H, int H_kv, int N_q, int N_pref
  *   K, V   : device, bf16 [B, H_kv, N_own, d], N_own >= 1 rows of room each, of
  *            which sequence b's first seq_lens[b] hold keys.
  *   seq_lens : device, int32 [B], 0 .. N_own, read on the device in stream
- *            order (a captured call may be replayed with other lengths).
+ *            order (a captured call may be replayed with other lengths). If
+ *            they change while the call runs, its results are undefined.
  *   LSE    : device, float32 [B, H, N_q], written (natural log).
  *   causal : 1: the N_q new tokens are the last N_q of the own cache and see
  *            each other in order: row i sees the own keys

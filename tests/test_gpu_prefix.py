@@ -292,3 +292,26 @@ def test_dropped_load_in_any_workspace(n_p, fill):
     assert st == fa.FA_ERR_TIMEOUT and 23 <= info[0] <= 26, (st, info)
     assert fa.fa_get_device_status()[0] == fa.FA_OK
     check(x, [40] * B)
+
+
+def test_lengths_that_change_under_the_call():
+    """Nobody may count on what such a call returns, but it ends, in time, and harms no other."""
+    B, room = 300, 700
+    x = make(24, B, 16, 8, 1, 200, room, 64)
+    dev = [t.cuda() for t in x]
+    g = torch.Generator("cuda").manual_seed(1)
+    good = torch.randint(0, room + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    alone = fa.fa_fwd_prefix(*dev, good)
+    lens = good.clone()
+    calls, writes, other = (torch.cuda.Stream() for _ in range(3))
+    torch.cuda.synchronize()
+    results = []
+    for _ in range(200):
+        with torch.cuda.stream(writes):
+            lens.random_(0, room + 1, generator=g)
+            lens[B // 2:] = 0
+            lens.fill_(room)
+        fa.fa_fwd_prefix(*dev, lens, stream=calls)
+        results.append(fa.fa_fwd_prefix(*dev, good, stream=other))
+    ok()
+    assert all(torch.equal(o, alone[0]) and torch.equal(lse, alone[1]) for o, lse in results)
