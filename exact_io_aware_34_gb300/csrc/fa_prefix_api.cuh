@@ -59,11 +59,12 @@ bool make_map4(CUtensorMap* m, const Cube& c, int b_row, int b_head, int b_batch
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Places of the line at most.
+// Places of the line at most, and whether they can be counted in 32 bits on the device.
 long long pre_places(const fa::PreShape& s) {
   return static_cast<long long>(s.p_units) * (s.p_blocks + fa::kUnitCost) +
          static_cast<long long>(s.B) * s.H_kv * s.ht * ((s.room + 127LL) / 128 + fa::kUnitCost);
 }
+bool places_countable(const fa::PreShape& s) { return pre_places(s) < (1LL << 31) - 65536; }
 
 fa::PreShape pre_shape(int B, int H, int H_kv, int N_q, int n_p, int room) {
   fa::PreShape s;
@@ -203,7 +204,7 @@ fa_status_t prefix_impl(const void* Q, const void* K_prefix, const void* V_prefi
   for (const void* a : {static_cast<const void*>(LSE), static_cast<const void*>(lens)})
     if (reinterpret_cast<uintptr_t>(a) % 4 != 0) return FA_ERR_INVALID_ARG;
   const fa::PreShape s = pre_shape(B, H, H_kv, N_q, n_p, room);
-  if (pre_places(s) >= (1LL << 31) - 65536) return FA_ERR_UNSUPPORTED;   // counted in 32 bits on the device
+  if (!places_countable(s)) return FA_ERR_UNSUPPORTED;
   const size_t need = pre_layout(s, d).bytes, n_lse = static_cast<size_t>(B) * H * N_q * 4;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 128 != 0 || workspace_bytes < need)
     return FA_ERR_INVALID_ARG;
@@ -227,7 +228,8 @@ extern "C" {
 
 size_t fa_fwd_prefix_workspace_bytes(int B, int H, int H_kv, int N_q, int N_prefix, int N_own, int d) {
   if (pre_sizes(B, H, H_kv, N_q, N_prefix, N_own, d) != FA_OK) return 0;
-  return pre_layout(pre_shape(B, H, H_kv, N_q, N_prefix, N_own), d).bytes;
+  const fa::PreShape s = pre_shape(B, H, H_kv, N_q, N_prefix, N_own);
+  return places_countable(s) ? pre_layout(s, d).bytes : 0;
 }
 
 fa_status_t fa_fwd_prefix(const void* Q, const void* K_prefix, const void* V_prefix, const void* K, const void* V,

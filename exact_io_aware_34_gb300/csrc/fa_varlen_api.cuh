@@ -103,6 +103,9 @@ long long varlen_fwd_cap(int B, int H, int H_kv, int T_q) {
   return T_q / (2 * tp) + static_cast<long long>(B);
 }
 
+// Whether all units of all K/V heads can be counted in 32 bits on the device.
+bool units_countable(long long units, int H_kv) { return units * H_kv < (1LL << 31) - 65536; }
+
 // Whether the grid holds every unit at once: then there is no list.
 bool varlen_fwd_direct(int B, int H, int H_kv, int T_q) {
   return varlen_fwd_cap(B, H, H_kv, T_q) * H_kv <= device_sm_count();
@@ -257,7 +260,7 @@ fa_status_t varlen_fwd_impl(const void* Q, const void* K, const void* V, void* O
     return FA_ERR_INVALID_ARG;
   for (const void* ptr : {static_cast<const void*>(LSE), static_cast<const void*>(cu_q), static_cast<const void*>(cu_kv)})
     if (reinterpret_cast<uintptr_t>(ptr) % 4 != 0) return FA_ERR_INVALID_ARG;
-  if (varlen_fwd_cap(B, H, H_kv, T_q) * H_kv >= (1LL << 31) - 65536) return FA_ERR_UNSUPPORTED;
+  if (!units_countable(varlen_fwd_cap(B, H, H_kv, T_q), H_kv)) return FA_ERR_UNSUPPORTED;
   const size_t need = varlen_fwd_ws(B, H, H_kv, T_q, T_kv, d, causal), n_lse = static_cast<size_t>(H) * T_q * 4;
   const size_t n_cu = (static_cast<size_t>(B) + 1) * 4;
   if (need > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 128 != 0 || workspace_bytes < need))
@@ -400,7 +403,7 @@ fa_status_t varlen_bwd_impl(const void* Q, const void* K, const void* V, const v
   for (const void* a : {static_cast<const void*>(LSE), static_cast<const void*>(cu_q), static_cast<const void*>(cu_kv)})
     if (reinterpret_cast<uintptr_t>(a) % 4 != 0) return FA_ERR_INVALID_ARG;
   const VarBwdLayout w = varlen_bwd_layout(B, H, H_kv, T_q, T_kv);
-  if (w.units * H_kv >= (1LL << 31) - 65536) return FA_ERR_UNSUPPORTED;
+  if (!units_countable(w.units, H_kv)) return FA_ERR_UNSUPPORTED;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 128 != 0 || workspace_bytes < w.bytes)
     return FA_ERR_INVALID_ARG;
   // dQ, dK, dV and the workspace are disjoint from every input and each other.
@@ -432,6 +435,7 @@ extern "C" {
 
 size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q, int T_kv, int d) {
   if (varlen_sizes(B, H, H_kv, T_q, T_kv, d, 1.f, 0) != FA_OK) return 0;
+  if (!units_countable(varlen_fwd_cap(B, H, H_kv, T_q), H_kv)) return 0;
   return std::max(varlen_fwd_ws(B, H, H_kv, T_q, T_kv, d, 0), varlen_fwd_ws(B, H, H_kv, T_q, T_kv, d, 1));
 }
 
@@ -453,8 +457,9 @@ fa_status_t fa_fwd_varlen_fault_test(const void* Q, const void* K, const void* V
 }
 
 size_t fa_bwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q, int T_kv) {
-  if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || H / H_kv > 128 || T_q < 1 || T_kv < 1) return 0;
-  return varlen_bwd_layout(B, H, H_kv, T_q, T_kv).bytes;
+  if (varlen_sizes(B, H, H_kv, T_q, T_kv, 64, 1.f, 0) != FA_OK) return 0;   // (the same for every d)
+  const VarBwdLayout w = varlen_bwd_layout(B, H, H_kv, T_q, T_kv);
+  return units_countable(w.units, H_kv) ? w.bytes : 0;
 }
 
 fa_status_t fa_bwd_varlen(const void* Q, const void* K, const void* V, const void* O, const void* dO,

@@ -67,3 +67,10 @@ def test_binding_refuses_cpu_tensors():
         fa.fa_fwd_prefix(x, None, None, x, x, torch.zeros(1, dtype=torch.int32))
     with pytest.raises(ValueError):
         fa.fa_fwd_prefix(None, None, None, x, x, torch.zeros(1, dtype=torch.int32))
+
+
+def test_workspace_of_rejected_sizes_is_zero(lib):
+    """More blocks in all than are counted: every sequence has three places of its own per head beside the prefix's."""
+    assert fa.fa_fwd_prefix_workspace_bytes(65535, 32768, 32768, 1, 0, 1, 64) == 0
+    assert call(lib, B=65535, H=32767, H_kv=32767, Nq=1, Np=0, room=1) == NO
+    assert fa.fa_fwd_prefix_workspace_bytes(65535, 32767, 32767, 1, 0, 1, 64) == 0

@@ -121,3 +121,12 @@ def test_a_causal_prompt_that_gains_by_split_keys_has_room_for_them(lib):
         assert fwd(lib, B=1, H=H, H_kv=H_kv, Tq=T, Tk=T, d=d, ws=0, n=0) == BAD
     for H, H_kv, T in ((16, 4, 2048), (16, 16, 2048), (16, 4, 2300), (32, 4, 1100)):
         assert need(1, H, H_kv, T, T, 128) == 0
+
+
+def test_workspace_of_rejected_sizes_is_zero(lib):
+    fwd_bytes, bwd_bytes = fa.fa_fwd_varlen_workspace_bytes, fa.fa_bwd_varlen_workspace_bytes
+    for B, H, H_kv, Tq, Tk in (((1 << 24) + 1, 8, 2, 9, 9), (1, 1 << 16, 1 << 16, 9, 9), (1, 8, 2, 1 << 28, 9),
+                               (1, 8, 2, 9, 1 << 30), (1 << 24, 4096, 4096, 9, 9)):
+        assert fwd_bytes(B, H, H_kv, Tq, Tk, 64) == 0 and bwd_bytes(B, H, H_kv, Tq, Tk) == 0
+    assert fwd(lib, B=1 << 24, H=4096, H_kv=4096, Tq=9, Tk=9) == NO
+    assert bwd(lib, B=1 << 24, H=4096, H_kv=4096, Tq=9, Tk=9) == NO
