@@ -108,7 +108,7 @@ fa_status_t pre_sizes(int B, int H, int H_kv, int N_q, int n_p, int room, int d)
   if (B > 65535 || H > 65535 || H % H_kv != 0) return FA_ERR_INVALID_ARG;
   const long long lim = 1LL << 31;
   if (static_cast<long long>(B) * H * N_q >= lim || static_cast<long long>(B) * H_kv * room >= lim ||
-      static_cast<long long>(H_kv) * n_p >= lim)
+      static_cast<long long>(H_kv) * n_p >= lim || n_p > kMaxLength || room > kMaxLength)
     return FA_ERR_INVALID_ARG;
   if ((d != 64 && d != 128) || N_q > 128 || H / H_kv > 128) return FA_ERR_UNSUPPORTED;
   return FA_OK;

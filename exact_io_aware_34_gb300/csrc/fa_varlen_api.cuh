@@ -76,12 +76,17 @@ float masked_scale_log2(float scale) {
   return std::max(static_cast<float>(std::fabs(static_cast<double>(scale)) * 1.4426950408889634074), 1.17549435e-38f);
 }
 
+// Longest T_q, T_kv, N_prefix and N_own: places and blocks behind one are counted
+// in 32 bits on the device.
+constexpr int kMaxLength = 0x7fff0000;
+
 // Sizes every entry point for packed sequences accepts.
 fa_status_t varlen_sizes(int B, int H, int H_kv, int T_q, int T_kv, int d, float scale, int causal) {
   if (B < 1 || H < 1 || H_kv < 1 || T_q < 1 || T_kv < 1 || d < 1) return FA_ERR_INVALID_ARG;
   if (B > (1 << 24) || H > 65535 || H % H_kv != 0) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(H) * T_q >= (1LL << 31) || static_cast<long long>(H_kv) * T_kv >= (1LL << 31))
     return FA_ERR_INVALID_ARG;
+  if (T_q > kMaxLength || T_kv > kMaxLength) return FA_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || (causal != 0 && causal != 1)) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (H / H_kv > 128) return FA_ERR_UNSUPPORTED;

@@ -569,7 +569,7 @@ __device__ __forceinline__ void varlen_dq_loop(const CUtensorMap& tmQ, const CUt
       if (p.causal) {
         const int tok0 = job.u.blk * p.tp;
         const int last = min(p.tp, job.u.nq - tok0) - 1;
-        limit = max(0, min(limit, tok0 + min(xr, last) + 1 + limit - job.u.nq));
+        limit = max(0, min(limit, tok0 + min(xr, last) + 1 + (limit - job.u.nq)));
       }
       return true;
     };

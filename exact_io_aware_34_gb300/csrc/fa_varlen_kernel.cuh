@@ -217,7 +217,7 @@ __device__ __forceinline__ VarUnit make_unit(const SeqSpan& s, int u, int tp, in
   r.n_tok = s.nq - x0;
   r.kv_row0 = s.kv0;
   r.n_kv = s.nkv;
-  r.lim0 = causal ? x0 + 1 + s.nkv - s.nq : s.nkv;
+  r.lim0 = causal ? x0 + 1 + (s.nkv - s.nq) : s.nkv;
   const int step = causal ? 1 : 0;
   const int last0 = min(s.nkv, r.lim0 + step * (min(tp, r.n_tok) - 1));
   const int last1 = min(s.nkv, r.lim0 + step * (min(2 * tp, r.n_tok) - 1));

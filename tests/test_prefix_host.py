@@ -69,6 +69,15 @@ def test_binding_refuses_cpu_tensors():
         fa.fa_fwd_prefix(None, None, None, x, x, torch.zeros(1, dtype=torch.int32))
 
 
+def test_lengths_whose_blocks_are_not_counted_in_32_bits_are_refused(lib):
+    size, most = fa.fa_fwd_prefix_workspace_bytes, (1 << 31) - (1 << 16)
+    for kw in (dict(Np=most + 1), dict(room=most + 1), dict(Np=(1 << 31) - 1), dict(room=(1 << 31) - 1)):
+        kw.update(B=1, H=1, H_kv=1, Nq=1)
+        assert call(lib, **kw) == BAD
+        assert size(1, 1, 1, 1, kw.get("Np", 1), kw.get("room", 1), 64) == 0
+    assert size(1, 1, 1, 1, most, 1, 64) > 0
+
+
 def test_workspace_of_rejected_sizes_is_zero(lib):
     """More blocks in all than are counted: every sequence has three places of its own per head beside the prefix's."""
     assert fa.fa_fwd_prefix_workspace_bytes(65535, 32768, 32768, 1, 0, 1, 64) == 0

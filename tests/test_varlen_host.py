@@ -123,6 +123,18 @@ def test_a_causal_prompt_that_gains_by_split_keys_has_room_for_them(lib):
         assert need(1, H, H_kv, T, T, 128) == 0
 
 
+LONG = (1 << 31) - (1 << 16)
+
+
+def test_lengths_whose_blocks_are_not_counted_in_32_bits_are_refused(lib):
+    for kw in (dict(Tq=LONG + 1), dict(Tk=LONG + 1), dict(Tq=(1 << 31) - 1), dict(Tk=(1 << 31) - 1)):
+        kw.update(B=1, H=1, H_kv=1)
+        assert fwd(lib, **kw) == BAD and bwd(lib, **kw) == BAD
+        assert fa.fa_fwd_varlen_workspace_bytes(1, 1, 1, kw.get("Tq", 1), kw.get("Tk", 1), 64) == 0
+        assert fa.fa_bwd_varlen_workspace_bytes(1, 1, 1, kw.get("Tq", 1), kw.get("Tk", 1)) == 0
+    assert fa.fa_fwd_varlen_workspace_bytes(1, 1, 1, LONG, LONG, 64) > 0
+
+
 def test_workspace_of_rejected_sizes_is_zero(lib):
     fwd_bytes, bwd_bytes = fa.fa_fwd_varlen_workspace_bytes, fa.fa_bwd_varlen_workspace_bytes
     for B, H, H_kv, Tq, Tk in (((1 << 24) + 1, 8, 2, 9, 9), (1, 1 << 16, 1 << 16, 9, 9), (1, 8, 2, 1 << 28, 9),
