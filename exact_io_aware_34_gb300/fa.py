@@ -626,7 +626,7 @@ def fa_fwd_varlen(q, k, v, cu_q, cu_kv, o=None, lse=None, scale: float | None = 
         st = load_library().fa_fwd_varlen(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), out_lse.data_ptr(), cu_q.data_ptr(),
             cu_kv.data_ptr(), B, H, H_kv, T_q, T_kv, d, _strides(dense and out_dense, q, k, v, out),
-            d ** -0.5 if scale is None else scale, bool(causal), ws_ptr, ws_bytes, _raw_stream(device))
+            d ** -0.5 if scale is None else float(scale), bool(causal), ws_ptr, ws_bytes, _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_fwd_varlen")
         return out, out_lse
@@ -677,7 +677,7 @@ def fa_bwd_varlen(q, k, v, o, do, lse, cu_q, cu_kv, dq=None, dk=None, dv=None, s
             q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(), gq.data_ptr(),
             gk.data_ptr(), gv.data_ptr(), cu_q.data_ptr(), cu_kv.data_ptr(), B, H, H_kv, T_q, T_kv, d,
             _strides(dense and q_dense and k_dense and v_dense, q, k, v, o, do, gq, gk, gv),
-            d ** -0.5 if scale is None else scale, bool(causal), ws_ptr, ws_bytes, _raw_stream(device))
+            d ** -0.5 if scale is None else float(scale), bool(causal), ws_ptr, ws_bytes, _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_bwd_varlen")
         return gq, gk, gv
@@ -740,7 +740,7 @@ def fa_fwd_prefix(q, k_prefix, v_prefix, k, v, seq_lens, o=None, lse=None, scale
         st = load_library().fa_fwd_prefix(
             q.data_ptr(), *p_ptr, k.data_ptr(), v.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), out_lse.data_ptr(),
             B, H, H_kv, N_q, N_prefix, N_own, d, _strides(dense and out_dense, q, k_prefix, v_prefix, k, v, out),
-            d ** -0.5 if scale is None else scale, bool(causal), ws_ptr, ws_bytes, _raw_stream(device))
+            d ** -0.5 if scale is None else float(scale), bool(causal), ws_ptr, ws_bytes, _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_fwd_prefix")
         return out, out_lse

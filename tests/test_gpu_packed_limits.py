@@ -1,6 +1,7 @@
 """Packed and prefix entry points at the edges of what they accept (needs a
 GB300): tensors past 2^31 elements, very many sequences, two calls at once,
 inputs that are one tensor."""
+import numpy as np
 import pytest
 import torch
 
@@ -161,3 +162,18 @@ def test_a_non_finite_value_row_reaches_no_further_where_keys_are_split():
             assert torch.equal(lse, lse2)
             assert torch.equal(o[:max(0, first - 254)], o2[:max(0, first - 254)])
             assert not bool(torch.isfinite(o2[first:].float()).any())
+
+
+def test_scale_of_any_number_type():
+    """As the other entry points take it: what float() takes."""
+    q, do = (x.cuda() for x in draw(13, (9, 4, 64), (9, 4, 64)))
+    c, = (x.cuda() for x in draw(14, (2, 4, 30, 64)))
+    cu, lens = offsets([4, 5]).cuda(), torch.tensor([30, 7], dtype=torch.int32, device="cuda")
+    for scale in (np.float32(0.25), np.float64(0.25), torch.tensor(0.25), 1):
+        o, lse = fa.fa_fwd_varlen(q, q, q, cu, cu, scale=float(scale))
+        a = (o, lse) + fa.fa_bwd_varlen(q, q, q, o, do, lse, cu, cu, scale=float(scale)) \
+            + fa.fa_fwd_prefix(c[:, :, :1], None, None, c, c, lens, scale=float(scale))
+        b = fa.fa_fwd_varlen(q, q, q, cu, cu, scale=scale) + fa.fa_bwd_varlen(q, q, q, o, do, lse, cu, cu, scale=scale) \
+            + fa.fa_fwd_prefix(c[:, :, :1], None, None, c, c, lens, scale=scale)
+        ok()
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
