@@ -447,3 +447,35 @@ def test_a_unit_may_last_longer_than_the_limit_of_a_wait():
     assert fa.fa_fwd_varlen_fault_test(q, k, v, o, lse, cq, ck, 0.1, True, ws, -1, 1_000_000) == fa.FA_OK
     ok()
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("H,H_kv", [(16, 4), (4, 4)])
+def test_long_prompts_of_64_columns(H, H_kv):
+    """Two prompts of some thousand tokens at d = 64: rows of every block against the oracle."""
+    lens, d = [6001, 3333], 64
+    T = sum(lens)
+    q, k, v = draw(44 + H, (T, H, d), (T, H_kv, d), (T, H_kv, d))
+    cu = offsets(lens).cuda()
+    o, lse = fa.fa_fwd_varlen(q.cuda(), k.cuda(), v.cuda(), cu, cu)
+    ok()
+    for at, n in zip((0, lens[0]), lens):
+        for i in list(range(0, n, 127)) + [n - 1]:
+            h, r, t = (i * 7) % H, slice(at + i, at + i + 1), slice(at, at + i + 1)
+            O, L, A, _ = oracle.masked_head(parity.to64(q[r, h]), parity.to64(k[t, h * H_kv // H]),
+                                            parity.to64(v[t, h * H_kv // H]), d ** -0.5, np.ones((1, i + 1), dtype=bool))
+            check_o(o[r, h], O, A)
+            check_lse(lse[h, r], L, lse_tol(q, k, d ** -0.5))
+
+
+def test_a_last_group_of_fewer_heads():
+    """K/V heads taken two at a time, of three: the bits of each head alone."""
+    T, d = 40_000, 128
+    q, k, v = (x.cuda() for x in draw(45, (T, 3, d), (T, 3, d), (T, 3, d)))
+    cu = offsets([T - 1000, 1000]).cuda()
+    o, lse = fa.fa_fwd_varlen(q, k, v, cu, cu)
+    ok()
+    for h in range(3):
+        s = slice(h, h + 1)
+        o1, lse1 = fa.fa_fwd_varlen(q[:, s], k[:, s], v[:, s], cu, cu)
+        ok()
+        assert torch.equal(o[:, s], o1) and torch.equal(lse[s], lse1)

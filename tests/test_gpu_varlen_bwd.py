@@ -234,3 +234,28 @@ def test_a_unit_may_last_longer_than_the_limit_of_a_wait():
     assert fa.fa_bwd_varlen_fault_test(q, k, v, o, do, lse, cq, ck, *g, 0.1, False, ws, -1, 2_000_000) == fa.FA_OK
     ok()
     assert all(torch.equal(x, y) for x, y in zip(g, ref))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,H_kv,d", [(4, 1, 128), (4, 2, 64), (2, 2, 64), (2, 2, 128)])
+def test_long_sequences(H, H_kv, d, causal):
+    """Units of one to 20 blocks, several for every CTA."""
+    ql, kl = [2500, 130, 1, 1200], [2500, 700, 64, 900]
+    T, Tk = sum(ql), sum(kl)
+    q, k, v, do = draw(60 + H + d, (T, H, d), (Tk, H_kv, d), (Tk, H_kv, d), (T, H, d))
+    check(q, k, v, do, ql, kl, causal)
+
+
+def test_a_last_group_of_fewer_heads():
+    """K/V heads taken two at a time, of three: the bits of each head alone."""
+    T, d = 20_000, 128
+    q, k, v, do = (x.cuda() for x in draw(61, *[(T, 3, d)] * 4))
+    cu = offsets([T - 1000, 1000]).cuda()
+    o, lse = fa.fa_fwd_varlen(q, k, v, cu, cu)
+    a = fa.fa_bwd_varlen(q, k, v, o, do, lse, cu, cu)
+    ok()
+    for h in range(3):
+        s = slice(h, h + 1)
+        b = fa.fa_bwd_varlen(*(x[:, s] for x in (q, k, v, o, do)), lse[s], cu, cu)
+        ok()
+        assert all(torch.equal(x[:, s], y) for x, y in zip(a, b))
