@@ -701,13 +701,14 @@ __global__ void __launch_bounds__(128)
   const int len = own_len(p, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // A unit's first slot and number of segments. A CTA that gave up on a wait has
-  // not noted the units behind it: their entries hold anything, and what is not a
-  // range of the unit's own slots counts as no segments.
+  // not noted the units behind it, and their entries hold anything: the range is
+  // clamped to the slots that the unit can have, [u, u + CTAs). (Checked with
+  // comparisons instead, two short sequences took 10.2 us, not 9.8.)
   auto segments = [&](int unit, int first_unit) {
     const int2 s = p.seg[unit];
     const int u = unit - first_unit;
-    const bool good = s.y > 0 && s.y <= sh.ctas && s.x >= u && s.x <= u + sh.ctas - s.y;
-    return good ? s : make_int2(u, 0);
+    const unsigned before = min(static_cast<unsigned>(s.x - u), static_cast<unsigned>(sh.ctas));
+    return make_int2(u + static_cast<int>(before), static_cast<int>(min(static_cast<unsigned>(s.y), sh.ctas - before)));
   };
   // Prefix segments [0, n0), own segments [n0, n): consecutive slots, one row of each.
   int2 s0 = make_int2(0, 0), s1 = make_int2(0, 0);
