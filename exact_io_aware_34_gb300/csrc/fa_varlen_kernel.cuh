@@ -410,7 +410,10 @@ __device__ __forceinline__ VarLine split_line(const VarParams& p, int pieces) { 
   long long sum = 0, most = 0;
   bool bad = false;
   for (int i = lane; i < p.B; i += 32) {
-    bad |= span_bad(p.cu_q, p.cu_kv, i, p.T_q, p.T_kv);
+    if (span_bad(p.cu_q, p.cu_kv, i, p.T_q, p.T_kv)) {   // no places: sums of such lengths can pass 2^63
+      bad = true;
+      continue;
+    }
     const LineSeq s = line_seq(p, seq_span(p.cu_q, p.cu_kv, i));
     sum += s.begin(s.nu);
     if (s.nu > 0) most = max(most, s.base + s.step * (s.nu - 1));

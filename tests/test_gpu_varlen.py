@@ -479,3 +479,19 @@ def test_a_last_group_of_fewer_heads():
         o1, lse1 = fa.fa_fwd_varlen(q[:, s], k[:, s], v[:, s], cu, cu)
         ok()
         assert torch.equal(o[:, s], o1) and torch.equal(lse[s], lse1)
+
+
+def test_bad_offsets_whose_places_pass_two_to_the_63():
+    """A first sequence of 2^31 - 1 rows whose places on the line of split keys end just below 2^63."""
+    q, k, v = (x.cuda() for x in draw(63, (40, 512, 64), (3000, 4, 64), (3000, 4, 64)))
+    assert fa.fa_fwd_varlen_workspace_bytes(2, 512, 4, 40, 3000, 64) > 0
+    o = torch.full((40, 512, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((512, 40), 3.0, device="cuda")
+    top = (1 << 31) - 1
+    for bq, bk in (([0, top, 40], [0, 2_143_188_680, 3000]), ([0, top, 40], [0, top - 300, 3000]), ([0, top, 40], [0, top, 3000])):
+        for causal in (False, True):
+            fa.fa_fwd_varlen(q, k, v, *(torch.tensor(b, dtype=torch.int32, device="cuda") for b in (bq, bk)), o=o, lse=lse,
+                             causal=causal)
+            st, info = fa.fa_get_device_status()
+            assert st == fa.FA_ERR_INVALID_ARG and info[0] == 16 and info[1] < 2, (st, info)
+    assert bool((o == 3).all()) and bool((lse == 3).all())
