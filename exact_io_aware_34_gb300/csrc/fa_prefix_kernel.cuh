@@ -29,7 +29,8 @@
 // rate; a prefix of 32768 rows for 32 answers: 41 us, 0.68). With little to read,
 // the latency of a unit's chain (loads, two products, softmax, partial result)
 // and of the merge: 64 answers on a prefix of 8192 rows 28.5 us against 10.4 of
-// reading, two answers on 500 rows 9.7 us.
+// reading, two answers on 500 rows 9.7 us. P is rounded to bf16 for P V, as in
+// fa_varlen_fwd_kernel: O is off by 0.0023 of its norm, by 0.0017 with P in float32.
 //
 // Per CTA (256 threads): warps 0-3 softmax and epilogue, warp 4 TMA producer,
 // warp 5 MMA issuer, warp 6 walks the segments one ahead and hands them to
