@@ -518,7 +518,7 @@ __device__ __forceinline__ void note_cut(const VarParams& p, const VarLine& line
   cut->first = c;
   // The last piece that holds a block of it. A unit's places may go on behind its
   // blocks, for several pieces where a causal sequence has more rows than keys
-  // (line_seq does not count the rows before the first key).
+  // (line_seq counts them as if row i saw the keys up to i).
   int last = static_cast<int>((v.x1 - 1) / line.piece);
   for (; last > c; --last) {
     const LinePart end = line_part(line, v, cut->u.nb1, last);

@@ -436,8 +436,8 @@ size_t fa_fwd_varlen_workspace_bytes(int B, int H, int H_kv, int T_q, int T_kv, 
  * their keys may be split. Results are the same from run to run. Where keys are
  * split, where they are split depends on the whole batch, and so does the last
  * bit of a row; in all other calls it depends on the row's sequence alone.
- * Limits: T_q, T_kv >= 1 and at most 2^31 - 2^16, H * T_q and H_kv * T_kv below 2^31, d in {64, 128},
- * scale finite. Q, K, V, O 16-byte, LSE and offsets 4-byte aligned; O, LSE and
+ * Limits: T_q, T_kv >= 1 and at most 2^31 - 2^16, H * T_q and H_kv * T_kv below
+ * 2^31, d in {64, 128}, scale finite. Q, K, V, O 16-byte, LSE and offsets 4-byte aligned; O, LSE and
  * the workspace overlap no input nor each other. FA_ERR_UNSUPPORTED for other
  * d or H / H_kv > 128, FA_ERR_INVALID_ARG for the rest.
  */
@@ -558,8 +558,8 @@ size_t fa_fwd_prefix_workspace_bytes(int B, int H, int H_kv, int N_q, int N_pref
  * programmatic dependent. The pieces, so the order of a row's sums, depend on
  * all lengths of the batch and the SM count; the same call gives the same bits.
  * Limits: B, H <= 65535; B * H * N_q, B * H_kv * N_own and H_kv * N_prefix below
- * 2^31, N_own and N_prefix at most 2^31 - 2^16; d in {64, 128}; scale finite. Pointers 16-byte, LSE and seq_lens 4-byte
- * aligned; O, LSE and the workspace overlap no input nor each other (judged by
+ * 2^31, N_own and N_prefix at most 2^31 - 2^16; d in {64, 128}; scale finite.
+ * Pointers 16-byte, LSE and seq_lens 4-byte aligned; O, LSE and the workspace overlap no input nor each other (judged by
  * first and last byte). FA_ERR_UNSUPPORTED for other d, N_q > 128,
  * H / H_kv > 128 or more than about 2^31 blocks of 128 keys in all,
  * FA_ERR_INVALID_ARG for the rest.
