@@ -19,6 +19,7 @@
 #include "fa_bwd_kernel.cuh"
 #include "fa_decode_kernel.cuh"
 #include "fa_fwd_kernel.cuh"
+#include "fa_paged_kernel.cuh"
 #include "fa_prefix_kernel.cuh"
 #include "fa_varlen_bwd_kernel.cuh"
 #include "fa_varlen_kernel.cuh"
@@ -1107,3 +1108,4 @@ int fa_last_cuda_error(void) { return t_last_cuda_error; }
 
 #include "fa_varlen_api.cuh"
 #include "fa_prefix_api.cuh"
+#include "fa_cache_api.cuh"

@@ -32,7 +32,8 @@ EXPORTED = ("fa_fwd", "fa_get_device_status", "fa_status_string", "fa_last_cuda_
             "fa_fwd_kv_f32", "fa_fwd_kv_f32_workspace_bytes", "fa_fwd_launch_shape",
             "fa_fwd_varlen", "fa_fwd_varlen_workspace_bytes", "fa_fwd_varlen_fault_test",
             "fa_bwd_varlen", "fa_bwd_varlen_workspace_bytes", "fa_bwd_varlen_fault_test",
-            "fa_fwd_prefix", "fa_fwd_prefix_workspace_bytes", "fa_fwd_prefix_fault_test")
+            "fa_fwd_prefix", "fa_fwd_prefix_workspace_bytes", "fa_fwd_prefix_fault_test",
+            "fa_rope_frequencies", "fa_rope", "fa_kv_append", "fa_fwd_paged", "fa_fwd_paged_workspace_bytes")
 
 _lib = None
 
@@ -45,6 +46,11 @@ class Strides(ctypes.Structure):
 class BatchStrides(ctypes.Structure):
     """fa_batch_strides_t: element strides of a tensor [B, heads, N, d]."""
     _fields_ = [("batch", ctypes.c_longlong), ("head", ctypes.c_longlong), ("row", ctypes.c_longlong)]
+
+
+class PageStrides(ctypes.Structure):
+    """fa_page_strides_t: byte strides of 8-bit pages [num_pages, H_kv, page_size, d]."""
+    _fields_ = [("page", ctypes.c_longlong), ("head", ctypes.c_longlong), ("row", ctypes.c_longlong)]
 
 
 class FaError(RuntimeError):
@@ -128,6 +134,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_fwd_prefix.restype = i
     lib.fa_fwd_prefix_fault_test.argtypes = [vp] * 8 + [i] * 7 + [f, i, vp, sz, i, u64, vp]
     lib.fa_fwd_prefix_fault_test.restype = i
+    dbl = ctypes.c_double
+    lib.fa_rope_frequencies.argtypes = [vp, i, dbl, i, dbl, dbl, dbl, dbl]
+    lib.fa_rope_frequencies.restype = i
+    lib.fa_rope.argtypes = [vp, vp, i, vp, vp, i, vp, vp, i, i, i, vp, i, i, f, vp]
+    lib.fa_rope.restype = i
+    lib.fa_kv_append.argtypes = [vp] * 13 + [i] * 9 + [vp, vp, i, f, vp]
+    lib.fa_kv_append.restype = i
+    lib.fa_fwd_paged_workspace_bytes.argtypes = [i] * 8
+    lib.fa_fwd_paged_workspace_bytes.restype = sz
+    lib.fa_fwd_paged.argtypes = [vp] * 10 + [i] * 8 + [vp, vp, f, i, vp, sz, vp]
+    lib.fa_fwd_paged.restype = i
     _lib = lib
     return lib
 
@@ -759,6 +776,217 @@ def fa_fwd_prefix_fault_test(q, k_prefix, v_prefix, k, v, seq_lens, o, lse, scal
             o.data_ptr(), lse.data_ptr(), B, H, k.shape[1], N_q, k_prefix.shape[1], k.shape[2], d, float(scale),
             bool(causal), workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(drop_load),
             int(timeout_ns), _stream_handle(stream, q.device)))
+
+
+#: how fa_rope_frequencies slows frequencies down for long contexts
+_RAMPS = {None: 0, "linear": 0, "turns": 1, "log_turns": 2}
+
+
+def fa_rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                        low_turns: float = 1.0, high_turns: float = 32.0, original: float = 4096.0, device=None):
+    """Radians per position of the rot / 2 pairs of a rotated head, float64, for
+    :func:`fa_rope` and :func:`fa_kv_append`: base^(-2 j / rot), and for contexts
+    longer than ``original``
+
+    "linear": every frequency divided by ``factor``;
+    "turns", "log_turns": a pair that turns ``high_turns`` times or more over the
+    original context keeps its frequency, one that turns ``low_turns`` times or less
+    has it divided by ``factor``, and between them both are mixed by where its
+    turns (their logarithm) lie.
+    """
+    if scaling not in _RAMPS:
+        raise ValueError(f"scaling must be one of {[k for k in _RAMPS]}")
+    out = torch.empty(max(0, int(rot)) // 2, dtype=torch.float64)
+    st = load_library().fa_rope_frequencies(out.data_ptr(), int(rot), float(base), _RAMPS[scaling],
+                                            float(factor) if scaling else 1.0, float(low_turns), float(high_turns),
+                                            float(original))
+    if st != FA_OK:
+        raise FaError(st, "fa_rope_frequencies")
+    return out if device is None else out.to(device)
+
+
+def _frequencies(inv_freq, device):
+    """Columns that these frequencies rotate."""
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 \
+            or inv_freq.device != device or not inv_freq.is_contiguous():
+        raise ValueError(f"inv_freq must be a contiguous float64 tensor [rot / 2] on {device}")
+    return 2 * inv_freq.shape[0]
+
+
+def fa_rope(x, positions, inv_freq, y=None, out=None, out_y=None, interleaved: bool = False, transpose: bool = False,
+            factor: float = 1.0, stream=None):
+    """Rotary positions of x (and y, as queries and keys) in one launch, or the
+    gradient of that.
+
+    x: bf16 [T, heads, d], y: bf16 [T, heads_y, d] or None; only d has to be
+    contiguous. positions: int32 [T]; inv_freq: float64 [rot / 2], radians per
+    position (:func:`fa_rope_frequencies`). Pairs are the columns j and
+    j + rot / 2, or with ``interleaved`` 2 j and 2 j + 1; columns from rot on are
+    copied. ``factor`` multiplies cos and sin. With ``transpose`` the transposed
+    rotation: given the gradient of the outputs it returns that of the inputs.
+    out, out_y: where the results go, x and y themselves for a rotation in place.
+    Returns out, or (out, out_y) with y.
+    """
+    T, heads, d = rows = _leading("x", x, 3)
+    device = x.device
+    dense = _bf16("x", x, device, rows)
+    heads_y, rows_y = 0, None
+    if y is not None:
+        heads_y = _leading("y", y, 3)[1]
+        rows_y = torch.Size((T, heads_y, d))
+        dense &= _bf16("y", y, device, rows_y)
+    elif out_y is not None:
+        raise ValueError("out_y comes with y")
+    _int32("positions", positions, device, T)
+    rot = _frequencies(inv_freq, device)
+
+    def run():
+        o, o_dense = _out_bf16("out", out, device, rows, x)
+        oy, oy_dense = (None, True) if y is None else _out_bf16("out_y", out_y, device, rows_y, y)
+        all_dense = dense and o_dense and oy_dense
+        st = load_library().fa_rope(
+            x.data_ptr(), o.data_ptr(), heads, None if y is None else y.data_ptr(),
+            None if y is None else oy.data_ptr(), heads_y, positions.data_ptr(), inv_freq.data_ptr(), T, d, rot,
+            _strides(all_dense, x, o, *(() if y is None else (y, oy))), bool(interleaved), bool(transpose),
+            float(factor), _raw_stream(device))
+        if st != FA_OK:
+            raise FaError(st, "fa_rope")
+        return o if y is None else (o, oy)
+
+    return _launch(run, stream, device)
+
+
+def _pages(name, t, device, shape):
+    """As _bf16, for a cache in pages of 8 bits."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float8_e4m3fn or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be a float8_e4m3fn tensor of shape {tuple(shape)} on {device}")
+    if t.is_contiguous():
+        return True
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return False
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, device, B):
+    """(pages' shape, entries of a sequence in the table, whether the pages are contiguous)."""
+    shape = _leading("k_cache", k_cache, 4)
+    dense = _pages("k_cache", k_cache, device, shape) & _pages("v_cache", v_cache, device, shape)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != shape[:2] \
+                or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor {list(shape[:2])} on {device}")
+    if not isinstance(page_table, torch.Tensor) or page_table.dtype is not torch.int32 or page_table.dim() != 2 \
+            or page_table.shape[0] != B or page_table.device != device or not page_table.is_contiguous():
+        raise ValueError(f"page_table must be a contiguous int32 tensor [{B}, max_pages] on {device}")
+    _int32("seq_lens", seq_lens, device, B)
+    return shape, page_table.shape[1], dense
+
+
+def fa_kv_append(k, v, cu_new, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, q=None, q_out=None,
+                 inv_freq=None, positions=None, interleaved: bool = False, factor: float = 1.0, stream=None):
+    """New keys and values into the pages of an 8-bit cache, the keys rotated to
+    their positions on the way, and the queries beside them; one launch.
+
+    k, v: bf16 [T, H_kv, d], packed: sequence b has the rows [cu_new[b],
+    cu_new[b+1]) (int32 CUDA [B + 1]), the last ones of its seq_lens[b] (int32 [B],
+    with the new tokens). k_cache, v_cache: float8_e4m3fn [num_pages, H_kv,
+    page_size, d]; k_scale, v_scale: float32 [num_pages, H_kv], the scale of each
+    page and head; page_table: int32 [B, max_pages]. All four are updated in place.
+    Only d has to be contiguous in q, k, v and the pages. q: bf16 [T, H, d],
+    rotated into q_out (q itself for a rotation in place). inv_freq, interleaved,
+    factor: as for :func:`fa_rope`; without inv_freq nothing is rotated.
+    positions: int32 [T], else a token's place in its sequence. See include/fa.h
+    for how scales are chosen. Lengths, offsets and pages that do not fit are left out and
+    reported by :func:`fa_get_device_status`. Returns the rotated q (q itself
+    without inv_freq), or None without q.
+    """
+    T, H_kv, d = rows = _leading("k", k, 3)
+    device = k.device
+    dense = _bf16("k", k, device, rows) & _bf16("v", v, device, rows)
+    if not isinstance(cu_new, torch.Tensor) or cu_new.dim() != 1 or cu_new.shape[0] < 2:
+        raise ValueError("cu_new must hold B + 1 offsets")
+    B = cu_new.shape[0] - 1
+    _int32("cu_new", cu_new, device, B + 1)
+    (num_pages, heads, page, d_cache), max_pages, dense_cache = _cache(k_cache, v_cache, k_scale, v_scale, page_table,
+                                                                       seq_lens, device, B)
+    if heads != H_kv or d_cache != d:
+        raise ValueError(f"the cache holds {heads} heads of {d_cache}, k has {H_kv} of {d}")
+    rot = 0 if inv_freq is None else _frequencies(inv_freq, device)
+    if positions is not None:
+        _int32("positions", positions, device, T)
+    H, rows_q = 0, None
+    if q is not None:
+        H = _leading("q", q, 3)[1]
+        rows_q = torch.Size((T, H, d))
+        dense &= _bf16("q", q, device, rows_q)
+    if q_out is not None and (q is None or not rot):
+        raise ValueError("q_out comes with q and inv_freq")
+    turn = q is not None and rot > 0
+
+    def run():
+        o, o_dense = _out_bf16("q_out", q_out, device, rows_q, q) if turn else (None, True)
+        st = load_library().fa_kv_append(
+            k.data_ptr(), v.data_ptr(), cu_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), q.data_ptr() if turn else None,
+            o.data_ptr() if turn else None, inv_freq.data_ptr() if rot else None,
+            None if positions is None else positions.data_ptr(), B, H, H_kv, T, d, num_pages, page, max_pages, rot,
+            _strides(dense and o_dense, k, v, *((q, o) if turn else ())), _strides(dense_cache, k_cache, v_cache),
+            bool(interleaved), float(factor), _raw_stream(device))
+        if st != FA_OK:
+            raise FaError(st, "fa_kv_append")
+        return o if turn else q
+
+    return _launch(run, stream, device)
+
+
+def fa_fwd_paged_workspace_bytes(B: int, H: int, H_kv: int, T_q: int, d: int, num_pages: int, page_size: int,
+                                 max_pages: int) -> int:
+    return int(load_library().fa_fwd_paged_workspace_bytes(int(B), int(H), int(H_kv), int(T_q), int(d), int(num_pages),
+                                                           int(page_size), int(max_pages)))
+
+
+def fa_fwd_paged(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_q, o=None, lse=None,
+                 scale: float | None = None, causal: bool = True, workspace=None, stream=None):
+    """Attention of new tokens over a paged 8-bit cache that holds their keys too
+    (:func:`fa_kv_append`): single tokens, drafted tokens and pieces of prompts in
+    any mixture.
+
+    q: bf16 [T_q, H, d], packed by cu_q (int32 CUDA [B + 1]). k_cache, v_cache:
+    float8_e4m3fn [num_pages, H_kv, page_size, d], H a multiple of H_kv; k_scale,
+    v_scale: float32 [num_pages, H_kv]; page_table: int32 [B, max_pages];
+    seq_lens: int32 [B]. Only d has to be contiguous in q and the pages. With
+    ``causal`` row i of n_q sees the keys j <= i + seq_lens[b] - n_q, else all
+    seq_lens[b]; a row that sees none gets o = 0 and lse = -inf. Rows of no
+    sequence are not written. Returns (o bf16 [T_q, H, d], lse float32 [H, T_q]).
+    """
+    T_q, H, d = rows = _leading("q", q, 3)
+    device = q.device
+    dense = _bf16("q", q, device, rows)
+    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise ValueError("cu_q must hold B + 1 offsets")
+    B = cu_q.shape[0] - 1
+    _int32("cu_q", cu_q, device, B + 1)
+    (num_pages, H_kv, page, d_cache), max_pages, dense_cache = _cache(k_cache, v_cache, k_scale, v_scale, page_table,
+                                                                      seq_lens, device, B)
+    if d_cache != d:
+        raise ValueError(f"the cache holds heads of {d_cache}, q of {d}")
+
+    def run():
+        out, out_dense = _out_bf16("o", o, device, rows, q)
+        out_lse = _out_lse(lse, (H, T_q), device)
+        need = _need("fa_fwd_paged_workspace_bytes", device, B, H, H_kv, T_q, d, num_pages, page, max_pages)
+        ws, ws_ptr, ws_bytes = _workspace(workspace, need, device)
+        st = load_library().fa_fwd_paged(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            page_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), out.data_ptr(), out_lse.data_ptr(), B, H,
+            H_kv, T_q, d, num_pages, page, max_pages, _strides(dense and out_dense, q, out),
+            _strides(dense_cache, k_cache, v_cache), d ** -0.5 if scale is None else float(scale), bool(causal),
+            ws_ptr, ws_bytes, _raw_stream(device))
+        if st != FA_OK:
+            raise FaError(st, "fa_fwd_paged")
+        return out, out_lse
+
+    return _launch(run, stream, device)
 
 
 def fa_bwd_fault_test(q, k, v, o, do, lse, dq, dk, dv, scale: float, workspace, drop_load: int, timeout_ns: int,

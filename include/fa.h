@@ -583,6 +583,136 @@ fa_status_t fa_fwd_prefix_fault_test(const void* Q, const void* K_prefix, const 
                                      float scale, int causal, void* workspace, size_t workspace_bytes,
                                      int drop_load, unsigned long long timeout_ns, cudaStream_t stream);
 
+/*
+ * fa_rope_frequencies -- radians per position of the rot / 2 pairs of a rotated
+ * head, on the host: inv_freq[j] = base^(-2 j / rot), slowed down for contexts
+ * longer than the one a model was trained for.
+ *   ramp   : 0: all frequencies are divided by `factor` (1: none is changed).
+ *            1, 2: a pair that turns r = original * base^(-2 j / rot) / 2 pi times over
+ *            the `original` context keeps its frequency for r >= high_turns, has it
+ *            divided by `factor` for r <= low_turns, and between the two takes the
+ *            mean of both weighted by where r (1) or ln r (2) lies between the limits.
+ * FA_ERR_INVALID_ARG for an odd or small rot, a base, factor or limit that is
+ * not positive and finite, high_turns <= low_turns or another ramp.
+ */
+fa_status_t fa_rope_frequencies(double* inv_freq, int rot, double base, int ramp, double factor, double low_turns,
+                                double high_turns, double original);
+
+/*
+ * fa_rope -- rotary positions of one or two packed tensors (queries and keys),
+ * or the gradient of that. Pair j of a head's first `rot` columns turns by the
+ * angle t = positions[token] * inv_freq[j]:
+ *     a' = factor (a cos t - b sin t),   b' = factor (a sin t + b cos t).
+ *   X, X_out : device, bf16 [T, heads, d]; Y, Y_out : bf16 [T, heads_y, d], or
+ *            heads_y = 0. An output may be its own input (the same address and
+ *            strides); else outputs overlap no input nor each other. Slices of one
+ *            projection's output may be given (their places are told apart).
+ *   positions : device, int32 [T], of any sign: angles are exact modulo one turn.
+ *   inv_freq : device, float64 [rot / 2], radians per position.
+ *   rot    : a multiple of 16, at most d; the columns behind are copied.
+ *   strides : NULL for contiguous tensors, else entries (host) for X, X_out, Y
+ *            and Y_out: positive multiples of 8 elements.
+ *   interleaved : 0: pair j is the columns j and j + rot / 2; 1: 2 j and 2 j + 1.
+ *   transpose : 1: the transposed rotation, which takes a gradient of the
+ *            outputs to the gradient of the inputs (the same factor).
+ *   factor : multiplies cos and sin (1, or what a scaled context asks for).
+ * Computed in float32, rounded once. One launch. Limits: heads, heads_y <= 65535, T * (heads + heads_y)
+ * < 2^31; d a multiple of 16, at most 256 (else FA_ERR_UNSUPPORTED). Rows 16-byte,
+ * positions 4-byte, inv_freq 8-byte aligned.
+ */
+fa_status_t fa_rope(const void* X, void* X_out, int heads, const void* Y, void* Y_out, int heads_y,
+                    const int* positions, const double* inv_freq, int T, int d, int rot, const fa_strides_t* strides,
+                    int interleaved, int transpose, float factor, cudaStream_t stream);
+
+/* Byte (= element) strides of 8-bit pages [num_pages, H_kv, page_size, d] whose d
+ * elements are contiguous. NULL in a call stands for contiguous pages. */
+typedef struct {
+  long long page;
+  long long head;
+  long long row;
+} fa_page_strides_t;
+
+/*
+ * fa_kv_append -- new keys and values into the pages of an 8-bit cache, the keys
+ * rotated to their positions on the way, and the queries beside them.
+ *   K, V   : device, bf16 [T, H_kv, d], packed: sequence b has the rows
+ *            [cu_new[b], cu_new[b+1]).
+ *   cu_new : device, int32 [B + 1], not decreasing. seq_lens : device, int32 [B],
+ *            the lengths with the new tokens: the n_b of sequence b are its last.
+ *   K_cache, V_cache : device, e4m3 [num_pages, H_kv, page_size, d], written in place;
+ *            page_size 16, 32, 64 or 128. They may be parts of one buffer.
+ *   k_scale, v_scale : device, float32 [num_pages, H_kv], read and written. A
+ *            value is its code times the scale of its page and head.
+ *   page_table : device, int32 [B, max_pages]: the page of each page_size tokens of
+ *            a sequence. Entries behind its length are not read.
+ *   Q, Q_out : device, bf16 [T, H, d], rotated like the keys (factor and all), or
+ *            NULL. Q_out may be Q.
+ *   inv_freq, rot, interleaved, factor : as for fa_rope; rot = 0 rotates nothing
+ *            (then Q is NULL). positions : device, int32 [T], or NULL: a token's
+ *            position is its place in its sequence.
+ *   strides : NULL, else entries for K, V, Q and Q_out; cache_strides : NULL, else
+ *            entries for K_cache and V_cache: positive multiples of 16.
+ * A page's scale of one head is the smallest power of two (2^-100 at least) by which the largest
+ * of the values fits 448; rounding is to nearest even, straight from float32. A
+ * page that has older rows keeps their scale if the new rows fit it, else those
+ * rows are brought to the new one (exactly, but for values that become
+ * subnormal). Values that are not finite are stored as NaN and have no part in
+ * the scale. Rows of pages behind a sequence's length keep what they hold, as do
+ * rows of Q_out of no sequence. A page that receives rows belongs to one
+ * sequence (copy shared pages first). Everything is read on the device in stream
+ * order: a captured call may be replayed with other lengths, tables and offsets.
+ * A sequence whose offsets or length do not fit (below zero, decreasing, beyond T or the
+ * table, fewer tokens than new ones) and a page outside 0 .. num_pages - 1 are left out,
+ * and reported by fa_get_device_status as FA_ERR_INVALID_ARG. One launch.
+ * Limits: B <= 2^20, H, H_kv <= 65535, T * H, T * H_kv and num_pages * H_kv below 2^31, max_pages *
+ * page_size at most 2^31 - 2^16; d in {64, 128}. Rows and pages 16-byte aligned, the rest by element. What is
+ * written overlaps nothing else that is given. FA_ERR_UNSUPPORTED for other d,
+ * page sizes and rot, FA_ERR_INVALID_ARG for the rest.
+ */
+fa_status_t fa_kv_append(const void* K, const void* V, const int* cu_new, void* K_cache, void* V_cache, float* k_scale,
+                         float* v_scale, const int* page_table, const int* seq_lens, const void* Q, void* Q_out,
+                         const double* inv_freq, const int* positions, int B, int H, int H_kv, int T, int d,
+                         int num_pages, int page_size, int max_pages, int rot, const fa_strides_t* strides,
+                         const fa_page_strides_t* cache_strides, int interleaved, float factor, cudaStream_t stream);
+
+/* fa_fwd_paged_workspace_bytes -- device workspace fa_fwd_paged needs; 0 also for
+ * sizes it rejects. Depends on the current device's SM count (148 when there is none). */
+size_t fa_fwd_paged_workspace_bytes(int B, int H, int H_kv, int T_q, int d, int num_pages, int page_size,
+                                    int max_pages);
+
+/*
+ * fa_fwd_paged -- attention of new tokens over a paged 8-bit cache that holds
+ * their keys too: single tokens of a batch of answers, drafted tokens, pieces of
+ * prompts, in any mixture.
+ *   Q, O   : device, bf16 [T_q, H, d], packed: sequence b has the rows
+ *            [cu_q[b], cu_q[b+1]); H is a multiple of H_kv with H / H_kv <= 128,
+ *            query head h attends to K/V head h / (H / H_kv).
+ *   LSE    : device, float32 [H, T_q], written (natural log).
+ *   K_cache, V_cache, k_scale, v_scale, page_table, seq_lens : as for
+ *            fa_kv_append, after it; read only. Pages may be shared by sequences. Scales are
+ *            not negative (any value, not powers of two alone).
+ *   causal : 1: the new tokens are the last of their sequence: row i of n_q sees
+ *            the keys j <= i + seq_lens[b] - n_q; 0: all seq_lens[b].
+ *   strides : NULL, else entries for Q and O; cache_strides : NULL, else entries for
+ *            K_cache and V_cache: positive multiples of 16.
+ *   workspace : device, fa_fwd_paged_workspace_bytes(...) bytes at least, 128-byte
+ *            aligned; overwritten. Calls that may run at the same time (other
+ *            streams, graph replays) need workspaces of their own.
+ * A row that sees no key gets O = 0 and LSE = -inf. Rows of no sequence are not
+ * written. Cache rows past a sequence's length are never part of a result,
+ * whatever they hold. Offsets, lengths and tables are read on the device in
+ * stream order; ones that do not fit are clamped or left out and reported by
+ * fa_get_device_status as FA_ERR_INVALID_ARG.
+ * Limits: as for fa_kv_append, T_q * H below 2^31; scale finite; O and LSE overlap
+ * nothing else that is given. FA_ERR_UNSUPPORTED for other d or page sizes and H / H_kv >
+ * 128, FA_ERR_INVALID_ARG for the rest.
+ */
+fa_status_t fa_fwd_paged(const void* Q, const void* K_cache, const void* V_cache, const float* k_scale,
+                         const float* v_scale, const int* page_table, const int* seq_lens, const int* cu_q, void* O,
+                         float* LSE, int B, int H, int H_kv, int T_q, int d, int num_pages, int page_size,
+                         int max_pages, const fa_strides_t* strides, const fa_page_strides_t* cache_strides,
+                         float scale, int causal, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

@@ -20,6 +20,13 @@ from .packed import (  # noqa: F401
     attention_prefix,
     masked_head,
 )
+from .cache import (  # noqa: F401
+    append_pages,
+    attention_paged,
+    least_scale,
+    rotate,
+    round_e4m3,
+)
 from .gqa import (  # noqa: F401
     attention_gqa,
     attention_gqa_rows,
