@@ -255,11 +255,108 @@ fa_status_t paged_sizes(int B, int H, int H_kv, int T_q, int d, int num_pages, i
   return FA_OK;
 }
 
+// 4-D map of 8-bit pages; a box is the rows of one page and head.
+bool make_page_map(CUtensorMap* m, const Pages& c) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.d), static_cast<cuuint64_t>(c.n[2]),
+                        static_cast<cuuint64_t>(c.n[1]), static_cast<cuuint64_t>(c.n[0])};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.s[2]), static_cast<cuuint64_t>(c.s[1]),
+                           static_cast<cuuint64_t>(c.s[0])};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(c.d), static_cast<cuuint32_t>(c.n[2]), 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(c.p), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, c.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of a unit's tile: 16 while the sequences' new tokens, on average, fill no more.
+int paged_rows(int B, int G, int T_q) { return static_cast<long long>(T_q) * G <= 16LL * B ? 16 : 64; }
+
+fa::PagedShape paged_shape(int B, int H, int H_kv, int T_q, int num_pages, int page, int max_pages, int causal) {
+  fa::PagedShape s;
+  const int N = paged_rows(B, H / H_kv, T_q);
+  s.B = B;
+  s.H = H;
+  s.H_kv = H_kv;
+  s.G = H / H_kv;
+  s.T_q = T_q;
+  s.hp = std::min(s.G, N);
+  s.ht = (s.G + s.hp - 1) / s.hp;
+  s.tp = s.ht == 1 ? N / s.hp : 1;
+  s.num_pages = num_pages;
+  s.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
+  s.max_pages = max_pages;
+  s.causal = causal;
+  return s;
+}
+
+// Places of the line at most (0: more than can be counted in 32 bits on the device), and the CTAs that share them.
+long long paged_places(const fa::PagedShape& s) {
+  const double units = (static_cast<double>(s.T_q / s.tp) + s.B) * s.H_kv * s.ht;
+  const double places = units * (((static_cast<long long>(s.max_pages) << s.page_shift) + 127) / 128 + fa::kPagedCost);
+  return places < 2147418112.0 ? static_cast<long long>(places) : 0;
+}
+int paged_ctas(const fa::PagedShape& s) {
+  return static_cast<int>(std::min(paged_places(s), 2LL * device_sm_count()));
+}
+
+struct PagedLayout {
+  size_t Lp, Op, bytes;    // the notes on split units are at the front
+};
+PagedLayout paged_layout(int ctas, int N, int d) {
+  PagedLayout w;
+  w.Lp = (static_cast<size_t>(ctas) * sizeof(fa::PagedSplit) + 127) / 128 * 128;
+  w.Op = w.Lp + static_cast<size_t>(2 * ctas) * N * 4;
+  w.bytes = w.Op + static_cast<size_t>(2 * ctas) * N * d * 4;
+  return w;
+}
+
+template <int HD, int N>
+fa_status_t paged_launch(const Pages& kc, const Pages& vc, const fa::PagedParams& p, cudaStream_t stream) {
+  using C = fa::PagedCfg<HD, N>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= 64) return FA_ERR_UNSUPPORTED;
+  static std::once_flag once[64];
+  static cudaError_t attr_err[64];
+  static bool regs_ok[64];
+  std::call_once(once[dev], [&] {
+    attr_err[dev] =
+        cudaFuncSetAttribute(fa::fa_paged_kernel<HD, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    // The warpgroups' register split must fit the registers the block is launched with (see the forward launch).
+    cudaFuncAttributes fattr;
+    if (attr_err[dev] == cudaSuccess) attr_err[dev] = cudaFuncGetAttributes(&fattr, fa::fa_paged_kernel<HD, N>);
+    regs_ok[dev] = attr_err[dev] == cudaSuccess && 4 * C::kRegsSoftmax + 4 * C::kRegsControl <= 8 * fattr.numRegs;
+  });
+  if (attr_err[dev] != cudaSuccess) return cuda_fail(attr_err[dev]);
+  if (!regs_ok[dev]) return FA_ERR_UNSUPPORTED;
+  CUtensorMap mk, mv;
+  if (!make_page_map(&mk, kc) || !make_page_map(&mv, vc)) return cuda_fail(cudaErrorInvalidValue);
+  fa::fa_paged_kernel<HD, N><<<static_cast<unsigned>(p.s.ctas), C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  // The merge as a programmatic dependent launch: it waits on the device.
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.s.ctas), N / 16);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, fa::paged_merge_kernel<HD, N>, p);
+  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
 fa_status_t paged_impl(const void* Q, const void* K_cache, const void* V_cache, const float* k_scale,
                        const float* v_scale, const int* page_table, const int* seq_lens, const int* cu_q, void* O,
                        float* LSE, int B, int H, int H_kv, int T_q, int d, int num_pages, int page, int max_pages,
                        const fa_strides_t* strides, const fa_page_strides_t* cache_strides, float scale, int causal,
-                       void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+                       void* workspace, size_t workspace_bytes, int drop_load,
+                       unsigned long long timeout_ns, cudaStream_t stream) {
   if (!Q || !K_cache || !V_cache || !k_scale || !v_scale || !page_table || !seq_lens || !cu_q || !O || !LSE)
     return FA_ERR_INVALID_ARG;
   const fa_status_t st = paged_sizes(B, H, H_kv, T_q, d, num_pages, page, max_pages);
@@ -276,14 +373,23 @@ fa_status_t paged_impl(const void* Q, const void* K_cache, const void* V_cache, 
       !make_pages(&vc, V_cache, num_pages, H_kv, page, d, cache_strides ? cache_strides + 1 : nullptr))
     return FA_ERR_INVALID_ARG;
   const size_t n_lse = static_cast<size_t>(H) * T_q * 4, n_scale = static_cast<size_t>(num_pages) * H_kv * 4;
-  auto clash = [&](const void* a, size_t na) { return rows_overlap(o, a, na) || overlaps(LSE, n_lse, a, na); };
+  fa::PagedParams p;
+  p.s = paged_shape(B, H, H_kv, T_q, num_pages, page, max_pages, causal);
+  if (paged_places(p.s) == 0) return FA_ERR_UNSUPPORTED;
+  p.s.ctas = paged_ctas(p.s);
+  const int N = paged_rows(B, H / H_kv, T_q);
+  const PagedLayout w = paged_layout(p.s.ctas, N, d);
+  if (!workspace || !aligned(workspace, 128) || workspace_bytes < w.bytes) return FA_ERR_INVALID_ARG;
+  auto clash = [&](const void* a, size_t na) { return rows_overlap(o, a, na) || overlaps(LSE, n_lse, a, na) ||
+                                                  overlaps(workspace, w.bytes, a, na); };
   if (rows_overlap(o, q) || rows_overlap(q, LSE, n_lse) || rows_overlap(o, LSE, n_lse) ||
+      rows_overlap(q, workspace, w.bytes) || rows_overlap(o, workspace, w.bytes) ||
+      overlaps(LSE, n_lse, workspace, w.bytes) ||
       clash(K_cache, static_cast<size_t>(kc.span())) || clash(V_cache, static_cast<size_t>(vc.span())) ||
       clash(k_scale, n_scale) || clash(v_scale, n_scale) ||
       clash(page_table, static_cast<size_t>(B) * max_pages * 4) || clash(seq_lens, static_cast<size_t>(B) * 4) ||
       clash(cu_q, (static_cast<size_t>(B) + 1) * 4))
     return FA_ERR_INVALID_ARG;
-  fa::PagedParams p;
   p.q = static_cast<const __nv_bfloat16*>(Q);
   p.o = static_cast<__nv_bfloat16*>(O);
   p.lse = LSE;
@@ -291,33 +397,22 @@ fa_status_t paged_impl(const void* Q, const void* K_cache, const void* V_cache, 
   p.q_h = q.sh;
   p.o_t = o.st;
   p.o_h = o.sh;
-  const Pages* pages[2] = {&kc, &vc};
-  for (int i = 0; i < 2; ++i) {
-    p.cache[i] = static_cast<const uint8_t*>(pages[i]->p);
-    p.c_page[i] = pages[i]->s[0];
-    p.c_head[i] = pages[i]->s[1];
-    p.c_row[i] = pages[i]->s[2];
-  }
-  p.scale[0] = k_scale;
-  p.scale[1] = v_scale;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
   p.table = page_table;
   p.lens = seq_lens;
   p.cu = cu_q;
-  p.B = B;
-  p.H = H;
-  p.H_kv = H_kv;
-  p.G = H / H_kv;
-  p.T_q = T_q;
-  p.num_pages = num_pages;
-  p.page = page;
-  p.max_pages = max_pages;
-  p.causal = causal;
+  char* ws = static_cast<char*>(workspace);
+  p.split = reinterpret_cast<fa::PagedSplit*>(ws);
+  p.Lp = reinterpret_cast<float*>(ws + w.Lp);
+  p.Op = reinterpret_cast<float*>(ws + w.Op);
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
-  const dim3 grid(static_cast<unsigned>(T_q), static_cast<unsigned>(H_kv));
-  if (d == 64) fa::fa_paged_kernel<64><<<grid, 128, 0, stream>>>(p);
-  else fa::fa_paged_kernel<128><<<grid, 128, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? FA_OK : cuda_fail(e);
+  p.keep = p.s.ht > 1 || T_q > static_cast<long long>(B) * p.s.tp;
+  p.timeout_ns = timeout_ns;
+  p.drop_load = drop_load;
+  if (d == 64)
+    return N == 16 ? paged_launch<64, 16>(kc, vc, p, stream) : paged_launch<64, 64>(kc, vc, p, stream);
+  return N == 16 ? paged_launch<128, 16>(kc, vc, p, stream) : paged_launch<128, 64>(kc, vc, p, stream);
 }
 
 }  // namespace
@@ -366,7 +461,8 @@ fa_status_t fa_kv_append(const void* K, const void* V, const int* cu_new, void* 
 size_t fa_fwd_paged_workspace_bytes(int B, int H, int H_kv, int T_q, int d, int num_pages, int page_size,
                                     int max_pages) {
   if (paged_sizes(B, H, H_kv, T_q, d, num_pages, page_size, max_pages) != FA_OK) return 0;
-  return 0;
+  const fa::PagedShape s = paged_shape(B, H, H_kv, T_q, num_pages, page_size, max_pages, 1);
+  return paged_places(s) ? paged_layout(paged_ctas(s), paged_rows(B, H / H_kv, T_q), d).bytes : 0;
 }
 
 fa_status_t fa_fwd_paged(const void* Q, const void* K_cache, const void* V_cache, const float* k_scale,
@@ -375,8 +471,20 @@ fa_status_t fa_fwd_paged(const void* Q, const void* K_cache, const void* V_cache
                          int max_pages, const fa_strides_t* strides, const fa_page_strides_t* cache_strides,
                          float scale, int causal, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   return paged_impl(Q, K_cache, V_cache, k_scale, v_scale, page_table, seq_lens, cu_q, O, LSE, B, H, H_kv, T_q, d,
-                    num_pages, page_size, max_pages, strides, cache_strides, scale, causal, workspace, workspace_bytes,
-                    stream);
+                    num_pages, page_size, max_pages, strides, cache_strides, scale, causal, workspace, workspace_bytes, -1,
+                    kDefaultTimeoutNs, stream);
+}
+
+fa_status_t fa_fwd_paged_fault_test(const void* Q, const void* K_cache, const void* V_cache, const float* k_scale,
+                                    const float* v_scale, const int* page_table, const int* seq_lens, const int* cu_q,
+                                    void* O, float* LSE, int B, int H, int H_kv, int T_q, int d, int num_pages,
+                                    int page_size, int max_pages, float scale, int causal, void* workspace,
+                                    size_t workspace_bytes, int drop_load, unsigned long long timeout_ns,
+                                    cudaStream_t stream) {
+  if (timeout_ns == 0) return FA_ERR_INVALID_ARG;
+  return paged_impl(Q, K_cache, V_cache, k_scale, v_scale, page_table, seq_lens, cu_q, O, LSE, B, H, H_kv, T_q, d,
+                    num_pages, page_size, max_pages, nullptr, nullptr, scale, causal, workspace, workspace_bytes,
+                    drop_load < 0 ? -1 : drop_load, timeout_ns, stream);
 }
 
 }  // extern "C"

@@ -33,7 +33,8 @@ EXPORTED = ("fa_fwd", "fa_get_device_status", "fa_status_string", "fa_last_cuda_
             "fa_fwd_varlen", "fa_fwd_varlen_workspace_bytes", "fa_fwd_varlen_fault_test",
             "fa_bwd_varlen", "fa_bwd_varlen_workspace_bytes", "fa_bwd_varlen_fault_test",
             "fa_fwd_prefix", "fa_fwd_prefix_workspace_bytes", "fa_fwd_prefix_fault_test",
-            "fa_rope_frequencies", "fa_rope", "fa_kv_append", "fa_fwd_paged", "fa_fwd_paged_workspace_bytes")
+            "fa_rope_frequencies", "fa_rope", "fa_kv_append", "fa_fwd_paged", "fa_fwd_paged_workspace_bytes",
+            "fa_fwd_paged_fault_test")
 
 _lib = None
 
@@ -145,6 +146,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fa_fwd_paged_workspace_bytes.restype = sz
     lib.fa_fwd_paged.argtypes = [vp] * 10 + [i] * 8 + [vp, vp, f, i, vp, sz, vp]
     lib.fa_fwd_paged.restype = i
+    lib.fa_fwd_paged_fault_test.argtypes = [vp] * 10 + [i] * 8 + [f, i, vp, sz, i, u64, vp]
+    lib.fa_fwd_paged_fault_test.restype = i
     _lib = lib
     return lib
 
@@ -987,6 +990,21 @@ def fa_fwd_paged(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu
         return out, out_lse
 
     return _launch(run, stream, device)
+
+
+def fa_fwd_paged_fault_test(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_q, o, lse, scale: float,
+                            causal: bool, workspace, drop_load: int, timeout_ns: int, stream=None) -> int:
+    """Test hook of the C ABI (see include/fa.h): returns the raw status code."""
+    T_q, H, d = q.shape
+    num_pages, H_kv, page, _ = k_cache.shape
+    lib = load_library()
+    with torch.cuda.device(q.device):
+        return int(lib.fa_fwd_paged_fault_test(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            page_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), o.data_ptr(), lse.data_ptr(),
+            cu_q.shape[0] - 1, H, H_kv, T_q, d, num_pages, page, page_table.shape[1], float(scale), bool(causal),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), int(drop_load), int(timeout_ns),
+            _stream_handle(stream, q.device)))
 
 
 def fa_bwd_fault_test(q, k, v, o, do, lse, dq, dk, dv, scale: float, workspace, drop_load: int, timeout_ns: int,

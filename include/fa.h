@@ -713,6 +713,19 @@ fa_status_t fa_fwd_paged(const void* Q, const void* K_cache, const void* V_cache
                          int max_pages, const fa_strides_t* strides, const fa_page_strides_t* cache_strides,
                          float scale, int causal, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * fa_fwd_paged_fault_test -- TEST HOOK, not for production use. fa_fwd_paged on
+ * contiguous tensors with every device-side wait limited to `timeout_ns` (64
+ * times that for the waits that last a whole unit of work), and, when drop_load
+ * >= 0, the drop_load-th tile load (K, V, K, ...) of every CTA skipped.
+ */
+fa_status_t fa_fwd_paged_fault_test(const void* Q, const void* K_cache, const void* V_cache, const float* k_scale,
+                                    const float* v_scale, const int* page_table, const int* seq_lens, const int* cu_q,
+                                    void* O, float* LSE, int B, int H, int H_kv, int T_q, int d, int num_pages,
+                                    int page_size, int max_pages, float scale, int causal, void* workspace,
+                                    size_t workspace_bytes, int drop_load, unsigned long long timeout_ns,
+                                    cudaStream_t stream);
+
 #ifdef __cplusplus
 }  /* extern "C" */
 #endif

@@ -136,6 +136,10 @@ PAGED_REFUSALS = [
     (dict(Q=A + 8), BAD), (dict(VC=A + 2 * GAP + 4), BAD), (dict(ks=A + 3 * GAP + 1), BAD), (dict(L=A + 9 * GAP + 2), BAD),
     (dict(O=A), BAD), (dict(O=A + GAP), BAD), (dict(L=A + 2 * GAP), BAD), (dict(L=A + 8 * GAP), BAD), (dict(L=A + 5 * GAP), BAD),
     (dict(O=A + 7 * GAP), BAD), (dict(st={"O": (128, 128)}), BAD), (dict(cst={"KC": (8192, 4096, 24)}), BAD),
+    (dict(ws=0), BAD), (dict(ws=A + 20 * GAP + 64), BAD), (dict(wn=1000), BAD), (dict(ws=A), BAD), (dict(ws=A + 2 * GAP), BAD),
+    (dict(ws=A + 8 * GAP), BAD), (dict(ws=A + 9 * GAP), BAD), (dict(ws=A + 5 * GAP), BAD),
+    # more places than are counted in 32 bits
+    (dict(B=1 << 20, T=1 << 20, m=1 << 20, n=9, Hk=1, H=1, page=128), NO),
 ]
 
 
@@ -149,6 +153,14 @@ def test_workspace_of_rejected_sizes_is_zero(lib):
     for bad in [(0, 8, 2, 1, 128, 9, 16, 9), (1, 8, 3, 1, 128, 9, 16, 9), (1, 8, 2, 0, 128, 9, 16, 9), (1, 8, 2, 1, 96, 9, 16, 9),
                 (1, 8, 2, 1, 128, 9, 20, 9), (1, 258, 2, 1, 128, 9, 16, 9), (1, 8, 2, 1, 128, 0, 16, 9)]:
         assert size(*bad) == 0
+    assert size(1 << 20, 1, 1, 1 << 20, 128, 9, 128, 1 << 20) == 0
+    need = size(3, 8, 2, 50, 128, 40, 32, 9)
+    assert need > 0 and paged(lib, wn=need - 1) == BAD
+
+
+def test_fault_hook_rejects_zero_timeout(lib):
+    assert lib.fa_fwd_paged_fault_test(*[A + i * GAP for i in range(10)], 1, 1, 1, 1, 64, 9, 16, 1, 0.1, 0, A + 20 * GAP,
+                                       1 << 30, 0, 0, None) == BAD
 
 
 def test_bindings_refuse_cpu_tensors():

@@ -380,3 +380,21 @@ def test_answers_token_by_token(d, page, interleaved):
     ok()
     # e4m3 moves keys and values by 2^-4 at most, 2^-5.5 of their norm on average; twice that is allowed
     assert float((o.float() - o2.float()).norm() / o2.float().norm()) < 2 * 2.0 ** -4
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [40, 1, 30]])
+@pytest.mark.parametrize("drop", [0, 1, 2, 3, 5])
+def test_a_wait_that_runs_out_is_reported(drop, new):
+    """A tile load left out: the call ends, says so, and the next one works."""
+    cache = Cache(50, [5000, 3000, 700], 2, 64, 128)
+    q = draw(15, (sum(new), 8, 128))[0].cuda()
+    dev, cu = cache.device(), i32(offsets(new))
+    ws = torch.zeros(fa.fa_fwd_paged_workspace_bytes(3, 8, 2, sum(new), 128, cache.n, 64, dev[4].shape[1]), dtype=torch.uint8,
+                     device="cuda")
+    o, lse = torch.zeros_like(q), torch.zeros(8, sum(new), device="cuda")
+    assert fa.fa_fwd_paged_fault_test(q, *dev, cu, o, lse, 0.1, True, ws, drop, 20_000_000) == fa.FA_OK
+    st, info = fa.fa_get_device_status()
+    if drop < 2:       # (with few tiles per CTA a third load is never due)
+        assert st == fa.FA_ERR_TIMEOUT and 30 <= info[0] <= 33, (st, info)
+    assert fa.fa_get_device_status()[0] == fa.FA_OK
+    check(cache, new, 8, 128, q=q.cpu())
