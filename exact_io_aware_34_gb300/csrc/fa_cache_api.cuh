@@ -270,8 +270,12 @@ bool make_page_map(CUtensorMap* m, const Pages& c) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a unit's tile: 16 while the sequences' new tokens, on average, fill no more.
-int paged_rows(int B, int G, int T_q) { return static_cast<long long>(T_q) * G <= 16LL * B ? 16 : 64; }
+// Rows of a unit: 4, 8 or 16 while the sequences' new tokens, on average, fill no more.
+int paged_rows(int B, int G, int T_q) {
+  for (int n : {4, 8, 16})
+    if (static_cast<long long>(T_q) * G <= static_cast<long long>(n) * B) return n;
+  return 64;
+}
 
 fa::PagedShape paged_shape(int B, int H, int H_kv, int T_q, int num_pages, int page, int max_pages, int causal) {
   fa::PagedShape s;
@@ -312,9 +316,33 @@ PagedLayout paged_layout(int ctas, int N, int d) {
   return w;
 }
 
+// Per kernel and device: the shared-memory opt-in, and, for a kernel whose
+// warpgroups share out registers, whether the built kernel has as many (see the forward launch).
+struct PagedKernel {
+  const void* main;
+  const void* merge;
+  int smem, threads, regs;      // regs: needed per thread at launch, 0: any
+};
+
 template <int HD, int N>
-fa_status_t paged_launch(const Pages& kc, const Pages& vc, const fa::PagedParams& p, cudaStream_t stream) {
-  using C = fa::PagedCfg<HD, N>;
+const PagedKernel& paged_kernel() {
+  if constexpr (N <= 16) {
+    using C = fa::PagedCfg<HD, N>;
+    static const PagedKernel k{reinterpret_cast<const void*>(&fa::fa_paged_kernel<HD, N>),
+                               reinterpret_cast<const void*>(&fa::paged_merge_kernel<HD, N>), C::kSmemBytes, C::kThreads, 0};
+    return k;
+  } else {
+    using C = fa::PagedWideCfg<HD, N>;
+    static const PagedKernel k{reinterpret_cast<const void*>(&fa::fa_paged_wide_kernel<HD, N>),
+                               reinterpret_cast<const void*>(&fa::paged_merge_kernel<HD, N>), C::kSmemBytes, C::kThreads,
+                               (C::kRegsSoftmax + C::kRegsControl) / 2};
+    return k;
+  }
+}
+
+template <int HD, int N>
+fa_status_t paged_launch(const Pages& kc, const Pages& vc, fa::PagedParams& p, cudaStream_t stream) {
+  const PagedKernel& k = paged_kernel<HD, N>();
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -323,32 +351,45 @@ fa_status_t paged_launch(const Pages& kc, const Pages& vc, const fa::PagedParams
   static cudaError_t attr_err[64];
   static bool regs_ok[64];
   std::call_once(once[dev], [&] {
-    attr_err[dev] =
-        cudaFuncSetAttribute(fa::fa_paged_kernel<HD, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-    // The warpgroups' register split must fit the registers the block is launched with (see the forward launch).
+    attr_err[dev] = cudaFuncSetAttribute(k.main, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem);
     cudaFuncAttributes fattr;
-    if (attr_err[dev] == cudaSuccess) attr_err[dev] = cudaFuncGetAttributes(&fattr, fa::fa_paged_kernel<HD, N>);
-    regs_ok[dev] = attr_err[dev] == cudaSuccess && 4 * C::kRegsSoftmax + 4 * C::kRegsControl <= 8 * fattr.numRegs;
+    if (attr_err[dev] == cudaSuccess) attr_err[dev] = cudaFuncGetAttributes(&fattr, k.main);
+    regs_ok[dev] = attr_err[dev] == cudaSuccess && fattr.numRegs >= k.regs;
   });
   if (attr_err[dev] != cudaSuccess) return cuda_fail(attr_err[dev]);
   if (!regs_ok[dev]) return FA_ERR_UNSUPPORTED;
   CUtensorMap mk, mv;
   if (!make_page_map(&mk, kc) || !make_page_map(&mv, vc)) return cuda_fail(cudaErrorInvalidValue);
-  fa::fa_paged_kernel<HD, N><<<static_cast<unsigned>(p.s.ctas), C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.s.ctas));
+  cfg.blockDim = dim3(static_cast<unsigned>(k.threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(k.smem);
+  cfg.stream = stream;
+  void* args[3] = {&mk, &mv, &p};
+  e = cudaLaunchKernelExC(&cfg, k.main, args);
   if (e != cudaSuccess) return cuda_fail(e);
   // The merge as a programmatic dependent launch: it waits on the device.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.s.ctas), N / 16);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.s.ctas), static_cast<unsigned>((N + 15) / 16));
   cfg.blockDim = dim3(128);
-  cfg.stream = stream;
+  cfg.dynamicSmemBytes = 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fa::paged_merge_kernel<HD, N>, p);
+  void* merge_args[1] = {&p};
+  e = cudaLaunchKernelExC(&cfg, k.merge, merge_args);
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
+}
+
+template <int HD>
+fa_status_t paged_launch_rows(int N, const Pages& kc, const Pages& vc, fa::PagedParams& p, cudaStream_t stream) {
+  switch (N) {
+    case 4: return paged_launch<HD, 4>(kc, vc, p, stream);
+    case 8: return paged_launch<HD, 8>(kc, vc, p, stream);
+    case 16: return paged_launch<HD, 16>(kc, vc, p, stream);
+    default: return paged_launch<HD, 64>(kc, vc, p, stream);
+  }
 }
 
 fa_status_t paged_impl(const void* Q, const void* K_cache, const void* V_cache, const float* k_scale,
@@ -410,9 +451,7 @@ fa_status_t paged_impl(const void* Q, const void* K_cache, const void* V_cache, 
   p.keep = p.s.ht > 1 || T_q > static_cast<long long>(B) * p.s.tp;
   p.timeout_ns = timeout_ns;
   p.drop_load = drop_load;
-  if (d == 64)
-    return N == 16 ? paged_launch<64, 16>(kc, vc, p, stream) : paged_launch<64, 64>(kc, vc, p, stream);
-  return N == 16 ? paged_launch<128, 16>(kc, vc, p, stream) : paged_launch<128, 64>(kc, vc, p, stream);
+  return d == 64 ? paged_launch_rows<64>(N, kc, vc, p, stream) : paged_launch_rows<128>(N, kc, vc, p, stream);
 }
 
 }  // namespace

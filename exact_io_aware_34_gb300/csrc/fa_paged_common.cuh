@@ -1,0 +1,522 @@
+// What the kernels of attention over a paged 8-bit cache share: the line of
+// units that equal CTAs cut up, its walk, the loads of pages, and the merge of
+// units that several CTAs worked on. See fa_paged_kernel.cuh.
+#pragma once
+
+#include "fa_append_kernel.cuh"
+#include "fa_decode_kernel.cuh"
+#include "fa_prefix_kernel.cuh"
+
+namespace fa {
+
+namespace ptx {
+
+// D[tmem] (+)= A[smem] B[smem]^T, both e4m3, K = 32, from a converged warp whose elected lane issues.
+__device__ __forceinline__ void mma_f8_warp(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                            uint32_t b_hi, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 ad, bd;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 ad, {%1, %2};\n\tmov.b64 bd, {%3, %4};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accum)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f8f6f4: e4m3 operands (format 0), f32 sums.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor: start, leading and stride byte offsets, swizzle (0 none, 2 128 B, 4 64 B).
+__device__ __forceinline__ uint64_t desc_of(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 | 1ull << 46 | static_cast<uint64_t>(swizzle) << 61;
+}
+
+// 32 lanes x 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
+// Maximum over the warp; NaN if any lane has one.
+__device__ __forceinline__ float warp_max_nan(float x) {
+  float y;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The 128 threads of warps 0-3 meet; true if `p` holds in any of them.
+__device__ __forceinline__ bool softmax_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(p))
+      : "memory");
+  return r != 0;
+}
+
+}  // namespace ptx
+
+enum : unsigned int { kRolePagedProducer = 30, kRolePagedMma = 31, kRolePagedSoftmax = 32, kRolePagedWalk = 33 };
+
+// Places of a unit in the line beside its tiles.
+constexpr int kPagedCost = 2;
+constexpr float kPagedJump = 20.f;   // the reference moves when a tile's maximum is 2^20 above it
+constexpr float kPagedTop = 8.f;     // a tile's largest weight is written as 2^8 (e4m3 ends at 448)
+
+struct PagedShape {
+  int B, H, H_kv, G, T_q;
+  int hp, ht, tp;          // heads and tokens of a row tile, head tiles of a group
+  int num_pages, page_shift, max_pages;
+  int causal, ctas;
+};
+
+struct PagedSplit {        // a unit that several CTAs share, noted by the one with its beginning
+  int n;                   // CTAs, 0: none
+  int token, head;         // first row's
+  int heads, rows;         // heads per token, rows
+  int pad[3];
+};
+
+struct PagedParams {
+  PagedShape s;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  float* lse;              // [H, T_q]
+  long long q_t, q_h, o_t, o_h;
+  const float* k_scale;    // [num_pages, H_kv]
+  const float* v_scale;
+  const int* table;        // [B, max_pages]
+  const int* lens;         // [B]
+  const int* cu;           // [B + 1]
+  PagedSplit* split;       // [ctas]
+  float* Lp;               // [2 * ctas][N]: partial results, slot 2 c: the end of a unit, 2 c + 1: a beginning
+  float* Op;               // [2 * ctas][N][d]
+  float scale_log2;
+  int keep;                // 1: K and V may be read by several CTAs
+  unsigned long long timeout_ns;
+  int drop_load;
+};
+
+struct PagedJob {
+  int b, kvh;              // b < 0: no more
+  int token, head;         // of row 0 (packed token, query head)
+  int heads, rows;         // heads per token, rows that hold queries
+  int lim0;                // keys that row 0's token sees; the next token one more (causal)
+  int n_keys;              // keys of the unit
+  int j0, j1;              // tiles
+  int slot;                // of the partial result; -1: none, the unit is whole
+};
+
+// sum over i < n of floor((a i + b) / m), in as many steps as Euclid's algorithm
+// takes for a and m (the lattice points under a line, counted by swapping axes).
+__device__ __forceinline__ unsigned floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  unsigned sum = 0;
+  while (n > 0) {
+    if (a >= m) {
+      sum += static_cast<unsigned>(static_cast<unsigned long long>(n - 1) * n / 2) * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += n * (b / m);
+      b %= m;
+    }
+    const unsigned long long y = static_cast<unsigned long long>(a) * n + b;
+    if (y < m) break;
+    n = static_cast<unsigned>(y / m);
+    b = static_cast<unsigned>(y % m);
+    const unsigned t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// One sequence as the line sees it, for one K/V head and head tile.
+struct PagedSeq {
+  int c0, n_q, n_kv;
+  int first, groups;       // row tiles [first, groups) see keys
+  __device__ __forceinline__ int keys(const PagedShape& s, int i) const {
+    return s.causal ? min(n_kv, n_kv - n_q + (i + 1) * s.tp) : n_kv;
+  }
+  // Places before tile i.
+  __device__ __forceinline__ int before(const PagedShape& s, int i) const {
+    const int k = i - first;
+    if (k <= 0) return 0;
+    const int last = (n_kv + 127) >> 7;
+    if (!s.causal || k == groups - first && k == 1) return k * (kPagedCost + last);
+    const int ramp = i == groups ? k - 1 : k;          // (the last tile may be short)
+    return k * kPagedCost + (i == groups ? last : 0) +
+           static_cast<int>(floor_sum(static_cast<unsigned>(ramp), 128u, static_cast<unsigned>(s.tp),
+                                      static_cast<unsigned>(n_kv - n_q + (first + 1) * s.tp + 127)));
+  }
+  __device__ __forceinline__ int places(const PagedShape& s) const { return before(s, groups); }
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
+  const int c0 = p.cu[b], c1 = p.cu[b + 1];
+  PagedSeq q;
+  q.c0 = c0;
+  q.n_q = c0 >= 0 && c0 <= c1 && c1 <= p.s.T_q ? c1 - c0 : 0;
+  q.n_kv = max(0, min(p.s.max_pages << p.s.page_shift, p.lens[b]));
+  q.groups = (q.n_q + p.s.tp - 1) / p.s.tp;
+  q.first = q.n_kv == 0 ? q.groups : p.s.causal && q.n_kv < q.n_q ? min(q.groups, (q.n_q - q.n_kv) / p.s.tp) : 0;
+  return q;
+}
+
+__device__ __forceinline__ void paged_bad(int b) {
+  if (atomicCAS(&g_status_word, 0u, kStatusBadOffsets) == 0u) {
+    g_status_info[0] = kRolePagedWalk;
+    g_status_info[1] = static_cast<unsigned int>(b);
+    g_status_info[2] = g_status_info[3] = 0u;
+  }
+}
+
+// A CTA's piece of the line, and where it begins.
+struct PagedLine {
+  int total, begin, end;
+  int b, cum;              // sequence of the first place; places (per K/V head and head tile) before it
+};
+
+// The line's length and this CTA's piece (as in fa_prefix_kernel): every CTA adds
+// up all sequences' places, then looks for its first. Ends with a barrier.
+template <int kThreads>
+__device__ __forceinline__ PagedLine paged_line(const PagedParams& p, int* warp_sum, int* start) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PagedShape& sh = p.s;
+  int sum = 0;
+  for (int b = threadIdx.x; b < sh.B; b += kThreads) sum += paged_seq(p, b).places(sh);
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if (lane == 0) warp_sum[warp] = sum;
+  if (threadIdx.x == 0) start[0] = sh.B, start[1] = 0;
+  __syncthreads();
+  int seq_sum = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) seq_sum += warp_sum[w];
+  const int copies = sh.H_kv * sh.ht;              // of a sequence's places
+  PagedLine l;
+  l.total = seq_sum * copies;
+  l.begin = line_begin(l.total, sh.ctas, blockIdx.x);
+  l.end = line_begin(l.total, sh.ctas, blockIdx.x + 1);
+  // (CTA 0 goes through all sequences and looks for ones that do not fit.)
+  const bool check = blockIdx.x == 0;
+  if (check || l.end > l.begin) {
+    const int target = l.begin / copies;
+    int base = 0;
+    for (int b0 = 0; b0 < sh.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      int nu = 0;
+      if (b < sh.B) {
+        nu = paged_seq(p, b).places(sh);
+        if (check) {
+          const int c0 = p.cu[b], c1 = p.cu[b + 1], len = p.lens[b];
+          if (c0 < 0 || c0 > c1 || c1 > sh.T_q || len < 0 || len > sh.max_pages << sh.page_shift) paged_bad(b);
+        }
+      }
+      int incl = nu;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      __syncthreads();
+      if (lane == 31) warp_sum[warp] = incl;
+      __syncthreads();
+      int before = base, chunk = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        chunk += warp_sum[w];
+      }
+      const int excl = before + incl - nu;
+      if (nu > 0 && excl <= target && target < excl + nu) start[0] = b, start[1] = excl;
+      base += chunk;
+      if (!check && base > target) break;
+    }
+  }
+  __syncthreads();
+  l.b = start[0];
+  l.cum = start[1];
+  return l;
+}
+
+// One lane walks a CTA's piece unit by unit and hands the units to the other
+// warps through a ring of two. The CTA with a unit's beginning notes it for the merge.
+__device__ __forceinline__ void paged_walk(const PagedParams& p, const PagedLine& line, PagedJob* jobs,
+                                           uint64_t* bar_job_full, uint64_t* bar_job_empty, volatile int* abort_ptr) {
+  const PagedShape& sh = p.s;
+  const int copies = sh.H_kv * sh.ht;
+  int x = line.begin, b = line.b, u = 0, i = 0, from = 0;
+  PagedSeq q{};
+  bool more = x < line.end && b < sh.B;
+  if (more) {
+    q = paged_seq(p, b);
+    const int places = q.places(sh), y = x - line.cum * copies;
+    more = places > 0 && y >= 0 && y < places * copies;
+    if (more) {
+      u = y / places;
+      const int rem = y - u * places;
+      int lo = q.first, hi = q.groups;           // before(lo) <= rem < before(hi)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (q.before(sh, mid) <= rem) lo = mid;
+        else hi = mid;
+      }
+      i = lo;
+      from = rem - q.before(sh, i);
+    }
+  }
+  for (int n = 0;; ++n) {
+    PagedJob job;
+    job.b = -1;
+    int end = 0;
+    while (more && x < line.end && job.b < 0) {
+      const int keys = q.keys(sh, i), tiles = (keys + 127) >> 7, places = kPagedCost + tiles;
+      // (Only lengths that change under the call can lead out of the unit. It ends then, with undefined results.)
+      if (keys <= 0 || from >= places) {
+        more = false;
+        break;
+      }
+      const int to = min(places, from + (line.end - x));
+      end = x - from + places - 1;               // the unit's last place
+      x += to - from;
+      job.j0 = max(0, from - kPagedCost);
+      job.j1 = max(0, to - kPagedCost);
+      if (job.j1 > job.j0) {
+        const int kvh = u / sh.ht, h0 = (u - kvh * sh.ht) * sh.hp, t0 = i * sh.tp;
+        job.b = b;
+        job.kvh = kvh;
+        job.token = q.c0 + t0;
+        job.head = kvh * sh.G + h0;
+        job.heads = min(sh.hp, sh.G - h0);
+        job.rows = job.heads * min(sh.tp, q.n_q - t0);
+        job.lim0 = sh.causal ? q.n_kv - q.n_q + t0 + 1 : q.n_kv;
+        job.n_keys = keys;
+        job.slot = job.j0 == 0 && job.j1 == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (job.j0 == 0 ? 1 : 0);
+      }
+      from = to;
+      if (to == places) {                        // on to the next unit
+        from = 0;
+        if (++i == q.groups) {
+          i = q.first;
+          if (++u == copies) {
+            u = 0;
+            do {
+              if (++b >= sh.B) break;
+              q = paged_seq(p, b);
+            } while (q.first >= q.groups);
+            more = b < sh.B;
+            i = q.first;
+          }
+        }
+      }
+    }
+    if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr,
+                       kUnitWaits * p.timeout_ns, kRolePagedWalk))
+      break;
+    jobs[n & 1] = job;
+    ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
+    if (job.b < 0) break;
+    if (job.slot >= 0 && job.j0 == 0) {
+      PagedSplit s{};
+      s.n = line_owner(line.total, sh.ctas, end) - static_cast<int>(blockIdx.x) + 1;
+      s.token = job.token;
+      s.head = job.head;
+      s.heads = job.heads;
+      s.rows = job.rows;
+      p.split[blockIdx.x] = s;
+    }
+  }
+}
+
+// A warp loads the pages of its CTA's units, tile by tile, into a ring of
+// kStages pairs of a K and a V tile. One lane has one page: 32 entries of the
+// table are read at a time, a batch ahead of their scales and copies.
+template <int HD, int kStages>
+__device__ __forceinline__ void paged_load(const PagedParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                                           const PagedJob* jobs, uint64_t* bar_job_full, uint64_t* bar_job_empty,
+                                           uint64_t* bar_k_full, uint64_t* bar_v_full, uint64_t* bar_empty,
+                                           float (*page_scale)[2][8], uint32_t tiles_at, volatile int* abort_ptr) {
+  constexpr uint32_t kTileBytes = 128 * HD;
+  const int lane = threadIdx.x & 31;
+  const PagedShape& sh = p.s;
+  const uint64_t policy = p.keep ? ptx::policy_evict_last() : ptx::policy_evict_first();
+  const int per_tile = 128 >> sh.page_shift, in_page = 1 << sh.page_shift;
+  int it = 0;
+  bool ok = true;
+  for (int n = 0; ok; ++n) {
+    ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, kUnitWaits * p.timeout_ns,
+                            kRolePagedProducer);
+    if (!ok) break;
+    const PagedJob job = jobs[n & 1];
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
+    if (job.b < 0) break;
+    const int* table = p.table + static_cast<long long>(job.b) * sh.max_pages;
+    const int entries = (job.n_keys + in_page - 1) >> sh.page_shift;
+    auto entry = [&](int e) { return e < entries ? table[e] : -1; };
+    int id = -1, id_next = entry(job.j0 * per_tile + lane);
+    float sk = 0.f, sv = 0.f;
+    for (int j = job.j0; j < job.j1 && ok; ++j) {
+      const int in_batch = (j - job.j0) * per_tile & 31;
+      if (in_batch == 0) {
+        const int e = j * per_tile + lane;
+        id = id_next;
+        sk = sv = 0.f;
+        if (e >= entries) {
+          id = -1;
+        } else if (id >= 0 && id < sh.num_pages) {
+          sk = p.k_scale[static_cast<long long>(id) * sh.H_kv + job.kvh];
+          sv = p.v_scale[static_cast<long long>(id) * sh.H_kv + job.kvh];
+        } else {
+          paged_bad(job.b);
+          id = sh.num_pages;            // outside the tensor: reads as zeros
+        }
+        id_next = entry(e + 32);
+      }
+      const int stage = it % kStages;
+      ok = wait_warp_or_abort(ptx::smem_u32(&bar_empty[stage]), ((it / kStages) & 1) ^ 1u, abort_ptr, p.timeout_ns,
+                              kRolePagedProducer);
+      if (!ok) break;
+      const int slot = lane - in_batch;
+      const bool mine = slot >= 0 && slot < per_tile;
+      if (mine) {
+        page_scale[stage][0][slot] = sk;
+        page_scale[stage][1][slot] = sv;
+      }
+      const bool copy = mine && id >= 0;
+      const uint32_t bytes = (static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, copy))) << sh.page_shift) * HD;
+      const uint32_t k_full = ptx::smem_u32(&bar_k_full[stage]), v_full = ptx::smem_u32(&bar_v_full[stage]);
+      const bool drop_k = 2 * it == p.drop_load, drop_v = 2 * it + 1 == p.drop_load;   // test hook
+      __syncwarp();
+      if (lane == 0) {
+        if (!drop_k) ptx::mbar_arrive_expect_tx(k_full, bytes);
+        if (!drop_v) ptx::mbar_arrive_expect_tx(v_full, bytes);
+      }
+      __syncwarp();
+      if (copy) {
+        const uint32_t to = tiles_at + 2 * stage * kTileBytes + (static_cast<uint32_t>(slot * HD) << sh.page_shift);
+        if (!drop_k) ptx::tma_load_4d(to, tmK, k_full, 0, 0, job.kvh, id, policy);
+        if (!drop_v) ptx::tma_load_4d(to + kTileBytes, tmV, v_full, 0, 0, job.kvh, id, policy);
+      }
+      __syncwarp();
+      ++it;
+    }
+  }
+  if (__any_sync(0xffffffffu, !ok || *abort_ptr)) {
+    for (int i = it > kStages ? it - kStages : 0; i < it; ++i) {
+      if (2 * i != p.drop_load) drain_wait(ptx::smem_u32(&bar_k_full[i % kStages]), (i / kStages) & 1, p.timeout_ns);
+      if (2 * i + 1 != p.drop_load)
+        drain_wait(ptx::smem_u32(&bar_v_full[i % kStages]), (i / kStages) & 1, p.timeout_ns);
+    }
+  }
+  __syncwarp();
+}
+
+// Joins the parts of the unit that CTA blockIdx.x began and others went on with:
+// one warp per row, LSE = m + ln sum_s e^{LSE_s - m}, O = sum_s e^{LSE_s - LSE} O_s.
+// Rows that see no key at all, of which no unit knows, are written here too.
+template <int HD, int N>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
+  constexpr int kPer = HD / 32;
+  const PagedShape& sh = p.s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
+  const int warps = 4 * gridDim.y, me = blockIdx.y * 4 + warp;
+  for (int b = c; b < sh.B; b += gridDim.x) {
+    const PagedSeq q = paged_seq(p, b);
+    const int blind = min(q.n_q, q.first * sh.tp);
+    for (int r = me; r < blind * sh.H; r += warps) {
+      const int t = r / sh.H, h = r - t * sh.H;
+      for (int e = lane; e < HD; e += 32) p.o[(q.c0 + t) * p.o_t + h * p.o_h + e] = __float2bfloat16(0.f);
+      if (lane == 0) p.lse[static_cast<long long>(h) * sh.T_q + q.c0 + t] = -INFINITY;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const PagedSplit s = p.split[c];
+  // (Clamped: lengths that change under the call leave anything here.)
+  const int n = min(s.n, sh.ctas - c), rows = min(s.rows, N);
+  if (n <= 0 || s.heads <= 0) return;
+  for (int r = me; r < rows; r += warps) {
+    const int ti = r / s.heads, token = s.token + ti, head = s.head + r - ti * s.heads;
+    if (token < 0 || token >= sh.T_q || head < 0 || head >= sh.H) continue;
+    // Part 0 is this CTA's beginning, part k the end in CTA c + k.
+    auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * N + r; };
+    float m = -INFINITY;
+    bool any = false;
+    for (int k = lane; k < n; k += 32) {
+      const float v = p.Lp[slot(k)];
+      any |= v != -INFINITY;
+      m = fmaxf(m, v);
+    }
+    const bool none = !__any_sync(0xffffffffu, any);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) m = 0.f;
+    float acc[kPer], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    if (!none) {
+      for (int k0 = 0; k0 < n; k0 += 32) {
+        const float w_me = k0 + lane < n ? __expf(p.Lp[slot(k0 + lane)] - m) : 0.f;
+        sum += w_me;
+        for (int k1 = 0; k1 < min(32, n - k0); k1 += 8) {
+          float v[8][kPer];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float* src = p.Op + slot(min(k0 + k1 + k, n - 1)) * HD + lane * kPer;
+            if constexpr (kPer == 4) {
+              const float4 f = *reinterpret_cast<const float4*>(src);
+              v[k][0] = f.x, v[k][1] = f.y, v[k][2] = f.z, v[k][3] = f.w;
+            } else {
+              const float2 f = *reinterpret_cast<const float2*>(src);
+              v[k][0] = f.x, v[k][1] = f.y;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float w = __shfl_sync(0xffffffffu, w_me, k1 + k);
+            if (k0 + k1 + k < n) {
+#pragma unroll
+              for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+            }
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = none ? 0.f : 1.f / sum;
+    uint32_t packed[kPer / 2];
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) packed[e / 2] = ptx::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    __nv_bfloat16* dst = p.o + token * p.o_t + head * p.o_h + lane * kPer;
+    if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = packed[0];
+    if (lane == 0) p.lse[static_cast<long long>(head) * sh.T_q + token] = none ? -INFINITY : m + __logf(sum);
+  }
+}
+
+}  // namespace fa

@@ -1,312 +1,128 @@
 // Exact attention of new tokens over a paged cache held in 8 bits (e4m3 with a
-// scale for each page and K/V head): single tokens of a batch of answers,
-// drafted tokens, pieces of prompts. sm_103a, tcgen05 (8-bit operands) + TMEM
-// + TMA.
+// scale for each page and K/V head), for units of few rows: single tokens of a
+// batch of answers, a few drafted tokens. sm_103a, tcgen05 (8-bit operands) +
+// TMEM + TMA.
 //
 // 8-bit operands on both sides. K and V go from memory to the tensor core as
 // they are stored; no thread converts them. The other operand, a bf16 query row
 // or a row of probabilities, enters as the sum of two e4m3 numbers, its first
 // four significant bits and the rest to four more (hi, lo): the products
-// K (q_hi + q_lo) and V (p_hi + p_lo) accumulate in the same place. An 8-bit product runs
-// at twice the bf16 rate, so both together cost what one of bf16 would, on
-// half the bytes. bf16 has eight significant bits: a query row, scaled by a power
-// of two so that its largest element lies in [128, 256), is exact but for
-// elements below 2^-9 of that (off by 2^-17 of it at most). A probability is
-// cut to four bits and its rest rounded to four: off by at most 2^-8 of
-// itself, as if rounded to bf16, or by 2^-17 of its tile's largest.
+// K (q_hi + q_lo) and V (p_hi + p_lo) accumulate in the same place. bf16 has
+// eight significant bits: a query row, scaled by a power of two so that its
+// largest element lies in [128, 256), is exact but for elements below 2^-9 of
+// that (off by 2^-17 of it at most). A probability is cut to four bits and its
+// rest rounded to four: off by at most 2^-8 of itself, as if rounded to bf16,
+// or where it is small by 2^-17 of the largest among its 32 keys.
 //
 // Transposed tiles. A 128-key tile is the M side of both products,
 //   S^T[key, row] = K Q^T,    O^T[column, row] = V^T P^T,
-// so that few query rows (N: 16 or up to 64) leave no lane of the softmax idle: a thread has
-// one key and all rows. V is read as it lies (M-major). A row's maximum is then
-// taken over lanes (redux.sync) and warps. Every tile has its own: P is
-// written relative to it, so that 8 bits always hold the tile's largest
-// weights, and the tile's O^T is added to the sum in registers (a thread has
-// one column of O for all rows) by the factor 2^(tile maximum - reference). The
-// sum of weights stays per thread until the unit's end.
+// so that few query rows (the N side, 16) leave no lane of the softmax idle: a
+// thread has one key and all rows. V is read as it lies (M-major).
+//
+// A warp for itself. The K side of one 8-bit product is 32 keys: the keys of
+// one warp. So each of the four warps takes its rows' maxima over its own 32
+// lanes alone (redux.sync), writes its P relative to them, and has its own
+// O^T in tensor memory; every 32 keys have 8 bits for themselves, however far
+// below the row's largest weight they lie. The four O^T are added to a sum in
+// registers (a thread has one column of O for all rows) by the factors
+// 2^(warp's maximum - reference). The sums of weights stay per thread until the
+// unit's end. Within a tile no warp waits for another but through the
+// tensor core, and the O^T of a tile are added after the next tile's P
+// is written: the products' latency is never waited for.
 //
 // Scales. A key's score is S times its page's K scale; log2 of its V scale
-// (relative to the tile's largest) is added to the exponent, so P carries it,
-// and is taken out of the sum of weights again.
+// (relative to the larger one of its warp's pages) is added to the exponent, so
+// P carries it, and is taken out of the sum of weights again.
 //
-// Work. A unit is (sequence, K/V head, tile of rows): rows are consecutive tokens x the
-// G heads of a group, row = token * hp + head. All units' 128-key tiles stand
-// in one line, each unit's behind kPagedCost empty places, and the CTAs (two per SM) take equal,
-// contiguous pieces, whatever the lengths are, which only the device knows.
-// A unit that lies within one piece is finished there; the parts of others go
-// to the workspace as float32 (a CTA has at most two: the end of one unit, the
-// beginning of another), and paged_merge_kernel joins them.
+// Work: see fa_paged_common.cuh. Rows of a unit are consecutive tokens x the heads of a
+// group, row = token * heads + head; N (4, 8 or 16) bounds them.
 //
-// Per CTA (256 threads): warps 0-3 softmax and sums, warp 4 TMA producer (it
-// reads the page table, 32 entries at a time, one lane a page), warp 5 MMA
-// issuer, warp 6 walks the line one unit ahead, warp 7 idle.
+// Per CTA (256 threads, two CTAs per SM): warps 0-3 softmax and sums, warp 4
+// TMA producer, warp 5 MMA issuer, warp 6 walks the line, warp 7 idle.
 #pragma once
 
-#include "fa_append_kernel.cuh"
-#include "fa_decode_kernel.cuh"
-#include "fa_prefix_kernel.cuh"
+#include "fa_paged_common.cuh"
 
 namespace fa {
 
 namespace ptx {
-
-// D[tmem] (+)= A[smem] B[smem]^T, both e4m3, K = 32, from a converged warp whose elected lane issues.
-__device__ __forceinline__ void mma_f8_warp(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
-                                            uint32_t b_hi, uint32_t idesc, uint32_t accum) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .b64 ad, bd;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "mov.b64 ad, {%1, %2};\n\tmov.b64 bd, {%3, %4};\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %5, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accum)
-      : "memory");
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+  } else if constexpr (N == 8) {
+    tmem_ld8(taddr, r);
+  } else {
+    tmem_ld16(taddr, r);
+  }
 }
-
-// Instruction descriptor of kind::f8f6f4: e4m3 operands (format 0), f32 sums.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
-  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
-         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+template <int N>
+__device__ __forceinline__ void reg_fence(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
-
-// Shared-memory matrix descriptor: start, leading and stride byte offsets, swizzle (0 none, 2 128 B, 4 64 B).
-__device__ __forceinline__ uint64_t desc_of(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
-         static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 | 1ull << 46 | static_cast<uint64_t>(swizzle) << 61;
-}
-
-// 32 lanes x 16 columns.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
-  asm volatile(""
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
-}
-
-// Maximum over the warp; NaN if any lane has one.
-__device__ __forceinline__ float warp_max_nan(float x) {
-  float y;
-  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-__device__ __forceinline__ float lg2_approx(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// The 128 threads of warps 0-3 meet; true if `p` holds in any of them.
-__device__ __forceinline__ bool softmax_any(bool p) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(p))
-      : "memory");
-  return r != 0;
-}
-
 }  // namespace ptx
-
-enum : unsigned int { kRolePagedProducer = 30, kRolePagedMma = 31, kRolePagedSoftmax = 32, kRolePagedWalk = 33 };
-
-// Places of a unit in the line beside its tiles.
-constexpr int kPagedCost = 2;
-constexpr float kPagedJump = 20.f;   // the reference moves when a tile's maximum is 2^20 above it
-constexpr float kPagedTop = 8.f;     // a tile's largest weight is written as 2^8 (e4m3 ends at 448)
-
-struct PagedShape {
-  int B, H, H_kv, G, T_q;
-  int hp, ht, tp;          // heads and tokens of a row tile, head tiles of a group
-  int num_pages, page_shift, max_pages;
-  int causal, ctas;
-};
-
-struct PagedSplit {        // a unit that several CTAs share, noted by the one with its beginning
-  int n;                   // CTAs, 0: none
-  int token, head;         // first row's
-  int heads, rows;         // heads per token, rows
-  int pad[3];
-};
-
-struct PagedParams {
-  PagedShape s;
-  const __nv_bfloat16* q;
-  __nv_bfloat16* o;
-  float* lse;              // [H, T_q]
-  long long q_t, q_h, o_t, o_h;
-  const float* k_scale;    // [num_pages, H_kv]
-  const float* v_scale;
-  const int* table;        // [B, max_pages]
-  const int* lens;         // [B]
-  const int* cu;           // [B + 1]
-  PagedSplit* split;       // [ctas]
-  float* Lp;               // [2 * ctas][N]: partial results, slot 2 c: the end of a unit, 2 c + 1: a beginning
-  float* Op;               // [2 * ctas][N][d]
-  float scale_log2;
-  int keep;                // 1: K and V may be read by several CTAs
-  unsigned long long timeout_ns;
-  int drop_load;
-};
-
-struct PagedJob {
-  int b, kvh;              // b < 0: no more
-  int token, head;         // of row 0 (packed token, query head)
-  int heads, rows;         // heads per token, rows that hold queries
-  int lim0;                // keys that row 0's token sees; the next token one more (causal)
-  int n_keys;              // keys of the unit
-  int j0, j1;              // tiles
-  int slot;                // of the partial result; -1: none, the unit is whole
-};
 
 template <int HD, int N>
 struct PagedCfg {
+  static constexpr int kRows = 16;                     // the N side of the products
   static constexpr int kThreads = 256;
   static constexpr int kCtasPerSm = 2;
-  static constexpr int kStages = N == 16 ? (HD == 128 ? 3 : 5) : (HD == 128 ? 2 : 4);
+  static constexpr int kStages = HD == 128 ? 3 : 5;    // pairs of tiles
   static constexpr int kTileBytes = 128 * HD;          // K or V
-  static constexpr int kPBytes = N * 128;              // hi or lo
-  static constexpr int kQBytes = N * HD;
+  static constexpr int kPBytes = kRows * 128;          // hi or lo
+  static constexpr int kQBytes = kRows * HD;
   // With d = 64 the M side of V^T P^T is V's 64 columns and 64 lanes that nobody
   // reads, fed from the 8 KB behind the tile: the last one has a pad.
   static constexpr int kPad = HD == 64 ? kTileBytes : 0;
-  static constexpr int kSmemBytes = 2 * kPBytes + 2 * kQBytes + kStages * 2 * kTileBytes + kPad + 1024;
-  static constexpr uint32_t kTmemCols = N == 16 ? 64 : 256;
+  static constexpr int kSmemBytes = 4 * kPBytes + 2 * kQBytes + kStages * 2 * kTileBytes + kPad + 1024;
+  static constexpr uint32_t kTmemCols = 256;
   static constexpr uint32_t kColS = 0;                 // two buffers
-  static constexpr uint32_t kColO = 2 * N;
+  static constexpr uint32_t kColO = 2 * kRows;         // two buffers x four warps
   static constexpr uint32_t kSwizzle = HD == 128 ? 2 : 4;
   static constexpr uint32_t kAtom = 8 * HD;            // eight rows
-  static constexpr int kRegsSoftmax = 200;
-  static constexpr int kRegsControl = 56;
-  static_assert(2 * (kSmemBytes + 5 * 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(kColO + 8 * kRows <= kTmemCols, "tensor memory");
+  static_assert(2 * (kSmemBytes + 4 * 1024) <= 228 * 1024, "two CTAs per SM");
 };
-
-// sum over i < n of floor((a i + b) / m), in as many steps as Euclid's algorithm
-// takes for a and m (the lattice points under a line, counted by swapping axes).
-__device__ __forceinline__ unsigned floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-  unsigned sum = 0;
-  while (n > 0) {
-    if (a >= m) {
-      sum += static_cast<unsigned>(static_cast<unsigned long long>(n - 1) * n / 2) * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      sum += n * (b / m);
-      b %= m;
-    }
-    const unsigned long long y = static_cast<unsigned long long>(a) * n + b;
-    if (y < m) break;
-    n = static_cast<unsigned>(y / m);
-    b = static_cast<unsigned>(y % m);
-    const unsigned t = m;
-    m = a;
-    a = t;
-  }
-  return sum;
-}
-
-// One sequence as the line sees it, for one K/V head and head tile.
-struct PagedSeq {
-  int c0, n_q, n_kv;
-  int first, groups;       // row tiles [first, groups) see keys
-  __device__ __forceinline__ int keys(const PagedShape& s, int i) const {
-    return s.causal ? min(n_kv, n_kv - n_q + (i + 1) * s.tp) : n_kv;
-  }
-  // Places before tile i.
-  __device__ __forceinline__ int before(const PagedShape& s, int i) const {
-    const int k = i - first;
-    if (k <= 0) return 0;
-    const int last = (n_kv + 127) >> 7;
-    if (!s.causal || k == groups - first && k == 1) return k * (kPagedCost + last);
-    const int ramp = i == groups ? k - 1 : k;          // (the last tile may be short)
-    return k * kPagedCost + (i == groups ? last : 0) +
-           static_cast<int>(floor_sum(static_cast<unsigned>(ramp), 128u, static_cast<unsigned>(s.tp),
-                                      static_cast<unsigned>(n_kv - n_q + (first + 1) * s.tp + 127)));
-  }
-  __device__ __forceinline__ int places(const PagedShape& s) const { return before(s, groups); }
-};
-
-__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
-  const int c0 = p.cu[b], c1 = p.cu[b + 1];
-  PagedSeq q;
-  q.c0 = c0;
-  q.n_q = c0 >= 0 && c0 <= c1 && c1 <= p.s.T_q ? c1 - c0 : 0;
-  q.n_kv = max(0, min(p.s.max_pages << p.s.page_shift, p.lens[b]));
-  q.groups = (q.n_q + p.s.tp - 1) / p.s.tp;
-  q.first = q.n_kv == 0 ? q.groups : p.s.causal && q.n_kv < q.n_q ? min(q.groups, (q.n_q - q.n_kv) / p.s.tp) : 0;
-  return q;
-}
-
-__device__ __forceinline__ void paged_bad(int b) {
-  if (atomicCAS(&g_status_word, 0u, kStatusBadOffsets) == 0u) {
-    g_status_info[0] = kRolePagedWalk;
-    g_status_info[1] = static_cast<unsigned int>(b);
-    g_status_info[2] = g_status_info[3] = 0u;
-  }
-}
-
-// x[i] over the 32 lanes of a warp for 16 values at a time: lane l returns the sum of value l % 16.
-__device__ __forceinline__ float lanes_sum16(float (&v)[16], int lane) {
-#pragma unroll
-  for (int h = 8; h > 0; h >>= 1) {
-    const bool up = (lane & h) != 0;
-#pragma unroll
-    for (int i = 0; i < h; ++i) {
-      const float send = up ? v[i] : v[i + h], mine = up ? v[i + h] : v[i];
-      v[i] = mine + __shfl_xor_sync(0xffffffffu, send, h);
-    }
-  }
-  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
-}
 
 template <int HD, int N>
 __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kCtasPerSm)
     fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const PagedParams p) {
   using C = PagedCfg<HD, N>;
-  constexpr int kChunks = N / 16;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_k_full[C::kStages];
   __shared__ __align__(8) uint64_t bar_v_full[C::kStages];
   __shared__ __align__(8) uint64_t bar_empty[C::kStages];
   __shared__ __align__(8) uint64_t bar_s_full[2];
-  __shared__ __align__(8) uint64_t bar_p_full;
-  __shared__ __align__(8) uint64_t bar_o_full;
+  __shared__ __align__(8) uint64_t bar_p_full[2];
+  __shared__ __align__(8) uint64_t bar_o_full[2];
   __shared__ __align__(8) uint64_t bar_q_full;
   __shared__ __align__(8) uint64_t bar_job_full[2];
   __shared__ __align__(8) uint64_t bar_job_empty[2];
   __shared__ __align__(8) uint64_t bar_drain;
   __shared__ __align__(16) PagedJob jobs[2];
   __shared__ __align__(16) float page_scale[C::kStages][2][8];   // K, V scales of a tile's pages
-  __shared__ __align__(16) float row_scale[N];      // of S, by row: the scores' scale over the query row's
-  __shared__ __align__(16) int row_lim[N];          // keys the row sees
-  __shared__ __align__(16) float red[4][N];         // by warp
-  __shared__ __align__(16) float row_max[N];        // the tile's maximum - kPagedTop
-  __shared__ __align__(16) float row_fac[N];        // 2^(that - reference)
-  __shared__ __align__(16) float row_fac_o[2][N];   // that times the tile's largest V scale, for two tiles
-  __shared__ __align__(16) float row_corr[2][N];    // what the sums before are multiplied by first
-  __shared__ int corr_any[2];
+  __shared__ __align__(16) float row_scale[16];         // of S, by row: the scores' scale over the query row's
+  __shared__ __align__(16) int row_lim[16];             // keys the row sees
+  // By tile (modulo 4: a warp may be three tiles behind the first to write), warp and row: the maximum - kPagedTop.
+  __shared__ __align__(16) float warp_max[4][4][N];
+  __shared__ float warp_top[4][4];                      // the larger V scale of the warp's pages
+  __shared__ __align__(16) float factor[4][4][N];       // by reading warp: what the four O^T are multiplied by
+  __shared__ __align__(16) float corr[4][N];
+  __shared__ float sums[2][4][2][16];                   // by unit (modulo 2) and warp: sums of weights, what they are relative to
   __shared__ int warp_sum[C::kThreads / 32];
-  __shared__ int start_b, start_cum;
+  __shared__ int start[2];
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PagedShape& sh = p.s;
   const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sP = smem_base, sQ = sP + 2 * C::kPBytes, sKV = sQ + 2 * C::kQBytes;
-  static_assert((2 * C::kPBytes) % 1024 == 0 && (2 * C::kQBytes) % 1024 == 0, "tiles begin on swizzle atoms");
+  const uint32_t sP = smem_base, sQ = sP + 4 * C::kPBytes, sKV = sQ + 2 * C::kQBytes;
+  static_assert((4 * C::kPBytes) % 1024 == 0 && (2 * C::kQBytes) % 1024 == 0, "tiles begin on swizzle atoms");
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -316,17 +132,14 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
     }
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(ptx::smem_u32(&bar_s_full[t]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bar_p_full[t]), 128);
+      ptx::mbar_init(ptx::smem_u32(&bar_o_full[t]), 1);
       ptx::mbar_init(ptx::smem_u32(&bar_job_full[t]), 1);
       ptx::mbar_init(ptx::smem_u32(&bar_job_empty[t]), 6);   // warps 0-5
-      corr_any[t] = 0;
     }
-    ptx::mbar_init(ptx::smem_u32(&bar_p_full), 128);
-    ptx::mbar_init(ptx::smem_u32(&bar_o_full), 1);
     ptx::mbar_init(ptx::smem_u32(&bar_q_full), 128);
     ptx::mbar_init(ptx::smem_u32(&bar_drain), 1);
     abort_flag = 0;
-    start_b = sh.B;
-    start_cum = 0;
     p.split[blockIdx.x].n = 0;
     ptx::fence_mbar_init();
   }
@@ -340,92 +153,36 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
   }
-
-  // The line's length and where this CTA's piece begins (as in fa_prefix_kernel).
-  int sum = 0;
-  for (int b = threadIdx.x; b < sh.B; b += C::kThreads) sum += paged_seq(p, b).places(sh);
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  if (lane == 0) warp_sum[warp] = sum;
-  __syncthreads();
-  int seq_sum = 0;
-#pragma unroll
-  for (int w = 0; w < C::kThreads / 32; ++w) seq_sum += warp_sum[w];
-  const int copies = sh.H_kv * sh.ht;              // of a sequence's places
-  const int total = seq_sum * copies;
-  const int x_begin = line_begin(total, sh.ctas, blockIdx.x), x_end = line_begin(total, sh.ctas, blockIdx.x + 1);
-  const bool check = blockIdx.x == 0;
-  if (check || x_end > x_begin) {
-    const int target = x_begin / copies;
-    int base = 0;
-    for (int b0 = 0; b0 < sh.B; b0 += C::kThreads) {
-      const int b = b0 + threadIdx.x;
-      int nu = 0;
-      if (b < sh.B) {
-        nu = paged_seq(p, b).places(sh);
-        if (check) {
-          const int c0 = p.cu[b], c1 = p.cu[b + 1], len = p.lens[b];
-          if (c0 < 0 || c0 > c1 || c1 > sh.T_q || len < 0 || len > sh.max_pages << sh.page_shift) paged_bad(b);
-        }
-      }
-      int incl = nu;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += u;
-      }
-      __syncthreads();
-      if (lane == 31) warp_sum[warp] = incl;
-      __syncthreads();
-      int before = base, chunk = 0;
-#pragma unroll
-      for (int w = 0; w < C::kThreads / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        chunk += warp_sum[w];
-      }
-      const int excl = before + incl - nu;
-      if (nu > 0 && excl <= target && target < excl + nu) {
-        start_b = b;
-        start_cum = excl;
-      }
-      base += chunk;
-      if (!check && base > target) break;
-    }
-  }
   ptx::tc_fence_before();
-  __syncthreads();
+  const PagedLine line = paged_line<C::kThreads>(p, warp_sum, start);
   ptx::tc_fence_after();
   const uint32_t tmem_base = tmem_base_slot;
   volatile int* abort_ptr = &abort_flag;
 
-  if (warp >= 4) ptx::setmaxnreg_dec<C::kRegsControl>();
   if (warp < 4) {
     // ------------------------------------------------------------ softmax and sums
-    ptx::setmaxnreg_inc<C::kRegsSoftmax>();
     const int tid = threadIdx.x;                   // this thread's key of a tile, and its column of O
     const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t tO = tmem_base + lane_addr + C::kColO;
-    const uint32_t tS0 = tmem_base + lane_addr + C::kColS;
+    const uint32_t tS0 = tmem_base + lane_addr + C::kColS, tO0 = tmem_base + lane_addr + C::kColO;
     const int page_slot = tid >> sh.page_shift;
+    const int slot0 = warp * 32 >> sh.page_shift, slot1 = (warp * 32 + 31) >> sh.page_shift;   // the warp's pages
     uint8_t* generic = smem_raw + (smem_base - ptx::smem_u32(smem_raw));
     int g = 0;                                     // tiles so far
-    bool stop = false;
-    for (int n = 0; !stop; ++n) {
+    for (int n = 0;; ++n) {
       bool ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr,
                                    kUnitWaits * p.timeout_ns, kRolePagedSoftmax);
-      // (All four warps leave together: a named barrier must not be left waiting.)
-      if (ptx::softmax_any(!ok)) break;
-      const PagedJob job = jobs[n & 1];
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
-      if (job.b < 0) break;
-      const int nch = (job.rows + 15) >> 4;        // 16-row chunks in use
-
-      // The query rows, as hi and lo in the swizzled K-major layout.
-      {
+      PagedJob job;
+      job.b = -1;
+      if (ok) {
+        job = jobs[n & 1];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
+      }
+      if (job.b >= 0) {
+        // The query rows, as hi and lo in the swizzled K-major layout.
         constexpr int kLanes = HD / 16;            // threads of a row, 16 elements each
-        const int part = tid % kLanes;
-#pragma unroll 1
-        for (int r = tid / kLanes; r < 16 * nch; r += 128 / kLanes) {
+        const int part = tid % kLanes, r = tid / kLanes;
+        if (r < 16) {
           float x[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = 0.f;
@@ -460,8 +217,8 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
               lo4[e] |= to_e4m3x2(a - back.x, b - back.y) << (16 * f);
             }
           }
-          const uint32_t at = static_cast<uint32_t>(r) * HD +
-                              ((part ^ (HD == 128 ? r & 7 : (r >> 1) & 3)) << 4);
+          const uint32_t at =
+              static_cast<uint32_t>(r) * HD + ((part ^ (HD == 128 ? r & 7 : (r >> 1) & 3)) << 4);
           *reinterpret_cast<uint4*>(generic + (sQ - smem_base) + at) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
           *reinterpret_cast<uint4*>(generic + (sQ - smem_base) + C::kQBytes + at) =
               make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
@@ -470,42 +227,72 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
             row_lim[r] = live ? min(job.n_keys, sh.causal ? job.lim0 + ti : job.lim0) : 0;
           }
         }
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(ptx::smem_u32(&bar_q_full));
       }
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(ptx::smem_u32(&bar_q_full));
+      // row_scale and row_lim stand. (All four warps leave together: a named barrier must not be left waiting.)
+      if (ptx::softmax_any(job.b < 0)) break;
       const int all_see = min(job.n_keys, job.lim0);   // keys that every row sees
-      ptx::softmax_any(false);                         // row_scale and row_lim stand
 
-      float acc[N], lsum[N];
+      float acc[N], lsum[N], lref[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] = lsum[i] = 0.f;
-      float ref = -INFINITY;                           // of row tid (tid < N): exponents in the sums are relative to it
-      // Adds O^T of the tile before (number g - 1).
-      auto add_tile = [&](int buf) {
+      for (int i = 0; i < N; ++i) {
+        acc[i] = lsum[i] = 0.f;
+        lref[i] = -INFINITY;
+      }
+      float ref = -INFINITY;                           // of row lane % N: what acc is relative to, the same in all warps
+      // Adds the four O^T of tile `t` (of this CTA).
+      auto add_tile = [&](int t) {
+        const int buf = t & 1;
+        // (The P of a tile is complete when every warp has written its maxima.)
+        if (!wait_warp_or_abort(ptx::smem_u32(&bar_p_full[buf]), (t >> 1) & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax))
+          return false;
+        {
+          // Lane l has (warp, row) = l / N, l % N (and 32 more with N = 16).
+          float m[N == 16 ? 2 : 1], top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < (N == 16 ? 2 : 1); ++k) {
+            const int at = min(lane + 32 * k, 4 * N - 1);
+            m[k] = (&warp_max[t & 3][0][0])[at];
+            top = ptx::max_nan(top, m[k]);
+          }
+#pragma unroll
+          for (int o = N; o < (N == 4 ? 16 : 32); o <<= 1) top = ptx::max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const bool jump = top != -INFINITY && !(top - ref <= kPagedJump);   // (also the first tile with keys, and NaN)
+          if (__any_sync(0xffffffffu, jump)) {
+            if (lane < N) corr[warp][lane] = jump ? ptx::ex2_approx(ref - top) : 1.f;
+            if (jump) ref = top;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] *= corr[warp][i];
+          }
+#pragma unroll
+          for (int k = 0; k < (N == 16 ? 2 : 1); ++k) {
+            const int at = lane + 32 * k;
+            if (at < 4 * N)
+              (&factor[warp][0][0])[at] = m[k] == -INFINITY ? 0.f : ptx::ex2_approx(m[k] - ref) * warp_top[t & 3][at / N];
+          }
+          __syncwarp();
+        }
+        if (!wait_warp_or_abort(ptx::smem_u32(&bar_o_full[buf]), (t >> 1) & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax))
+          return false;
         ptx::tc_fence_after();
-        const bool corr = corr_any[buf] != 0;
+        constexpr int kAtOnce = N == 16 ? 1 : 4;       // (registers)
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          if (c < nch) {
-            uint32_t o[16];
-            ptx::tmem_ld16(tO + 16 * c, o);
-            ptx::tmem_ld_wait();
-            ptx::reg_fence16(o);
-            if (corr) {
+        for (int w0 = 0; w0 < 4; w0 += kAtOnce) {
+          uint32_t o[kAtOnce][N];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) acc[16 * c + i] *= row_corr[buf][16 * c + i];
-            }
+          for (int w = 0; w < kAtOnce; ++w) ptx::tmem_ld<N>(tO0 + (buf * 4 + w0 + w) * C::kRows, o[w]);
+          ptx::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&row_fac_o[buf][16 * c + i]);
-              acc[16 * c + i] = fmaf(__uint_as_float(o[i]), f.x, acc[16 * c + i]);
-              acc[16 * c + i + 1] = fmaf(__uint_as_float(o[i + 1]), f.y, acc[16 * c + i + 1]);
-              acc[16 * c + i + 2] = fmaf(__uint_as_float(o[i + 2]), f.z, acc[16 * c + i + 2]);
-              acc[16 * c + i + 3] = fmaf(__uint_as_float(o[i + 3]), f.w, acc[16 * c + i + 3]);
-            }
+          for (int w = 0; w < kAtOnce; ++w) {
+            ptx::reg_fence<N>(o[w]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] = fmaf(__uint_as_float(o[w][i]), factor[warp][w0 + w][i], acc[i]);
           }
         }
-        ptx::tc_fence_before();
+        __syncwarp();                                  // (factor is used again)
+        return true;
       };
       for (int j = job.j0; j < job.j1; ++j, ++g) {
         const int stage = g % C::kStages, buf = g & 1;
@@ -514,279 +301,149 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
         if (ok)
           ok = wait_warp_or_abort(ptx::smem_u32(&bar_v_full[stage]), (g / C::kStages) & 1, abort_ptr, p.timeout_ns,
                                   kRolePagedSoftmax);
+        if (!ok) break;
         ptx::tc_fence_after();
+        uint32_t s[N];
+        ptx::tmem_ld<N>(tS0 + buf * C::kRows, s);
         const int key = j * 128 + tid;
-        const bool masked = (j + 1) * 128 > all_see;
-        const uint32_t tS = tS0 + buf * N;
-        float v_top = 0.f, k_sc = 0.f, v_log = 0.f, v_out = 1.f;
-        if (ok) {
-          const float4 a = *reinterpret_cast<const float4*>(&page_scale[stage][1][0]);
-          const float4 b = *reinterpret_cast<const float4*>(&page_scale[stage][1][4]);
-          v_top = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
-          k_sc = page_scale[stage][0][page_slot];
-          // The key's V scale relative to the tile's largest; below 2^-60 it counts as that.
-          const float rel = page_scale[stage][1][page_slot] / (v_top > 0.f ? v_top : 1.f);
+        const float k_sc = page_scale[stage][0][page_slot], v_sc = page_scale[stage][1][page_slot];
+        // The key's V scale relative to the larger one of its warp's pages; below 2^-60 of that it counts as that.
+        float v_top = v_sc, v_log = 0.f, v_out = 1.f;
+        if (slot0 != slot1) {
+          v_top = fmaxf(page_scale[stage][1][slot0], page_scale[stage][1][slot1]);
+          const float rel = v_sc / (v_top > 0.f ? v_top : 1.f);
           v_log = rel < 8.673617379884035e-19f ? -60.f : ptx::lg2_approx(rel);
           v_out = ptx::ex2_approx(-v_log);
         }
-        auto scores = [&](int c, float (&x)[16]) {
-          uint32_t s[16];
-          ptx::tmem_ld16(tS + 16 * c, s);
-          ptx::tmem_ld_wait();
-          ptx::reg_fence16(s);
+        ptx::tmem_ld_wait();
+        ptx::reg_fence<N>(s);
+        float x[N], m[N];
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(&row_scale[16 * c + i]);
-            x[i] = fmaf(__uint_as_float(s[i]), f.x * k_sc, v_log);
-            x[i + 1] = fmaf(__uint_as_float(s[i + 1]), f.y * k_sc, v_log);
-            x[i + 2] = fmaf(__uint_as_float(s[i + 2]), f.z * k_sc, v_log);
-            x[i + 3] = fmaf(__uint_as_float(s[i + 3]), f.w * k_sc, v_log);
-          }
-          if (masked) {
+        for (int i = 0; i < N; ++i) x[i] = fmaf(__uint_as_float(s[i]), row_scale[i] * k_sc, v_log);
+        if ((j + 1) * 128 > all_see) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (key >= row_lim[16 * c + i]) x[i] = -INFINITY;
-          }
-        };
-        if (ok) {
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            if (c < nch) {
-              float x[16];
-              scores(c, x);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] = ptx::warp_max_nan(x[i]);
-              if (lane == 0) {
-#pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                  *reinterpret_cast<float4*>(&red[warp][16 * c + i]) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-              }
-            }
-          }
-          if (tid == 0) corr_any[buf] = 0;
-          // V rows behind the unit's keys may hold anything, and a weight of zero does not cancel a NaN.
-          if (key >= job.n_keys) {
-            uint4* row = reinterpret_cast<uint4*>(generic + (sKV - smem_base) + (2 * stage + 1) * C::kTileBytes + tid * HD);
-#pragma unroll
-            for (int i = 0; i < HD / 16; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
-          }
+          for (int i = 0; i < N; ++i)
+            if (key >= row_lim[i]) x[i] = -INFINITY;
         }
-        stop = ptx::softmax_any(!ok);
-        if (stop) break;
-        if (tid < 16 * nch) {
-          const float m = ptx::max_nan(ptx::max_nan(red[0][tid], red[1][tid]), ptx::max_nan(red[2][tid], red[3][tid])) -
-                          kPagedTop;
-          float fac = 0.f, corr = 1.f;
-          if (m != -INFINITY) {
-            if (!(m - ref <= kPagedJump)) {            // (also the first tile with keys, and NaN)
-              corr = ptx::ex2_approx(ref - m);
-              if (ref != -INFINITY) corr_any[buf] = 1;
-              ref = m;
-            }
-            fac = ptx::ex2_approx(m - ref);
-          }
-          row_max[tid] = m == -INFINITY ? 0.f : m;
-          row_fac[tid] = fac;
-          row_fac_o[buf][tid] = fac * v_top;
-          row_corr[buf][tid] = corr;
+#pragma unroll
+        for (int i = 0; i < N; ++i) m[i] = ptx::warp_max_nan(x[i]) - kPagedTop;
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<float4*>(&warp_max[g & 3][warp][i]) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
+          warp_top[g & 3][warp] = v_top;
         }
-        // O^T of the tile before, while the maxima are joined
-        if (j > job.j0) {
-          ok = wait_warp_or_abort(ptx::smem_u32(&bar_o_full), (g - 1) & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax);
-          if (ok) add_tile(buf ^ 1);
-        }
-        stop = ptx::softmax_any(!ok);
-        if (stop) break;
-        const bool corr = corr_any[buf] != 0;
+        uint32_t hi4[4] = {0u, 0u, 0u, 0u}, lo4[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          if (c < nch) {
-            float x[16];
-            scores(c, x);
-            uint32_t hi4[4], lo4[4];
+        for (int i = 0; i < N; i += 4) {
+          float w[4], h[4];
 #pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const float4 m = *reinterpret_cast<const float4*>(&row_max[16 * c + i]);
-              const float4 f = *reinterpret_cast<const float4*>(&row_fac[16 * c + i]);
-              float w[4] = {ptx::ex2_approx(x[i] - m.x), ptx::ex2_approx(x[i + 1] - m.y),
-                            ptx::ex2_approx(x[i + 2] - m.z), ptx::ex2_approx(x[i + 3] - m.w)};
-              if (corr) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) lsum[16 * c + i + e] *= row_corr[buf][16 * c + i + e];
-              }
-              lsum[16 * c + i] = fmaf(w[0], f.x * v_out, lsum[16 * c + i]);
-              lsum[16 * c + i + 1] = fmaf(w[1], f.y * v_out, lsum[16 * c + i + 1]);
-              lsum[16 * c + i + 2] = fmaf(w[2], f.z * v_out, lsum[16 * c + i + 2]);
-              lsum[16 * c + i + 3] = fmaf(w[3], f.w * v_out, lsum[16 * c + i + 3]);
-              float h[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) h[e] = __uint_as_float(__float_as_uint(w[e]) & 0xfff00000u);
-              hi4[i / 4] = to_e4m3x2(h[0], h[1]) | to_e4m3x2(h[2], h[3]) << 16;
-              lo4[i / 4] = to_e4m3x2(w[0] - h[0], w[1] - h[1]) | to_e4m3x2(w[2] - h[2], w[3] - h[3]) << 16;
+          for (int e = 0; e < 4; ++e) {
+            const float mi = m[i + e];
+            w[e] = ptx::ex2_approx(x[i + e] - (mi == -INFINITY ? 0.f : mi));
+            if (mi != -INFINITY && !(mi - lref[i + e] <= kPagedJump)) {
+              lsum[i + e] *= lref[i + e] == -INFINITY ? 0.f : ptx::ex2_approx(lref[i + e] - mi);
+              lref[i + e] = mi;
             }
-            // [16 rows][key][16 bytes]: N-major without swizzle
-            uint4* at = reinterpret_cast<uint4*>(generic + c * 2048 + tid * 16);
-            *at = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-            *reinterpret_cast<uint4*>(generic + C::kPBytes + c * 2048 + tid * 16) =
-                make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+            const float f = mi == -INFINITY ? 0.f : ptx::ex2_approx(mi - lref[i + e]);
+            lsum[i + e] = fmaf(w[e], f * v_out, lsum[i + e]);
+            h[e] = __uint_as_float(__float_as_uint(w[e]) & 0xfff00000u);
           }
+          hi4[i / 4] = to_e4m3x2(h[0], h[1]) | to_e4m3x2(h[2], h[3]) << 16;
+          lo4[i / 4] = to_e4m3x2(w[0] - h[0], w[1] - h[1]) | to_e4m3x2(w[2] - h[2], w[3] - h[3]) << 16;
+        }
+        // [key][16 bytes]: N-major without swizzle
+        uint8_t* to = generic + buf * 2 * C::kPBytes + tid * 16;
+        *reinterpret_cast<uint4*>(to) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+        *reinterpret_cast<uint4*>(to + C::kPBytes) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+        // V rows behind the unit's keys may hold anything, and a weight of zero does not cancel a NaN.
+        if (key >= job.n_keys) {
+          uint4* row = reinterpret_cast<uint4*>(generic + (sKV - smem_base) + (2 * stage + 1) * C::kTileBytes + tid * HD);
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i) row[i] = make_uint4(0u, 0u, 0u, 0u);
         }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_u32(&bar_p_full));
-      }
-      if (stop) break;
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_o_full), (g - 1) & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax);
-      stop = ptx::softmax_any(!ok);
-      if (stop) break;
-      add_tile((g - 1) & 1);
-      // The sums of weights over the 128 threads.
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        if (c < nch) {
-          float v[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = lsum[16 * c + i];
-          const float l = lanes_sum16(v, lane);
-          if (lane < 16) red[warp][16 * c + lane] = l;
+        ptx::mbar_arrive(ptx::smem_u32(&bar_p_full[buf]));
+        if (j > job.j0 && !add_tile(g - 1)) {
+          ok = false;
+          break;
         }
       }
-      ptx::softmax_any(false);
-      if (tid < 16 * nch) {
-        const float l = (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
+      if (ok) ok = add_tile(g - 1);
+      // The unit's end: sums over lanes here, over warps by everyone.
+      float l_me = 0.f, r_me = -INFINITY;              // of row lane (< N)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float l = lsum[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == i) {
+          l_me = l;
+          r_me = lref[i];
+        }
+      }
+      if (lane < N) {
+        sums[n & 1][warp][0][lane] = l_me;
+        sums[n & 1][warp][1][lane] = r_me;
+      }
+      if (ptx::softmax_any(!ok)) break;
+      float inv = 0.f;                                 // of row lane
+      if (lane < N) {
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float r = sums[n & 1][w][1][lane];
+          if (r != -INFINITY) l = fmaf(sums[n & 1][w][0][lane], ptx::ex2_approx(r - ref), l);
+        }
         const bool none = l == 0.f;
-        row_max[tid] = none ? 0.f : 1.f / l;
-        const float lse = none ? -INFINITY : (ref + __log2f(l)) * 0.69314718055994530942f;
-        if (tid < job.rows) {
+        inv = none ? 0.f : 1.f / l;
+        if (warp == 0 && lane < job.rows) {
+          const float lse = none ? -INFINITY : (ref + __log2f(l)) * 0.69314718055994530942f;
           if (job.slot >= 0) {
-            p.Lp[static_cast<size_t>(job.slot) * N + tid] = lse;
+            p.Lp[static_cast<size_t>(job.slot) * N + lane] = lse;
           } else {
-            const int ti = tid / job.heads;
-            p.lse[static_cast<long long>(job.head + tid - ti * job.heads) * sh.T_q + job.token + ti] = lse;
+            const int ti = lane / job.heads;
+            p.lse[static_cast<long long>(job.head + lane - ti * job.heads) * sh.T_q + job.token + ti] = lse;
           }
         }
       }
-      ptx::softmax_any(false);
-      if (tid < HD) {
+      int ti = 0, hi = 0;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          if (c < nch) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = 16 * c + i;
-              if (r < job.rows) {
-                const float o = acc[r] * row_max[r];
-                if (job.slot >= 0) {
-                  p.Op[(static_cast<size_t>(job.slot) * N + r) * HD + tid] = o;
-                } else {
-                  const int ti = r / job.heads;
-                  p.o[(job.token + ti) * p.o_t + (job.head + r - ti * job.heads) * p.o_h + tid] = __float2bfloat16(o);
-                }
-              }
-            }
-          }
+      for (int r = 0; r < N; ++r) {
+        const float o = acc[r] * __shfl_sync(0xffffffffu, inv, r);
+        if (r < job.rows && tid < HD) {
+          if (job.slot >= 0)
+            p.Op[(static_cast<size_t>(job.slot) * N + r) * HD + tid] = o;
+          else
+            p.o[(job.token + ti) * p.o_t + (job.head + hi) * p.o_h + tid] = __float2bfloat16(o);
+        }
+        if (++hi == job.heads) {
+          hi = 0;
+          ++ti;
         }
       }
-      ptx::softmax_any(false);      // (row_max and red are used again)
     }
   } else if (warp == 4) {
-    // ------------------------------------------------------------ TMA producer
-    const uint64_t policy = p.keep ? ptx::policy_evict_last() : ptx::policy_evict_first();
-    const int per_tile = 128 >> sh.page_shift, in_page = 1 << sh.page_shift;
-    int it = 0, loads = 0;
-    bool ok = true;
-    for (int n = 0; ok; ++n) {
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, kUnitWaits * p.timeout_ns,
-                              kRolePagedProducer);
-      if (!ok) break;
-      const PagedJob job = jobs[n & 1];
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
-      if (job.b < 0) break;
-      const int* table = p.table + static_cast<long long>(job.b) * sh.max_pages;
-      const int entries = (job.n_keys + in_page - 1) >> sh.page_shift;
-      int id = -1, id_next = -1;
-      float sk = 0.f, sv = 0.f;
-      // One lane a page: its number, and then its scales; the next 32 are asked for a batch ahead.
-      auto entry = [&](int e) { return e < entries ? table[e] : -1; };
-      id_next = entry(job.j0 * per_tile + lane);
-      for (int j = job.j0; j < job.j1 && ok; ++j, ++it) {
-        const int in_batch = (j - job.j0) * per_tile & 31;
-        if (in_batch == 0) {
-          const int e = j * per_tile + lane;
-          id = id_next;
-          const bool good = id >= 0 && id < sh.num_pages;
-          sk = sv = 0.f;
-          if (e < entries) {
-            if (good) {
-              sk = p.k_scale[static_cast<long long>(id) * sh.H_kv + job.kvh];
-              sv = p.v_scale[static_cast<long long>(id) * sh.H_kv + job.kvh];
-            } else {
-              paged_bad(job.b);
-              id = sh.num_pages;            // outside the tensor: reads as zeros
-            }
-          } else {
-            id = -1;
-          }
-          id_next = entry(e + 32);
-        }
-        const int stage = it % C::kStages;
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_empty[stage]), ((it / C::kStages) & 1) ^ 1u, abort_ptr,
-                                p.timeout_ns, kRolePagedProducer);
-        if (!ok) break;
-        const int slot = lane - in_batch;
-        const bool mine = slot >= 0 && slot < per_tile;
-        if (mine) {
-          page_scale[stage][0][slot] = sk;
-          page_scale[stage][1][slot] = sv;
-        }
-        const bool copy = mine && id >= 0;
-        const int n_copies = __popc(__ballot_sync(0xffffffffu, copy));
-        const uint32_t bytes = static_cast<uint32_t>(n_copies) << sh.page_shift;
-        const uint32_t k_full = ptx::smem_u32(&bar_k_full[stage]), v_full = ptx::smem_u32(&bar_v_full[stage]);
-        __syncwarp();
-        const bool drop_k = 2 * it == p.drop_load, drop_v = 2 * it + 1 == p.drop_load;   // test hook
-        if (lane == 0) {
-          if (!drop_k) ptx::mbar_arrive_expect_tx(k_full, bytes * HD);
-          if (!drop_v) ptx::mbar_arrive_expect_tx(v_full, bytes * HD);
-        }
-        __syncwarp();
-        if (copy) {
-          const uint32_t to = sKV + 2 * stage * C::kTileBytes + (static_cast<uint32_t>(slot * HD) << sh.page_shift);
-          if (!drop_k) ptx::tma_load_4d(to, &tmK, k_full, 0, 0, job.kvh, id, policy);
-          if (!drop_v) ptx::tma_load_4d(to + C::kTileBytes, &tmV, v_full, 0, 0, job.kvh, id, policy);
-        }
-        __syncwarp();
-        loads = it + 1;
-      }
-    }
-    if (__any_sync(0xffffffffu, !ok || *abort_ptr)) {
-      for (int i = loads > C::kStages ? loads - C::kStages : 0; i < loads; ++i) {
-        if (2 * i != p.drop_load) drain_wait(ptx::smem_u32(&bar_k_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
-        if (2 * i + 1 != p.drop_load)
-          drain_wait(ptx::smem_u32(&bar_v_full[i % C::kStages]), (i / C::kStages) & 1, p.timeout_ns);
-      }
-    }
-    __syncwarp();
+    paged_load<HD, C::kStages>(p, &tmK, &tmV, jobs, bar_job_full, bar_job_empty, bar_k_full, bar_v_full, bar_empty,
+                               page_scale, sKV, abort_ptr);
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
     const uint64_t dq = ptx::desc_of(sQ, 16, C::kAtom, C::kSwizzle);
-    const uint64_t dp = ptx::desc_of(sP, 128, 2048, 0);
+    constexpr uint32_t idesc_qk = ptx::idesc_e4m3_f32(128, 16, false, false);
+    constexpr uint32_t idesc_pv = ptx::idesc_e4m3_f32(128, 16, true, true);
     bool ok = true;
     int g0 = 0;             // tiles of the jobs before
     for (int n = 0; ok; ++n) {
       ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, kUnitWaits * p.timeout_ns,
                               kRolePagedMma);
       if (!ok) break;
-      const int b = jobs[n & 1].b, tiles = jobs[n & 1].j1 - jobs[n & 1].j0, rows = jobs[n & 1].rows;
+      const int b = jobs[n & 1].b, tiles = jobs[n & 1].j1 - jobs[n & 1].j0;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
       if (b < 0) break;
-      const int nn = (rows + 15) & ~15;
-      const uint32_t idesc_qk = ptx::idesc_e4m3_f32(128, 0, false, false) | static_cast<uint32_t>(nn >> 3) << 17;
-      const uint32_t idesc_pv = ptx::idesc_e4m3_f32(128, 0, true, true) | static_cast<uint32_t>(nn >> 3) << 17;
       ok = wait_warp_or_abort(ptx::smem_u32(&bar_q_full), n & 1, abort_ptr, p.timeout_ns, kRolePagedMma);
-      // Step t: S of tile t, then O of tile t - 2 (whose weights are written meanwhile).
+      // S of tile t + 2 follows O of tile t: its buffer has been read when P of tile t is there.
       auto qk = [&](int t) {
         const int g = g0 + t, stage = g % C::kStages;
         if (!wait_warp_or_abort(ptx::smem_u32(&bar_k_full[stage]), (g / C::kStages) & 1, abort_ptr, p.timeout_ns,
@@ -798,7 +455,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int k = 0; k < HD / 32; ++k)
-            ptx::mma_f8_warp(tmem_base + C::kColS + (g & 1) * N, ptx::desc_lo(dk) + 2 * k, ptx::desc_hi(dk),
+            ptx::mma_f8_warp(tmem_base + C::kColS + (g & 1) * C::kRows, ptx::desc_lo(dk) + 2 * k, ptx::desc_hi(dk),
                              ptx::desc_lo(dq) + part * (C::kQBytes >> 4) + 2 * k, ptx::desc_hi(dq), idesc_qk,
                              part + k > 0 ? 1u : 0u);
         ptx::mma_commit_warp(ptx::smem_u32(&bar_s_full[g & 1]));
@@ -806,19 +463,20 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
       };
       for (int t = 0; t < 2 && t < tiles && ok; ++t) ok = qk(t);
       for (int t = 0; t < tiles && ok; ++t) {
-        const int g = g0 + t, stage = g % C::kStages;
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_p_full), g & 1, abort_ptr, p.timeout_ns, kRolePagedMma);
+        const int g = g0 + t, stage = g % C::kStages, buf = g & 1;
+        ok = wait_warp_or_abort(ptx::smem_u32(&bar_p_full[buf]), (g >> 1) & 1, abort_ptr, p.timeout_ns, kRolePagedMma);
         if (!ok) break;
         ptx::tc_fence_after();
         const uint64_t dv = ptx::desc_of(sKV + (2 * stage + 1) * C::kTileBytes, C::kTileBytes, C::kAtom, C::kSwizzle);
+        const uint64_t dp = ptx::desc_of(sP + buf * 2 * C::kPBytes, 128, 2048, 0);
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            ptx::mma_f8_warp(tmem_base + C::kColO, ptx::desc_lo(dv) + k * (32 * HD >> 4), ptx::desc_hi(dv),
-                             ptx::desc_lo(dp) + part * (C::kPBytes >> 4) + k * 32, ptx::desc_hi(dp), idesc_pv,
-                             part + k > 0 ? 1u : 0u);
-        ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full));
+          for (int part = 0; part < 2; ++part)
+            ptx::mma_f8_warp(tmem_base + C::kColO + (buf * 4 + k) * C::kRows, ptx::desc_lo(dv) + k * (32 * HD >> 4),
+                             ptx::desc_hi(dv), ptx::desc_lo(dp) + part * (C::kPBytes >> 4) + k * 32, ptx::desc_hi(dp),
+                             idesc_pv, part > 0 ? 1u : 0u);
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[buf]));
         ptx::mma_commit_warp(ptx::smem_u32(&bar_empty[stage]));
         if (t + 2 < tiles) ok = qk(t + 2);
       }
@@ -830,90 +488,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
     }
     __syncwarp();
   } else if (warp == 6) {
-    // ------------------------------------------------------------ units
-    if (lane == 0) {
-      int x = x_begin, b = start_b, u = 0, i = 0, from = 0;
-      PagedSeq q{};
-      bool more = x < x_end && b < sh.B;
-      if (more) {
-        q = paged_seq(p, b);
-        const int places = q.places(sh), y = x - start_cum * copies;
-        more = places > 0 && y >= 0 && y < places * copies;
-        if (more) {
-          u = y / places;
-          const int rem = y - u * places;
-          int lo = q.first, hi = q.groups;           // before(lo) <= rem < before(hi)
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (q.before(sh, mid) <= rem) lo = mid;
-            else hi = mid;
-          }
-          i = lo;
-          from = rem - q.before(sh, i);
-        }
-      }
-      for (int n = 0;; ++n) {
-        PagedJob job;
-        job.b = -1;
-        int end = 0;
-        while (more && x < x_end && job.b < 0) {
-          const int keys = q.keys(sh, i), tiles = (keys + 127) >> 7, places = kPagedCost + tiles;
-          // (Only lengths that change under the call can lead out of the unit. It ends then, with undefined results.)
-          if (keys <= 0 || from >= places) {
-            more = false;
-            break;
-          }
-          const int to = min(places, from + (x_end - x));
-          end = x - from + places - 1;               // the unit's last place
-          x += to - from;
-          job.j0 = max(0, from - kPagedCost);
-          job.j1 = max(0, to - kPagedCost);
-          if (job.j1 > job.j0) {
-            const int kvh = u / sh.ht, h0 = (u - kvh * sh.ht) * sh.hp, t0 = i * sh.tp;
-            job.b = b;
-            job.kvh = kvh;
-            job.token = q.c0 + t0;
-            job.head = kvh * sh.G + h0;
-            job.heads = min(sh.hp, sh.G - h0);
-            job.rows = job.heads * min(sh.tp, q.n_q - t0);
-            job.lim0 = sh.causal ? q.n_kv - q.n_q + t0 + 1 : q.n_kv;
-            job.n_keys = keys;
-            job.slot = job.j0 == 0 && job.j1 == tiles ? -1 : 2 * static_cast<int>(blockIdx.x) + (job.j0 == 0 ? 1 : 0);
-          }
-          from = to;
-          if (to == places) {                        // on to the next unit
-            from = 0;
-            if (++i == q.groups) {
-              i = q.first;
-              if (++u == copies) {
-                u = 0;
-                do {
-                  if (++b >= sh.B) break;
-                  q = paged_seq(p, b);
-                } while (q.first >= q.groups);
-                more = b < sh.B;
-                i = q.first;
-              }
-            }
-          }
-        }
-        if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr,
-                           kUnitWaits * p.timeout_ns, kRolePagedWalk))
-          break;
-        jobs[n & 1] = job;
-        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
-        if (job.b < 0) break;
-        if (job.slot >= 0 && job.j0 == 0) {
-          PagedSplit s{};
-          s.n = line_owner(total, sh.ctas, end) - static_cast<int>(blockIdx.x) + 1;
-          s.token = job.token;
-          s.head = job.head;
-          s.heads = job.heads;
-          s.rows = job.rows;
-          p.split[blockIdx.x] = s;
-        }
-      }
-    }
+    if (lane == 0) paged_walk(p, line, jobs, bar_job_full, bar_job_empty, abort_ptr);
     __syncwarp();
   }
 
@@ -924,89 +499,6 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
   if (warp == 5) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem_base, C::kTmemCols);
-  }
-}
-
-// Joins the parts of the unit that CTA blockIdx.x began and others went on with:
-// one warp per row, LSE = m + ln sum_s e^{LSE_s - m}, O = sum_s e^{LSE_s - LSE} O_s.
-// Rows that see no key at all, of which no unit knows, are written here too.
-template <int HD, int N>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
-  constexpr int kPer = HD / 32;
-  const PagedShape& sh = p.s;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
-  const int warps = 4 * gridDim.y, me = blockIdx.y * 4 + warp;
-  for (int b = c; b < sh.B; b += gridDim.x) {
-    const PagedSeq q = paged_seq(p, b);
-    const int blind = min(q.n_q, q.first * sh.tp);
-    for (int r = me; r < blind * sh.H; r += warps) {
-      const int t = r / sh.H, h = r - t * sh.H;
-      for (int e = lane; e < HD; e += 32) p.o[(q.c0 + t) * p.o_t + h * p.o_h + e] = __float2bfloat16(0.f);
-      if (lane == 0) p.lse[static_cast<long long>(h) * sh.T_q + q.c0 + t] = -INFINITY;
-    }
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const PagedSplit s = p.split[c];
-  // (Clamped: lengths that change under the call leave anything here.)
-  const int n = min(s.n, sh.ctas - c), rows = min(s.rows, N);
-  if (n <= 0 || s.heads <= 0) return;
-  for (int r = me; r < rows; r += warps) {
-    const int ti = r / s.heads, token = s.token + ti, head = s.head + r - ti * s.heads;
-    if (token < 0 || token >= sh.T_q || head < 0 || head >= sh.H) continue;
-    // Part 0 is this CTA's beginning, part k the end in CTA c + k.
-    auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * N + r; };
-    float m = -INFINITY;
-    bool any = false;
-    for (int k = lane; k < n; k += 32) {
-      const float v = p.Lp[slot(k)];
-      any |= v != -INFINITY;
-      m = fmaxf(m, v);
-    }
-    const bool none = !__any_sync(0xffffffffu, any);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m == -INFINITY) m = 0.f;
-    float acc[kPer], sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-    if (!none) {
-      for (int k0 = 0; k0 < n; k0 += 32) {
-        const float w_me = k0 + lane < n ? __expf(p.Lp[slot(k0 + lane)] - m) : 0.f;
-        sum += w_me;
-        for (int k1 = 0; k1 < min(32, n - k0); k1 += 8) {
-          float v[8][kPer];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float* src = p.Op + slot(min(k0 + k1 + k, n - 1)) * HD + lane * kPer;
-            if constexpr (kPer == 4) {
-              const float4 f = *reinterpret_cast<const float4*>(src);
-              v[k][0] = f.x, v[k][1] = f.y, v[k][2] = f.z, v[k][3] = f.w;
-            } else {
-              const float2 f = *reinterpret_cast<const float2*>(src);
-              v[k][0] = f.x, v[k][1] = f.y;
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float w = __shfl_sync(0xffffffffu, w_me, k1 + k);
-            if (k0 + k1 + k < n) {
-#pragma unroll
-              for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
-            }
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float inv = none ? 0.f : 1.f / sum;
-    uint32_t packed[kPer / 2];
-#pragma unroll
-    for (int e = 0; e < kPer; e += 2) packed[e / 2] = ptx::pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    __nv_bfloat16* dst = p.o + token * p.o_t + head * p.o_h + lane * kPer;
-    if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(packed[0], packed[1]);
-    else *reinterpret_cast<uint32_t*>(dst) = packed[0];
-    if (lane == 0) p.lse[static_cast<long long>(head) * sh.T_q + token] = none ? -INFINITY : m + __logf(sum);
   }
 }
 
