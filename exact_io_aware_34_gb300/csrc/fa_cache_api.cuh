@@ -272,9 +272,9 @@ bool make_page_map(CUtensorMap* m, const Pages& c) {
 
 // Rows of a unit: 4, 8 or 16 while the sequences' new tokens, on average, fill no more.
 int paged_rows(int B, int G, int T_q) {
-  for (int n : {4, 8, 16})
+  for (int n : {4, 8})
     if (static_cast<long long>(T_q) * G <= static_cast<long long>(n) * B) return n;
-  return 64;
+  return 16;
 }
 
 fa::PagedShape paged_shape(int B, int H, int H_kv, int T_q, int num_pages, int page, int max_pages, int causal) {
@@ -326,18 +326,10 @@ struct PagedKernel {
 
 template <int HD, int N>
 const PagedKernel& paged_kernel() {
-  if constexpr (N <= 16) {
-    using C = fa::PagedCfg<HD, N>;
-    static const PagedKernel k{reinterpret_cast<const void*>(&fa::fa_paged_kernel<HD, N>),
-                               reinterpret_cast<const void*>(&fa::paged_merge_kernel<HD, N>), C::kSmemBytes, C::kThreads, 0};
-    return k;
-  } else {
-    using C = fa::PagedWideCfg<HD, N>;
-    static const PagedKernel k{reinterpret_cast<const void*>(&fa::fa_paged_wide_kernel<HD, N>),
-                               reinterpret_cast<const void*>(&fa::paged_merge_kernel<HD, N>), C::kSmemBytes, C::kThreads,
-                               (C::kRegsSoftmax + C::kRegsControl) / 2};
-    return k;
-  }
+  using C = fa::PagedCfg<HD, N>;
+  static const PagedKernel k{reinterpret_cast<const void*>(&fa::fa_paged_kernel<HD, N>),
+                             reinterpret_cast<const void*>(&fa::paged_merge_kernel<HD, N>), C::kSmemBytes, C::kThreads, 0};
+  return k;
 }
 
 template <int HD, int N>
@@ -365,18 +357,19 @@ fa_status_t paged_launch(const Pages& kc, const Pages& vc, fa::PagedParams& p, c
   cfg.blockDim = dim3(static_cast<unsigned>(k.threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(k.smem);
   cfg.stream = stream;
-  void* args[3] = {&mk, &mv, &p};
-  e = cudaLaunchKernelExC(&cfg, k.main, args);
-  if (e != cudaSuccess) return cuda_fail(e);
-  // The merge as a programmatic dependent launch: it waits on the device.
+  // Both as programmatic dependent launches: they wait on the device for what
+  // came before, the merge for the main grid's end.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[3] = {&mk, &mv, &p};
+  e = cudaLaunchKernelExC(&cfg, k.main, args);
+  if (e != cudaSuccess) return cuda_fail(e);
   cfg.gridDim = dim3(static_cast<unsigned>(p.s.ctas), static_cast<unsigned>((N + 15) / 16));
   cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   void* merge_args[1] = {&p};
   e = cudaLaunchKernelExC(&cfg, k.merge, merge_args);
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
@@ -387,8 +380,7 @@ fa_status_t paged_launch_rows(int N, const Pages& kc, const Pages& vc, fa::Paged
   switch (N) {
     case 4: return paged_launch<HD, 4>(kc, vc, p, stream);
     case 8: return paged_launch<HD, 8>(kc, vc, p, stream);
-    case 16: return paged_launch<HD, 16>(kc, vc, p, stream);
-    default: return paged_launch<HD, 64>(kc, vc, p, stream);
+    default: return paged_launch<HD, 16>(kc, vc, p, stream);
   }
 }
 

@@ -49,6 +49,16 @@ __device__ __forceinline__ void reg_fence16(uint32_t (&r)[16]) {
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
+// Raises the byte count that a barrier's phase waits for, without arriving.
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// Programmatic dependent launches: what follows waits until the grids before
+// have ended and their writes are visible; the next grid may be scheduled.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Maximum over the warp; NaN if any lane has one.
 __device__ __forceinline__ float warp_max_nan(float x) {
   float y;
@@ -80,7 +90,7 @@ __device__ __forceinline__ bool softmax_any(bool p) {
 
 }  // namespace ptx
 
-enum : unsigned int { kRolePagedProducer = 30, kRolePagedMma = 31, kRolePagedSoftmax = 32, kRolePagedWalk = 33 };
+enum : unsigned int { kRolePagedProducer = 30, kRolePagedMma = 31, kRolePagedSoftmax = 32, kRolePagedWalk = 33, kRolePagedQuery = 34 };
 
 // Places of a unit in the line beside its tiles.
 constexpr int kPagedCost = 2;
@@ -133,7 +143,7 @@ struct PagedJob {
 
 // sum over i < n of floor((a i + b) / m), in as many steps as Euclid's algorithm
 // takes for a and m (the lattice points under a line, counted by swapping axes).
-__device__ __forceinline__ unsigned floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+__device__ __noinline__ unsigned floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   unsigned sum = 0;
   while (n > 0) {
     if (a >= m) {
@@ -155,6 +165,8 @@ __device__ __forceinline__ unsigned floor_sum(unsigned n, unsigned m, unsigned a
   return sum;
 }
 
+__device__ __noinline__ int paged_div(int a, int b) { return a / b; }
+
 // One sequence as the line sees it, for one K/V head and head tile.
 struct PagedSeq {
   int c0, n_q, n_kv;
@@ -167,7 +179,7 @@ struct PagedSeq {
     const int k = i - first;
     if (k <= 0) return 0;
     const int last = (n_kv + 127) >> 7;
-    if (!s.causal || k == groups - first && k == 1) return k * (kPagedCost + last);
+    if (!s.causal || (k == groups - first && k == 1)) return k * (kPagedCost + last);
     const int ramp = i == groups ? k - 1 : k;          // (the last tile may be short)
     return k * kPagedCost + (i == groups ? last : 0) +
            static_cast<int>(floor_sum(static_cast<unsigned>(ramp), 128u, static_cast<unsigned>(s.tp),
@@ -182,12 +194,14 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int b) {
   q.c0 = c0;
   q.n_q = c0 >= 0 && c0 <= c1 && c1 <= p.s.T_q ? c1 - c0 : 0;
   q.n_kv = max(0, min(p.s.max_pages << p.s.page_shift, p.lens[b]));
-  q.groups = (q.n_q + p.s.tp - 1) / p.s.tp;
-  q.first = q.n_kv == 0 ? q.groups : p.s.causal && q.n_kv < q.n_q ? min(q.groups, (q.n_q - q.n_kv) / p.s.tp) : 0;
+  // (Code that a decode step does not need is not on its way: a launch meets a cold instruction cache.)
+  q.groups = q.n_q > p.s.tp ? paged_div(q.n_q + p.s.tp - 1, p.s.tp) : min(q.n_q, 1);
+  q.first = q.n_kv == 0 ? q.groups : 0;
+  if (p.s.causal && q.n_kv < q.n_q && q.n_kv > 0) q.first = min(q.groups, paged_div(q.n_q - q.n_kv, p.s.tp));
   return q;
 }
 
-__device__ __forceinline__ void paged_bad(int b) {
+__device__ __noinline__ void paged_bad(int b) {
   if (atomicCAS(&g_status_word, 0u, kStatusBadOffsets) == 0u) {
     g_status_info[0] = kRolePagedWalk;
     g_status_info[1] = static_cast<unsigned int>(b);
@@ -197,45 +211,86 @@ __device__ __forceinline__ void paged_bad(int b) {
 
 // A CTA's piece of the line, and where it begins.
 struct PagedLine {
-  int total, begin, end;
+  int each, rest;          // pieces of each + 1 places for the first `rest` CTAs, of each for the others
+  int begin, end;
   int b, cum;              // sequence of the first place; places (per K/V head and head tile) before it
 };
 
-// The line's length and this CTA's piece (as in fa_prefix_kernel): every CTA adds
-// up all sequences' places, then looks for its first. Ends with a barrier.
+// Most sequences whose line one warp adds up by itself.
+constexpr int kPagedWarpSeqs = 256;
+
+__device__ __forceinline__ int paged_places(const PagedParams& p, int b) {
+  if (b >= p.s.B) return 0;
+  if (blockIdx.x == 0) {   // (CTA 0 looks for sequences that do not fit.)
+    const int c0 = p.cu[b], c1 = p.cu[b + 1], len = p.lens[b];
+    if (c0 < 0 || c0 > c1 || c1 > p.s.T_q || len < 0 || len > p.s.max_pages << p.s.page_shift) paged_bad(b);
+  }
+  return paged_seq(p, b).places(p.s);
+}
+
+__device__ __forceinline__ void paged_cut(PagedLine* l, int seq_sum, int copies, int ctas) {
+  const int total = seq_sum * copies, c = static_cast<int>(blockIdx.x);
+  l->each = total / ctas;
+  l->rest = total - l->each * ctas;
+  l->begin = c * l->each + min(c, l->rest);
+  l->end = l->begin + l->each + (c < l->rest ? 1 : 0);
+}
+
+// The line's length and this CTA's piece, found by one warp (all lanes return
+// it): it adds up all sequences' places, then looks for the piece's first.
+__device__ __forceinline__ PagedLine paged_line_warp(const PagedParams& p) {
+  const int lane = threadIdx.x & 31, copies = p.s.H_kv * p.s.ht;
+  const int first = paged_places(p, lane);
+  int sum = first;
+#pragma unroll 1
+  for (int b = lane + 32; b < p.s.B; b += 32) sum += paged_places(p, b);
+  PagedLine l;
+  paged_cut(&l, __reduce_add_sync(0xffffffffu, sum), copies, p.s.ctas);
+  l.b = p.s.B;
+  l.cum = 0;
+  int base = 0;
+#pragma unroll 1
+  for (int b0 = 0; b0 < p.s.B; b0 += 32) {
+    const int nu = b0 == 0 ? first : paged_seq(p, min(b0 + lane, p.s.B - 1)).places(p.s) * (b0 + lane < p.s.B ? 1 : 0);
+    int incl = nu;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    const int excl = base + incl - nu;
+    const unsigned hit = __ballot_sync(0xffffffffu, nu > 0 && excl * copies <= l.begin && l.begin < (excl + nu) * copies);
+    if (hit) {
+      const int at = __ffs(hit) - 1;
+      l.b = b0 + at;
+      l.cum = __shfl_sync(0xffffffffu, excl, at);
+      break;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return l;
+}
+
+// The same by a whole CTA, for more sequences. Ends with a barrier.
 template <int kThreads>
-__device__ __forceinline__ PagedLine paged_line(const PagedParams& p, int* warp_sum, int* start) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const PagedShape& sh = p.s;
+__device__ __forceinline__ PagedLine paged_line_block(const PagedParams& p, int* warp_sum, int* start) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, copies = p.s.H_kv * p.s.ht;
+  if (threadIdx.x == 0) start[0] = p.s.B, start[1] = 0;
   int sum = 0;
-  for (int b = threadIdx.x; b < sh.B; b += kThreads) sum += paged_seq(p, b).places(sh);
+  for (int b = threadIdx.x; b < p.s.B; b += kThreads) sum += paged_places(p, b);
   sum = __reduce_add_sync(0xffffffffu, sum);
   if (lane == 0) warp_sum[warp] = sum;
-  if (threadIdx.x == 0) start[0] = sh.B, start[1] = 0;
   __syncthreads();
   int seq_sum = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) seq_sum += warp_sum[w];
-  const int copies = sh.H_kv * sh.ht;              // of a sequence's places
   PagedLine l;
-  l.total = seq_sum * copies;
-  l.begin = line_begin(l.total, sh.ctas, blockIdx.x);
-  l.end = line_begin(l.total, sh.ctas, blockIdx.x + 1);
-  // (CTA 0 goes through all sequences and looks for ones that do not fit.)
-  const bool check = blockIdx.x == 0;
-  if (check || l.end > l.begin) {
+  paged_cut(&l, seq_sum, copies, p.s.ctas);
+  if (l.end > l.begin) {
     const int target = l.begin / copies;
     int base = 0;
-    for (int b0 = 0; b0 < sh.B; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      int nu = 0;
-      if (b < sh.B) {
-        nu = paged_seq(p, b).places(sh);
-        if (check) {
-          const int c0 = p.cu[b], c1 = p.cu[b + 1], len = p.lens[b];
-          if (c0 < 0 || c0 > c1 || c1 > sh.T_q || len < 0 || len > sh.max_pages << sh.page_shift) paged_bad(b);
-        }
-      }
+    for (int b0 = 0; b0 < p.s.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x, nu = paged_places(p, b);
       int incl = nu;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -254,7 +309,7 @@ __device__ __forceinline__ PagedLine paged_line(const PagedParams& p, int* warp_
       const int excl = before + incl - nu;
       if (nu > 0 && excl <= target && target < excl + nu) start[0] = b, start[1] = excl;
       base += chunk;
-      if (!check && base > target) break;
+      if (base > target) break;
     }
   }
   __syncthreads();
@@ -263,36 +318,46 @@ __device__ __forceinline__ PagedLine paged_line(const PagedParams& p, int* warp_
   return l;
 }
 
-// One lane walks a CTA's piece unit by unit and hands the units to the other
-// warps through a ring of two. The CTA with a unit's beginning notes it for the merge.
-__device__ __forceinline__ void paged_walk(const PagedParams& p, const PagedLine& line, PagedJob* jobs,
-                                           uint64_t* bar_job_full, uint64_t* bar_job_empty, volatile int* abort_ptr) {
-  const PagedShape& sh = p.s;
-  const int copies = sh.H_kv * sh.ht;
-  int x = line.begin, b = line.b, u = 0, i = 0, from = 0;
-  PagedSeq q{};
-  bool more = x < line.end && b < sh.B;
-  if (more) {
+// Walks a CTA's piece unit by unit; a warp's lanes all hold the same state.
+struct PagedWalk {
+  PagedLine line;
+  PagedSeq q;
+  int x, b, u, i, from;    // next place; its sequence, copy, row tile and place within the unit
+  bool more;
+
+  __device__ __forceinline__ void begin(const PagedParams& p, const PagedLine& l) {
+    const PagedShape& sh = p.s;
+    const int copies = sh.H_kv * sh.ht;
+    line = l;
+    x = l.begin;
+    b = l.b;
+    u = i = from = 0;
+    more = x < l.end && b < sh.B;
+    if (!more) return;
     q = paged_seq(p, b);
-    const int places = q.places(sh), y = x - line.cum * copies;
+    const int places = q.places(sh), y = x - l.cum * copies;
     more = places > 0 && y >= 0 && y < places * copies;
-    if (more) {
-      u = y / places;
-      const int rem = y - u * places;
-      int lo = q.first, hi = q.groups;           // before(lo) <= rem < before(hi)
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (q.before(sh, mid) <= rem) lo = mid;
+    if (!more) return;
+    u = y / places;
+    from = y - u * places;
+    i = q.first;
+    int hi = q.groups;                           // before(i) <= from < before(hi)
+    if (hi - i > 1) {
+#pragma unroll 1
+      while (hi - i > 1) {
+        const int mid = (i + hi) >> 1;
+        if (q.before(sh, mid) <= from) i = mid;
         else hi = mid;
       }
-      i = lo;
-      from = rem - q.before(sh, i);
+      from -= q.before(sh, i);
     }
   }
-  for (int n = 0;; ++n) {
-    PagedJob job;
+
+  // The next unit's part in this piece (job.b < 0: none); *end is the unit's last place.
+  __device__ __forceinline__ PagedJob next(const PagedParams& p, int* end) {
+    const PagedShape& sh = p.s;
+    PagedJob job{};
     job.b = -1;
-    int end = 0;
     while (more && x < line.end && job.b < 0) {
       const int keys = q.keys(sh, i), tiles = (keys + 127) >> 7, places = kPagedCost + tiles;
       // (Only lengths that change under the call can lead out of the unit. It ends then, with undefined results.)
@@ -301,12 +366,12 @@ __device__ __forceinline__ void paged_walk(const PagedParams& p, const PagedLine
         break;
       }
       const int to = min(places, from + (line.end - x));
-      end = x - from + places - 1;               // the unit's last place
+      *end = x - from + places - 1;
       x += to - from;
       job.j0 = max(0, from - kPagedCost);
       job.j1 = max(0, to - kPagedCost);
       if (job.j1 > job.j0) {
-        const int kvh = u / sh.ht, h0 = (u - kvh * sh.ht) * sh.hp, t0 = i * sh.tp;
+        const int kvh = sh.ht == 1 ? u : u / sh.ht, h0 = (u - kvh * sh.ht) * sh.hp, t0 = i * sh.tp;
         job.b = b;
         job.kvh = kvh;
         job.token = q.c0 + t0;
@@ -322,7 +387,7 @@ __device__ __forceinline__ void paged_walk(const PagedParams& p, const PagedLine
         from = 0;
         if (++i == q.groups) {
           i = q.first;
-          if (++u == copies) {
+          if (++u == sh.H_kv * sh.ht) {
             u = 0;
             do {
               if (++b >= sh.B) break;
@@ -334,59 +399,71 @@ __device__ __forceinline__ void paged_walk(const PagedParams& p, const PagedLine
         }
       }
     }
-    if (!wait_or_abort(ptx::smem_u32(&bar_job_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr,
-                       kUnitWaits * p.timeout_ns, kRolePagedWalk))
-      break;
-    jobs[n & 1] = job;
-    ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[n & 1]));
-    if (job.b < 0) break;
-    if (job.slot >= 0 && job.j0 == 0) {
-      PagedSplit s{};
-      s.n = line_owner(line.total, sh.ctas, end) - static_cast<int>(blockIdx.x) + 1;
-      s.token = job.token;
-      s.head = job.head;
-      s.heads = job.heads;
-      s.rows = job.rows;
-      p.split[blockIdx.x] = s;
-    }
+    return job;
   }
-}
 
-// A warp loads the pages of its CTA's units, tile by tile, into a ring of
-// kStages pairs of a K and a V tile. One lane has one page: 32 entries of the
-// table are read at a time, a batch ahead of their scales and copies.
+  // The CTA that takes place y.
+  __device__ __forceinline__ int owner(int y) const {
+    const int split = line.rest * (line.each + 1);
+    return y < split ? y / (line.each + 1) : line.rest + (y - split) / line.each;
+  }
+};
+
+constexpr int kPagedJobs = 4;            // the ring through which units are handed on
+
+// A warp walks its CTA's piece, hands the units on and loads their pages, tile
+// by tile, into a ring of kStages pairs of a K and a V tile. A lane has one
+// page: 32 entries of the table are read at a time, a batch (or a unit) ahead.
 template <int HD, int kStages>
-__device__ __forceinline__ void paged_load(const PagedParams& p, const CUtensorMap* tmK, const CUtensorMap* tmV,
-                                           const PagedJob* jobs, uint64_t* bar_job_full, uint64_t* bar_job_empty,
-                                           uint64_t* bar_k_full, uint64_t* bar_v_full, uint64_t* bar_empty,
-                                           float (*page_scale)[2][8], uint32_t tiles_at, volatile int* abort_ptr) {
+__device__ __forceinline__ void paged_load(const PagedParams& p, const PagedLine& line, const CUtensorMap* tmK,
+                                           const CUtensorMap* tmV, PagedJob* jobs, uint64_t* bar_job_full,
+                                           uint64_t* bar_job_empty, uint64_t* bar_k_full, uint64_t* bar_v_full,
+                                           uint64_t* bar_empty, float (*page_scale)[2][8], uint32_t tiles_at,
+                                           volatile int* abort_ptr) {
   constexpr uint32_t kTileBytes = 128 * HD;
   const int lane = threadIdx.x & 31;
   const PagedShape& sh = p.s;
   const uint64_t policy = p.keep ? ptx::policy_evict_last() : ptx::policy_evict_first();
   const int per_tile = 128 >> sh.page_shift, in_page = 1 << sh.page_shift;
-  int it = 0;
+  PagedWalk walk;
+  walk.begin(p, line);
+  auto entry = [&](const PagedJob& job, int e) {
+    return job.b >= 0 && e < (job.n_keys + in_page - 1) >> sh.page_shift
+               ? p.table[static_cast<long long>(job.b) * sh.max_pages + e] : -1;
+  };
+  int it = 0, end = 0, end_next = 0;
+  PagedJob job{};
+  int id_next = -1;
   bool ok = true;
-  for (int n = 0; ok; ++n) {
-    ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_full[n & 1]), (n >> 1) & 1, abort_ptr, kUnitWaits * p.timeout_ns,
-                            kRolePagedProducer);
-    if (!ok) break;
-    const PagedJob job = jobs[n & 1];
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[n & 1]));
-    if (job.b < 0) break;
-    const int* table = p.table + static_cast<long long>(job.b) * sh.max_pages;
-    const int entries = (job.n_keys + in_page - 1) >> sh.page_shift;
-    auto entry = [&](int e) { return e < entries ? table[e] : -1; };
-    int id = -1, id_next = entry(job.j0 * per_tile + lane);
+  // (Unit -1 has no tiles: the first unit is found where the next of any other is.)
+#pragma unroll 1
+  for (int n = -1;; ++n) {
+    if (n >= 0) {
+      const int ring = n & (kPagedJobs - 1);
+      ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_empty[ring]), ((n / kPagedJobs) & 1) ^ 1u, abort_ptr,
+                              kUnitWaits * p.timeout_ns, kRolePagedWalk);
+      if (!ok) break;
+      if (lane == 0) {
+        jobs[ring] = job;
+        ptx::mbar_arrive(ptx::smem_u32(&bar_job_full[ring]));
+      }
+      if (job.b < 0) break;
+    }
+    PagedJob after{};
+    int id = -1, id_after = -1;
     float sk = 0.f, sv = 0.f;
-    for (int j = job.j0; j < job.j1 && ok; ++j) {
+    int j = job.j0;
+#pragma unroll 1
+    do {
+     int stage = 0, slot = 0;
+     bool mine = false, drop_v = false;
+     if (n >= 0) {
       const int in_batch = (j - job.j0) * per_tile & 31;
       if (in_batch == 0) {
         const int e = j * per_tile + lane;
         id = id_next;
         sk = sv = 0.f;
-        if (e >= entries) {
+        if (e >= (job.n_keys + in_page - 1) >> sh.page_shift) {
           id = -1;
         } else if (id >= 0 && id < sh.num_pages) {
           sk = p.k_scale[static_cast<long long>(id) * sh.H_kv + job.kvh];
@@ -395,26 +472,21 @@ __device__ __forceinline__ void paged_load(const PagedParams& p, const CUtensorM
           paged_bad(job.b);
           id = sh.num_pages;            // outside the tensor: reads as zeros
         }
-        id_next = entry(e + 32);
+        id_next = entry(job, e + 32);
       }
-      const int stage = it % kStages;
+      stage = it % kStages;
       ok = wait_warp_or_abort(ptx::smem_u32(&bar_empty[stage]), ((it / kStages) & 1) ^ 1u, abort_ptr, p.timeout_ns,
                               kRolePagedProducer);
       if (!ok) break;
-      const int slot = lane - in_batch;
-      const bool mine = slot >= 0 && slot < per_tile;
-      if (mine) {
-        page_scale[stage][0][slot] = sk;
-        page_scale[stage][1][slot] = sv;
-      }
-      const bool copy = mine && id >= 0;
+      slot = lane - in_batch;
+      mine = slot >= 0 && slot < per_tile;
+      const bool copy = mine && id >= 0, drop_k = 2 * it == p.drop_load;   // test hook
+      drop_v = 2 * it + 1 == p.drop_load;
       const uint32_t bytes = (static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, copy))) << sh.page_shift) * HD;
       const uint32_t k_full = ptx::smem_u32(&bar_k_full[stage]), v_full = ptx::smem_u32(&bar_v_full[stage]);
-      const bool drop_k = 2 * it == p.drop_load, drop_v = 2 * it + 1 == p.drop_load;   // test hook
-      __syncwarp();
       if (lane == 0) {
         if (!drop_k) ptx::mbar_arrive_expect_tx(k_full, bytes);
-        if (!drop_v) ptx::mbar_arrive_expect_tx(v_full, bytes);
+        if (!drop_v) ptx::mbar_expect_tx(v_full, bytes);
       }
       __syncwarp();
       if (copy) {
@@ -422,9 +494,36 @@ __device__ __forceinline__ void paged_load(const PagedParams& p, const CUtensorM
         if (!drop_k) ptx::tma_load_4d(to, tmK, k_full, 0, 0, job.kvh, id, policy);
         if (!drop_v) ptx::tma_load_4d(to + kTileBytes, tmV, v_full, 0, 0, job.kvh, id, policy);
       }
-      __syncwarp();
-      ++it;
-    }
+     }
+     if (j == job.j0) {
+       // While the first copies are on their way: a beginning is noted for the merge; the next unit and its entries.
+       if (n >= 0 && job.slot >= 0 && job.j0 == 0 && lane == 0) {
+         PagedSplit s{};
+         s.n = walk.owner(end) - static_cast<int>(blockIdx.x) + 1;
+         s.token = job.token;
+         s.head = job.head;
+         s.heads = job.heads;
+         s.rows = job.rows;
+         p.split[blockIdx.x] = s;
+       }
+       after = walk.next(p, &end_next);
+       id_after = entry(after, after.j0 * per_tile + lane);
+     }
+     if (n >= 0) {
+       // The scales follow; the V tile counts as full when both are there.
+       if (mine) {
+         page_scale[stage][0][slot] = sk;
+         page_scale[stage][1][slot] = sv;
+       }
+       __syncwarp();
+       if (lane == 0 && !drop_v) ptx::mbar_arrive(ptx::smem_u32(&bar_v_full[stage]));
+       ++it;
+     }
+    } while (++j < job.j1);
+    if (!ok) break;
+    job = after;
+    id_next = id_after;
+    end = end_next;
   }
   if (__any_sync(0xffffffffu, !ok || *abort_ptr)) {
     for (int i = it > kStages ? it - kStages : 0; i < it; ++i) {
@@ -445,6 +544,21 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
   const PagedShape& sh = p.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
   const int warps = 4 * gridDim.y, me = blockIdx.y * 4 + warp;
+  ptx::grid_wait();
+  // Part 0 of a unit is CTA c's beginning, part k the end in CTA c + k. The first
+  // parts' LSE and rows are asked for together with the note that says how many there are.
+  auto slot = [&](int k, int r) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * N + r; };
+  constexpr int kEarly = 4;
+  const PagedSplit s = p.split[c];
+  const int r0 = min(me, N - 1);
+  const float lse_early = c + lane < sh.ctas ? p.Lp[slot(lane, r0)] : -INFINITY;
+  float early[kEarly][kPer];
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k) {
+    const float* src = p.Op + slot(min(k, sh.ctas - 1 - c), r0) * HD + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) early[k][e] = src[e];
+  }
   for (int b = c; b < sh.B; b += gridDim.x) {
     const PagedSeq q = paged_seq(p, b);
     const int blind = min(q.n_q, q.first * sh.tp);
@@ -454,20 +568,17 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
       if (lane == 0) p.lse[static_cast<long long>(h) * sh.T_q + q.c0 + t] = -INFINITY;
     }
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const PagedSplit s = p.split[c];
   // (Clamped: lengths that change under the call leave anything here.)
   const int n = min(s.n, sh.ctas - c), rows = min(s.rows, N);
   if (n <= 0 || s.heads <= 0) return;
   for (int r = me; r < rows; r += warps) {
     const int ti = r / s.heads, token = s.token + ti, head = s.head + r - ti * s.heads;
     if (token < 0 || token >= sh.T_q || head < 0 || head >= sh.H) continue;
-    // Part 0 is this CTA's beginning, part k the end in CTA c + k.
-    auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * c + 1 : 2 * (c + k)) * N + r; };
-    float m = -INFINITY;
-    bool any = false;
-    for (int k = lane; k < n; k += 32) {
-      const float v = p.Lp[slot(k)];
+    const float first = lane >= n ? -INFINITY : r == me ? lse_early : p.Lp[slot(lane, r)];
+    float m = first;
+    bool any = first != -INFINITY;
+    for (int k = lane + 32; k < n; k += 32) {
+      const float v = p.Lp[slot(k, r)];
       any |= v != -INFINITY;
       m = fmaxf(m, v);
     }
@@ -480,13 +591,25 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
     if (!none) {
       for (int k0 = 0; k0 < n; k0 += 32) {
-        const float w_me = k0 + lane < n ? __expf(p.Lp[slot(k0 + lane)] - m) : 0.f;
+        const float w_me = k0 + lane >= n ? 0.f : __expf((k0 == 0 ? first : p.Lp[slot(k0 + lane, r)]) - m);
         sum += w_me;
-        for (int k1 = 0; k1 < min(32, n - k0); k1 += 8) {
-          float v[8][kPer];
+        int k1 = 0;
+        if (k0 == 0 && r == me) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float* src = p.Op + slot(min(k0 + k1 + k, n - 1)) * HD + lane * kPer;
+          for (int k = 0; k < kEarly; ++k) {
+            const float w = __shfl_sync(0xffffffffu, w_me, k);
+            if (k < n) {
+#pragma unroll
+              for (int e = 0; e < kPer; ++e) acc[e] = fmaf(w, early[k][e], acc[e]);
+            }
+          }
+          k1 = kEarly;
+        }
+        for (; k1 < min(32, n - k0); k1 += 4) {
+          float v[4][kPer];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float* src = p.Op + slot(min(k0 + k1 + k, n - 1), r) * HD + lane * kPer;
             if constexpr (kPer == 4) {
               const float4 f = *reinterpret_cast<const float4*>(src);
               v[k][0] = f.x, v[k][1] = f.y, v[k][2] = f.z, v[k][3] = f.w;
@@ -496,7 +619,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
             }
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < 4; ++k) {
             const float w = __shfl_sync(0xffffffffu, w_me, k1 + k);
             if (k0 + k1 + k < n) {
 #pragma unroll

@@ -395,6 +395,6 @@ def test_a_wait_that_runs_out_is_reported(drop, new):
     assert fa.fa_fwd_paged_fault_test(q, *dev, cu, o, lse, 0.1, True, ws, drop, 20_000_000) == fa.FA_OK
     st, info = fa.fa_get_device_status()
     if drop < 2:       # (with few tiles per CTA a third load is never due)
-        assert st == fa.FA_ERR_TIMEOUT and 30 <= info[0] <= 33, (st, info)
+        assert st == fa.FA_ERR_TIMEOUT and 30 <= info[0] <= 34, (st, info)
     assert fa.fa_get_device_status()[0] == fa.FA_OK
     check(cache, new, 8, 128, q=q.cpu())
