@@ -544,6 +544,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
   const PagedShape& sh = p.s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
   const int warps = 4 * gridDim.y, me = blockIdx.y * 4 + warp;
+  ptx::grid_next();
   ptx::grid_wait();
   // Part 0 of a unit is CTA c's beginning, part k the end in CTA c + k. The first
   // parts' LSE and rows are asked for together with the note that says how many there are.
