@@ -411,15 +411,15 @@ struct PagedWalk {
 
 constexpr int kPagedJobs = 4;            // the ring through which units are handed on
 
-// A warp walks its CTA's piece, hands the units on and loads their pages, tile
-// by tile, into a ring of kStages pairs of a K and a V tile. A lane has one
-// page: 32 entries of the table are read at a time, a batch (or a unit) ahead.
-template <int HD, int kStages>
+// A warp walks its CTA's piece, hands the units on and loads their pages into a
+// ring of kTiles tiles, K and V of a key tile in turn. A lane has one page: 32
+// entries of the table are read at a time, a batch (or a unit) ahead. The scales
+// of a pair of tiles go to page_scale[pair % kScales] and count as part of the V tile.
+template <int HD, int kTiles, int kScales>
 __device__ __forceinline__ void paged_load(const PagedParams& p, const PagedLine& line, const CUtensorMap* tmK,
                                            const CUtensorMap* tmV, PagedJob* jobs, uint64_t* bar_job_full,
-                                           uint64_t* bar_job_empty, uint64_t* bar_k_full, uint64_t* bar_v_full,
-                                           uint64_t* bar_empty, float (*page_scale)[2][8], uint32_t tiles_at,
-                                           volatile int* abort_ptr) {
+                                           uint64_t* bar_job_empty, uint64_t* bar_full, uint64_t* bar_empty,
+                                           float (*page_scale)[2][8], uint32_t tiles_at, volatile int* abort_ptr) {
   constexpr uint32_t kTileBytes = 128 * HD;
   const int lane = threadIdx.x & 31;
   const PagedShape& sh = p.s;
@@ -431,7 +431,7 @@ __device__ __forceinline__ void paged_load(const PagedParams& p, const PagedLine
     return job.b >= 0 && e < (job.n_keys + in_page - 1) >> sh.page_shift
                ? p.table[static_cast<long long>(job.b) * sh.max_pages + e] : -1;
   };
-  int it = 0, end = 0, end_next = 0;
+  int it = 0, end = 0, end_next = 0;       // tiles so far
   PagedJob job{};
   int id_next = -1;
   bool ok = true;
@@ -455,70 +455,70 @@ __device__ __forceinline__ void paged_load(const PagedParams& p, const PagedLine
     int j = job.j0;
 #pragma unroll 1
     do {
-     int stage = 0, slot = 0;
-     bool mine = false, drop_v = false;
-     if (n >= 0) {
-      const int in_batch = (j - job.j0) * per_tile & 31;
-      if (in_batch == 0) {
-        const int e = j * per_tile + lane;
-        id = id_next;
-        sk = sv = 0.f;
-        if (e >= (job.n_keys + in_page - 1) >> sh.page_shift) {
-          id = -1;
-        } else if (id >= 0 && id < sh.num_pages) {
-          sk = p.k_scale[static_cast<long long>(id) * sh.H_kv + job.kvh];
-          sv = p.v_scale[static_cast<long long>(id) * sh.H_kv + job.kvh];
-        } else {
-          paged_bad(job.b);
-          id = sh.num_pages;            // outside the tensor: reads as zeros
+      const int in_batch = (j - job.j0) * per_tile & 31, slot = lane - in_batch;
+      const bool mine = n >= 0 && slot >= 0 && slot < per_tile;
+      bool drop = false;
+      uint32_t full = 0;
+      if (n >= 0) {
+        if (in_batch == 0) {
+          const int e = j * per_tile + lane;
+          id = id_next;
+          sk = sv = 0.f;
+          if (e >= (job.n_keys + in_page - 1) >> sh.page_shift) {
+            id = -1;
+          } else if (id >= 0 && id < sh.num_pages) {
+            sk = p.k_scale[static_cast<long long>(id) * sh.H_kv + job.kvh];
+            sv = p.v_scale[static_cast<long long>(id) * sh.H_kv + job.kvh];
+          } else {
+            paged_bad(job.b);
+            id = sh.num_pages;            // outside the tensor: reads as zeros
+          }
+          id_next = entry(job, e + 32);
         }
-        id_next = entry(job, e + 32);
+        const bool copy = mine && id >= 0;
+        const uint32_t bytes = (static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, copy))) << sh.page_shift) * HD;
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++it) {
+          const int tile = it % kTiles;
+          ok = wait_warp_or_abort(ptx::smem_u32(&bar_empty[tile]), ((it / kTiles) & 1) ^ 1u, abort_ptr, p.timeout_ns,
+                                  kRolePagedProducer);
+          if (!ok) break;
+          drop = it == p.drop_load;       // test hook
+          full = ptx::smem_u32(&bar_full[tile]);
+          if (lane == 0 && !drop) {
+            if (kv == 0) ptx::mbar_arrive_expect_tx(full, bytes);
+            else ptx::mbar_expect_tx(full, bytes);
+          }
+          __syncwarp();
+          if (copy && !drop)
+            ptx::tma_load_4d(tiles_at + tile * kTileBytes + (static_cast<uint32_t>(slot * HD) << sh.page_shift),
+                             kv == 0 ? tmK : tmV, full, 0, 0, job.kvh, id, policy);
+        }
+        if (!ok) break;
       }
-      stage = it % kStages;
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_empty[stage]), ((it / kStages) & 1) ^ 1u, abort_ptr, p.timeout_ns,
-                              kRolePagedProducer);
-      if (!ok) break;
-      slot = lane - in_batch;
-      mine = slot >= 0 && slot < per_tile;
-      const bool copy = mine && id >= 0, drop_k = 2 * it == p.drop_load;   // test hook
-      drop_v = 2 * it + 1 == p.drop_load;
-      const uint32_t bytes = (static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, copy))) << sh.page_shift) * HD;
-      const uint32_t k_full = ptx::smem_u32(&bar_k_full[stage]), v_full = ptx::smem_u32(&bar_v_full[stage]);
-      if (lane == 0) {
-        if (!drop_k) ptx::mbar_arrive_expect_tx(k_full, bytes);
-        if (!drop_v) ptx::mbar_expect_tx(v_full, bytes);
+      if (j == job.j0) {
+        // While the first copies are on their way: a beginning is noted for the merge; the next unit and its entries.
+        if (n >= 0 && job.slot >= 0 && job.j0 == 0 && lane == 0) {
+          PagedSplit s{};
+          s.n = walk.owner(end) - static_cast<int>(blockIdx.x) + 1;
+          s.token = job.token;
+          s.head = job.head;
+          s.heads = job.heads;
+          s.rows = job.rows;
+          p.split[blockIdx.x] = s;
+        }
+        after = walk.next(p, &end_next);
+        id_after = entry(after, after.j0 * per_tile + lane);
       }
-      __syncwarp();
-      if (copy) {
-        const uint32_t to = tiles_at + 2 * stage * kTileBytes + (static_cast<uint32_t>(slot * HD) << sh.page_shift);
-        if (!drop_k) ptx::tma_load_4d(to, tmK, k_full, 0, 0, job.kvh, id, policy);
-        if (!drop_v) ptx::tma_load_4d(to + kTileBytes, tmV, v_full, 0, 0, job.kvh, id, policy);
+      if (n >= 0) {
+        // The scales follow; the V tile counts as full when both are there.
+        if (mine) {
+          page_scale[((it >> 1) - 1) % kScales][0][slot] = sk;
+          page_scale[((it >> 1) - 1) % kScales][1][slot] = sv;
+        }
+        __syncwarp();
+        if (lane == 0 && !drop) ptx::mbar_arrive(full);
       }
-     }
-     if (j == job.j0) {
-       // While the first copies are on their way: a beginning is noted for the merge; the next unit and its entries.
-       if (n >= 0 && job.slot >= 0 && job.j0 == 0 && lane == 0) {
-         PagedSplit s{};
-         s.n = walk.owner(end) - static_cast<int>(blockIdx.x) + 1;
-         s.token = job.token;
-         s.head = job.head;
-         s.heads = job.heads;
-         s.rows = job.rows;
-         p.split[blockIdx.x] = s;
-       }
-       after = walk.next(p, &end_next);
-       id_after = entry(after, after.j0 * per_tile + lane);
-     }
-     if (n >= 0) {
-       // The scales follow; the V tile counts as full when both are there.
-       if (mine) {
-         page_scale[stage][0][slot] = sk;
-         page_scale[stage][1][slot] = sv;
-       }
-       __syncwarp();
-       if (lane == 0 && !drop_v) ptx::mbar_arrive(ptx::smem_u32(&bar_v_full[stage]));
-       ++it;
-     }
     } while (++j < job.j1);
     if (!ok) break;
     job = after;
@@ -526,11 +526,8 @@ __device__ __forceinline__ void paged_load(const PagedParams& p, const PagedLine
     end = end_next;
   }
   if (__any_sync(0xffffffffu, !ok || *abort_ptr)) {
-    for (int i = it > kStages ? it - kStages : 0; i < it; ++i) {
-      if (2 * i != p.drop_load) drain_wait(ptx::smem_u32(&bar_k_full[i % kStages]), (i / kStages) & 1, p.timeout_ns);
-      if (2 * i + 1 != p.drop_load)
-        drain_wait(ptx::smem_u32(&bar_v_full[i % kStages]), (i / kStages) & 1, p.timeout_ns);
-    }
+    for (int i = it > kTiles ? it - kTiles : 0; i < it; ++i)
+      if (i != p.drop_load) drain_wait(ptx::smem_u32(&bar_full[i % kTiles]), (i / kTiles) & 1, p.timeout_ns);
   }
   __syncwarp();
 }

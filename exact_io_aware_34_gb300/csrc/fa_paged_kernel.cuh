@@ -73,6 +73,7 @@ struct PagedCfg {
   static constexpr int kThreads = 224;
   static constexpr int kCtasPerSm = 2;
   static constexpr int kStages = HD == 128 ? 3 : 5;    // pairs of tiles
+  static constexpr int kTiles = 2 * kStages;
   static constexpr int kTileBytes = 128 * HD;          // K or V
   // With N <= 8 the hi and lo of a row stand side by side among the 16: one
   // product instead of two, the sums of both halves are added by the reader.
@@ -102,9 +103,8 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
   using C = PagedCfg<HD, N>;
   constexpr int kJobs = kPagedJobs;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_k_full[C::kStages];
-  __shared__ __align__(8) uint64_t bar_v_full[C::kStages];
-  __shared__ __align__(8) uint64_t bar_empty[C::kStages];
+  __shared__ __align__(8) uint64_t bar_full[C::kTiles];    // K and V of a key tile in turn
+  __shared__ __align__(8) uint64_t bar_empty[C::kTiles];
   __shared__ __align__(8) uint64_t bar_s_full[2];
   __shared__ __align__(8) uint64_t bar_p_full[2];
   __shared__ __align__(8) uint64_t bar_o_full[2];
@@ -140,9 +140,8 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
                     C::kQBytes % 1024 == 0, "tiles begin on swizzle atoms");
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&bar_k_full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bar_v_full[s]), 1);
+    for (int s = 0; s < C::kTiles; ++s) {
+      ptx::mbar_init(ptx::smem_u32(&bar_full[s]), 1);
       ptx::mbar_init(ptx::smem_u32(&bar_empty[s]), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -330,7 +329,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
         ok = wait_warp_or_abort(ptx::smem_u32(&bar_s_full[buf]), (g >> 1) & 1, abort_ptr, p.timeout_ns,
                                 kRolePagedSoftmax);
         if (ok)
-          ok = wait_warp_or_abort(ptx::smem_u32(&bar_v_full[stage]), (g / C::kStages) & 1, abort_ptr, p.timeout_ns,
+          ok = wait_warp_or_abort(ptx::smem_u32(&bar_full[2 * stage + 1]), (g / C::kStages) & 1, abort_ptr, p.timeout_ns,
                                   kRolePagedSoftmax);
         if (!ok) break;
         ptx::tc_fence_after();
@@ -430,8 +429,8 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
       last = job;
     }
   } else if (warp == 4) {
-    paged_load<HD, C::kStages>(p, line, &tmK, &tmV, jobs, bar_job_full, bar_job_empty, bar_k_full, bar_v_full,
-                               bar_empty, page_scale, sKV, abort_ptr);
+    paged_load<HD, C::kTiles, C::kStages>(p, line, &tmK, &tmV, jobs, bar_job_full, bar_job_empty, bar_full, bar_empty,
+                                          page_scale, sKV, abort_ptr);
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
     // One stream of tiles over all units: S of tile g + 2 follows O of tile g,
@@ -456,7 +455,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
           return false;
       }
       const int stage = gq % C::kStages;
-      if (!wait_warp_or_abort(ptx::smem_u32(&bar_k_full[stage]), (gq / C::kStages) & 1, abort_ptr, p.timeout_ns,
+      if (!wait_warp_or_abort(ptx::smem_u32(&bar_full[2 * stage]), (gq / C::kStages) & 1, abort_ptr, p.timeout_ns,
                               kRolePagedMma))
         return false;
       ptx::tc_fence_after();
@@ -470,6 +469,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
                            ptx::desc_lo(dq) + part * (C::kQBytes >> 4) + 2 * k, ptx::desc_hi(dq), idesc_qk,
                            part + k > 0 ? 1u : 0u);
       ptx::mma_commit_warp(ptx::smem_u32(&bar_s_full[gq & 1]));
+      ptx::mma_commit_warp(ptx::smem_u32(&bar_empty[2 * stage]));
       ++gq;
       if (--left == 0) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[n % C::kQBufs]));
       return true;
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
                            ptx::desc_hi(dv), ptx::desc_lo(dp) + part * (C::kPBytes >> 4) + k * 32, ptx::desc_hi(dp),
                            idesc_pv, part > 0 ? 1u : 0u);
       ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[buf]));
-      ptx::mma_commit_warp(ptx::smem_u32(&bar_empty[stage]));
+      ptx::mma_commit_warp(ptx::smem_u32(&bar_empty[2 * stage + 1]));
       if (more) ok = qk();
     }
     if (!ok) {
