@@ -20,6 +20,7 @@
 #include "fa_decode_kernel.cuh"
 #include "fa_fwd_kernel.cuh"
 #include "fa_paged_kernel.cuh"
+#include "fa_paged_wide_kernel.cuh"
 #include "fa_prefix_kernel.cuh"
 #include "fa_varlen_bwd_kernel.cuh"
 #include "fa_varlen_kernel.cuh"

@@ -68,6 +68,10 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3)));
 }
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+}
 
 // The smallest power of two s >= 2^-100 with amax <= 448 s (448 = 1.75 * 2^8).
 __device__ __forceinline__ float least_scale(float amax) {

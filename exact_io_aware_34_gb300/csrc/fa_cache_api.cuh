@@ -270,11 +270,12 @@ bool make_page_map(CUtensorMap* m, const Pages& c) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a unit: 4, 8 or 16 while the sequences' new tokens, on average, fill no more.
+// Rows of a unit: 4, 8 or 16 while the sequences' new tokens, on average, fill no
+// more (fa_paged_kernel), else 256 (fa_paged_wide_kernel).
 int paged_rows(int B, int G, int T_q) {
-  for (int n : {4, 8})
+  for (int n : {4, 8, 16})
     if (static_cast<long long>(T_q) * G <= static_cast<long long>(n) * B) return n;
-  return 16;
+  return 256;
 }
 
 fa::PagedShape paged_shape(int B, int H, int H_kv, int T_q, int num_pages, int page, int max_pages, int causal) {
@@ -301,8 +302,8 @@ long long paged_places(const fa::PagedShape& s) {
   const double places = units * (((static_cast<long long>(s.max_pages) << s.page_shift) + 127) / 128 + fa::kPagedCost);
   return places < 2147418112.0 ? static_cast<long long>(places) : 0;
 }
-int paged_ctas(const fa::PagedShape& s) {
-  return static_cast<int>(std::min(paged_places(s), 2LL * device_sm_count()));
+int paged_ctas(const fa::PagedShape& s, int N) {
+  return static_cast<int>(std::min(paged_places(s), (N > 16 ? 1LL : 2LL) * device_sm_count()));
 }
 
 struct PagedLayout {
@@ -326,10 +327,19 @@ struct PagedKernel {
 
 template <int HD, int N>
 const PagedKernel& paged_kernel() {
-  using C = fa::PagedCfg<HD, N>;
-  static const PagedKernel k{reinterpret_cast<const void*>(&fa::fa_paged_kernel<HD, N>),
-                             reinterpret_cast<const void*>(&fa::paged_merge_kernel<HD, N>), C::kSmemBytes, C::kThreads, 0};
-  return k;
+  if constexpr (N <= 16) {
+    using C = fa::PagedCfg<HD, N>;
+    static const PagedKernel k{reinterpret_cast<const void*>(&fa::fa_paged_kernel<HD, N>),
+                               reinterpret_cast<const void*>(&fa::paged_merge_kernel<HD, N>), C::kSmemBytes, C::kThreads, 0};
+    return k;
+  } else {
+    using C = fa::PagedWideCfg<HD>;
+    static_assert(N == C::kRows, "rows of a unit");
+    static const PagedKernel k{reinterpret_cast<const void*>(&fa::fa_paged_wide_kernel<HD>),
+                               reinterpret_cast<const void*>(&fa::paged_merge_kernel<HD, N>), C::kSmemBytes, C::kThreads,
+                               (C::kRegsSoftmax + C::kRegsOther) / 2};
+    return k;
+  }
 }
 
 template <int HD, int N>
@@ -380,7 +390,8 @@ fa_status_t paged_launch_rows(int N, const Pages& kc, const Pages& vc, fa::Paged
   switch (N) {
     case 4: return paged_launch<HD, 4>(kc, vc, p, stream);
     case 8: return paged_launch<HD, 8>(kc, vc, p, stream);
-    default: return paged_launch<HD, 16>(kc, vc, p, stream);
+    case 16: return paged_launch<HD, 16>(kc, vc, p, stream);
+    default: return paged_launch<HD, 256>(kc, vc, p, stream);
   }
 }
 
@@ -409,8 +420,8 @@ fa_status_t paged_impl(const void* Q, const void* K_cache, const void* V_cache, 
   fa::PagedParams p;
   p.s = paged_shape(B, H, H_kv, T_q, num_pages, page, max_pages, causal);
   if (paged_places(p.s) == 0) return FA_ERR_UNSUPPORTED;
-  p.s.ctas = paged_ctas(p.s);
   const int N = paged_rows(B, H / H_kv, T_q);
+  p.s.ctas = paged_ctas(p.s, N);
   const PagedLayout w = paged_layout(p.s.ctas, N, d);
   if (!workspace || !aligned(workspace, 128) || workspace_bytes < w.bytes) return FA_ERR_INVALID_ARG;
   auto clash = [&](const void* a, size_t na) { return rows_overlap(o, a, na) || overlaps(LSE, n_lse, a, na) ||
@@ -439,7 +450,8 @@ fa_status_t paged_impl(const void* Q, const void* K_cache, const void* V_cache, 
   p.split = reinterpret_cast<fa::PagedSplit*>(ws);
   p.Lp = reinterpret_cast<float*>(ws + w.Lp);
   p.Op = reinterpret_cast<float*>(ws + w.Op);
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  p.scale_log2 = N > 16 ? masked_scale_log2(scale) : static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  p.negate = scale < 0.f;
   p.keep = p.s.ht > 1 || T_q > static_cast<long long>(B) * p.s.tp;
   p.timeout_ns = timeout_ns;
   p.drop_load = drop_load;
@@ -493,7 +505,8 @@ size_t fa_fwd_paged_workspace_bytes(int B, int H, int H_kv, int T_q, int d, int 
                                     int max_pages) {
   if (paged_sizes(B, H, H_kv, T_q, d, num_pages, page_size, max_pages) != FA_OK) return 0;
   const fa::PagedShape s = paged_shape(B, H, H_kv, T_q, num_pages, page_size, max_pages, 1);
-  return paged_places(s) ? paged_layout(paged_ctas(s), paged_rows(B, H / H_kv, T_q), d).bytes : 0;
+  const int N = paged_rows(B, H / H_kv, T_q);
+  return paged_places(s) ? paged_layout(paged_ctas(s, N), N, d).bytes : 0;
 }
 
 fa_status_t fa_fwd_paged(const void* Q, const void* K_cache, const void* V_cache, const float* k_scale,

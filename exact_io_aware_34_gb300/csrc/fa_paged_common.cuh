@@ -125,7 +125,8 @@ struct PagedParams {
   PagedSplit* split;       // [ctas]
   float* Lp;               // [2 * ctas][N]: partial results, slot 2 c: the end of a unit, 2 c + 1: a beginning
   float* Op;               // [2 * ctas][N][d]
-  float scale_log2;
+  float scale_log2;        // fa_paged_wide_kernel: its size, and whether to negate
+  int negate;
   int keep;                // 1: K and V may be read by several CTAs
   unsigned long long timeout_ns;
   int drop_load;
