@@ -3,6 +3,8 @@
 // units that several CTAs worked on. See fa_paged_kernel.cuh.
 #pragma once
 
+#include <climits>
+
 #include "fa_append_kernel.cuh"
 #include "fa_decode_kernel.cuh"
 #include "fa_prefix_kernel.cuh"
@@ -142,26 +144,31 @@ struct PagedJob {
   int slot;                // of the partial result; -1: none, the unit is whole
 };
 
-// sum over i < n of floor((a i + b) / m), in as many steps as Euclid's algorithm
-// takes for a and m (the lattice points under a line, counted by swapping axes).
-__device__ __noinline__ unsigned floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-  unsigned sum = 0;
+// sum over i < n of floor((a i + b) / 128), in as many steps as Euclid's
+// algorithm takes for a and 128 (the lattice points under a line, counted by
+// swapping axes). a n + b stays below 2^32: it is a number of keys.
+__device__ __forceinline__ unsigned floor_sum128(unsigned n, unsigned a, unsigned b) {
+  if (n == 0) return 0;
+  unsigned sum = static_cast<unsigned>(static_cast<unsigned long long>(n - 1) * n / 2) * (a >> 7) + n * (b >> 7);
+  a &= 127u;
+  b &= 127u;
+  unsigned y = a * n + b, m = a;
+  n = y >> 7;
+  b = y & 127u;
+  a = 128;
+#pragma unroll 1
   while (n > 0) {
-    if (a >= m) {
-      sum += static_cast<unsigned>(static_cast<unsigned long long>(n - 1) * n / 2) * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      sum += n * (b / m);
-      b %= m;
-    }
-    const unsigned long long y = static_cast<unsigned long long>(a) * n + b;
+    const unsigned qa = a / m, qb = b / m;
+    sum += static_cast<unsigned>(static_cast<unsigned long long>(n - 1) * n / 2) * qa + n * qb;
+    a -= qa * m;
+    b -= qb * m;
+    y = a * n + b;
     if (y < m) break;
-    n = static_cast<unsigned>(y / m);
-    b = static_cast<unsigned>(y % m);
-    const unsigned t = m;
+    n = y / m;
+    b = y - n * m;
+    const unsigned was = m;
     m = a;
-    a = t;
+    a = was;
   }
   return sum;
 }
@@ -183,8 +190,8 @@ struct PagedSeq {
     if (!s.causal || (k == groups - first && k == 1)) return k * (kPagedCost + last);
     const int ramp = i == groups ? k - 1 : k;          // (the last tile may be short)
     return k * kPagedCost + (i == groups ? last : 0) +
-           static_cast<int>(floor_sum(static_cast<unsigned>(ramp), 128u, static_cast<unsigned>(s.tp),
-                                      static_cast<unsigned>(n_kv - n_q + (first + 1) * s.tp + 127)));
+           static_cast<int>(floor_sum128(static_cast<unsigned>(ramp), static_cast<unsigned>(s.tp),
+                                         static_cast<unsigned>(n_kv - n_q + (first + 1) * s.tp + 127)));
   }
   __device__ __forceinline__ int places(const PagedShape& s) const { return before(s, groups); }
 };
@@ -272,9 +279,11 @@ __device__ __forceinline__ PagedLine paged_line_warp(const PagedParams& p) {
   return l;
 }
 
-// The same by a whole CTA, for more sequences. Ends with a barrier.
+// The same by a whole CTA, for more sequences, into *line.
 template <int kThreads>
-__device__ __forceinline__ PagedLine paged_line_block(const PagedParams& p, int* warp_sum, int* start) {
+__device__ __noinline__ void paged_line_block(const PagedParams& p, PagedLine* line) {
+  __shared__ int warp_sum[kThreads / 32];
+  __shared__ int start[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, copies = p.s.H_kv * p.s.ht;
   if (threadIdx.x == 0) start[0] = p.s.B, start[1] = 0;
   int sum = 0;
@@ -316,7 +325,7 @@ __device__ __forceinline__ PagedLine paged_line_block(const PagedParams& p, int*
   __syncthreads();
   l.b = start[0];
   l.cum = start[1];
-  return l;
+  if (threadIdx.x == 0) *line = l;
 }
 
 // Walks a CTA's piece unit by unit; a warp's lanes all hold the same state.
@@ -342,15 +351,20 @@ struct PagedWalk {
     u = y / places;
     from = y - u * places;
     i = q.first;
-    int hi = q.groups;                           // before(i) <= from < before(hi)
+    int hi = q.groups;                           // before(i) <= from < before(hi): the lanes try 32 places at a time
     if (hi - i > 1) {
+      const int lane = threadIdx.x & 31;
+      int base = 0;
 #pragma unroll 1
       while (hi - i > 1) {
-        const int mid = (i + hi) >> 1;
-        if (q.before(sh, mid) <= from) i = mid;
-        else hi = mid;
+        const int step = (hi - i + 31) >> 5, mid = i + lane * step;
+        const int at = mid < hi ? q.before(sh, mid) : INT_MAX;
+        const int best = 31 - __clz(__ballot_sync(0xffffffffu, at <= from));
+        base = __shfl_sync(0xffffffffu, at, best);
+        hi = min(hi, i + (best + 1) * step);
+        i += best * step;
       }
-      from -= q.before(sh, i);
+      from -= base;
     }
   }
 
@@ -415,19 +429,21 @@ constexpr int kPagedJobs = 4;            // the ring through which units are han
 // A warp walks its CTA's piece, hands the units on and loads their pages into a
 // ring of kTiles tiles, K and V of a key tile in turn. A lane has one page: 32
 // entries of the table are read at a time, a batch (or a unit) ahead. The scales
-// of a pair of tiles go to page_scale[pair % kScales] and count as part of the V tile.
-template <int HD, int kTiles, int kScales>
-__device__ __forceinline__ void paged_load(const PagedParams& p, const PagedLine& line, const CUtensorMap* tmK,
+// of a pair of tiles go to page_scale[pair % kScales] (K, V, and with kLogs V's
+// logarithm and reciprocal) and count as part of the V tile.
+template <int HD, int kTiles, int kScales, bool kLogs>
+__device__ __forceinline__ void paged_load(const PagedParams& p, const PagedLine* line, const CUtensorMap* tmK,
                                            const CUtensorMap* tmV, PagedJob* jobs, uint64_t* bar_job_full,
                                            uint64_t* bar_job_empty, uint64_t* bar_full, uint64_t* bar_empty,
-                                           float (*page_scale)[2][8], uint32_t tiles_at, volatile int* abort_ptr) {
+                                           float (*page_scale)[kLogs ? 4 : 2][8], uint32_t tiles_at,
+                                           volatile int* abort_ptr) {
   constexpr uint32_t kTileBytes = 128 * HD;
   const int lane = threadIdx.x & 31;
   const PagedShape& sh = p.s;
   const uint64_t policy = p.keep ? ptx::policy_evict_last() : ptx::policy_evict_first();
   const int per_tile = 128 >> sh.page_shift, in_page = 1 << sh.page_shift;
   PagedWalk walk;
-  walk.begin(p, line);
+  walk.begin(p, p.s.B > kPagedWarpSeqs ? *line : paged_line_warp(p));
   auto entry = [&](const PagedJob& job, int e) {
     return job.b >= 0 && e < (job.n_keys + in_page - 1) >> sh.page_shift
                ? p.table[static_cast<long long>(job.b) * sh.max_pages + e] : -1;
@@ -516,6 +532,10 @@ __device__ __forceinline__ void paged_load(const PagedParams& p, const PagedLine
         if (mine) {
           page_scale[((it >> 1) - 1) % kScales][0][slot] = sk;
           page_scale[((it >> 1) - 1) % kScales][1][slot] = sv;
+          if (kLogs) {
+            page_scale[((it >> 1) - 1) % kScales][kLogs ? 2 : 0][slot] = ptx::lg2_approx(sv);
+            page_scale[((it >> 1) - 1) % kScales][kLogs ? 3 : 0][slot] = 1.f / sv;
+          }
         }
         __syncwarp();
         if (lane == 0 && !drop) ptx::mbar_arrive(full);

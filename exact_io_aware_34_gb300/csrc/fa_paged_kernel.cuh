@@ -125,8 +125,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
   __shared__ __align__(16) float factor[4][4][N];       // by reading warp: what the four O^T are multiplied by
   __shared__ __align__(16) float corr[4][N];
   __shared__ float sums[4][4][2][16];                   // by unit (modulo 4) and warp: sums of weights, what they are relative to
-  __shared__ int warp_sum[8];
-  __shared__ int start[2];
+  __shared__ PagedLine line;
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
 
@@ -179,9 +178,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
   ptx::grid_wait();
   ptx::grid_next();
   if (threadIdx.x == 0) p.split[blockIdx.x].n = 0;
-  PagedLine line{};
-  if (sh.B > kPagedWarpSeqs) line = paged_line_block<C::kThreads>(p, warp_sum, start);
-  else if (warp == 4) line = paged_line_warp(p);
+  if (sh.B > kPagedWarpSeqs) paged_line_block<C::kThreads>(p, &line);   // (else the loading warp does)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -429,7 +426,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
       last = job;
     }
   } else if (warp == 4) {
-    paged_load<HD, C::kTiles, C::kStages>(p, line, &tmK, &tmV, jobs, bar_job_full, bar_job_empty, bar_full, bar_empty,
+    paged_load<HD, C::kTiles, C::kStages, false>(p, &line, &tmK, &tmV, jobs, bar_job_full, bar_job_empty, bar_full, bar_empty,
                                           page_scale, sKV, abort_ptr);
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer

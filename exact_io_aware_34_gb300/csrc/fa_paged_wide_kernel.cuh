@@ -47,6 +47,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// A float from shared memory, read here (not kept from an earlier read).
+__device__ __forceinline__ float lds(uint32_t at) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at));
+  return x;
+}
+// 16 bytes from global to shared memory, asynchronously; and all of this thread's have come.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 }  // namespace ptx
 
 constexpr float kWideTop = 7.f;
@@ -93,10 +104,9 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
   __shared__ __align__(8) uint64_t bar_job_empty[kJobs];
   __shared__ __align__(8) uint64_t bar_drain;
   __shared__ __align__(16) PagedJob jobs[kJobs];
-  __shared__ __align__(16) float page_scale[C::kScales][2][8];
+  __shared__ __align__(16) float page_scale[C::kScales][4][8];
   __shared__ float row_scale[2][C::kRows];              // by unit (modulo 2)
-  __shared__ int warp_sum[16];
-  __shared__ int start[2];
+  __shared__ PagedLine line;
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
 
@@ -138,14 +148,12 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
   }
-  for (int i = threadIdx.x; i < C::kScales * 16; i += C::kThreads) (&page_scale[0][0][0])[i] = 0.f;
+  for (int i = threadIdx.x; i < C::kScales * 32; i += C::kThreads) (&page_scale[0][0][0])[i] = 0.f;
   // The grid before ends; the merge may be scheduled (all CTAs are resident, so it takes no one's place).
   ptx::grid_wait();
   ptx::grid_next();
   if (threadIdx.x == 0) p.split[blockIdx.x].n = 0;
-  PagedLine line{};
-  if (sh.B > kPagedWarpSeqs) line = paged_line_block<C::kThreads>(p, warp_sum, start);
-  else if (warp == 8) line = paged_line_warp(p);
+  if (sh.B > kPagedWarpSeqs) paged_line_block<C::kThreads>(p, &line);   // (else the loading warp does)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
       const bool live = row < job.rows;
       // Rows that hold no query take the last token's limit, so that they do not mask what the others need not.
       const int seen = sh.causal ? max(0, min(job.n_keys, job.lim0 + min(ti, (job.rows - 1) / job.heads))) : job.n_keys;
-      float m_use = -INFINITY, l = 0.f, q_scale = 0.f, v_ref = 0.f;   // v_ref: log2 of the V scale that O is in units of
+      float m_use = -INFINITY, l = 0.f, q_scale = 0.f, v_ref = 0.f, v_unit = 1.f;   // V scale that O is in units of, and its log2
       for (int jj = 0; jj < blocks; ++jj, ++g) {
         const int j = job.j0 + jj, pair = pair0 + jj, itV = 2 * pair + 1;
         ok = wait_warp_or_abort(ptx::smem_u32(&bar_slot_full[itV % C::kSlots]), (itV / C::kSlots) & 1, abort_ptr,
@@ -208,34 +216,38 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
           }
           ptx::tmem_st_wait();
         }
-        uint32_t s[8][16];
-        float mr[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) ptx::tmem_ld16_max(tS + 16 * c, s[c], mr[c]);
-        // Per 16 keys: the factor of S (never zero, so that -inf stays) and what is added to it.
-        float a[8], b[8];
-        {
-          const float(*ps)[8] = page_scale[pair % C::kScales];
-          if (jj == 0) {
-            float top = 0.f;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) top = fmaxf(top, ps[1][c]);
-            v_ref = top > 0.f ? ptx::lg2_approx(top) : 0.f;
-          }
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int page = 16 * c >> sh.page_shift;
-            a[c] = ptx::max_nan(q_scale * ps[0][page], 1.17549435e-38f);
-            b[c] = ptx::max_nan(ptx::lg2_approx(ps[1][page]) - v_ref, -60.f);   // (a scale of zero, too)
-          }
+        const uint32_t scales = ptx::smem_u32(page_scale[pair % C::kScales]);
+        if (jj == 0) {
+          float top = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) top = fmaxf(top, ptx::lds(scales + 32 + 4 * c));
+          v_ref = top > 0.f ? ptx::lg2_approx(top) : 0.f;
+          v_unit = ptx::ex2_approx(v_ref);
         }
-        ptx::tmem_ld_wait();
+        // Per 16 keys: the factor of S (never zero, so that -inf stays), what is added
+        // to it, and 2^- that. (Read again where they are needed: registers.)
+        auto factor = [&](int c) {
+          return ptx::max_nan(q_scale * ptx::lds(scales + 4 * (16 * c >> sh.page_shift)), 1.17549435e-38f);
+        };
+        auto offset = [&](int c) {           // (a scale of zero counts as 2^-60 of v_unit)
+          return ptx::max_nan(ptx::lds(scales + 64 + 4 * (16 * c >> sh.page_shift)) - v_ref, -60.f);
+        };
+        // The maximum: keys 64-127 first, so that keys 0-63 are in registers afterwards
+        // (all 128 scores and their weights would not fit; the others are read again).
+        uint32_t s[4][16];
         float mt = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          ptx::reg_fence16(s[c]);
-          ptx::reg_fence1(mr[c]);
-          mt = fmaxf(mt, fmaf(mr[c], a[c], b[c]));
+        for (int h = 1; h >= 0; --h) {
+          float mr[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) ptx::tmem_ld16_max(tS + 64 * h + 16 * c, s[c], mr[c]);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            ptx::reg_fence16(s[c]);
+            ptx::reg_fence1(mr[c]);
+            mt = fmaxf(mt, fmaf(mr[c], factor(4 * h + c), offset(4 * h + c)));
+          }
         }
         float alpha = 1.f;
         bool rescale_o = false;
@@ -252,26 +264,29 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
         rescale_o = __any_sync(0xffffffffu, rescale_o);
         const float neg_m = m_use == -INFINITY ? 0.f : kWideTop - m_use;
         float sum = 0.f;
-        uint32_t pk[2][32];
-        auto exponents = [&](int c) {
-          const uint64_t a2 = ptx::f2_pack(a[c], a[c]);
-          const float off = b[c] + neg_m;
-          const uint64_t off2 = ptx::f2_pack(off, off);
+        uint32_t pk[32];
+        auto exponents = [&](int c) {        // of keys 16 c .., whose scores are in s[c % 4]
+          const float a = factor(c), off = offset(c) + neg_m;
+          const uint64_t a2 = ptx::f2_pack(a, a), off2 = ptx::f2_pack(off, off);
           uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
             float x0, x1;
-            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])), a2, off2), x0, x1);
+            ptx::f2_unpack(
+                ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[c & 3][i]), __uint_as_float(s[c & 3][i + 1])), a2, off2), x0, x1);
             const float p0 = ptx::ex2_approx(x0), p1 = ptx::ex2_approx(x1);
             acc[(i >> 1) & 1] = ptx::f2_add(acc[(i >> 1) & 1], ptx::f2_pack(p0, p1));
-            pk[c >> 2][(c & 3) * 8 + (i >> 1)] = ptx::pack_f16x2(p0, p1);
+            pk[(c & 3) * 8 + (i >> 1)] = ptx::pack_f16x2(p0, p1);
           }
           float s0, s1;
           ptx::f2_unpack(ptx::f2_add(acc[0], acc[1]), s0, s1);
-          sum = fmaf(s0 + s1, ptx::ex2_approx(-b[c]), sum);
+          sum = fmaf(s0 + s1, fminf(ptx::lds(scales + 96 + 4 * (16 * c >> sh.page_shift)) * v_unit, 1.152921504606847e18f), sum);
         };
 #pragma unroll
         for (int c = 0; c < 4; ++c) exponents(c);
+        ptx::tmem_st32(tS, pk);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::tmem_ld16(tS + 64 + 16 * c, s[c]);
         if (rescale_o && jj > 0) {
 #pragma unroll
           for (int c = 0; c < HD / 32; ++c) {
@@ -284,11 +299,13 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
             ptx::tmem_st32(tO + 32 * c, o);
           }
         }
-        ptx::tmem_st32(tS, pk[0]);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ptx::reg_fence16(s[c]);
 #pragma unroll
         for (int c = 4; c < 8; ++c) exponents(c);
         l = l * alpha + sum;
-        ptx::tmem_st32(tS + 32, pk[1]);
+        ptx::tmem_st32(tS + 32, pk);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(ptx::smem_u32(&bar_p_full[t]));
@@ -299,7 +316,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
       if (!ok) break;
       ptx::tc_fence_after();
       const bool none = l == 0.f;
-      const float inv = none ? 0.f : ptx::ex2_approx(v_ref) / l;
+      const float inv = none ? 0.f : v_unit / l;
       const float lse = none ? -INFINITY : (m_use - kWideTop + __log2f(l)) * 0.69314718055994530942f;
       const int head = job.head + row - ti * job.heads, token = job.token + ti;
       if (live) {
@@ -334,7 +351,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
       ptx::tc_fence_before();
     }
   } else if (warp == 8) {
-    paged_load<HD, C::kTiles, C::kScales>(p, line, &tmK, &tmV, jobs, bar_job_full, bar_job_empty, bar_full, bar_empty,
+    paged_load<HD, C::kTiles, C::kScales, true>(p, &line, &tmK, &tmV, jobs, bar_job_full, bar_job_empty, bar_full, bar_empty,
                                           page_scale, sTiles, abort_ptr);
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
@@ -378,14 +395,22 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
         const bool last = jj + 1 == blocks;
         for (int t = 0; t < nt && ok; ++t) {
           ok = wait_warp_or_abort(ptx::smem_u32(&bar_p_full[t]), (g[t] - 1) & 1, abort_ptr, p.timeout_ns, kRolePagedMma);
-          if (ok && t == 0) ok = slot_wait(itV) && (last || slot_wait(itK));
+          if (ok && t == 0) ok = slot_wait(itV);
           if (!ok) break;
           ptx::tc_fence_after();
           const uint64_t v = ptx::desc_mnmajor_sw128(sSlots + (itV % C::kSlots) * C::kTileBytes, C::kChunkBytes);
           ptx::mma_ts_k128_warp<32>(tmem_base + C::kColO + HD * t, tmem_base + C::kColS + 128 * t, ptx::desc_lo(v),
                                     ptx::desc_hi(v), C::kIdescPV, jj > 0 ? 1u : 0u);
-          if (last) ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[t]));
-          else qk(t, itK);
+          if (last) {
+            ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[t]));
+            continue;
+          }
+          if (t == 0) {
+            ok = slot_wait(itK);
+            if (!ok) break;
+            ptx::tc_fence_after();
+          }
+          qk(t, itK);
         }
         if (!ok) break;
         ptx::mma_commit_warp(ptx::smem_u32(&bar_slot_empty[itV % C::kSlots]));
@@ -415,47 +440,6 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[ring]));
       if (job.b < 0) break;
-      // The query rows: kLanes lanes a row, 16 elements each.
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_q_empty), (n & 1) ^ 1u, abort_ptr, kUnitWaits * p.timeout_ns,
-                              kRolePagedQuery);
-      if (!ok) break;
-      {
-        constexpr int kLanes = HD / 16, kStep = 128 / kLanes;
-        const int part = tid % kLanes, rows = job.rows <= 128 ? 128 : 256;
-#pragma unroll 2
-        for (int r = tid / kLanes; r < rows; r += kStep) {
-          uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
-          if (r < job.rows) {
-            const int ti = r / job.heads;
-            const __nv_bfloat16* src = p.q + (job.token + ti) * p.q_t + (job.head + r - ti * job.heads) * p.q_h + 16 * part;
-            v0 = *reinterpret_cast<const uint4*>(src);
-            v1 = *reinterpret_cast<const uint4*>(src + 8);
-          }
-          float x[16], amax = 0.f;
-          unpack8(v0, x);
-          unpack8(v1, x + 8);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (fabsf(x[e]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(x[e]));
-            else x[e] = __uint_as_float(0x7fffffffu);
-          }
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          const int up = amax > 0.f ? max(-120, min(120, 134 - static_cast<int>(__float_as_uint(amax) >> 23))) : 0;
-          const float scale = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = ptx::pack_f16x2(x[2 * e] * scale, x[2 * e + 1] * scale);
-          // Row r of tile r / 128; 16-byte units 2 part and 2 part + 1, swizzled within their 128-byte chunk.
-          uint8_t* to = generic + (r >> 7) * C::kTileBytes + (part >> 2) * C::kChunkBytes + (r & 127) * 128;
-          const int u = 2 * (part & 3);
-          *reinterpret_cast<uint4*>(to + ((u ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(to + (((u + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-          if (part == 0) row_scale[n & 1][r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-        }
-      }
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(ptx::smem_u32(&bar_q_full));
       // The tiles: a thread has a key's row.
       for (int j = job.j0; j < job.j1 && ok; ++j) {
         const bool clear = j * 128 + tid >= job.n_keys;   // (rows behind the unit's keys may hold anything)
@@ -496,6 +480,60 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
           if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_empty[tile]));
           ptx::fence_proxy_async_smem();
           ptx::mbar_arrive(ptx::smem_u32(&bar_slot_full[slot]));
+          if (j > job.j0 || kv > 0) continue;
+          // The query rows, behind the unit's first K tile: kLanes lanes a row, 16
+          // elements each. They come as bf16 to where they will stand as f16 (all
+          // at once: a loop of loads took 15000 cycles and more), and every thread
+          // converts what it asked for.
+          ok = wait_warp_or_abort(ptx::smem_u32(&bar_q_empty), (n & 1) ^ 1u, abort_ptr, kUnitWaits * p.timeout_ns,
+                                  kRolePagedQuery);
+          if (!ok) break;
+          constexpr int kLanes = HD / 16, kStep = 128 / kLanes;
+          const int part = tid % kLanes, rows = job.rows <= 128 ? 128 : 256, u = 2 * (part & 3);
+          // Row r of tile r / 128; 16-byte units 2 part and 2 part + 1, swizzled within their 128-byte chunk.
+          auto place = [&](int r) {
+            return static_cast<uint32_t>((r >> 7) * C::kTileBytes + (part >> 2) * C::kChunkBytes + (r & 127) * 128);
+          };
+          int ti = (tid / kLanes) / job.heads, hi = tid / kLanes - ti * job.heads;
+#pragma unroll 1
+          for (int r = tid / kLanes; r < job.rows; r += kStep) {
+            const __nv_bfloat16* src = p.q + (job.token + ti) * p.q_t + (job.head + hi) * p.q_h + 16 * part;
+            const uint32_t dst = sQ + place(r);
+            ptx::cp_async16(dst + ((u ^ (r & 7)) << 4), src);
+            ptx::cp_async16(dst + (((u + 1) ^ (r & 7)) << 4), src + 8);
+            for (hi += kStep; hi >= job.heads; hi -= job.heads) ++ti;
+          }
+          ptx::cp_async_wait();
+#pragma unroll 1
+          for (int r = tid / kLanes; r < rows; r += kStep) {
+            uint8_t* to0 = generic + place(r) + ((u ^ (r & 7)) << 4);
+            uint8_t* to1 = generic + place(r) + (((u + 1) ^ (r & 7)) << 4);
+            uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
+            if (r < job.rows) {
+              v0 = *reinterpret_cast<const uint4*>(to0);
+              v1 = *reinterpret_cast<const uint4*>(to1);
+            }
+            float x[16], amax = 0.f;
+            unpack8(v0, x);
+            unpack8(v1, x + 8);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              if (fabsf(x[e]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(x[e]));
+              else x[e] = __uint_as_float(0x7fffffffu);
+            }
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const int up = amax > 0.f ? max(-120, min(120, 134 - static_cast<int>(__float_as_uint(amax) >> 23))) : 0;
+            const float scale = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = ptx::pack_f16x2(x[2 * e] * scale, x[2 * e + 1] * scale);
+            *reinterpret_cast<uint4*>(to0) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(to1) = make_uint4(h[4], h[5], h[6], h[7]);
+            if (part == 0) row_scale[n & 1][r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+          }
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(ptx::smem_u32(&bar_q_full));
         }
       }
     }
