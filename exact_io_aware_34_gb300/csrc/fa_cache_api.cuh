@@ -325,7 +325,7 @@ struct PagedKernel {
   int smem, threads, regs;      // regs: needed per thread at launch, 0: any
 };
 
-template <int HD, int N>
+template <int HD, int N, int NG>
 const PagedKernel& paged_kernel() {
   if constexpr (N <= 16) {
     using C = fa::PagedCfg<HD, N>;
@@ -333,18 +333,18 @@ const PagedKernel& paged_kernel() {
                                reinterpret_cast<const void*>(&fa::paged_merge_kernel<HD, N>), C::kSmemBytes, C::kThreads, 0};
     return k;
   } else {
-    using C = fa::PagedWideCfg<HD>;
+    using C = fa::PagedWideCfg<HD, NG>;
     static_assert(N == C::kRows, "rows of a unit");
-    static const PagedKernel k{reinterpret_cast<const void*>(&fa::fa_paged_wide_kernel<HD>),
+    static const PagedKernel k{reinterpret_cast<const void*>(&fa::fa_paged_wide_kernel<HD, NG>),
                                reinterpret_cast<const void*>(&fa::paged_merge_kernel<HD, N>), C::kSmemBytes, C::kThreads,
                                (C::kRegsSoftmax + C::kRegsOther) / 2};
     return k;
   }
 }
 
-template <int HD, int N>
+template <int HD, int N, int NG = 0>
 fa_status_t paged_launch(const Pages& kc, const Pages& vc, fa::PagedParams& p, cudaStream_t stream) {
-  const PagedKernel& k = paged_kernel<HD, N>();
+  const PagedKernel& k = paged_kernel<HD, N, NG>();
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -391,7 +391,9 @@ fa_status_t paged_launch_rows(int N, const Pages& kc, const Pages& vc, fa::Paged
     case 4: return paged_launch<HD, 4>(kc, vc, p, stream);
     case 8: return paged_launch<HD, 8>(kc, vc, p, stream);
     case 16: return paged_launch<HD, 16>(kc, vc, p, stream);
-    default: return paged_launch<HD, 256>(kc, vc, p, stream);
+    default:
+      return p.s.page_shift >= 6 ? paged_launch<HD, 256, 2>(kc, vc, p, stream)
+                                 : paged_launch<HD, 256, 8>(kc, vc, p, stream);
   }
 }
 

@@ -3,13 +3,12 @@
 //
 // With hundreds of query rows per key the tensor core is what bounds the work,
 // and fa_paged_kernel's transposed tiles, whose softmax needs a maximum over
-// lanes, are in its way. Here a lane has a row, as in fa_varlen_fwd_kernel, and
-// both products run in f16: an e4m3 number is exact in f16, a bf16 query row is
-// too once a power of two has brought its largest element to [128, 256) (all
-// but elements below 2^-25 of that), and P has eleven bits. Four warps convert
-// the tiles of K and V from their 8-bit ring into a ring of f16 tiles in the
-// tensor core's layout: 2 x 16 K elements for each 128 keys, beside products
-// that take 2048 cycles for the unit's 256 rows.
+// lanes, are in its way. Here a lane has a row, as in fa_varlen_fwd_kernel.
+// Q K^T takes K as it is stored, and a query row as two e4m3 numbers (see
+// fa_paged_kernel.cuh: the cost of one bf16 product). P V runs in f16, in which
+// e4m3 numbers are exact and P has eleven bits: four warps convert each V tile
+// into the tensor core's layout, 16 K elements for each 128 keys, beside
+// products that take 2048 cycles for the unit's 256 rows.
 //
 // Scales. S times (row's scale x page's K scale) is a score in powers of two;
 // log2 of the page's V scale is added to it, so P carries that scale and P V
@@ -24,7 +23,7 @@
 //
 // Per CTA (512 threads, one per SM): warps 0-7 softmax and epilogue, warp 8
 // walks the line and loads pages, warp 9 issues products, warps 10 and 11 idle,
-// warps 12-15 convert query rows and tiles.
+// warps 12-15 convert query rows and V tiles.
 #pragma once
 
 #include "fa_paged_common.cuh"
@@ -32,13 +31,15 @@
 namespace fa {
 
 namespace ptx {
-// tmem_ld32_max for 16 columns.
-__device__ __forceinline__ void tmem_ld16_max(uint32_t taddr, uint32_t (&r)[16], float& mx) {
+// tmem_ld32_max for 16 columns, into r[O] .. r[O + 15].
+template <int O>
+__device__ __forceinline__ void tmem_ld16_max(uint32_t taddr, uint32_t (&r)[32], float& mx) {
   asm volatile(
       "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, [%17];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=f"(mx)
+      : "=r"(r[O]), "=r"(r[O + 1]), "=r"(r[O + 2]), "=r"(r[O + 3]), "=r"(r[O + 4]), "=r"(r[O + 5]), "=r"(r[O + 6]),
+        "=r"(r[O + 7]), "=r"(r[O + 8]), "=r"(r[O + 9]), "=r"(r[O + 10]), "=r"(r[O + 11]), "=r"(r[O + 12]),
+        "=r"(r[O + 13]), "=r"(r[O + 14]), "=r"(r[O + 15]), "=f"(mx)
       : "r"(taddr));
 }
 // Two floats to packed f16x2: `lo` in bits [0,16).
@@ -62,33 +63,38 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_al
 
 constexpr float kWideTop = 7.f;
 
-template <int HD>
+// NG: equal parts of a tile whose keys share their pages' scales, 2 for pages of 64
+// rows and more, else 8.
+template <int HD, int NG>
 struct PagedWideCfg {
   static constexpr int kRows = 256;
   static constexpr int kThreads = 512;
   static constexpr int kChunks = HD / 64;              // 128-byte swizzle chunks of a row
   static constexpr int kChunkBytes = 128 * 128;
-  static constexpr int kTileBytes = kChunks * kChunkBytes;   // f16
-  static constexpr int kSlots = HD == 128 ? 3 : 6;     // f16 tiles
-  static constexpr int kTiles = HD == 128 ? 3 : 6;     // 8-bit tiles
+  static constexpr int kSlotBytes = kChunks * kChunkBytes;   // a V tile in f16
+  static constexpr int kSlots = HD == 128 ? 2 : 4;
+  static constexpr int kTileBytes = 128 * HD;          // 8 bits
+  static constexpr int kTiles = HD == 128 ? 4 : 8;     // (even: K and V tiles keep their places)
   static constexpr int kScales = 8;                    // pairs whose scales are held
-  static constexpr int kSmemQ = 2 * kTileBytes;
-  static constexpr int kSmemBytes = kSmemQ + kSlots * kTileBytes + kTiles * 128 * HD + 1024;
+  static constexpr int kSmemQ = 4 * kTileBytes;        // row tile, hi or lo
+  static constexpr int kSmemBytes = kSmemQ + kSlots * kSlotBytes + kTiles * kTileBytes + 1024;
+  static constexpr uint32_t kSwizzle = HD == 128 ? 2 : 4;
+  static constexpr uint32_t kAtom = 8 * HD;            // eight rows of 8 bits
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0;                 // + 128 * tile
   static constexpr uint32_t kColO = 256;               // + HD * tile
   static constexpr int kRegsSoftmax = 184, kRegsOther = 72;
   static_assert(8 * kRegsSoftmax + 8 * kRegsOther <= 16 * 128, "register split exceeds the launch");
   // kind::f16 with f16 operands (format 0).
-  static constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(128, 128, false, false) & ~(1u << 7 | 1u << 10);
   static constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(128, HD, false, true) & ~(1u << 7 | 1u << 10);
+  static constexpr uint32_t kIdescQK = ptx::idesc_e4m3_f32(128, 128, false, false);
 };
 
-template <int HD>
-__global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
+template <int HD, int NG>
+__global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
     fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const PagedParams p) {
-  using C = PagedWideCfg<HD>;
+  using C = PagedWideCfg<HD, NG>;
   constexpr int kJobs = kPagedJobs;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[C::kTiles];    // 8-bit tiles, K and V of a key tile in turn
@@ -96,6 +102,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
   __shared__ __align__(8) uint64_t bar_slot_full[C::kSlots];
   __shared__ __align__(8) uint64_t bar_slot_empty[C::kSlots];
   __shared__ __align__(8) uint64_t bar_s_full[2];
+  __shared__ __align__(8) uint64_t bar_p_half[2];          // weights of keys 0-63
   __shared__ __align__(8) uint64_t bar_p_full[2];
   __shared__ __align__(8) uint64_t bar_o_full[2];
   __shared__ __align__(8) uint64_t bar_q_full;
@@ -114,12 +121,12 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
   const PagedShape& sh = p.s;
   const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* generic = smem_raw + (smem_base - ptx::smem_u32(smem_raw));
-  const uint32_t sQ = smem_base, sSlots = sQ + C::kSmemQ, sTiles = sSlots + C::kSlots * C::kTileBytes;
+  const uint32_t sQ = smem_base, sSlots = sQ + C::kSmemQ, sTiles = sSlots + C::kSlots * C::kSlotBytes;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kTiles; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bar_full[s]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bar_empty[s]), 4);
+      ptx::mbar_init(ptx::smem_u32(&bar_empty[s]), s & 1 ? 4 : 1);   // V: the converting warps, K: the products
     }
     for (int s = 0; s < C::kSlots; ++s) {
       ptx::mbar_init(ptx::smem_u32(&bar_slot_full[s]), 128);
@@ -127,6 +134,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(ptx::smem_u32(&bar_s_full[t]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bar_p_half[t]), 128);
       ptx::mbar_init(ptx::smem_u32(&bar_p_full[t]), 128);
       ptx::mbar_init(ptx::smem_u32(&bar_o_full[t]), 1);
     }
@@ -190,8 +198,9 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
       const int seen = sh.causal ? max(0, min(job.n_keys, job.lim0 + min(ti, (job.rows - 1) / job.heads))) : job.n_keys;
       float m_use = -INFINITY, l = 0.f, q_scale = 0.f, v_ref = 0.f, v_unit = 1.f;   // V scale that O is in units of, and its log2
       for (int jj = 0; jj < blocks; ++jj, ++g) {
-        const int j = job.j0 + jj, pair = pair0 + jj, itV = 2 * pair + 1;
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_slot_full[itV % C::kSlots]), (itV / C::kSlots) & 1, abort_ptr,
+        const int j = job.j0 + jj, pair = pair0 + jj;
+        // (V's slot is waited for because the scales come with it.)
+        ok = wait_warp_or_abort(ptx::smem_u32(&bar_slot_full[pair % C::kSlots]), (pair / C::kSlots) & 1, abort_ptr,
                                 p.timeout_ns, kRolePagedSoftmax);
         if (ok)
           ok = wait_warp_or_abort(ptx::smem_u32(&bar_s_full[t]), g & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax);
@@ -224,29 +233,50 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
           v_ref = top > 0.f ? ptx::lg2_approx(top) : 0.f;
           v_unit = ptx::ex2_approx(v_ref);
         }
-        // Per 16 keys: the factor of S (never zero, so that -inf stays), what is added
-        // to it, and 2^- that. (Read again where they are needed: registers.)
-        auto factor = [&](int c) {
-          return ptx::max_nan(q_scale * ptx::lds(scales + 4 * (16 * c >> sh.page_shift)), 1.17549435e-38f);
+        uint32_t s[4][32];
+        float mr[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if constexpr (NG == 2) {
+            ptx::tmem_ld32_max(tS + 32 * c, s[c], mr[c]);
+          } else {
+            ptx::tmem_ld16_max<0>(tS + 32 * c, s[c], mr[2 * c]);
+            ptx::tmem_ld16_max<16>(tS + 32 * c + 16, s[c], mr[2 * c + 1]);
+          }
+        }
+        // Per part: the factor of S (never zero, so that -inf stays), what is added
+        // to it, and 2^- that. Eight parts' are read again where they are needed (registers).
+        const int part_shift = NG == 2 ? 6 : 4;
+        auto factor = [&](int g) {
+          return ptx::max_nan(q_scale * ptx::lds(scales + 4 * ((g << part_shift) >> sh.page_shift)), 1.17549435e-38f);
         };
-        auto offset = [&](int c) {           // (a scale of zero counts as 2^-60 of v_unit)
-          return ptx::max_nan(ptx::lds(scales + 64 + 4 * (16 * c >> sh.page_shift)) - v_ref, -60.f);
+        auto offset = [&](int g) {           // (a scale of zero counts as 2^-60 of v_unit)
+          return ptx::max_nan(ptx::lds(scales + 64 + 4 * ((g << part_shift) >> sh.page_shift)) - v_ref, -60.f);
         };
-        // The maximum: keys 64-127 first, so that keys 0-63 are in registers afterwards
-        // (all 128 scores and their weights would not fit; the others are read again).
-        uint32_t s[4][16];
+        auto back = [&](int g) {
+          return fminf(ptx::lds(scales + 96 + 4 * ((g << part_shift) >> sh.page_shift)) * v_unit, 1.152921504606847e18f);
+        };
+        float fa2[2], fb2[2];
+        if constexpr (NG == 2) {
+#pragma unroll
+          for (int g2 = 0; g2 < 2; ++g2) {
+            fa2[g2] = factor(g2);
+            fb2[g2] = offset(g2);
+          }
+        }
+        ptx::tmem_ld_wait();
         float mt = -INFINITY;
 #pragma unroll
-        for (int h = 1; h >= 0; --h) {
-          float mr[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) ptx::tmem_ld16_max(tS + 64 * h + 16 * c, s[c], mr[c]);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            ptx::reg_fence16(s[c]);
+        for (int c = 0; c < 4; ++c) {
+          ptx::reg_fence32(s[c]);
+          if constexpr (NG == 2) {
             ptx::reg_fence1(mr[c]);
-            mt = fmaxf(mt, fmaf(mr[c], factor(4 * h + c), offset(4 * h + c)));
+            mt = fmaxf(mt, fmaf(mr[c], fa2[c >> 1], fb2[c >> 1]));
+          } else {
+            ptx::reg_fence1(mr[2 * c]);
+            ptx::reg_fence1(mr[2 * c + 1]);
+            mt = fmaxf(mt, fmaxf(fmaf(mr[2 * c], factor(2 * c), offset(2 * c)),
+                                 fmaf(mr[2 * c + 1], factor(2 * c + 1), offset(2 * c + 1))));
           }
         }
         float alpha = 1.f;
@@ -265,28 +295,37 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
         const float neg_m = m_use == -INFINITY ? 0.f : kWideTop - m_use;
         float sum = 0.f;
         uint32_t pk[32];
-        auto exponents = [&](int c) {        // of keys 16 c .., whose scores are in s[c % 4]
-          const float a = factor(c), off = offset(c) + neg_m;
-          const uint64_t a2 = ptx::f2_pack(a, a), off2 = ptx::f2_pack(off, off);
-          uint64_t acc[2] = {0ull, 0ull};
+        // Weights of keys 32 c .. 32 c + 31.
+        auto exponents = [&](int c) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float x0, x1;
-            ptx::f2_unpack(
-                ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[c & 3][i]), __uint_as_float(s[c & 3][i + 1])), a2, off2), x0, x1);
-            const float p0 = ptx::ex2_approx(x0), p1 = ptx::ex2_approx(x1);
-            acc[(i >> 1) & 1] = ptx::f2_add(acc[(i >> 1) & 1], ptx::f2_pack(p0, p1));
-            pk[(c & 3) * 8 + (i >> 1)] = ptx::pack_f16x2(p0, p1);
+          for (int q = 0; q < 2; ++q) {
+            const int part = NG == 2 ? c >> 1 : 2 * c + q;
+            float a, off;
+            if constexpr (NG == 2) {
+              a = fa2[part & 1];
+              off = fb2[part & 1] + neg_m;
+            } else {
+              a = factor(part);
+              off = offset(part) + neg_m;
+            }
+            const uint64_t a2 = ptx::f2_pack(a, a), off2 = ptx::f2_pack(off, off);
+            uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+            for (int i = 16 * q; i < 16 * q + 16; i += 2) {
+              float x0, x1;
+              ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1])), a2, off2),
+                             x0, x1);
+              const float p0 = ptx::ex2_approx(x0), p1 = ptx::ex2_approx(x1);
+              acc[(i >> 1) & 1] = ptx::f2_add(acc[(i >> 1) & 1], ptx::f2_pack(p0, p1));
+              pk[(c & 1) * 16 + (i >> 1)] = ptx::pack_f16x2(p0, p1);
+            }
+            float s0, s1;
+            ptx::f2_unpack(ptx::f2_add(acc[0], acc[1]), s0, s1);
+            sum = fmaf(s0 + s1, back(part), sum);
           }
-          float s0, s1;
-          ptx::f2_unpack(ptx::f2_add(acc[0], acc[1]), s0, s1);
-          sum = fmaf(s0 + s1, fminf(ptx::lds(scales + 96 + 4 * (16 * c >> sh.page_shift)) * v_unit, 1.152921504606847e18f), sum);
         };
-#pragma unroll
-        for (int c = 0; c < 4; ++c) exponents(c);
-        ptx::tmem_st32(tS, pk);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld16(tS + 64 + 16 * c, s[c]);
+        exponents(0);
+        exponents(1);
         if (rescale_o && jj > 0) {
 #pragma unroll
           for (int c = 0; c < HD / 32; ++c) {
@@ -299,11 +338,12 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
             ptx::tmem_st32(tO + 32 * c, o);
           }
         }
-        ptx::tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::reg_fence16(s[c]);
-#pragma unroll
-        for (int c = 4; c < 8; ++c) exponents(c);
+        ptx::tmem_st32(tS, pk);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_u32(&bar_p_half[t]));
+        exponents(2);
+        exponents(3);
         l = l * alpha + sum;
         ptx::tmem_st32(tS + 32, pk);
         ptx::tmem_st_wait();
@@ -356,21 +396,27 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
     bool ok = true;
-    int it0 = 0;                             // tiles (K and V) of the units before
-    int g[2] = {0, 0};                       // key blocks of each row tile so far
-    auto slot_wait = [&](int it) {
-      return wait_warp_or_abort(ptx::smem_u32(&bar_slot_full[it % C::kSlots]), (it / C::kSlots) & 1, abort_ptr,
-                                p.timeout_ns, kRolePagedMma);
+    int pair0 = 0;                           // key tiles of the units before
+    int g[2] = {0, 0};                       // key tiles of each row tile so far
+    // S_t = K tile `pair` times the row tile's hi and lo.
+    auto k_wait = [&](int pair) {
+      const int it = 2 * pair;
+      if (!wait_warp_or_abort(ptx::smem_u32(&bar_full[it % C::kTiles]), (it / C::kTiles) & 1, abort_ptr, p.timeout_ns,
+                              kRolePagedMma))
+        return false;
+      ptx::tc_fence_after();
+      return true;
     };
     const uint32_t idesc_qk = C::kIdescQK | (p.negate ? ptx::kIdescNegateA : 0u);
-    auto qk = [&](int t, int it) {
-      const uint64_t a = ptx::desc_kmajor_sw128(sQ + t * C::kTileBytes);
-      const uint64_t b = ptx::desc_kmajor_sw128(sSlots + (it % C::kSlots) * C::kTileBytes);
-      const uint32_t d = tmem_base + C::kColS + 128 * t;
-      if constexpr (HD == 128)
-        ptx::mma_ss_k128_warp(d, ptx::desc_lo(a), ptx::desc_lo(b), ptx::desc_hi(a), idesc_qk, 0u);
-      else
-        ptx::mma_ss_k64_warp(d, ptx::desc_lo(a), ptx::desc_lo(b), ptx::desc_hi(a), idesc_qk, 0u);
+    auto qk = [&](int t, int pair) {
+      const uint64_t a = ptx::desc_of(sQ + 2 * t * C::kTileBytes, 16, C::kAtom, C::kSwizzle);
+      const uint64_t b = ptx::desc_of(sTiles + (2 * pair % C::kTiles) * C::kTileBytes, 16, C::kAtom, C::kSwizzle);
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int k = 0; k < HD / 32; ++k)
+          ptx::mma_f8_warp(tmem_base + C::kColS + 128 * t, ptx::desc_lo(a) + part * (C::kTileBytes >> 4) + 2 * k,
+                           ptx::desc_hi(a), ptx::desc_lo(b) + 2 * k, ptx::desc_hi(b), idesc_qk, part + k > 0 ? 1u : 0u);
       ptx::mma_commit_warp(ptx::smem_u32(&bar_s_full[t]));
       ++g[t];
     };
@@ -383,43 +429,46 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[ring]));
       if (b < 0) break;
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_q_full), n & 1, abort_ptr, p.timeout_ns, kRolePagedMma) && slot_wait(it0);
+      ok = wait_warp_or_abort(ptx::smem_u32(&bar_q_full), n & 1, abort_ptr, p.timeout_ns, kRolePagedMma) && k_wait(pair0);
       if (!ok) break;
-      ptx::tc_fence_after();
       // (Every P of the unit before has been waited for, so S is free; its O is read before this unit's first P.)
-      for (int t = 0; t < nt; ++t) qk(t, it0);
-      ptx::mma_commit_warp(ptx::smem_u32(&bar_slot_empty[it0 % C::kSlots]));
+      for (int t = 0; t < nt; ++t) qk(t, pair0);
+      ptx::mma_commit_warp(ptx::smem_u32(&bar_empty[2 * pair0 % C::kTiles]));
       if (blocks == 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty));
       for (int jj = 0; jj < blocks && ok; ++jj) {
-        const int itV = it0 + 2 * jj + 1, itK = itV + 1;
+        const int pair = pair0 + jj;
         const bool last = jj + 1 == blocks;
+        const uint64_t v = ptx::desc_mnmajor_sw128(sSlots + (pair % C::kSlots) * C::kSlotBytes, C::kChunkBytes);
         for (int t = 0; t < nt && ok; ++t) {
-          ok = wait_warp_or_abort(ptx::smem_u32(&bar_p_full[t]), (g[t] - 1) & 1, abort_ptr, p.timeout_ns, kRolePagedMma);
-          if (ok && t == 0) ok = slot_wait(itV);
+          // P V in two halves: the first runs while the weights of keys 64-127 are still computed.
+          const uint32_t d = tmem_base + C::kColO + HD * t, a = tmem_base + C::kColS + 128 * t, par = (g[t] - 1) & 1;
+          ok = wait_warp_or_abort(ptx::smem_u32(&bar_p_half[t]), par, abort_ptr, p.timeout_ns, kRolePagedMma);
+          if (ok && t == 0)
+            ok = wait_warp_or_abort(ptx::smem_u32(&bar_slot_full[pair % C::kSlots]), (pair / C::kSlots) & 1, abort_ptr,
+                                    p.timeout_ns, kRolePagedMma);
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint64_t v = ptx::desc_mnmajor_sw128(sSlots + (itV % C::kSlots) * C::kTileBytes, C::kChunkBytes);
-          ptx::mma_ts_k128_warp<32>(tmem_base + C::kColO + HD * t, tmem_base + C::kColS + 128 * t, ptx::desc_lo(v),
-                                    ptx::desc_hi(v), C::kIdescPV, jj > 0 ? 1u : 0u);
+          ptx::mma_ts_k64half_warp<0>(d, a, ptx::desc_lo(v), ptx::desc_hi(v), C::kIdescPV, jj > 0 ? 1u : 0u);
+          ok = wait_warp_or_abort(ptx::smem_u32(&bar_p_full[t]), par, abort_ptr, p.timeout_ns, kRolePagedMma);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          ptx::mma_ts_k64half_warp<1>(d, a, ptx::desc_lo(v), ptx::desc_hi(v), C::kIdescPV, 1u);
           if (last) {
             ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[t]));
-            continue;
+          } else {
+            // (Behind P V of the same tile, whose P lies where S will: products run in order.)
+            if (t == 0) ok = k_wait(pair + 1);
+            if (ok) qk(t, pair + 1);
           }
-          if (t == 0) {
-            ok = slot_wait(itK);
-            if (!ok) break;
-            ptx::tc_fence_after();
-          }
-          qk(t, itK);
         }
         if (!ok) break;
-        ptx::mma_commit_warp(ptx::smem_u32(&bar_slot_empty[itV % C::kSlots]));
+        ptx::mma_commit_warp(ptx::smem_u32(&bar_slot_empty[pair % C::kSlots]));
         if (!last) {
-          ptx::mma_commit_warp(ptx::smem_u32(&bar_slot_empty[itK % C::kSlots]));
+          ptx::mma_commit_warp(ptx::smem_u32(&bar_empty[2 * (pair + 1) % C::kTiles]));
           if (jj + 2 == blocks) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty));
         }
       }
-      it0 += 2 * blocks;
+      pair0 += blocks;
     }
     if (!ok) {
       ptx::mma_commit_warp(ptx::smem_u32(&bar_drain));
@@ -427,10 +476,10 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
     }
     __syncwarp();
   } else if (warp >= 12) {
-    // ------------------------------------------------------------ conversion to f16
+    // ------------------------------------------------------------ conversion
     const int tid = threadIdx.x - 384;
     bool ok = true;
-    int it = 0;                              // tiles so far
+    int pair = 0;                            // key tiles so far
     for (int n = 0; ok; ++n) {
       const int ring = n & (kJobs - 1);
       ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_full[ring]), (n / kJobs) & 1, abort_ptr,
@@ -440,101 +489,103 @@ __global__ void __launch_bounds__(PagedWideCfg<HD>::kThreads, 1)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[ring]));
       if (job.b < 0) break;
-      // The tiles: a thread has a key's row.
-      for (int j = job.j0; j < job.j1 && ok; ++j) {
-        const bool clear = j * 128 + tid >= job.n_keys;   // (rows behind the unit's keys may hold anything)
+      // The query rows, kLanes lanes a row, 16 elements each: as bf16 to where
+      // their hi and lo will stand (all at once: a loop of loads took 15000 cycles
+      // and more); then every thread converts what it asked for.
+      ok = wait_warp_or_abort(ptx::smem_u32(&bar_q_empty), (n & 1) ^ 1u, abort_ptr, kUnitWaits * p.timeout_ns,
+                              kRolePagedQuery);
+      if (!ok) break;
+      {
+        constexpr int kLanes = HD / 16, kStep = 128 / kLanes;
+        const int part = tid % kLanes, rows = job.rows <= 128 ? 128 : 256;
+        // Row r of tile r / 128: 16 bytes of hi, and kTileBytes behind them of lo.
+        auto place = [&](int r) {
+          return static_cast<uint32_t>((r >> 7) * 2 * C::kTileBytes + (r & 127) * HD +
+                                       ((part ^ (HD == 128 ? r & 7 : (r >> 1) & 3)) << 4));
+        };
+        int ti = (tid / kLanes) / job.heads, hi = tid / kLanes - ti * job.heads;
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int tile = it % C::kTiles, slot = it % C::kSlots;
-          ok = wait_warp_or_abort(ptx::smem_u32(&bar_full[tile]), (it / C::kTiles) & 1, abort_ptr, p.timeout_ns,
-                                  kRolePagedQuery);
-          if (!ok) break;
-          uint4 v[HD / 16];
-          const uint8_t* from = generic + (sTiles - smem_base) + tile * 128 * HD + tid * HD;
-#pragma unroll
-          for (int i = 0; i < HD / 16; ++i)
-            v[i] = *reinterpret_cast<const uint4*>(from + ((i ^ (HD == 128 ? tid & 7 : (tid >> 1) & 3)) << 4));
-          ok = wait_warp_or_abort(ptx::smem_u32(&bar_slot_empty[slot]), ((it / C::kSlots) & 1) ^ 1u, abort_ptr,
-                                  p.timeout_ns, kRolePagedQuery);
-          if (!ok) break;
-          uint8_t* to = generic + (sSlots - smem_base) + slot * C::kTileBytes + tid * 128;
-#pragma unroll
-          for (int i = 0; i < HD / 16; ++i) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t h[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              h[2 * e] = e4m3x2_to_f16x2(w[e] & 0xffffu);
-              h[2 * e + 1] = e4m3x2_to_f16x2(w[e] >> 16);
-            }
-            if (clear) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) h[e] = 0u;
-            }
-            uint8_t* chunk = to + (i >> 2) * C::kChunkBytes;
-            const int u = 2 * (i & 3);
-            *reinterpret_cast<uint4*>(chunk + ((u ^ (tid & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(chunk + (((u + 1) ^ (tid & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-          }
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_empty[tile]));
-          ptx::fence_proxy_async_smem();
-          ptx::mbar_arrive(ptx::smem_u32(&bar_slot_full[slot]));
-          if (j > job.j0 || kv > 0) continue;
-          // The query rows, behind the unit's first K tile: kLanes lanes a row, 16
-          // elements each. They come as bf16 to where they will stand as f16 (all
-          // at once: a loop of loads took 15000 cycles and more), and every thread
-          // converts what it asked for.
-          ok = wait_warp_or_abort(ptx::smem_u32(&bar_q_empty), (n & 1) ^ 1u, abort_ptr, kUnitWaits * p.timeout_ns,
-                                  kRolePagedQuery);
-          if (!ok) break;
-          constexpr int kLanes = HD / 16, kStep = 128 / kLanes;
-          const int part = tid % kLanes, rows = job.rows <= 128 ? 128 : 256, u = 2 * (part & 3);
-          // Row r of tile r / 128; 16-byte units 2 part and 2 part + 1, swizzled within their 128-byte chunk.
-          auto place = [&](int r) {
-            return static_cast<uint32_t>((r >> 7) * C::kTileBytes + (part >> 2) * C::kChunkBytes + (r & 127) * 128);
-          };
-          int ti = (tid / kLanes) / job.heads, hi = tid / kLanes - ti * job.heads;
-#pragma unroll 1
-          for (int r = tid / kLanes; r < job.rows; r += kStep) {
-            const __nv_bfloat16* src = p.q + (job.token + ti) * p.q_t + (job.head + hi) * p.q_h + 16 * part;
-            const uint32_t dst = sQ + place(r);
-            ptx::cp_async16(dst + ((u ^ (r & 7)) << 4), src);
-            ptx::cp_async16(dst + (((u + 1) ^ (r & 7)) << 4), src + 8);
-            for (hi += kStep; hi >= job.heads; hi -= job.heads) ++ti;
-          }
-          ptx::cp_async_wait();
-#pragma unroll 1
-          for (int r = tid / kLanes; r < rows; r += kStep) {
-            uint8_t* to0 = generic + place(r) + ((u ^ (r & 7)) << 4);
-            uint8_t* to1 = generic + place(r) + (((u + 1) ^ (r & 7)) << 4);
-            uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
-            if (r < job.rows) {
-              v0 = *reinterpret_cast<const uint4*>(to0);
-              v1 = *reinterpret_cast<const uint4*>(to1);
-            }
-            float x[16], amax = 0.f;
-            unpack8(v0, x);
-            unpack8(v1, x + 8);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              if (fabsf(x[e]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(x[e]));
-              else x[e] = __uint_as_float(0x7fffffffu);
-            }
-#pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const int up = amax > 0.f ? max(-120, min(120, 134 - static_cast<int>(__float_as_uint(amax) >> 23))) : 0;
-            const float scale = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-            uint32_t h[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] = ptx::pack_f16x2(x[2 * e] * scale, x[2 * e + 1] * scale);
-            *reinterpret_cast<uint4*>(to0) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(to1) = make_uint4(h[4], h[5], h[6], h[7]);
-            if (part == 0) row_scale[n & 1][r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-          }
-          ptx::fence_proxy_async_smem();
-          ptx::mbar_arrive(ptx::smem_u32(&bar_q_full));
+        for (int r = tid / kLanes; r < job.rows; r += kStep) {
+          const __nv_bfloat16* src = p.q + (job.token + ti) * p.q_t + (job.head + hi) * p.q_h + 16 * part;
+          ptx::cp_async16(sQ + place(r), src);
+          ptx::cp_async16(sQ + place(r) + C::kTileBytes, src + 8);
+          for (hi += kStep; hi >= job.heads; hi -= job.heads) ++ti;
         }
+        ptx::cp_async_wait();
+#pragma unroll 2
+        for (int r = tid / kLanes; r < rows; r += kStep) {
+          uint4* to0 = reinterpret_cast<uint4*>(generic + place(r));
+          uint4* to1 = reinterpret_cast<uint4*>(generic + place(r) + C::kTileBytes);
+          float x[16], amax = 0.f;
+          unpack8(r < job.rows ? *to0 : make_uint4(0u, 0u, 0u, 0u), x);
+          unpack8(r < job.rows ? *to1 : make_uint4(0u, 0u, 0u, 0u), x + 8);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if (fabsf(x[e]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(x[e]));
+            else x[e] = __uint_as_float(0x7fffffffu);
+          }
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const int up = amax > 0.f ? max(-120, min(120, 134 - static_cast<int>(__float_as_uint(amax) >> 23))) : 0;
+          const float scale = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+          uint32_t hi4[4], lo4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            hi4[e] = lo4[e] = 0;
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const float a = x[4 * e + 2 * f] * scale, b = x[4 * e + 2 * f + 1] * scale;
+              const uint32_t h = to_e4m3x2(a, b);
+              const float2 back = from_e4m3x2(h);
+              hi4[e] |= h << (16 * f);
+              lo4[e] |= to_e4m3x2(a - back.x, b - back.y) << (16 * f);
+            }
+          }
+          *to0 = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+          *to1 = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+          if (part == 0) row_scale[n & 1][r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(ptx::smem_u32(&bar_q_full));
+      // The V tiles: a thread has a key's row.
+      for (int j = job.j0; j < job.j1 && ok; ++j, ++pair) {
+        const bool clear = j * 128 + tid >= job.n_keys;   // (rows behind the unit's keys may hold anything)
+        const int it = 2 * pair + 1, tile = it % C::kTiles, slot = pair % C::kSlots;
+        ok = wait_warp_or_abort(ptx::smem_u32(&bar_full[tile]), (it / C::kTiles) & 1, abort_ptr, p.timeout_ns,
+                                kRolePagedQuery);
+        if (!ok) break;
+        uint4 v[HD / 16];
+        const uint8_t* from = generic + (sTiles - smem_base) + tile * C::kTileBytes + tid * HD;
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i)
+          v[i] = *reinterpret_cast<const uint4*>(from + ((i ^ (HD == 128 ? tid & 7 : (tid >> 1) & 3)) << 4));
+        ok = wait_warp_or_abort(ptx::smem_u32(&bar_slot_empty[slot]), ((pair / C::kSlots) & 1) ^ 1u, abort_ptr,
+                                p.timeout_ns, kRolePagedQuery);
+        if (!ok) break;
+        uint8_t* to = generic + (sSlots - smem_base) + slot * C::kSlotBytes + tid * 128;
+#pragma unroll
+        for (int i = 0; i < HD / 16; ++i) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h[2 * e] = e4m3x2_to_f16x2(w[e] & 0xffffu);
+            h[2 * e + 1] = e4m3x2_to_f16x2(w[e] >> 16);
+          }
+          if (clear) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = 0u;
+          }
+          uint8_t* chunk = to + (i >> 2) * C::kChunkBytes;
+          const int u = 2 * (i & 3);
+          *reinterpret_cast<uint4*>(chunk + ((u ^ (tid & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(chunk + (((u + 1) ^ (tid & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_empty[tile]));
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(ptx::smem_u32(&bar_slot_full[slot]));
       }
     }
     __syncwarp();

@@ -65,12 +65,6 @@ def check(cache, new, H, d, causal=True, scale=None, seed=0, q=None, T_extra=0, 
     return o, lse
 
 
-def small(cache, k=2.0 ** -5):
-    """Scores of ordinary size: codes of about 60 times scales of about 2^-7."""
-    cache.ks.mul_(2.0)
-    return cache
-
-
 @pytest.mark.parametrize("by_token", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
@@ -90,6 +84,20 @@ def test_pages_and_heads(H, H_kv, page, d, by_token):
 def test_new_tokens(new, lens, d, causal):
     """Drafts, prompts, pieces of them; rows that see nothing; sequences without new tokens or keys."""
     check(Cache(sum(new), lens, 2, 32, d), new, 8, d, causal, seed=sum(lens))
+
+
+@pytest.mark.parametrize("by_token", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_pieces_of_prompts(page, d, by_token):
+    """Long and short pieces beside single tokens; with the last, blocks of unequal scale."""
+    new, lens = [200, 1, 33, 128, 7], [900, 300, 33, 140, 2000]
+    cache = Cache(page + d, lens, 2, page, d, by_token)
+    check(cache, new, 8, d, seed=page)
+    g = torch.Generator().manual_seed(page)
+    for s in (cache.ks, cache.vs):
+        s.mul_(torch.exp2(torch.rand(s.shape, generator=g) * 6 - 5).cuda())
+    check(cache, new, 8, d, seed=page, scale=-0.11)
 
 
 @pytest.mark.parametrize("G,n", [(1, 1), (16, 1), (17, 1), (64, 1), (65, 1), (128, 1), (100, 3), (5, 13), (3, 22), (33, 2), (1, 200)])
