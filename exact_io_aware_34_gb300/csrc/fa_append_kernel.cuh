@@ -11,13 +11,15 @@
 // of two is exact but for values that become subnormal. Values that are not
 // finite are stored as NaN and have no part in the scale.
 //
-// Work. The rows that one call adds to one page, of one head, of K or of V, are
-// a CTA's work: their largest value decides about all of them. Lengths are
-// known to the device alone, so the grid has room for every way to cut T tokens
-// into pages: with T <= T / page + 2 B one place per token, of which those work
-// that begin a page or a sequence (a decode step: all of them); else sequence b
-// has the places from cu[b] / page + 2 b on, at least as many as it touches pages.
-// Behind them stand the CTAs that rotate queries.
+// Work. The rows that one call adds to one page, of one head, of K or of V,
+// belong together: their largest value decides about all of them. They are the
+// work of one warp, or, where many rows meet large pages, of page / 16 warps: 16 rows
+// a warp stay in registers between the maximum and the rounding (more are read
+// again). Lengths are known to the device alone, so the grid has room for every
+// way to cut T tokens into pages: with T <= T / page + 2 B one place per token, of
+// which those work that begin a page or a sequence (a decode step: all of them);
+// else sequence b has the places from cu[b] / page + 2 b on, at least as many as it
+// touches pages. Behind them stand the CTAs that rotate queries (fa_rope_kernel's rows).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -25,6 +27,14 @@
 #include "fa_rope_kernel.cuh"
 
 namespace fa {
+
+namespace ptx {
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+}  // namespace ptx
 
 enum : unsigned int { kRoleAppend = 29 };
 
@@ -39,11 +49,12 @@ struct AppendParams {
   const int* lens;                 // [B], with the new tokens
   const int* positions;            // [T] or null: the token's place in its sequence
   const double* inv_freq;          // [rot / 2]
-  RopeTensor q;                    // q.heads = 0: none
+  RopeRows q;                      // queries (q.x.heads = 0: none)
   int B, H_kv, T, d, num_pages, page, max_pages, rot, interleaved;
   int per_token;                   // places: 1 one per token, 0 by page
-  int places, q_tokens;            // q_tokens: tokens of a query CTA
-  int q_split;                     // query CTAs that share their tokens
+  int places;
+  int warps;                       // of a head: 1, 2, 4 or 8
+  int head_groups;                 // CTAs of a place, each with 8 / warps heads
   float factor;
 };
 
@@ -80,66 +91,173 @@ __device__ __forceinline__ float least_scale(float amax) {
   return __uint_as_float(static_cast<uint32_t>(max(e, -100) + 127) << 23);
 }
 
-template <int kThreads, int kItems>
-__global__ void __launch_bounds__(kThreads) fa_append_kernel(const AppendParams p) {
-  __shared__ __align__(16) float2 cs[kRopeTokens * 64];
-  __shared__ int found[4], at[kRopeTokens], skip[kRopeTokens];
-  __shared__ float warp_max[kThreads / 32];
-  const int half = p.rot / 2;
-  const int kv_ctas = p.places * p.H_kv * 2;
+constexpr int kAppendThreads = 256;
+
+// Up to 16 rows of a head as kItems items of 16 columns a lane, rotated. Lane l's
+// item k is item l % items of row (l / items) + k * (32 / items), items = HD / 16.
+template <int HD>
+struct AppendRows {
+  static constexpr int kPerRow = HD / 16, kRowStep = 32 / kPerRow, kItems = 16 / kRowStep;
+  float x[kItems][16];
+  float amax;                      // of the finite values
+
+  __device__ __forceinline__ void load(const AppendParams& p, const uint64_t* turns_at, int which, int head, int t0, int p0,
+                                       int rows) {
+    const int lane = threadIdx.x & 31, row0 = lane / kPerRow, i = lane % kPerRow;
+    const bool inter = p.interleaved != 0, turns = which == 0 && i < p.rot / 16;
+    const RopeItem it = rope_item(i, which == 0 ? p.rot : 0, inter);
+    const __nv_bfloat16* in = p.kv[which] + t0 * p.in_t[which] + head * p.in_h[which];
+    uint4 v[kItems][2];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int r = row0 + k * kRowStep;
+      v[k][0] = v[k][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows) {
+        v[k][0] = *reinterpret_cast<const uint4*>(in + r * p.in_t[which] + it.c0);
+        v[k][1] = *reinterpret_cast<const uint4*>(in + r * p.in_t[which] + it.c1);
+      }
+    }
+    amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int r = row0 + k * kRowStep;
+      if (k > 0 && k * kRowStep >= rows) {     // (no lane has a row here)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[k][e] = 0.f;
+        continue;
+      }
+      unpack8(v[k][0], x[k]);
+      unpack8(v[k][1], x[k] + 8);
+      if (turns && r < rows) {
+        const int position = p.positions ? p.positions[t0 + r] : p0 + r;
+        float2 t[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = turn(position, turns_at[8 * i + e], p.factor);
+        rope_turn(x[k], t, inter);
+      }
+      float m = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) m = ptx::max_nan(m, fabsf(x[k][e]));
+      if (!(m <= 3.402823466e38f)) {
+        m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (fabsf(x[k][e]) <= 3.402823466e38f) m = fmaxf(m, fabsf(x[k][e]));
+          else x[k][e] = __uint_as_float(0x7fffffffu);      // NaN
+        }
+      }
+      amax = fmaxf(amax, m);
+    }
+  }
+
+  // To rows row0 .. of a page at `out`.
+  __device__ __forceinline__ void store(const AppendParams& p, int which, uint8_t* out, int rows, float scale) const {
+    const int lane = threadIdx.x & 31, row0 = lane / kPerRow, i = lane % kPerRow;
+    const RopeItem it = rope_item(i, which == 0 ? p.rot : 0, p.interleaved != 0);
+    // (A scale that other code left here need not be a power of two.)
+    const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0u;
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int r = row0 + k * kRowStep;
+      if (r >= rows) break;
+      uint32_t c[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float y[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) y[f] = exact ? x[k][4 * e + f] * inv : x[k][4 * e + f] / scale;
+        c[e] = to_e4m3x2(y[0], y[1]) | to_e4m3x2(y[2], y[3]) << 16;
+      }
+      uint8_t* dst = out + r * p.c_row[which];
+      *reinterpret_cast<uint2*>(dst + it.c0) = make_uint2(c[0], c[1]);
+      *reinterpret_cast<uint2*>(dst + it.c1) = make_uint2(c[2], c[3]);
+    }
+  }
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendParams p) {
+  constexpr int kThreads = kAppendThreads;
+  __shared__ __align__(16) float2 cs[kRopeAngles];
+  __shared__ int found[4], at[kRopeMaxTokens], skip[kRopeMaxTokens];
+  __shared__ float warp_max[8];
+  ptx::grid_wait();
+  ptx::grid_next();
+  const int half = p.rot / 2, kv_ctas = p.places * p.head_groups * 2;
 
   if (static_cast<int>(blockIdx.x) >= kv_ctas) {
     // ------------------------------------------------------------ queries
-    const int w0 = static_cast<int>(blockIdx.x) - kv_ctas, part = w0 % p.q_split;
-    const int t0 = w0 / p.q_split * p.q_tokens, n = min(p.q_tokens, p.T - t0);
-    if (threadIdx.x < kRopeTokens) skip[threadIdx.x] = 1;
-    __syncthreads();
-    for (int b = threadIdx.x; b < p.B; b += kThreads) {
-      const int c0 = p.cu[b], c1 = p.cu[b + 1];
-      if (c0 >= t0 + n || c1 <= t0) continue;
-      const int len = p.lens[b];
-      if (!append_fits(p, c0, c1, len)) continue;
-      for (int t = max(c0, t0); t < min(c1, t0 + n); ++t) {
-        at[t - t0] = p.positions ? p.positions[t] : len - (c1 - t);
-        skip[t - t0] = 0;
+    const int t0 = (static_cast<int>(blockIdx.x) - kv_ctas) * p.q.tokens, n = min(p.q.tokens, p.T - t0);
+    rope_rows<kThreads>(p.q, t0, n, cs, skip, [&] {
+      if (threadIdx.x < kRopeMaxTokens) skip[threadIdx.x] = 1;
+      __syncthreads();
+      for (int b = threadIdx.x; b < p.B; b += kThreads) {
+        const int c0 = p.cu[b], c1 = p.cu[b + 1];
+        if (c0 >= t0 + n || c1 <= t0) continue;
+        const int len = p.lens[b];
+        if (!append_fits(p, c0, c1, len)) continue;
+        for (int t = max(c0, t0); t < min(c1, t0 + n); ++t) {
+          at[t - t0] = p.positions ? p.positions[t] : len - (c1 - t);
+          skip[t - t0] = 0;
+        }
       }
-    }
-    __syncthreads();
-    for (int w = threadIdx.x; w < n * half; w += kThreads) {
-      const int k = w / half, j = w - k * half;
-      if (!skip[k]) cs[w] = turn(at[k], turns_of(p.inv_freq[j]), p.factor);
-    }
-    __syncthreads();
-    rope_rows(p.q, t0, n, p.d, p.rot, p.interleaved != 0, cs, skip, part * kThreads + threadIdx.x,
-              p.q_split * kThreads);
+      __syncthreads();
+      for (int w = threadIdx.x; w < n * half; w += kThreads) {
+        const int k = w / half, j = w - k * half;
+        if (!skip[k]) cs[w] = turn(at[k], turns_of(p.inv_freq[j]), p.factor);
+      }
+      __syncthreads();
+    });
     return;
   }
 
   // -------------------------------------------------------------- keys, values
   const int which = static_cast<int>(blockIdx.x) & 1, u = static_cast<int>(blockIdx.x) >> 1;
-  const int place = u / p.H_kv, head = u - place * p.H_kv;
-  if (threadIdx.x == 0) found[0] = -1;
-  __syncthreads();
+  const int place = p.head_groups == 1 ? u : u / p.head_groups, group = u - place * p.head_groups;
   const bool check = blockIdx.x == 0;
-  for (int b = threadIdx.x; b < p.B; b += kThreads) {
-    const int c0 = p.cu[b], c1 = p.cu[b + 1];
-    const bool mine = p.per_token ? c0 <= place && place < c1
-                                  : c0 / p.page + 2 * b <= place && place < c1 / p.page + 2 * b + 2;
-    if (!mine && !check) continue;
-    const int len = p.lens[b];
-    if (!append_fits(p, c0, c1, len)) {
-      append_bad(b);
-    } else if (mine) {
-      found[0] = b;
-      found[1] = c0;
-      found[2] = c1;
-      found[3] = len;
+  // The frequencies, once for all heads.
+  uint64_t* turns = reinterpret_cast<uint64_t*>(cs);
+  if (which == 0 && half > 0) {
+    if (threadIdx.x < half) turns[threadIdx.x] = turns_of(p.inv_freq[threadIdx.x]);
+    __syncthreads();
+  }
+  // A decode step's token t is sequence t's; else all threads look for the place's sequence.
+  int b = -1, c0 = 0, c1 = 0, len = 0;
+  if (p.per_token && place < p.B) {
+    c0 = p.cu[place];
+    c1 = p.cu[place + 1];
+    if (c0 == place && c1 == place + 1) {
+      len = p.lens[place];
+      if (append_fits(p, c0, c1, len)) b = place;
     }
   }
-  __syncthreads();
-  const int b = found[0];
+  if (b < 0 || check) {            // (the same in all threads)
+    if (threadIdx.x == 0) found[0] = -1;
+    __syncthreads();
+    for (int s = threadIdx.x; s < p.B; s += kThreads) {
+      const int s0 = p.cu[s], s1 = p.cu[s + 1];
+      const bool mine = p.per_token ? s0 <= place && place < s1
+                                    : s0 / p.page + 2 * s <= place && place < s1 / p.page + 2 * s + 2;
+      if (!mine && !check) continue;
+      const int n = p.lens[s];
+      if (!append_fits(p, s0, s1, n)) {
+        append_bad(s);
+      } else if (mine) {
+        found[0] = s;
+        found[1] = s0;
+        found[2] = s1;
+        found[3] = n;
+      }
+    }
+    __syncthreads();
+    b = found[0];
+    c0 = found[1];
+    c1 = found[2];
+    len = found[3];
+  }
   if (b < 0) return;
-  const int c0 = found[1], len = found[3], before = len - (found[2] - c0);
+  const int before = len - (c1 - c0);
   int p0, p1;                      // places [p0, p1) of the sequence, all in one page
   if (p.per_token) {
     p0 = before + (place - c0);
@@ -152,72 +270,48 @@ __global__ void __launch_bounds__(kThreads) fa_append_kernel(const AppendParams 
     if (p0 >= p1) return;
   }
   const int id = p.table[static_cast<long long>(b) * p.max_pages + p0 / p.page];
+  // Warp `sub` of the head's takes every p.warps-th block of 16 rows.
+  const int warp = threadIdx.x >> 5, sub = warp & (p.warps - 1), head = group * (8 / p.warps) + warp / p.warps;
+  const bool live = head < p.H_kv;
+  const int row0 = p0 % p.page, rows = p1 - p0, t0 = c0 + (p0 - before);
+  AppendRows<HD> x;
+  x.amax = 0.f;
+  float amax = 0.f;
+  if (live) {
+#pragma unroll 1
+    for (int r = 16 * sub; r < rows; r += 16 * p.warps) {
+      x.load(p, turns, which, head, t0 + r, p0 + r, min(16, rows - r));
+      amax = fmaxf(amax, x.amax);
+    }
+  }
   if (id < 0 || id >= p.num_pages) {
     if (threadIdx.x == 0) append_bad(b);
     return;
   }
-  const int row0 = p0 % p.page, rows = p1 - p0, t0 = c0 + (p0 - before);
   float* scale_at = p.scale[which] + static_cast<long long>(id) * p.H_kv + head;
-  const float old = row0 > 0 ? *scale_at : 0.f;
-  const bool turns = which == 0 && half > 0;
-  const int items = p.d / 16;
-  const __nv_bfloat16* in = p.kv[which] + t0 * p.in_t[which] + head * p.in_h[which];
-  uint8_t* out = p.cache[which] + id * p.c_page[which] + head * p.c_head[which];
-
-  float x[kItems][16];
-  float amax = 0.f;
-#pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    const int w = threadIdx.x + k * kThreads, r = w / items, i = w - r * items;
-    if (r >= rows) break;
-    const RopeItem it = rope_item(i, which == 0 ? p.rot : 0, p.interleaved != 0);
-    unpack8(*reinterpret_cast<const uint4*>(in + r * p.in_t[which] + it.c0), x[k]);
-    unpack8(*reinterpret_cast<const uint4*>(in + r * p.in_t[which] + it.c1), x[k] + 8);
-    if (turns && i < p.rot / 16) {
-      const int position = p.positions ? p.positions[t0 + r] : p0 + r;
-      float2 t[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] = turn(position, turns_of(p.inv_freq[8 * i + e]), p.factor);
-      rope_turn(x[k], t, p.interleaved != 0);
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if (fabsf(x[k][e]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(x[k][e]));
-      else x[k][e] = __uint_as_float(0x7fffffffu);      // NaN
-    }
-  }
+  const float old = live && row0 > 0 ? *scale_at : 0.f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
-  __syncthreads();                 // (the old scale has been read, too)
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, warp_max[w]);
+  __syncwarp();                    // (every lane has read the old scale)
+  if (p.warps > 1) {
+    if ((threadIdx.x & 31) == 0) warp_max[warp] = amax;
+    __syncthreads();
+    for (int w = 0; w < p.warps; ++w) amax = fmaxf(amax, warp_max[warp - sub + w]);
+  }
+  if (!live) return;
   const float scale = fmaxf(least_scale(amax), old);
-  if (threadIdx.x == 0) *scale_at = scale;
-  // (A scale that other code left here need not be a power of two.)
-  const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0u;
-  const float inv = 1.f / scale;
-#pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    const int w = threadIdx.x + k * kThreads, r = w / items, i = w - r * items;
-    if (r >= rows) break;
-    const RopeItem it = rope_item(i, which == 0 ? p.rot : 0, p.interleaved != 0);
-    uint32_t c[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float y[4];
-#pragma unroll
-      for (int f = 0; f < 4; ++f) y[f] = exact ? x[k][4 * e + f] * inv : x[k][4 * e + f] / scale;
-      c[e] = to_e4m3x2(y[0], y[1]) | to_e4m3x2(y[2], y[3]) << 16;
-    }
-    uint8_t* dst = out + (row0 + r) * p.c_row[which];
-    *reinterpret_cast<uint2*>(dst + it.c0) = make_uint2(c[0], c[1]);
-    *reinterpret_cast<uint2*>(dst + it.c1) = make_uint2(c[2], c[3]);
+  if (sub == 0 && (threadIdx.x & 31) == 0) *scale_at = scale;
+  uint8_t* out = p.cache[which] + id * p.c_page[which] + head * p.c_head[which];
+#pragma unroll 1
+  for (int r = 16 * sub; r < rows; r += 16 * p.warps) {
+    if (rows > 16 * p.warps) x.load(p, turns, which, head, t0 + r, p0 + r, min(16, rows - r));   // (more than one block: again)
+    x.store(p, which, out + (row0 + r) * p.c_row[which], min(16, rows - r), scale);
   }
   if (row0 > 0 && scale != old) {
     const float ratio = old / scale;
-    for (int w = threadIdx.x; w < row0 * items; w += kThreads) {
-      const int r = w / items, i = w - r * items;
+    constexpr int kPerRow = HD / 16;
+    for (int w = sub * 32 + (threadIdx.x & 31); w < row0 * kPerRow; w += 32 * p.warps) {
+      const int r = w / kPerRow, i = w % kPerRow;
       uint4* at16 = reinterpret_cast<uint4*>(out + r * p.c_row[which] + 16 * i);
       uint4 v = *at16;
       uint32_t* c = reinterpret_cast<uint32_t*>(&v);

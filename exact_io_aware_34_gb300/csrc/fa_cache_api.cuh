@@ -86,6 +86,40 @@ fa::RopeTensor rope_tensor(const Rows& in, const Rows& out) {
                         static_cast<__nv_bfloat16*>(const_cast<void*>(out.p)), in.st, in.sh, out.st, out.sh, in.heads};
 }
 
+// A CTA's tokens: about 40 KB of rows, as many angles as fit, and no fewer CTAs than four per SM where T allows.
+fa::RopeRows rope_rows(const fa::RopeTensor& x, const fa::RopeTensor& y, int T, int d, int rot, int interleaved) {
+  const int heads = x.heads + y.heads;
+  fa::RopeRows r;
+  r.x = x;
+  r.y = y;
+  r.T = T;
+  r.d = d;
+  r.rot = rot;
+  r.interleaved = interleaved;
+  int n = 40960 / (heads * d * 2);
+  n = std::min(n, 2 * fa::kRopeAngles / rot);
+  n = std::min(n, T / (4 * device_sm_count()));
+  r.tokens = heads > 4096 ? 1 : std::max(1, std::min(n, fa::kRopeMaxTokens));
+  r.inv_heads = r.tokens == 1 ? 0u : static_cast<unsigned>(((1ull << 32) + heads - 1) / heads);
+  return r;
+}
+
+// One launch on `stream`, as a programmatic dependent of what came before (every
+// kernel here waits for that on the device before it touches memory).
+cudaError_t launch_dependent(const void* kernel, dim3 grid, int threads, int smem, cudaStream_t stream, void** args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
 fa_status_t rope_impl(const void* X, void* X_out, int heads, const void* Y, void* Y_out, int heads_y,
                       const int* positions, const double* inv_freq, int T, int d, int rot,
                       const fa_strides_t* strides, int interleaved, int transpose, float factor, cudaStream_t stream) {
@@ -116,19 +150,15 @@ fa_status_t rope_impl(const void* X, void* X_out, int heads, const void* Y, void
   if (n == 2 && rows_overlap(out[0], out[1])) return FA_ERR_INVALID_ARG;
 
   fa::RopeParams p;
-  p.x = rope_tensor(in[0], out[0]);
-  p.y = n == 2 ? rope_tensor(in[1], out[1]) : fa::RopeTensor{};
+  p.r = rope_rows(rope_tensor(in[0], out[0]), n == 2 ? rope_tensor(in[1], out[1]) : fa::RopeTensor{}, T, d, rot, interleaved);
   p.positions = positions;
   p.inv_freq = inv_freq;
-  p.T = T;
-  p.d = d;
-  p.rot = rot;
-  p.interleaved = interleaved;
   p.transpose = transpose;
   p.factor = factor;
-  p.tokens = T >= 16 * device_sm_count() ? fa::kRopeTokens : 1;
-  fa::fa_rope_kernel<<<dim3(static_cast<unsigned>((T + p.tokens - 1) / p.tokens)), fa::kRopeThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  void* args[1] = {&p};
+  const cudaError_t e = launch_dependent(reinterpret_cast<const void*>(&fa::fa_rope_kernel),
+                                         dim3(static_cast<unsigned>((T + p.r.tokens - 1) / p.r.tokens)),
+                                         fa::kRopeThreads, 0, stream, args);
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
@@ -216,7 +246,8 @@ fa_status_t append_impl(const void* K, const void* V, const int* cu_new, void* K
   p.lens = seq_lens;
   p.positions = positions;
   p.inv_freq = inv_freq;
-  p.q = Q ? rope_tensor(q, qo) : fa::RopeTensor{};
+  p.q = fa::RopeRows{};
+  if (Q) p.q = rope_rows(rope_tensor(q, qo), fa::RopeTensor{}, T, d, rot, interleaved);
   p.B = B;
   p.H_kv = H_kv;
   p.T = T;
@@ -230,18 +261,14 @@ fa_status_t append_impl(const void* K, const void* V, const int* cu_new, void* K
   const long long by_page = T / page + 2LL * B;
   p.per_token = T <= by_page;
   p.places = static_cast<int>(std::min<long long>(T, by_page));
-  p.q_tokens = T >= 16 * device_sm_count() ? fa::kRopeTokens : 1;
-  p.q_split = 1;
-  const long long ctas = 2LL * p.places * H_kv +
-                         (Q ? static_cast<long long>((T + p.q_tokens - 1) / p.q_tokens) * p.q_split : 0);
+  p.warps = p.per_token ? 1 : page / 16;
+  p.head_groups = (H_kv * p.warps + 7) / 8;
+  const long long ctas = 2LL * p.places * p.head_groups + (Q ? (T + p.q.tokens - 1) / p.q.tokens : 0);
   if (ctas >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
-  const unsigned grid = static_cast<unsigned>(ctas);
-  const int items = page * d / 16;
-  if (items <= 128) fa::fa_append_kernel<128, 1><<<grid, 128, 0, stream>>>(p);
-  else if (items <= 256) fa::fa_append_kernel<128, 2><<<grid, 128, 0, stream>>>(p);
-  else if (items <= 512) fa::fa_append_kernel<128, 4><<<grid, 128, 0, stream>>>(p);
-  else fa::fa_append_kernel<256, 4><<<grid, 256, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  void* args[1] = {&p};
+  const cudaError_t e = launch_dependent(
+      d == 64 ? reinterpret_cast<const void*>(&fa::fa_append_kernel<64>) : reinterpret_cast<const void*>(&fa::fa_append_kernel<128>),
+      dim3(static_cast<unsigned>(ctas)), fa::kAppendThreads, 0, stream, args);
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 
@@ -293,13 +320,14 @@ fa::PagedShape paged_shape(int B, int H, int H_kv, int T_q, int num_pages, int p
   s.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
   s.max_pages = max_pages;
   s.causal = causal;
+  s.cost = N > 16 ? fa::kWideCost : fa::kPagedCost;
   return s;
 }
 
 // Places of the line at most (0: more than can be counted in 32 bits on the device), and the CTAs that share them.
 long long paged_places(const fa::PagedShape& s) {
   const double units = (static_cast<double>(s.T_q / s.tp) + s.B) * s.H_kv * s.ht;
-  const double places = units * (((static_cast<long long>(s.max_pages) << s.page_shift) + 127) / 128 + fa::kPagedCost);
+  const double places = units * (((static_cast<long long>(s.max_pages) << s.page_shift) + 127) / 128 + s.cost);
   return places < 2147418112.0 ? static_cast<long long>(places) : 0;
 }
 int paged_ctas(const fa::PagedShape& s, int N) {
@@ -362,26 +390,12 @@ fa_status_t paged_launch(const Pages& kc, const Pages& vc, fa::PagedParams& p, c
   if (!regs_ok[dev]) return FA_ERR_UNSUPPORTED;
   CUtensorMap mk, mv;
   if (!make_page_map(&mk, kc) || !make_page_map(&mv, vc)) return cuda_fail(cudaErrorInvalidValue);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.s.ctas));
-  cfg.blockDim = dim3(static_cast<unsigned>(k.threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(k.smem);
-  cfg.stream = stream;
-  // Both as programmatic dependent launches: they wait on the device for what
-  // came before, the merge for the main grid's end.
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   void* args[3] = {&mk, &mv, &p};
-  e = cudaLaunchKernelExC(&cfg, k.main, args);
+  e = launch_dependent(k.main, dim3(static_cast<unsigned>(p.s.ctas)), k.threads, k.smem, stream, args);
   if (e != cudaSuccess) return cuda_fail(e);
-  cfg.gridDim = dim3(static_cast<unsigned>(p.s.ctas), static_cast<unsigned>((N + 15) / 16));
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
   void* merge_args[1] = {&p};
-  e = cudaLaunchKernelExC(&cfg, k.merge, merge_args);
+  e = launch_dependent(k.merge, dim3(static_cast<unsigned>(p.s.ctas), static_cast<unsigned>((N + 15) / 16)), 128, 0, stream,
+                       merge_args);
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 

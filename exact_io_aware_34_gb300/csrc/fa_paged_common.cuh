@@ -56,20 +56,10 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-// Programmatic dependent launches: what follows waits until the grids before
-// have ended and their writes are visible; the next grid may be scheduled.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // Maximum over the warp; NaN if any lane has one.
 __device__ __forceinline__ float warp_max_nan(float x) {
   float y;
   asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
 __device__ __forceinline__ float lg2_approx(float x) {
@@ -94,8 +84,9 @@ __device__ __forceinline__ bool softmax_any(bool p) {
 
 enum : unsigned int { kRolePagedProducer = 30, kRolePagedMma = 31, kRolePagedSoftmax = 32, kRolePagedWalk = 33, kRolePagedQuery = 34 };
 
-// Places of a unit in the line beside its tiles.
-constexpr int kPagedCost = 2;
+// Places of a unit in the line beside its tiles: what it costs beyond them.
+constexpr int kPagedCost = 2;            // fa_paged_kernel (64 answers: 1 32.7 us, 2 29.7, 3 30.1)
+constexpr int kWideCost = 12;           // fa_paged_wide_kernel: its query rows, the first products, its results (6: 171 us, 12: 166, 18: 168)
 constexpr float kPagedJump = 20.f;   // the reference moves when a tile's maximum is 2^20 above it
 constexpr float kPagedTop = 8.f;     // a tile's largest weight is written as 2^8 (e4m3 ends at 448)
 
@@ -104,6 +95,7 @@ struct PagedShape {
   int hp, ht, tp;          // heads and tokens of a row tile, head tiles of a group
   int num_pages, page_shift, max_pages;
   int causal, ctas;
+  int cost;                // kPagedCost or kWideCost
 };
 
 struct PagedSplit {        // a unit that several CTAs share, noted by the one with its beginning
@@ -187,9 +179,9 @@ struct PagedSeq {
     const int k = i - first;
     if (k <= 0) return 0;
     const int last = (n_kv + 127) >> 7;
-    if (!s.causal || (k == groups - first && k == 1)) return k * (kPagedCost + last);
+    if (!s.causal || (k == groups - first && k == 1)) return k * (s.cost + last);
     const int ramp = i == groups ? k - 1 : k;          // (the last tile may be short)
-    return k * kPagedCost + (i == groups ? last : 0) +
+    return k * s.cost + (i == groups ? last : 0) +
            static_cast<int>(floor_sum128(static_cast<unsigned>(ramp), static_cast<unsigned>(s.tp),
                                          static_cast<unsigned>(n_kv - n_q + (first + 1) * s.tp + 127)));
   }
@@ -374,7 +366,7 @@ struct PagedWalk {
     PagedJob job{};
     job.b = -1;
     while (more && x < line.end && job.b < 0) {
-      const int keys = q.keys(sh, i), tiles = (keys + 127) >> 7, places = kPagedCost + tiles;
+      const int keys = q.keys(sh, i), tiles = (keys + 127) >> 7, places = sh.cost + tiles;
       // (Only lengths that change under the call can lead out of the unit. It ends then, with undefined results.)
       if (keys <= 0 || from >= places) {
         more = false;
@@ -383,8 +375,8 @@ struct PagedWalk {
       const int to = min(places, from + (line.end - x));
       *end = x - from + places - 1;
       x += to - from;
-      job.j0 = max(0, from - kPagedCost);
-      job.j1 = max(0, to - kPagedCost);
+      job.j0 = max(0, from - sh.cost);
+      job.j1 = max(0, to - sh.cost);
       if (job.j1 > job.j0) {
         const int kvh = sh.ht == 1 ? u : u / sh.ht, h0 = (u - kvh * sh.ht) * sh.hp, t0 = i * sh.tp;
         job.b = b;

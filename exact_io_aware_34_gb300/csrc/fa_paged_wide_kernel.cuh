@@ -23,7 +23,7 @@
 //
 // Per CTA (512 threads, one per SM): warps 0-7 softmax and epilogue, warp 8
 // walks the line and loads pages, warp 9 issues products, warps 10 and 11 idle,
-// warps 12-15 convert query rows and V tiles.
+// warps 12-15 convert V tiles.
 #pragma once
 
 #include "fa_paged_common.cuh"
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
     fa_paged_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const PagedParams p) {
   using C = PagedWideCfg<HD, NG>;
-  constexpr int kJobs = kPagedJobs;
+  constexpr int kJobs = kPagedJobs, kPolls = 8;   // (polls: as in the forward kernel)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[C::kTiles];    // 8-bit tiles, K and V of a key tile in turn
   __shared__ __align__(8) uint64_t bar_empty[C::kTiles];
@@ -105,14 +105,13 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
   __shared__ __align__(8) uint64_t bar_p_half[2];          // weights of keys 0-63
   __shared__ __align__(8) uint64_t bar_p_full[2];
   __shared__ __align__(8) uint64_t bar_o_full[2];
-  __shared__ __align__(8) uint64_t bar_q_full;
-  __shared__ __align__(8) uint64_t bar_q_empty;
+  __shared__ __align__(8) uint64_t bar_q_full[2];
   __shared__ __align__(8) uint64_t bar_job_full[kJobs];
   __shared__ __align__(8) uint64_t bar_job_empty[kJobs];
   __shared__ __align__(8) uint64_t bar_drain;
   __shared__ __align__(16) PagedJob jobs[kJobs];
   __shared__ __align__(16) float page_scale[C::kScales][4][8];
-  __shared__ float row_scale[2][C::kRows];              // by unit (modulo 2)
+  __shared__ float row_scale[C::kRows];
   __shared__ PagedLine line;
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
@@ -134,6 +133,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(ptx::smem_u32(&bar_s_full[t]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bar_q_full[t]), 128);
       ptx::mbar_init(ptx::smem_u32(&bar_p_half[t]), 128);
       ptx::mbar_init(ptx::smem_u32(&bar_p_full[t]), 128);
       ptx::mbar_init(ptx::smem_u32(&bar_o_full[t]), 1);
@@ -142,8 +142,6 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&bar_job_full[t]), 1);
       ptx::mbar_init(ptx::smem_u32(&bar_job_empty[t]), 13);   // warps 0-7, 9 and 12-15
     }
-    ptx::mbar_init(ptx::smem_u32(&bar_q_full), 128);
-    ptx::mbar_init(ptx::smem_u32(&bar_q_empty), 1);
     ptx::mbar_init(ptx::smem_u32(&bar_drain), 1);
     abort_flag = 0;
     ptx::fence_mbar_init();
@@ -180,7 +178,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
     int g = 0, pair0 = 0, units = 0;         // key blocks of this tile so far; of the CTA before this unit; this tile's units
     for (int n = 0; ok; ++n) {
       const int ring = n & (kJobs - 1);
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_full[ring]), (n / kJobs) & 1, abort_ptr,
+      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[ring]), (n / kJobs) & 1, abort_ptr,
                               kUnitWaits * p.timeout_ns, kRolePagedSoftmax);
       if (!ok) break;
       const PagedJob job = jobs[ring];
@@ -188,25 +186,93 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[ring]));
       if (job.b < 0) break;
       const int blocks = job.j1 - job.j0;
+      const int inv_heads = (1 << 20) / job.heads + 1;   // (r * that) >> 20 = r / heads for r < 256
       if (t == 1 && job.rows <= 128) {       // no rows in this tile: it is not computed
         pair0 += blocks;
         continue;
       }
-      const int ti = row / job.heads;
+      // The warp's query rows, as hi and lo in the swizzled K-major layout: kLanes
+      // lanes a row, 16 elements each. (This tile's products of the unit before
+      // have all been waited for.)
+      {
+        constexpr int kLanes = HD / 16, kPass = 32 / kLanes, kPasses = 32 / kPass;
+        const int part = lane % kLanes, r0 = t * 128 + quarter * 32 + lane / kLanes;
+        // 16 bytes of hi, and kTileBytes behind them of lo; first they hold the bf16 (all
+        // rows are asked for at once, asynchronously, and every lane converts what it asked
+        // for; as short loops: unrolled, the code took longer to fetch than to run).
+        auto place = [&](int r) {
+          return static_cast<uint32_t>(2 * t * C::kTileBytes + (r & 127) * HD +
+                                       ((part ^ (HD == 128 ? r & 7 : (r >> 1) & 3)) << 4));
+        };
+#pragma unroll 1
+        for (int k = 0; k < kPasses; ++k) {
+          const int r = r0 + k * kPass;
+          if (r >= job.rows) break;
+          const int ti = (r * inv_heads) >> 20;
+          const __nv_bfloat16* src = p.q + (job.token + ti) * p.q_t + (job.head + r - ti * job.heads) * p.q_h + 16 * part;
+          ptx::cp_async16(sQ + place(r), src);
+          ptx::cp_async16(sQ + place(r) + C::kTileBytes, src + 8);
+        }
+        ptx::cp_async_wait();
+#pragma unroll 1
+        for (int k = 0; k < kPasses; ++k) {
+          const int r = r0 + k * kPass;
+          uint4* to0 = reinterpret_cast<uint4*>(generic + place(r));
+          uint4* to1 = reinterpret_cast<uint4*>(generic + place(r) + C::kTileBytes);
+          float x[16], amax = 0.f;
+          unpack8(r < job.rows ? *to0 : make_uint4(0u, 0u, 0u, 0u), x);
+          unpack8(r < job.rows ? *to1 : make_uint4(0u, 0u, 0u, 0u), x + 8);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) amax = ptx::max_nan(amax, fabsf(x[e]));
+          if (!(amax <= 3.402823466e38f)) {
+            amax = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              if (fabsf(x[e]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(x[e]));
+              else x[e] = __uint_as_float(0x7fffffffu);
+            }
+          }
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          const int up = amax > 0.f ? max(-120, min(120, 134 - static_cast<int>(__float_as_uint(amax) >> 23))) : 0;
+          const float scale = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+          uint32_t hi4[4], lo4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            hi4[e] = lo4[e] = 0;
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const float a = x[4 * e + 2 * f] * scale, b = x[4 * e + 2 * f + 1] * scale;
+              const uint32_t h = to_e4m3x2(a, b);
+              const float2 back = from_e4m3x2(h);
+              hi4[e] |= h << (16 * f);
+              lo4[e] |= to_e4m3x2(a - back.x, b - back.y) << (16 * f);
+            }
+          }
+          *to0 = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
+          *to1 = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+          if (part == 0) row_scale[r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        }
+      }
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(ptx::smem_u32(&bar_q_full[t]));
+      __syncwarp();
+      const float q_scale = row_scale[row];
+      __syncwarp();                          // (written again for the next unit)
+      const int ti = (row * inv_heads) >> 20;
       const bool live = row < job.rows;
       // Rows that hold no query take the last token's limit, so that they do not mask what the others need not.
       const int seen = sh.causal ? max(0, min(job.n_keys, job.lim0 + min(ti, (job.rows - 1) / job.heads))) : job.n_keys;
-      float m_use = -INFINITY, l = 0.f, q_scale = 0.f, v_ref = 0.f, v_unit = 1.f;   // V scale that O is in units of, and its log2
+      float m_use = -INFINITY, l = 0.f, v_ref = 0.f, v_unit = 1.f;   // V scale that O is in units of, and its log2
       for (int jj = 0; jj < blocks; ++jj, ++g) {
         const int j = job.j0 + jj, pair = pair0 + jj;
         // (V's slot is waited for because the scales come with it.)
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_slot_full[pair % C::kSlots]), (pair / C::kSlots) & 1, abort_ptr,
+        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_slot_full[pair % C::kSlots]), (pair / C::kSlots) & 1, abort_ptr,
                                 p.timeout_ns, kRolePagedSoftmax);
         if (ok)
-          ok = wait_warp_or_abort(ptx::smem_u32(&bar_s_full[t]), g & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax);
+          ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_s_full[t]), g & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax);
         if (!ok) break;
         ptx::tc_fence_after();
-        if (jj == 0) q_scale = row_scale[n & 1][row];
         const int valid = seen - j * 128;
         // Scores past a row's limit become -inf in TMEM, in a short loop (see fa_varlen_fwd_kernel).
         if (!__all_sync(0xffffffffu, valid >= 128)) {
@@ -352,7 +418,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
       }
       if (!ok) break;
       pair0 += blocks;
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_o_full[t]), units++ & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax);
+      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_o_full[t]), units++ & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax);
       if (!ok) break;
       ptx::tc_fence_after();
       const bool none = l == 0.f;
@@ -397,11 +463,11 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     bool ok = true;
     int pair0 = 0;                           // key tiles of the units before
-    int g[2] = {0, 0};                       // key tiles of each row tile so far
+    int g[2] = {0, 0}, units[2] = {0, 0};    // key tiles and units of each row tile so far
     // S_t = K tile `pair` times the row tile's hi and lo.
     auto k_wait = [&](int pair) {
       const int it = 2 * pair;
-      if (!wait_warp_or_abort(ptx::smem_u32(&bar_full[it % C::kTiles]), (it / C::kTiles) & 1, abort_ptr, p.timeout_ns,
+      if (!wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_full[it % C::kTiles]), (it / C::kTiles) & 1, abort_ptr, p.timeout_ns,
                               kRolePagedMma))
         return false;
       ptx::tc_fence_after();
@@ -422,19 +488,23 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
     };
     for (int n = 0; ok; ++n) {
       const int ring = n & (kJobs - 1);
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_full[ring]), (n / kJobs) & 1, abort_ptr,
+      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[ring]), (n / kJobs) & 1, abort_ptr,
                               kUnitWaits * p.timeout_ns, kRolePagedMma);
       if (!ok) break;
       const int b = jobs[ring].b, blocks = jobs[ring].j1 - jobs[ring].j0, nt = jobs[ring].rows > 128 ? 2 : 1;
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[ring]));
       if (b < 0) break;
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_q_full), n & 1, abort_ptr, p.timeout_ns, kRolePagedMma) && k_wait(pair0);
-      if (!ok) break;
+      ok = k_wait(pair0);
       // (Every P of the unit before has been waited for, so S is free; its O is read before this unit's first P.)
-      for (int t = 0; t < nt; ++t) qk(t, pair0);
+      for (int t = 0; t < nt && ok; ++t) {
+        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_q_full[t]), units[t]++ & 1, abort_ptr, p.timeout_ns, kRolePagedMma);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        qk(t, pair0);
+      }
+      if (!ok) break;
       ptx::mma_commit_warp(ptx::smem_u32(&bar_empty[2 * pair0 % C::kTiles]));
-      if (blocks == 1) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty));
       for (int jj = 0; jj < blocks && ok; ++jj) {
         const int pair = pair0 + jj;
         const bool last = jj + 1 == blocks;
@@ -442,14 +512,14 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
         for (int t = 0; t < nt && ok; ++t) {
           // P V in two halves: the first runs while the weights of keys 64-127 are still computed.
           const uint32_t d = tmem_base + C::kColO + HD * t, a = tmem_base + C::kColS + 128 * t, par = (g[t] - 1) & 1;
-          ok = wait_warp_or_abort(ptx::smem_u32(&bar_p_half[t]), par, abort_ptr, p.timeout_ns, kRolePagedMma);
+          ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_half[t]), par, abort_ptr, p.timeout_ns, kRolePagedMma);
           if (ok && t == 0)
-            ok = wait_warp_or_abort(ptx::smem_u32(&bar_slot_full[pair % C::kSlots]), (pair / C::kSlots) & 1, abort_ptr,
+            ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_slot_full[pair % C::kSlots]), (pair / C::kSlots) & 1, abort_ptr,
                                     p.timeout_ns, kRolePagedMma);
           if (!ok) break;
           ptx::tc_fence_after();
           ptx::mma_ts_k64half_warp<0>(d, a, ptx::desc_lo(v), ptx::desc_hi(v), C::kIdescPV, jj > 0 ? 1u : 0u);
-          ok = wait_warp_or_abort(ptx::smem_u32(&bar_p_full[t]), par, abort_ptr, p.timeout_ns, kRolePagedMma);
+          ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_full[t]), par, abort_ptr, p.timeout_ns, kRolePagedMma);
           if (!ok) break;
           ptx::tc_fence_after();
           ptx::mma_ts_k64half_warp<1>(d, a, ptx::desc_lo(v), ptx::desc_hi(v), C::kIdescPV, 1u);
@@ -463,10 +533,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
         }
         if (!ok) break;
         ptx::mma_commit_warp(ptx::smem_u32(&bar_slot_empty[pair % C::kSlots]));
-        if (!last) {
-          ptx::mma_commit_warp(ptx::smem_u32(&bar_empty[2 * (pair + 1) % C::kTiles]));
-          if (jj + 2 == blocks) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty));
-        }
+        if (!last) ptx::mma_commit_warp(ptx::smem_u32(&bar_empty[2 * (pair + 1) % C::kTiles]));
       }
       pair0 += blocks;
     }
@@ -482,77 +549,18 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
     int pair = 0;                            // key tiles so far
     for (int n = 0; ok; ++n) {
       const int ring = n & (kJobs - 1);
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_job_full[ring]), (n / kJobs) & 1, abort_ptr,
+      ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_job_full[ring]), (n / kJobs) & 1, abort_ptr,
                               kUnitWaits * p.timeout_ns, kRolePagedQuery);
       if (!ok) break;
       const PagedJob job = jobs[ring];
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bar_job_empty[ring]));
       if (job.b < 0) break;
-      // The query rows, kLanes lanes a row, 16 elements each: as bf16 to where
-      // their hi and lo will stand (all at once: a loop of loads took 15000 cycles
-      // and more); then every thread converts what it asked for.
-      ok = wait_warp_or_abort(ptx::smem_u32(&bar_q_empty), (n & 1) ^ 1u, abort_ptr, kUnitWaits * p.timeout_ns,
-                              kRolePagedQuery);
-      if (!ok) break;
-      {
-        constexpr int kLanes = HD / 16, kStep = 128 / kLanes;
-        const int part = tid % kLanes, rows = job.rows <= 128 ? 128 : 256;
-        // Row r of tile r / 128: 16 bytes of hi, and kTileBytes behind them of lo.
-        auto place = [&](int r) {
-          return static_cast<uint32_t>((r >> 7) * 2 * C::kTileBytes + (r & 127) * HD +
-                                       ((part ^ (HD == 128 ? r & 7 : (r >> 1) & 3)) << 4));
-        };
-        int ti = (tid / kLanes) / job.heads, hi = tid / kLanes - ti * job.heads;
-#pragma unroll 1
-        for (int r = tid / kLanes; r < job.rows; r += kStep) {
-          const __nv_bfloat16* src = p.q + (job.token + ti) * p.q_t + (job.head + hi) * p.q_h + 16 * part;
-          ptx::cp_async16(sQ + place(r), src);
-          ptx::cp_async16(sQ + place(r) + C::kTileBytes, src + 8);
-          for (hi += kStep; hi >= job.heads; hi -= job.heads) ++ti;
-        }
-        ptx::cp_async_wait();
-#pragma unroll 2
-        for (int r = tid / kLanes; r < rows; r += kStep) {
-          uint4* to0 = reinterpret_cast<uint4*>(generic + place(r));
-          uint4* to1 = reinterpret_cast<uint4*>(generic + place(r) + C::kTileBytes);
-          float x[16], amax = 0.f;
-          unpack8(r < job.rows ? *to0 : make_uint4(0u, 0u, 0u, 0u), x);
-          unpack8(r < job.rows ? *to1 : make_uint4(0u, 0u, 0u, 0u), x + 8);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            if (fabsf(x[e]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(x[e]));
-            else x[e] = __uint_as_float(0x7fffffffu);
-          }
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          const int up = amax > 0.f ? max(-120, min(120, 134 - static_cast<int>(__float_as_uint(amax) >> 23))) : 0;
-          const float scale = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-          uint32_t hi4[4], lo4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            hi4[e] = lo4[e] = 0;
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              const float a = x[4 * e + 2 * f] * scale, b = x[4 * e + 2 * f + 1] * scale;
-              const uint32_t h = to_e4m3x2(a, b);
-              const float2 back = from_e4m3x2(h);
-              hi4[e] |= h << (16 * f);
-              lo4[e] |= to_e4m3x2(a - back.x, b - back.y) << (16 * f);
-            }
-          }
-          *to0 = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-          *to1 = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
-          if (part == 0) row_scale[n & 1][r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-        }
-      }
-      ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(ptx::smem_u32(&bar_q_full));
       // The V tiles: a thread has a key's row.
       for (int j = job.j0; j < job.j1 && ok; ++j, ++pair) {
         const bool clear = j * 128 + tid >= job.n_keys;   // (rows behind the unit's keys may hold anything)
         const int it = 2 * pair + 1, tile = it % C::kTiles, slot = pair % C::kSlots;
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_full[tile]), (it / C::kTiles) & 1, abort_ptr, p.timeout_ns,
+        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_full[tile]), (it / C::kTiles) & 1, abort_ptr, p.timeout_ns,
                                 kRolePagedQuery);
         if (!ok) break;
         uint4 v[HD / 16];
@@ -560,7 +568,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < HD / 16; ++i)
           v[i] = *reinterpret_cast<const uint4*>(from + ((i ^ (HD == 128 ? tid & 7 : (tid >> 1) & 3)) << 4));
-        ok = wait_warp_or_abort(ptx::smem_u32(&bar_slot_empty[slot]), ((pair / C::kSlots) & 1) ^ 1u, abort_ptr,
+        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_slot_empty[slot]), ((pair / C::kSlots) & 1) ^ 1u, abort_ptr,
                                 p.timeout_ns, kRolePagedQuery);
         if (!ok) break;
         uint8_t* to = generic + (sSlots - smem_base) + slot * C::kSlotBytes + tid * 128;

@@ -9,8 +9,10 @@
 // frequency's own rounding (2^-53 of itself): one integer product per angle.
 // Its top 32 bits, as a signed fraction of half a turn, go through sincospif.
 //
-// Work. A CTA takes a few tokens and all heads of both tensors: the angles of
-// its tokens are computed once, into shared memory, and used for every head.
+// What bounds it: memory, one read and one write of every element. A CTA takes
+// about 40 KB of rows (a few tokens, all heads of both tensors); its angles are
+// computed once, into shared memory, for all heads, while the first rows are on
+// their way. A thread keeps its columns for all its rows.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -19,6 +21,13 @@
 #include "fa_varlen_kernel.cuh"
 
 namespace fa {
+
+namespace ptx {
+// Programmatic dependent launches: what follows waits until the grids before
+// have ended and their writes are visible; the next grid may be scheduled.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+}  // namespace ptx
 
 // Turns per position (modulo 1) in 2^-64.
 __device__ __forceinline__ uint64_t turns_of(double inv_freq) {
@@ -87,57 +96,95 @@ struct RopeTensor {
   int heads;
 };
 
-struct RopeParams {
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxTokens = 16;
+constexpr int kRopeMaxPairs = 128;
+constexpr int kRopeAngles = 1024;        // pairs of a CTA's tokens
+
+// The rows of a CTA's tokens: all heads of x, then of y, token by token.
+struct RopeRows {
   RopeTensor x, y;           // y.heads = 0: none
+  int T, d, rot, interleaved;
+  int tokens;                // of a CTA
+  unsigned inv_heads;        // ceil(2^32 / (x.heads + y.heads)), for several tokens a CTA and more than one head
+};
+
+struct RopeParams {
+  RopeRows r;
   const int* positions;      // [T]
   const double* inv_freq;    // [rot / 2]
-  int T, d, rot, interleaved, transpose;
-  int tokens;                // of a CTA, at most kRopeTokens
+  int transpose;
   float factor;
 };
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 4;
-constexpr int kRopeMaxPairs = 128;
-
-// `n` tokens from t0 on, whose angles stand in cs [tokens][rot / 2]; rows with
-// skip[token] != 0 are left alone.
-__device__ __forceinline__ void rope_rows(const RopeTensor& t, int t0, int n, int d, int rot, bool interleaved,
-                                          const float2* cs, const int* skip, int first, int step) {
-  const int items = d / 16, per_token = t.heads * items;
-  for (int w = first; w < n * per_token; w += step) {
-    const int k = w / per_token, r = w - k * per_token, h = r / items, i = r - h * items;
-    if (skip && skip[k]) continue;
-    const RopeItem it = rope_item(i, rot, interleaved);
-    const __nv_bfloat16* in = t.in + (t0 + k) * t.in_t + h * t.in_h;
-    __nv_bfloat16* out = t.out + (t0 + k) * t.out_t + h * t.out_h;
-    uint4 v0 = *reinterpret_cast<const uint4*>(in + it.c0), v1 = *reinterpret_cast<const uint4*>(in + it.c1);
-    if (i < rot / 16) {
-      float x[16];
-      unpack8(v0, x);
-      unpack8(v1, x + 8);
-      rope_turn(x, cs + k * (rot / 2) + 8 * i, interleaved);
-      v0 = pack8(x);
-      v1 = pack8(x + 8);
+// Rotates the rows of the tokens t0 .. t0 + n - 1, whose angles `angles` writes
+// to cs [token][rot / 2] (all threads call it, behind their first loads).
+// Tokens with skip[token] != 0, as `angles` left it, are left alone.
+template <int kThreads, class Angles>
+__device__ __forceinline__ void rope_rows(const RopeRows& p, int t0, int n, const float2* cs, const int* skip,
+                                          Angles angles) {
+  constexpr int kBatch = 4;
+  const int items = p.d / 16, heads = p.x.heads + p.y.heads, rows = n * heads;
+  const int step = kThreads / items, row0 = threadIdx.x / items, i = threadIdx.x - row0 * items;
+  const bool inter = p.interleaved != 0, turns = i < p.rot / 16;
+  const RopeItem it = rope_item(i, p.rot, inter);
+  const bool idle = row0 >= step;            // (threads beyond the last whole row)
+  bool first = true;
+#pragma unroll 1
+  for (int r0 = row0; first || r0 < rows; r0 += kBatch * step) {
+    uint4 v[kBatch][2];
+    __nv_bfloat16* out[kBatch];
+    int token[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = r0 + k * step;
+      token[k] = -1;
+      if (r < rows && !idle) {
+        const int t = p.tokens == 1 ? 0 : heads == 1 ? r : static_cast<int>(__umulhi(static_cast<unsigned>(r), p.inv_heads));
+        int h = r - t * heads;
+        const bool second = h >= p.x.heads;
+        const RopeTensor& a = second ? p.y : p.x;
+        if (second) h -= p.x.heads;
+        const __nv_bfloat16* in = a.in + (t0 + t) * a.in_t + h * a.in_h;
+        out[k] = a.out + (t0 + t) * a.out_t + h * a.out_h;
+        token[k] = t;
+        v[k][0] = *reinterpret_cast<const uint4*>(in + it.c0);
+        v[k][1] = *reinterpret_cast<const uint4*>(in + it.c1);
+      }
     }
-    *reinterpret_cast<uint4*>(out + it.c0) = v0;
-    *reinterpret_cast<uint4*>(out + it.c1) = v1;
+    if (first) angles();
+    first = false;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (token[k] < 0 || (skip && skip[token[k]])) continue;
+      if (turns) {
+        float x[16];
+        unpack8(v[k][0], x);
+        unpack8(v[k][1], x + 8);
+        rope_turn(x, cs + token[k] * (p.rot / 2) + 8 * i, inter);
+        v[k][0] = pack8(x);
+        v[k][1] = pack8(x + 8);
+      }
+      *reinterpret_cast<uint4*>(out[k] + it.c0) = v[k][0];
+      *reinterpret_cast<uint4*>(out[k] + it.c1) = v[k][1];
+    }
   }
 }
 
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p) {
-  __shared__ __align__(16) float2 cs[kRopeTokens * kRopeMaxPairs];
-  const int t0 = blockIdx.x * p.tokens, n = min(p.tokens, p.T - t0), half = p.rot / 2;
-  for (int w = threadIdx.x; w < n * half; w += kRopeThreads) {
-    const int k = w / half, j = w - k * half;
-    float2 t = turn(p.positions[t0 + k], turns_of(p.inv_freq[j]), p.factor);
-    if (p.transpose) t.y = -t.y;
-    cs[w] = t;
-  }
-  __syncthreads();
-  const int first = blockIdx.y * kRopeThreads + threadIdx.x, step = gridDim.y * kRopeThreads;
-  rope_rows(p.x, t0, n, p.d, p.rot, p.interleaved != 0, cs, nullptr, first, step);
-  if (p.y.heads) rope_rows(p.y, t0, n, p.d, p.rot, p.interleaved != 0, cs, nullptr, first, step);
+  __shared__ __align__(16) float2 cs[kRopeAngles];
+  ptx::grid_wait();
+  ptx::grid_next();
+  const int t0 = blockIdx.x * p.r.tokens, n = min(p.r.tokens, p.r.T - t0), half = p.r.rot / 2;
+  rope_rows<kRopeThreads>(p.r, t0, n, cs, nullptr, [&] {
+    for (int w = threadIdx.x; w < n * half; w += kRopeThreads) {
+      const int k = w / half, j = w - k * half;
+      float2 t = turn(p.positions[t0 + k], turns_of(p.inv_freq[j]), p.factor);
+      if (p.transpose) t.y = -t.y;
+      cs[w] = t;
+    }
+    __syncthreads();
+  });
 }
 
 }  // namespace fa
