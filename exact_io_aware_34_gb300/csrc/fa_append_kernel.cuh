@@ -92,6 +92,8 @@ __device__ __forceinline__ float least_scale(float amax) {
 }
 
 constexpr int kAppendThreads = 256;
+// Dynamic shared memory at most: the angles of a page's rows (or kRopeAngles for queries).
+constexpr int kAppendMaxSmem = 128 * 64 * static_cast<int>(sizeof(float2));
 
 // Up to 16 rows of a head as kItems items of 16 columns a lane, rotated. Lane l's
 // item k is item l % items of row (l / items) + k * (32 / items), items = HD / 16.
@@ -101,8 +103,8 @@ struct AppendRows {
   float x[kItems][16];
   float amax;                      // of the finite values
 
-  __device__ __forceinline__ void load(const AppendParams& p, const uint64_t* turns_at, int which, int head, int t0, int p0,
-                                       int rows) {
+  // cs: the rows' angles (keys).
+  __device__ __forceinline__ void load(const AppendParams& p, const float2* cs, int which, int head, int t0, int rows) {
     const int lane = threadIdx.x & 31, row0 = lane / kPerRow, i = lane % kPerRow;
     const bool inter = p.interleaved != 0, turns = which == 0 && i < p.rot / 16;
     const RopeItem it = rope_item(i, which == 0 ? p.rot : 0, inter);
@@ -129,10 +131,8 @@ struct AppendRows {
       unpack8(v[k][0], x[k]);
       unpack8(v[k][1], x[k] + 8);
       if (turns && r < rows) {
-        const int position = p.positions ? p.positions[t0 + r] : p0 + r;
         float2 t[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = turn(position, turns_at[8 * i + e], p.factor);
+        item_angles(t, cs + r * (p.rot / 2), i, p.rot);
         rope_turn(x[k], t, inter);
       }
       float m = 0.f;
@@ -179,7 +179,7 @@ struct AppendRows {
 template <int HD>
 __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendParams p) {
   constexpr int kThreads = kAppendThreads;
-  __shared__ __align__(16) float2 cs[kRopeAngles];
+  extern __shared__ __align__(16) float2 cs[];
   __shared__ int found[4], at[kRopeMaxTokens], skip[kRopeMaxTokens];
   __shared__ float warp_max[8];
   ptx::grid_wait();
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
       __syncthreads();
       for (int w = threadIdx.x; w < n * half; w += kThreads) {
         const int k = w / half, j = w - k * half;
-        if (!skip[k]) cs[w] = turn(at[k], turns_of(p.inv_freq[j]), p.factor);
+        if (!skip[k]) cs[k * half + angle_at(j, p.rot)] = turn(at[k], turns_of(p.inv_freq[j]), p.factor);
       }
       __syncthreads();
     });
@@ -216,12 +216,6 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
   const int which = static_cast<int>(blockIdx.x) & 1, u = static_cast<int>(blockIdx.x) >> 1;
   const int place = p.head_groups == 1 ? u : u / p.head_groups, group = u - place * p.head_groups;
   const bool check = blockIdx.x == 0;
-  // The frequencies, once for all heads.
-  uint64_t* turns = reinterpret_cast<uint64_t*>(cs);
-  if (which == 0 && half > 0) {
-    if (threadIdx.x < half) turns[threadIdx.x] = turns_of(p.inv_freq[threadIdx.x]);
-    __syncthreads();
-  }
   // A decode step's token t is sequence t's; else all threads look for the place's sequence.
   int b = -1, c0 = 0, c1 = 0, len = 0;
   if (p.per_token && place < p.B) {
@@ -274,15 +268,14 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
   const int warp = threadIdx.x >> 5, sub = warp & (p.warps - 1), head = group * (8 / p.warps) + warp / p.warps;
   const bool live = head < p.H_kv;
   const int row0 = p0 % p.page, rows = p1 - p0, t0 = c0 + (p0 - before);
-  AppendRows<HD> x;
-  x.amax = 0.f;
-  float amax = 0.f;
-  if (live) {
-#pragma unroll 1
-    for (int r = 16 * sub; r < rows; r += 16 * p.warps) {
-      x.load(p, turns, which, head, t0 + r, p0 + r, min(16, rows - r));
-      amax = fmaxf(amax, x.amax);
+  // The angles of the keys' rows, for all heads of the CTA.
+  if (which == 0 && half > 0) {
+    for (int w = threadIdx.x; w < rows * half; w += kThreads) {
+      const int k = w / half, j = w - k * half;
+      cs[k * half + angle_at(j, p.rot)] =
+          turn(p.positions ? p.positions[t0 + k] : p0 + k, turns_of(p.inv_freq[j]), p.factor);
     }
+    __syncthreads();
   }
   if (id < 0 || id >= p.num_pages) {
     if (threadIdx.x == 0) append_bad(b);
@@ -290,23 +283,33 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
   }
   float* scale_at = p.scale[which] + static_cast<long long>(id) * p.H_kv + head;
   const float old = live && row0 > 0 ? *scale_at : 0.f;
+  uint8_t* out = p.cache[which] + id * p.c_page[which] + head * p.c_head[which];
+  AppendRows<HD> x;
+  float amax = 0.f, scale = 0.f;
+  // First the largest value, then the rounding; rows of more than one block are read again for it.
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int r = 16 * sub; r < rows && live; r += 16 * p.warps) {
+      if (pass == 0 || rows > 16 * p.warps) {
+        x.load(p, cs + r * half, which, head, t0 + r, min(16, rows - r));
+        amax = fmaxf(amax, x.amax);
+      }
+      if (pass == 1) x.store(p, which, out + (row0 + r) * p.c_row[which], min(16, rows - r), scale);
+    }
+    if (pass == 1) break;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  __syncwarp();                    // (every lane has read the old scale)
-  if (p.warps > 1) {
-    if ((threadIdx.x & 31) == 0) warp_max[warp] = amax;
-    __syncthreads();
-    for (int w = 0; w < p.warps; ++w) amax = fmaxf(amax, warp_max[warp - sub + w]);
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    __syncwarp();                  // (every lane has read the old scale)
+    if (p.warps > 1) {
+      if ((threadIdx.x & 31) == 0) warp_max[warp] = amax;
+      __syncthreads();
+      for (int w = 0; w < p.warps; ++w) amax = fmaxf(amax, warp_max[warp - sub + w]);
+    }
+    scale = fmaxf(least_scale(amax), old);
+    if (live && sub == 0 && (threadIdx.x & 31) == 0) *scale_at = scale;
   }
   if (!live) return;
-  const float scale = fmaxf(least_scale(amax), old);
-  if (sub == 0 && (threadIdx.x & 31) == 0) *scale_at = scale;
-  uint8_t* out = p.cache[which] + id * p.c_page[which] + head * p.c_head[which];
-#pragma unroll 1
-  for (int r = 16 * sub; r < rows; r += 16 * p.warps) {
-    if (rows > 16 * p.warps) x.load(p, turns, which, head, t0 + r, p0 + r, min(16, rows - r));   // (more than one block: again)
-    x.store(p, which, out + (row0 + r) * p.c_row[which], min(16, rows - r), scale);
-  }
   if (row0 > 0 && scale != old) {
     const float ratio = old / scale;
     constexpr int kPerRow = HD / 16;

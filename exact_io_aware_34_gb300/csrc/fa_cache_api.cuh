@@ -265,10 +265,24 @@ fa_status_t append_impl(const void* K, const void* V, const int* cu_new, void* K
   p.head_groups = (H_kv * p.warps + 7) / 8;
   const long long ctas = 2LL * p.places * p.head_groups + (Q ? (T + p.q.tokens - 1) / p.q.tokens : 0);
   if (ctas >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  const void* kernel = d == 64 ? reinterpret_cast<const void*>(&fa::fa_append_kernel<64>)
+                               : reinterpret_cast<const void*>(&fa::fa_append_kernel<128>);
+  // The angles of a page's rows; of a query CTA's tokens.
+  const int smem = static_cast<int>(sizeof(float2)) * std::max(page * rot / 2, Q ? p.q.tokens * rot / 2 : 0);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (dev < 0 || dev >= 64) return FA_ERR_UNSUPPORTED;
+  static std::once_flag once[64];
+  static cudaError_t attr_err[64];
+  std::call_once(once[dev], [&] {
+    attr_err[dev] = cudaFuncSetAttribute(fa::fa_append_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, fa::kAppendMaxSmem);
+    if (attr_err[dev] == cudaSuccess)
+      attr_err[dev] = cudaFuncSetAttribute(fa::fa_append_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, fa::kAppendMaxSmem);
+  });
+  if (attr_err[dev] != cudaSuccess) return cuda_fail(attr_err[dev]);
   void* args[1] = {&p};
-  const cudaError_t e = launch_dependent(
-      d == 64 ? reinterpret_cast<const void*>(&fa::fa_append_kernel<64>) : reinterpret_cast<const void*>(&fa::fa_append_kernel<128>),
-      dim3(static_cast<unsigned>(ctas)), fa::kAppendThreads, 0, stream, args);
+  e = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), fa::kAppendThreads, smem, stream, args);
   return e == cudaSuccess ? FA_OK : cuda_fail(e);
 }
 

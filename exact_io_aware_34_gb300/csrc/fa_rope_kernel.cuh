@@ -5,8 +5,8 @@
 //
 // Angles. position * inv_freq in float32 is off by 0.06 at position 10^6. Here
 // a frequency becomes turns per position in 64-bit fixed point; position times
-// that, modulo 2^64, is the angle modulo one turn, exactly but for the
-// frequency's own rounding (2^-53 of itself): one integer product per angle.
+// that, modulo 2^64, is the angle modulo one turn, exactly but for position *
+// 2^-64 turns: one integer product per angle.
 // Its top 32 bits, as a signed fraction of half a turn, go through sincospif.
 //
 // What bounds it: memory, one read and one write of every element. A CTA takes
@@ -29,12 +29,18 @@ __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;
 __device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 }  // namespace ptx
 
-// Turns per position (modulo 1) in 2^-64.
+// Turns per position (modulo 1) in 2^-64, cut: the 53 bits of inv_freq times
+// 2^66 / 2 pi, in integers (the SM has few float64 units: with them this took an
+// eighth of the time of a large call).
 __device__ __forceinline__ uint64_t turns_of(double inv_freq) {
-  double t = inv_freq * 0.15915494309189533577;      // / 2 pi
-  t -= floor(t);
-  // (t may round up to 1, which is 0.)
-  return t < 1.0 ? static_cast<uint64_t>(t * 18446744073709551616.0) : 0ull;
+  const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(inv_freq));
+  const int ex = static_cast<int>(bits >> 52) & 0x7ff;
+  const uint64_t m = ((bits & 0xfffffffffffffull) | (ex ? 1ull << 52 : 0ull)) << 11;
+  constexpr uint64_t kC = 0xa2f9836e4e441529ull;            // floor(2^66 / 2 pi)
+  const uint64_t hi = __umul64hi(m, kC), lo = m * kC;
+  const int s = (ex ? ex : 1) - 1024;
+  const uint64_t r = s <= 0 ? (s > -64 ? hi >> -s : 0ull) : s < 64 ? hi << s | lo >> (64 - s) : 0ull;
+  return bits >> 63 ? 0ull - r : r;
 }
 
 // f cos, f sin of position * inv_freq.
@@ -55,8 +61,21 @@ __device__ __forceinline__ RopeItem rope_item(int i, int rot, bool interleaved) 
   return RopeItem{8 * i, 8 * i + rot / 2};
 }
 
+// A token's angles as pairs of (f cos, f sin), so that neighbouring items' are
+// neighbours: those of the pairs 8 i + 2 e and 8 i + 2 e + 1 at [e][i], `rot / 16`
+// items. This is where pair j of a token lies, in float2.
+__device__ __forceinline__ int angle_at(int j, int rot) { return ((j & 7) >> 1) * (rot / 8) + (j >> 3) * 2 + (j & 1); }
+__device__ __forceinline__ void item_angles(float2 (&t)[8], const float2* cs, int i, int rot) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float4 v = *reinterpret_cast<const float4*>(cs + e * (rot / 8) + 2 * i);
+    t[2 * e] = make_float2(v.x, v.y);
+    t[2 * e + 1] = make_float2(v.z, v.w);
+  }
+}
+
 // The pairs of an item, in place; cs[e] belongs to its pair e.
-__device__ __forceinline__ void rope_turn(float (&x)[16], const float2* cs, bool interleaved) {
+__device__ __forceinline__ void rope_turn(float (&x)[16], const float2 (&cs)[8], bool interleaved) {
   if (interleaved) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -118,7 +137,7 @@ struct RopeParams {
 };
 
 // Rotates the rows of the tokens t0 .. t0 + n - 1, whose angles `angles` writes
-// to cs [token][rot / 2] (all threads call it, behind their first loads).
+// to cs, rot / 2 a token (see angle_at; all threads call it, behind their first loads).
 // Tokens with skip[token] != 0, as `angles` left it, are left alone.
 template <int kThreads, class Angles>
 __device__ __forceinline__ void rope_rows(const RopeRows& p, int t0, int n, const float2* cs, const int* skip,
@@ -161,7 +180,9 @@ __device__ __forceinline__ void rope_rows(const RopeRows& p, int t0, int n, cons
         float x[16];
         unpack8(v[k][0], x);
         unpack8(v[k][1], x + 8);
-        rope_turn(x, cs + token[k] * (p.rot / 2) + 8 * i, inter);
+        float2 t[8];
+        item_angles(t, cs + token[k] * (p.rot / 2), i, p.rot);
+        rope_turn(x, t, inter);
         v[k][0] = pack8(x);
         v[k][1] = pack8(x + 8);
       }
@@ -181,7 +202,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
       const int k = w / half, j = w - k * half;
       float2 t = turn(p.positions[t0 + k], turns_of(p.inv_freq[j]), p.factor);
       if (p.transpose) t.y = -t.y;
-      cs[w] = t;
+      cs[k * half + angle_at(j, p.r.rot)] = t;
     }
     __syncthreads();
   });
