@@ -4,6 +4,13 @@
 
 namespace {
 
+// device_sm_count, asked once per device.
+int cached_sm_count() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return device_sm_count();
+  return sm_count(dev);
+}
+
 // 8-bit pages [num_pages, H_kv, page, d] with byte strides (d contiguous).
 struct Pages {
   const void* p;
@@ -98,7 +105,7 @@ fa::RopeRows rope_rows(const fa::RopeTensor& x, const fa::RopeTensor& y, int T, 
   r.interleaved = interleaved;
   int n = 40960 / (heads * d * 2);
   n = std::min(n, 2 * fa::kRopeAngles / rot);
-  n = std::min(n, T / (4 * device_sm_count()));
+  n = std::min(n, T / (4 * cached_sm_count()));
   r.tokens = heads > 4096 ? 1 : std::max(1, std::min(n, fa::kRopeMaxTokens));
   r.inv_heads = r.tokens == 1 ? 0u : static_cast<unsigned>(((1ull << 32) + heads - 1) / heads);
   return r;
@@ -345,7 +352,7 @@ long long paged_places(const fa::PagedShape& s) {
   return places < 2147418112.0 ? static_cast<long long>(places) : 0;
 }
 int paged_ctas(const fa::PagedShape& s, int N) {
-  return static_cast<int>(std::min(paged_places(s), (N > 16 ? 1LL : 2LL) * device_sm_count()));
+  return static_cast<int>(std::min(paged_places(s), (N > 16 ? 1LL : 2LL) * cached_sm_count()));
 }
 
 struct PagedLayout {

@@ -179,11 +179,15 @@ def _on_stream(stream, device):
     return torch.cuda.stream(stream)
 
 
+#: index of the current device (torch.cuda.current_device without its initialisation, which a CUDA tensor has seen)
+_current_device = torch._C._cuda_getDevice
+
+
 def _launch(fn, stream, device):
     """fn() with ``device`` current and ``stream`` torch's current stream: what
     fn allocates and enqueues belongs to it. (The usual case enters no context;
     small calls are bound by the host.)"""
-    if stream is None and torch.cuda.current_device() == device.index:
+    if stream is None and _current_device() == device.index:
         return fn()
     with _on_stream(stream, device):
         return fn()
@@ -833,25 +837,31 @@ def fa_rope(x, positions, inv_freq, y=None, out=None, out_y=None, interleaved: b
     T, heads, d = rows = _leading("x", x, 3)
     device = x.device
     dense = _bf16("x", x, device, rows)
-    heads_y, rows_y = 0, None
+    heads_y, rows_y, y_ptr = 0, None, None
     if y is not None:
         heads_y = _leading("y", y, 3)[1]
-        rows_y = torch.Size((T, heads_y, d))
+        rows_y = (T, heads_y, d)
         dense &= _bf16("y", y, device, rows_y)
+        y_ptr = y.data_ptr()
     elif out_y is not None:
         raise ValueError("out_y comes with y")
     _int32("positions", positions, device, T)
     rot = _frequencies(inv_freq, device)
 
     def run():
-        o, o_dense = _out_bf16("out", out, device, rows, x)
-        oy, oy_dense = (None, True) if y is None else _out_bf16("out_y", out_y, device, rows_y, y)
-        all_dense = dense and o_dense and oy_dense
-        st = load_library().fa_rope(
-            x.data_ptr(), o.data_ptr(), heads, None if y is None else y.data_ptr(),
-            None if y is None else oy.data_ptr(), heads_y, positions.data_ptr(), inv_freq.data_ptr(), T, d, rot,
-            _strides(all_dense, x, o, *(() if y is None else (y, oy))), bool(interleaved), bool(transpose),
-            float(factor), _raw_stream(device))
+        o, all_dense = _out_bf16("out", out, device, rows, x)
+        all_dense &= dense
+        oy = oy_ptr = None
+        if y is not None:
+            oy, oy_dense = _out_bf16("out_y", out_y, device, rows_y, y)
+            all_dense &= oy_dense
+            oy_ptr = oy.data_ptr()
+        strides = None
+        if not all_dense:
+            strides = _strides(False, x, o) if y is None else _strides(False, x, o, y, oy)
+        st = (_lib or load_library()).fa_rope(
+            x.data_ptr(), o.data_ptr(), heads, y_ptr, oy_ptr, heads_y, positions.data_ptr(), inv_freq.data_ptr(), T, d,
+            rot, strides, interleaved, transpose, factor, _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_rope")
         return o if y is None else (o, oy)
@@ -874,15 +884,30 @@ def _cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, device, B):
     """(pages' shape, entries of a sequence in the table, whether the pages are contiguous)."""
     shape = _leading("k_cache", k_cache, 4)
     dense = _pages("k_cache", k_cache, device, shape) & _pages("v_cache", v_cache, device, shape)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != shape[:2] \
-                or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 tensor {list(shape[:2])} on {device}")
+    scales = shape[:2]
+    for t in (k_scale, v_scale):
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.shape != scales or t.device != device \
+                or not t.is_contiguous():
+            raise ValueError(f"k_scale and v_scale must be contiguous float32 tensors {list(scales)} on {device}")
     if not isinstance(page_table, torch.Tensor) or page_table.dtype is not torch.int32 or page_table.dim() != 2 \
-            or page_table.shape[0] != B or page_table.device != device or not page_table.is_contiguous():
+            or page_table.device != device or not page_table.is_contiguous():
         raise ValueError(f"page_table must be a contiguous int32 tensor [{B}, max_pages] on {device}")
+    sequences, max_pages = page_table.shape
+    if sequences != B:
+        raise ValueError(f"page_table must have a row for each of {B} sequences")
     _int32("seq_lens", seq_lens, device, B)
-    return shape, page_table.shape[1], dense
+    return shape, max_pages, dense
+
+
+def _sequences(name, cu, device):
+    """Number of sequences that these offsets separate."""
+    if not isinstance(cu, torch.Tensor) or cu.dtype is not torch.int32 or cu.dim() != 1 or cu.device != device \
+            or not cu.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [B + 1] on {device}")
+    n = len(cu) - 1
+    if n < 1:
+        raise ValueError(f"{name} must hold B + 1 offsets")
+    return n
 
 
 def fa_kv_append(k, v, cu_new, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, q=None, q_out=None,
@@ -906,10 +931,7 @@ def fa_kv_append(k, v, cu_new, k_cache, v_cache, k_scale, v_scale, page_table, s
     T, H_kv, d = rows = _leading("k", k, 3)
     device = k.device
     dense = _bf16("k", k, device, rows) & _bf16("v", v, device, rows)
-    if not isinstance(cu_new, torch.Tensor) or cu_new.dim() != 1 or cu_new.shape[0] < 2:
-        raise ValueError("cu_new must hold B + 1 offsets")
-    B = cu_new.shape[0] - 1
-    _int32("cu_new", cu_new, device, B + 1)
+    B = _sequences("cu_new", cu_new, device)
     (num_pages, heads, page, d_cache), max_pages, dense_cache = _cache(k_cache, v_cache, k_scale, v_scale, page_table,
                                                                        seq_lens, device, B)
     if heads != H_kv or d_cache != d:
@@ -920,21 +942,28 @@ def fa_kv_append(k, v, cu_new, k_cache, v_cache, k_scale, v_scale, page_table, s
     H, rows_q = 0, None
     if q is not None:
         H = _leading("q", q, 3)[1]
-        rows_q = torch.Size((T, H, d))
+        rows_q = (T, H, d)
         dense &= _bf16("q", q, device, rows_q)
     if q_out is not None and (q is None or not rot):
         raise ValueError("q_out comes with q and inv_freq")
     turn = q is not None and rot > 0
 
     def run():
-        o, o_dense = _out_bf16("q_out", q_out, device, rows_q, q) if turn else (None, True)
-        st = load_library().fa_kv_append(
+        o = q_ptr = o_ptr = None
+        all_dense = dense
+        if turn:
+            o, o_dense = _out_bf16("q_out", q_out, device, rows_q, q)
+            all_dense &= o_dense
+            q_ptr, o_ptr = q.data_ptr(), o.data_ptr()
+        strides = None
+        if not all_dense:
+            strides = _strides(False, k, v, q, o) if turn else _strides(False, k, v)
+        st = (_lib or load_library()).fa_kv_append(
             k.data_ptr(), v.data_ptr(), cu_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), q.data_ptr() if turn else None,
-            o.data_ptr() if turn else None, inv_freq.data_ptr() if rot else None,
-            None if positions is None else positions.data_ptr(), B, H, H_kv, T, d, num_pages, page, max_pages, rot,
-            _strides(dense and o_dense, k, v, *((q, o) if turn else ())), _strides(dense_cache, k_cache, v_cache),
-            bool(interleaved), float(factor), _raw_stream(device))
+            v_scale.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), q_ptr, o_ptr,
+            inv_freq.data_ptr() if rot else None, None if positions is None else positions.data_ptr(), B, H, H_kv, T, d,
+            num_pages, page, max_pages, rot, strides, None if dense_cache else _strides(False, k_cache, v_cache),
+            interleaved, factor, _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_kv_append")
         return o if turn else q
@@ -965,10 +994,7 @@ def fa_fwd_paged(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu
     T_q, H, d = rows = _leading("q", q, 3)
     device = q.device
     dense = _bf16("q", q, device, rows)
-    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 2:
-        raise ValueError("cu_q must hold B + 1 offsets")
-    B = cu_q.shape[0] - 1
-    _int32("cu_q", cu_q, device, B + 1)
+    B = _sequences("cu_q", cu_q, device)
     (num_pages, H_kv, page, d_cache), max_pages, dense_cache = _cache(k_cache, v_cache, k_scale, v_scale, page_table,
                                                                       seq_lens, device, B)
     if d_cache != d:
@@ -979,11 +1005,11 @@ def fa_fwd_paged(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu
         out_lse = _out_lse(lse, (H, T_q), device)
         need = _need("fa_fwd_paged_workspace_bytes", device, B, H, H_kv, T_q, d, num_pages, page, max_pages)
         ws, ws_ptr, ws_bytes = _workspace(workspace, need, device)
-        st = load_library().fa_fwd_paged(
+        st = (_lib or load_library()).fa_fwd_paged(
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             page_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), out.data_ptr(), out_lse.data_ptr(), B, H,
-            H_kv, T_q, d, num_pages, page, max_pages, _strides(dense and out_dense, q, out),
-            _strides(dense_cache, k_cache, v_cache), d ** -0.5 if scale is None else float(scale), bool(causal),
+            H_kv, T_q, d, num_pages, page, max_pages, None if dense and out_dense else _strides(False, q, out),
+            None if dense_cache else _strides(False, k_cache, v_cache), d ** -0.5 if scale is None else scale, causal,
             ws_ptr, ws_bytes, _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_fwd_paged")
