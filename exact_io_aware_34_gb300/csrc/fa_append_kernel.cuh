@@ -19,7 +19,7 @@
 // way to cut T tokens into pages: with T <= T / page + 2 B one place per token, of
 // which those work that begin a page or a sequence (a decode step: all of them);
 // else sequence b has the places from cu[b] / page + 2 b on, at least as many as it
-// touches pages. Behind them stand the CTAs that rotate queries (fa_rope_kernel's rows).
+// touches pages. Between them stand the CTAs that rotate queries (fa_rope_kernel's rows).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -55,6 +55,7 @@ struct AppendParams {
   int places;
   int warps;                       // of a head: 1, 2, 4 or 8
   int head_groups;                 // CTAs of a place, each with 8 / warps heads
+  int query_ctas, period;
   float factor;
 };
 
@@ -150,25 +151,37 @@ struct AppendRows {
     }
   }
 
-  // To rows row0 .. of a page at `out`.
-  __device__ __forceinline__ void store(const AppendParams& p, int which, uint8_t* out, int rows, float scale) const {
+  // In units of the scale. (One that other code left here need not be a power of two.)
+  __device__ __forceinline__ void divide(float scale) {
+    if ((__float_as_uint(scale) & 0x7fffffu) == 0u) {
+      const float inv = 1.f / scale;
+#pragma unroll
+      for (int k = 0; k < kItems; ++k)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[k][e] *= inv;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kItems; ++k)
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if ((e >> 2) == q) x[k][e] /= scale;
+    }
+  }
+
+  // To the page's rows from `out` on.
+  __device__ __forceinline__ void store(const AppendParams& p, int which, uint8_t* out, int rows) const {
     const int lane = threadIdx.x & 31, row0 = lane / kPerRow, i = lane % kPerRow;
     const RopeItem it = rope_item(i, which == 0 ? p.rot : 0, p.interleaved != 0);
-    // (A scale that other code left here need not be a power of two.)
-    const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0u;
-    const float inv = 1.f / scale;
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
       const int r = row0 + k * kRowStep;
       if (r >= rows) break;
       uint32_t c[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float y[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) y[f] = exact ? x[k][4 * e + f] * inv : x[k][4 * e + f] / scale;
-        c[e] = to_e4m3x2(y[0], y[1]) | to_e4m3x2(y[2], y[3]) << 16;
-      }
+      for (int e = 0; e < 4; ++e)
+        c[e] = to_e4m3x2(x[k][4 * e], x[k][4 * e + 1]) | to_e4m3x2(x[k][4 * e + 2], x[k][4 * e + 3]) << 16;
       uint8_t* dst = out + r * p.c_row[which];
       *reinterpret_cast<uint2*>(dst + it.c0) = make_uint2(c[0], c[1]);
       *reinterpret_cast<uint2*>(dst + it.c1) = make_uint2(c[2], c[3]);
@@ -184,11 +197,16 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
   __shared__ float warp_max[8];
   ptx::grid_wait();
   ptx::grid_next();
-  const int half = p.rot / 2, kv_ctas = p.places * p.head_groups * 2;
+  const int half = p.rot / 2;
+  // Query CTAs wait for memory, the others mostly compute: every p.period-th CTA is a query CTA while there are any.
+  int cta = static_cast<int>(blockIdx.x);
+  const int turn_of = (cta + 1) / p.period;        // query CTAs up to this one
+  const bool query = turn_of * p.period == cta + 1 && turn_of <= p.query_ctas;
+  cta = query ? turn_of - 1 : cta - min(turn_of, p.query_ctas);
 
-  if (static_cast<int>(blockIdx.x) >= kv_ctas) {
+  if (query) {
     // ------------------------------------------------------------ queries
-    const int t0 = (static_cast<int>(blockIdx.x) - kv_ctas) * p.q.tokens, n = min(p.q.tokens, p.T - t0);
+    const int t0 = cta * p.q.tokens, n = min(p.q.tokens, p.T - t0);
     rope_rows<kThreads>(p.q, t0, n, cs, skip, [&] {
       if (threadIdx.x < kRopeMaxTokens) skip[threadIdx.x] = 1;
       __syncthreads();
@@ -213,9 +231,9 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
   }
 
   // -------------------------------------------------------------- keys, values
-  const int which = static_cast<int>(blockIdx.x) & 1, u = static_cast<int>(blockIdx.x) >> 1;
+  const int which = cta & 1, u = cta >> 1;
   const int place = p.head_groups == 1 ? u : u / p.head_groups, group = u - place * p.head_groups;
-  const bool check = blockIdx.x == 0;
+  const bool check = cta == 0;
   // A decode step's token t is sequence t's; else all threads look for the place's sequence.
   int b = -1, c0 = 0, c1 = 0, len = 0;
   if (p.per_token && place < p.B) {
@@ -295,7 +313,10 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
         x.load(p, cs + r * half, which, head, t0 + r, min(16, rows - r));
         amax = fmaxf(amax, x.amax);
       }
-      if (pass == 1) x.store(p, which, out + (row0 + r) * p.c_row[which], min(16, rows - r), scale);
+      if (pass == 1) {
+        x.divide(scale);
+        x.store(p, which, out + (row0 + r) * p.c_row[which], min(16, rows - r));
+      }
     }
     if (pass == 1) break;
 #pragma unroll

@@ -270,8 +270,10 @@ fa_status_t append_impl(const void* K, const void* V, const int* cu_new, void* K
   p.places = static_cast<int>(std::min<long long>(T, by_page));
   p.warps = p.per_token ? 1 : page / 16;
   p.head_groups = (H_kv * p.warps + 7) / 8;
-  const long long ctas = 2LL * p.places * p.head_groups + (Q ? (T + p.q.tokens - 1) / p.q.tokens : 0);
+  p.query_ctas = Q ? (T + p.q.tokens - 1) / p.q.tokens : 0;
+  const long long kv_ctas = 2LL * p.places * p.head_groups, ctas = kv_ctas + p.query_ctas;
   if (ctas >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  p.period = p.query_ctas ? static_cast<int>(kv_ctas / p.query_ctas) + 1 : 1;
   const void* kernel = d == 64 ? reinterpret_cast<const void*>(&fa::fa_append_kernel<64>)
                                : reinterpret_cast<const void*>(&fa::fa_append_kernel<128>);
   // The angles of a page's rows; of a query CTA's tokens.
