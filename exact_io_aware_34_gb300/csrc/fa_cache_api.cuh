@@ -320,10 +320,12 @@ bool make_page_map(CUtensorMap* m, const Pages& c) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a unit: 4, 8 or 16 while the sequences' new tokens, on average, fill no
-// more (fa_paged_kernel), else 256 (fa_paged_wide_kernel).
+// Rows of a unit: 4 or 8 while the sequences' new tokens, on average, fill no more
+// (fa_paged_kernel), else 256 (fa_paged_wide_kernel). A variant with 16 rows, which
+// needs two products for hi and lo, took 74 us for four long caches with 16 rows,
+// fa_paged_wide_kernel 48; with 8 rows it takes 80, fa_paged_kernel 46.
 int paged_rows(int B, int G, int T_q) {
-  for (int n : {4, 8, 16})
+  for (int n : {4, 8})
     if (static_cast<long long>(T_q) * G <= static_cast<long long>(n) * B) return n;
   return 256;
 }
@@ -343,7 +345,7 @@ fa::PagedShape paged_shape(int B, int H, int H_kv, int T_q, int num_pages, int p
   s.page_shift = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
   s.max_pages = max_pages;
   s.causal = causal;
-  s.cost = N > 16 ? fa::kWideCost : fa::kPagedCost;
+  s.cost = N > 8 ? fa::kWideCost : fa::kPagedCost;
   return s;
 }
 
@@ -354,7 +356,7 @@ long long paged_places(const fa::PagedShape& s) {
   return places < 2147418112.0 ? static_cast<long long>(places) : 0;
 }
 int paged_ctas(const fa::PagedShape& s, int N) {
-  return static_cast<int>(std::min(paged_places(s), (N > 16 ? 1LL : 2LL) * cached_sm_count()));
+  return static_cast<int>(std::min(paged_places(s), (N > 8 ? 1LL : 2LL) * cached_sm_count()));
 }
 
 struct PagedLayout {
@@ -378,7 +380,7 @@ struct PagedKernel {
 
 template <int HD, int N, int NG>
 const PagedKernel& paged_kernel() {
-  if constexpr (N <= 16) {
+  if constexpr (N <= 8) {
     using C = fa::PagedCfg<HD, N>;
     static const PagedKernel k{reinterpret_cast<const void*>(&fa::fa_paged_kernel<HD, N>),
                                reinterpret_cast<const void*>(&fa::paged_merge_kernel<HD, N>), C::kSmemBytes, C::kThreads, 0};
@@ -427,7 +429,6 @@ fa_status_t paged_launch_rows(int N, const Pages& kc, const Pages& vc, fa::Paged
   switch (N) {
     case 4: return paged_launch<HD, 4>(kc, vc, p, stream);
     case 8: return paged_launch<HD, 8>(kc, vc, p, stream);
-    case 16: return paged_launch<HD, 16>(kc, vc, p, stream);
     default:
       return p.s.page_shift >= 6 ? paged_launch<HD, 256, 2>(kc, vc, p, stream)
                                  : paged_launch<HD, 256, 8>(kc, vc, p, stream);
@@ -489,7 +490,7 @@ fa_status_t paged_impl(const void* Q, const void* K_cache, const void* V_cache, 
   p.split = reinterpret_cast<fa::PagedSplit*>(ws);
   p.Lp = reinterpret_cast<float*>(ws + w.Lp);
   p.Op = reinterpret_cast<float*>(ws + w.Op);
-  p.scale_log2 = N > 16 ? masked_scale_log2(scale) : static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  p.scale_log2 = N > 8 ? masked_scale_log2(scale) : static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.negate = scale < 0.f;
   p.keep = p.s.ht > 1 || T_q > static_cast<long long>(B) * p.s.tp;
   p.timeout_ns = timeout_ns;

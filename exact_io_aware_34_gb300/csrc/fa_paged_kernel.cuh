@@ -6,8 +6,8 @@
 // 8-bit operands on both sides. K and V go from memory to the tensor core as
 // they are stored; no thread converts them. The other operand, a bf16 query row
 // or a row of probabilities, enters as the sum of two e4m3 numbers, its first
-// four significant bits and the rest to four more (hi, lo): the products
-// K (q_hi + q_lo) and V (p_hi + p_lo) accumulate in the same place. bf16 has
+// four significant bits and the rest to four more (hi, lo), side by side among the
+// 16 rows of the products; the reader adds the two halves of S and of O. bf16 has
 // eight significant bits: a query row, scaled by a power of two so that its
 // largest element lies in [128, 256), is exact but for elements below 2^-9 of
 // that (off by 2^-17 of it at most). A probability is cut to four bits and its
@@ -35,7 +35,7 @@
 // P carries it, and is taken out of the sum of weights again.
 //
 // Work: see fa_paged_common.cuh. Rows of a unit are consecutive tokens x the heads of a
-// group, row = token * heads + head; N (4, 8 or 16) bounds them. One stream of
+// group, row = token * heads + head; N (4 or 8) bounds them. One stream of
 // tiles runs through a CTA's units: the next unit's S is computed and its
 // first P written before the last O^T of a unit is added and its rows stored.
 //
@@ -50,15 +50,8 @@ namespace fa {
 namespace ptx {
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 4) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(taddr));
-  } else if constexpr (N == 8) {
-    tmem_ld8(taddr, r);
-  } else {
-    tmem_ld16(taddr, r);
-  }
+  if constexpr (N == 8) tmem_ld8(taddr, r);
+  else tmem_ld16(taddr, r);
 }
 template <int N>
 __device__ __forceinline__ void reg_fence(uint32_t (&r)[N]) {
@@ -75,18 +68,13 @@ struct PagedCfg {
   static constexpr int kStages = HD == 128 ? 3 : 5;    // pairs of tiles
   static constexpr int kTiles = 2 * kStages;
   static constexpr int kTileBytes = 128 * HD;          // K or V
-  // With N <= 8 the hi and lo of a row stand side by side among the 16: one
-  // product instead of two, the sums of both halves are added by the reader.
-  static constexpr bool kPair = N <= 8;
-  static constexpr int kParts = kPair ? 1 : 2;         // products
-  static constexpr int kCols = kPair ? 2 * N : N;      // columns of S and O^T that are read
-  static constexpr int kPBytes = kRows * 128;          // of a product
+  static constexpr int kCols = 2 * N;                  // columns of S and O^T that are read: hi, lo
+  static constexpr int kPBytes = kRows * 128;
   static constexpr int kQBytes = kRows * HD;
-  static constexpr int kQBufs = kPair ? 2 : 1;         // units whose query rows are held (shared memory)
   // With d = 64 the M side of V^T P^T is V's 64 columns and 64 lanes that nobody
   // reads, fed from the 8 KB behind the tile: the last one has a pad.
   static constexpr int kPad = HD == 64 ? kTileBytes : 0;
-  static constexpr int kSmemBytes = 2 * kParts * kPBytes + kQBufs * kParts * kQBytes + kStages * 2 * kTileBytes + kPad + 1024;
+  static constexpr int kSmemBytes = 2 * kPBytes + 2 * kQBytes + kStages * 2 * kTileBytes + kPad + 1024;
   static constexpr uint32_t kTmemCols = 256;
   static constexpr uint32_t kColS = 0;                 // two buffers
   static constexpr uint32_t kColO = 2 * kRows;         // two buffers x four warps
@@ -117,14 +105,14 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
   __shared__ __align__(16) PagedJob jobs[kJobs];
   __shared__ __align__(16) float page_scale[C::kStages][2][8];   // K, V scales of a tile's pages
   // By unit (modulo 4: written two units ahead of a reader) and row: the scores' scale over the query row's, keys seen.
-  __shared__ __align__(16) float row_scale[4][16];
-  __shared__ __align__(16) int row_lim[4][16];
+  __shared__ __align__(16) float row_scale[4][N];
+  __shared__ __align__(16) int row_lim[4][N];
   // By tile (modulo 4: a warp may be three tiles behind the first to write), warp and row: the maximum - kPagedTop.
   __shared__ __align__(16) float warp_max[4][4][N];
   __shared__ float warp_top[4][4];                      // the larger V scale of the warp's pages
   __shared__ __align__(16) float factor[4][4][N];       // by reading warp: what the four O^T are multiplied by
   __shared__ __align__(16) float corr[4][N];
-  __shared__ float sums[4][4][2][16];                   // by unit (modulo 4) and warp: sums of weights, what they are relative to
+  __shared__ float sums[4][4][2][N];                    // by unit (modulo 4) and warp: sums of weights, what they are relative to
   __shared__ PagedLine line;
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
@@ -133,10 +121,8 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
   const PagedShape& sh = p.s;
   const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* generic = smem_raw + (smem_base - ptx::smem_u32(smem_raw));
-  const uint32_t sP = smem_base, sQ = sP + 2 * C::kParts * C::kPBytes,
-                 sKV = sQ + C::kQBufs * C::kParts * C::kQBytes;
-  static_assert((2 * C::kParts * C::kPBytes) % 1024 == 0 && (C::kQBufs * C::kParts * C::kQBytes) % 1024 == 0 &&
-                    C::kQBytes % 1024 == 0, "tiles begin on swizzle atoms");
+  const uint32_t sP = smem_base, sQ = sP + 2 * C::kPBytes, sKV = sQ + 2 * C::kQBytes;
+  static_assert((2 * C::kPBytes) % 1024 == 0 && C::kQBytes % 1024 == 0, "tiles begin on swizzle atoms");
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kTiles; ++s) {
@@ -170,7 +156,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
   // (Rows that hold no query are multiplied, too; their results are not used. Of
   // pages above 16 rows only the first scales are ever written.)
   if (warp == 6) {
-    for (int i = lane; i < C::kQBufs * C::kParts * C::kQBytes / 16; i += 32)
+    for (int i = lane; i < 2 * C::kQBytes / 16; i += 32)
       reinterpret_cast<uint4*>(generic + (sQ - smem_base))[i] = make_uint4(0u, 0u, 0u, 0u);
     for (int i = lane; i < C::kStages * 16; i += 32) (&page_scale[0][0][0])[i] = 0.f;
   }
@@ -203,16 +189,11 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
       // (Every warp has written its maxima when the tile's P is complete.)
       if (!wait_warp_or_abort(ptx::smem_u32(&bar_p_full[buf]), (t >> 1) & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax))
         return false;
-      // Lane l has (warp, row) = l / N, l % N (and 32 more with N = 16).
-      constexpr int kTwice = N == 16 ? 2 : 1;
-      float m[kTwice], top = -INFINITY;
+      // Lane l has (warp, row) = l / N, l % N.
+      const float m = (&warp_max[t & 3][0][0])[min(lane, 4 * N - 1)];
+      float top = m;
 #pragma unroll
-      for (int k = 0; k < kTwice; ++k) {
-        m[k] = (&warp_max[t & 3][0][0])[min(lane + 32 * k, 4 * N - 1)];
-        top = ptx::max_nan(top, m[k]);
-      }
-#pragma unroll
-      for (int o = N; o < (N == 4 ? 16 : 32); o <<= 1) top = ptx::max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = N; o < 4 * N; o <<= 1) top = ptx::max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
       const bool jump = top != -INFINITY && !(top - ref <= kPagedJump);   // (also the first tile with keys, and NaN)
       if (__any_sync(0xffffffffu, jump)) {
         if (lane < N) corr[warp][lane] = jump ? ptx::ex2_approx(ref - top) : 1.f;
@@ -221,17 +202,13 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] *= corr[warp][i];
       }
-#pragma unroll
-      for (int k = 0; k < kTwice; ++k) {
-        const int at = lane + 32 * k;
-        if (at < 4 * N)
-          (&factor[warp][0][0])[at] = m[k] == -INFINITY ? 0.f : ptx::ex2_approx(m[k] - ref) * warp_top[t & 3][at / N];
-      }
+      if (lane < 4 * N)
+        (&factor[warp][0][0])[lane] = m == -INFINITY ? 0.f : ptx::ex2_approx(m - ref) * warp_top[t & 3][lane / N];
       __syncwarp();
       if (!wait_warp_or_abort(ptx::smem_u32(&bar_o_full[buf]), (t >> 1) & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax))
         return false;
       ptx::tc_fence_after();
-      constexpr int kAtOnce = 16 / C::kCols >= 2 ? 4 : N == 8 ? 2 : 1;   // (registers)
+      constexpr int kAtOnce = N == 8 ? 2 : 4;        // (registers)
 #pragma unroll
       for (int w0 = 0; w0 < 4; w0 += kAtOnce) {
         uint32_t o[kAtOnce][C::kCols];
@@ -243,7 +220,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
           ptx::reg_fence<C::kCols>(o[w]);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const float sum = __uint_as_float(o[w][i]) + (C::kPair ? __uint_as_float(o[w][C::kCols - N + i]) : 0.f);
+            const float sum = __uint_as_float(o[w][i]) + __uint_as_float(o[w][N + i]);
             acc[i] = fmaf(sum, factor[warp][w0 + w][i], acc[i]);
           }
         }
@@ -347,7 +324,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
         float x[N], m[N];
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          x[i] = fmaf(__uint_as_float(s[i]) + (C::kPair ? __uint_as_float(s[C::kCols - N + i]) : 0.f), row_scale[n & 3][i] * k_sc, v_log);
+          x[i] = fmaf(__uint_as_float(s[i]) + __uint_as_float(s[N + i]), row_scale[n & 3][i] * k_sc, v_log);
         if ((j + 1) * 128 > all_see) {
 #pragma unroll
           for (int i = 0; i < N; ++i)
@@ -361,7 +338,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
             *reinterpret_cast<float4*>(&warp_max[g & 3][warp][i]) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
           warp_top[g & 3][warp] = v_top;
         }
-        uint32_t hi4[4] = {0u, 0u, 0u, 0u}, lo4[4] = {0u, 0u, 0u, 0u};
+        uint32_t hi4[N / 4], lo4[N / 4];
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
           float w[4], h[4];
@@ -381,15 +358,8 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
           lo4[i / 4] = to_e4m3x2(w[0] - h[0], w[1] - h[1]) | to_e4m3x2(w[2] - h[2], w[3] - h[3]) << 16;
         }
         // [key][16 bytes]: N-major without swizzle
-        uint8_t* to = generic + buf * C::kParts * C::kPBytes + tid * 16;
-        if constexpr (N == 4) {
-          *reinterpret_cast<uint4*>(to) = make_uint4(hi4[0], lo4[0], 0u, 0u);
-        } else if constexpr (N == 8) {
-          *reinterpret_cast<uint4*>(to) = make_uint4(hi4[0], hi4[1], lo4[0], lo4[1]);
-        } else {
-          *reinterpret_cast<uint4*>(to) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-          *reinterpret_cast<uint4*>(to + C::kPBytes) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
-        }
+        *reinterpret_cast<uint4*>(generic + buf * C::kPBytes + tid * 16) =
+            N == 4 ? make_uint4(hi4[0], lo4[0], 0u, 0u) : make_uint4(hi4[0], hi4[N / 4 - 1], lo4[0], lo4[N / 4 - 1]);
         // V rows behind the unit's keys may hold anything, and a weight of zero does not cancel a NaN.
         if (key >= job.n_keys) {
           uint4* row = reinterpret_cast<uint4*>(generic + (sKV - smem_base) + (2 * stage + 1) * C::kTileBytes + tid * HD);
@@ -457,18 +427,15 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
         return false;
       ptx::tc_fence_after();
       const uint64_t dk = ptx::desc_of(sKV + 2 * stage * C::kTileBytes, 16, C::kAtom, C::kSwizzle);
-      const uint64_t dq = ptx::desc_of(sQ + n % C::kQBufs * C::kParts * C::kQBytes, 16, C::kAtom, C::kSwizzle);
+      const uint64_t dq = ptx::desc_of(sQ + (n & 1) * C::kQBytes, 16, C::kAtom, C::kSwizzle);
 #pragma unroll
-      for (int part = 0; part < C::kParts; ++part)
-#pragma unroll
-        for (int k = 0; k < HD / 32; ++k)
-          ptx::mma_f8_warp(tmem_base + C::kColS + (gq & 1) * C::kRows, ptx::desc_lo(dk) + 2 * k, ptx::desc_hi(dk),
-                           ptx::desc_lo(dq) + part * (C::kQBytes >> 4) + 2 * k, ptx::desc_hi(dq), idesc_qk,
-                           part + k > 0 ? 1u : 0u);
+      for (int k = 0; k < HD / 32; ++k)
+        ptx::mma_f8_warp(tmem_base + C::kColS + (gq & 1) * C::kRows, ptx::desc_lo(dk) + 2 * k, ptx::desc_hi(dk),
+                         ptx::desc_lo(dq) + 2 * k, ptx::desc_hi(dq), idesc_qk, k > 0 ? 1u : 0u);
       ptx::mma_commit_warp(ptx::smem_u32(&bar_s_full[gq & 1]));
       ptx::mma_commit_warp(ptx::smem_u32(&bar_empty[2 * stage]));
       ++gq;
-      if (--left == 0) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[n % C::kQBufs]));
+      if (--left == 0) ptx::mma_commit_warp(ptx::smem_u32(&bar_q_empty[n & 1]));
       return true;
     };
     ok = qk();
@@ -479,14 +446,11 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
       if (!ok) break;
       ptx::tc_fence_after();
       const uint64_t dv = ptx::desc_of(sKV + (2 * stage + 1) * C::kTileBytes, C::kTileBytes, C::kAtom, C::kSwizzle);
-      const uint64_t dp = ptx::desc_of(sP + buf * C::kParts * C::kPBytes, 128, 2048, 0);
+      const uint64_t dp = ptx::desc_of(sP + buf * C::kPBytes, 128, 2048, 0);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int part = 0; part < C::kParts; ++part)
-          ptx::mma_f8_warp(tmem_base + C::kColO + (buf * 4 + k) * C::kRows, ptx::desc_lo(dv) + k * (32 * HD >> 4),
-                           ptx::desc_hi(dv), ptx::desc_lo(dp) + part * (C::kPBytes >> 4) + k * 32, ptx::desc_hi(dp),
-                           idesc_pv, part > 0 ? 1u : 0u);
+        ptx::mma_f8_warp(tmem_base + C::kColO + (buf * 4 + k) * C::kRows, ptx::desc_lo(dv) + k * (32 * HD >> 4),
+                         ptx::desc_hi(dv), ptx::desc_lo(dp) + k * 32, ptx::desc_hi(dp), idesc_pv, 0u);
       ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[buf]));
       ptx::mma_commit_warp(ptx::smem_u32(&bar_empty[2 * stage + 1]));
       if (more) ok = qk();
@@ -523,10 +487,10 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
         }
       }
       // The unit before the last has read its rows.
-      if (!wait_warp_or_abort(ptx::smem_u32(&bar_q_empty[n % C::kQBufs]), ((n / C::kQBufs) & 1) ^ 1u, abort_ptr,
+      if (!wait_warp_or_abort(ptx::smem_u32(&bar_q_empty[n & 1]), ((n >> 1) & 1) ^ 1u, abort_ptr,
                               kUnitWaits * p.timeout_ns, kRolePagedQuery))
         break;
-      uint8_t* to = generic + (sQ - smem_base) + n % C::kQBufs * C::kParts * C::kQBytes;
+      uint8_t* to = generic + (sQ - smem_base) + (n & 1) * C::kQBytes;
 #pragma unroll
       for (int k = 0; k < kPasses; ++k) {
         const int r = k * kPass + lane / kLanes;
@@ -562,8 +526,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
             return static_cast<uint32_t>(row) * HD + ((part ^ (HD == 128 ? row & 7 : (row >> 1) & 3)) << 4);
           };
           *reinterpret_cast<uint4*>(to + at(r)) = make_uint4(hi4[0], hi4[1], hi4[2], hi4[3]);
-          *reinterpret_cast<uint4*>(to + (C::kPair ? at(N + r) : C::kQBytes + at(r))) =
-              make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
+          *reinterpret_cast<uint4*>(to + at(N + r)) = make_uint4(lo4[0], lo4[1], lo4[2], lo4[3]);
           if (part == 0) {
             row_scale[n & 3][r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
             row_lim[n & 3][r] = r >= job.rows ? 0 : min(job.n_keys, sh.causal ? job.lim0 + r / job.heads : job.lim0);
