@@ -193,7 +193,7 @@ template <int HD>
 __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendParams p) {
   constexpr int kThreads = kAppendThreads;
   extern __shared__ __align__(16) float2 cs[];
-  __shared__ int found[4], at[kRopeMaxTokens], skip[kRopeMaxTokens];
+  __shared__ int found, at[kRopeMaxTokens], skip[kRopeMaxTokens];
   __shared__ float warp_max[8];
   ptx::grid_wait();
   ptx::grid_next();
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
     }
   }
   if (b < 0 || check) {            // (the same in all threads)
-    if (threadIdx.x == 0) found[0] = -1;
+    if (threadIdx.x == 0) found = -1;
     __syncthreads();
     for (int s = threadIdx.x; s < p.B; s += kThreads) {
       const int s0 = p.cu[s], s1 = p.cu[s + 1];
@@ -256,17 +256,16 @@ __global__ void __launch_bounds__(kAppendThreads) fa_append_kernel(const AppendP
       if (!append_fits(p, s0, s1, n)) {
         append_bad(s);
       } else if (mine) {
-        found[0] = s;
-        found[1] = s0;
-        found[2] = s1;
-        found[3] = n;
+        atomicMax(&found, s);      // (offsets that decrease in between may give a place to several)
       }
     }
     __syncthreads();
-    b = found[0];
-    c0 = found[1];
-    c1 = found[2];
-    len = found[3];
+    b = found;
+    if (b >= 0) {
+      c0 = p.cu[b];
+      c1 = p.cu[b + 1];
+      len = p.lens[b];
+    }
   }
   if (b < 0) return;
   const int before = len - (c1 - c0);

@@ -252,6 +252,25 @@ def test_offsets_and_lengths_that_do_not_fit_are_reported(cu, lens):
             assert i in touched or np.array_equal(x[i], y[i], equal_nan=True)
 
 
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("cu,lens", [([0, 60, 20, 80], [70, 30, 64]), ([0, 6, 2, 8, 8], [6, 30, 77, 9]), ([0, 300, 10, 310], [300, 1, 301])])
+def test_offsets_that_decrease_in_between(cu, lens, page):
+    """Rows that two sequences claim: one of them gets each, whole, and nobody else's pages change."""
+    cache = Cache(23, lens, 2, page, 64)
+    k, = draw(12, (cu[-1], 2, 64))
+    before = cache.host()
+    for _ in range(5):
+        fa.fa_kv_append(k.cuda(), k.cuda(), i32(cu), *cache.device(), q=k.cuda(), inv_freq=fa.fa_rope_frequencies(64, device="cuda"))
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status()[0] == fa.FA_ERR_INVALID_ARG
+    ok()
+    fit = [b for b in range(len(lens)) if cu[b] <= cu[b + 1]]
+    mine = {int(i) for b in fit for i in cache.table[b] if i >= 0}
+    for x, y in zip(before, cache.host()):
+        for i in set(range(cache.n)) - mine:
+            assert np.array_equal(x[i], y[i], equal_nan=True)
+
+
 @pytest.mark.parametrize("bad", [-1, 10 ** 6, -2 ** 31, 2 ** 31 - 1])
 def test_pages_that_do_not_exist_are_left_out_and_reported(bad):
     cache = Cache(19, [30, 30], 2, 16, 64)
@@ -267,6 +286,29 @@ def test_pages_that_do_not_exist_are_left_out_and_reported(bad):
     assert np.array_equal(before[0][i], after[0][i])
     j = int(cache.table[1, 1])
     assert not np.array_equal(before[0][j], after[0][j])
+
+
+def test_side_stream():
+    caches = [Cache(24, [400, 90], 2, 32, 128) for _ in range(2)]
+    k, v, q = (t.cuda() for t in draw(13, (301, 2, 128), (301, 2, 128), (301, 4, 128)))
+    f, cu = fa.fa_rope_frequencies(128, device="cuda"), i32([0, 300, 301])
+    side, dev = torch.cuda.Stream(), [c.device() for c in caches]
+    torch.cuda.synchronize()
+    got = fa.fa_kv_append(k, v, cu, *dev[0], q=q, inv_freq=f, stream=side)
+    side.synchronize()
+    want = fa.fa_kv_append(k, v, cu, *dev[1], q=q, inv_freq=f)
+    ok()
+    assert torch.equal(got, want)
+    for x, y in zip(*(c.host() for c in caches)):
+        assert np.array_equal(x, y, equal_nan=True)
+
+
+def test_one_page():
+    """A cache of a single page and head, of every size."""
+    for page in (16, 32, 64, 128):
+        for d in (64, 128):
+            cache = Cache(25, [page], 1, page, d, spare=0, extra=0)
+            check(cache, [page // 2 + 1], 1, 1, d, rot=d)
 
 
 def test_graph_replay_with_other_lengths():
