@@ -861,7 +861,7 @@ def fa_rope(x, positions, inv_freq, y=None, out=None, out_y=None, interleaved: b
             strides = _strides(False, x, o) if y is None else _strides(False, x, o, y, oy)
         st = (_lib or load_library()).fa_rope(
             x.data_ptr(), o.data_ptr(), heads, y_ptr, oy_ptr, heads_y, positions.data_ptr(), inv_freq.data_ptr(), T, d,
-            rot, strides, interleaved, transpose, factor, _raw_stream(device))
+            rot, strides, bool(interleaved), bool(transpose), float(factor), _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_rope")
         return o if y is None else (o, oy)
@@ -963,7 +963,7 @@ def fa_kv_append(k, v, cu_new, k_cache, v_cache, k_scale, v_scale, page_table, s
             v_scale.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), q_ptr, o_ptr,
             inv_freq.data_ptr() if rot else None, None if positions is None else positions.data_ptr(), B, H, H_kv, T, d,
             num_pages, page, max_pages, rot, strides, None if dense_cache else _strides(False, k_cache, v_cache),
-            interleaved, factor, _raw_stream(device))
+            bool(interleaved), float(factor), _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_kv_append")
         return o if turn else q
@@ -1009,8 +1009,8 @@ def fa_fwd_paged(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             page_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), out.data_ptr(), out_lse.data_ptr(), B, H,
             H_kv, T_q, d, num_pages, page, max_pages, None if dense and out_dense else _strides(False, q, out),
-            None if dense_cache else _strides(False, k_cache, v_cache), d ** -0.5 if scale is None else scale, causal,
-            ws_ptr, ws_bytes, _raw_stream(device))
+            None if dense_cache else _strides(False, k_cache, v_cache), d ** -0.5 if scale is None else float(scale),
+            bool(causal), ws_ptr, ws_bytes, _raw_stream(device))
         if st != FA_OK:
             raise FaError(st, "fa_fwd_paged")
         return out, out_lse

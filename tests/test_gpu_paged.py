@@ -1,10 +1,11 @@
 """fa_fwd_paged against the float64 oracle, through the C ABI (needs a GB300).
 
-Tolerances, from the arithmetic. A weight enters P V as two e4m3 numbers: the
-first four significant bits and the rest to four more, off by at most 2^-8 of
-itself, or where it is small by 2^-17 of its 128-key tile's largest product of
-probability and scale; O is rounded once. So |O - ref| <= 2^-8 (A + |ref|) +
-2^-17 F, with A = P |V| and F as the oracle returns them, and float32 sums and
+Tolerances, from the arithmetic. With few rows a weight enters P V as two e4m3
+numbers: the first four significant bits and the rest to four more, off by at
+most 2^-8 of itself, or where it is small by 2^-17 of the largest product of
+probability and scale among its 32 keys. With many it enters as f16: off by 2^-12 of
+itself, or by 2^-31 of its row's largest. O is rounded once. So |O - ref| <=
+2^-8 (A + |ref|) + 2^-17 F, with A = P |V| and F as the oracle returns them, and float32 sums and
 exponentials add a few 2^-22 of A. A query element is exact as two e4m3 numbers unless it
 is below 2^-9 of its row's largest, and then off by at most 2^-17 of that: a
 score is off by that times the sum of |k|, and by d 2^-24 scale |q|.|k| for its
@@ -120,6 +121,39 @@ def test_long_caches(d):
 def test_many_sequences():
     lens = np.random.default_rng(3).integers(0, 200, 700)
     check(Cache(32, lens, 2, 16, 64), [1] * 700, 4, 64)
+
+
+def test_many_sequences_with_pieces():
+    """More sequences than one warp adds up, some with a piece of a prompt."""
+    r = np.random.default_rng(4)
+    lens, new = r.integers(0, 300, 400), np.where(r.random(400) < 0.2, r.integers(0, 90, 400), 1)
+    check(Cache(38, lens, 2, 64, 64), new.tolist(), 8, 64)
+
+
+@pytest.mark.parametrize("new", [1, 5, 16])
+def test_one_page(new):
+    """A cache of a single page and head, of every size."""
+    for page in (16, 32, 64, 128):
+        for d in (64, 128):
+            check(Cache(39, [page], 1, page, d, spare=0, extra=0), [new], 2, d)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_offsets_that_decrease_in_between(rows):
+    """Rows that two sequences claim get one result or the other's; those of one alone get theirs."""
+    lens, n = [900, 30, 500], 4 * rows
+    cache = Cache(36, lens, 2, 32, 64)
+    q = draw(16, (n, 4, 64))[0].cuda()
+    cu = [0, 3 * rows, 2 * rows, n]
+    o, lse = fa.fa_fwd_paged(q, *cache.device(), i32(cu))
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status()[0] == fa.FA_ERR_INVALID_ARG
+    ok()
+    one = [reference(cache, q, c, 0.125, True) for c in ([0, 3 * rows, 3 * rows, 3 * rows], [2 * rows, 2 * rows, 2 * rows, n])]
+    O, L, A, F = one[0]
+    check_o(o[:2 * rows], O[:2 * rows], A[:2 * rows], F[:2 * rows])
+    O, L, A, F = one[1]
+    check_o(o[3 * rows:], O[3 * rows:], A[3 * rows:], F[3 * rows:])
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.09, 2.0])
