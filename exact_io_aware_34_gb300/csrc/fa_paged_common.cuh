@@ -1,6 +1,16 @@
 // What the kernels of attention over a paged 8-bit cache share: the line of
 // units that equal CTAs cut up, its walk, the loads of pages, and the merge of
 // units that several CTAs worked on. See fa_paged_kernel.cuh.
+//
+// The line. A unit is a tile of query rows of one sequence and K/V head with all
+// the keys it sees. All units stand in a line by sequence, head and tile; each takes as
+// many places as it has 128-key tiles, and a few for what it costs beside
+// them. Every CTA takes an equal piece, whatever the lengths, so one long answer
+// among short ones is spread over the device. Causal tiles see ever more keys; their sum is one of floors of
+// a line, found in a logarithmic number of steps, so that a piece's first unit is
+// found without a list of units or a launch that writes one.
+// The merge is launched as a programmatic dependent of the main kernel and costs
+// 1.5 us of a call.
 #pragma once
 
 #include <climits>

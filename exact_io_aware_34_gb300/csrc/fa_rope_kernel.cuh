@@ -12,7 +12,9 @@
 // What bounds it: memory, one read and one write of every element. A CTA takes
 // about 40 KB of rows (a few tokens, all heads of both tensors); its angles are
 // computed once, into shared memory, for all heads, while the first rows are on
-// their way. A thread keeps its columns for all its rows.
+// their way. A thread keeps its columns for all its rows. Measured: 8192 tokens x 40 heads of 128 columns,
+// strided, 29.2 us, 5.7 TB/s (0.85 of a copy); 16001 tokens x 20 heads of 64
+// columns, half of them rotated, 17.7 us, 4.6 TB/s; 37 tokens 2.1 us, a launch.
 #pragma once
 
 #include <cuda_bf16.h>

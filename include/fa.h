@@ -608,7 +608,7 @@ fa_status_t fa_rope_frequencies(double* inv_freq, int rot, double base, int ramp
  *            strides); else outputs overlap no input nor each other. Slices of one
  *            projection's output may be given (their places are told apart).
  *   positions : device, int32 [T], of any sign: angles are exact modulo one turn.
- *   inv_freq : device, float64 [rot / 2], radians per position.
+ *   inv_freq : device, float64 [rot / 2], radians per position, finite.
  *   rot    : a multiple of 16, at most d; the columns behind are copied.
  *   strides : NULL for contiguous tensors, else entries (host) for X, X_out, Y
  *            and Y_out: positive multiples of 8 elements.
@@ -700,9 +700,16 @@ size_t fa_fwd_paged_workspace_bytes(int B, int H, int H_kv, int T_q, int d, int 
  *            streams, graph replays) need workspaces of their own.
  * A row that sees no key gets O = 0 and LSE = -inf. Rows of no sequence are not
  * written. Cache rows past a sequence's length are never part of a result,
- * whatever they hold. Offsets, lengths and tables are read on the device in
- * stream order; ones that do not fit are clamped or left out and reported by
- * fa_get_device_status as FA_ERR_INVALID_ARG.
+ * whatever they hold; with causal, a V row that is not finite can reach rows of its
+ * sequence that do not see it. Two launches, the second of which joins what
+ * several CTAs computed of a row. Where rows are divided depends on the lengths and
+ * the SM count; the same call gives the same bits. Queries and weights enter the
+ * 8-bit products as two numbers each (as if rounded to bf16, see the kernels).
+ * Offsets, lengths and tables are read on the device in stream order, and a captured
+ * call may be replayed with others; ones that do not fit are clamped (lengths), left
+ * out (offsets) or read as zeros (pages), and reported by fa_get_device_status as
+ * FA_ERR_INVALID_ARG. Where offsets decrease in between, rows that two sequences claim
+ * get either's result.
  * Limits: as for fa_kv_append, T_q * H below 2^31; scale finite; O and LSE overlap
  * nothing else that is given. FA_ERR_UNSUPPORTED for other d or page sizes and H / H_kv >
  * 128, FA_ERR_INVALID_ARG for the rest.
