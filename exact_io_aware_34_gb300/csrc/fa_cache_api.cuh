@@ -320,14 +320,16 @@ bool make_page_map(CUtensorMap* m, const Pages& c) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a unit: 4 or 8 while the sequences' new tokens, on average, fill no more
-// (fa_paged_kernel), else 256 (fa_paged_wide_kernel). A variant with 16 rows, which
-// needs two products for hi and lo, took 74 us for four long caches with 16 rows,
-// fa_paged_wide_kernel 48; with 8 rows it takes 80, fa_paged_kernel 46.
+// Rows of a unit: 4 or 8 (fa_paged_kernel) while the sequences' new tokens, on
+// average, fill no more than a unit of 4 or two of 8, else 256 (fa_paged_wide_kernel).
+// Two units read K and V twice, the second time mostly from L2: with 16 rows 24 caches of
+// 100 to 8000 keys take 49 us so and 65 in the other kernel, with four tokens of 24 drafts
+// at d = 64 20 and 26, four long caches 46 and 48. With 20 rows of 5 heads 39 and 35, with
+// 32 rows 68 and 53. (A variant with 16 rows in a unit, and hi and lo as two products,
+// took 74 us for the four long caches.)
 int paged_rows(int B, int G, int T_q) {
-  for (int n : {4, 8})
-    if (static_cast<long long>(T_q) * G <= static_cast<long long>(n) * B) return n;
-  return 256;
+  const long long rows = static_cast<long long>(T_q) * G;
+  return rows <= 4LL * B ? 4 : rows <= 16LL * B ? 8 : 256;
 }
 
 fa::PagedShape paged_shape(int B, int H, int H_kv, int T_q, int num_pages, int page, int max_pages, int causal) {
