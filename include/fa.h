@@ -711,8 +711,9 @@ size_t fa_fwd_paged_workspace_bytes(int B, int H, int H_kv, int T_q, int d, int 
  * FA_ERR_INVALID_ARG. Where offsets decrease in between, rows that two sequences claim
  * get either's result.
  * Limits: as for fa_kv_append, T_q * H below 2^31; scale finite; O and LSE overlap
- * nothing else that is given. FA_ERR_UNSUPPORTED for other d or page sizes and H / H_kv >
- * 128, FA_ERR_INVALID_ARG for the rest.
+ * nothing else that is given. FA_ERR_UNSUPPORTED for other d or page sizes, H / H_kv >
+ * 128 and more work than is counted in 32 bits (about (T_q + B) * H_kv * max_pages *
+ * page_size / 128 >= 2^31), FA_ERR_INVALID_ARG for the rest.
  */
 fa_status_t fa_fwd_paged(const void* Q, const void* K_cache, const void* V_cache, const float* k_scale,
                          const float* v_scale, const int* page_table, const int* seq_lens, const int* cu_q, void* O,
