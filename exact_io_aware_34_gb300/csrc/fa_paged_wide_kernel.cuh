@@ -273,11 +273,13 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
       float m_use = -INFINITY, l = 0.f, v_ref = 0.f, v_unit = 1.f;   // V scale that O is in units of, and its log2
       for (int jj = 0; jj < blocks; ++jj, ++g) {
         const int j = job.j0 + jj, pair = pair0 + jj;
-        // (V's slot is waited for because the scales come with it.)
-        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_slot_full[pair % C::kSlots]), (pair / C::kSlots) & 1, abort_ptr,
-                                p.timeout_ns, kRolePagedSoftmax);
+        // The scales come with V, so its slot is waited for, too, but behind S: the issuer has then seen every
+        // earlier tile in its slot. Before that, the barrier of a warpgroup that skipped units may be
+        // two phases behind, which its parity does not tell from done.
+        ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_s_full[t]), g & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax);
         if (ok)
-          ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_s_full[t]), g & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax);
+          ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_slot_full[pair % C::kSlots]), (pair / C::kSlots) & 1, abort_ptr,
+                                  p.timeout_ns, kRolePagedSoftmax);
         if (!ok) break;
         ptx::tc_fence_after();
         const int valid = seen - j * 128;

@@ -1,0 +1,48 @@
+"""fa_fwd_paged where sequences have many rows (pieces of prompts): the kernel with row tiles of 128, over
+the same masks, scales, layouts and calls that test_gpu_paged has for few rows, with its
+tolerances (needs a GB300). More than 16 rows (new tokens x heads of a group) per sequence on average
+take this kernel; pages of 64 rows and more one form of it, smaller ones the other.
+"""
+import numpy as np
+import pytest
+import torch
+
+from exact_io_aware_34_gb300 import fa
+from tests.test_gpu_append import Cache, i32, offsets
+from tests.test_gpu_paged import check
+from tests.test_gpu_varlen import draw, ok
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from exact_io_aware_34_gb300 import build
+    build.build()
+    fa.load_library()
+
+
+def unequal(cache, seed, octaves=6):
+    """Scales that differ from page to page, not powers of two."""
+    g = torch.Generator().manual_seed(seed)
+    for s in (cache.ks, cache.vs):
+        s.mul_(torch.exp2(torch.rand(s.shape, generator=g) * octaves - octaves).cuda())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 64])
+def test_units_of_one_row_tile_before_units_of_two(page, d):
+    """Many units of a CTA that leave its second row tile out, then one that has it: it reads its own pages'
+    scales. The same bits from run to run."""
+    new, lens = [], []
+    for i in range(360):
+        new.append(20 if i % 12 < 9 else 64)              # 80 rows, or 256
+        lens.append((40, 100, 128)[i % 3] if i % 12 < 9 else (64, 200, 333)[i % 3])
+    cache = Cache(page + d, lens, 2, page, d)
+    unequal(cache, 1)
+    a = check(cache, new, 8, d, seed=3)
+    q = draw(3, (sum(new), 8, d))[0].cuda()
+    for _ in range(10):
+        b = fa.fa_fwd_paged(q, *cache.device(), i32(offsets(new)))
+        ok()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
