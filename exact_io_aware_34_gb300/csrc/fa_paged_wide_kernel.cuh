@@ -438,20 +438,20 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
         if (job.slot >= 0) p.Lp[static_cast<size_t>(job.slot) * C::kRows + row] = lse;
         else p.lse[static_cast<long long>(head) * sh.T_q + token] = lse;
       }
+      __syncwarp();                          // (tensor memory is read by whole warps, rows are written by lanes that have one)
 #pragma unroll 1
       for (int c = 0; c < HD / 32; ++c) {
         uint32_t o[32];
         ptx::tmem_ld32(tO + 32 * c, o);
         ptx::tmem_ld_wait();
         ptx::reg_fence32(o);
-        if (!live) continue;
-        if (job.slot >= 0) {
+        if (live && job.slot >= 0) {
           float4* dst = reinterpret_cast<float4*>(p.Op + (static_cast<size_t>(job.slot) * C::kRows + row) * HD + 32 * c);
 #pragma unroll
           for (int v = 0; v < 8; ++v)
             dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
                                  __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
-        } else {
+        } else if (live) {
           uint4* dst = reinterpret_cast<uint4*>(p.o + token * p.o_t + head * p.o_h + 32 * c);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
             dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
+        __syncwarp();
       }
       ptx::tc_fence_before();
     }

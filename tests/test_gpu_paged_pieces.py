@@ -46,3 +46,20 @@ def test_units_of_one_row_tile_before_units_of_two(page, d):
         b = fa.fa_fwd_paged(q, *cache.device(), i32(offsets(new)))
         ok()
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("G", [1, 3, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_that_end_inside_a_warp(d, G):
+    """Units whose last rows hold no query, whole and in parts; what stands between the rows of O stays."""
+    new, lens = [17, 31, 33, 50, 64, 95, 100], [300, 31, 4000, 50, 1000, 777, 129]
+    cache, n, H = Cache(d + G, lens, 2, 32, d), sum(new), 2 * G
+    q = draw(G, (n, H, d))[0]
+    o, lse = check(cache, new, H, d, q=q)
+    wide, l2 = torch.full((H, n + 2, d + 8), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((H, n + 2), 5.0, device="cuda")
+    out = wide[:, :, :d].transpose(0, 1)
+    fa.fa_fwd_paged(torch.cat([q, q[:2]]).cuda(), *cache.device(), i32(offsets(new)), o=out, lse=l2)
+    ok()
+    assert torch.equal(out[:n], o) and torch.equal(l2[:, :n], lse) and (l2[:, n:] == 5.0).all()
+    out[:n] = 7.0
+    assert (wide == 7.0).all()
