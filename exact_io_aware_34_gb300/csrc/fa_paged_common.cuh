@@ -583,8 +583,9 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
   for (int b = c; b < sh.B; b += gridDim.x) {
     const PagedSeq q = paged_seq(p, b);
     const int blind = min(q.n_q, q.first * sh.tp);
-    for (int r = me; r < blind * sh.H; r += warps) {
-      const int t = r / sh.H, h = r - t * sh.H;
+    // (Rows are below 2^31; the step behind the last one may not be.)
+    for (unsigned r = me; r < static_cast<unsigned>(blind) * sh.H; r += warps) {
+      const int t = static_cast<int>(r / sh.H), h = static_cast<int>(r - static_cast<unsigned>(t) * sh.H);
       for (int e = lane; e < HD; e += 32) p.o[(q.c0 + t) * p.o_t + h * p.o_h + e] = __float2bfloat16(0.f);
       if (lane == 0) p.lse[static_cast<long long>(h) * sh.T_q + q.c0 + t] = -INFINITY;
     }

@@ -158,6 +158,13 @@ def test_workspace_of_rejected_sizes_is_zero(lib):
     assert need > 0 and paged(lib, wn=need - 1) == BAD
 
 
+def test_most_rows(lib):
+    """T_q * H up to 2^31 - 2: the merge's row numbers stay below 2^31, with a step of 64 behind the last within 32 bits."""
+    size, rows = fa.fa_fwd_paged_workspace_bytes, (1 << 30) - 1
+    assert size(1, 2, 1, rows, 64, 9, 16, 9) > 0 and size(1, 2, 1, rows + 1, 64, 9, 16, 9) == 0
+    assert 2 * rows - 1 + 64 < 1 << 32
+
+
 def test_fault_hook_rejects_zero_timeout(lib):
     assert lib.fa_fwd_paged_fault_test(*[A + i * GAP for i in range(10)], 1, 1, 1, 1, 64, 9, 16, 1, 0.1, 0, A + 20 * GAP,
                                        1 << 30, 0, 0, None) == BAD
