@@ -432,12 +432,12 @@ constexpr int kPagedJobs = 4;            // the ring through which units are han
 // ring of kTiles tiles, K and V of a key tile in turn. A lane has one page: 32
 // entries of the table are read at a time, a batch (or a unit) ahead. The scales
 // of a pair of tiles go to page_scale[pair % kScales] (K, V, and with kLogs V's
-// logarithm and reciprocal) and count as part of the V tile.
+// logarithm) and count as part of the V tile.
 template <int HD, int kTiles, int kScales, bool kLogs>
 __device__ __forceinline__ void paged_load(const PagedParams& p, const PagedLine* line, const CUtensorMap* tmK,
                                            const CUtensorMap* tmV, PagedJob* jobs, uint64_t* bar_job_full,
                                            uint64_t* bar_job_empty, uint64_t* bar_full, uint64_t* bar_empty,
-                                           float (*page_scale)[kLogs ? 4 : 2][8], uint32_t tiles_at,
+                                           float (*page_scale)[kLogs ? 3 : 2][8], uint32_t tiles_at,
                                            volatile int* abort_ptr) {
   constexpr uint32_t kTileBytes = 128 * HD;
   const int lane = threadIdx.x & 31;
@@ -535,8 +535,7 @@ __device__ __forceinline__ void paged_load(const PagedParams& p, const PagedLine
           page_scale[((it >> 1) - 1) % kScales][0][slot] = sk;
           page_scale[((it >> 1) - 1) % kScales][1][slot] = sv;
           if (kLogs) {
-            page_scale[((it >> 1) - 1) % kScales][kLogs ? 2 : 0][slot] = ptx::lg2_approx(sv);
-            page_scale[((it >> 1) - 1) % kScales][kLogs ? 3 : 0][slot] = 1.f / sv;
+            page_scale[((it >> 1) - 1) % kScales][kLogs ? 2 : 0][slot] = ptx::max_nan(ptx::lg2_approx(sv), -200.f);   // (zero, too)
           }
         }
         __syncwarp();

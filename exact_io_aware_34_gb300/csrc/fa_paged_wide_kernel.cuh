@@ -10,12 +10,14 @@
 // into the tensor core's layout, 16 K elements for each 128 keys, beside
 // products that take 2048 cycles for the unit's 256 rows.
 //
-// Scales. S times (row's scale x page's K scale) is a score in powers of two;
-// log2 of the page's V scale is added to it, so P carries that scale and P V
-// needs no other. The maximum that P is written against is that of these sums;
-// a page's weights are summed apart and divided by its scale.
-// P is written as at most 2^kWideTop times 2^kRescaleLog2 (the maximum moves
-// lazily): f16 then resolves weights 2^-31 below the row's largest.
+// Scales. S times (row's scale x page's K scale) is a score s in powers of two;
+// log2 of the page's V scale v is added to it, so P = 2^(s + log2 v - m) carries that
+// scale and P V needs no other. m is the maximum of s + log2 v, moved lazily: P is at most
+// 2^kWideTop times 2^kRescaleLog2, and f16 resolves what is 2^-31 below the row's largest.
+// The sum of weights needs another reference, as V scales may differ by any factor: it is
+// sum 2^(s - n), n the maximum of s, moved like m. A page's part of it is its sum of P
+// times 2^(m - log2 v - n), which stays at 2^60 where v is so small that f16 holds
+// none of its P anyway (these then count as 2^-60 of their weight).
 //
 // Work: see fa_paged_common.cuh; a unit has up to 256 rows (row = token *
 // heads + head), two tiles of 128, each with a softmax warpgroup. The update
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
   __shared__ __align__(8) uint64_t bar_job_empty[kJobs];
   __shared__ __align__(8) uint64_t bar_drain;
   __shared__ __align__(16) PagedJob jobs[kJobs];
-  __shared__ __align__(16) float page_scale[C::kScales][4][8];
+  __shared__ __align__(16) float page_scale[C::kScales][3][8];
   __shared__ float row_scale[C::kRows];
   __shared__ PagedLine line;
   __shared__ uint32_t tmem_base_slot;
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
     ptx::prefetch_tmap(&tmK);
     ptx::prefetch_tmap(&tmV);
   }
-  for (int i = threadIdx.x; i < C::kScales * 32; i += C::kThreads) (&page_scale[0][0][0])[i] = 0.f;
+  for (int i = threadIdx.x; i < C::kScales * 24; i += C::kThreads) (&page_scale[0][0][0])[i] = 0.f;
   // The grid before ends; the merge may be scheduled (all CTAs are resident, so it takes no one's place).
   ptx::grid_wait();
   ptx::grid_next();
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
       const bool live = row < job.rows;
       // Rows that hold no query take the last token's limit, so that they do not mask what the others need not.
       const int seen = sh.causal ? max(0, min(job.n_keys, job.lim0 + min(ti, (job.rows - 1) / job.heads))) : job.n_keys;
-      float m_use = -INFINITY, l = 0.f, v_ref = 0.f, v_unit = 1.f;   // V scale that O is in units of, and its log2
+      float m_use = -INFINITY, n_use = -INFINITY, l = 0.f;   // what O and l are relative to
       for (int jj = 0; jj < blocks; ++jj, ++g) {
         const int j = job.j0 + jj, pair = pair0 + jj;
         // The scales come with V, so its slot is waited for, too, but behind S: the issuer has then seen every
@@ -301,13 +303,6 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
           ptx::tmem_st_wait();
         }
         const uint32_t scales = ptx::smem_u32(page_scale[pair % C::kScales]);
-        if (jj == 0) {
-          float top = 0.f;
-#pragma unroll 1
-          for (int c = 0; c < 8; ++c) top = fmaxf(top, ptx::lds(scales + 32 + 4 * c));
-          v_ref = top > 0.f ? ptx::lg2_approx(top) : 0.f;
-          v_unit = ptx::ex2_approx(v_ref);
-        }
         uint32_t s[4][32];
         float mr[8];
 #pragma unroll
@@ -319,69 +314,72 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
             ptx::tmem_ld16_max<16>(tS + 32 * c + 16, s[c], mr[2 * c + 1]);
           }
         }
-        // Per part: the factor of S (never zero, so that -inf stays), what is added
-        // to it, and 2^- that. Eight parts' are read again where they are needed (registers).
+        // Per part: the factor of S (never zero, so that -inf stays) and log2 of the V scale (finite, or NaN).
+        // Eight parts' are read again where they are needed (registers).
         const int part_shift = NG == 2 ? 6 : 4;
         auto factor = [&](int g) {
           return ptx::max_nan(q_scale * ptx::lds(scales + 4 * ((g << part_shift) >> sh.page_shift)), 1.17549435e-38f);
         };
-        auto offset = [&](int g) {           // (a scale of zero counts as 2^-60 of v_unit)
-          return ptx::max_nan(ptx::lds(scales + 64 + 4 * ((g << part_shift) >> sh.page_shift)) - v_ref, -60.f);
-        };
-        auto back = [&](int g) {
-          return fminf(ptx::lds(scales + 96 + 4 * ((g << part_shift) >> sh.page_shift)) * v_unit, 1.152921504606847e18f);
-        };
+        auto v_log = [&](int g) { return ptx::lds(scales + 64 + 4 * ((g << part_shift) >> sh.page_shift)); };
         float fa2[2], fb2[2];
         if constexpr (NG == 2) {
 #pragma unroll
           for (int g2 = 0; g2 < 2; ++g2) {
             fa2[g2] = factor(g2);
-            fb2[g2] = offset(g2);
+            fb2[g2] = v_log(g2);
           }
         }
         ptx::tmem_ld_wait();
-        float mt = -INFINITY;
+        float mt = -INFINITY, nt = -INFINITY;
+        auto top = [&](float mx, float a, float log) {
+          nt = fmaxf(nt, mx * a);
+          mt = fmaxf(mt, fmaf(mx, a, log));
+        };
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           ptx::reg_fence32(s[c]);
+          ptx::reg_fence1(mr[NG == 2 ? c : 2 * c]);
           if constexpr (NG == 2) {
-            ptx::reg_fence1(mr[c]);
-            mt = fmaxf(mt, fmaf(mr[c], fa2[c >> 1], fb2[c >> 1]));
+            top(mr[c], fa2[c >> 1], fb2[c >> 1]);
           } else {
-            ptx::reg_fence1(mr[2 * c]);
             ptx::reg_fence1(mr[2 * c + 1]);
-            mt = fmaxf(mt, fmaxf(fmaf(mr[2 * c], factor(2 * c), offset(2 * c)),
-                                 fmaf(mr[2 * c + 1], factor(2 * c + 1), offset(2 * c + 1))));
+            top(mr[2 * c], factor(2 * c), v_log(2 * c));
+            top(mr[2 * c + 1], factor(2 * c + 1), v_log(2 * c + 1));
           }
         }
         float alpha = 1.f;
         bool rescale_o = false;
         if (m_use == -INFINITY) {
           m_use = mt;                        // (nothing but zeros has been added)
-        } else {
-          const bool need = mt - m_use > kRescaleLog2;
-          if (need) {
-            alpha = ptx::ex2_approx(m_use - mt);
-            m_use = mt;
-          }
-          rescale_o = need;
+          n_use = nt;
+        } else if (fmaxf(mt - m_use, nt - n_use) > kRescaleLog2) {
+          const float m_new = fmaxf(m_use, mt), n_new = fmaxf(n_use, nt);
+          alpha = ptx::ex2_approx(m_use - m_new);
+          l *= ptx::ex2_approx(n_use - n_new);
+          m_use = m_new;
+          n_use = n_new;
+          rescale_o = true;
         }
         rescale_o = __any_sync(0xffffffffu, rescale_o);
         const float neg_m = m_use == -INFINITY ? 0.f : kWideTop - m_use;
-        float sum = 0.f;
+        const float neg_n = n_use == -INFINITY ? 0.f : -n_use;
+        auto offset = [&](float log) { return ptx::max_nan(log + neg_m, neg_n - 60.f); };
+        if constexpr (NG == 2) {
+#pragma unroll
+          for (int g2 = 0; g2 < 2; ++g2) fb2[g2] = offset(fb2[g2]);
+        }
         uint32_t pk[32];
-        // Weights of keys 32 c .. 32 c + 31.
+        // Weights of keys 32 c .. 32 c + 31, added to l.
         auto exponents = [&](int c) {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const int part = NG == 2 ? c >> 1 : 2 * c + q;
             float a, off;
             if constexpr (NG == 2) {
-              a = fa2[part & 1];
-              off = fb2[part & 1] + neg_m;
+              a = fa2[c >> 1];
+              off = fb2[c >> 1];
             } else {
-              a = factor(part);
-              off = offset(part) + neg_m;
+              a = factor(2 * c + q);
+              off = offset(v_log(2 * c + q));
             }
             const uint64_t a2 = ptx::f2_pack(a, a), off2 = ptx::f2_pack(off, off);
             uint64_t acc[2] = {0ull, 0ull};
@@ -396,7 +394,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
             }
             float s0, s1;
             ptx::f2_unpack(ptx::f2_add(acc[0], acc[1]), s0, s1);
-            sum = fmaf(s0 + s1, back(part), sum);
+            l = fmaf(s0 + s1, ptx::ex2_approx(neg_n - off), l);
           }
         };
         exponents(0);
@@ -419,7 +417,6 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
         ptx::mbar_arrive(ptx::smem_u32(&bar_p_half[t]));
         exponents(2);
         exponents(3);
-        l = l * alpha + sum;
         ptx::tmem_st32(tS + 32, pk);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
@@ -431,8 +428,9 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
       if (!ok) break;
       ptx::tc_fence_after();
       const bool none = l == 0.f;
-      const float inv = none ? 0.f : v_unit / l;
-      const float lse = none ? -INFINITY : (m_use - kWideTop + __log2f(l)) * 0.69314718055994530942f;
+      const float total = n_use + __log2f(l);
+      const float inv = none ? 0.f : ptx::ex2_approx(m_use - kWideTop - total);
+      const float lse = none ? -INFINITY : total * 0.69314718055994530942f;
       const int head = job.head + row - ti * job.heads, token = job.token + ti;
       if (live) {
         if (job.slot >= 0) p.Lp[static_cast<size_t>(job.slot) * C::kRows + row] = lse;

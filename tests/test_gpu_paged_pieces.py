@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from exact_io_aware_34_gb300 import fa
-from tests.test_gpu_append import Cache, i32, offsets
+from tests.test_gpu_append import Cache, E4M3, i32, offsets
 from tests.test_gpu_paged import check
 from tests.test_gpu_varlen import draw, ok
 
@@ -63,3 +63,49 @@ def test_rows_that_end_inside_a_warp(d, G):
     assert torch.equal(out[:n], o) and torch.equal(l2[:, :n], lse) and (l2[:, n:] == 5.0).all()
     out[:n] = 7.0
     assert (wide == 7.0).all()
+
+
+def set_page(cache, seq, k, v_scale, codes=True):
+    """V scale of page k of a sequence; codes False: zeros, as fa_kv_append writes them with a scale of 2^-100."""
+    i = int(cache.table[seq, k])
+    cache.vs[i] = v_scale
+    if not codes:
+        cache.v.view(torch.uint8)[i] = 0
+
+
+@pytest.mark.parametrize("rows", [40])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("first,later,codes", [
+    (-100, 51, False), (-100, 28, False), (-100, 119, True), (-135, -6, True), (-135, -6, False), (51, -100, True),
+    (118, -140, True), (-60, 40, True),
+])
+def test_v_scales_of_any_size(first, later, codes, d, page, rows):
+    """Whole tiles whose V scale is 2^first before and between ones with 2^later (-100: what zeros get, -135: an
+    amax of 2^-126 over 448): every weight stays in the sum, whatever its V scale. Units of several tiles,
+    most of them whole."""
+    lens = [300, 520, 140] * 40
+    cache = Cache(page + d, lens, 2, page, d)
+    for b, n in enumerate(lens):
+        for k in range(-(-n // page)):
+            low = (k * page // 128) % 2 == 0
+            set_page(cache, b, k, 2.0 ** (first if low else later), codes or not low)
+    check(cache, [rows] * len(lens), 8, d, seed=rows)
+
+
+@pytest.mark.parametrize("rows", [40])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("small,large", [(-70, 0), (-100, 20), (-30, 50)])
+def test_a_large_v_scale_without_weight(small, large, page, rows):
+    """Pages of large values whose keys have no weight (2^-280 of the others') leave small ones as they are, with
+    both in one tile, in another order, and in tiles of their own."""
+    d, lens = 64, [32 + page, 64 + page, 400] * 40
+    cache = Cache(page, lens, 2, page, d)
+    q = torch.full((len(lens) * rows, 4, d), 1.0, dtype=torch.bfloat16)
+    for b, n in enumerate(lens):
+        for k in range(-(-n // page)):
+            i, heavy = int(cache.table[b, k]), (k % 3 == 1) if b % 3 < 2 else (k * page // 128 == 1)
+            cache.k[i] = torch.full((2, page, d), -4.0 if heavy else 2.0).to(E4M3).cuda()
+            cache.ks[i] = 1.0
+            set_page(cache, b, k, 2.0 ** (large if heavy else small))
+    check(cache, [rows] * len(lens), 4, d, scale=0.5, q=q, causal=False)
