@@ -98,6 +98,7 @@ enum : unsigned int { kRolePagedProducer = 30, kRolePagedMma = 31, kRolePagedSof
 constexpr int kPagedCost = 2;            // fa_paged_kernel (64 answers: 1 32.7 us, 2 29.7, 3 30.1)
 constexpr int kWideCost = 12;           // fa_paged_wide_kernel: its query rows, the first products, its results (6: 171 us, 12: 166, 18: 168)
 constexpr float kPagedJump = 20.f;   // the reference moves when a tile's maximum is 2^20 above it
+constexpr float kPagedNone = -3e38f; // the maximum of no keys (finite, so that differences are)
 constexpr float kPagedTop = 8.f;     // a tile's largest weight is written as 2^8 (e4m3 ends at 448)
 
 struct PagedShape {

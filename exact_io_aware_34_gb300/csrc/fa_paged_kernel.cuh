@@ -31,8 +31,10 @@
 // is written: the products' latency is never waited for.
 //
 // Scales. A key's score is S times its page's K scale; log2 of its V scale
-// (relative to the larger one of its warp's pages) is added to the exponent, so
-// P carries it, and is taken out of the sum of weights again.
+// (relative to the larger one of its warp's pages, of which there are two where pages have
+// 16 rows) is added to the exponent, so P carries it. The weight itself is exponentiated once more. O is
+// relative to the maximum of score + log2 V scale, the sum of weights to one of the scores, so V
+// scales may differ by any factor.
 //
 // Work: see fa_paged_common.cuh. Rows of a unit are consecutive tokens x the heads of a
 // group, row = token * heads + head; N (4 or 8) bounds them. One stream of
@@ -41,9 +43,9 @@
 //
 // What bounds it. Long caches: memory (eight answers to 32768 tokens, 8 K/V
 // heads of 128: 51 us, 5.4 TB/s, 0.80 of a copy, of which 3 us go by before the first
-// tiles are there and 1.5 in the merge). 64 answers of 1 to 8192 tokens: 29.7 us,
-// 3.5 TB/s: unit boundaries, which two small CTAs per SM hide in part. Two answers of
-// 500 tokens: 9.6 us, latencies alone (a cold instruction cache, the line, the
+// tiles are there and 1.5 in the merge). 64 answers of 1 to 8192 tokens: 28.8 us,
+// 3.6 TB/s: unit boundaries, which two small CTAs per SM hide in part. Two answers of
+// 500 tokens: 9.5 us, latencies alone (a cold instruction cache, the line, the
 // table, the first tile, its chain, the merge).
 //
 // Per CTA (224 threads, two CTAs per SM): warps 0-3 softmax and sums, warp 4
@@ -114,9 +116,9 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
   // By unit (modulo 4: written two units ahead of a reader) and row: the scores' scale over the query row's, keys seen.
   __shared__ __align__(16) float row_scale[4][N];
   __shared__ __align__(16) int row_lim[4][N];
-  // By tile (modulo 4: a warp may be three tiles behind the first to write), warp and row: the maximum - kPagedTop.
+  // By tile (modulo 4: a warp may be three tiles behind the first to write), warp and row: the maximum with the V
+  // scale - kPagedTop.
   __shared__ __align__(16) float warp_max[4][4][N];
-  __shared__ float warp_top[4][4];                      // the larger V scale of the warp's pages
   __shared__ __align__(16) float factor[4][4][N];       // by reading warp: what the four O^T are multiplied by
   __shared__ __align__(16) float corr[4][N];
   __shared__ float sums[4][4][2][N];                    // by unit (modulo 4) and warp: sums of weights, what they are relative to
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
     const int page_slot = tid >> sh.page_shift;
     const int slot0 = warp * 32 >> sh.page_shift, slot1 = (warp * 32 + 31) >> sh.page_shift;   // the warp's pages
     float acc[N];                                  // O^T of the unit, relative to ref
-    float ref = -INFINITY;                         // of row lane % N, the same in all warps
+    float ref = kPagedNone;                        // of row lane % N, the same in all warps
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.f;
 
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
       float top = m;
 #pragma unroll
       for (int o = N; o < 4 * N; o <<= 1) top = ptx::max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const bool jump = top != -INFINITY && !(top - ref <= kPagedJump);   // (also the first tile with keys, and NaN)
+      const bool jump = !(top - ref <= kPagedJump);   // (also the first tile with keys, and NaN)
       if (__any_sync(0xffffffffu, jump)) {
         if (lane < N) corr[warp][lane] = jump ? ptx::ex2_approx(ref - top) : 1.f;
         if (jump) ref = top;
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
         for (int i = 0; i < N; ++i) acc[i] *= corr[warp][i];
       }
       if (lane < 4 * N)
-        (&factor[warp][0][0])[lane] = m == -INFINITY ? 0.f : ptx::ex2_approx(m - ref) * warp_top[t & 3][lane / N];
+        (&factor[warp][0][0])[lane] = ptx::ex2_approx(m - ref);
       __syncwarp();
       if (!wait_warp_or_abort(ptx::smem_u32(&bar_o_full[buf]), (t >> 1) & 1, abort_ptr, p.timeout_ns, kRolePagedSoftmax))
         return false;
@@ -242,16 +244,20 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
         return false;
       float inv = 0.f;                                 // of row lane
       if (lane < N) {
-        float l = 0.f;
+        float l = 0.f, r[4], n_ref = kPagedNone;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const float r = sums[n & 3][w][1][lane];
-          if (r != -INFINITY) l = fmaf(sums[n & 3][w][0][lane], ptx::ex2_approx(r - ref), l);
+          r[w] = sums[n & 3][w][1][lane];
+          n_ref = fmaxf(n_ref, r[w]);
         }
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          l = fmaf(sums[n & 3][w][0][lane], ptx::ex2_approx(r[w] - n_ref), l);
         const bool none = l == 0.f;
-        inv = none ? 0.f : 1.f / l;
+        const float total = n_ref + __log2f(l);
+        inv = none ? 0.f : ptx::ex2_approx(ref - total);
         if (warp == 0 && lane < job.rows) {
-          const float lse = none ? -INFINITY : (ref + __log2f(l)) * 0.69314718055994530942f;
+          const float lse = none ? -INFINITY : total * 0.69314718055994530942f;
           if (job.slot >= 0) {
             p.Lp[static_cast<size_t>(job.slot) * N + lane] = lse;
           } else {
@@ -276,7 +282,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
         }
         acc[r] = 0.f;
       }
-      ref = -INFINITY;
+      ref = kPagedNone;
       return true;
     };
 
@@ -300,7 +306,7 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         lsum[i] = 0.f;
-        lref[i] = -INFINITY;
+        lref[i] = kPagedNone;
       }
       int j = job.j0;
 #pragma unroll 1
@@ -318,14 +324,17 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
         ptx::tmem_ld<C::kCols>(tS0 + buf * C::kRows, s);
         const int key = j * 128 + tid;
         const float k_sc = page_scale[stage][0][page_slot], v_sc = page_scale[stage][1][page_slot];
-        // The key's V scale relative to the larger one of its warp's pages; below 2^-60 of that it counts as that.
-        float v_top = v_sc, v_log = 0.f, v_out = 1.f;
+        // log2 of the larger V scale of the warp's pages (finite, or NaN), and of the key's relative to that.
+        auto log = [](float v) { return ptx::max_nan(ptx::lg2_approx(v), -200.f); };
+        float v_top = log(v_sc), v_log = 0.f;
         if (slot0 != slot1) {
-          v_top = fmaxf(page_scale[stage][1][slot0], page_scale[stage][1][slot1]);
-          const float rel = v_sc / (v_top > 0.f ? v_top : 1.f);
-          v_log = rel < 8.673617379884035e-19f ? -60.f : ptx::lg2_approx(rel);
-          v_out = ptx::ex2_approx(-v_log);
+          v_log = v_top;
+          v_top = log(fmaxf(page_scale[stage][1][slot0], page_scale[stage][1][slot1]));
+          v_log -= v_top;
         }
+        // (Within 2^60 of each other the maximum of the sums does for the weights' reference, too; beyond, one
+        // page's keys may be all that P holds and the other's all the weight, and the scores have a maximum of their own.)
+        const bool apart = __any_sync(0xffffffffu, v_log < -60.f);
         ptx::tmem_ld_wait();
         ptx::reg_fence<C::kCols>(s);
         float x[N], m[N];
@@ -338,12 +347,13 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
             if (key >= row_lim[n & 3][i]) x[i] = -INFINITY;
         }
 #pragma unroll
-        for (int i = 0; i < N; ++i) m[i] = ptx::warp_max_nan(x[i]) - kPagedTop;
+        for (int i = 0; i < N; ++i) m[i] = ptx::max_nan(ptx::warp_max_nan(x[i]) - kPagedTop, kPagedNone);
         if (lane == 0) {
+          auto with_v = [&](float mi) { return mi == kPagedNone ? mi : mi + v_top; };
 #pragma unroll
           for (int i = 0; i < N; i += 4)
-            *reinterpret_cast<float4*>(&warp_max[g & 3][warp][i]) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
-          warp_top[g & 3][warp] = v_top;
+            *reinterpret_cast<float4*>(&warp_max[g & 3][warp][i]) =
+                make_float4(with_v(m[i]), with_v(m[i + 1]), with_v(m[i + 2]), with_v(m[i + 3]));
         }
         uint32_t hi4[N / 4], lo4[N / 4];
 #pragma unroll
@@ -352,13 +362,13 @@ __global__ void __launch_bounds__(PagedCfg<HD, N>::kThreads, PagedCfg<HD, N>::kC
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float mi = m[i + e];
-            w[e] = ptx::ex2_approx(x[i + e] - (mi == -INFINITY ? 0.f : mi));
-            if (mi != -INFINITY && !(mi - lref[i + e] <= kPagedJump)) {
-              lsum[i + e] *= lref[i + e] == -INFINITY ? 0.f : ptx::ex2_approx(lref[i + e] - mi);
-              lref[i + e] = mi;
+            w[e] = ptx::ex2_approx(x[i + e] - mi);
+            const float score = x[i + e] - v_log, ni = apart ? ptx::warp_max_nan(score) - kPagedTop : mi;
+            if (!(ni - lref[i + e] <= kPagedJump)) {
+              lsum[i + e] *= ptx::ex2_approx(lref[i + e] - ni);
+              lref[i + e] = ni;
             }
-            const float f = mi == -INFINITY ? 0.f : ptx::ex2_approx(mi - lref[i + e]);
-            lsum[i + e] = fmaf(w[e], f * v_out, lsum[i + e]);
+            lsum[i + e] += ptx::ex2_approx(score - lref[i + e]);
             h[e] = __uint_as_float(__float_as_uint(w[e]) & 0xfff00000u);
           }
           hi4[i / 4] = to_e4m3x2(h[0], h[1]) | to_e4m3x2(h[2], h[3]) << 16;

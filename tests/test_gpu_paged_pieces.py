@@ -1,6 +1,6 @@
 """fa_fwd_paged where sequences have many rows (pieces of prompts): the kernel with row tiles of 128, over
 the same masks, scales, layouts and calls that test_gpu_paged has for few rows, with its
-tolerances (needs a GB300). More than 16 rows (new tokens x heads of a group) per sequence on average
+tolerances (needs a GB300); V scales of any size in both kernels. More than 16 rows (new tokens x heads of a group) per sequence on average
 take this kernel; pages of 64 rows and more one form of it, smaller ones the other.
 """
 import numpy as np
@@ -73,27 +73,28 @@ def set_page(cache, seq, k, v_scale, codes=True):
         cache.v.view(torch.uint8)[i] = 0
 
 
-@pytest.mark.parametrize("rows", [40])
+@pytest.mark.parametrize("rows", [1, 2, 40])
 @pytest.mark.parametrize("page", [16, 64])
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("stride", [128, 16])
 @pytest.mark.parametrize("first,later,codes", [
     (-100, 51, False), (-100, 28, False), (-100, 119, True), (-135, -6, True), (-135, -6, False), (51, -100, True),
     (118, -140, True), (-60, 40, True),
 ])
-def test_v_scales_of_any_size(first, later, codes, d, page, rows):
-    """Whole tiles whose V scale is 2^first before and between ones with 2^later (-100: what zeros get, -135: an
+def test_v_scales_of_any_size(first, later, codes, stride, d, page, rows):
+    """Whole tiles, or pages in turn, whose V scale is 2^first before and between ones with 2^later (-100: what zeros get, -135: an
     amax of 2^-126 over 448): every weight stays in the sum, whatever its V scale. Units of several tiles,
     most of them whole."""
     lens = [300, 520, 140] * 40
     cache = Cache(page + d, lens, 2, page, d)
     for b, n in enumerate(lens):
         for k in range(-(-n // page)):
-            low = (k * page // 128) % 2 == 0
+            low = (k * page // max(page, stride)) % 2 == 0
             set_page(cache, b, k, 2.0 ** (first if low else later), codes or not low)
     check(cache, [rows] * len(lens), 8, d, seed=rows)
 
 
-@pytest.mark.parametrize("rows", [40])
+@pytest.mark.parametrize("rows", [1, 2, 40])
 @pytest.mark.parametrize("page", [16, 64])
 @pytest.mark.parametrize("small,large", [(-70, 0), (-100, 20), (-30, 50)])
 def test_a_large_v_scale_without_weight(small, large, page, rows):
