@@ -179,8 +179,9 @@ def _on_stream(stream, device):
     return torch.cuda.stream(stream)
 
 
-#: index of the current device (torch.cuda.current_device without its initialisation, which a CUDA tensor has seen)
-_current_device = torch._C._cuda_getDevice
+#: index of the current device (torch.cuda.current_device without its initialisation, which a CUDA tensor has seen;
+#: a torch built without CUDA lacks it)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch(fn, stream, device):

@@ -1,5 +1,8 @@
 """fa_rope, fa_kv_append, fa_fwd_paged: argument checks on the host (CPU only; no address is dereferenced)."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -181,3 +184,16 @@ def test_bindings_refuse_cpu_tensors():
         fa.fa_kv_append(x, x, i, pages, pages, s, s, i[None], i)
     with pytest.raises(ValueError):
         fa.fa_fwd_paged(x, pages, pages, s, s, i[None], i, i)
+
+
+def test_imports_with_a_torch_built_without_cuda():
+    """Such a build has no torch._C._cuda_* functions."""
+    code = ("import torch\n"
+            "for n in [n for n in dir(torch._C) if n.startswith('_cuda_')]: delattr(torch._C, n)\n"
+            "from exact_io_aware_34_gb300 import fa\n"
+            "x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)\n"
+            "try: fa.fa_rope(x, torch.zeros(4, dtype=torch.int32), torch.zeros(32, dtype=torch.float64))\n"
+            "except ValueError: print('refused')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert out.returncode == 0 and out.stdout.strip() == "refused", out.stderr
