@@ -92,6 +92,8 @@ struct PagedWideCfg {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0;                 // + 128 * tile
   static constexpr uint32_t kColO = 256;               // + HD * tile
+  static constexpr uint32_t kColP = HD == 64 ? 384 : kColS;  // + 64 or 128 * tile: over S only where there is no other place
+  static constexpr uint32_t kStepP = HD == 64 ? 64 : 128;
   static constexpr int kRegsSoftmax = 184, kRegsOther = 72;
   static_assert(8 * kRegsSoftmax + 8 * kRegsOther <= 16 * 128, "register split exceeds the launch");
   // kind::f16 with f16 operands (format 0).
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
     const int t = warp >> 2, quarter = warp & 3, row = t * 128 + quarter * 32 + lane;   // row of the unit
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem_base + lane_addr + C::kColS + 128 * t;
-    const uint32_t tO = tmem_base + lane_addr + C::kColO + HD * t;
+    const uint32_t tO = tmem_base + lane_addr + C::kColO + HD * t, tP = tmem_base + lane_addr + C::kColP + C::kStepP * t;
     bool ok = true;
     int g = 0, pair0 = 0, units = 0;         // key blocks of this tile so far; of the CTA before this unit; this tile's units
     for (int n = 0; ok; ++n) {
@@ -411,13 +413,13 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
             ptx::tmem_st32(tO + 32 * c, o);
           }
         }
-        ptx::tmem_st32(tS, pk);
+        ptx::tmem_st32(tP, pk);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(ptx::smem_u32(&bar_p_half[t]));
         exponents(2);
         exponents(3);
-        ptx::tmem_st32(tS + 32, pk);
+        ptx::tmem_st32(tP + 32, pk);
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(ptx::smem_u32(&bar_p_full[t]));
@@ -519,7 +521,7 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
         const uint64_t v = ptx::desc_mnmajor_sw128(sSlots + (pair % C::kSlots) * C::kSlotBytes, C::kChunkBytes);
         for (int t = 0; t < nt && ok; ++t) {
           // P V in two halves: the first runs while the weights of keys 64-127 are still computed.
-          const uint32_t d = tmem_base + C::kColO + HD * t, a = tmem_base + C::kColS + 128 * t, par = (g[t] - 1) & 1;
+          const uint32_t d = tmem_base + C::kColO + HD * t, a = tmem_base + C::kColP + C::kStepP * t, par = (g[t] - 1) & 1;
           ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_p_half[t]), par, abort_ptr, p.timeout_ns, kRolePagedMma);
           if (ok && t == 0)
             ok = wait_warp_or_abort<kPolls>(ptx::smem_u32(&bar_slot_full[pair % C::kSlots]), (pair / C::kSlots) & 1, abort_ptr,
@@ -534,7 +536,11 @@ __global__ void __launch_bounds__(PagedWideCfg<HD, NG>::kThreads, 1)
           if (last) {
             ptx::mma_commit_warp(ptx::smem_u32(&bar_o_full[t]));
           } else {
-            // (Behind P V of the same tile, whose P lies where S will: products run in order.)
+            // At d = 128 this S is written where the P lies that P V, just issued, reads. Nothing waits for P V in
+            // between: products that one thread issues run one after another, as the forward and
+            // backward kernels rely on, too (PTX says so of one accumulator and shape; here the kinds differ as well).
+            // With a wait for P V the results have the same bits (400 calls of random sizes, ten times each),
+            // and the pieces above take 187 us instead of 166.
             if (t == 0) ok = k_wait(pair + 1);
             if (ok) qk(t, pair + 1);
           }
