@@ -22,10 +22,12 @@
 // touches pages. Between them stand the CTAs that rotate queries (fa_rope_kernel's rows).
 //
 // What bounds it. A decode step is one chain: offsets, table, rows and old scale,
-// maximum, rounding (2 tokens 3.8 us, 64 tokens 4.1; all heads' angles once
-// for a CTA, a division of places by pages once for a block). Prompts pass every
+// maximum, rounding (2 tokens 3.8 us, 64 tokens 4.1; a page's angles once
+// for the CTA's heads, a division of places by pages once for a block). Prompts pass every
 // row through registers once: 8414 tokens, 32 query heads on 8, pages of 16 rows,
-// 47.5 us, 4.0 TB/s (0.59 of a copy). Half of that time is computing (46 % of issue
+// 47.5 us, 4.0 TB/s (0.59 of a copy). Larger pages take longer, 32 rows 52 us, 64 rows 58, 128 rows
+// 70: a head's page is then the work of 2, 4 or 8 warps, a CTA has 4, 2 or 1 heads instead of 8, and its
+// angles (16, 32 or 64 KB instead of 8) serve only those. With 16 rows half of the time is computing (46 % of issue
 // slots busy) in chains of load, rotation, maximum and rounding, which is why the CTAs of
 // the queries, which wait for memory, stand between the others and not behind (50.7 us).
 // Rows fetched before the angles are computed cost registers and with them

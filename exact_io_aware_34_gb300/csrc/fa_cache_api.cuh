@@ -323,10 +323,13 @@ bool make_page_map(CUtensorMap* m, const Pages& c) {
 // Rows of a unit: 4 or 8 (fa_paged_kernel) while the sequences' new tokens, on
 // average, fill no more than a unit of 4 or two of 8, else 256 (fa_paged_wide_kernel).
 // Two units read K and V twice, the second time mostly from L2: with 16 rows 24 caches of
-// 100 to 8000 keys take 49 us so and 65 in the other kernel, with four tokens of 24 drafts
-// at d = 64 20 and 26, four long caches 46 and 48. With 20 rows of 5 heads 39 and 35, with
-// 32 rows 68 and 53. (A variant with 16 rows in a unit, and hi and lo as two products,
-// took 74 us for the four long caches.)
+// 100 to 8000 keys take 44 us so and 66 in the other kernel, with four tokens of 24 drafts
+// at d = 64 19 and 26, four long caches 42 and 48. With 20 rows of 5 heads 37 and 35, with
+// 32 rows 62 and 53. (A variant with 16 rows in a unit, and hi and lo as two products,
+// took 74 us for the four long caches.) An average says little where rows are unequal: 511 single
+// tokens on caches of 300 to 4000 beside 1500 tokens on one, 32 heads on 8, take 973 us in units of 8 and
+// 1077 in units of 256 where that one has 4000 keys, 3230 and 1474 where it has 16000; as two calls
+// 235 + 115 and 235 + 346. The host knows no sequence's rows, so it cannot tell these from drafts.
 int paged_rows(int B, int G, int T_q) {
   const long long rows = static_cast<long long>(T_q) * G;
   return rows <= 4LL * B ? 4 : rows <= 16LL * B ? 8 : 256;

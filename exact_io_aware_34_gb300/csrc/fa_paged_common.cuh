@@ -78,8 +78,13 @@ __device__ __forceinline__ float lg2_approx(float x) {
 enum : unsigned int { kRolePagedProducer = 30, kRolePagedMma = 31, kRolePagedSoftmax = 32, kRolePagedWalk = 33, kRolePagedQuery = 34 };
 
 // Places of a unit in the line beside its tiles: what it costs beyond them.
-constexpr int kPagedCost = 2;            // fa_paged_kernel (64 answers: 1 32.7 us, 2 29.7, 3 30.1)
-constexpr int kWideCost = 12;           // fa_paged_wide_kernel: its query rows, the first products, its results (6: 171 us, 12: 166, 18: 168)
+// fa_paged_kernel, 1, 2 or 3: 64 answers of 1 to 8192 tokens 31.5, 28.7, 29.1 us; 300 of 16 to 512 49.5, 49.8,
+// 51.9; eight long caches 51.7, 51.1, 50.7; 24 drafts at d = 64 17.9, 18.9, 19.5.
+constexpr int kPagedCost = 2;
+// fa_paged_wide_kernel (its query rows, the first products, its results), 6, 12 or 18: pieces of 1 to 1024 tokens
+// on pages of 64 170, 166, 167 us, of 16 190, 188, 190, at d = 64 130, 132, 134; 32 caches
+// with 16 new tokens each 95, 102, 108; eight pieces of 512 on 8192 481, 479, 481.
+constexpr int kWideCost = 12;
 constexpr float kPagedJump = 20.f;   // the reference moves when a tile's maximum is 2^20 above it
 constexpr float kPagedNone = -3e38f; // the maximum of no keys (finite, so that differences are)
 constexpr float kPagedTop = 8.f;     // a tile's largest weight is written as 2^8 (e4m3 ends at 448)
@@ -130,7 +135,7 @@ struct PagedJob {
   int slot;                // of the partial result; -1: none, the unit is whole
 };
 
-// sum over i < n of floor((a i + b) / 128), in as many steps as Euclid's
+// sum over i < n of floor((a i + b) / 128): the "floor sum", in as many steps as Euclid's
 // algorithm takes for a and 128 (the lattice points under a line, counted by
 // swapping axes). a n + b stays below 2^32: it is a number of keys.
 __device__ __forceinline__ unsigned floor_sum128(unsigned n, unsigned a, unsigned b) {

@@ -50,6 +50,7 @@
 //
 // Per CTA (224 threads, two CTAs per SM): warps 0-3 softmax and sums, warp 4
 // walks the line and loads pages, warp 5 issues products, warp 6 prepares query rows.
+// 128 registers a thread; with N = 8 ptxas spills 20 bytes.
 #pragma once
 
 #include "fa_paged_common.cuh"

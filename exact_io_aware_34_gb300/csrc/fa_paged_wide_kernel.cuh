@@ -26,8 +26,10 @@
 // What bounds it: per key tile about 3200 cycles, of which 2048 are products, the
 // rest the chain from S to P, which two row tiles hide in part; and about 10000
 // cycles at a unit's beginning, mostly its query rows. Pieces of prompts of 1 to
-// 1024 tokens on caches to 8192, 32 heads on 8, d = 128: 167 us, 843 TFLOP/s over
-// the pairs that are seen (0.43 of the bf16 rate). Keys converted to f16 as well
+// 1024 tokens on caches to 8192, 32 heads on 8, d = 128: 166 us, 848 TFLOP/s over
+// the pairs that are seen (0.43 of the bf16 rate); on pages of 16 or 32 rows, where a tile has
+// up to eight scales that are read again where they are needed, 188 us. ptxas
+// spills 48 to 88 bytes of the 128 registers a thread. Keys converted to f16 as well
 // took 207 us where keys in 8 bits took 188; transposed tiles with 64 rows 704.
 //
 // Per CTA (512 threads, one per SM): warps 0-7 softmax and epilogue, warp 8

@@ -800,7 +800,7 @@ def fa_rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = N
     "turns", "log_turns": a pair that turns ``high_turns`` times or more over the
     original context keeps its frequency, one that turns ``low_turns`` times or less
     has it divided by ``factor``, and between them both are mixed by where its
-    turns (their logarithm) lie.
+    turns (their logarithm) lie. (The limits are not moved to whole pairs.)
     """
     if scaling not in _RAMPS:
         raise ValueError(f"scaling must be one of {[k for k in _RAMPS]}")
@@ -990,7 +990,8 @@ def fa_fwd_paged(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu
     seq_lens: int32 [B]. Only d has to be contiguous in q and the pages. With
     ``causal`` row i of n_q sees the keys j <= i + seq_lens[b] - n_q, else all
     seq_lens[b]; a row that sees none gets o = 0 and lse = -inf. Rows of no
-    sequence are not written. Returns (o bf16 [T_q, H, d], lse float32 [H, T_q]).
+    sequence are not written. A long piece of a prompt among many single tokens is
+    better off in a call of its own (see include/fa.h). Returns (o bf16 [T_q, H, d], lse float32 [H, T_q]).
     """
     T_q, H, d = rows = _leading("q", q, 3)
     device = q.device

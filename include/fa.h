@@ -591,7 +591,9 @@ fa_status_t fa_fwd_prefix_fault_test(const void* Q, const void* K_prefix, const 
  *            1, 2: a pair that turns r = original * base^(-2 j / rot) / 2 pi times over
  *            the `original` context keeps its frequency for r >= high_turns, has it
  *            divided by `factor` for r <= low_turns, and between the two takes the
- *            mean of both weighted by where r (1) or ln r (2) lies between the limits.
+ *            mean of both weighted by where r (1) or ln r (2) lies between the limits. The
+ *            limits are taken as they are: implementations that move them outward to
+ *            whole pairs have slightly other frequencies for the pairs in between.
  * FA_ERR_INVALID_ARG for an odd or small rot, a base, factor or limit that is
  * not positive and finite, high_turns <= low_turns or another ramp.
  */
@@ -690,7 +692,7 @@ size_t fa_fwd_paged_workspace_bytes(int B, int H, int H_kv, int T_q, int d, int 
  *   LSE    : device, float32 [H, T_q], written (natural log).
  *   K_cache, V_cache, k_scale, v_scale, page_table, seq_lens : as for
  *            fa_kv_append, after it; read only. Pages may be shared by sequences. Scales are
- *            not negative (any value, not powers of two alone).
+ *            not negative (any finite value, not powers of two alone, and as far apart as they like).
  *   causal : 1: the new tokens are the last of their sequence: row i of n_q sees
  *            the keys j <= i + seq_lens[b] - n_q; 0: all seq_lens[b].
  *   strides : NULL, else entries for Q and O; cache_strides : NULL, else entries for
@@ -702,8 +704,12 @@ size_t fa_fwd_paged_workspace_bytes(int B, int H, int H_kv, int T_q, int d, int 
  * written. Cache rows past a sequence's length are never part of a result,
  * whatever they hold; with causal, a V row that is not finite can reach rows of its
  * sequence that do not see it. Two launches, the second of which joins what
- * several CTAs computed of a row. Where rows are divided depends on the lengths and
- * the SM count; the same call gives the same bits. Queries and weights enter the
+ * several CTAs computed of a row. The average of new tokens x heads of a group per sequence decides
+ * how a call's rows are tiled (up to 16: 4 or 8 rows together, else 256), so one long piece among
+ * many single tokens is slow where its cache is long: 511 tokens and a piece of 1500, 32 heads on 8,
+ * take 1.0 ms with the piece on a cache of 4000 and 3.2 ms on 16000; in two calls, one for the
+ * tokens and one for the piece (offsets, lengths and table rows of their sequences), 0.35 and 0.58 ms.
+ * Where rows are divided depends on the lengths and the SM count; the same call gives the same bits. Queries and weights enter the
  * 8-bit products as two numbers each (as if rounded to bf16, see the kernels).
  * Offsets, lengths and tables are read on the device in stream order, and a captured
  * call may be replayed with others; ones that do not fit are clamped (lengths), left
